@@ -1,6 +1,6 @@
 /*
- * libmx -- MXFP8 quantize, scale layout, block-scaled GEMM and grid equality on NVIDIA B200
- * (sm_100a). C ABI: plain pointers and sizes; no allocation, no host synchronisation (except
+ * libmx -- MXFP8 and MXFP4 quantize, scale layout, block-scaled GEMM, expert routing and grid
+ * equality on NVIDIA B200 (sm_100a). C ABI: plain pointers and sizes; no allocation, no host synchronisation (except
  * mx_device_error), every call asynchronous on `stream`.
  *
  * The operations follow "End-to-End MXFP8 Reinforcement Learning on Blackwell: What Matching
@@ -24,8 +24,8 @@
  *     inside a block, scale (r, c) is at byte (r % 32) * 16 + ((r % 128) / 32) * 4 + c % 4.
  *
  * Memory: the caller allocates and owns every buffer. All buffers named "device" must be device
- * memory of the current CUDA device; all of them must be 16-byte aligned. Buffers must not
- * overlap unless stated.
+ * memory of the current CUDA device; all of them must be 16-byte aligned unless stated. Buffers
+ * must not overlap unless stated.
  *
  * Errors: arguments are checked on the host before any launch and reported as mx_status; nothing
  * is launched when a check fails. MX_ERR_CUDA reports a failed launch or driver call. Device-side
@@ -204,6 +204,156 @@ mx_status mx_grouped_gemm_swiglu_quant(const uint8_t* qa, const uint8_t* sa_swz,
  */
 mx_status mx_quantize_block128(const void* x, int64_t M, int64_t K, int64_t ld_x, int pow2_scales, uint8_t* q,
                                float* scales, mx_stream stream);
+
+/* ---- MXFP4 ----------------------------------------------------------------------------------------
+ * The 4-bit member of the microscaling formats: E2M1 elements (magnitudes 0, 0.5, 1, 1.5, 2, 3, 4, 6)
+ * under the same E8M0 scale per 32 elements and the same tensor-core scale layout as MXFP8, at half
+ * the bytes and twice the tensor-core rate. Rule: e = floor(log2(amax)) - 2, clamped to [-127, 127],
+ * stored as e + 127, an all-zero block byte 0; element = round-to-nearest-even(x * 2^-e), saturated
+ * to +-6, signed zero kept; a block holding NaN or +-Inf gets scale 0xFF (every value is then NaN)
+ * and codes sign | 7. Two codes per byte: element 2 i in bits 0-3, element 2 i + 1 in bits 4-7.
+ */
+
+/*
+ * MXFP4 quantization of a BF16 matrix: mx_quantize with 4-bit codes. Same flags, scale outputs,
+ * requirements and errors; q_row is [M, K / 2] bytes, q_col [K, M / 2] bytes (packed codes).
+ * Bit-exact to the rule above.
+ */
+mx_status mx_quantize_fp4(const void* x_bf16, int64_t M, int64_t K, int64_t ld_x, int flags, uint8_t* q_row,
+                          uint8_t* s_row, uint8_t* q_col, uint8_t* s_col, mx_stream stream);
+
+/*
+ * The values MXFP4 codes stand for, as BF16 (exact): out[m, k] = dec(q[m, k]) * 2^(s[m, k/32] - 127);
+ * NaN under scale 0xFF, an infinity where a scale above 252 (which quantization never writes) takes the
+ * product past BF16's range.
+ *   q: [M, K / 2] (device, packed); s: raw [M, K/32], or with swizzled != 0 the tensor-core layout;
+ *   out: BF16 [M, K] (device), row stride ld_out elements; columns >= K are not written.
+ * Requirements: K % 32 == 0, M, K < 2^31, ld_out >= K and ld_out % 8 == 0, q and out 16-byte aligned (s too
+ * when swizzled). M == 0 or K == 0 is a no-op.
+ */
+mx_status mx_dequantize_fp4(const uint8_t* q, const uint8_t* s, int64_t M, int64_t K, int swizzled, void* out,
+                            int64_t ld_out, mx_stream stream);
+
+/*
+ * Dense and grouped block-scaled MXFP4 products: mx_gemm and mx_grouped_gemm on packed 4-bit codes
+ * (qa [M, K / 2], qb [N, K / 2] or [G, N, K / 2] bytes; K counts elements). Same scale layouts,
+ * requirements, errors, device-side checks and accuracy. Always run the CTA-pair kernel.
+ */
+mx_status mx_gemm_fp4(const uint8_t* qa, const uint8_t* sa_swz, const uint8_t* qb, const uint8_t* sb_swz, int64_t M,
+                      int64_t N, int64_t K, void* c, int64_t ld_c, mx_out_dtype out_dtype, mx_stream stream);
+mx_status mx_grouped_gemm_fp4(const uint8_t* qa, const uint8_t* sa_swz, const uint8_t* qb, const uint8_t* sb_swz,
+                              const int32_t* row_offsets_dev, int64_t G, int64_t total_rows, int64_t N, int64_t K,
+                              void* c, int64_t ld_c, mx_out_dtype out_dtype, mx_stream stream);
+
+/* ---- routing to experts ----------------------------------------------------------------------------
+ * What stands around the grouped GEMMs in an MoE layer (Table 2: Qwen3-30B-A3B, 128 experts, top-8):
+ * mx_route chooses every token's experts, mx_route_plan turns the choice into the row partition the
+ * grouped GEMMs read, mx_dispatch_quantize writes the tokens into the experts' rows as their A operand,
+ * and mx_combine sums the experts' output rows back into tokens. mx_route_bwd and mx_combine_bwd are the
+ * gradients; the gradient of an unquantized dispatch is mx_combine with weights == NULL.
+ * Limits: 1 <= E <= 1024 experts, topk * T < 2^31 slots.
+ */
+
+/* How mx_route scores an expert, and how it ranks a group of experts. */
+enum { MX_SCORE_SOFTMAX = 0, MX_SCORE_SIGMOID = 1 };
+enum { MX_GROUP_MAX = 0, MX_GROUP_TOP2 = 1 };
+
+/* Element format of a quantized operand. */
+typedef enum { MX_FORMAT_E4M3 = 0, MX_FORMAT_E2M1 = 1 } mx_format;
+
+/*
+ * The topk experts of each of T tokens and their weights, from router logits [T, E] (device, row stride
+ * ld elements; dtype MX_OUT_F32 or MX_OUT_BF16).
+ *   Scores: s = softmax over the row's experts, or sigmoid of each logit. A logit of -inf or NaN takes its
+ *   expert out of the token's row; +inf counts as the largest finite float.
+ *   Keys: s + bias[e] (bias: fp32 [E], device, or NULL; it moves the choice, not the weights; an expert whose
+ *   key is -inf or NaN cannot be chosen). Without a bias, and unless groups are ranked by sums of scores,
+ *   experts are ordered by their logits, which is the same order.
+ *   Groups: the E experts form `groups` groups of E / groups consecutive ones, ranked by their largest key
+ *   (MX_GROUP_MAX) or by the sum of their two largest (MX_GROUP_TOP2; one, if only one can be chosen); experts
+ *   outside the topk_groups best groups cannot be chosen. groups == 1: no such limit.
+ *   Choice: the topk largest keys, largest first; equal keys (of experts and of groups): the lower index first.
+ *   It is the choice that the definition gives in fp64, whatever the input type.
+ *   Weights: scale * s, divided by the sum of the chosen experts' s if renormalize != 0.
+ *   ids [T, topk] int32, weights [T, topk] fp32 (device, packed). Slots for which no expert is left have id -1
+ *   and weight 0.
+ * Requirements: 1 <= E <= 1024, 1 <= topk <= min(16, E), ld >= E, 1 <= groups <= 32, E % groups == 0,
+ * 1 <= topk_groups <= groups (else MX_ERR_ARG for values below their range, MX_ERR_SHAPE above); logits aligned to
+ * their element, the rest to 4 bytes (MX_ERR_ALIGN). T == 0 is a no-op.
+ */
+mx_status mx_route(const void* logits, mx_out_dtype dtype, int64_t T, int64_t E, int64_t ld, const float* bias, int score,
+                   int64_t groups, int64_t topk_groups, int group_score, int64_t topk, int renormalize, float scale,
+                   int32_t* ids, float* weights, mx_stream stream);
+
+/*
+ * The gradient of mx_route's weights with respect to the logits, the choice held fixed (the bias and the
+ * groups only move the choice, so they have no part in it): d_logits[T, E] in the logits' type (row stride
+ * ld_d), from d_weights[T, topk] fp32 and the same logits, ids, score, renormalize and scale. Slots with an id
+ * outside [0, E) have no part; entries of experts that are out of the row (-inf or NaN) are 0. Computed in fp32,
+ * rounded once. Requirements as mx_route; ld_d >= E.
+ */
+mx_status mx_route_bwd(const float* d_weights, const void* logits, mx_out_dtype dtype, int64_t T, int64_t E, int64_t ld,
+                       const int32_t* ids, int score, int64_t topk, int renormalize, float scale, void* d_logits,
+                       int64_t ld_d, mx_stream stream);
+
+/* Bytes of mx_route_plan's workspace (0: none needed); -1 for sizes it does not take. */
+int64_t mx_route_plan_workspace_bytes(int64_t slots, int64_t E);
+
+/*
+ * The experts' rows of a batch, from the experts of `slots` = T * topk slots (ids, int32, device): a stable sort
+ * by expert, in slot order within one.
+ *   row_offsets[E + 1]: rows [row_offsets[e], row_offsets[e + 1]) belong to expert e, as the grouped GEMMs take it.
+ *     Slots without an expert (an id outside [0, E)) come after the last expert's slots and are padding rows of the
+ *     last group, so row_offsets[E] == slots whatever the ids are, and no host needs to know how many there are.
+ *   slot_row[slots]: the slot's row, or ~row (negative) for a slot without an expert.
+ *   counts[E]: slots of each expert, padding rows not counted.
+ *   workspace: mx_route_plan_workspace_bytes(slots, E) device bytes, used during this call only (calls that may
+ *     run at the same time need their own).
+ * Deterministic. slots == 0 writes zero offsets and counts.
+ */
+mx_status mx_route_plan(const int32_t* ids, int64_t slots, int64_t E, int32_t* row_offsets, int32_t* slot_row,
+                        int32_t* counts, void* workspace, mx_stream stream);
+
+/*
+ * Bytes that the grouped tensor-core scale layout of `rows` rows in `groups` groups takes at most, however the
+ * rows are split over them (every group is padded to 128 rows): what a caller allocates that does not know the
+ * split on the host. -1 for bad sizes.
+ */
+int64_t mx_grouped_scale_bytes(int64_t rows, int64_t groups, int64_t kblocks);
+
+/*
+ * Tokens quantized into the experts' rows: for every slot (t, j), row slot_row[t, j] of q gets the rowwise
+ * quantization of x[t, :] (BF16 [T, K], device, row stride ld_x), as mx_quantize (MX_FORMAT_E4M3, q [T * topk, K])
+ * or mx_quantize_fp4 (MX_FORMAT_E2M1, q [T * topk, K / 2]) gives it, and s_swz its scales in the grouped tensor-core
+ * layout of row_offsets: the A operand of mx_grouped_gemm / mx_grouped_gemm_fp4. Rows of slots without an expert
+ * (slot_row < 0) get zero codes and scales. All mx_grouped_scale_bytes(T * topk, E, K / 32) bytes of s_swz are
+ * written, zeros where no row lies. slot_row and row_offsets: as mx_route_plan writes them. A row index or a place
+ * in the layout that lies outside these buffers is skipped.
+ * Requirements: those of mx_quantize for x and q, s_swz 16-byte aligned, E <= 1024. T == 0 or K == 0 is a no-op.
+ */
+mx_status mx_dispatch_quantize(const void* x_bf16, int64_t T, int64_t K, int64_t ld_x, const int32_t* slot_row, int64_t topk,
+                               const int32_t* row_offsets, int64_t E, mx_format format, uint8_t* q, uint8_t* s_swz,
+                               mx_stream stream);
+
+/*
+ * The experts' rows summed back into tokens: y[t, :] = sum_j weights[t, j] * c[slot_row[t, j], :], added in slot
+ * order in fp32 and rounded once. c [rows, N] and y [T, N] (device, row strides ld_c, ld_y) are fp32 or BF16 each;
+ * weights NULL: all 1. Slots with slot_row < 0 or >= rows have no part; a token without any gets zeros. Rows whose
+ * starts are 16-byte aligned move in 16-byte pieces, others element by element.
+ */
+mx_status mx_combine(const void* c, mx_out_dtype c_dtype, int64_t rows, int64_t ld_c, const int32_t* slot_row,
+                     const float* weights, int64_t T, int64_t topk, int64_t N, void* y, mx_out_dtype y_dtype, int64_t ld_y,
+                     mx_stream stream);
+
+/*
+ * The gradients of mx_combine from dy [T, N]: d_c[slot_row[t, j], :] = weights[t, j] * dy[t, :] (in c's type; zeros in
+ * the padding rows of slots without an expert) and d_weights[t, j] = sum_n dy[t, n] * c[slot_row[t, j], n] (fp32; 0 for
+ * such slots), summed in a fixed order. Either output may be NULL (not both); c is read for d_weights only. Rows of d_c
+ * that no slot names are not written.
+ */
+mx_status mx_combine_bwd(const void* dy, mx_out_dtype y_dtype, int64_t ld_dy, const void* c, mx_out_dtype c_dtype,
+                         int64_t rows, int64_t ld_c, const int32_t* slot_row, const float* weights, int64_t T, int64_t topk,
+                         int64_t N, void* d_c, int64_t ld_dc, float* d_weights, mx_stream stream);
 
 /*
  * Selects the kernel behind later mx_gemm / mx_grouped_gemm calls (process-wide): 0 (default) the

@@ -43,8 +43,8 @@ namespace mx {
 constexpr int kBM = 128;            // rows of A per CTA
 constexpr int kBN = 256;            // columns of C per tile
 constexpr int kBK = 128;            // bytes of K per stage (= one 128-byte swizzle row)
-constexpr int kSfaBytes = 512;
-constexpr int kSfbBytes = 1024;
+constexpr int kSfaBytes = 512;        // MXFP8 scale bytes per stage: one 128 x 4 block of A, two of B
+constexpr int kSfbBytes = 1024;       // (MXFP4: 256 elements per stage, twice the blocks)
 constexpr int kEpiWarps = 8;          // two groups of four, one warp per TMEM lane quadrant each
 constexpr int kGemmThreads = 64 + 32 * kEpiWarps;
 constexpr int kMaxGroups = 1024;
@@ -56,15 +56,16 @@ constexpr uint32_t kOvlCol = 240;
 constexpr uint32_t kSfCol = 496;
 constexpr int kStageBytes = 32 * 128;  // epilogue staging per warp: 32 rows x 128 bytes
 
-// Shared-memory layout of one kernel configuration. B_ROWS: rows of B per CTA and stage.
-template <int STAGES, int B_ROWS, int GROUP_ARRAYS>
+// Shared-memory layout of one kernel configuration. B_ROWS: rows of B per CTA and stage; SF: scale
+// blocks per 128 rows and stage.
+template <int STAGES, int B_ROWS, int GROUP_ARRAYS, int SF = 1>
 struct GemmSmem {
     static constexpr int kStages = STAGES;
     static constexpr int kA = 0;
     static constexpr int kB = kA + STAGES * kBM * kBK;
     static constexpr int kSfa = kB + STAGES * B_ROWS * kBK;
-    static constexpr int kSfb = kSfa + STAGES * kSfaBytes;
-    static constexpr int kStage = (kSfb + STAGES * kSfbBytes + 1023) / 1024 * 1024;
+    static constexpr int kSfb = kSfa + STAGES * SF * kSfaBytes;
+    static constexpr int kStage = (kSfb + STAGES * SF * kSfbBytes + 1023) / 1024 * 1024;
     static_assert(kA % 1024 == 0 && kB % 1024 == 0, "swizzled operand buffers 1024-aligned");
     static constexpr int kBar = kStage + kEpiWarps * kStageBytes;
     static constexpr int kMisc = kBar + (2 * STAGES + 6) * 8;
@@ -75,10 +76,15 @@ using Smem1Dense = GemmSmem<3, kBN, 0>;                    // single-CTA kernel
 using Smem1Grouped = GemmSmem<3, kBN, 2>;
 using SmemPairDense = GemmSmem<5, kBN / 2, 0>;             // pair kernel
 using SmemPairGrouped = GemmSmem<5, kBN / 2, 3>;
+using SmemPairDenseFp4 = GemmSmem<5, kBN / 2, 0, 2>;       // pair kernel, MXFP4
+using SmemPairGroupedFp4 = GemmSmem<5, kBN / 2, 3, 2>;
 constexpr int kGemmSmemDense = Smem1Dense::kBytes;
 constexpr int kGemmSmemGrouped = Smem1Grouped::kBytes;
 constexpr int kGemmPairSmemDense = SmemPairDense::kBytes;
 constexpr int kGemmPairSmemGrouped = SmemPairGrouped::kBytes;
+constexpr int kGemmPairSmemDenseFp4 = SmemPairDenseFp4::kBytes;
+constexpr int kGemmPairSmemGroupedFp4 = SmemPairGroupedFp4::kBytes;
+static_assert(kGemmPairSmemDenseFp4 <= 232448 && kGemmPairSmemGroupedFp4 <= 232448, "shared memory per CTA");
 static_assert(kGemmPairSmemDense <= 232448 && kGemmPairSmemGrouped <= 232448 && kGemmSmemGrouped <= 232448 &&
                   kGemmSmemDense <= 232448,
               "shared memory per CTA");
@@ -90,7 +96,8 @@ struct GemmArgs {
     int64_t ldc;
     int M;              // dense: rows of A; grouped: total rows
     int N, K;
-    int nkb;            // ceil(K / 128)
+    int nkb;            // stages: ceil(K / 128), MXFP4 ceil(K / 256)
+    int sf_ctiles;      // MXFP4: scale blocks per 128-row tile, ceil(K / 128)
     int tiles_m;        // dense: row tiles (128 rows single-CTA, 256 rows pair)
     int tiles_n;        // 256-column tiles
     int sfa_tiles;      // 128-row tiles in A's scale layout (dense), for clamping
@@ -622,15 +629,27 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
 // ---------------------------------------------------------------------------------------------
 // CTA-pair kernel: 256 x 256 tiles, cluster of 2 (launched with cluster dimension 2).
 // ---------------------------------------------------------------------------------------------
-constexpr uint32_t kPairStageBytes = kBM * kBK + (kBN / 2) * kBK + kSfaBytes + kSfbBytes;   // per CTA
+//
+// FP4 == true: MXFP4 operands (packed E2M1, kind::mxf4). A stage's 128 bytes of K are 256 elements, i.e.
+// two scale blocks of 4 K-blocks per 128 rows and four MMAs of 64 elements; the scale slot in TMEM takes
+// the first blocks for MMAs 0 and 1, then the second for MMAs 2 and 3 (tcgen05 operations of one thread
+// run in order). K past the end is zero-filled by TMA, and MMAs that lie wholly past it are not issued.
+// An MMA reads the same bytes as an MXFP8 one and does twice the products, so loads, epilogue and scale
+// copies weigh twice.
+template <bool FP4>
+constexpr uint32_t kPairStageBytesOf = kBM * kBK + (kBN / 2) * kBK + (FP4 ? 2 : 1) * (kSfaBytes + kSfbBytes);   // per CTA
 
 // EPI 0: C written as fp32 / BF16; EPI 1 (grouped only): the fused SwiGLU + MXFP8 epilogue.
-template <bool GROUPED, int EPI = 0>
+template <bool GROUPED, int EPI = 0, bool FP4 = false>
 __global__ void __launch_bounds__(kGemmThreads, 1)
     mx_gemm_pair_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_constant__ CUtensorMap tmap_b,
                         const __grid_constant__ CUtensorMap tmap_sfa, const __grid_constant__ CUtensorMap tmap_sfb,
                         const GemmArgs a) {
-    using L = typename std::conditional<GROUPED, SmemPairGrouped, SmemPairDense>::type;
+    using L8 = typename std::conditional<GROUPED, SmemPairGrouped, SmemPairDense>::type;
+    using L4 = typename std::conditional<GROUPED, SmemPairGroupedFp4, SmemPairDenseFp4>::type;
+    using L = typename std::conditional<FP4, L4, L8>::type;
+    constexpr uint32_t kPairStageBytes = kPairStageBytesOf<FP4>;
+    constexpr int kSfaStage = (FP4 ? 2 : 1) * kSfaBytes, kSfbStage = (FP4 ? 2 : 1) * kSfbBytes;
     constexpr int S = L::kStages;
     constexpr int kBRows = kBN / 2;
     extern __shared__ uint8_t smem_raw[];
@@ -705,13 +724,20 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
                 if (leader) mbar_arrive_expect_tx_elect(&full[stage], 2 * kPairStageBytes);
                 tma_load_2d_pair_elect(smem + L::kA + stage * kBM * kBK, &tmap_a, fb, kb * kBK, T.a_row0);
                 tma_load_2d_pair_elect(smem + L::kB + stage * kBRows * kBK, &tmap_b, fb, kb * kBK, T.b_row0);
-                // Scale blocks: the layout viewed as rows of 256 bytes, one block = 2 rows.
-                tma_load_2d_pair_elect(smem + L::kSfa + stage * kSfaBytes, &tmap_sfa, fb, 0,
-                                       2 * (T.sfa_tile * a.nkb + kb));
-                tma_load_2d_pair_elect(smem + L::kSfb + stage * kSfbBytes, &tmap_sfb, fb, 0,
-                                       2 * (T.sfb_tile0 * a.nkb + kb));
-                tma_load_2d_pair_elect(smem + L::kSfb + stage * kSfbBytes + 512, &tmap_sfb, fb, 0,
-                                       2 * (T.sfb_tile1 * a.nkb + kb));
+                // Scale blocks: the layout viewed as rows of 256 bytes, one block = 2 rows. MXFP4 takes two
+                // consecutive blocks of each row tile; where the last stage has only one, that one is loaded
+                // twice (the copy is not used), so no load leaves the layout and every stage has its bytes.
+                const int sf_ct = FP4 ? a.sf_ctiles : a.nkb;
+#pragma unroll
+                for (int h = 0; h < (FP4 ? 2 : 1); ++h) {
+                    const int blk = FP4 ? min(2 * kb + h, sf_ct - 1) : kb;
+                    tma_load_2d_pair_elect(smem + L::kSfa + stage * kSfaStage + 512 * h, &tmap_sfa, fb, 0,
+                                           2 * (T.sfa_tile * sf_ct + blk));
+                    tma_load_2d_pair_elect(smem + L::kSfb + stage * kSfbStage + 512 * h, &tmap_sfb, fb, 0,
+                                           2 * (T.sfb_tile0 * sf_ct + blk));
+                    tma_load_2d_pair_elect(smem + L::kSfb + stage * kSfbStage + kSfbStage / 2 + 512 * h, &tmap_sfb,
+                                           fb, 0, 2 * (T.sfb_tile1 * sf_ct + blk));
+                }
                 ++issued;
                 if (++stage == S) { stage = 0; phase ^= 1u; }
             }
@@ -745,16 +771,37 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
                     if (!mbar_wait(&full[stage], phase, abort, a.err, a.timeout_ns)) { ok = false; break; }
                     __syncwarp();
                     tc_fence_after();
-                    tc_cp_pair_elect(sfa_t, sdesc_scale_block(smem_u32(smem + L::kSfa + stage * kSfaBytes)));
-                    tc_cp_pair_elect(sfb_t, sdesc_scale_block(smem_u32(smem + L::kSfb + stage * kSfbBytes)));
-                    tc_cp_pair_elect(sfb_t + 4, sdesc_scale_block(smem_u32(smem + L::kSfb + stage * kSfbBytes + 512)));
+                    const uint32_t sfa_s = smem_u32(smem + L::kSfa + stage * kSfaStage);
+                    const uint32_t sfb_s = smem_u32(smem + L::kSfb + stage * kSfbStage);
+                    tc_cp_pair_elect(sfa_t, sdesc_scale_block(sfa_s));
+                    tc_cp_pair_elect(sfb_t, sdesc_scale_block(sfb_s));
+                    tc_cp_pair_elect(sfb_t + 4, sdesc_scale_block(sfb_s + kSfbStage / 2));
                     const uint64_t adesc = sdesc_kmajor_sw128(smem_u32(smem + L::kA + stage * kBM * kBK));
                     const uint64_t bdesc = sdesc_kmajor_sw128(smem_u32(smem + L::kB + stage * kBRows * kBK));
+                    if constexpr (FP4) {
+                        const int steps = min(4, (a.K - kb * 256 + 63) / 64);
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {
+                            if (k < steps) {
+                                if (k == 2) {
+                                    tc_cp_pair_elect(sfa_t, sdesc_scale_block(sfa_s + 512));
+                                    tc_cp_pair_elect(sfb_t, sdesc_scale_block(sfb_s + 512));
+                                    tc_cp_pair_elect(sfb_t + 4, sdesc_scale_block(sfb_s + kSfbStage / 2 + 512));
+                                }
+                                // K-step k: +32 bytes (64 elements); scale bytes 2 (k % 2), +1 of the word.
+                                const uint32_t id = 2u * (k & 1);
+                                tc_mma_mxf4_pair_elect(acc, adesc + 2u * k, bdesc + 2u * k,
+                                                       idesc_mxf4(2 * kBM, kBN, id), sfa_t | (id << 30),
+                                                       sfb_t | (id << 30), (kb | k) != 0 ? 1u : 0u);
+                            }
+                        }
+                    } else {
 #pragma unroll
                     for (int k = 0; k < 4; ++k) {
                         tc_mma_mxf8_pair_elect(acc, adesc + 2u * k, bdesc + 2u * k, idesc_mxf8_e4m3(2 * kBM, kBN, k),
                                                sfa_t | (static_cast<uint32_t>(k) << 30),
                                                sfb_t | (static_cast<uint32_t>(k) << 30), (kb | k) != 0 ? 1u : 0u);
+                    }
                     }
                     tc_commit_pair_elect(&empty[stage], 0x3);     // both CTAs' stage is free again
                     if (++stage == S) { stage = 0; phase ^= 1u; }

@@ -1,6 +1,6 @@
 // libmx: the C-ABI entry points declared in include/mx.h. Host-side argument checks, tensor-map
-// construction and kernel launches; the kernels themselves are in quantize.cuh, grid_equal.cuh
-// and gemm.cuh. Nothing here allocates device memory or synchronizes (except mx_device_error).
+// construction and kernel launches; the kernels themselves are in quantize.cuh, fp4.cuh, gemm.cuh,
+// route.cuh, experts.cuh, swizzle.cuh, blockwise.cuh and grid_equal.cuh. Nothing here allocates device memory or synchronizes (except mx_device_error).
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -13,11 +13,14 @@
 
 #include "../../include/mx.h"
 #include "blockwise.cuh"
+#include "experts.cuh"
+#include "fp4.cuh"
 #include "gemm.cuh"
 #include "grid_equal.cuh"
 #include "ptx.cuh"
 #include "quantize.cuh"
 #include "quantize_tma.cuh"
+#include "route.cuh"
 #include "swizzle.cuh"
 
 namespace mx {
@@ -52,6 +55,9 @@ struct DeviceInfo {
     int qt_blocks_per_sm[4] = {0, 0, 0, 0};   // TMA-staged quantizer, by direction bits
     int ge_blocks_per_sm = 1;
     int pair_clusters[2] = {0, 0};    // co-resident 2-CTA clusters of the pair GEMM (dense, grouped)
+    int pair_clusters_fp4[2] = {0, 0};
+    int dispatch_blocks_per_sm[2] = {1, 1};   // MXFP8, MXFP4
+    int fp4_blocks_per_sm[4] = {1, 1, 1, 1};  // MXFP4 quantizer, by direction bits
     bool ok = false;
 };
 
@@ -100,6 +106,13 @@ template <bool ROW>
 int quant_occupancy() {
     int n = 0;
     cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, quantize_rowcol_kernel<ROW, kQMaxTensors>, kQThreads, 0);
+    return n > 0 ? n : 1;
+}
+
+template <class K>
+int occupancy(K kernel, int threads) {
+    int n = 0;
+    cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kernel, threads, 0);
     return n > 0 ? n : 1;
 }
 
@@ -169,6 +182,20 @@ const DeviceInfo* device_info() {
             return nullptr;
         d.pair_clusters[0] = max_pair_clusters(mx_gemm_pair_kernel<false>, kGemmPairSmemDense, d.sms);
         d.pair_clusters[1] = max_pair_clusters(mx_gemm_pair_kernel<true>, kGemmPairSmemGrouped, d.sms);
+        if (cudaFuncSetAttribute(mx_gemm_pair_kernel<false, 0, true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 kGemmPairSmemDenseFp4) != cudaSuccess ||
+            cudaFuncSetAttribute(mx_gemm_pair_kernel<true, 0, true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 kGemmPairSmemGroupedFp4) != cudaSuccess ||
+            cudaFuncSetAttribute(plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 plan_smem_bytes(kRouteMaxExperts)) != cudaSuccess)
+            return nullptr;
+        d.pair_clusters_fp4[0] = max_pair_clusters(mx_gemm_pair_kernel<false, 0, true>, kGemmPairSmemDenseFp4, d.sms);
+        d.pair_clusters_fp4[1] = max_pair_clusters(mx_gemm_pair_kernel<true, 0, true>, kGemmPairSmemGroupedFp4, d.sms);
+        d.dispatch_blocks_per_sm[0] = occupancy(dispatch_kernel<false>, kExThreads);
+        d.dispatch_blocks_per_sm[1] = occupancy(dispatch_kernel<true>, kExThreads);
+        d.fp4_blocks_per_sm[1] = occupancy(quantize_fp4_kernel<true, false>, kQThreads);
+        d.fp4_blocks_per_sm[2] = occupancy(quantize_fp4_kernel<false, true>, kQThreads);
+        d.fp4_blocks_per_sm[3] = occupancy(quantize_fp4_kernel<true, true>, kQThreads);
         d.ok = true;
     }
     return &d;
@@ -286,13 +313,14 @@ bool make_tmap_sf(CUtensorMap* map, const void* base, int64_t blocks) {
 }
 
 // Launches the CTA-pair GEMM with a cluster dimension of 2.
-template <bool GROUPED, int EPI = 0>
+template <bool GROUPED, int EPI = 0, bool FP4 = false>
 mx_status launch_pair(int pairs, const CUtensorMap& ta, const CUtensorMap& tb, const CUtensorMap& tsa,
                       const CUtensorMap& tsb, const GemmArgs& a, mx_stream stream) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(2 * pairs, 1, 1);
     cfg.blockDim = dim3(kGemmThreads, 1, 1);
-    cfg.dynamicSmemBytes = GROUPED ? kGemmPairSmemGrouped : kGemmPairSmemDense;
+    cfg.dynamicSmemBytes = FP4 ? (GROUPED ? kGemmPairSmemGroupedFp4 : kGemmPairSmemDenseFp4)
+                               : (GROUPED ? kGemmPairSmemGrouped : kGemmPairSmemDense);
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -301,7 +329,7 @@ mx_status launch_pair(int pairs, const CUtensorMap& ta, const CUtensorMap& tb, c
     attr[0].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    if (cudaLaunchKernelEx(&cfg, mx_gemm_pair_kernel<GROUPED, EPI>, ta, tb, tsa, tsb, a) != cudaSuccess) {
+    if (cudaLaunchKernelEx(&cfg, mx_gemm_pair_kernel<GROUPED, EPI, FP4>, ta, tb, tsa, tsb, a) != cudaSuccess) {
         cudaGetLastError();
         return MX_ERR_CUDA;
     }
@@ -867,5 +895,432 @@ mx_status mx_quantize_block128(const void* x, int64_t M, int64_t K, int64_t ld_x
 void mx_set_gemm_variant(int variant) { g_gemm_variant.store(variant == 1 ? 1 : 0); }
 
 void mx_set_quantize_variant(int variant) { g_quant_variant.store(variant == 1 || variant == 2 ? variant : 0); }
+
+}  // extern "C"
+
+// ---- MXFP4 --------------------------------------------------------------------------------------------
+
+namespace mx {
+namespace {
+
+// The arguments the two MXFP4 products share, past their own checks. A grouped call has `offsets`.
+mx_status launch_gemm_fp4(const uint8_t* qa, const uint8_t* sa, const uint8_t* qb, const uint8_t* sb,
+                          const int32_t* offsets, int64_t G, int64_t M, int64_t N, int64_t K, void* c, int64_t ld_c,
+                          mx_out_dtype out_dtype, const DeviceInfo* d, mx_stream stream) {
+    GemmArgs a{};
+    a.sfa = sa;
+    a.sfb = sb;
+    a.c = c;
+    a.ldc = ld_c;
+    a.M = static_cast<int>(M);
+    a.N = static_cast<int>(N);
+    a.K = static_cast<int>(K);
+    a.nkb = static_cast<int>(ceil_div(K, 2 * kBK));
+    a.sf_ctiles = static_cast<int>(ceil_div(K, 128));
+    a.tiles_m = offsets ? 0 : static_cast<int>(ceil_div(M, 2 * kBM));
+    a.tiles_n = static_cast<int>(ceil_div(N, kBN));
+    a.sfa_tiles = static_cast<int>(ceil_div(M, 128));
+    a.out_bf16 = out_dtype == MX_OUT_BF16;
+    a.vec_store = vector_store_ok(c, ld_c, out_dtype);
+    a.G = static_cast<int>(G);
+    a.n_fast = M > N;
+    a.n_rowtiles = static_cast<int>(ceil_div(N, 128));
+    a.row_offsets = offsets;
+    a.err = d->status;
+    a.timeout_ns = g_timeout_ns.load();
+    // Upper bounds (grouped): every group adds at most one partial tile.
+    const int64_t sfa_tiles = offsets ? ceil_div(M, 128) + G : a.sfa_tiles;
+    const int64_t tiles = (offsets ? ceil_div(M, 2 * kBM) + G : a.tiles_m) * a.tiles_n;
+    CUtensorMap ta, tb, tsa, tsb;
+    if (!make_tmap(&ta, qa, K / 2, M, kBK, kBM) || !make_tmap(&tb, qb, K / 2, G * N, kBK, kBN / 2) ||
+        !make_tmap_sf(&tsa, sa, sfa_tiles * a.sf_ctiles) ||
+        !make_tmap_sf(&tsb, sb, G * a.n_rowtiles * a.sf_ctiles))
+        return MX_ERR_CUDA;
+    const int pairs = static_cast<int>(std::min<int64_t>(tiles, d->pair_clusters_fp4[offsets ? 1 : 0]));
+    return offsets ? launch_pair<true, 0, true>(pairs, ta, tb, tsa, tsb, a, stream)
+                   : launch_pair<false, 0, true>(pairs, ta, tb, tsa, tsb, a, stream);
+}
+
+}  // namespace
+}  // namespace mx
+
+extern "C" {
+
+mx_status mx_quantize_fp4(const void* x, int64_t M, int64_t K, int64_t ld_x, int flags, uint8_t* q_row,
+                          uint8_t* s_row, uint8_t* q_col, uint8_t* s_col, mx_stream stream) {
+    const bool row = flags & MX_ROWWISE, col = flags & MX_COLWISE;
+    if (flags & ~(MX_ROWWISE | MX_COLWISE | MX_SWIZZLE)) return MX_ERR_ARG;
+    if (!row && !col) return MX_ERR_ARG;
+    const mx_quant_tensor t{x, M, K, ld_x, q_row, s_row, q_col, s_col};
+    bool empty = false;
+    if (mx_status st = check_quant_tensor(t, row, col, &empty)) return st;
+    if (empty) return MX_OK;
+    const DeviceInfo* d = nullptr;
+    if (mx_status st = check_device(&d)) return st;
+    QuantArgs<1> one;
+    one.n = 0;
+    one.total_tiles = 0;
+    add_quant_tensor(one, t);
+    Fp4Args a;
+    a.t = one.t[0];
+    // Input loads alone decide here (codes leave in 16-byte pieces).
+    a.t.vec32 = reinterpret_cast<uintptr_t>(x) % 32 == 0 && ld_x % 16 == 0;
+    a.swz = (flags & MX_SWIZZLE) != 0;
+    a.total_tiles = one.total_tiles;
+    const int which = (row ? 1 : 0) | (col ? 2 : 0);
+    const int64_t grid = std::min<int64_t>(a.total_tiles, int64_t(d->sms) * d->fp4_blocks_per_sm[which]);
+    if (row && col)
+        quantize_fp4_kernel<true, true><<<grid, kQThreads, 0, stream>>>(a);
+    else if (row)
+        quantize_fp4_kernel<true, false><<<grid, kQThreads, 0, stream>>>(a);
+    else
+        quantize_fp4_kernel<false, true><<<grid, kQThreads, 0, stream>>>(a);
+    return launched();
+}
+
+mx_status mx_dequantize_fp4(const uint8_t* q, const uint8_t* s, int64_t M, int64_t K, int swizzled, void* out,
+                            int64_t ld_out, mx_stream stream) {
+    if (M < 0 || K < 0) return MX_ERR_ARG;
+    if (K % 32 != 0 || M >= (int64_t(1) << 31) || K >= (int64_t(1) << 31)) return MX_ERR_SHAPE;
+    if (M == 0 || K == 0) return MX_OK;
+    if (!q || !s || !out) return MX_ERR_ARG;
+    if (ld_out < K) return MX_ERR_SHAPE;
+    if (!aligned16(q) || !aligned16(out) || ld_out % 8 != 0 || (swizzled && !aligned16(s))) return MX_ERR_ALIGN;
+    const DeviceInfo* d = nullptr;
+    if (mx_status st = check_device(&d)) return st;
+    Fp4DeqArgs a;
+    a.q = q;
+    a.s = s;
+    a.out = static_cast<uint16_t*>(out);
+    a.kblocks = K / 32;
+    a.blocks = M * a.kblocks;
+    a.ld = ld_out;
+    a.ctiles = ceil_div(a.kblocks, 4);
+    a.swz = swizzled != 0;
+    if (ceil_div(a.blocks, 256) >= (int64_t(1) << 31)) return MX_ERR_SHAPE;
+    dequantize_fp4_kernel<<<static_cast<unsigned>(ceil_div(a.blocks, 256)), 256, 0, stream>>>(a);
+    return launched();
+}
+
+mx_status mx_gemm_fp4(const uint8_t* qa, const uint8_t* sa_swz, const uint8_t* qb, const uint8_t* sb_swz, int64_t M,
+                      int64_t N, int64_t K, void* c, int64_t ld_c, mx_out_dtype out_dtype, mx_stream stream) {
+    bool empty = false;
+    if (mx_status st = gemm_checks(qa, sa_swz, qb, sb_swz, M, N, K, c, ld_c, out_dtype, &empty)) return st;
+    if (empty) return MX_OK;
+    const DeviceInfo* d = nullptr;
+    if (mx_status st = check_device(&d)) return st;
+    return launch_gemm_fp4(qa, sa_swz, qb, sb_swz, nullptr, 1, M, N, K, c, ld_c, out_dtype, d, stream);
+}
+
+mx_status mx_grouped_gemm_fp4(const uint8_t* qa, const uint8_t* sa_swz, const uint8_t* qb, const uint8_t* sb_swz,
+                              const int32_t* row_offsets_dev, int64_t G, int64_t total_rows, int64_t N, int64_t K,
+                              void* c, int64_t ld_c, mx_out_dtype out_dtype, mx_stream stream) {
+    if (!row_offsets_dev || G < 1) return MX_ERR_ARG;
+    if (G > kMaxGroups) return MX_ERR_SHAPE;
+    if (reinterpret_cast<uintptr_t>(row_offsets_dev) & 3u) return MX_ERR_ALIGN;
+    bool empty = false;
+    if (mx_status st = gemm_checks(qa, sa_swz, qb, sb_swz, total_rows, N, K, c, ld_c, out_dtype, &empty)) return st;
+    if (G * N >= (int64_t(1) << 31)) return MX_ERR_SHAPE;
+    if (empty) return MX_OK;
+    const DeviceInfo* d = nullptr;
+    if (mx_status st = check_device(&d)) return st;
+    return launch_gemm_fp4(qa, sa_swz, qb, sb_swz, row_offsets_dev, G, total_rows, N, K, c, ld_c, out_dtype, d, stream);
+}
+
+}  // extern "C"
+
+// ---- expert routing, dispatch, combine ---------------------------------------------------------------------
+
+namespace mx {
+namespace {
+
+bool elt_ok(mx_out_dtype dt) { return dt == MX_OUT_F32 || dt == MX_OUT_BF16; }
+int64_t elt_size(mx_out_dtype dt) { return dt == MX_OUT_BF16 ? 2 : 4; }
+bool elt_aligned(const void* p, mx_out_dtype dt) { return reinterpret_cast<uintptr_t>(p) % elt_size(dt) == 0; }
+bool word_aligned(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+constexpr int64_t kInt32End = int64_t(1) << 31;
+
+// Experts per lane of the routing kernels.
+int route_nv(int64_t E) {
+    int nv = 1;
+    while (32 * nv < E) nv *= 2;
+    return nv;
+}
+
+// Whether rows of E elements can be read (or written) as each lane's whole vector of nv.
+int route_vec(const void* p, int64_t ld, int64_t E, int nv, mx_out_dtype dt) {
+    const int64_t bytes = std::min<int64_t>(16, nv * elt_size(dt));
+    return E % nv == 0 && reinterpret_cast<uintptr_t>(p) % bytes == 0 && (ld * elt_size(dt)) % bytes == 0;
+}
+
+mx_status route_shape(int64_t T, int64_t E, int64_t topk, int64_t ld, mx_out_dtype dt, int score) {
+    if (T < 0 || E < 1 || topk < 1 || !elt_ok(dt) || (score != MX_SCORE_SOFTMAX && score != MX_SCORE_SIGMOID))
+        return MX_ERR_ARG;
+    if (E > kRouteMaxExperts || topk > kRouteMaxTopk || topk > E || ld < E || T * topk >= kInt32End || T >= kInt32End)
+        return MX_ERR_SHAPE;
+    return MX_OK;
+}
+
+template <int NV>
+void launch_route(const RouteArgs& a, bool backward, mx_stream stream) {
+    const unsigned grid = static_cast<unsigned>(ceil_div(a.T, kRouteThreads / 32));
+    if (backward)
+        route_bwd_kernel<NV><<<grid, kRouteThreads, 0, stream>>>(a);
+    else
+        route_kernel<NV><<<grid, kRouteThreads, 0, stream>>>(a);
+}
+
+mx_status launch_route_nv(int nv, const RouteArgs& a, bool backward, mx_stream stream) {
+    switch (nv) {
+        case 1: launch_route<1>(a, backward, stream); break;
+        case 2: launch_route<2>(a, backward, stream); break;
+        case 4: launch_route<4>(a, backward, stream); break;
+        case 8: launch_route<8>(a, backward, stream); break;
+        case 16: launch_route<16>(a, backward, stream); break;
+        default: launch_route<32>(a, backward, stream); break;
+    }
+    return launched();
+}
+
+int plan_blocks(int64_t n) {
+    return n <= kPlanOneBlock ? 1 : static_cast<int>(std::min<int64_t>(kPlanMaxBlocks, ceil_div(n, kPlanThreads)));
+}
+
+template <class CT, class YT>
+mx_status launch_combine(const CombineArgs& a, bool backward, mx_stream stream) {
+    if (backward) {
+        combine_bwd_kernel<CT, YT><<<static_cast<unsigned>(a.T), kExThreads, 0, stream>>>(a);
+    } else {
+        const int64_t grid = ceil_div(a.T * a.chunks, kExThreads / 32);
+        if (grid >= kInt32End) return MX_ERR_SHAPE;
+        combine_kernel<CT, YT><<<static_cast<unsigned>(grid), kExThreads, 0, stream>>>(a);
+    }
+    return launched();
+}
+
+mx_status launch_combine_types(const CombineArgs& a, mx_out_dtype ct, mx_out_dtype yt, bool backward, mx_stream stream) {
+    if (ct == MX_OUT_BF16 && yt == MX_OUT_BF16) return launch_combine<uint16_t, uint16_t>(a, backward, stream);
+    if (ct == MX_OUT_BF16) return launch_combine<uint16_t, float>(a, backward, stream);
+    if (yt == MX_OUT_BF16) return launch_combine<float, uint16_t>(a, backward, stream);
+    return launch_combine<float, float>(a, backward, stream);
+}
+
+bool rows_vec(const void* p, int64_t ld, mx_out_dtype dt) { return aligned16(p) && (ld * elt_size(dt)) % 16 == 0; }
+
+}  // namespace
+}  // namespace mx
+
+extern "C" {
+
+mx_status mx_route(const void* logits, mx_out_dtype dtype, int64_t T, int64_t E, int64_t ld, const float* bias, int score,
+                   int64_t groups, int64_t topk_groups, int group_score, int64_t topk, int renormalize, float scale,
+                   int32_t* ids, float* weights, mx_stream stream) {
+    if (mx_status st = route_shape(T, E, topk, ld, dtype, score)) return st;
+    if (groups < 1 || topk_groups < 1 || (group_score != MX_GROUP_MAX && group_score != MX_GROUP_TOP2)) return MX_ERR_ARG;
+    if (groups > kRouteMaxGroups || E % groups != 0 || topk_groups > groups) return MX_ERR_SHAPE;
+    if (T == 0) return MX_OK;
+    if (!logits || !ids || !weights) return MX_ERR_ARG;
+    if (!elt_aligned(logits, dtype) || !word_aligned(ids) || !word_aligned(weights) || !word_aligned(bias))
+        return MX_ERR_ALIGN;
+    const DeviceInfo* d = nullptr;
+    if (mx_status st = check_device(&d)) return st;
+    const int nv = route_nv(E);
+    RouteArgs a{};
+    a.x = logits;
+    a.bias = bias;
+    a.ids = ids;
+    a.w = weights;
+    a.T = T;
+    a.ld = ld;
+    a.E = static_cast<int>(E);
+    a.k = static_cast<int>(topk);
+    // All groups kept: the same as none.
+    a.G = topk_groups == groups ? 1 : static_cast<int>(groups);
+    a.topg = a.G == 1 ? 1 : static_cast<int>(topk_groups);
+    a.bf16 = dtype == MX_OUT_BF16;
+    a.vec = route_vec(logits, ld, E, nv, dtype);
+    a.sigmoid = score == MX_SCORE_SIGMOID;
+    a.top2 = group_score == MX_GROUP_TOP2;
+    a.renorm = renormalize != 0;
+    a.scale = scale;
+    return launch_route_nv(nv, a, false, stream);
+}
+
+mx_status mx_route_bwd(const float* d_weights, const void* logits, mx_out_dtype dtype, int64_t T, int64_t E, int64_t ld,
+                       const int32_t* ids, int score, int64_t topk, int renormalize, float scale, void* d_logits,
+                       int64_t ld_d, mx_stream stream) {
+    if (mx_status st = route_shape(T, E, topk, ld, dtype, score)) return st;
+    if (ld_d < E) return MX_ERR_SHAPE;
+    if (T == 0) return MX_OK;
+    if (!d_weights || !logits || !ids || !d_logits) return MX_ERR_ARG;
+    if (!elt_aligned(logits, dtype) || !elt_aligned(d_logits, dtype) || !word_aligned(ids) || !word_aligned(d_weights))
+        return MX_ERR_ALIGN;
+    const DeviceInfo* d = nullptr;
+    if (mx_status st = check_device(&d)) return st;
+    const int nv = route_nv(E);
+    RouteArgs a{};
+    a.x = logits;
+    a.ids = const_cast<int32_t*>(ids);
+    a.T = T;
+    a.ld = ld;
+    a.E = static_cast<int>(E);
+    a.k = static_cast<int>(topk);
+    a.bf16 = dtype == MX_OUT_BF16;
+    a.vec = route_vec(logits, ld, E, nv, dtype);
+    a.sigmoid = score == MX_SCORE_SIGMOID;
+    a.renorm = renormalize != 0;
+    a.scale = scale;
+    a.dw = d_weights;
+    a.dx = d_logits;
+    a.ld_dx = ld_d;
+    a.vec_dx = route_vec(d_logits, ld_d, E, nv, dtype);
+    return launch_route_nv(nv, a, true, stream);
+}
+
+int64_t mx_route_plan_workspace_bytes(int64_t slots, int64_t E) {
+    if (slots < 0 || slots >= kInt32End || E < 1 || E > kRouteMaxExperts) return -1;
+    const int blocks = plan_blocks(slots);
+    return blocks == 1 ? 0 : int64_t(blocks) * (E + 1) * 4;
+}
+
+mx_status mx_route_plan(const int32_t* ids, int64_t slots, int64_t E, int32_t* row_offsets, int32_t* slot_row,
+                        int32_t* counts, void* workspace, mx_stream stream) {
+    if (slots < 0 || E < 1) return MX_ERR_ARG;
+    if (slots >= kInt32End || E > kRouteMaxExperts) return MX_ERR_SHAPE;
+    const int blocks = plan_blocks(slots);
+    if (!row_offsets || !counts || (slots > 0 && (!ids || !slot_row)) || (blocks > 1 && !workspace)) return MX_ERR_ARG;
+    if (!word_aligned(ids) || !word_aligned(row_offsets) || !word_aligned(slot_row) || !word_aligned(counts) ||
+        !word_aligned(workspace))
+        return MX_ERR_ALIGN;
+    const DeviceInfo* d = nullptr;
+    if (mx_status st = check_device(&d)) return st;
+    PlanArgs a;
+    a.ids = ids;
+    a.offsets = row_offsets;
+    a.slot_row = slot_row;
+    a.counts = counts;
+    a.block_counts = blocks > 1 ? static_cast<int32_t*>(workspace) : nullptr;
+    a.n = static_cast<int32_t>(slots);
+    a.E = static_cast<int32_t>(E);
+    a.chunk = static_cast<int32_t>(ceil_div(std::max<int64_t>(slots, 1), blocks));
+    if (blocks > 1) {
+        counts_kernel<<<blocks, kPlanThreads, static_cast<size_t>(E + 1) * 4, stream>>>(a);
+        if (mx_status st = launched()) return st;
+    }
+    plan_kernel<<<blocks, kPlanThreads, plan_smem_bytes(static_cast<int>(E)), stream>>>(a);
+    return launched();
+}
+
+int64_t mx_grouped_scale_bytes(int64_t rows, int64_t groups, int64_t kblocks) {
+    if (rows < 0 || groups < 1 || kblocks < 0) return -1;
+    return (rows + 127 * std::min(groups, rows)) / 128 * 128 * (ceil_div(kblocks, 4) * 4);
+}
+
+mx_status mx_dispatch_quantize(const void* x, int64_t T, int64_t K, int64_t ld_x, const int32_t* slot_row, int64_t topk,
+                               const int32_t* row_offsets, int64_t E, mx_format format, uint8_t* q, uint8_t* s_swz,
+                               mx_stream stream) {
+    if (T < 0 || K < 0 || topk < 1 || E < 1 || (format != MX_FORMAT_E4M3 && format != MX_FORMAT_E2M1)) return MX_ERR_ARG;
+    if (K % 32 != 0 || K >= kInt32End || E > kRouteMaxExperts || T >= kInt32End || topk >= kInt32End ||
+        T * topk >= kInt32End)
+        return MX_ERR_SHAPE;
+    if (T == 0 || K == 0) return MX_OK;
+    if (!x || !slot_row || !row_offsets || !q || !s_swz) return MX_ERR_ARG;
+    if (ld_x < K) return MX_ERR_SHAPE;
+    if (!aligned16(x) || ld_x % 8 != 0 || !aligned16(q) || !aligned16(s_swz) || !word_aligned(slot_row) ||
+        !word_aligned(row_offsets))
+        return MX_ERR_ALIGN;
+    const DeviceInfo* d = nullptr;
+    if (mx_status st = check_device(&d)) return st;
+    DispatchArgs a;
+    a.x = static_cast<const uint16_t*>(x);
+    a.slot_row = slot_row;
+    a.offsets = row_offsets;
+    a.q = q;
+    a.s = s_swz;
+    a.T = T;
+    a.K = K;
+    a.ldx = ld_x;
+    a.n = T * topk;
+    a.k = static_cast<int>(topk);
+    a.E = static_cast<int>(E);
+    a.kblocks = static_cast<int>(K / 32);
+    a.ctiles = static_cast<int>(ceil_div(a.kblocks, 4));
+    a.chunks = static_cast<int>(ceil_div(a.kblocks, 32));
+    const int64_t tiles = (a.n + 127 * std::min<int64_t>(E, a.n)) / 128;
+    if (tiles * 128 >= kInt32End) return MX_ERR_SHAPE;
+    a.tiles = static_cast<int>(tiles);
+    a.units = T * a.chunks + tiles;
+    a.vec32 = reinterpret_cast<uintptr_t>(x) % 32 == 0 && ld_x % 16 == 0 && reinterpret_cast<uintptr_t>(q) % 32 == 0;
+    const bool fp4 = format == MX_FORMAT_E2M1;
+    const int64_t grid = std::min<int64_t>(ceil_div(a.units, kExThreads / 32), int64_t(d->sms) * d->dispatch_blocks_per_sm[fp4]);
+    if (fp4)
+        dispatch_kernel<true><<<static_cast<unsigned>(grid), kExThreads, 0, stream>>>(a);
+    else
+        dispatch_kernel<false><<<static_cast<unsigned>(grid), kExThreads, 0, stream>>>(a);
+    return launched();
+}
+
+mx_status mx_combine(const void* c, mx_out_dtype c_dtype, int64_t rows, int64_t ld_c, const int32_t* slot_row,
+                     const float* weights, int64_t T, int64_t topk, int64_t N, void* y, mx_out_dtype y_dtype, int64_t ld_y,
+                     mx_stream stream) {
+    if (rows < 0 || T < 0 || N < 0 || topk < 1 || !elt_ok(c_dtype) || !elt_ok(y_dtype)) return MX_ERR_ARG;
+    if (ld_c < N || ld_y < N || rows >= kInt32End || T >= kInt32End || N >= kInt32End || topk >= kInt32End ||
+        T * topk >= kInt32End)
+        return MX_ERR_SHAPE;
+    if (T == 0 || N == 0) return MX_OK;
+    if ((!c && rows > 0) || !slot_row || !y) return MX_ERR_ARG;
+    if (!elt_aligned(c, c_dtype) || !elt_aligned(y, y_dtype) || !word_aligned(slot_row) || !word_aligned(weights))
+        return MX_ERR_ALIGN;
+    const DeviceInfo* d = nullptr;
+    if (mx_status st = check_device(&d)) return st;
+    CombineArgs a{};
+    a.c = c;
+    a.slot_row = slot_row;
+    a.w = weights;
+    a.y = y;
+    a.T = T;
+    a.N = N;
+    a.ldc = ld_c;
+    a.ldy = ld_y;
+    a.rows = rows;
+    a.k = static_cast<int>(topk);
+    a.chunks = static_cast<int>(ceil_div(N, 256));
+    a.vec = rows_vec(c, ld_c, c_dtype) && rows_vec(y, ld_y, y_dtype);
+    return launch_combine_types(a, c_dtype, y_dtype, false, stream);
+}
+
+mx_status mx_combine_bwd(const void* dy, mx_out_dtype y_dtype, int64_t ld_dy, const void* c, mx_out_dtype c_dtype,
+                         int64_t rows, int64_t ld_c, const int32_t* slot_row, const float* weights, int64_t T, int64_t topk,
+                         int64_t N, void* d_c, int64_t ld_dc, float* d_weights, mx_stream stream) {
+    if (rows < 0 || T < 0 || N < 0 || topk < 1 || !elt_ok(c_dtype) || !elt_ok(y_dtype)) return MX_ERR_ARG;
+    if (!d_c && !d_weights) return MX_ERR_ARG;
+    if (ld_dy < N || (d_weights && ld_c < N) || (d_c && ld_dc < N) || rows >= kInt32End || T >= kInt32End ||
+        N >= kInt32End || topk >= kInt32End || T * topk >= kInt32End)
+        return MX_ERR_SHAPE;
+    if (T == 0) return MX_OK;
+    if (!slot_row || (N > 0 && (!dy || (d_weights && !c && rows > 0)))) return MX_ERR_ARG;
+    if (!elt_aligned(dy, y_dtype) || !elt_aligned(c, c_dtype) || !elt_aligned(d_c, c_dtype) || !word_aligned(slot_row) ||
+        !word_aligned(weights) || !word_aligned(d_weights))
+        return MX_ERR_ALIGN;
+    const DeviceInfo* d = nullptr;
+    if (mx_status st = check_device(&d)) return st;
+    CombineArgs a{};
+    a.c = c;
+    a.slot_row = slot_row;
+    a.w = weights;
+    a.T = T;
+    a.N = N;
+    a.ldc = ld_c;
+    a.rows = rows;
+    a.k = static_cast<int>(topk);
+    a.dy = dy;
+    a.lddy = ld_dy;
+    a.dc = d_c;
+    a.lddc = ld_dc;
+    a.dw = d_weights;
+    a.vec = rows_vec(dy, ld_dy, y_dtype) && (!d_weights || rows_vec(c, ld_c, c_dtype)) &&
+            (!d_c || rows_vec(d_c, ld_dc, c_dtype));
+    return launch_combine_types(a, c_dtype, y_dtype, true, stream);
+}
 
 }  // extern "C"

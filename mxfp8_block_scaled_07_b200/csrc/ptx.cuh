@@ -278,6 +278,16 @@ __device__ __forceinline__ void tc_mma_mxf8_pair_elect(uint32_t d_tmem, uint64_t
         "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate), "r"(sfa_tmem), "r"(sfb_tmem)
         : "memory");
 }
+// MXFP4: packed E2M1 operands, K = 64 per instruction, two E8M0 scales (blocks of 32) per row and instruction.
+__device__ __forceinline__ void tc_mma_mxf4_pair_elect(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
+                                                       uint32_t sfa_tmem, uint32_t sfb_tmem, uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred e, p;\n\telect.sync _|e, 0xffffffff;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "@e tcgen05.mma.cta_group::2.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%5], [%6], p;\n\t}" ::"r"(
+            d_tmem),
+        "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate), "r"(sfa_tmem), "r"(sfb_tmem)
+        : "memory");
+}
 __device__ __forceinline__ void tc_commit_elect(uint64_t* bar) {
     asm volatile(MX_ELECT_PRED "tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(
                      smem_u32(bar))
@@ -325,6 +335,19 @@ __host__ __device__ constexpr uint32_t idesc_mxf8_e4m3(uint32_t M, uint32_t N, u
            | ((N >> 3) << 17)      // N / 8
            | (1u << 23)            // scale format: E8M0
            | ((M >> 4) << 24)      // M / 16
+           | (sf_id << 29);        // A scale-factor id
+}
+
+// Instruction descriptor for kind::mxf4: E2M1 x E2M1 (format code 1), E8M0 scales, both operands K-major,
+// K = 64; sf_id (0 or 2) picks the pair of scale bytes inside each 32-bit TMEM scale word. M is a multiple
+// of 128.
+__host__ __device__ constexpr uint32_t idesc_mxf4(uint32_t M, uint32_t N, uint32_t sf_id) {
+    return (sf_id << 4)            // B scale-factor id
+           | (1u << 7)             // A format: E2M1
+           | (1u << 10)            // B format: E2M1
+           | ((N >> 3) << 17)      // N / 8
+           | (1u << 23)            // scale format: E8M0
+           | ((M >> 7) << 27)      // M / 128
            | (sf_id << 29);        // A scale-factor id
 }
 

@@ -18,6 +18,9 @@ LIB_PATH = os.path.join(_HERE, "libmx.so")
 
 MX_ROWWISE, MX_COLWISE, MX_SWIZZLE = 1, 2, 4
 MX_OUT_F32, MX_OUT_BF16 = 0, 1
+MX_SCORE = {"softmax": 0, "sigmoid": 1}
+MX_GROUP = {"max": 0, "top2": 1}
+MX_FORMAT = {"mxfp8": 0, "mxfp4": 1}
 _STATUS = {0: "MX_OK", -1: "MX_ERR_ARG", -2: "MX_ERR_SHAPE", -3: "MX_ERR_ALIGN", -4: "MX_ERR_CUDA",
            -5: "MX_ERR_UNSUPPORTED", -6: "MX_ERR_DEVICE"}
 
@@ -78,6 +81,25 @@ def lib() -> ctypes.CDLL:
     L.mx_grid_equal_multi.restype = I32
     L.mx_quantize_compare_multi.argtypes = [P, P, I64, P, P, P]
     L.mx_quantize_compare_multi.restype = I32
+    F32 = ctypes.c_float
+    for name, args in (
+            ("mx_quantize_fp4", [P, I64, I64, I64, I32, P, P, P, P, P]),
+            ("mx_dequantize_fp4", [P, P, I64, I64, I32, P, I64, P]),
+            ("mx_gemm_fp4", [P, P, P, P, I64, I64, I64, P, I64, I32, P]),
+            ("mx_grouped_gemm_fp4", [P, P, P, P, P, I64, I64, I64, I64, P, I64, I32, P]),
+            ("mx_route", [P, I32, I64, I64, I64, P, I32, I64, I64, I32, I64, I32, F32, P, P, P]),
+            ("mx_route_bwd", [P, P, I32, I64, I64, I64, P, I32, I64, I32, F32, P, I64, P]),
+            ("mx_route_plan", [P, I64, I64, P, P, P, P, P]),
+            ("mx_dispatch_quantize", [P, I64, I64, I64, P, I64, P, I64, I32, P, P, P]),
+            ("mx_combine", [P, I32, I64, I64, P, P, I64, I64, I64, P, I32, I64, P]),
+            ("mx_combine_bwd", [P, I32, I64, P, I32, I64, I64, P, P, I64, I64, I64, P, I64, P, P])):
+        fn = getattr(L, name)
+        fn.argtypes = args
+        fn.restype = I32
+    L.mx_route_plan_workspace_bytes.argtypes = [I64, I64]
+    L.mx_route_plan_workspace_bytes.restype = I64
+    L.mx_grouped_scale_bytes.argtypes = [I64, I64, I64]
+    L.mx_grouped_scale_bytes.restype = I64
     L.mx_status_string.argtypes = [I32]
     L.mx_status_string.restype = ctypes.c_char_p
     L.mx_device_error.argtypes = [ctypes.POINTER(ctypes.c_uint32)]
@@ -301,6 +323,253 @@ def quantize_block128(x: torch.Tensor, pow2_scales: bool, out=None):
                                     ctypes.c_void_p(_stream(x.device)))
     _check(st, "mx_quantize_block128")
     return q, sc
+
+
+# ---- MXFP4 and expert routing: tensors are checked here (type, device, layout), sizes by the library ----
+
+def _need(ok: bool, what: str):
+    if not ok:
+        raise MxError(-1, what)
+
+
+def _matrix(t, what: str, dtypes, shape=None, dev=None) -> int:
+    """Checks a 2-D CUDA tensor with unit column stride (and its shape and device); returns its address."""
+    _need(isinstance(t, torch.Tensor) and t.is_cuda and t.dim() == 2 and t.dtype in dtypes
+          and (t.stride(1) == 1 or t.shape[1] <= 1) and (dev is None or t.device == dev)
+          and (shape is None or tuple(t.shape) == tuple(shape)), what)
+    return t.data_ptr()
+
+
+def _packed(t, what: str, dtype, numel: int, dev) -> int:
+    """Checks a contiguous CUDA tensor of `numel` elements on `dev`; returns its address."""
+    _need(isinstance(t, torch.Tensor) and t.is_cuda and t.dtype == dtype and t.is_contiguous()
+          and t.numel() == numel and t.device == dev, what)
+    return t.data_ptr()
+
+
+def _ld(t) -> int:
+    """Row stride in elements. A tensor of at most one row may carry any stride: its own width stands for it."""
+    return t.stride(0) if t.shape[0] > 1 else max(t.stride(0), t.shape[1])
+
+
+def _call(name: str, dev, *args):
+    """One library call on `dev`'s current stream, with `dev` as the current device."""
+    fn = getattr(lib(), name)
+    if dev.index == torch.cuda.current_device():
+        st = fn(*args, torch.cuda.current_stream(dev).cuda_stream)
+    else:
+        with torch.cuda.device(dev):
+            st = fn(*args, torch.cuda.current_stream(dev).cuda_stream)
+    if st != 0:
+        raise MxError(st, name)
+
+
+_FLOATS = (torch.float32, torch.bfloat16)
+_U8, _BF16, _I32, _F32 = (torch.uint8,), (torch.bfloat16,), (torch.int32,), (torch.float32,)
+
+
+def quantize_fp4(x: torch.Tensor, rowwise: bool = True, colwise: bool = False, swizzle: bool = True, out=None):
+    """mx_quantize_fp4 on a 2-D BF16 CUDA tensor. Returns (q_row [M, K/2], s_row, q_col [K, M/2], s_col), uint8;
+    two E2M1 codes per byte, the even element in the low four bits; scales as quantize() gives them. Entries of a
+    direction not requested are None. ``out`` may supply the four buffers."""
+    px = _matrix(x, "quantize_fp4: x must be a 2-D BF16 CUDA tensor with unit column stride", _BF16)
+    M, K = x.shape
+    dev = x.device
+    flags = (MX_ROWWISE if rowwise else 0) | (MX_COLWISE if colwise else 0) | (MX_SWIZZLE if swizzle else 0)
+
+    def scale_bytes(rows, n):
+        return swizzled_scale_bytes(rows, n // 32) if swizzle else rows * (n // 32)
+
+    if out is None:
+        _need(K % 32 == 0 and (not colwise or M % 32 == 0), "quantize_fp4: blocks of 32 along the quantized axis")
+        u8 = dict(dtype=torch.uint8, device=dev)
+        q_row = torch.empty((M, K // 2), **u8) if rowwise else None
+        s_row = torch.empty(scale_bytes(M, K) if swizzle else (M, K // 32), **u8) if rowwise else None
+        q_col = torch.empty((K, M // 2), **u8) if colwise else None
+        s_col = torch.empty(scale_bytes(K, M) if swizzle else (K, M // 32), **u8) if colwise else None
+    else:
+        q_row, s_row, q_col, s_col = out
+    p = [None] * 4
+    if rowwise:
+        p[0] = _packed(q_row, "quantize_fp4: q_row", torch.uint8, M * K // 2, dev)
+        p[1] = _packed(s_row, "quantize_fp4: s_row", torch.uint8, scale_bytes(M, K), dev)
+    if colwise:
+        p[2] = _packed(q_col, "quantize_fp4: q_col", torch.uint8, M * K // 2, dev)
+        p[3] = _packed(s_col, "quantize_fp4: s_col", torch.uint8, scale_bytes(K, M), dev)
+    _call("mx_quantize_fp4", dev, px, M, K, _ld(x), flags, *p)
+    return q_row, s_row, q_col, s_col
+
+
+def dequantize_fp4(q: torch.Tensor, s: torch.Tensor, swizzled: bool = True, out=None):
+    """mx_dequantize_fp4: the BF16 values [M, K] of packed codes q [M, K/2] and their scales (the tensor-core
+    layout, or raw [M, K/32] with swizzled=False)."""
+    dev = q.device
+    pq = _matrix(q, "dequantize_fp4: q must be a 2-D uint8 CUDA tensor", _U8)
+    M, K = q.shape[0], 2 * q.shape[1]
+    _packed(q, "dequantize_fp4: q must be contiguous", torch.uint8, M * K // 2, dev)
+    ps = _packed(s, "dequantize_fp4: s", torch.uint8, swizzled_scale_bytes(M, K // 32) if swizzled else M * (K // 32), dev)
+    if out is None:
+        out = torch.empty((M, K), dtype=torch.bfloat16, device=dev)
+    _call("mx_dequantize_fp4", dev, pq, ps, M, K, int(swizzled), _matrix(out, "dequantize_fp4: out", _BF16, (M, K), dev),
+          _ld(out))
+    return out
+
+
+def gemm_fp4(qa, sa_swz, qb, sb_swz, out_dtype=torch.bfloat16, out=None):
+    """mx_gemm_fp4: C[M, N] = A . B^T from packed K-major E2M1 operands (qa [M, K/2], qb [N, K/2]) and
+    tensor-core-layout scales."""
+    dev = qa.device
+    _matrix(qa, "gemm_fp4: qa", _U8)
+    _matrix(qb, "gemm_fp4: qb", _U8, (qb.shape[0], qa.shape[1]), dev)
+    M, N, K = qa.shape[0], qb.shape[0], 2 * qa.shape[1]
+    pa, pb = (_packed(t, "gemm_fp4: packed operands", torch.uint8, n * K // 2, dev) for t, n in ((qa, M), (qb, N)))
+    psa, psb = (_packed(t, "gemm_fp4: scales", torch.uint8, swizzled_scale_bytes(n, K // 32), dev)
+                for t, n in ((sa_swz, M), (sb_swz, N)))
+    if out is None:
+        out = torch.empty((M, N), dtype=out_dtype, device=dev)
+    _call("mx_gemm_fp4", dev, pa, psa, pb, psb, M, N, K, _matrix(out, "gemm_fp4: out", _FLOATS, (M, N), dev), _ld(out),
+          _out_code(out.dtype))
+    return out
+
+
+def grouped_gemm_fp4(qa, sa_swz, qb, sb_swz, row_offsets, out_dtype=torch.bfloat16, out=None):
+    """mx_grouped_gemm_fp4: rows [off[g], off[g+1]) of A (packed [rows, K/2]) against qb[g] ([G, N, K/2] packed,
+    sb_swz G consecutive layouts). sa_swz: A's grouped layout, at least as many bytes as the groups' rows need
+    (grouped_scale_bytes_bound() always suffices). row_offsets: int32 CUDA [G + 1]."""
+    dev = qa.device
+    _matrix(qa, "grouped_gemm_fp4: qa", _U8)
+    _need(isinstance(qb, torch.Tensor) and qb.dim() == 3 and qb.shape[2] == qa.shape[1], "grouped_gemm_fp4: qb must be [G, N, K/2]")
+    rows, K = qa.shape[0], 2 * qa.shape[1]
+    G, N = qb.shape[0], qb.shape[1]
+    pa = _packed(qa, "grouped_gemm_fp4: qa must be contiguous", torch.uint8, rows * K // 2, dev)
+    pb = _packed(qb, "grouped_gemm_fp4: qb", torch.uint8, G * N * K // 2, dev)
+    psb = _packed(sb_swz, "grouped_gemm_fp4: sb_swz", torch.uint8, G * swizzled_scale_bytes(N, K // 32), dev)
+    _need(isinstance(sa_swz, torch.Tensor) and sa_swz.numel() >= swizzled_scale_bytes(rows, K // 32), "grouped_gemm_fp4: sa_swz")
+    psa = _packed(sa_swz, "grouped_gemm_fp4: sa_swz", torch.uint8, sa_swz.numel(), dev)
+    poff = _packed(row_offsets, "grouped_gemm_fp4: row_offsets must be int32 [G + 1]", torch.int32, G + 1, dev)
+    if out is None:
+        out = torch.empty((rows, N), dtype=out_dtype, device=dev)
+    _call("mx_grouped_gemm_fp4", dev, pa, psa, pb, psb, poff, G, rows, N, K,
+          _matrix(out, "grouped_gemm_fp4: out", _FLOATS, (rows, N), dev), _ld(out), _out_code(out.dtype))
+    return out
+
+
+def route(logits: torch.Tensor, topk: int, score: str = "softmax", bias=None, groups: int = 1, topk_groups: int = 1,
+          group_score: str = "max", renormalize: bool = True, scale: float = 1.0, out=None):
+    """mx_route: the topk experts of every token and their weights from router logits [T, E] (fp32 or BF16).
+
+    score: "softmax" or "sigmoid"; bias: fp32 [E] added to the scores for the choice only; groups, topk_groups,
+    group_score ("max" or "top2"): experts outside the best groups are left out; weights are scale * score, over the
+    chosen experts' sum if renormalize. Returns (ids int32 [T, topk], weights fp32 [T, topk]); id -1 and weight 0
+    where no expert is left (logits of -inf or NaN take an expert out)."""
+    p = _matrix(logits, "route: logits must be a 2-D fp32 or BF16 CUDA tensor with unit column stride", _FLOATS)
+    _need(score in MX_SCORE and group_score in MX_GROUP, "route: score is 'softmax' or 'sigmoid', group_score 'max' or 'top2'")
+    T, E = logits.shape
+    dev = logits.device
+    pb = None if bias is None else _packed(bias, "route: bias must be fp32 [E]", torch.float32, E, dev)
+    if out is None:
+        _need(topk >= 1, "route: topk")
+        out = (torch.empty((T, topk), dtype=torch.int32, device=dev), torch.empty((T, topk), dtype=torch.float32, device=dev))
+    ids, weights = out
+    _call("mx_route", dev, p, _out_code(logits.dtype), T, E, _ld(logits), pb, MX_SCORE[score], groups, topk_groups,
+          MX_GROUP[group_score], topk, int(renormalize), scale, _packed(ids, "route: ids", torch.int32, T * topk, dev),
+          _packed(weights, "route: weights", torch.float32, T * topk, dev))
+    return ids, weights
+
+
+def route_backward(d_weights: torch.Tensor, logits: torch.Tensor, ids: torch.Tensor, score: str = "softmax",
+                   renormalize: bool = True, scale: float = 1.0, out=None):
+    """mx_route_bwd: the gradient of route()'s weights with respect to the logits, the choice (ids) held fixed."""
+    p = _matrix(logits, "route_backward: logits must be a 2-D fp32 or BF16 CUDA tensor with unit column stride", _FLOATS)
+    _need(score in MX_SCORE and ids.dim() == 2, "route_backward: score is 'softmax' or 'sigmoid', ids [T, topk]")
+    T, E = logits.shape
+    dev, topk = logits.device, ids.shape[1]
+    if out is None:
+        out = torch.empty((T, E), dtype=logits.dtype, device=dev)
+    _call("mx_route_bwd", dev, _packed(d_weights, "route_backward: d_weights must be fp32 [T, topk]", torch.float32, T * topk, dev),
+          p, _out_code(logits.dtype), T, E, _ld(logits), _packed(ids, "route_backward: ids must be int32 [T, topk]", torch.int32, T * topk, dev),
+          MX_SCORE[score], topk, int(renormalize), scale, _matrix(out, "route_backward: out", (logits.dtype,), (T, E), dev), _ld(out))
+    return out
+
+
+def route_plan(ids: torch.Tensor, experts: int, out=None):
+    """mx_route_plan: (row_offsets int32 [experts + 1], slot_row int32 like ids, counts int32 [experts]) of the
+    experts' ids [T, topk]. row_offsets always ends at ids.numel(): slots without an expert are padding rows of the
+    last group, and their slot_row is ~row."""
+    _need(isinstance(ids, torch.Tensor) and ids.is_cuda, "route_plan: ids must be an int32 CUDA tensor")
+    dev, n = ids.device, ids.numel()
+    p = _packed(ids, "route_plan: ids must be a contiguous int32 tensor", torch.int32, n, dev)
+    size = int(lib().mx_route_plan_workspace_bytes(n, experts))
+    _need(size >= 0, "route_plan: 1 to 1024 experts")
+    i32 = dict(dtype=torch.int32, device=dev)
+    if out is None:
+        out = (torch.empty(experts + 1, **i32), torch.empty(ids.shape, **i32), torch.empty(experts, **i32))
+    off, slot_row, counts = out
+    ws = torch.empty(size, dtype=torch.uint8, device=dev) if size else None
+    _call("mx_route_plan", dev, p, n, experts, _packed(off, "route_plan: row_offsets", torch.int32, experts + 1, dev),
+          _packed(slot_row, "route_plan: slot_row", torch.int32, n, dev),
+          _packed(counts, "route_plan: counts", torch.int32, experts, dev), None if ws is None else ws.data_ptr())
+    return off, slot_row, counts
+
+
+def grouped_scale_bytes_bound(rows: int, groups: int, kblocks: int) -> int:
+    """mx_grouped_scale_bytes: bytes that hold the grouped scale layout of any split of `rows` into `groups`."""
+    return int(lib().mx_grouped_scale_bytes(rows, groups, kblocks))
+
+
+def dispatch_quantize(x: torch.Tensor, slot_row: torch.Tensor, row_offsets: torch.Tensor, fmt: str = "mxfp8", out=None):
+    """mx_dispatch_quantize: tokens x [T, K] (BF16) quantized into the experts' rows that route_plan() laid out.
+    Returns (q, s): uint8 codes [T * topk, K] ("mxfp8") or [T * topk, K/2] ("mxfp4") and the grouped scale layout
+    (grouped_scale_bytes_bound() bytes, zeros where no row lies): the A operand of the grouped products."""
+    p = _matrix(x, "dispatch_quantize: x must be a 2-D BF16 CUDA tensor with unit column stride", _BF16)
+    _need(fmt in MX_FORMAT and slot_row.dim() == 2 and slot_row.shape[0] == x.shape[0] and row_offsets.numel() >= 2,
+          "dispatch_quantize: fmt is 'mxfp8' or 'mxfp4', slot_row [T, topk], row_offsets [E + 1]")
+    T, K = x.shape
+    dev, topk, E = x.device, slot_row.shape[1], row_offsets.numel() - 1
+    width = K if fmt == "mxfp8" else K // 2
+    size = max(grouped_scale_bytes_bound(T * topk, E, K // 32), 0)
+    if out is None:
+        out = (torch.empty((T * topk, width), dtype=torch.uint8, device=dev), torch.empty(size, dtype=torch.uint8, device=dev))
+    q, s = out
+    _call("mx_dispatch_quantize", dev, p, T, K, _ld(x), _packed(slot_row, "dispatch_quantize: slot_row must be int32", torch.int32, T * topk, dev),
+          topk, _packed(row_offsets, "dispatch_quantize: row_offsets must be int32", torch.int32, E + 1, dev), E, MX_FORMAT[fmt],
+          _packed(q, "dispatch_quantize: q", torch.uint8, T * topk * width, dev), _packed(s, "dispatch_quantize: s", torch.uint8, size, dev))
+    return q, s
+
+
+def combine(rows: torch.Tensor, slot_row: torch.Tensor, weights=None, out_dtype=None, out=None):
+    """mx_combine: y[t] = sum_j weights[t, j] * rows[slot_row[t, j]] (weights None: all 1), in fp32, rounded once to
+    out_dtype (rows' type if None). Slots with a negative slot_row have no part. With weights=None it is also the
+    gradient of an unquantized dispatch."""
+    p = _matrix(rows, "combine: rows must be a 2-D fp32 or BF16 CUDA tensor with unit column stride", _FLOATS)
+    _need(slot_row.dim() == 2, "combine: slot_row [T, topk]")
+    (T, topk), N, dev = slot_row.shape, rows.shape[1], rows.device
+    if out is None:
+        out = torch.empty((T, N), dtype=out_dtype or rows.dtype, device=dev)
+    _call("mx_combine", dev, p, _out_code(rows.dtype), rows.shape[0], _ld(rows),
+          _packed(slot_row, "combine: slot_row must be int32", torch.int32, T * topk, dev),
+          None if weights is None else _packed(weights, "combine: weights must be fp32 [T, topk]", torch.float32, T * topk, dev),
+          T, topk, N, _matrix(out, "combine: out", _FLOATS, (T, N), dev), _out_code(out.dtype), _ld(out))
+    return out
+
+
+def combine_backward(dy: torch.Tensor, rows: torch.Tensor, slot_row: torch.Tensor, weights=None, need_weights: bool = True, out=None):
+    """mx_combine_bwd: (d_rows like rows, d_weights fp32 [T, topk]) from dy [T, N]. need_weights=False leaves
+    d_weights out (None), and rows is then only asked for its shape and type. Padding rows get zeros."""
+    p = _matrix(rows, "combine_backward: rows must be a 2-D fp32 or BF16 CUDA tensor with unit column stride", _FLOATS)
+    _need(slot_row.dim() == 2, "combine_backward: slot_row [T, topk]")
+    (T, topk), (R, N), dev = slot_row.shape, rows.shape, rows.device
+    if out is None:
+        # Every row of a plan's partition is written; rows that no slot names stay as they are, so they start as 0.
+        out = (torch.empty((R, N), dtype=rows.dtype, device=dev) if R == T * topk else torch.zeros((R, N), dtype=rows.dtype, device=dev),
+               torch.empty((T, topk), dtype=torch.float32, device=dev) if need_weights else None)
+    d_rows, d_weights = out
+    _call("mx_combine_bwd", dev, _matrix(dy, "combine_backward: dy must be [T, N], fp32 or BF16", _FLOATS, (T, N), dev), _out_code(dy.dtype), _ld(dy),
+          p, _out_code(rows.dtype), R, _ld(rows), _packed(slot_row, "combine_backward: slot_row must be int32", torch.int32, T * topk, dev),
+          None if weights is None else _packed(weights, "combine_backward: weights must be fp32 [T, topk]", torch.float32, T * topk, dev),
+          T, topk, N, _matrix(d_rows, "combine_backward: d_rows", (rows.dtype,), (R, N), dev), _ld(d_rows),
+          None if d_weights is None else _packed(d_weights, "combine_backward: d_weights", torch.float32, T * topk, dev))
+    return d_rows, d_weights
 
 
 def grid_equal(a: torch.Tensor, b: torch.Tensor, out=None):
