@@ -29,8 +29,9 @@ struct DispatchArgs {
     uint8_t* q;               // [T * k, K] E4M3 or [T * k, K / 2] packed E2M1
     uint8_t* s;               // grouped tensor-core layout, `tiles` 128-row tiles of ctiles blocks
     int64_t T, K, ldx, n;     // n = T * k rows
-    int64_t units;            // T * chunks warp units, then `tiles` units for the layout's pads
-    int k, E, chunks, ctiles, kblocks, tiles;
+    uint32_t tok_units, units;    // T * chunks warp units, then `tiles` units for the layout's pads
+    FastDiv chunks;           // pieces of 1024 columns per token
+    int k, E, ctiles, kblocks, tiles;
     int vec32;                // x rows and q 32-byte aligned: 256-bit accesses
 };
 
@@ -90,13 +91,11 @@ __global__ void __launch_bounds__(kExThreads) dispatch_kernel(const __grid_const
     __shared__ int32_t warp_sums[kExThreads / 32];
     expert_tiles(a.offsets, a.E, off, first, warp_sums);
     const int lane = threadIdx.x & 31;
-    const int64_t nwarps = static_cast<int64_t>(gridDim.x) * (kExThreads / 32);
+    const uint32_t nwarps = gridDim.x * (kExThreads / 32);
     const int64_t row_bytes = FP4 ? a.K / 2 : a.K;
-    const int64_t tok_units = a.T * a.chunks;
-    for (int64_t u = static_cast<int64_t>(blockIdx.x) * (kExThreads / 32) + (threadIdx.x >> 5); u < a.units;
-         u += nwarps) {
-        if (u >= tok_units) {
-            const int tile = static_cast<int>(u - tok_units);
+    for (uint32_t u = blockIdx.x * (kExThreads / 32) + (threadIdx.x >> 5); u < a.units; u += nwarps) {
+        if (u >= a.tok_units) {
+            const int tile = static_cast<int>(u - a.tok_units);
             int valid = 0;
             if (tile < first[a.E]) {
                 const int e = last_not_above(first, a.E, tile);
@@ -111,8 +110,9 @@ __global__ void __launch_bounds__(kExThreads) dispatch_kernel(const __grid_const
             }
             continue;
         }
-        const int64_t t = u / a.chunks;
-        const int kb = static_cast<int>(u % a.chunks) * 32 + lane;
+        const uint32_t tu = a.chunks.div(u);
+        const int64_t t = tu;
+        const int kb = static_cast<int>(u - tu * a.chunks.d) * 32 + lane;
         const bool in = kb < a.kblocks;
         Block32 b;
         b.v[0] = b.v[1] = b.v[2] = b.v[3] = make_uint4(0, 0, 0, 0);
@@ -197,7 +197,9 @@ struct CombineArgs {
     const float* w;           // [T, k] or null (all 1)
     void* y;                  // [T, N], row stride ldy
     int64_t T, N, ldc, ldy, rows;
-    int k, chunks;
+    uint32_t units;           // T * chunks, < 2^31
+    FastDiv chunks;           // pieces of a row, 512 bytes of c each
+    int k;
     int vec;                  // 16-byte aligned rows: vector accesses
     // backward
     const void* dy;           // [T, N], row stride lddy
@@ -206,183 +208,264 @@ struct CombineArgs {
     int64_t lddy, lddc;
 };
 
-// Eight consecutive columns per lane: 16 bytes of BF16, 32 of fp32.
-template <class ELT>
-__device__ __forceinline__ void load8(const ELT* p, float (&f)[8]) {
-    if constexpr (sizeof(ELT) == 2) {
-        const uint4 v = ld_stream_v4(p);
-        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            f[2 * i] = __uint_as_float(w[i] << 16);
-            f[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
-        }
-    } else {
-        const uint4 v0 = ld_stream_v4(p), v1 = ld_stream_v4(p + 4);
-        const uint32_t w[8] = {v0.x, v0.y, v0.z, v0.w, v1.x, v1.y, v1.z, v1.w};
-#pragma unroll
-        for (int i = 0; i < 8; ++i) f[i] = __uint_as_float(w[i]);
-    }
-}
-
-template <class ELT>
-__device__ __forceinline__ void store8(ELT* p, const float (&f)[8]) {
-    if constexpr (sizeof(ELT) == 2) {
-        uint32_t w[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const __nv_bfloat162 h = __floats2bfloat162_rn(f[2 * i], f[2 * i + 1]);
-            w[i] = *reinterpret_cast<const uint32_t*>(&h);
-        }
-        *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
-    } else {
-        reinterpret_cast<float4*>(p)[0] = make_float4(f[0], f[1], f[2], f[3]);
-        reinterpret_cast<float4*>(p)[1] = make_float4(f[4], f[5], f[6], f[7]);
-    }
-}
+constexpr int kCombineSlots = 8;      // slots whose rows are in flight together
 
 __device__ __forceinline__ float elt_to_float(uint16_t v) { return __uint_as_float(static_cast<uint32_t>(v) << 16); }
 __device__ __forceinline__ float elt_to_float(float v) { return v; }
 __device__ __forceinline__ void float_to_elt(float f, uint16_t& o) { o = __bfloat16_as_ushort(__float2bfloat16_rn(f)); }
 __device__ __forceinline__ void float_to_elt(float f, float& o) { o = f; }
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+    const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&h);
+}
 
-// A lane's eight columns of the 256-column piece that starts at column c0: consecutive ones with vector
-// accesses, else every 32nd (element accesses stay coalesced). Entries past N read 0.
-template <class ELT>
-__device__ __forceinline__ void load_piece(const ELT* row, int64_t c0, int64_t N, int lane, bool vec, float (&f)[8]) {
-    if (vec) {
-        const int64_t c = c0 + lane * 8;
-        if (c + 8 <= N) {
-            load8(row + c, f);
+// A piece of a row is 32 lanes x P elements. With vector accesses a lane has P consecutive elements
+// (c0 + P lane ..), else every 32nd (c0 + lane + 32 i), so that element accesses stay coalesced.
+template <int P>
+__device__ __forceinline__ int64_t piece_col(int64_t c0, int lane, int i, bool vec) {
+    return vec ? c0 + lane * P + i : c0 + lane + 32 * i;
+}
+
+// A lane's part of a piece of c, as it lies in memory: 8 BF16 or 4 fp32 in 16 bytes. Entries past N are 0.
+__device__ __forceinline__ uint4 load_raw(const uint16_t* row, int64_t c0, int64_t N, int lane, bool vec) {
+    if (vec && c0 + lane * 8 + 8 <= N) return ld_stream_v4(row + c0 + lane * 8);
+    uint32_t w[4] = {0, 0, 0, 0};
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const int64_t col = piece_col<8>(c0, lane, i, vec);
+        if (col < N) w[i >> 1] |= static_cast<uint32_t>(row[col]) << (16 * (i & 1));
+    }
+    return make_uint4(w[0], w[1], w[2], w[3]);
+}
+__device__ __forceinline__ uint4 load_raw(const float* row, int64_t c0, int64_t N, int lane, bool vec) {
+    if (vec && c0 + lane * 4 + 4 <= N) return ld_stream_v4(row + c0 + lane * 4);
+    uint32_t w[4] = {0, 0, 0, 0};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int64_t col = piece_col<4>(c0, lane, i, vec);
+        if (col < N) w[i] = __float_as_uint(row[col]);
+    }
+    return make_uint4(w[0], w[1], w[2], w[3]);
+}
+__device__ __forceinline__ void unpack(const uint4& v, float (&f)[8]) {
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        f[2 * i] = __uint_as_float(w[i] << 16);
+        f[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+    }
+}
+__device__ __forceinline__ void unpack(const uint4& v, float (&f)[4]) {
+    f[0] = __uint_as_float(v.x);
+    f[1] = __uint_as_float(v.y);
+    f[2] = __uint_as_float(v.z);
+    f[3] = __uint_as_float(v.w);
+}
+
+// P elements of a row in any of the two types.
+template <int P, class ELT>
+__device__ __forceinline__ void load_floats(const ELT* row, int64_t c0, int64_t N, int lane, bool vec, float (&f)[P]) {
+    if constexpr (P * sizeof(ELT) == 16) {
+        unpack(load_raw(row, c0, N, lane, vec), f);
+    } else {
+        if (vec && c0 + lane * P + P <= N) {
+            const ELT* p = row + c0 + lane * P;
+            if constexpr (sizeof(ELT) == 2) {               // 4 BF16
+                const uint2 v = *reinterpret_cast<const uint2*>(p);
+                f[0] = __uint_as_float(v.x << 16);
+                f[1] = __uint_as_float(v.x & 0xFFFF0000u);
+                f[2] = __uint_as_float(v.y << 16);
+                f[3] = __uint_as_float(v.y & 0xFFFF0000u);
+            } else {                                        // 8 fp32
+                const float4 a = reinterpret_cast<const float4*>(p)[0], b = reinterpret_cast<const float4*>(p)[1];
+                f[0] = a.x; f[1] = a.y; f[2] = a.z; f[3] = a.w;
+                f[4] = b.x; f[5] = b.y; f[6] = b.z; f[7] = b.w;
+            }
         } else {
 #pragma unroll
-            for (int i = 0; i < 8; ++i) f[i] = c + i < N ? elt_to_float(row[c + i]) : 0.0f;
+            for (int i = 0; i < P; ++i) {
+                const int64_t col = piece_col<P>(c0, lane, i, vec);
+                f[i] = col < N ? elt_to_float(row[col]) : 0.0f;
+            }
+        }
+    }
+}
+template <int P, class ELT>
+__device__ __forceinline__ void store_floats(ELT* row, int64_t c0, int64_t N, int lane, bool vec, const float (&f)[P]) {
+    if (vec && c0 + lane * P + P <= N) {
+        ELT* p = row + c0 + lane * P;
+        if constexpr (sizeof(ELT) == 2 && P == 8) {
+            st_global_v4(p, make_uint4(pack_bf16(f[0], f[1]), pack_bf16(f[2], f[3]), pack_bf16(f[4], f[5]), pack_bf16(f[6], f[7])));
+        } else if constexpr (sizeof(ELT) == 2) {
+            *reinterpret_cast<uint2*>(p) = make_uint2(pack_bf16(f[0], f[1]), pack_bf16(f[2], f[3]));
+        } else {
+#pragma unroll
+            for (int q = 0; q < P / 4; ++q)
+                st_global_v4(p + 4 * q, make_uint4(__float_as_uint(f[4 * q]), __float_as_uint(f[4 * q + 1]),
+                                                   __float_as_uint(f[4 * q + 2]), __float_as_uint(f[4 * q + 3])));
         }
     } else {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const int64_t c = c0 + lane + 32 * i;
-            f[i] = c < N ? elt_to_float(row[c]) : 0.0f;
+        for (int i = 0; i < P; ++i) {
+            const int64_t col = piece_col<P>(c0, lane, i, vec);
+            if (col < N) float_to_elt(f[i], row[col]);
         }
     }
 }
 
-template <class ELT>
-__device__ __forceinline__ void store_piece(ELT* row, int64_t c0, int64_t N, int lane, bool vec, const float (&f)[8]) {
-    if (vec && c0 + lane * 8 + 8 <= N) {
-        store8(row + c0 + lane * 8, f);
-    } else {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const int64_t c = vec ? c0 + lane * 8 + i : c0 + lane + 32 * i;
-            if (c < N) float_to_elt(f[i], row[c]);
-        }
+// Slot j0 + lane of token t for lanes < min(8, k - j0): its row (negative: none) and weight.
+__device__ __forceinline__ void load_slot(const CombineArgs& a, int64_t t, int j0, int lane, int& row, float& w) {
+    row = -1;
+    w = 1.0f;
+    if (lane < kCombineSlots && j0 + lane < a.k) {
+        row = a.slot_row[t * a.k + j0 + lane];
+        if (a.w) w = a.w[t * a.k + j0 + lane];
     }
 }
 
-// One warp per (token, 256 columns): the k rows' pieces are loaded four at a time, so that four
-// independent loads are in flight per lane, and added in slot order in fp32; one rounding at the end.
+// One warp per (token, 512 bytes of a row), warps walking the pieces of consecutive tokens together. The
+// pieces of up to 8 rows are loaded before any is used, and the next unit's slots before this unit's
+// arithmetic, so a warp has 4 KB in flight nearly all the time; terms are added in slot order in fp32 and
+// rounded once. 20 480 tokens x 8 rows x 2048 BF16: 122 us, 6.2 TB/s (four rows at a time, slots loaded one by
+// one: 271 us). Three blocks per SM: 122 us; two (no register limit) 137, four 129.
 template <class CT, class YT>
-__global__ void __launch_bounds__(kExThreads) combine_kernel(const __grid_constant__ CombineArgs a) {
+__global__ void __launch_bounds__(kExThreads, 3) combine_kernel(const __grid_constant__ CombineArgs a) {
+    constexpr int P = 16 / static_cast<int>(sizeof(CT));
     const int lane = threadIdx.x & 31;
-    const int64_t u = static_cast<int64_t>(blockIdx.x) * (kExThreads / 32) + (threadIdx.x >> 5);
-    if (u >= a.T * a.chunks) return;
-    const int64_t t = u / a.chunks, c0 = (u % a.chunks) * 256;
+    const uint32_t step = gridDim.x * (kExThreads / 32);
     const CT* c = static_cast<const CT*>(a.c);
-    float acc[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-    for (int j0 = 0; j0 < a.k; j0 += 4) {
-        float f[4][8], w[4];
-        int64_t r[4];
+    uint32_t u = blockIdx.x * (kExThreads / 32) + (threadIdx.x >> 5);
+    if (u >= a.units) return;
+    int row;
+    float w;
+    load_slot(a, a.chunks.div(u), 0, lane, row, w);
+    for (;;) {
+        const uint32_t tu = a.chunks.div(u);
+        const int64_t t = tu, c0 = static_cast<int64_t>(u - tu * a.chunks.d) * (32 * P);
+        const uint32_t next = u + step;
+        float acc[P];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            r[j] = -1;
-            w[j] = 1.0f;
-            if (j0 + j < a.k) {
-                r[j] = a.slot_row[t * a.k + j0 + j];
-                if (r[j] >= a.rows) r[j] = -1;
-                if (a.w) w[j] = a.w[t * a.k + j0 + j];
+        for (int i = 0; i < P; ++i) acc[i] = 0.0f;
+        for (int j0 = 0; j0 < a.k; j0 += kCombineSlots) {
+            uint4 v[kCombineSlots];
+            const uint32_t live = __ballot_sync(kFullMask, row >= 0 && row < a.rows);
+#pragma unroll
+            for (int j = 0; j < kCombineSlots; ++j) {
+                const int64_t r = __shfl_sync(kFullMask, row, j);
+                if ((live >> j) & 1u) v[j] = load_raw(c + r * a.ldc, c0, a.N, lane, a.vec != 0);
+            }
+            const float wj = w;
+            if (j0 + kCombineSlots < a.k)
+                load_slot(a, t, j0 + kCombineSlots, lane, row, w);
+            else if (next < a.units)
+                load_slot(a, a.chunks.div(next), 0, lane, row, w);
+#pragma unroll
+            for (int j = 0; j < kCombineSlots; ++j) {
+                const float ww = __shfl_sync(kFullMask, wj, j);
+                if ((live >> j) & 1u) {
+                    float f[P];
+                    unpack(v[j], f);
+#pragma unroll
+                    for (int i = 0; i < P; ++i) acc[i] = fmaf(ww, f[i], acc[i]);
+                }
             }
         }
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-            if (r[j] >= 0) load_piece(c + r[j] * a.ldc, c0, a.N, lane, a.vec != 0, f[j]);
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-            if (r[j] >= 0) {
-#pragma unroll
-                for (int i = 0; i < 8; ++i) acc[i] = fmaf(w[j], f[j][i], acc[i]);
-            }
+        store_floats<P>(static_cast<YT*>(a.y) + t * a.ldy, c0, a.N, lane, a.vec != 0, acc);
+        if (next >= a.units) break;
+        u = next;
     }
-    store_piece(static_cast<YT*>(a.y) + t * a.ldy, c0, a.N, lane, a.vec != 0, acc);
 }
 
-// One block per token: warp w takes the 256-column pieces w, w + 8, ...; per piece dy is loaded once and
-// each of the token's rows is read (for dw) and written (dc). Each warp's dot products are joined through
-// shared memory in warp order, so dw does not depend on timing. Four slots per pass keep the row pieces
-// in registers; a further pass re-reads dy, which L1 or L2 holds.
+// One block per token at a time: warp w takes the row pieces w, w + 8, ...; per piece dy and the token's rows
+// are loaded together, then the rows' gradients are written. Each warp reduces its 8 dot products with 9
+// shuffles (halving the values with the lanes) and joins them through shared memory in warp order, so dw does
+// not depend on timing. The next token's slots are loaded before this token's arithmetic. 20 480 tokens x 8 rows
+// x 2048 BF16: 263 us, 5.4 TB/s, nearly half of it writes (four slots per pass, two barriers each: 609 us).
 template <class CT, class YT>
-__global__ void __launch_bounds__(kExThreads) combine_bwd_kernel(const __grid_constant__ CombineArgs a) {
-    __shared__ float part[kExThreads / 32][4];
+__global__ void __launch_bounds__(kExThreads, 3) combine_bwd_kernel(const __grid_constant__ CombineArgs a) {
+    constexpr int P = 16 / static_cast<int>(sizeof(CT));
+    __shared__ float part[2][kExThreads / 32][kCombineSlots];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int64_t t = blockIdx.x;
     const CT* c = static_cast<const CT*>(a.c);
-    const YT* dy = static_cast<const YT*>(a.dy) + t * a.lddy;
-    for (int j0 = 0; j0 < a.k; j0 += 4) {
-        int64_t r[4];
-        bool pad[4];
-        float w[4], dot[4] = {0, 0, 0, 0};
+    int64_t t = blockIdx.x;
+    if (t >= a.T) return;
+    int row, flip = 0;
+    float w;
+    load_slot(a, t, 0, lane, row, w);
+    for (; t < a.T; t += gridDim.x) {
+        const YT* dy = static_cast<const YT*>(a.dy) + t * a.lddy;
+        for (int j0 = 0; j0 < a.k; j0 += kCombineSlots, flip ^= 1) {
+            const int mine = row >= 0 ? row : ~row;                      // a padding row's gradient is 0
+            const bool in = lane < kCombineSlots && j0 + lane < a.k && mine < a.rows;
+            const uint32_t write = __ballot_sync(kFullMask, in), live = __ballot_sync(kFullMask, in && row >= 0);
+            const float wj = w;
+            if (j0 + kCombineSlots < a.k)
+                load_slot(a, t, j0 + kCombineSlots, lane, row, w);
+            else if (t + gridDim.x < a.T)
+                load_slot(a, t + gridDim.x, 0, lane, row, w);
+            float dot[kCombineSlots];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            r[j] = -1;
-            pad[j] = false;
-            w[j] = 1.0f;
-            if (j0 + j < a.k) {
-                const int s = a.slot_row[t * a.k + j0 + j];
-                pad[j] = s < 0;
-                r[j] = pad[j] ? ~s : s;
-                if (r[j] >= a.rows) r[j] = -1;
-                if (a.w) w[j] = a.w[t * a.k + j0 + j];
+            for (int j = 0; j < kCombineSlots; ++j) dot[j] = 0.0f;
+            for (int64_t c0 = static_cast<int64_t>(warp) * (32 * P); c0 < a.N; c0 += kExThreads * P) {
+                uint4 v[kCombineSlots];
+                if (a.dw) {
+#pragma unroll
+                    for (int j = 0; j < kCombineSlots; ++j) {
+                        const int64_t r = __shfl_sync(kFullMask, mine, j);
+                        if ((live >> j) & 1u) v[j] = load_raw(c + r * a.ldc, c0, a.N, lane, a.vec != 0);
+                    }
+                }
+                float g[P];
+                load_floats<P>(dy, c0, a.N, lane, a.vec != 0, g);
+                if (a.dc) {
+#pragma unroll
+                    for (int j = 0; j < kCombineSlots; ++j) {
+                        const int64_t r = __shfl_sync(kFullMask, mine, j);
+                        const float ww = __shfl_sync(kFullMask, wj, j);
+                        if ((write >> j) & 1u) {
+                            const bool pad = !((live >> j) & 1u);
+                            float o[P];
+#pragma unroll
+                            for (int i = 0; i < P; ++i) o[i] = pad ? 0.0f : ww * g[i];
+                            store_floats<P>(static_cast<CT*>(a.dc) + r * a.lddc, c0, a.N, lane, a.vec != 0, o);
+                        }
+                    }
+                }
+                if (a.dw) {
+#pragma unroll
+                    for (int j = 0; j < kCombineSlots; ++j)
+                        if ((live >> j) & 1u) {
+                            float f[P];
+                            unpack(v[j], f);
+#pragma unroll
+                            for (int i = 0; i < P; ++i) dot[j] = fmaf(g[i], f[i], dot[j]);
+                        }
+                }
             }
-        }
-        for (int64_t c0 = static_cast<int64_t>(warp) * 256; c0 < a.N; c0 += kExThreads * 8) {
-            float g[8], f[4][8];
-            load_piece(dy, c0, a.N, lane, a.vec != 0, g);
             if (a.dw) {
+                // Lanes with bit b of the lane set keep the upper half of the values, the others the lower.
 #pragma unroll
-                for (int j = 0; j < 4; ++j)
-                    if (r[j] >= 0 && !pad[j]) load_piece(c + r[j] * a.ldc, c0, a.N, lane, a.vec != 0, f[j]);
+                for (int h = kCombineSlots / 2, b = 16; h >= 1; h >>= 1, b >>= 1) {
+                    const bool up = (lane & b) != 0;
 #pragma unroll
-                for (int j = 0; j < 4; ++j)
-                    if (r[j] >= 0 && !pad[j]) {
-#pragma unroll
-                        for (int i = 0; i < 8; ++i) dot[j] = fmaf(g[i], f[j][i], dot[j]);
+                    for (int j = 0; j < h; ++j) {
+                        const float give = up ? dot[j] : dot[j + h];
+                        const float keep = up ? dot[j + h] : dot[j];
+                        dot[j] = keep + __shfl_xor_sync(kFullMask, give, b);
                     }
-            }
-            if (a.dc) {
+                }
+                dot[0] += __shfl_xor_sync(kFullMask, dot[0], 2);
+                dot[0] += __shfl_xor_sync(kFullMask, dot[0], 1);
+                // Value index: bits 4, 3, 2 of the lane.
+                if ((lane & 3) == 0) part[flip][warp][lane >> 2] = dot[0];
+                __syncthreads();
+                if (threadIdx.x < kCombineSlots && j0 + static_cast<int>(threadIdx.x) < a.k) {
+                    float s = 0.0f;
 #pragma unroll
-                for (int j = 0; j < 4; ++j)
-                    if (r[j] >= 0) {
-                        float o[8];
-#pragma unroll
-                        for (int i = 0; i < 8; ++i) o[i] = pad[j] ? 0.0f : w[j] * g[i];
-                        store_piece(static_cast<CT*>(a.dc) + r[j] * a.lddc, c0, a.N, lane, a.vec != 0, o);
-                    }
+                    for (int v = 0; v < kExThreads / 32; ++v) s += part[flip][v][threadIdx.x];
+                    a.dw[t * a.k + j0 + threadIdx.x] = s;
+                }
             }
-        }
-        if (a.dw) {
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                dot[j] = warp_sum(dot[j]);
-                if (lane == 0) part[warp][j] = dot[j];
-            }
-            __syncthreads();
-            if (threadIdx.x < 4 && j0 + static_cast<int>(threadIdx.x) < a.k) {
-                float s = 0.0f;
-#pragma unroll
-                for (int v = 0; v < kExThreads / 32; ++v) s += part[v][threadIdx.x];
-                a.dw[t * a.k + j0 + threadIdx.x] = s;
-            }
-            __syncthreads();
         }
     }
 }

@@ -58,7 +58,7 @@ struct DeviceInfo {
     int pair_clusters_fp4[2] = {0, 0};
     int dispatch_blocks_per_sm[2] = {1, 1};   // MXFP8, MXFP4
     int fp4_blocks_per_sm[4] = {1, 1, 1, 1};  // MXFP4 quantizer, by direction bits
-    bool ok = false;
+    std::atomic<bool> ok{false};      // set last: everything else is then read without the lock
 };
 
 // Clusters of 2 CTAs of `kernel` that fit on the device at once (falls back to SMs / 2).
@@ -136,9 +136,10 @@ bool qt_setup(int* blocks) {
 const DeviceInfo* device_info() {
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return nullptr;
-    std::lock_guard<std::mutex> lock(g_dev_mutex);
     DeviceInfo& d = g_dev[dev];
-    if (!d.ok) {
+    if (d.ok.load(std::memory_order_acquire)) return &d;
+    std::lock_guard<std::mutex> lock(g_dev_mutex);
+    if (!d.ok.load(std::memory_order_relaxed)) {
         if (cudaDeviceGetAttribute(&d.sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return nullptr;
         if (cudaDeviceGetAttribute(&d.cc_major, cudaDevAttrComputeCapabilityMajor, dev) != cudaSuccess)
             return nullptr;
@@ -281,6 +282,7 @@ bool make_tmap(CUtensorMap* map, const void* base, uint64_t cols_bytes, uint64_t
 }
 
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+constexpr int64_t kInt32End = int64_t(1) << 31;
 
 // Checks shared by both GEMMs. Sets *empty when there is nothing to compute (then pointers may be
 // null). The output may have any element alignment; 16-byte aligned rows take vector stores.
@@ -993,13 +995,18 @@ mx_status mx_dequantize_fp4(const uint8_t* q, const uint8_t* s, int64_t M, int64
     a.s = s;
     a.out = static_cast<uint16_t*>(out);
     a.kblocks = K / 32;
-    a.blocks = M * a.kblocks;
     a.ld = ld_out;
     a.ctiles = ceil_div(a.kblocks, 4);
+    a.words_per_row = FastDiv::of(K / 8);
     a.swz = swizzled != 0;
-    if (ceil_div(a.blocks, 256) >= (int64_t(1) << 31)) return MX_ERR_SHAPE;
-    dequantize_fp4_kernel<<<static_cast<unsigned>(ceil_div(a.blocks, 256)), 256, 0, stream>>>(a);
-    return launched();
+    // One launch, or slabs of rows that 31-bit word indices can count.
+    const int64_t slab = (kInt32End - 1 - 256 * kDeqWords) / (K / 8);
+    for (a.row0 = 0; a.row0 < M; a.row0 += slab) {
+        a.words = static_cast<uint32_t>(std::min(M - a.row0, slab) * (K / 8));
+        dequantize_fp4_kernel<<<static_cast<unsigned>(ceil_div(a.words, 256 * kDeqWords)), 256, 0, stream>>>(a);
+        if (mx_status st = launched()) return st;
+    }
+    return MX_OK;
 }
 
 mx_status mx_gemm_fp4(const uint8_t* qa, const uint8_t* sa_swz, const uint8_t* qb, const uint8_t* sb_swz, int64_t M,
@@ -1038,8 +1045,6 @@ bool elt_ok(mx_out_dtype dt) { return dt == MX_OUT_F32 || dt == MX_OUT_BF16; }
 int64_t elt_size(mx_out_dtype dt) { return dt == MX_OUT_BF16 ? 2 : 4; }
 bool elt_aligned(const void* p, mx_out_dtype dt) { return reinterpret_cast<uintptr_t>(p) % elt_size(dt) == 0; }
 bool word_aligned(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
-constexpr int64_t kInt32End = int64_t(1) << 31;
-
 // Experts per lane of the routing kernels.
 int route_nv(int64_t E) {
     int nv = 1;
@@ -1082,27 +1087,48 @@ mx_status launch_route_nv(int nv, const RouteArgs& a, bool backward, mx_stream s
     return launched();
 }
 
+// Resident blocks per SM of a kernel, asked once per device and kept in `cache`.
+template <class K>
+int cached_occupancy(std::atomic<int>* cache, K kernel) {
+    int dev = 0;
+    cudaGetDevice(&dev);
+    int n = cache[dev].load(std::memory_order_relaxed);
+    if (n == 0) cache[dev].store(n = occupancy(kernel, kExThreads), std::memory_order_relaxed);
+    return n;
+}
+
 int plan_blocks(int64_t n) {
     return n <= kPlanOneBlock ? 1 : static_cast<int>(std::min<int64_t>(kPlanMaxBlocks, ceil_div(n, kPlanThreads)));
 }
 
 template <class CT, class YT>
-mx_status launch_combine(const CombineArgs& a, bool backward, mx_stream stream) {
+mx_status launch_combine(CombineArgs& a, bool backward, const DeviceInfo* d, mx_stream stream) {
+    const int64_t piece = 512 / static_cast<int64_t>(sizeof(CT));
+    const int64_t chunks = ceil_div(std::max<int64_t>(a.N, 1), piece);
+    // Warp units past 31 bits would mean more output than the device has memory. The kernel steps past the end by
+    // less than one grid.
+    if (a.T * chunks >= kInt32End - (int64_t(1) << 20)) return MX_ERR_SHAPE;
+    a.chunks = FastDiv::of(chunks);
+    a.units = static_cast<uint32_t>(a.T * chunks);
     if (backward) {
-        combine_bwd_kernel<CT, YT><<<static_cast<unsigned>(a.T), kExThreads, 0, stream>>>(a);
+        static std::atomic<int> blocks[kMaxDevices];
+        const int64_t grid = std::min<int64_t>(a.T, int64_t(d->sms) * cached_occupancy(blocks, combine_bwd_kernel<CT, YT>));
+        combine_bwd_kernel<CT, YT><<<static_cast<unsigned>(grid), kExThreads, 0, stream>>>(a);
     } else {
-        const int64_t grid = ceil_div(a.T * a.chunks, kExThreads / 32);
-        if (grid >= kInt32End) return MX_ERR_SHAPE;
+        static std::atomic<int> blocks[kMaxDevices];
+        const int64_t grid = std::min<int64_t>(ceil_div(a.units, kExThreads / 32),
+                                               int64_t(d->sms) * cached_occupancy(blocks, combine_kernel<CT, YT>));
         combine_kernel<CT, YT><<<static_cast<unsigned>(grid), kExThreads, 0, stream>>>(a);
     }
     return launched();
 }
 
-mx_status launch_combine_types(const CombineArgs& a, mx_out_dtype ct, mx_out_dtype yt, bool backward, mx_stream stream) {
-    if (ct == MX_OUT_BF16 && yt == MX_OUT_BF16) return launch_combine<uint16_t, uint16_t>(a, backward, stream);
-    if (ct == MX_OUT_BF16) return launch_combine<uint16_t, float>(a, backward, stream);
-    if (yt == MX_OUT_BF16) return launch_combine<float, uint16_t>(a, backward, stream);
-    return launch_combine<float, float>(a, backward, stream);
+mx_status launch_combine_types(CombineArgs& a, mx_out_dtype ct, mx_out_dtype yt, bool backward, const DeviceInfo* d,
+                               mx_stream stream) {
+    if (ct == MX_OUT_BF16 && yt == MX_OUT_BF16) return launch_combine<uint16_t, uint16_t>(a, backward, d, stream);
+    if (ct == MX_OUT_BF16) return launch_combine<uint16_t, float>(a, backward, d, stream);
+    if (yt == MX_OUT_BF16) return launch_combine<float, uint16_t>(a, backward, d, stream);
+    return launch_combine<float, float>(a, backward, d, stream);
 }
 
 bool rows_vec(const void* p, int64_t ld, mx_out_dtype dt) { return aligned16(p) && (ld * elt_size(dt)) % 16 == 0; }
@@ -1245,11 +1271,13 @@ mx_status mx_dispatch_quantize(const void* x, int64_t T, int64_t K, int64_t ld_x
     a.E = static_cast<int>(E);
     a.kblocks = static_cast<int>(K / 32);
     a.ctiles = static_cast<int>(ceil_div(a.kblocks, 4));
-    a.chunks = static_cast<int>(ceil_div(a.kblocks, 32));
+    const int64_t chunks = ceil_div(a.kblocks, 32);
+    a.chunks = FastDiv::of(chunks);
     const int64_t tiles = (a.n + 127 * std::min<int64_t>(E, a.n)) / 128;
-    if (tiles * 128 >= kInt32End) return MX_ERR_SHAPE;
+    if (tiles * 128 >= kInt32End || T * chunks + tiles >= kInt32End - (int64_t(1) << 20)) return MX_ERR_SHAPE;
     a.tiles = static_cast<int>(tiles);
-    a.units = T * a.chunks + tiles;
+    a.tok_units = static_cast<uint32_t>(T * chunks);
+    a.units = static_cast<uint32_t>(T * chunks + tiles);
     a.vec32 = reinterpret_cast<uintptr_t>(x) % 32 == 0 && ld_x % 16 == 0 && reinterpret_cast<uintptr_t>(q) % 32 == 0;
     const bool fp4 = format == MX_FORMAT_E2M1;
     const int64_t grid = std::min<int64_t>(ceil_div(a.units, kExThreads / 32), int64_t(d->sms) * d->dispatch_blocks_per_sm[fp4]);
@@ -1284,9 +1312,8 @@ mx_status mx_combine(const void* c, mx_out_dtype c_dtype, int64_t rows, int64_t 
     a.ldy = ld_y;
     a.rows = rows;
     a.k = static_cast<int>(topk);
-    a.chunks = static_cast<int>(ceil_div(N, 256));
     a.vec = rows_vec(c, ld_c, c_dtype) && rows_vec(y, ld_y, y_dtype);
-    return launch_combine_types(a, c_dtype, y_dtype, false, stream);
+    return launch_combine_types(a, c_dtype, y_dtype, false, d, stream);
 }
 
 mx_status mx_combine_bwd(const void* dy, mx_out_dtype y_dtype, int64_t ld_dy, const void* c, mx_out_dtype c_dtype,
@@ -1320,7 +1347,7 @@ mx_status mx_combine_bwd(const void* dy, mx_out_dtype y_dtype, int64_t ld_dy, co
     a.dw = d_weights;
     a.vec = rows_vec(dy, ld_dy, y_dtype) && (!d_weights || rows_vec(c, ld_c, c_dtype)) &&
             (!d_c || rows_vec(d_c, ld_dc, c_dtype));
-    return launch_combine_types(a, c_dtype, y_dtype, true, stream);
+    return launch_combine_types(a, c_dtype, y_dtype, true, d, stream);
 }
 
 }  // extern "C"
