@@ -54,6 +54,10 @@ constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kAcc1Col = 240;
 constexpr uint32_t kOvlCol = 240;
 constexpr uint32_t kSfCol = 496;
+// MXFP4: accumulator 1 = [232, 488) (24 columns shared), two scale slots [488, 500) and [500, 512), one for
+// each half of a stage.
+constexpr uint32_t kAcc1ColFp4 = 232;
+constexpr uint32_t kSfColFp4 = 488;
 constexpr int kStageBytes = 32 * 128;  // epilogue staging per warp: 32 rows x 128 bytes
 
 // Shared-memory layout of one kernel configuration. B_ROWS: rows of B per CTA and stage; SF: scale
@@ -97,12 +101,12 @@ struct GemmArgs {
     int M;              // dense: rows of A; grouped: total rows
     int N, K;
     int nkb;            // stages: ceil(K / 128), MXFP4 ceil(K / 256)
-    int sf_ctiles;      // MXFP4: scale blocks per 128-row tile, ceil(K / 128)
     int tiles_m;        // dense: row tiles (128 rows single-CTA, 256 rows pair)
     int tiles_n;        // 256-column tiles
     int sfa_tiles;      // 128-row tiles in A's scale layout (dense), for clamping
     int out_bf16;
     int vec_store;      // output rows 16-byte aligned: full 16-byte chunks use 16-byte stores
+    int direct;         // MXFP4: rows and N are whole 32-byte pieces: stored from registers, no staging
     int G;
     int n_fast;         // dense: consecutive tiles step along N (B re-read from L2, A streamed once)
     int n_rowtiles;     // ceil(N / 128): scale row-tiles of one B operand
@@ -211,18 +215,22 @@ __device__ __forceinline__ Tile decode_tile_pair(int t, int rank, const GemmArgs
 // 4 rows per instruction), masked to the tile's valid rows and to N. The stores go through the
 // load/store path, not TMA: TMA stores share the SM's TMA unit with the operand loads and were
 // measured to slow those down. Barrier addresses are shared::cluster addresses.
-template <bool GROUPED>
+// ACC1: first column of accumulator 1; columns [ACC1, 256) are shared.
+// DIRECT: where a.direct is set, each lane writes its row's pieces with 32-byte stores from registers.
+template <bool GROUPED, uint32_t ACC1 = kAcc1Col, bool DIRECT = false>
 __device__ __forceinline__ void epilogue_tile(const GemmArgs& a, const Tile& T, uint32_t tmem_base, bool acc1,
                                               uint8_t* stage, uint32_t ovl_free_addr, uint32_t acc_empty_addr,
                                               int q, int lane) {
     const int warp_rows = min(32, max(0, T.rows_valid - q * 32));
     const int64_t row0 = static_cast<int64_t>(T.a_row0) + q * 32;
     const uint32_t lanes = tmem_base + (static_cast<uint32_t>(q * 32) << 16);
-    const uint32_t tq = lanes + (acc1 ? kAcc1Col : 0u);
+    constexpr int kOvl = 256 - static_cast<int>(ACC1);   // shared columns: 16 or 24
+    const uint32_t tq = lanes + (acc1 ? ACC1 : 0u);
     const uint32_t swz = static_cast<uint32_t>(lane & 7);
 
-    uint32_t ov[16];                     // tile columns 240..255 of accumulator 0, 0..15 of accumulator 1
-    tc_ld_32x32b_x16(lanes + kOvlCol, ov);
+    uint32_t ov[kOvl];                   // the last kOvl tile columns of accumulator 0, the first of accumulator 1
+    tc_ld_32x32b_x16(lanes + ACC1, *reinterpret_cast<uint32_t(*)[16]>(&ov[0]));
+    if constexpr (kOvl == 24) tc_ld_32x32b_x8(lanes + ACC1 + 16u, *reinterpret_cast<uint32_t(*)[8]>(&ov[16]));
     tc_wait_ld_regs(ov);
     tc_fence_before();
     __syncwarp();
@@ -234,6 +242,19 @@ __device__ __forceinline__ void epilogue_tile(const GemmArgs& a, const Tile& T, 
     const int epc = 16 / esz;                            // elements per 16-byte chunk
     auto emit = [&](const uint32_t(&p)[32], int col0) {
         if (col0 >= a.N) return;
+        if constexpr (DIRECT) {
+            if (a.direct) {
+                uint8_t* dst = static_cast<uint8_t*>(a.c) + ((row0 + lane) * a.ldc + col0) * esz;
+                if (lane < warp_rows) {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        if (col0 + 2 * i * epc < a.N)
+                            st_global_v8(dst + 32 * i, p[8 * i], p[8 * i + 1], p[8 * i + 2], p[8 * i + 3], p[8 * i + 4],
+                                         p[8 * i + 5], p[8 * i + 6], p[8 * i + 7]);
+                }
+                return;
+            }
+        }
         const uint32_t row = box + lane * 128;
 #pragma unroll
         for (int i = 0; i < 8; ++i)
@@ -272,14 +293,21 @@ __device__ __forceinline__ void epilogue_tile(const GemmArgs& a, const Tile& T, 
     // Issues the TMEM loads of tile columns [32 c, 32 c + 32) into p; the shared columns come from `ov`.
     // The caller waits (tc_wait_ld_regs) before reading p.
     auto load32 = [&](int c, uint32_t(&p)[32]) {
+        constexpr int kOwn = 32 - kOvl;                  // columns of a mixed piece that are not shared
         if (acc1 && c == 0) {
-            tc_ld_32x32b_x16(tq + 16u, *reinterpret_cast<uint32_t(*)[16]>(&p[16]));
+            if constexpr (kOwn == 16)
+                tc_ld_32x32b_x16(tq + 16u, *reinterpret_cast<uint32_t(*)[16]>(&p[16]));
+            else
+                tc_ld_32x32b_x8(tq + 24u, *reinterpret_cast<uint32_t(*)[8]>(&p[24]));
 #pragma unroll
-            for (int i = 0; i < 16; ++i) p[i] = ov[i];
+            for (int i = 0; i < kOvl; ++i) p[i] = ov[i];
         } else if (!acc1 && c == 7) {
-            tc_ld_32x32b_x16(tq + 224u, *reinterpret_cast<uint32_t(*)[16]>(&p[0]));
+            if constexpr (kOwn == 16)
+                tc_ld_32x32b_x16(tq + 224u, *reinterpret_cast<uint32_t(*)[16]>(&p[0]));
+            else
+                tc_ld_32x32b_x8(tq + 224u, *reinterpret_cast<uint32_t(*)[8]>(&p[0]));
 #pragma unroll
-            for (int i = 0; i < 16; ++i) p[16 + i] = ov[i];
+            for (int i = 0; i < kOvl; ++i) p[kOwn + i] = ov[i];
         } else {
             tc_ld_32x32b_x32(tq + 32u * c, p);
         }
@@ -631,11 +659,14 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
 // ---------------------------------------------------------------------------------------------
 //
 // FP4 == true: MXFP4 operands (packed E2M1, kind::mxf4). A stage's 128 bytes of K are 256 elements, i.e.
-// two scale blocks of 4 K-blocks per 128 rows and four MMAs of 64 elements; the scale slot in TMEM takes
-// the first blocks for MMAs 0 and 1, then the second for MMAs 2 and 3 (tcgen05 operations of one thread
-// run in order). K past the end is zero-filled by TMA, and MMAs that lie wholly past it are not issued.
-// An MMA reads the same bytes as an MXFP8 one and does twice the products, so loads, epilogue and scale
-// copies weigh twice.
+// two scale blocks of 4 K-blocks per 128 rows, each with its own slot in TMEM, and four MMAs of 64
+// elements, two per slot. K past the end is zero-filled by TMA, and MMAs that lie wholly past it are not issued.
+// An MMA reads the same bytes as an MXFP8 one and does twice the products, so everything around the MMAs
+// weighs twice. Measured at 5200 x 8192 x 4096 (cycles per SM, of which 74 400 are MMAs): 150 cycles
+// of issue per stage were the first cost (see tc_mxf4_stage_pair_elect: 134 400 -> 110 900), the epilogue's staging in
+// shared memory, which the MMAs and TMA writes already keep busy, the next (-> 105 600 with 32-byte stores from
+// registers); what is left are the hand-over between tiles (some 770 cycles each), the C stores and the scale copies.
+// 5200 x 24576 x 4096: 189 us, 5.5 PFLOP/s; back to back under the power cap 213 us, 4.9 PFLOP/s.
 template <bool FP4>
 constexpr uint32_t kPairStageBytesOf = kBM * kBK + (kBN / 2) * kBK + (FP4 ? 2 : 1) * (kSfaBytes + kSfbBytes);   // per CTA
 
@@ -725,18 +756,18 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
                 tma_load_2d_pair_elect(smem + L::kA + stage * kBM * kBK, &tmap_a, fb, kb * kBK, T.a_row0);
                 tma_load_2d_pair_elect(smem + L::kB + stage * kBRows * kBK, &tmap_b, fb, kb * kBK, T.b_row0);
                 // Scale blocks: the layout viewed as rows of 256 bytes, one block = 2 rows. MXFP4 takes two
-                // consecutive blocks of each row tile; where the last stage has only one, that one is loaded
-                // twice (the copy is not used), so no load leaves the layout and every stage has its bytes.
-                const int sf_ct = FP4 ? a.sf_ctiles : a.nkb;
-#pragma unroll
-                for (int h = 0; h < (FP4 ? 2 : 1); ++h) {
-                    const int blk = FP4 ? min(2 * kb + h, sf_ct - 1) : kb;
-                    tma_load_2d_pair_elect(smem + L::kSfa + stage * kSfaStage + 512 * h, &tmap_sfa, fb, 0,
-                                           2 * (T.sfa_tile * sf_ct + blk));
-                    tma_load_2d_pair_elect(smem + L::kSfb + stage * kSfbStage + 512 * h, &tmap_sfb, fb, 0,
-                                           2 * (T.sfb_tile0 * sf_ct + blk));
-                    tma_load_2d_pair_elect(smem + L::kSfb + stage * kSfbStage + kSfbStage / 2 + 512 * h, &tmap_sfb,
-                                           fb, 0, 2 * (T.sfb_tile1 * sf_ct + blk));
+                // consecutive blocks of each row tile with one box of 4 rows, B's two row tiles in one copy; a block
+                // past K's last or a row tile past the last is filled with zeros, so no load leaves the layout.
+                if constexpr (FP4) {
+                    tma_load_3d_pair_elect(smem + L::kSfa + stage * kSfaStage, &tmap_sfa, fb, 0, 4 * kb, T.sfa_tile);
+                    tma_load_3d_pair_elect(smem + L::kSfb + stage * kSfbStage, &tmap_sfb, fb, 0, 4 * kb, T.sfb_tile0);
+                } else {
+                    tma_load_2d_pair_elect(smem + L::kSfa + stage * kSfaStage, &tmap_sfa, fb, 0,
+                                           2 * (T.sfa_tile * a.nkb + kb));
+                    tma_load_2d_pair_elect(smem + L::kSfb + stage * kSfbStage, &tmap_sfb, fb, 0,
+                                           2 * (T.sfb_tile0 * a.nkb + kb));
+                    tma_load_2d_pair_elect(smem + L::kSfb + stage * kSfbStage + 512, &tmap_sfb, fb, 0,
+                                           2 * (T.sfb_tile1 * a.nkb + kb));
                 }
                 ++issued;
                 if (++stage == S) { stage = 0; phase ^= 1u; }
@@ -749,7 +780,8 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
             int stage = 0;
             uint32_t phase = 0, ovl_phase = 0, empty_phase = 0;
             bool ok = true;
-            const uint32_t sfa_t = tmem_base + kSfCol;
+            constexpr uint32_t kAcc1 = FP4 ? kAcc1ColFp4 : kAcc1Col;
+            const uint32_t sfa_t = tmem_base + (FP4 ? kSfColFp4 : kSfCol);
             const uint32_t sfb_t = sfa_t + 4;
             int j = 0;
             for (int t = pair; t < tiles && ok; t += npairs, ++j) {
@@ -766,44 +798,50 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
                     ovl_phase ^= 1u;
                 }
                 tc_fence_after();
-                const uint32_t acc = tmem_base + ((j & 1) ? kAcc1Col : 0u);
+                const uint32_t acc = tmem_base + ((j & 1) ? kAcc1 : 0u);
                 for (int kb = 0; kb < a.nkb; ++kb) {
                     if (!mbar_wait(&full[stage], phase, abort, a.err, a.timeout_ns)) { ok = false; break; }
                     __syncwarp();
                     tc_fence_after();
                     const uint32_t sfa_s = smem_u32(smem + L::kSfa + stage * kSfaStage);
                     const uint32_t sfb_s = smem_u32(smem + L::kSfb + stage * kSfbStage);
-                    tc_cp_pair_elect(sfa_t, sdesc_scale_block(sfa_s));
-                    tc_cp_pair_elect(sfb_t, sdesc_scale_block(sfb_s));
-                    tc_cp_pair_elect(sfb_t + 4, sdesc_scale_block(sfb_s + kSfbStage / 2));
                     const uint64_t adesc = sdesc_kmajor_sw128(smem_u32(smem + L::kA + stage * kBM * kBK));
                     const uint64_t bdesc = sdesc_kmajor_sw128(smem_u32(smem + L::kB + stage * kBRows * kBK));
-                    if constexpr (FP4) {
-                        const int steps = min(4, (a.K - kb * 256 + 63) / 64);
+                    const uint64_t sda = sdesc_scale_block(sfa_s), sdb0 = sdesc_scale_block(sfb_s);
+                    const uint64_t sdb1 = sdesc_scale_block(sfb_s + kSfbStage / 2);
+                    const int left = FP4 ? a.K - kb * 256 : 0;
+                    if (FP4 && left >= 256) {
+                        tc_mxf4_stage_pair_elect(acc, adesc, bdesc, idesc_mxf4(2 * kBM, kBN, 0), idesc_mxf4(2 * kBM, kBN, 2),
+                                                 sfa_t, sda, sdb0, sdb1, kb != 0 ? 1u : 0u, &empty[stage]);
+                    } else {
+                        tc_cp_pair_elect(sfa_t, sda);
+                        tc_cp_pair_elect(sfb_t, sdb0);
+                        tc_cp_pair_elect(sfb_t + 4, sdb1);
+                        if constexpr (FP4) {
+                            // K's ragged end: the same copies, and only the MMAs that still have elements.
+                            tc_cp_pair_elect(sfa_t + 12, sda + 32);
+                            tc_cp_pair_elect(sfb_t + 12, sdb0 + 32);
+                            tc_cp_pair_elect(sfb_t + 16, sdb1 + 32);
 #pragma unroll
-                        for (int k = 0; k < 4; ++k) {
-                            if (k < steps) {
-                                if (k == 2) {
-                                    tc_cp_pair_elect(sfa_t, sdesc_scale_block(sfa_s + 512));
-                                    tc_cp_pair_elect(sfb_t, sdesc_scale_block(sfb_s + 512));
-                                    tc_cp_pair_elect(sfb_t + 4, sdesc_scale_block(sfb_s + kSfbStage / 2 + 512));
-                                }
-                                // K-step k: +32 bytes (64 elements); scale bytes 2 (k % 2), +1 of the word.
-                                const uint32_t id = 2u * (k & 1);
-                                tc_mma_mxf4_pair_elect(acc, adesc + 2u * k, bdesc + 2u * k,
-                                                       idesc_mxf4(2 * kBM, kBN, id), sfa_t | (id << 30),
-                                                       sfb_t | (id << 30), (kb | k) != 0 ? 1u : 0u);
+                            for (int k = 0; k < 4; ++k) {
+                                // K-step k: +32 bytes; scale slot k / 2, scale bytes 2 (k % 2), +1 of the word.
+                                const uint32_t id = 2u * (k & 1), slot = 12u * (k >> 1);
+                                if (64 * k < left)
+                                    tc_mma_mxf4_pair_elect(acc, adesc + 2u * k, bdesc + 2u * k,
+                                                           idesc_mxf4(2 * kBM, kBN, id), (sfa_t + slot) | (id << 30),
+                                                           (sfb_t + slot) | (id << 30), (kb | k) != 0 ? 1u : 0u);
+                            }
+                        } else {
+#pragma unroll
+                            for (int k = 0; k < 4; ++k) {
+                                tc_mma_mxf8_pair_elect(acc, adesc + 2u * k, bdesc + 2u * k,
+                                                       idesc_mxf8_e4m3(2 * kBM, kBN, k),
+                                                       sfa_t | (static_cast<uint32_t>(k) << 30),
+                                                       sfb_t | (static_cast<uint32_t>(k) << 30), (kb | k) != 0 ? 1u : 0u);
                             }
                         }
-                    } else {
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        tc_mma_mxf8_pair_elect(acc, adesc + 2u * k, bdesc + 2u * k, idesc_mxf8_e4m3(2 * kBM, kBN, k),
-                                               sfa_t | (static_cast<uint32_t>(k) << 30),
-                                               sfb_t | (static_cast<uint32_t>(k) << 30), (kb | k) != 0 ? 1u : 0u);
+                        tc_commit_pair_elect(&empty[stage], 0x3);     // both CTAs' stage is free again
                     }
-                    }
-                    tc_commit_pair_elect(&empty[stage], 0x3);     // both CTAs' stage is free again
                     if (++stage == S) { stage = 0; phase ^= 1u; }
                 }
                 if (!ok) break;
@@ -827,7 +865,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
             full_phase ^= 1u;
             tc_fence_after();
             if constexpr (EPI == 0)
-                epilogue_tile<GROUPED>(a, T, tmem_base, g != 0, stage, ovl_addr, empty_addr, q, lane);
+                epilogue_tile<GROUPED, FP4 ? kAcc1ColFp4 : kAcc1Col, FP4>(a, T, tmem_base, g != 0, stage, ovl_addr, empty_addr, q, lane);
             else
                 epilogue_swiglu_tile(a, T, tmem_base, g != 0, ovl_addr, empty_addr, q, lane);
         }

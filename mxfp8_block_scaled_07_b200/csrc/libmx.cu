@@ -314,6 +314,31 @@ bool make_tmap_sf(CUtensorMap* map, const void* base, int64_t blocks) {
     return encode_2d(map, 1, base, 256, static_cast<uint64_t>(2 * blocks), 256, 256, 2);
 }
 
+// The same layout with its row tiles as a third dimension: `tiles` row tiles of ctiles blocks; a box is two
+// consecutive blocks of box_tiles row tiles (MXFP4: one copy per operand and stage).
+bool make_tmap_sf_tiles(CUtensorMap* map, const void* base, int64_t ctiles, int64_t tiles, uint32_t box_tiles) {
+    static thread_local std::unordered_map<TmapKey, CUtensorMap, TmapKeyHash> cache;
+    const TmapKey key{reinterpret_cast<uintptr_t>(base), static_cast<uint64_t>(ctiles), static_cast<uint64_t>(tiles), 0,
+                      box_tiles, 0, 3};
+    auto it = cache.find(key);
+    if (it != cache.end()) {
+        *map = it->second;
+        return true;
+    }
+    if (!encode_fn()) return false;
+    const cuuint64_t dims[3] = {256, static_cast<cuuint64_t>(2 * ctiles), static_cast<cuuint64_t>(tiles)};
+    const cuuint64_t strides[2] = {256, static_cast<cuuint64_t>(512 * ctiles)};
+    const cuuint32_t box[3] = {256, 4, box_tiles};
+    const cuuint32_t estr[3] = {1, 1, 1};
+    if (g_encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void*>(base), dims, strides, box, estr,
+                 CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                 CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+        return false;
+    if (cache.size() >= kTmapCacheMax) cache.clear();
+    cache.emplace(key, *map);
+    return true;
+}
+
 // Launches the CTA-pair GEMM with a cluster dimension of 2.
 template <bool GROUPED, int EPI = 0, bool FP4 = false>
 mx_status launch_pair(int pairs, const CUtensorMap& ta, const CUtensorMap& tb, const CUtensorMap& tsa,
@@ -918,12 +943,13 @@ mx_status launch_gemm_fp4(const uint8_t* qa, const uint8_t* sa, const uint8_t* q
     a.N = static_cast<int>(N);
     a.K = static_cast<int>(K);
     a.nkb = static_cast<int>(ceil_div(K, 2 * kBK));
-    a.sf_ctiles = static_cast<int>(ceil_div(K, 128));
     a.tiles_m = offsets ? 0 : static_cast<int>(ceil_div(M, 2 * kBM));
     a.tiles_n = static_cast<int>(ceil_div(N, kBN));
     a.sfa_tiles = static_cast<int>(ceil_div(M, 128));
     a.out_bf16 = out_dtype == MX_OUT_BF16;
     a.vec_store = vector_store_ok(c, ld_c, out_dtype);
+    const int64_t esz = out_dtype == MX_OUT_BF16 ? 2 : 4;
+    a.direct = reinterpret_cast<uintptr_t>(c) % 32 == 0 && (ld_c * esz) % 32 == 0 && (N * esz) % 32 == 0;
     a.G = static_cast<int>(G);
     a.n_fast = M > N;
     a.n_rowtiles = static_cast<int>(ceil_div(N, 128));
@@ -935,8 +961,8 @@ mx_status launch_gemm_fp4(const uint8_t* qa, const uint8_t* sa, const uint8_t* q
     const int64_t tiles = (offsets ? ceil_div(M, 2 * kBM) + G : a.tiles_m) * a.tiles_n;
     CUtensorMap ta, tb, tsa, tsb;
     if (!make_tmap(&ta, qa, K / 2, M, kBK, kBM) || !make_tmap(&tb, qb, K / 2, G * N, kBK, kBN / 2) ||
-        !make_tmap_sf(&tsa, sa, sfa_tiles * a.sf_ctiles) ||
-        !make_tmap_sf(&tsb, sb, G * a.n_rowtiles * a.sf_ctiles))
+        !make_tmap_sf_tiles(&tsa, sa, ceil_div(K, 128), sfa_tiles, 1) ||
+        !make_tmap_sf_tiles(&tsb, sb, ceil_div(K, 128), G * a.n_rowtiles, 2))
         return MX_ERR_CUDA;
     const int pairs = static_cast<int>(std::min<int64_t>(tiles, d->pair_clusters_fp4[offsets ? 1 : 0]));
     return offsets ? launch_pair<true, 0, true>(pairs, ta, tb, tsa, tsb, a, stream)

@@ -107,6 +107,13 @@ __device__ __forceinline__ void st_global_v4(void* p, const uint4& v) {
                  : "memory");
 }
 
+__device__ __forceinline__ void st_global_v8(void* p, uint32_t a, uint32_t b, uint32_t c, uint32_t d, uint32_t e,
+                                             uint32_t f, uint32_t g, uint32_t h) {
+    asm volatile("st.global.cs.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(a), "r"(b), "r"(c),
+                 "r"(d), "r"(e), "r"(f), "r"(g), "r"(h)
+                 : "memory");
+}
+
 __device__ __forceinline__ void prefetch_tensormap(const CUtensorMap* map) {
     asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(map)) : "memory");
 }
@@ -173,6 +180,14 @@ __device__ __forceinline__ void tc_ld_32x32b_x16(uint32_t taddr, uint32_t (&r)[1
           "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
         : "r"(taddr)
         : "memory");
+}
+
+// 32 lanes x 8 columns of 32-bit words.
+__device__ __forceinline__ void tc_ld_32x32b_x8(uint32_t taddr, uint32_t (&r)[8]) {
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+                 : "r"(taddr)
+                 : "memory");
 }
 
 // ---- CTA pairs (cluster of 2, cta_group::2) -----------------------------------------------------
@@ -254,6 +269,14 @@ __device__ __forceinline__ void tma_load_2d_pair_elect(void* smem_dst, const CUt
                  "l"(reinterpret_cast<uint64_t>(map)), "r"(bar_cluster_addr), "r"(c0), "r"(c1)
                  : "memory");
 }
+__device__ __forceinline__ void tma_load_3d_pair_elect(void* smem_dst, const CUtensorMap* map,
+                                                       uint32_t bar_cluster_addr, int32_t c0, int32_t c1, int32_t c2) {
+    asm volatile(MX_ELECT_PRED
+                 "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, "
+                 "{%3, %4, %5}], [%2];\n\t}" ::"r"(smem_u32(smem_dst)),
+                 "l"(reinterpret_cast<uint64_t>(map)), "r"(bar_cluster_addr), "r"(c0), "r"(c1), "r"(c2)
+                 : "memory");
+}
 __device__ __forceinline__ void tc_cp_elect(uint32_t taddr, uint64_t sdesc) {
     asm volatile(MX_ELECT_PRED "tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;\n\t}" ::"r"(taddr), "l"(sdesc)
                  : "memory");
@@ -286,6 +309,42 @@ __device__ __forceinline__ void tc_mma_mxf4_pair_elect(uint32_t d_tmem, uint64_t
         "@e tcgen05.mma.cta_group::2.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%5], [%6], p;\n\t}" ::"r"(
             d_tmem),
         "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate), "r"(sfa_tmem), "r"(sfb_tmem)
+        : "memory");
+}
+// A whole MXFP4 stage (256 elements of K) under one election: per half of the stage the scale copies (A's and B's two
+// row tiles' blocks; the second half's slot is 12 columns on) and two MMAs of 64 elements, then the commit on `bar` in
+// both CTAs. Issued one by one, each with its own election, the issuing warp and not the tensor core set the pace:
+// 5200 x 24576 x 4096 took 201 us (with a test before each MMA 230), like this, with the epilogue's direct stores, 189;
+// all copies before all MMAs 192; the next stage's copies between this stage's MMAs 221.
+// sda / sdb0 / sdb1: descriptors of the scale blocks of A and of B's row tiles in shared memory; the second block
+// of each lies 512 bytes (32 descriptor units) behind the first.
+__device__ __forceinline__ void tc_mxf4_stage_pair_elect(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc0,
+                                                         uint32_t idesc2, uint32_t sfa_t, uint64_t sda, uint64_t sdb0,
+                                                         uint64_t sdb1, uint32_t accumulate, uint64_t* bar) {
+    asm volatile(
+        "{\n\t.reg .pred e, p, t;\n\t.reg .b64 x, y;\n\t.reg .b32 b0, b1, a1, b2, b3, a0h, b0h, a1h, b2h;\n\t.reg .b16 m;\n\t"
+        "elect.sync _|e, 0xffffffff;\n\tsetp.ne.b32 p, %9, 0;\n\tsetp.eq.b32 t, 0, 0;\n\tmov.b16 m, 3;\n\t"
+        "add.u32 b0, %5, 4;\n\tadd.u32 b1, %5, 8;\n\tadd.u32 a1, %5, 12;\n\tadd.u32 b2, %5, 16;\n\tadd.u32 b3, %5, 20;\n\t"
+        "or.b32 a0h, %5, 0x80000000;\n\tor.b32 b0h, b0, 0x80000000;\n\tor.b32 a1h, a1, 0x80000000;\n\tor.b32 b2h, b2, 0x80000000;\n\t"
+        "@e tcgen05.cp.cta_group::2.32x128b.warpx4 [%5], %6;\n\t"
+        "@e tcgen05.cp.cta_group::2.32x128b.warpx4 [b0], %7;\n\t"
+        "@e tcgen05.cp.cta_group::2.32x128b.warpx4 [b1], %8;\n\t"
+        "@e tcgen05.mma.cta_group::2.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%5], [b0], p;\n\t"
+        "add.s64 x, %1, 2;\n\tadd.s64 y, %2, 2;\n\t"
+        "@e tcgen05.mma.cta_group::2.kind::mxf4.block_scale.scale_vec::2X [%0], x, y, %4, [a0h], [b0h], t;\n\t"
+        "add.s64 x, %6, 32;\n\t"
+        "@e tcgen05.cp.cta_group::2.32x128b.warpx4 [a1], x;\n\t"
+        "add.s64 x, %7, 32;\n\t"
+        "@e tcgen05.cp.cta_group::2.32x128b.warpx4 [b2], x;\n\t"
+        "add.s64 x, %8, 32;\n\t"
+        "@e tcgen05.cp.cta_group::2.32x128b.warpx4 [b3], x;\n\t"
+        "add.s64 x, %1, 4;\n\tadd.s64 y, %2, 4;\n\t"
+        "@e tcgen05.mma.cta_group::2.kind::mxf4.block_scale.scale_vec::2X [%0], x, y, %3, [a1], [b2], t;\n\t"
+        "add.s64 x, %1, 6;\n\tadd.s64 y, %2, 6;\n\t"
+        "@e tcgen05.mma.cta_group::2.kind::mxf4.block_scale.scale_vec::2X [%0], x, y, %4, [a1h], [b2h], t;\n\t"
+        "@e tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%10], m;\n\t}" ::"r"(d_tmem),
+        "l"(adesc), "l"(bdesc), "r"(idesc0), "r"(idesc2), "r"(sfa_t), "l"(sda), "l"(sdb0), "l"(sdb1), "r"(accumulate),
+        "r"(smem_u32(bar))
         : "memory");
 }
 __device__ __forceinline__ void tc_commit_elect(uint64_t* bar) {

@@ -352,14 +352,19 @@ def _ld(t) -> int:
     return t.stride(0) if t.shape[0] > 1 else max(t.stride(0), t.shape[1])
 
 
+# The current stream's handle without a Stream object around it: half a call's Python time where a call takes 10 us.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (lambda i: torch.cuda.current_stream(i).cuda_stream)
+
+
 def _call(name: str, dev, *args):
     """One library call on `dev`'s current stream, with `dev` as the current device."""
-    fn = getattr(lib(), name)
-    if dev.index == torch.cuda.current_device():
-        st = fn(*args, torch.cuda.current_stream(dev).cuda_stream)
+    fn = getattr(_lib or lib(), name)
+    i = dev.index
+    if i == torch.cuda.current_device():
+        st = fn(*args, _raw_stream(i))
     else:
-        with torch.cuda.device(dev):
-            st = fn(*args, torch.cuda.current_stream(dev).cuda_stream)
+        with torch.cuda.device(i):
+            st = fn(*args, _raw_stream(i))
     if st != 0:
         raise MxError(st, name)
 
@@ -382,20 +387,21 @@ def quantize_fp4(x: torch.Tensor, rowwise: bool = True, colwise: bool = False, s
 
     if out is None:
         _need(K % 32 == 0 and (not colwise or M % 32 == 0), "quantize_fp4: blocks of 32 along the quantized axis")
-        u8 = dict(dtype=torch.uint8, device=dev)
-        q_row = torch.empty((M, K // 2), **u8) if rowwise else None
-        s_row = torch.empty(scale_bytes(M, K) if swizzle else (M, K // 32), **u8) if rowwise else None
-        q_col = torch.empty((K, M // 2), **u8) if colwise else None
-        s_col = torch.empty(scale_bytes(K, M) if swizzle else (K, M // 32), **u8) if colwise else None
+        new = x.new_empty
+        q_row = new((M, K // 2), dtype=torch.uint8) if rowwise else None
+        s_row = new(scale_bytes(M, K) if swizzle else (M, K // 32), dtype=torch.uint8) if rowwise else None
+        q_col = new((K, M // 2), dtype=torch.uint8) if colwise else None
+        s_col = new(scale_bytes(K, M) if swizzle else (K, M // 32), dtype=torch.uint8) if colwise else None
+        p = [None if t is None else t.data_ptr() for t in (q_row, s_row, q_col, s_col)]
     else:
         q_row, s_row, q_col, s_col = out
-    p = [None] * 4
-    if rowwise:
-        p[0] = _packed(q_row, "quantize_fp4: q_row", torch.uint8, M * K // 2, dev)
-        p[1] = _packed(s_row, "quantize_fp4: s_row", torch.uint8, scale_bytes(M, K), dev)
-    if colwise:
-        p[2] = _packed(q_col, "quantize_fp4: q_col", torch.uint8, M * K // 2, dev)
-        p[3] = _packed(s_col, "quantize_fp4: s_col", torch.uint8, scale_bytes(K, M), dev)
+        p = [None] * 4
+        if rowwise:
+            p[0] = _packed(q_row, "quantize_fp4: q_row", torch.uint8, M * K // 2, dev)
+            p[1] = _packed(s_row, "quantize_fp4: s_row", torch.uint8, scale_bytes(M, K), dev)
+        if colwise:
+            p[2] = _packed(q_col, "quantize_fp4: q_col", torch.uint8, M * K // 2, dev)
+            p[3] = _packed(s_col, "quantize_fp4: s_col", torch.uint8, scale_bytes(K, M), dev)
     _call("mx_quantize_fp4", dev, px, M, K, _ld(x), flags, *p)
     return q_row, s_row, q_col, s_col
 
@@ -404,12 +410,12 @@ def dequantize_fp4(q: torch.Tensor, s: torch.Tensor, swizzled: bool = True, out=
     """mx_dequantize_fp4: the BF16 values [M, K] of packed codes q [M, K/2] and their scales (the tensor-core
     layout, or raw [M, K/32] with swizzled=False)."""
     dev = q.device
-    pq = _matrix(q, "dequantize_fp4: q must be a 2-D uint8 CUDA tensor", _U8)
+    _need(isinstance(q, torch.Tensor) and q.dim() == 2, "dequantize_fp4: q must be a 2-D uint8 CUDA tensor")
     M, K = q.shape[0], 2 * q.shape[1]
-    _packed(q, "dequantize_fp4: q must be contiguous", torch.uint8, M * K // 2, dev)
+    pq = _packed(q, "dequantize_fp4: q must be a contiguous uint8 CUDA tensor", torch.uint8, M * K // 2, dev)
     ps = _packed(s, "dequantize_fp4: s", torch.uint8, swizzled_scale_bytes(M, K // 32) if swizzled else M * (K // 32), dev)
     if out is None:
-        out = torch.empty((M, K), dtype=torch.bfloat16, device=dev)
+        out = q.new_empty((M, K), dtype=torch.bfloat16)
     _call("mx_dequantize_fp4", dev, pq, ps, M, K, int(swizzled), _matrix(out, "dequantize_fp4: out", _BF16, (M, K), dev),
           _ld(out))
     return out
@@ -419,14 +425,15 @@ def gemm_fp4(qa, sa_swz, qb, sb_swz, out_dtype=torch.bfloat16, out=None):
     """mx_gemm_fp4: C[M, N] = A . B^T from packed K-major E2M1 operands (qa [M, K/2], qb [N, K/2]) and
     tensor-core-layout scales."""
     dev = qa.device
-    _matrix(qa, "gemm_fp4: qa", _U8)
-    _matrix(qb, "gemm_fp4: qb", _U8, (qb.shape[0], qa.shape[1]), dev)
-    M, N, K = qa.shape[0], qb.shape[0], 2 * qa.shape[1]
-    pa, pb = (_packed(t, "gemm_fp4: packed operands", torch.uint8, n * K // 2, dev) for t, n in ((qa, M), (qb, N)))
-    psa, psb = (_packed(t, "gemm_fp4: scales", torch.uint8, swizzled_scale_bytes(n, K // 32), dev)
-                for t, n in ((sa_swz, M), (sb_swz, N)))
+    _need(qa.dim() == 2 and qb.dim() == 2 and qa.shape[1] == qb.shape[1], "gemm_fp4: qa [M, K/2] and qb [N, K/2]")
+    (M, K), N = qa.shape, qb.shape[0]
+    K *= 2
+    pa = _packed(qa, "gemm_fp4: qa", torch.uint8, M * K // 2, dev)
+    pb = _packed(qb, "gemm_fp4: qb", torch.uint8, N * K // 2, dev)
+    psa = _packed(sa_swz, "gemm_fp4: sa_swz", torch.uint8, swizzled_scale_bytes(M, K // 32), dev)
+    psb = _packed(sb_swz, "gemm_fp4: sb_swz", torch.uint8, swizzled_scale_bytes(N, K // 32), dev)
     if out is None:
-        out = torch.empty((M, N), dtype=out_dtype, device=dev)
+        out = qa.new_empty((M, N), dtype=out_dtype)
     _call("mx_gemm_fp4", dev, pa, psa, pb, psb, M, N, K, _matrix(out, "gemm_fp4: out", _FLOATS, (M, N), dev), _ld(out),
           _out_code(out.dtype))
     return out
@@ -437,8 +444,7 @@ def grouped_gemm_fp4(qa, sa_swz, qb, sb_swz, row_offsets, out_dtype=torch.bfloat
     sb_swz G consecutive layouts). sa_swz: A's grouped layout, at least as many bytes as the groups' rows need
     (grouped_scale_bytes_bound() always suffices). row_offsets: int32 CUDA [G + 1]."""
     dev = qa.device
-    _matrix(qa, "grouped_gemm_fp4: qa", _U8)
-    _need(isinstance(qb, torch.Tensor) and qb.dim() == 3 and qb.shape[2] == qa.shape[1], "grouped_gemm_fp4: qb must be [G, N, K/2]")
+    _need(qa.dim() == 2 and qb.dim() == 3 and qb.shape[2] == qa.shape[1], "grouped_gemm_fp4: qa [rows, K/2] and qb [G, N, K/2]")
     rows, K = qa.shape[0], 2 * qa.shape[1]
     G, N = qb.shape[0], qb.shape[1]
     pa = _packed(qa, "grouped_gemm_fp4: qa must be contiguous", torch.uint8, rows * K // 2, dev)
@@ -448,7 +454,7 @@ def grouped_gemm_fp4(qa, sa_swz, qb, sb_swz, row_offsets, out_dtype=torch.bfloat
     psa = _packed(sa_swz, "grouped_gemm_fp4: sa_swz", torch.uint8, sa_swz.numel(), dev)
     poff = _packed(row_offsets, "grouped_gemm_fp4: row_offsets must be int32 [G + 1]", torch.int32, G + 1, dev)
     if out is None:
-        out = torch.empty((rows, N), dtype=out_dtype, device=dev)
+        out = qa.new_empty((rows, N), dtype=out_dtype)
     _call("mx_grouped_gemm_fp4", dev, pa, psa, pb, psb, poff, G, rows, N, K,
           _matrix(out, "grouped_gemm_fp4: out", _FLOATS, (rows, N), dev), _ld(out), _out_code(out.dtype))
     return out
@@ -469,11 +475,14 @@ def route(logits: torch.Tensor, topk: int, score: str = "softmax", bias=None, gr
     pb = None if bias is None else _packed(bias, "route: bias must be fp32 [E]", torch.float32, E, dev)
     if out is None:
         _need(topk >= 1, "route: topk")
-        out = (torch.empty((T, topk), dtype=torch.int32, device=dev), torch.empty((T, topk), dtype=torch.float32, device=dev))
-    ids, weights = out
+        ids, weights = logits.new_empty((T, topk), dtype=torch.int32), logits.new_empty((T, topk), dtype=torch.float32)
+        pi, pw = ids.data_ptr(), weights.data_ptr()
+    else:
+        ids, weights = out
+        pi = _packed(ids, "route: ids must be int32 [T, topk]", torch.int32, T * topk, dev)
+        pw = _packed(weights, "route: weights must be fp32 [T, topk]", torch.float32, T * topk, dev)
     _call("mx_route", dev, p, _out_code(logits.dtype), T, E, _ld(logits), pb, MX_SCORE[score], groups, topk_groups,
-          MX_GROUP[group_score], topk, int(renormalize), scale, _packed(ids, "route: ids", torch.int32, T * topk, dev),
-          _packed(weights, "route: weights", torch.float32, T * topk, dev))
+          MX_GROUP[group_score], topk, int(renormalize), scale, pi, pw)
     return ids, weights
 
 
@@ -485,7 +494,7 @@ def route_backward(d_weights: torch.Tensor, logits: torch.Tensor, ids: torch.Ten
     T, E = logits.shape
     dev, topk = logits.device, ids.shape[1]
     if out is None:
-        out = torch.empty((T, E), dtype=logits.dtype, device=dev)
+        out = logits.new_empty((T, E))
     _call("mx_route_bwd", dev, _packed(d_weights, "route_backward: d_weights must be fp32 [T, topk]", torch.float32, T * topk, dev),
           p, _out_code(logits.dtype), T, E, _ld(logits), _packed(ids, "route_backward: ids must be int32 [T, topk]", torch.int32, T * topk, dev),
           MX_SCORE[score], topk, int(renormalize), scale, _matrix(out, "route_backward: out", (logits.dtype,), (T, E), dev), _ld(out))
@@ -501,14 +510,16 @@ def route_plan(ids: torch.Tensor, experts: int, out=None):
     p = _packed(ids, "route_plan: ids must be a contiguous int32 tensor", torch.int32, n, dev)
     size = int(lib().mx_route_plan_workspace_bytes(n, experts))
     _need(size >= 0, "route_plan: 1 to 1024 experts")
-    i32 = dict(dtype=torch.int32, device=dev)
     if out is None:
-        out = (torch.empty(experts + 1, **i32), torch.empty(ids.shape, **i32), torch.empty(experts, **i32))
-    off, slot_row, counts = out
-    ws = torch.empty(size, dtype=torch.uint8, device=dev) if size else None
-    _call("mx_route_plan", dev, p, n, experts, _packed(off, "route_plan: row_offsets", torch.int32, experts + 1, dev),
-          _packed(slot_row, "route_plan: slot_row", torch.int32, n, dev),
-          _packed(counts, "route_plan: counts", torch.int32, experts, dev), None if ws is None else ws.data_ptr())
+        off, slot_row, counts = ids.new_empty(experts + 1), torch.empty_like(ids), ids.new_empty(experts)
+        po, ps, pc = off.data_ptr(), slot_row.data_ptr(), counts.data_ptr()
+    else:
+        off, slot_row, counts = out
+        po = _packed(off, "route_plan: row_offsets must be int32 [experts + 1]", torch.int32, experts + 1, dev)
+        ps = _packed(slot_row, "route_plan: slot_row must be int32 like ids", torch.int32, n, dev)
+        pc = _packed(counts, "route_plan: counts must be int32 [experts]", torch.int32, experts, dev)
+    ws = ids.new_empty(size, dtype=torch.uint8) if size else None
+    _call("mx_route_plan", dev, p, n, experts, po, ps, pc, None if ws is None else ws.data_ptr())
     return off, slot_row, counts
 
 
@@ -529,7 +540,7 @@ def dispatch_quantize(x: torch.Tensor, slot_row: torch.Tensor, row_offsets: torc
     width = K if fmt == "mxfp8" else K // 2
     size = max(grouped_scale_bytes_bound(T * topk, E, K // 32), 0)
     if out is None:
-        out = (torch.empty((T * topk, width), dtype=torch.uint8, device=dev), torch.empty(size, dtype=torch.uint8, device=dev))
+        out = x.new_empty((T * topk, width), dtype=torch.uint8), x.new_empty(size, dtype=torch.uint8)
     q, s = out
     _call("mx_dispatch_quantize", dev, p, T, K, _ld(x), _packed(slot_row, "dispatch_quantize: slot_row must be int32", torch.int32, T * topk, dev),
           topk, _packed(row_offsets, "dispatch_quantize: row_offsets must be int32", torch.int32, E + 1, dev), E, MX_FORMAT[fmt],
@@ -545,7 +556,7 @@ def combine(rows: torch.Tensor, slot_row: torch.Tensor, weights=None, out_dtype=
     _need(slot_row.dim() == 2, "combine: slot_row [T, topk]")
     (T, topk), N, dev = slot_row.shape, rows.shape[1], rows.device
     if out is None:
-        out = torch.empty((T, N), dtype=out_dtype or rows.dtype, device=dev)
+        out = rows.new_empty((T, N), dtype=out_dtype or rows.dtype)
     _call("mx_combine", dev, p, _out_code(rows.dtype), rows.shape[0], _ld(rows),
           _packed(slot_row, "combine: slot_row must be int32", torch.int32, T * topk, dev),
           None if weights is None else _packed(weights, "combine: weights must be fp32 [T, topk]", torch.float32, T * topk, dev),
@@ -561,8 +572,8 @@ def combine_backward(dy: torch.Tensor, rows: torch.Tensor, slot_row: torch.Tenso
     (T, topk), (R, N), dev = slot_row.shape, rows.shape, rows.device
     if out is None:
         # Every row of a plan's partition is written; rows that no slot names stay as they are, so they start as 0.
-        out = (torch.empty((R, N), dtype=rows.dtype, device=dev) if R == T * topk else torch.zeros((R, N), dtype=rows.dtype, device=dev),
-               torch.empty((T, topk), dtype=torch.float32, device=dev) if need_weights else None)
+        out = (rows.new_empty((R, N)) if R == T * topk else rows.new_zeros((R, N)),
+               rows.new_empty((T, topk), dtype=torch.float32) if need_weights else None)
     d_rows, d_weights = out
     _call("mx_combine_bwd", dev, _matrix(dy, "combine_backward: dy must be [T, N], fp32 or BF16", _FLOATS, (T, N), dev), _out_code(dy.dtype), _ld(dy),
           p, _out_code(rows.dtype), R, _ld(rows), _packed(slot_row, "combine_backward: slot_row must be int32", torch.int32, T * topk, dev),
