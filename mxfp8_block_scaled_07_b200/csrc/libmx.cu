@@ -1092,25 +1092,29 @@ mx_status route_shape(int64_t T, int64_t E, int64_t topk, int64_t ld, mx_out_dty
     return MX_OK;
 }
 
-template <int NV>
-void launch_route(const RouteArgs& a, bool backward, mx_stream stream) {
-    const unsigned grid = static_cast<unsigned>(ceil_div(a.T, kRouteThreads / 32));
-    if (backward)
-        route_bwd_kernel<NV><<<grid, kRouteThreads, 0, stream>>>(a);
-    else
-        route_kernel<NV><<<grid, kRouteThreads, 0, stream>>>(a);
-}
+// route_kernel for nv experts per lane. Packed keys: BF16 logits that decide by themselves; several tokens per warp
+// where that measured faster (at most 128 experts and a batch that fills the device without it).
+constexpr int64_t kRouteManyTokens = 4096;
 
-mx_status launch_route_nv(int nv, const RouteArgs& a, bool backward, mx_stream stream) {
-    switch (nv) {
-        case 1: launch_route<1>(a, backward, stream); break;
-        case 2: launch_route<2>(a, backward, stream); break;
-        case 4: launch_route<4>(a, backward, stream); break;
-        case 8: launch_route<8>(a, backward, stream); break;
-        case 16: launch_route<16>(a, backward, stream); break;
-        default: launch_route<32>(a, backward, stream); break;
+template <int NV>
+void launch_route(const RouteArgs& a, bool packed, mx_stream stream) {
+    const bool many = packed && NV <= 4 && a.T >= kRouteManyTokens;
+    const int lanes = !many ? 32 : (a.k <= 8 ? 8 : 16);
+    const unsigned grid = static_cast<unsigned>(ceil_div(a.T, kRouteThreads / lanes));
+    if constexpr (NV <= 4) {
+        if (lanes == 8) {
+            route_kernel<NV, 8, true><<<grid, kRouteThreads, 0, stream>>>(a);
+            return;
+        }
+        if (lanes == 16) {
+            route_kernel<NV, 16, true><<<grid, kRouteThreads, 0, stream>>>(a);
+            return;
+        }
     }
-    return launched();
+    if (packed)
+        route_kernel<NV, 32, true><<<grid, kRouteThreads, 0, stream>>>(a);
+    else
+        route_kernel<NV, 32, false><<<grid, kRouteThreads, 0, stream>>>(a);
 }
 
 // Resident blocks per SM of a kernel, asked once per device and kept in `cache`.
@@ -1189,13 +1193,27 @@ mx_status mx_route(const void* logits, mx_out_dtype dtype, int64_t T, int64_t E,
     // All groups kept: the same as none.
     a.G = topk_groups == groups ? 1 : static_cast<int>(groups);
     a.topg = a.G == 1 ? 1 : static_cast<int>(topk_groups);
+    const int64_t per = E / groups;
+    a.per = FastDiv::of(per);
+    const int64_t lanes = per % nv == 0 ? per / nv : 0;
+    a.lanes_per_group = (lanes & (lanes - 1)) == 0 ? static_cast<int>(lanes) : 0;
+    a.vec_bias = bias && route_vec(bias, E, E, nv, MX_OUT_F32);
     a.bf16 = dtype == MX_OUT_BF16;
     a.vec = route_vec(logits, ld, E, nv, dtype);
     a.sigmoid = score == MX_SCORE_SIGMOID;
     a.top2 = group_score == MX_GROUP_TOP2;
     a.renorm = renormalize != 0;
     a.scale = scale;
-    return launch_route_nv(nv, a, false, stream);
+    const bool packed = a.bf16 && !bias && !(a.G > 1 && a.top2);
+    switch (nv) {
+        case 1: launch_route<1>(a, packed, stream); break;
+        case 2: launch_route<2>(a, packed, stream); break;
+        case 4: launch_route<4>(a, packed, stream); break;
+        case 8: launch_route<8>(a, packed, stream); break;
+        case 16: launch_route<16>(a, packed, stream); break;
+        default: launch_route<32>(a, packed, stream); break;
+    }
+    return launched();
 }
 
 mx_status mx_route_bwd(const float* d_weights, const void* logits, mx_out_dtype dtype, int64_t T, int64_t E, int64_t ld,
@@ -1209,7 +1227,6 @@ mx_status mx_route_bwd(const float* d_weights, const void* logits, mx_out_dtype 
         return MX_ERR_ALIGN;
     const DeviceInfo* d = nullptr;
     if (mx_status st = check_device(&d)) return st;
-    const int nv = route_nv(E);
     RouteArgs a{};
     a.x = logits;
     a.ids = const_cast<int32_t*>(ids);
@@ -1218,15 +1235,21 @@ mx_status mx_route_bwd(const float* d_weights, const void* logits, mx_out_dtype 
     a.E = static_cast<int>(E);
     a.k = static_cast<int>(topk);
     a.bf16 = dtype == MX_OUT_BF16;
-    a.vec = route_vec(logits, ld, E, nv, dtype);
+    a.vec = route_vec(logits, ld, E, 4, dtype);
     a.sigmoid = score == MX_SCORE_SIGMOID;
     a.renorm = renormalize != 0;
     a.scale = scale;
     a.dw = d_weights;
     a.dx = d_logits;
     a.ld_dx = ld_d;
-    a.vec_dx = route_vec(d_logits, ld_d, E, nv, dtype);
-    return launch_route_nv(nv, a, true, stream);
+    a.vec_dx = route_vec(d_logits, ld_d, E, 4, dtype);
+    const int lanes = topk <= 8 ? 8 : 16;             // one per slot; the other 32 / lanes - 1 tokens share the warp
+    const unsigned grid = static_cast<unsigned>(ceil_div(T, kRouteThreads / lanes));
+    if (lanes == 8)
+        route_bwd_kernel<8><<<grid, kRouteThreads, 0, stream>>>(a);
+    else
+        route_bwd_kernel<16><<<grid, kRouteThreads, 0, stream>>>(a);
+    return launched();
 }
 
 int64_t mx_route_plan_workspace_bytes(int64_t slots, int64_t E) {
@@ -1255,11 +1278,27 @@ mx_status mx_route_plan(const int32_t* ids, int64_t slots, int64_t E, int32_t* r
     a.n = static_cast<int32_t>(slots);
     a.E = static_cast<int32_t>(E);
     a.chunk = static_cast<int32_t>(ceil_div(std::max<int64_t>(slots, 1), blocks));
-    if (blocks > 1) {
-        counts_kernel<<<blocks, kPlanThreads, static_cast<size_t>(E + 1) * 4, stream>>>(a);
-        if (mx_status st = launched()) return st;
+    if (blocks == 1) {
+        plan_kernel<<<1, kPlanThreads, plan_smem_bytes(static_cast<int>(E)), stream>>>(a);
+        return launched();
     }
-    plan_kernel<<<blocks, kPlanThreads, plan_smem_bytes(static_cast<int>(E)), stream>>>(a);
+    counts_kernel<<<blocks, kPlanThreads, static_cast<size_t>(E + 1) * 4, stream>>>(a);
+    if (mx_status st = launched()) return st;
+    // The second kernel may start while the first still runs; it waits for it before it reads the counts.
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(blocks, 1, 1);
+    cfg.blockDim = dim3(kPlanThreads, 1, 1);
+    cfg.dynamicSmemBytes = plan_smem_bytes(static_cast<int>(E));
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    if (cudaLaunchKernelEx(&cfg, plan_kernel, a) != cudaSuccess) {
+        cudaGetLastError();
+        return MX_ERR_CUDA;
+    }
     return launched();
 }
 

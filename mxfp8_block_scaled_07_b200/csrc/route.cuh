@@ -20,6 +20,8 @@
 
 #include <cstdint>
 
+#include "fastdiv.cuh"
+
 namespace mx {
 
 constexpr int kRouteThreads = 128;
@@ -35,14 +37,17 @@ struct RouteArgs {
     float* w;                 // [T, k]
     int64_t T, ld;
     int E, k, G, topg;
+    FastDiv per;              // experts per group
+    int lanes_per_group;      // lanes whose experts make up one group (a power of two), 0: groups cut lanes
     int bf16, vec;            // element type; rows of NV experts per lane can be loaded as vectors
+    int vec_bias;
     int sigmoid, top2, renorm;
     float scale;
     // backward
     const float* dw;          // [T, k]
     void* dx;                 // [T, E], row stride ld_dx
     int64_t ld_dx;
-    int vec_dx;
+    int vec_dx;               // rows of four consecutive experts can be stored (vec: loaded) as vectors
 };
 
 // ---- rows of NV consecutive experts per lane ------------------------------------------------------
@@ -130,10 +135,16 @@ __device__ __forceinline__ double value_of(uint64_t k) {
     return __longlong_as_double(static_cast<long long>((k >> 63) ? k ^ 0x8000000000000000ull : ~k));
 }
 __device__ __forceinline__ uint32_t warp_max(uint32_t k) { return __reduce_max_sync(kFullMask, k); }
+__device__ __forceinline__ uint32_t warp_min(uint32_t k) { return __reduce_min_sync(kFullMask, k); }
 __device__ __forceinline__ uint64_t warp_max(uint64_t k) {
     const uint32_t hi = __reduce_max_sync(kFullMask, static_cast<uint32_t>(k >> 32));
     const uint32_t lo = __reduce_max_sync(kFullMask, (k >> 32) == hi ? static_cast<uint32_t>(k) : 0u);
     return (static_cast<uint64_t>(hi) << 32) | lo;
+}
+__device__ __forceinline__ uint64_t warp_min(uint64_t k) { return ~warp_max(~k); }
+template <class U>
+__device__ __forceinline__ U shfl_xor(U v, int o) {
+    return __shfl_xor_sync(kFullMask, v, o);
 }
 
 // Whether two keys lie too near together for fp32 to order them: also where the difference of two
@@ -142,92 +153,193 @@ __device__ __forceinline__ bool too_near(float hi, float lo, float tol) {
     return !(hi - lo > tol + 2.4e-7f * fmaxf(fabsf(hi), fabsf(lo)));
 }
 
-// Ranks the groups and clears the keys of all but the topg best. `last` and `next`: the ranks of the
-// worst group kept and the best one left (0 if none). Lane g ends up with group g's rank.
+// Rank of a group whose two largest keys are m and c (0: there is no such expert).
+template <class U>
+__device__ __forceinline__ U group_rank(U m, U c, bool top2) {
+    if (!top2 || c == 0) return m;
+    const U s = key_of(value_of(m) + value_of(c));
+    return s != 0 ? s : 1;           // a sum that overflows to -inf still ranks above a group without any expert
+}
+
+// Ranks the groups and clears the keys of all but the topg best. `last` and `next`: the ranks of the worst group
+// kept and the best one left (0 if none). Where groups are whole lanes (a power of two of them), a group's two
+// largest keys are merged over its lanes by shuffles and every group counts the groups before it with G
+// independent shuffles; otherwise groups are walked one by one.
 template <int NV, class U>
-__device__ __forceinline__ void route_groups(U (&key)[NV], int G, int per, int topg, bool top2, int lane, U& last,
-                                             U& next) {
+__device__ __forceinline__ void route_groups(const RouteArgs& a, U (&key)[NV], int lane, U& last, U& next) {
+    const int G = a.G, L = a.lanes_per_group, per = static_cast<int>(a.per.d);
+    const bool top2 = a.top2 != 0;
     U rank = 0;
-    for (int g = 0; g < G; ++g) {
-        const int lo = g * per - lane * NV, hi = lo + per;      // the group's range in this lane's indices
-        U b = 0;
-        int bi = -1;
+    int mine = lane;                 // the group whose rank this lane holds
+    if (L > 0) {
+        U m = 0, c = 0;
 #pragma unroll
-        for (int i = 0; i < NV; ++i)
-            if (i >= lo && i < hi && key[i] > b) {
-                b = key[i];
-                bi = i;
-            }
-        U m = warp_max(b);
-        if (top2 && m != 0) {
-            const int owner = __ffs(__ballot_sync(kFullMask, b == m)) - 1;
-            U c = 0;
+        for (int i = 0; i < NV; ++i) {
+            const U lo = key[i] < m ? key[i] : m;
+            m = key[i] < m ? m : key[i];
+            c = lo < c ? c : lo;
+        }
+        for (int o = 1; o < L; o <<= 1) {
+            const U m2 = shfl_xor(m, o), c2 = shfl_xor(c, o);
+            const U lo = m2 < m ? m2 : m, hi = m2 < m ? m : m2, cc = c2 < c ? c : c2;
+            m = hi;
+            c = lo < cc ? cc : lo;
+        }
+        rank = group_rank(m, c, top2);
+        mine = lane / L;
+    } else {
+        for (int g = 0; g < G; ++g) {
+            const int lo = g * per - lane * NV, hi = lo + per;      // the group's range in this lane's indices
+            U b = 0;
+            int bi = -1;
 #pragma unroll
             for (int i = 0; i < NV; ++i)
-                if (i >= lo && i < hi && !(lane == owner && i == bi) && key[i] > c) c = key[i];
-            c = warp_max(c);
-            if (c != 0) {
-                // A sum that overflows to -inf still ranks above a group without a choosable expert.
-                const U s = key_of(value_of(m) + value_of(c));
-                m = s != 0 ? s : 1;
+                if (i >= lo && i < hi && key[i] > b) {
+                    b = key[i];
+                    bi = i;
+                }
+            const U m = warp_max(b);
+            U c = 0;
+            if (top2 && m != 0) {
+                const int owner = __ffs(__ballot_sync(kFullMask, b == m)) - 1;
+#pragma unroll
+                for (int i = 0; i < NV; ++i)
+                    if (i >= lo && i < hi && !(lane == owner && i == bi) && key[i] > c) c = key[i];
+                c = warp_max(c);
             }
+            if (lane == g) rank = group_rank(m, c, top2);
         }
-        if (lane == g) rank = m;
     }
-    uint32_t kept = 0;
-    last = next = 0;
-    for (int j = 0; j <= topg; ++j) {
-        const U m = warp_max(rank);
-        if (m == 0) break;
-        if (j == topg) {
-            next = m;
-            break;
-        }
-        last = m;
-        const int g = __ffs(__ballot_sync(kFullMask, rank == m)) - 1;
-        kept |= 1u << g;
-        if (lane == g) rank = 0;
+    int before = 0;
+    for (int g = 0; g < G; ++g) {
+        const U r = __shfl_sync(kFullMask, rank, L > 0 ? g * L : g);
+        before += r > rank || (r == rank && g < mine);
     }
+    const bool kept = rank != 0 && before < a.topg;
+    last = warp_min(kept ? rank : ~static_cast<U>(0));
+    next = warp_max(kept ? static_cast<U>(0) : rank);
+    const uint32_t mask = __ballot_sync(kFullMask, kept);
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-        const int g = (lane * NV + i) / per;
-        if (g >= 32 || !((kept >> g) & 1u)) key[i] = 0;
+        const bool in = L > 0 ? kept : ((mask >> (a.per.div(lane * NV + i) & 31u)) & 1u) != 0;
+        if (!in) key[i] = 0;
     }
 }
 
-// The n largest keys, largest first, ties to the lowest index: lane j < n gets slot j's expert and key
-// (-1 and 0 when fewer experts can be chosen). Lanes hold consecutive experts, so the lowest lane that
-// holds the maximum holds the lowest index.
-template <int NV, class U>
-__device__ __forceinline__ void route_select(U (&key)[NV], int n, int lane, int& id, U& slot_key) {
-    id = -1;
-    slot_key = 0;
-    for (int j = 0; j < n; ++j) {
-        U b = key[0];
-        int bi = 0;
+// The n largest keys, largest first, ties to the lowest index: lane j gets slot j's expert and key; they stay
+// as they are where fewer experts can be chosen. Lanes hold consecutive experts, so the lowest lane that holds
+// the maximum holds the lowest index, and inside a lane the tree keeps the lower one of equals. LEFT: also the best
+// expert left out and its key (-1 and 0 if none), in every lane.
+template <int NV, bool LEFT, class U>
+__device__ __forceinline__ void route_select(U (&key)[NV], int n, int lane, int& id, U& slot_key, int& left, U& left_key) {
+    left = -1;
+    left_key = 0;
+    for (int j = 0; j < n + (LEFT ? 1 : 0); ++j) {
+        U b[NV];
+        int bi[NV];
 #pragma unroll
-        for (int i = 1; i < NV; ++i)
-            if (key[i] > b) {
-                b = key[i];
-                bi = i;
+        for (int i = 0; i < NV; ++i) {
+            b[i] = key[i];
+            bi[i] = i;
+        }
+#pragma unroll
+        for (int h = 1; h < NV; h <<= 1)
+#pragma unroll
+            for (int i = 0; i < NV; i += 2 * h) {
+                const bool right = b[i + h] > b[i];
+                b[i] = right ? b[i + h] : b[i];
+                bi[i] = right ? bi[i + h] : bi[i];
             }
-        const U m = warp_max(b);
+        const U m = warp_max(b[0]);
         if (m == 0) break;
-        const int owner = __ffs(__ballot_sync(kFullMask, b == m)) - 1;
-        const int e = __shfl_sync(kFullMask, lane * NV + bi, owner);
+        const int owner = __ffs(__ballot_sync(kFullMask, b[0] == m)) - 1;
+        const int e = __shfl_sync(kFullMask, lane * NV + bi[0], owner);
+        if (LEFT && j == n) {
+            left = e;
+            left_key = m;
+            break;
+        }
         if (lane == j) {
             id = e;
             slot_key = m;
         }
-        if (lane == owner) {
 #pragma unroll
-            for (int i = 0; i < NV; ++i)
-                if (i == bi) key[i] = 0;
-        }
+        for (int i = 0; i < NV; ++i)
+            if (lane * NV + i == e) key[i] = 0;
     }
 }
 
-// The choice in fp64, for a token that fp32 cannot decide.
+// BF16 logits that decide by themselves: the key's 16 bits above the expert's index counted down, one word per
+// expert, all different. One warp maximum then is the key, the expert and the tie rule at once. Each lane sorts
+// its words (a network of 0, 1, 5 or 19 exchanges) and the winner's lane moves up its next.
+// (key_of() + 0x8000) >> 16: BF16 values have 16 zero bits (ones below zero, which carry alike), and the largest
+// finite float, which +inf stands for, rounds up past BF16's largest.
+template <int NV>
+__device__ __forceinline__ uint32_t packed_key(uint32_t key, int e) {
+    return ((key + 0x8000u) & 0xFFFF0000u) | (0xFFFFu - static_cast<uint32_t>(e));
+}
+__device__ __forceinline__ void exchange(uint32_t& a, uint32_t& b) {
+    const uint32_t hi = max(a, b);
+    b = min(a, b);
+    a = hi;
+}
+template <int NV>
+__device__ __forceinline__ void sort_keys(uint32_t (&key)[NV]) {
+    if constexpr (NV == 2) exchange(key[0], key[1]);
+    if constexpr (NV == 4) {
+        exchange(key[0], key[1]);
+        exchange(key[2], key[3]);
+        exchange(key[0], key[2]);
+        exchange(key[1], key[3]);
+        exchange(key[1], key[2]);
+    }
+    if constexpr (NV == 8) {
+        constexpr int kNet[19][2] = {{0, 1}, {2, 3}, {4, 5}, {6, 7}, {0, 2}, {1, 3}, {4, 6}, {5, 7}, {1, 2}, {5, 6},
+                                     {0, 4}, {3, 7}, {1, 5}, {2, 6}, {1, 4}, {3, 6}, {2, 4}, {3, 5}, {3, 4}};
+#pragma unroll
+        for (int i = 0; i < 19; ++i) exchange(key[kNet[i][0]], key[kNet[i][1]]);
+    }
+}
+// The choice of TOK tokens at once (their chains of maxima run side by side): lane q * LPT + j gets token q's slot j
+// as its packed key, 0 if there is none.
+template <int NV, int TOK, int LPT>
+__device__ __forceinline__ uint32_t route_select_packed(uint32_t (&key)[TOK][NV], int n, int lane) {
+    constexpr bool kSorted = NV <= 8;
+    if constexpr (kSorted) {
+#pragma unroll
+        for (int q = 0; q < TOK; ++q) sort_keys<NV>(key[q]);
+    }
+    uint32_t got = 0;
+    for (int j = 0; j < n; ++j) {
+        uint32_t m[TOK];
+#pragma unroll
+        for (int q = 0; q < TOK; ++q) {
+            uint32_t b = key[q][0];
+            if constexpr (!kSorted) {
+#pragma unroll
+                for (int i = 1; i < NV; ++i) b = max(b, key[q][i]);
+            }
+            m[q] = __reduce_max_sync(kFullMask, b);
+        }
+#pragma unroll
+        for (int q = 0; q < TOK; ++q) {
+            if (lane == q * LPT + j) got = m[q];
+            if constexpr (kSorted) {
+                if (key[q][0] == m[q]) {
+#pragma unroll
+                    for (int i = 0; i + 1 < NV; ++i) key[q][i] = key[q][i + 1];
+                    key[q][NV - 1] = 0;
+                }
+            } else {
+#pragma unroll
+                for (int i = 0; i < NV; ++i) key[q][i] = key[q][i] == m[q] ? 0u : key[q][i];
+            }
+        }
+    }
+    return got >= 0x10000u ? got : 0u;       // below: nothing was left that can be chosen
+}
+
+// The choice in fp64, for a token that fp32 cannot decide: slot j's expert in lane j.
 template <int NV>
 __device__ __noinline__ int route_exact(const RouteArgs& a, const float (&v)[NV], float M, int lane) {
     const double kNone = __longlong_as_double(0xFFF0000000000000ll);
@@ -250,216 +362,353 @@ __device__ __noinline__ int route_exact(const RouteArgs& a, const float (&v)[NV]
         }
         key[i] = key_of(s);
     }
-    uint64_t last, next, slot_key;
-    if (a.G > 1) route_groups(key, a.G, a.E / a.G, a.topg, a.top2 != 0, lane, last, next);
-    int id;
-    route_select(key, a.k, lane, id, slot_key);
+    uint64_t last, next, slot_key = 0, left_key;
+    if (a.G > 1) route_groups(a, key, lane, last, next);
+    int id = -1, left;
+    route_select<NV, false>(key, a.k, lane, id, slot_key, left, left_key);
     return id;
 }
 
-// One warp per token; lane l holds the NV consecutive experts l * NV .. of the row.
-//
-// Bound: one read of the logits. Measured figures and what they are made of stand with the entry point
-// table of the design notes; at these sizes (a few MB) the selection's dependent warp reductions, two
-// per chosen expert, weigh more than the bytes.
 template <int NV>
-__global__ void __launch_bounds__(kRouteThreads) route_kernel(const __grid_constant__ RouteArgs a) {
-    const int lane = threadIdx.x & 31;
-    const int64_t t = static_cast<int64_t>(blockIdx.x) * (kRouteThreads / 32) + (threadIdx.x >> 5);
-    if (t >= a.T) return;
-    float v[NV];
+__device__ __forceinline__ void route_load_row(const RouteArgs& a, int64_t t, int lane, float (&v)[NV]) {
     if (a.bf16)
         route_load<NV>(static_cast<const uint16_t*>(a.x) + t * a.ld, a.E, lane, a.vec != 0, v);
     else
         route_load<NV>(static_cast<const uint32_t*>(a.x) + t * a.ld, a.E, lane, a.vec != 0, v);
+}
 
+// A warp takes 32 / LPT tokens, LPT lanes for the slots of each. A row is spread over the whole warp, NV consecutive
+// experts l * NV .. in lane l, while its experts are chosen; the slots' arithmetic and stores then run for all of
+// the warp's tokens at once. PACKED: BF16 logits that decide by themselves.
+//
+// Bound by the choice's instructions and their latency, not by the one read of the logits (20 480 x 128 BF16 are
+// 5 MB, less than a microsecond): some 25 instructions per chosen expert, 8 with packed keys, whose chains of maxima
+// run side by side for the warp's tokens. Several tokens per warp are for large batches with packed keys and at most
+// 128 experts: 20 480 x 128, top 8: 8.8 us with four tokens a warp, 11.1 us with one; 16 tokens: 3.5 and 2.6 us;
+// 20 480 x 256: 15.4 and 15.1 us. Without packed keys a warp's tokens only queue up (sigmoid with bias, 20 480 x 128:
+// 28.8 us with four, 23.1 us with one).
+template <int NV, int LPT, bool PACKED>
+__global__ void __launch_bounds__(kRouteThreads) route_kernel(const __grid_constant__ RouteArgs a) {
+    constexpr int kTokens = 32 / LPT;
+    static_assert(PACKED || kTokens == 1, "the general form takes one token per warp");
+    const int lane = threadIdx.x & 31;
+    const int64_t t0 = (static_cast<int64_t>(blockIdx.x) * (kRouteThreads / 32) + (threadIdx.x >> 5)) * kTokens;
+    if (t0 >= a.T) return;
     const float kNone = __int_as_float(0xFF800000);
     const bool by_logit = a.bias == nullptr && !(a.G > 1 && a.top2);
-    float M = kNone, z = 0.0f;
-    if (!a.sigmoid && !(by_logit && a.renorm)) {
-        // Softmax over the row. M of a row without any expert stays -inf and is never subtracted.
+    const bool row_softmax = !a.sigmoid && !(by_logit && a.renorm);     // the weights or keys need the row's sum
+    int id = -1;
+    float x = kNone, M = kNone, z = 0.0f;                               // the slot's expert and logit; its row's max, sum
+    auto row_max_sum = [&](const float(&v)[NV], float(&f)[NV], float& m, float& sum) {
+        // M of a row without any expert stays -inf and is never subtracted.
+        m = kNone;
+        sum = 0.0f;
 #pragma unroll
-        for (int i = 0; i < NV; ++i) M = fmaxf(M, v[i]);
+        for (int i = 0; i < NV; ++i) m = fmaxf(m, v[i]);
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(kFullMask, M, o));
-#pragma unroll
-        for (int i = 0; i < NV; ++i) z += v[i] > kNone ? expf(v[i] - M) : 0.0f;
-        z = warp_sum(z);
-    }
-    uint32_t key[NV];
-    float tol = 0.0f;
-    if (by_logit) {
-#pragma unroll
-        for (int i = 0; i < NV; ++i) key[i] = key_of(v[i]);
-    } else {
-        // |fp32 score - score|: sigmoid below 2.5e-7 (x > 0: half of expf's 2 ulp, 2^-23, and two roundings,
-        // 2^-23, of a score of at most 1; x <= 0: 2^-22 and 2^-23 of at most a half); softmax at
-        // most (2^-22 expf + 5 * 2^-24 from rounded x - max weighted by p + (NV + 5) * 2^-24 from the
-        // sum + 2^-24 from the division) of the row's largest score 1 / z. Twice that for a pair; the
-        // rounding of the sum with the bias, 2^-24 of each key, is in too_near(); twice all for a sum of two.
-        tol = a.sigmoid ? 5e-7f : (1.4e-6f + 1.2e-7f * NV) / z;
-        if (a.G > 1 && a.top2) tol *= 2.0f;
+        for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(kFullMask, m, o));
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
-            const int e = lane * NV + i;
-            float s = kNone;
-            if (e < a.E && v[i] > kNone) {
-                s = a.sigmoid ? route_sigmoid(v[i], 0.0f) : expf(v[i] - M) / z;
-                if (a.bias) s += a.bias[e];
+            f[i] = v[i] > kNone ? expf(v[i] - m) : 0.0f;
+            sum += f[i];
+        }
+        sum = warp_sum(sum);
+    };
+    if constexpr (PACKED) {
+        uint32_t key[kTokens][NV];
+#pragma unroll
+        for (int q = 0; q < kTokens; ++q) {
+            const int64_t t = t0 + q < a.T ? t0 + q : a.T - 1;
+            float v[NV];
+            route_load_row<NV>(a, t, lane, v);
+            if (row_softmax) {
+                float f[NV], m, sum;
+                row_max_sum(v, f, m, sum);
+                if (lane / LPT == q) {
+                    M = m;
+                    z = sum;
+                }
             }
-            key[i] = key_of(s);
+#pragma unroll
+            for (int i = 0; i < NV; ++i) key[q][i] = packed_key<NV>(key_of(v[i]), lane * NV + i);
+            if (a.G > 1) {
+                // A group without any expert to choose must not be kept for its indices alone.
+                uint32_t last, next;
+#pragma unroll
+                for (int i = 0; i < NV; ++i) key[q][i] = key[q][i] < 0x10000u ? 0u : key[q][i];
+                route_groups(a, key[q], lane, last, next);
+            }
+        }
+        const uint32_t got = route_select_packed<NV, kTokens, LPT>(key, a.k, lane);
+        if (got != 0) {
+            id = static_cast<int>(0xFFFFu - (got & 0xFFFFu));
+            // The logit back from its key: positive as it was, negative less the rounding's carry, +inf's stand-in.
+            const uint32_t top = got & 0xFFFF0000u;
+            x = value_of(top >= 0xFF800000u ? 0xFF7FFFFFu : (top & 0x80000000u ? top : top - 1u));
+        }
+    } else {
+        const int64_t t = t0;
+        float v[NV], f[NV];
+        route_load_row<NV>(a, t, lane, v);
+        if (row_softmax) row_max_sum(v, f, M, z);
+        uint32_t key[NV], last, next, slot_key = 0, left_key;
+        int left;
+        if (by_logit) {
+#pragma unroll
+            for (int i = 0; i < NV; ++i) key[i] = key_of(v[i]);
+            if (a.G > 1) route_groups(a, key, lane, last, next);
+            route_select<NV, false>(key, a.k, lane, id, slot_key, left, left_key);
+            if (slot_key != 0) x = value_of(slot_key);
+        } else {
+            float b[NV];
+            if (a.bias) {
+                route_load<NV>(reinterpret_cast<const uint32_t*>(a.bias), a.E, lane, a.vec_bias != 0, b);
+            } else {
+#pragma unroll
+                for (int i = 0; i < NV; ++i) b[i] = 0.0f;
+            }
+            // |fp32 score - score|. Sigmoid, 1 / (1 + e^-x) with __expf (2 + 1.17 |x| ulp) and __fdividef (2 ulp):
+            // s (1 - s) (2 + 1.17 |x|) 2^-23 <= 0.65 * 2^-23, + 2^-22 + 2^-24 < 3.9e-7. Softmax, of the row's largest
+            // score 1 / z: expf and the sum's terms 2^-22 each, x - M rounded 2^-24 |x - M|, weighted by p in the score
+            // (0.4) and in z (its mean is below ln 1024 = 6.9), the sum (NV + 5) 2^-24, two products 2^-23:
+            // 1.4e-6 + 6e-8 NV. Twice that for a pair of keys, and twice again for a sum of two; the rounding of a
+            // key, 2^-24 of it, is in too_near().
+            float tol = a.sigmoid ? 8e-7f : (2.8e-6f + 1.2e-7f * NV) / z;
+            if (a.G > 1 && a.top2) tol *= 2.0f;
+            const float inv_z = 1.0f / z;
+#pragma unroll
+            for (int i = 0; i < NV; ++i) {
+                float s = a.sigmoid ? __fdividef(1.0f, 1.0f + __expf(-v[i])) : f[i] * inv_z;
+                s = v[i] > kNone ? s + b[i] : kNone;
+                key[i] = key_of(s);
+            }
+            bool near = false;
+            if (a.G > 1) {
+                route_groups(a, key, lane, last, next);
+                if (next != 0) near = too_near(value_of(last), value_of(next), tol);
+            }
+            route_select<NV, true>(key, a.k, lane, id, slot_key, left, left_key);
+            // Slot j against slot j + 1, the last one against the best expert left out. Two experts with the same
+            // logit and the same bias have the same score in any precision.
+            const int slot = lane;
+            const bool mine = slot < a.k && slot_key != 0;
+            float bj = 0.0f;
+            if (mine) {
+                x = route_logit(a, t, id);
+                if (a.bias) bj = a.bias[id];
+            }
+            uint32_t k2 = __shfl_down_sync(kFullMask, slot_key, 1);
+            float x2 = __shfl_down_sync(kFullMask, x, 1), b2 = __shfl_down_sync(kFullMask, bj, 1);
+            if (slot == a.k - 1) {
+                k2 = left_key;
+                if (left >= 0) {
+                    x2 = route_logit(a, t, left);
+                    b2 = a.bias ? a.bias[left] : 0.0f;
+                }
+            }
+            if (mine && k2 != 0 && !(x == x2 && bj == b2)) near |= too_near(value_of(slot_key), value_of(k2), tol);
+            if (__any_sync(kFullMask, near)) {
+                id = route_exact<NV>(a, v, M, lane);
+                x = id >= 0 ? route_logit(a, t, id) : kNone;
+            }
         }
     }
-    bool near = false;
-    if (a.G > 1) {
-        uint32_t last, next;
-        route_groups(key, a.G, a.E / a.G, a.topg, a.top2 != 0, lane, last, next);
-        if (!by_logit && next != 0) near = too_near(value_of(last), value_of(next), tol);
-    }
-    int id;
-    uint32_t slot_key;
-    route_select(key, by_logit ? a.k : a.k + 1, lane, id, slot_key);
-    float x = kNone;
-    if (id >= 0) x = route_logit(a, t, id);
-    if (!by_logit) {
-        // Slot j against slot j + 1; slot k is the best expert left out. Two experts with the same logit
-        // and the same bias have the same score in any precision.
-        const float b = id >= 0 && a.bias ? a.bias[id] : 0.0f;
-        const uint32_t k2 = __shfl_down_sync(kFullMask, slot_key, 1);
-        const float x2 = __shfl_down_sync(kFullMask, x, 1), b2 = __shfl_down_sync(kFullMask, b, 1);
-        if (lane < a.k && slot_key != 0 && k2 != 0 && !(x == x2 && b == b2))
-            near |= too_near(value_of(slot_key), value_of(k2), tol);
-        if (__any_sync(kFullMask, near)) {
-            id = route_exact<NV>(a, v, M, lane);
-            x = id >= 0 && lane < a.k ? route_logit(a, t, id) : kNone;
-        }
-    }
-    if (lane >= a.k) x = kNone;
     const bool got = x > kNone;
     float s = 0.0f;
     if (a.renorm) {
         // Ratios of the chosen scores. Softmax: a softmax over the chosen alone.
         float m = x;
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(kFullMask, m, o));
+        for (int o = LPT / 2; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(kFullMask, m, o));
         if (got) s = a.sigmoid ? route_sigmoid(x, fminf(m, 0.0f)) : expf(x - m);
-        const float sum = warp_sum(s);
+        float sum = s;
+#pragma unroll
+        for (int o = LPT / 2; o > 0; o >>= 1) sum += __shfl_xor_sync(kFullMask, sum, o);
         if (got) s /= sum;
     } else if (got) {
         s = a.sigmoid ? route_sigmoid(x, 0.0f) : expf(x - M) / z;
     }
-    if (lane < a.k) {
-        a.ids[t * a.k + lane] = got ? id : -1;
-        a.w[t * a.k + lane] = a.scale * s;
+    const int64_t t = t0 + lane / LPT;
+    const int j = lane % LPT;
+    if (t < a.T && j < a.k) {
+        a.ids[t * a.k + j] = got ? id : -1;
+        a.w[t * a.k + j] = a.scale * s;
     }
 }
 
 // Gradient of the weights with respect to the logits, the choice held fixed. With dw the incoming
 // gradient and r_j = s_j / sum of the chosen s:
-//   renormalized: ds-part c_j = scale * r_j * (dw_j - sum dw r); softmax: dx_j = c_j;
+//   renormalized: c_j = scale * r_j * (dw_j - sum dw r); softmax: dx_j = c_j;
 //                 sigmoid: dx_j = c_j * (1 - s_j); every other dx is 0;
 //   otherwise:    sigmoid: dx_j = scale * dw_j * s_j (1 - s_j), others 0;
 //                 softmax: dx_e = p_e * (d_e - sum_j d_j p_j) with d_j = scale * dw_j at the chosen.
-// Only the last form reads the whole row; the others read the k chosen logits and write the row.
-template <int NV>
+// Only the last form reads whole rows; the others read the k chosen logits and write the row.
+//
+// A warp takes 32 / LPT tokens (LPT = 8 or 16 lanes, one per slot, for each): the slots' arithmetic runs for all of
+// them at once. Then row by row: the chosen experts' parts are put into a row of zeros in shared memory, the row is
+// read back four experts per lane, finished and stored, and the parts are cleared again. An expert named twice gets
+// the sum of its parts in slot order.
+template <int LPT>
 __global__ void __launch_bounds__(kRouteThreads) route_bwd_kernel(const __grid_constant__ RouteArgs a) {
+    constexpr int kTokens = 32 / LPT;
+    __shared__ __align__(16) float rows[kRouteThreads / 32][kRouteMaxExperts];
     const int lane = threadIdx.x & 31;
-    const int64_t t = static_cast<int64_t>(blockIdx.x) * (kRouteThreads / 32) + (threadIdx.x >> 5);
-    if (t >= a.T) return;
+    const int64_t t0 = (static_cast<int64_t>(blockIdx.x) * (kRouteThreads / 32) + (threadIdx.x >> 5)) * kTokens;
+    if (t0 >= a.T) return;
     const float kNone = __int_as_float(0xFF800000);
+    float* buf = rows[threadIdx.x >> 5];
+    const int q = lane / LPT, j = lane % LPT;
     int id = -1;
     float g = 0.0f, x = kNone;
-    if (lane < a.k) {
-        id = a.ids[t * a.k + lane];
-        if (id < 0 || id >= a.E) id = -1;
-        if (id >= 0) {
-            x = route_logit(a, t, id);
-            if (x > kNone) g = a.dw[t * a.k + lane];
-        }
+    if (t0 + q < a.T && j < a.k) {
+        const int64_t at = (t0 + q) * a.k + j;
+        id = a.ids[at];
+        g = a.dw[at];
+        if (id >= 0 && id < a.E) x = route_logit(a, t0 + q, id);
     }
+    const int chunks = (a.E + 127) / 128;                 // pieces of 128 experts, four per lane
+    for (int c = 0; c < chunks; ++c) reinterpret_cast<float4*>(buf)[c * 32 + lane] = make_float4(0, 0, 0, 0);
     const bool got = x > kNone;
-    float out[NV];
+    if (!got) g = 0.0f;
+
+    auto load4 = [&](int64_t t, int c, float(&v)[4]) {
+        const int e0 = c * 128 + lane * 4;
+        if (a.vec && e0 < a.E) {
+            if (a.bf16) {
+                const uint2 r = __ldg(reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(a.x) + t * a.ld + e0));
+                v[0] = __uint_as_float(r.x << 16);
+                v[1] = __uint_as_float(r.x & 0xFFFF0000u);
+                v[2] = __uint_as_float(r.y << 16);
+                v[3] = __uint_as_float(r.y & 0xFFFF0000u);
+            } else {
+                const float4 r = __ldg(reinterpret_cast<const float4*>(static_cast<const float*>(a.x) + t * a.ld + e0));
+                v[0] = r.x; v[1] = r.y; v[2] = r.z; v[3] = r.w;
+            }
 #pragma unroll
-    for (int i = 0; i < NV; ++i) out[i] = 0.0f;
-    float c = 0.0f, row = 0.0f;              // chosen expert's own part; what every expert's p is multiplied with
-    float v[NV], M = kNone, z = 1.0f;
-    const bool dense = !a.sigmoid && !a.renorm;
-    if (dense) {
-        if (a.bf16)
-            route_load<NV>(static_cast<const uint16_t*>(a.x) + t * a.ld, a.E, lane, a.vec != 0, v);
-        else
-            route_load<NV>(static_cast<const uint32_t*>(a.x) + t * a.ld, a.E, lane, a.vec != 0, v);
+            for (int i = 0; i < 4; ++i) v[i] = v[i] == v[i] ? fminf(v[i], 3.402823466e38f) : kNone;
+        } else {
 #pragma unroll
-        for (int i = 0; i < NV; ++i) M = fmaxf(M, v[i]);
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(kFullMask, M, o));
-        z = 0.0f;
-#pragma unroll
-        for (int i = 0; i < NV; ++i) {
-            v[i] = v[i] > kNone ? expf(v[i] - M) : 0.0f;
-            z += v[i];
+            for (int i = 0; i < 4; ++i) v[i] = e0 + i < a.E ? route_logit(a, t, e0 + i) : kNone;
         }
-        z = warp_sum(z);
+    };
+    auto sum_slots = [&](float s) {
+#pragma unroll
+        for (int o = LPT / 2; o > 0; o >>= 1) s += __shfl_xor_sync(kFullMask, s, o);
+        return s;
+    };
+    const bool dense = !a.sigmoid && !a.renorm;
+    float c = 0.0f, row = 0.0f, M = kNone, z = 0.0f;      // the chosen expert's part; the token's sum of d p, max, sum
+    if (dense) {
+        // All tokens' rows side by side (a token past the end stands for the last one): the maxima and the sums.
+        float m[kTokens], s[kTokens];
+#pragma unroll
+        for (int qq = 0; qq < kTokens; ++qq) {
+            m[qq] = kNone;
+            s[qq] = 0.0f;
+        }
+        for (int ch = 0; ch < chunks; ++ch) {
+            float v[kTokens][4];
+#pragma unroll
+            for (int qq = 0; qq < kTokens; ++qq) load4(t0 + qq < a.T ? t0 + qq : a.T - 1, ch, v[qq]);
+#pragma unroll
+            for (int qq = 0; qq < kTokens; ++qq) {
+                // A running maximum and the sum relative to it.
+                const float mm = fmaxf(fmaxf(fmaxf(v[qq][0], v[qq][1]), fmaxf(v[qq][2], v[qq][3])), m[qq]);
+                if (mm > m[qq]) s[qq] = m[qq] > kNone ? s[qq] * expf(m[qq] - mm) : 0.0f;
+                m[qq] = mm;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) s[qq] += v[qq][i] > kNone ? expf(v[qq][i] - mm) : 0.0f;
+            }
+        }
+#pragma unroll
+        for (int qq = 0; qq < kTokens; ++qq) {
+            float mm = m[qq];
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) mm = fmaxf(mm, __shfl_xor_sync(kFullMask, mm, o));
+            const float sum = warp_sum(m[qq] > kNone ? s[qq] * expf(m[qq] - mm) : 0.0f);
+            if (q == qq) {
+                M = mm;
+                z = sum;
+            }
+        }
         const float p = got ? expf(x - M) / z : 0.0f;
         c = a.scale * g * p;
-        row = warp_sum(c);
+        row = sum_slots(c);
     } else if (a.renorm) {
         float m = x;
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(kFullMask, m, o));
+        for (int o = LPT / 2; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(kFullMask, m, o));
         float s = 0.0f;
         if (got) s = a.sigmoid ? route_sigmoid(x, fminf(m, 0.0f)) : expf(x - m);
-        const float sum = warp_sum(s);
+        const float sum = sum_slots(s);
         const float r = got ? s / sum : 0.0f;
-        const float dot = warp_sum(g * r);
+        const float dot = sum_slots(g * r);
         c = a.scale * r * (g - dot);
         if (a.sigmoid && got) c *= route_sigmoid(-x, 0.0f);       // 1 - s
     } else if (got) {
         c = a.scale * g * route_sigmoid(x, 0.0f) * route_sigmoid(-x, 0.0f);
     }
-    for (int j = 0; j < a.k; ++j) {
-        const int e = __shfl_sync(kFullMask, id, j) - lane * NV;
-        const float cj = __shfl_sync(kFullMask, c, j);
-#pragma unroll
-        for (int i = 0; i < NV; ++i)
-            if (i == e) out[i] += cj;
-    }
-    if (dense && z > 0.0f) {
-#pragma unroll
-        for (int i = 0; i < NV; ++i) out[i] -= v[i] / z * row;
-    }
-    const int e0 = lane * NV;
-    if (a.bf16) {
-        uint16_t h[NV];
-#pragma unroll
-        for (int i = 0; i < NV; ++i) h[i] = __bfloat16_as_ushort(__float2bfloat16_rn(out[i]));
-        uint16_t* dst = static_cast<uint16_t*>(a.dx) + t * a.ld_dx + e0;
-        constexpr int kBytes = NV * 2 < 16 ? NV * 2 : 16;
-        using V = typename RouteVec<kBytes>::T;
-        if (a.vec_dx) {
-            if (e0 < a.E)
-#pragma unroll
-                for (int q = 0; q < NV * 2 / kBytes; ++q)
-                    reinterpret_cast<V*>(dst)[q] = *reinterpret_cast<const V*>(&h[q * (kBytes / 2)]);
-        } else {
-#pragma unroll
-            for (int i = 0; i < NV; ++i)
-                if (e0 + i < a.E) dst[i] = h[i];
+    // An expert that two slots of a token name: the first one's lane gets the sum.
+    const uint32_t same = __match_any_sync(kFullMask, got ? (static_cast<uint32_t>(q) << 16) | static_cast<uint32_t>(id)
+                                                          : 0x80000000u | static_cast<uint32_t>(lane));
+    bool put = got;
+    if (__any_sync(kFullMask, __popc(same) > 1)) {
+        put = got && lane == __ffs(same) - 1;
+        float s = 0.0f;
+        for (int jj = 0; jj < LPT; ++jj) {
+            const float cj = __shfl_sync(kFullMask, c, q * LPT + jj);
+            if ((same >> (q * LPT + jj)) & 1u) s += cj;
         }
-    } else {
-        float* dst = static_cast<float*>(a.dx) + t * a.ld_dx + e0;
-        constexpr int kBytes = NV * 4 < 16 ? NV * 4 : 16;
-        using V = typename RouteVec<kBytes>::T;
-        if (a.vec_dx) {
-            if (e0 < a.E)
+        c = s;
+    }
 #pragma unroll
-                for (int q = 0; q < NV * 4 / kBytes; ++q)
-                    reinterpret_cast<V*>(dst)[q] = *reinterpret_cast<const V*>(&out[q * (kBytes / 4)]);
-        } else {
+    for (int qq = 0; qq < kTokens; ++qq) {
+        const int64_t t = t0 + qq;
+        if (t >= a.T) break;
+        if (put && q == qq) buf[id] = c;
+        __syncwarp();
+        const float mq = __shfl_sync(kFullMask, M, qq * LPT), zq = __shfl_sync(kFullMask, z, qq * LPT);
+        const float rq = __shfl_sync(kFullMask, row, qq * LPT);
+        for (int ch = 0; ch < chunks; ++ch) {
+            const float4 o4 = reinterpret_cast<const float4*>(buf)[ch * 32 + lane];
+            float o[4] = {o4.x, o4.y, o4.z, o4.w};
+            if (dense) {
+                float v[4];
+                load4(t, ch, v);
 #pragma unroll
-            for (int i = 0; i < NV; ++i)
-                if (e0 + i < a.E) dst[i] = out[i];
+                for (int i = 0; i < 4; ++i)
+                    if (v[i] > kNone) o[i] -= expf(v[i] - mq) / zq * rq;
+            }
+            const int e0 = ch * 128 + lane * 4;
+            const int64_t at = t * a.ld_dx + e0;
+            if (a.bf16) {
+                uint16_t h[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) h[i] = __bfloat16_as_ushort(__float2bfloat16_rn(o[i]));
+                uint16_t* dst = static_cast<uint16_t*>(a.dx) + at;
+                if (a.vec_dx) {
+                    if (e0 < a.E)
+                        *reinterpret_cast<uint2*>(dst) = make_uint2(h[0] | (static_cast<uint32_t>(h[1]) << 16),
+                                                                    h[2] | (static_cast<uint32_t>(h[3]) << 16));
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        if (e0 + i < a.E) dst[i] = h[i];
+                }
+            } else {
+                float* dst = static_cast<float*>(a.dx) + at;
+                if (a.vec_dx) {
+                    if (e0 < a.E) *reinterpret_cast<float4*>(dst) = make_float4(o[0], o[1], o[2], o[3]);
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        if (e0 + i < a.E) dst[i] = o[i];
+                }
+            }
         }
+        __syncwarp();
+        if (put && q == qq) buf[id] = 0.0f;
+        __syncwarp();
     }
 }
 
@@ -471,12 +720,13 @@ __global__ void __launch_bounds__(kRouteThreads) route_bwd_kernel(const __grid_c
 //   counts_kernel: every block counts the experts of its chunk of slots (n above one block's share);
 //   plan_kernel:   every block adds up the counts of the blocks before it and of all blocks (the
 //                  totals, whose scan are the offsets) and ranks the slots of its chunk.
-// Ranks come from per-warp counts in shared memory: a warp owns consecutive slots of the chunk, lanes
-// with the same expert find one another with match_any, so the order never depends on timing.
+// Ranks come from per-warp counts in shared memory: a warp owns consecutive slots of the chunk and lanes
+// with the same expert find one another by ballots, so the order never depends on timing.
 
 constexpr int kPlanThreads = 1024;
 constexpr int kPlanWarps = kPlanThreads / 32;
 constexpr int kPlanOneBlock = 4096;       // slots that one block sorts by itself
+constexpr int kPlanAhead = 4;             // loads of ids in flight per lane
 constexpr int kPlanMaxBlocks = 128;
 
 struct PlanArgs {
@@ -496,6 +746,7 @@ __device__ __forceinline__ int plan_bucket(const PlanArgs& a, int i) {
 __global__ void __launch_bounds__(kPlanThreads) counts_kernel(const __grid_constant__ PlanArgs a) {
     extern __shared__ int32_t plan_smem[];
     const int B = a.E + 1;
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     for (int e = threadIdx.x; e < B; e += kPlanThreads) plan_smem[e] = 0;
     __syncthreads();
     const int64_t lo = static_cast<int64_t>(blockIdx.x) * a.chunk;
@@ -506,6 +757,9 @@ __global__ void __launch_bounds__(kPlanThreads) counts_kernel(const __grid_const
 }
 
 // Shared memory: warp counts [kPlanWarps][B], base [B], total [B], scan [kPlanWarps].
+//
+// Lanes with the same bucket are found by a ballot per bit of the bucket (match_any takes its time per distinct
+// value: with 128 experts the one-block form spent 11.8 us on 4096 slots, most of it there).
 __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const __grid_constant__ PlanArgs a) {
     extern __shared__ int32_t plan_smem[];
     const int B = a.E + 1;
@@ -522,14 +776,39 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const __grid_constan
     const int per_warp = ((a.chunk + kPlanWarps - 1) / kPlanWarps + 31) / 32 * 32;
     const int64_t lo = blk_lo + static_cast<int64_t>(warp) * per_warp;
     const int64_t hi = lo + per_warp < blk_hi ? lo + per_warp : blk_hi;
-    for (int64_t i0 = lo; i0 < hi; i0 += 32) {
-        const bool ok = i0 + lane < hi;
-        const int b = ok ? plan_bucket(a, static_cast<int>(i0 + lane)) : -1;
-        const uint32_t same = __match_any_sync(kFullMask, b);
-        if (ok && lane == __ffs(same) - 1) wcount[warp * B + b] += __popc(same);
-        __syncwarp();
+    // Buckets of this warp's next kPlanAhead x 32 slots (-1 past its end).
+    auto load = [&](int64_t i0, int(&b)[kPlanAhead]) {
+#pragma unroll
+        for (int r = 0; r < kPlanAhead; ++r) {
+            const int64_t i = i0 + 32 * r + lane;
+            b[r] = i < hi ? plan_bucket(a, static_cast<int>(i)) : -1;
+        }
+    };
+    const int bits = 32 - __clz(a.E);
+    auto same_bucket = [&](int b) {
+        uint32_t same = __ballot_sync(kFullMask, b >= 0);
+        for (int i = 0; i < bits; ++i) {
+            const bool one = (b >> i) & 1;
+            const uint32_t ones = __ballot_sync(kFullMask, one);
+            same &= one ? ones : ~ones;
+        }
+        return same;
+    };
+    int b[kPlanAhead];
+    uint32_t same[kPlanAhead];
+    for (int64_t i0 = lo; i0 < hi; i0 += 32 * kPlanAhead) {
+        load(i0, b);
+#pragma unroll
+        for (int r = 0; r < kPlanAhead; ++r) same[r] = same_bucket(b[r]);
+#pragma unroll
+        for (int r = 0; r < kPlanAhead; ++r) {
+            if (b[r] >= 0 && lane == __ffs(same[r]) - 1) wcount[warp * B + b[r]] += __popc(same[r]);
+            __syncwarp();
+        }
     }
     if (a.block_counts) {
+        // Launched before the counting kernel has ended (programmatic launch); what stands above needs the ids only.
+        asm volatile("griddepcontrol.wait;" ::: "memory");
         // Earlier blocks' and all blocks' counts of every bucket; a bucket's blocks are split over threads.
         const int blocks = gridDim.x, parts = kPlanThreads / B > 1 ? kPlanThreads / B : 1;
         for (int e = tid; e < B * parts; e += kPlanThreads) {
@@ -549,6 +828,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const __grid_constan
         __syncthreads();
         for (int e = tid; e < B; e += kPlanThreads) {
             int sum = 0;
+#pragma unroll
             for (int w = 0; w < kPlanWarps; ++w) sum += wcount[w * B + e];
             total[e] = sum;
         }
@@ -588,24 +868,32 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const __grid_constan
     __syncthreads();
     // First row of every (warp, bucket).
     for (int e = tid; e < B; e += kPlanThreads) {
-        int row = base[e];
+        int row = base[e], c[kPlanWarps];
+#pragma unroll
+        for (int w = 0; w < kPlanWarps; ++w) c[w] = wcount[w * B + e];
+#pragma unroll
         for (int w = 0; w < kPlanWarps; ++w) {
-            const int c = wcount[w * B + e];
             wcount[w * B + e] = row;
-            row += c;
+            row += c[w];
         }
     }
     __syncthreads();
-    for (int64_t i0 = lo; i0 < hi; i0 += 32) {
-        const bool ok = i0 + lane < hi;
-        const int b = ok ? plan_bucket(a, static_cast<int>(i0 + lane)) : -1;
-        const uint32_t same = __match_any_sync(kFullMask, b);
-        int row = 0;
-        if (ok) row = wcount[warp * B + b] + __popc(same & ((1u << lane) - 1u));
-        __syncwarp();
-        if (ok && lane == __ffs(same) - 1) wcount[warp * B + b] += __popc(same);
-        __syncwarp();
-        if (ok) a.slot_row[i0 + lane] = b < a.E ? row : ~row;
+    const bool once = per_warp <= 32 * kPlanAhead;       // buckets and lane masks are still in registers
+    for (int64_t i0 = lo; i0 < hi; i0 += 32 * kPlanAhead) {
+        if (!once) {
+            load(i0, b);
+#pragma unroll
+            for (int r = 0; r < kPlanAhead; ++r) same[r] = same_bucket(b[r]);
+        }
+#pragma unroll
+        for (int r = 0; r < kPlanAhead; ++r) {
+            int row = 0;
+            if (b[r] >= 0) row = wcount[warp * B + b[r]] + __popc(same[r] & ((1u << lane) - 1u));
+            __syncwarp();
+            if (b[r] >= 0 && lane == __ffs(same[r]) - 1) wcount[warp * B + b[r]] += __popc(same[r]);
+            __syncwarp();
+            if (b[r] >= 0) a.slot_row[i0 + 32 * r + lane] = b[r] < a.E ? row : ~row;
+        }
     }
 }
 
