@@ -17,7 +17,7 @@ CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libmx.so")
 SOURCES = [os.path.join(CSRC, f) for f in ("libmx.cu",)]
 DEPS = SOURCES + [os.path.join(CSRC, f) for f in ("ptx.cuh", "quantize.cuh", "quantize_tma.cuh", "swizzle.cuh",
-                                                       "grid_equal.cuh", "gemm.cuh", "blockwise.cuh", "fastdiv.cuh", "fp4.cuh",
+                                                       "grid_equal.cuh", "gemm.cuh", "gemm_few.cuh", "blockwise.cuh", "fastdiv.cuh", "fp4.cuh",
                                                        "route.cuh", "experts.cuh")] + [
     os.path.join(ROOT, "include", "mx.h")
 ]

@@ -467,21 +467,39 @@ __device__ __forceinline__ int setup_groups(const GemmArgs& a, int32_t* off, int
     for (int g = threadIdx.x; g <= a.G; g += blockDim.x) off[g] = a.row_offsets[g];
     __syncthreads();
     __shared__ int total;
-    if (threadIdx.x == 0) {
+    if (threadIdx.x < 32) {
+        // One warp scans 32 groups at a time (a serial walk by one thread took 20 ns a group).
+        const int lane = threadIdx.x;
         bool ok = off[0] == 0 && off[a.G] == a.M;
         int acc128 = 0, acc256 = 0;
-        for (int g = 0; g < a.G; ++g) {
-            pm128[g] = acc128;
-            if (pm256) pm256[g] = acc256;
-            const int n = off[g + 1] - off[g];
+        for (int g0 = 0; g0 < a.G; g0 += 32) {
+            const int g = g0 + lane;
+            const int n = g < a.G ? off[g + 1] - off[g] : 0;
             if (n < 0) ok = false;
-            acc128 += n > 0 ? (n + 127) / 128 : 0;
-            acc256 += n > 0 ? (n + 255) / 256 : 0;
+            const int t128 = n > 0 ? (n + 127) / 128 : 0, t256 = n > 0 ? (n + 255) / 256 : 0;
+            int i128 = t128, i256 = t256;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int u128 = __shfl_up_sync(0xFFFFFFFFu, i128, o), u256 = __shfl_up_sync(0xFFFFFFFFu, i256, o);
+                if (lane >= o) {
+                    i128 += u128;
+                    i256 += u256;
+                }
+            }
+            if (g < a.G) {
+                pm128[g] = acc128 + i128 - t128;
+                if (pm256) pm256[g] = acc256 + i256 - t256;
+            }
+            acc128 += __shfl_sync(0xFFFFFFFFu, i128, 31);
+            acc256 += __shfl_sync(0xFFFFFFFFu, i256, 31);
         }
-        pm128[a.G] = acc128;
-        if (pm256) pm256[a.G] = acc256;
-        if (!ok) atomicOr(a.err, kErrBadOffsets);
-        total = ok ? (pm256 ? acc256 : acc128) * tiles_n : 0;
+        ok = __all_sync(0xFFFFFFFFu, ok);
+        if (lane == 0) {
+            pm128[a.G] = acc128;
+            if (pm256) pm256[a.G] = acc256;
+            if (!ok) atomicOr(a.err, kErrBadOffsets);
+            total = ok ? (pm256 ? acc256 : acc128) * tiles_n : 0;
+        }
     }
     __syncthreads();
     return total;

@@ -1,0 +1,239 @@
+// MXFP4 product for few rows of A (at most 64: the tokens of a decoding step), bound by one pass over the weight.
+//
+// C[m, n] = sum_k A[m, k] B[n, k] is computed as its transpose: 128 rows of the weight B are the tensor core's 128
+// rows and the tokens its columns (NPAD = 16, 32 or 64 of them), so no lane of the MMA works on padding and a CTA's
+// loads are almost all weight bytes. The CTA-pair kernel's 256 x 256 tiles would leave two thirds of the SMs without
+// work at N = 6144 and fill its A tiles with zeros.
+//
+// K is split over the CTAs of a cluster (1, 2, 4 or 8), as many as keep every SM busy: CTA r takes a contiguous share
+// of the 256-element stages, its fp32 accumulator goes to its shared memory, and after a cluster barrier each CTA sums
+// 128 / cluster columns of C over all of them in rank order through distributed shared memory, so neither a workspace
+// nor atomics are needed and the result does not depend on timing.
+//
+// Roles (192 threads): warp 0 TMA producer, warp 1 TMEM owner and MMA issuer, warps 2-5 epilogue. Four stages of at
+// most 26 KB, two CTAs per SM, so up to 130 KB of weight are in flight per SM. Waits are bounded as in the other
+// kernels; no load uses cluster multicast.
+//
+// Measured with weights that are not in L2 (a graph over 20 of them): 16 x 6144 x 4096 8.1 us (13.4 MB; the pair kernel
+// 10.4 us with the weight in L2), 64 rows 11.5 us (pair 11.9 us), 16 x 24576 x 4096 14.5 us, 16 x 151936 x 4096 61 us,
+// 5.4 TB/s. The smallest call takes 4.4 us: launch, tensor maps, one load, one MMA, the cluster's sum.
+#pragma once
+#include <cstdint>
+
+#include "gemm.cuh"
+
+namespace mx {
+
+constexpr int kFewMaxRows = 64;
+constexpr int kFewThreads = 192;
+constexpr int kFewStages = 4;
+constexpr int kFewSf = 1024;                    // two 512-byte scale blocks per operand and stage
+
+template <int NPAD>
+struct FewSmem {
+    static constexpr int kA = 0;                                        // weight tiles, 128 rows x 128 bytes
+    static constexpr int kB = kA + kFewStages * 128 * 128;              // token tiles, NPAD rows x 128 bytes
+    static constexpr int kSfa = kB + kFewStages * NPAD * 128;
+    static constexpr int kSfb = kSfa + kFewStages * kFewSf;
+    static constexpr int kBar = kSfb + kFewStages * kFewSf;
+    static constexpr int kMisc = kBar + (2 * kFewStages + 1) * 8;
+    static constexpr int kBytes = kMisc + 16 + 1024;                    // + alignment slack
+    static constexpr uint32_t kStageBytes = 128 * 128 + NPAD * 128 + 2 * kFewSf;
+    static_assert(NPAD * 128 * 4 <= kFewStages * 128 * 128, "the partial sums reuse the weight tiles");
+};
+
+struct FewArgs {
+    void* c;
+    int64_t ldc;
+    int M, N, K;
+    int nkb;                 // stages of 256 elements of K
+    int out_bf16;
+    uint32_t* err;
+    uint64_t timeout_ns;
+};
+
+__device__ __forceinline__ float4 ld_shared_cluster_f32x4(uint32_t cluster_addr) {
+    float4 v;
+    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                 : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+                 : "r"(cluster_addr)
+                 : "memory");
+    return v;
+}
+
+template <int NPAD>
+__global__ void __launch_bounds__(kFewThreads, 2)
+    mx_gemm_fp4_few_kernel(const __grid_constant__ CUtensorMap tmap_w, const __grid_constant__ CUtensorMap tmap_x,
+                           const __grid_constant__ CUtensorMap tmap_sfw, const __grid_constant__ CUtensorMap tmap_sfx,
+                           const FewArgs a) {
+    using L = FewSmem<NPAD>;
+    constexpr int S = kFewStages;
+    constexpr uint32_t kCols = 128;             // TMEM: NPAD accumulator columns, then two scale slots of 8
+    constexpr uint32_t kSf = 64;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    uint64_t* full = reinterpret_cast<uint64_t*>(smem + L::kBar);
+    uint64_t* empty = full + S;
+    uint64_t* done = empty + S;
+    uint32_t* tmem_base_slot = reinterpret_cast<uint32_t*>(smem + L::kMisc);
+    volatile int* abort = reinterpret_cast<volatile int*>(smem + L::kMisc + 4);
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int ranks = static_cast<int>(cluster_nctarank()), rank = static_cast<int>(cluster_ctarank());
+    const int tile = static_cast<int>(blockIdx.x) / ranks;
+    const int n0 = tile * 128;
+    const int kb_begin = a.nkb * rank / ranks, kb_end = a.nkb * (rank + 1) / ranks;
+
+    auto load = [&](int kb, int stage) {
+        mbar_arrive_expect_tx_elect(&full[stage], L::kStageBytes);
+        tma_load_2d_elect(smem + L::kA + stage * 128 * 128, &tmap_w, &full[stage], kb * kBK, n0);
+        tma_load_2d_elect(smem + L::kB + stage * NPAD * 128, &tmap_x, &full[stage], kb * kBK, 0);
+        tma_load_3d_elect(smem + L::kSfa + stage * kFewSf, &tmap_sfw, &full[stage], 0, 4 * kb, tile);
+        tma_load_3d_elect(smem + L::kSfb + stage * kFewSf, &tmap_sfx, &full[stage], 0, 4 * kb, 0);
+    };
+    const int ahead = min(S, kb_end - kb_begin);
+    if (warp == 0) {
+        if (lane == 0) {
+            for (int s = 0; s < S; ++s) {
+                mbar_init(&full[s], 1);
+                mbar_init(&empty[s], 1);
+            }
+            mbar_init(done, 1);
+            *abort = 0;
+            fence_barrier_init();
+        }
+        __syncwarp();
+        // The first stages' loads start before the rest of the CTA is set up.
+        for (int i = 0; i < ahead; ++i) load(kb_begin + i, i);
+    }
+    if (warp == 1) {
+        tmem_alloc(tmem_base_slot, kCols);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem_base = *tmem_base_slot;
+
+    if (warp == 0) {
+        int stage = ahead % S, issued = ahead;
+        uint32_t phase = ahead / S;
+        for (int kb = kb_begin + ahead; kb < kb_end; ++kb) {
+            if (!mbar_wait(&empty[stage], phase ^ 1u, abort, a.err, a.timeout_ns)) break;
+            __syncwarp();
+            load(kb, stage);
+            ++issued;
+            if (++stage == S) { stage = 0; phase ^= 1u; }
+        }
+        // No copy may be in flight when the CTA leaves, whatever the other roles did: wait for the last
+        // min(issued, S) fills.
+        int s = stage;
+        uint32_t p = phase;
+        for (int i = 0; i < min(issued, S); ++i) {
+            if (--s < 0) { s = S - 1; p ^= 1u; }
+            mbar_wait_drain(&full[s], p, a.timeout_ns);
+        }
+    } else if (warp == 1) {
+        int stage = 0;
+        uint32_t phase = 0;
+        for (int kb = kb_begin; kb < kb_end; ++kb) {
+            if (!mbar_wait(&full[stage], phase, abort, a.err, a.timeout_ns)) break;
+            __syncwarp();
+            tc_fence_after();
+            const uint64_t adesc = sdesc_kmajor_sw128(smem_u32(smem + L::kA + stage * 128 * 128));
+            const uint64_t bdesc = sdesc_kmajor_sw128(smem_u32(smem + L::kB + stage * NPAD * 128));
+            const uint64_t sda = sdesc_scale_block(smem_u32(smem + L::kSfa + stage * kFewSf));
+            const uint64_t sdb = sdesc_scale_block(smem_u32(smem + L::kSfb + stage * kFewSf));
+            const int left = a.K - kb * 256;
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const uint32_t sfa_t = tmem_base + kSf + 8u * h, sfb_t = sfa_t + 4u;
+                tc_cp_elect(sfa_t, sda + 32u * h);
+                tc_cp_elect(sfb_t, sdb + 32u * h);
+            }
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                // K-step k: +32 bytes (64 elements); scale slot k / 2, scale bytes 2 (k % 2), +1 of the word.
+                const uint32_t id = 2u * (k & 1), sfa_t = tmem_base + kSf + 8u * (k >> 1);
+                if (64 * k < left)
+                    tc_mma_mxf4_elect(tmem_base, adesc + 2u * k, bdesc + 2u * k, idesc_mxf4(128, NPAD, id),
+                                      sfa_t | (id << 30), (sfa_t + 4u) | (id << 30), (kb != kb_begin || k != 0) ? 1u : 0u);
+            }
+            tc_commit_elect(&empty[stage]);
+            if (++stage == S) { stage = 0; phase ^= 1u; }
+        }
+        // Every MMA issued by this warp has completed once `done` fires; the epilogue waits for it too.
+        __syncwarp();
+        tc_commit_elect(done);
+        mbar_wait_drain(done, 0, a.timeout_ns);
+    } else {
+        // The accumulator: lane l of quadrant q is weight row 32 q + l, column m token m.
+        const int q = warp & 3;
+        const int n = n0 + 32 * q + lane;
+        const bool ok = mbar_wait(done, 0, abort, a.err, a.timeout_ns) && !*abort;
+        tc_fence_after();
+        float* part = reinterpret_cast<float*>(smem + L::kA);            // [NPAD][128]
+        if (ok) {
+#pragma unroll
+            for (int m0 = 0; m0 < NPAD; m0 += 16) {
+                uint32_t r[16];
+                tc_ld_32x32b_x16(tmem_base + (static_cast<uint32_t>(32 * q) << 16) + m0, r);
+                tc_wait_ld_regs(r);
+#pragma unroll
+                for (int i = 0; i < 16; ++i) {
+                    const int m = m0 + i;
+                    if (ranks > 1) {
+                        part[m * 128 + 32 * q + lane] = __uint_as_float(r[i]);
+                    } else if (m < a.M && n < a.N) {
+                        if (a.out_bf16)
+                            static_cast<__nv_bfloat16*>(a.c)[m * a.ldc + n] = __float2bfloat16_rn(__uint_as_float(r[i]));
+                        else
+                            static_cast<float*>(a.c)[m * a.ldc + n] = __uint_as_float(r[i]);
+                    }
+                }
+            }
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (ranks > 1) {
+        cluster_sync();                         // every CTA's partial sums are in its shared memory
+        if (warp >= 2 && !*abort) {
+            // Four consecutive columns per thread; width / 4 (a power of two) threads per row.
+            const int width = 128 / ranks, per_row = width / 4, t = threadIdx.x - 64;
+            const uint32_t part = smem_u32(smem + L::kA);
+            const int nl = rank * width + 4 * (t & (per_row - 1));
+            const int n = n0 + nl;
+            for (int m = t / per_row; m < a.M; m += 128 / per_row) {
+                float4 v[8], sum = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+                for (int r = 0; r < 8; ++r)
+                    if (r < ranks) v[r] = ld_shared_cluster_f32x4(mapa_shared(part + (m * 128 + nl) * 4, r));
+#pragma unroll
+                for (int r = 0; r < 8; ++r)
+                    if (r < ranks) {
+                        sum.x += v[r].x;
+                        sum.y += v[r].y;
+                        sum.z += v[r].z;
+                        sum.w += v[r].w;
+                    }
+                const float out[4] = {sum.x, sum.y, sum.z, sum.w};
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    if (n + i < a.N) {
+                        if (a.out_bf16)
+                            static_cast<__nv_bfloat16*>(a.c)[m * a.ldc + n + i] = __float2bfloat16_rn(out[i]);
+                        else
+                            static_cast<float*>(a.c)[m * a.ldc + n + i] = out[i];
+                    }
+            }
+        }
+        cluster_sync();                         // no CTA leaves while another reads its shared memory
+    }
+    if (warp == 1) {
+        tc_fence_after();
+        tmem_dealloc(tmem_base, kCols);
+    }
+}
+
+}  // namespace mx

@@ -16,6 +16,7 @@
 #include "experts.cuh"
 #include "fp4.cuh"
 #include "gemm.cuh"
+#include "gemm_few.cuh"
 #include "grid_equal.cuh"
 #include "ptx.cuh"
 #include "quantize.cuh"
@@ -192,6 +193,13 @@ const DeviceInfo* device_info() {
             return nullptr;
         d.pair_clusters_fp4[0] = max_pair_clusters(mx_gemm_pair_kernel<false, 0, true>, kGemmPairSmemDenseFp4, d.sms);
         d.pair_clusters_fp4[1] = max_pair_clusters(mx_gemm_pair_kernel<true, 0, true>, kGemmPairSmemGroupedFp4, d.sms);
+        if (cudaFuncSetAttribute(mx_gemm_fp4_few_kernel<16>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 FewSmem<16>::kBytes) != cudaSuccess ||
+            cudaFuncSetAttribute(mx_gemm_fp4_few_kernel<32>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 FewSmem<32>::kBytes) != cudaSuccess ||
+            cudaFuncSetAttribute(mx_gemm_fp4_few_kernel<64>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 FewSmem<64>::kBytes) != cudaSuccess)
+            return nullptr;
         d.dispatch_blocks_per_sm[0] = occupancy(dispatch_kernel<false>, kExThreads);
         d.dispatch_blocks_per_sm[1] = occupancy(dispatch_kernel<true>, kExThreads);
         d.fp4_blocks_per_sm[1] = occupancy(quantize_fp4_kernel<true, false>, kQThreads);
@@ -969,6 +977,37 @@ mx_status launch_gemm_fp4(const uint8_t* qa, const uint8_t* sa, const uint8_t* q
                    : launch_pair<false, 0, true>(pairs, ta, tb, tsa, tsb, a, stream);
 }
 
+// The product for at most kFewMaxRows rows: tiles of 128 weight rows, K split over a cluster of CTAs as long as that
+// gives every CTA its own place (two per SM) and at least two stages.
+template <int NPAD>
+mx_status launch_few(const uint8_t* qa, const uint8_t* sa, const uint8_t* qb, const uint8_t* sb, const FewArgs& a,
+                     const DeviceInfo* d, mx_stream stream) {
+    const int64_t tiles = ceil_div(a.N, 128), ct = ceil_div(a.K, 128);
+    CUtensorMap tw, tx, tsw, tsx;
+    if (!make_tmap(&tw, qb, a.K / 2, a.N, kBK, 128) || !make_tmap(&tx, qa, a.K / 2, a.M, kBK, NPAD) ||
+        !make_tmap_sf_tiles(&tsw, sb, ct, tiles, 1) || !make_tmap_sf_tiles(&tsx, sa, ct, 1, 1))
+        return MX_ERR_CUDA;
+    int ranks = 1;
+    while (ranks < 8 && tiles * ranks * 2 <= 2 * int64_t(d->sms) && a.nkb >= 4 * ranks) ranks *= 2;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(tiles * ranks), 1, 1);
+    cfg.blockDim = dim3(kFewThreads, 1, 1);
+    cfg.dynamicSmemBytes = FewSmem<NPAD>::kBytes;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = ranks;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    if (cudaLaunchKernelEx(&cfg, mx_gemm_fp4_few_kernel<NPAD>, tw, tx, tsw, tsx, a) != cudaSuccess) {
+        cudaGetLastError();
+        return MX_ERR_CUDA;
+    }
+    return launched();
+}
+
 }  // namespace
 }  // namespace mx
 
@@ -1042,6 +1081,21 @@ mx_status mx_gemm_fp4(const uint8_t* qa, const uint8_t* sa_swz, const uint8_t* q
     if (empty) return MX_OK;
     const DeviceInfo* d = nullptr;
     if (mx_status st = check_device(&d)) return st;
+    if (M <= kFewMaxRows) {
+        FewArgs a;
+        a.c = c;
+        a.ldc = ld_c;
+        a.M = static_cast<int>(M);
+        a.N = static_cast<int>(N);
+        a.K = static_cast<int>(K);
+        a.nkb = static_cast<int>(ceil_div(K, 2 * kBK));
+        a.out_bf16 = out_dtype == MX_OUT_BF16;
+        a.err = d->status;
+        a.timeout_ns = g_timeout_ns.load();
+        if (M <= 16) return launch_few<16>(qa, sa_swz, qb, sb_swz, a, d, stream);
+        if (M <= 32) return launch_few<32>(qa, sa_swz, qb, sb_swz, a, d, stream);
+        return launch_few<64>(qa, sa_swz, qb, sb_swz, a, d, stream);
+    }
     return launch_gemm_fp4(qa, sa_swz, qb, sb_swz, nullptr, 1, M, N, K, c, ld_c, out_dtype, d, stream);
 }
 

@@ -347,6 +347,11 @@ def _packed(t, what: str, dtype, numel: int, dev) -> int:
     return t.data_ptr()
 
 
+def _layout_bytes(rows: int, kblocks: int) -> int:
+    """mx_swizzled_scale_bytes without the library call (for sizes known to be >= 0)."""
+    return (rows + 127) // 128 * 128 * ((kblocks + 3) // 4 * 4)
+
+
 def _ld(t) -> int:
     """Row stride in elements. A tensor of at most one row may carry any stride: its own width stands for it."""
     return t.stride(0) if t.shape[0] > 1 else max(t.stride(0), t.shape[1])
@@ -383,7 +388,7 @@ def quantize_fp4(x: torch.Tensor, rowwise: bool = True, colwise: bool = False, s
     flags = (MX_ROWWISE if rowwise else 0) | (MX_COLWISE if colwise else 0) | (MX_SWIZZLE if swizzle else 0)
 
     def scale_bytes(rows, n):
-        return swizzled_scale_bytes(rows, n // 32) if swizzle else rows * (n // 32)
+        return _layout_bytes(rows, n // 32) if swizzle else rows * (n // 32)
 
     if out is None:
         _need(K % 32 == 0 and (not colwise or M % 32 == 0), "quantize_fp4: blocks of 32 along the quantized axis")
@@ -413,7 +418,7 @@ def dequantize_fp4(q: torch.Tensor, s: torch.Tensor, swizzled: bool = True, out=
     _need(isinstance(q, torch.Tensor) and q.dim() == 2, "dequantize_fp4: q must be a 2-D uint8 CUDA tensor")
     M, K = q.shape[0], 2 * q.shape[1]
     pq = _packed(q, "dequantize_fp4: q must be a contiguous uint8 CUDA tensor", torch.uint8, M * K // 2, dev)
-    ps = _packed(s, "dequantize_fp4: s", torch.uint8, swizzled_scale_bytes(M, K // 32) if swizzled else M * (K // 32), dev)
+    ps = _packed(s, "dequantize_fp4: s", torch.uint8, _layout_bytes(M, K // 32) if swizzled else M * (K // 32), dev)
     if out is None:
         out = q.new_empty((M, K), dtype=torch.bfloat16)
     _call("mx_dequantize_fp4", dev, pq, ps, M, K, int(swizzled), _matrix(out, "dequantize_fp4: out", _BF16, (M, K), dev),
@@ -430,8 +435,8 @@ def gemm_fp4(qa, sa_swz, qb, sb_swz, out_dtype=torch.bfloat16, out=None):
     K *= 2
     pa = _packed(qa, "gemm_fp4: qa", torch.uint8, M * K // 2, dev)
     pb = _packed(qb, "gemm_fp4: qb", torch.uint8, N * K // 2, dev)
-    psa = _packed(sa_swz, "gemm_fp4: sa_swz", torch.uint8, swizzled_scale_bytes(M, K // 32), dev)
-    psb = _packed(sb_swz, "gemm_fp4: sb_swz", torch.uint8, swizzled_scale_bytes(N, K // 32), dev)
+    psa = _packed(sa_swz, "gemm_fp4: sa_swz", torch.uint8, _layout_bytes(M, K // 32), dev)
+    psb = _packed(sb_swz, "gemm_fp4: sb_swz", torch.uint8, _layout_bytes(N, K // 32), dev)
     if out is None:
         out = qa.new_empty((M, N), dtype=out_dtype)
     _call("mx_gemm_fp4", dev, pa, psa, pb, psb, M, N, K, _matrix(out, "gemm_fp4: out", _FLOATS, (M, N), dev), _ld(out),
@@ -449,8 +454,8 @@ def grouped_gemm_fp4(qa, sa_swz, qb, sb_swz, row_offsets, out_dtype=torch.bfloat
     G, N = qb.shape[0], qb.shape[1]
     pa = _packed(qa, "grouped_gemm_fp4: qa must be contiguous", torch.uint8, rows * K // 2, dev)
     pb = _packed(qb, "grouped_gemm_fp4: qb", torch.uint8, G * N * K // 2, dev)
-    psb = _packed(sb_swz, "grouped_gemm_fp4: sb_swz", torch.uint8, G * swizzled_scale_bytes(N, K // 32), dev)
-    _need(isinstance(sa_swz, torch.Tensor) and sa_swz.numel() >= swizzled_scale_bytes(rows, K // 32), "grouped_gemm_fp4: sa_swz")
+    psb = _packed(sb_swz, "grouped_gemm_fp4: sb_swz", torch.uint8, G * _layout_bytes(N, K // 32), dev)
+    _need(isinstance(sa_swz, torch.Tensor) and sa_swz.numel() >= _layout_bytes(rows, K // 32), "grouped_gemm_fp4: sa_swz")
     psa = _packed(sa_swz, "grouped_gemm_fp4: sa_swz", torch.uint8, sa_swz.numel(), dev)
     poff = _packed(row_offsets, "grouped_gemm_fp4: row_offsets must be int32 [G + 1]", torch.int32, G + 1, dev)
     if out is None:
@@ -524,8 +529,11 @@ def route_plan(ids: torch.Tensor, experts: int, out=None):
 
 
 def grouped_scale_bytes_bound(rows: int, groups: int, kblocks: int) -> int:
-    """mx_grouped_scale_bytes: bytes that hold the grouped scale layout of any split of `rows` into `groups`."""
-    return int(lib().mx_grouped_scale_bytes(rows, groups, kblocks))
+    """mx_grouped_scale_bytes: bytes that hold the grouped scale layout of any split of `rows` into `groups` (-1 for bad
+    sizes)."""
+    if rows < 0 or groups < 1 or kblocks < 0:
+        return -1
+    return (rows + 127 * min(groups, rows)) // 128 * 128 * ((kblocks + 3) // 4 * 4)
 
 
 def dispatch_quantize(x: torch.Tensor, slot_row: torch.Tensor, row_offsets: torch.Tensor, fmt: str = "mxfp8", out=None):
