@@ -353,8 +353,8 @@ def _layout_bytes(rows: int, kblocks: int) -> int:
 
 
 def _ld(t) -> int:
-    """Row stride in elements. A tensor of at most one row may carry any stride: its own width stands for it."""
-    return t.stride(0) if t.shape[0] > 1 else max(t.stride(0), t.shape[1])
+    """Row stride in elements. Of a single row no stride is ever used: its own width stands for it."""
+    return t.stride(0) if t.shape[0] > 1 else t.shape[1]
 
 
 # The current stream's handle without a Stream object around it: half a call's Python time where a call takes 10 us.

@@ -129,6 +129,31 @@ def test_gemm(M, N, K, out_dtype):
     assert_gemm_close(to_np(c.float()), a @ b.T, np.abs(a) @ np.abs(b).T, out_dtype == torch.bfloat16, f"{M}x{N}x{K}")
 
 
+# At most 64 rows: every token-tile width (16, 32, 64 and the first row count past them), K split over 1, 2, 4 and 8
+# CTAs with equal and unequal shares, N that ends inside a tile.
+@pytest.mark.parametrize("M", [1, 16, 17, 32, 33, 64, 65])
+@pytest.mark.parametrize("N,K", [(128, 256), (200, 1024), (130, 2080), (260, 4128), (33, 6400)])
+def test_gemm_few_rows(M, N, K):
+    for out_dtype in (torch.float32, torch.bfloat16):
+        test_gemm(M, N, K, out_dtype)
+
+
+def test_gemm_few_rows_strided_output_and_nan_row():
+    M, N, K = 40, 300, 4096
+    qa, sa, a = operand(M, K, 11)
+    qb, sb, b = operand(N, K, 12)
+    sa[7, 100], sb[250, 3] = 255, 255
+    buf = torch.full((M + 2, N + 5), 3.0, device="cuda")
+    mx.gemm_fp4(cuda(qa), cuda(oracle.swizzle(sa)), cuda(qb), cuda(oracle.swizzle(sb)), out=buf[1:M + 1, :N])
+    c = to_np(buf[1:M + 1, :N])
+    bad = np.zeros((M, N), bool)
+    bad[7], bad[:, 250] = True, True
+    assert np.array_equal(np.isnan(c), bad)
+    ok = ~bad
+    assert_gemm_close(c[ok], (a @ b.T)[ok], (np.abs(a) @ np.abs(b).T)[ok], False, "beside NaN")
+    assert torch.all(buf[:, N:] == 3.0) and torch.all(buf[0] == 3.0) and torch.all(buf[M + 1] == 3.0)
+
+
 def test_gemm_many_tiles_per_pair_and_strided_output():
     """More tiles than CTA pairs (both accumulators in turn), and an output with untouched padding columns."""
     M, N, K = 2600, 2100, 512
@@ -236,19 +261,21 @@ def test_large_forward_sampled():
     assert np.array_equal(to_np(sx)[pos[rows]], sb)
 
 
-def test_expired_waits_end_the_product_cleanly():
+@pytest.mark.parametrize("M,N,K", [(64, 40960, 32768), (4096, 4096, 16384)])
+def test_expired_waits_end_the_product_cleanly(M, N, K):
     """With a 1 ns deadline waits that do not succeed at once expire: the kernel records error bit 1, drains and
-    returns, and the next product is right."""
-    M, N, K = 4096, 4096, 16384
+    returns, and the next product is right. Both kernels. A wait's first try may itself block for a while (the
+    hardware's suspend window), so the sizes are such that a CTA's work outlasts it: the few-row kernel must not split
+    K over a cluster, which would leave each CTA a few microseconds."""
     g = torch.Generator(device="cuda").manual_seed(1)
     q = [torch.randint(0, 256, (n, K // 2), generator=g, dtype=torch.uint8, device="cuda") for n in (M, N)]
-    s = torch.full((mx.swizzled_scale_bytes(M, K // 32),), 127, dtype=torch.uint8, device="cuda")
+    s, t = (torch.full((mx.swizzled_scale_bytes(n, K // 32),), 127, dtype=torch.uint8, device="cuda") for n in (M, N))
     torch.cuda.synchronize()
     assert mx.device_error() == 0
     mx.set_wait_timeout_ns(1)
     try:
         for _ in range(8):
-            mx.gemm_fp4(q[0], s, q[1], s)
+            mx.gemm_fp4(q[0], s, q[1], t)
             torch.cuda.synchronize()
             bits = mx.device_error()
             if bits:
@@ -257,3 +284,4 @@ def test_expired_waits_end_the_product_cleanly():
         mx.set_wait_timeout_ns(0)
     assert bits == 1
     test_gemm(257, 130, 416, torch.float32)
+    test_gemm(16, 1000, 2048, torch.float32)

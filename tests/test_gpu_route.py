@@ -128,6 +128,19 @@ def test_extreme_logits(score, renormalize):
     check(torch.tensor(rows), 4, score, renormalize=renormalize)
 
 
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("group_score", ["max", "top2"])
+def test_extreme_logits_with_bias_and_groups(score, group_score):
+    """The same range of logits where scores and biases are added: saturated and vanishing scores, equal keys."""
+    rows = torch.tensor([[-200.0, -201.0, 300.0, 299.0, 0.0, -3.0e38, 1.0, 40.0], [50.0, 60.0, 70.0, 80.0, 90.0, 100.0, 45.0, 44.0],
+                         [-3.3e38] * 8, [float("inf"), 1.0, float("inf"), 0.0, float("-inf"), float("nan"), 2.0, 2.0],
+                         [float("-inf")] * 7 + [-1000.0], [-300.0, -310.0, -320.0, -330.0, -340.0, -350.0, -360.0, -370.0]])
+    for b in (torch.zeros(8), torch.full((8,), 0.25), torch.linspace(-1, 1, 8), torch.linspace(1e4, 2e4, 8)):
+        check(rows, 5, score, b, backward=False)
+        check(rows, 3, score, b, 4, 2, group_score, backward=False)
+        check(rows.to(torch.bfloat16), 4, score, b, 2, 1, group_score, backward=False)
+
+
 def test_bias_that_cannot_be_chosen():
     x = logits(20, 16, 1, torch.float32)
     b = torch.zeros(16)
@@ -201,6 +214,58 @@ def test_plan(T, k, E, dropped):
     off, slot_row, counts = mx.route_plan(torch.from_numpy(ids.astype(np.int32)).cuda(), E)
     o, s, c = plain.plan(ids, E)
     assert np.array_equal(to_np(off), o) and np.array_equal(to_np(counts), c) and np.array_equal(to_np(slot_row), s)
+
+
+def test_plan_in_a_graph_and_two_at_once():
+    """More slots than one block sorts (two kernels, the second launched early): captured and replayed on other ids,
+    and two calls on two streams at the same time, each with its own workspace."""
+    T, k, E = 3000, 8, 100
+    g = np.random.default_rng(8)
+    draw = lambda: torch.from_numpy(g.integers(-1, E, (T, k)).astype(np.int32))  # noqa: E731
+    ids = draw().cuda()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        mx.route_plan(ids, E)
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = mx.route_plan(ids, E)
+    for _ in range(3):
+        new = draw()
+        ids.copy_(new)
+        graph.replay()
+        for got, want in zip(out, plain.plan(new.numpy(), E)):
+            assert np.array_equal(to_np(got), want)
+    a, b = draw().cuda(), draw().cuda()
+    torch.cuda.synchronize()
+    other = torch.cuda.Stream()
+    res = []
+    for _ in range(5):
+        with torch.cuda.stream(side):
+            res.append((a, mx.route_plan(a, E)))
+        with torch.cuda.stream(other):
+            res.append((b, mx.route_plan(b, E)))
+    torch.cuda.synchronize()
+    for x, out in res:
+        for got, want in zip(out, plain.plan(to_np(x), E)):
+            assert np.array_equal(to_np(got), want)
+
+
+def test_many_tokens_per_warp_with_every_tail():
+    """Batches above the size where a warp takes several tokens, ending inside a warp's tokens."""
+    for T, E, k in ((4096, 40, 8), (4097, 128, 3), (4099, 64, 16), (5003, 17, 9), (4098, 128, 8)):
+        x = logits(T, E, T + k, torch.bfloat16, masked=True)
+        x[::7] = (x[::7] * 2).round() / 2                             # ties
+        x[5, :2] = torch.tensor([float("inf"), 3.38e38])
+        want = torch.sort(torch.nan_to_num(x.double(), nan=float("-inf"), posinf=3.4028234e38, neginf=float("-inf")), dim=1, descending=True, stable=True)
+        for renorm in (True, False):
+            ids, w = mx.route(x.cuda(), k, renormalize=renorm)
+            exp = torch.where(want.values[:, :k] > -np.inf, want.indices[:, :k], -1)
+            assert torch.equal(ids.cpu().long(), exp)
+            sub = slice(0, 200)
+            _, w64 = plain.route(x[sub].double().numpy(), k, renormalize=renorm)
+            assert np.all(np.abs(to_np(w)[sub] - w64) <= relative(E, x[sub].double().numpy()) * w64 + 2.0 ** -126)
 
 
 def test_plan_without_slots_and_without_experts():
