@@ -261,8 +261,11 @@ def swizzle_scales(s: torch.Tensor, group_rows=None, out=None):
     return out
 
 
+_OUT_CODES = {torch.float32: MX_OUT_F32, torch.bfloat16: MX_OUT_BF16}
+
+
 def _out_code(dtype) -> int:
-    return {torch.float32: MX_OUT_F32, torch.bfloat16: MX_OUT_BF16}[dtype]
+    return _OUT_CODES[dtype]
 
 
 def gemm(qa, sa_swz, qb, sb_swz, out_dtype=torch.bfloat16, out=None):
@@ -332,18 +335,29 @@ def _need(ok: bool, what: str):
         raise MxError(-1, what)
 
 
+# (Attribute checks in the order of their cost; anything that is no tensor fails them too. A host tensor is refused by
+# _call(), which every function ends in, or by the device check against the first operand.)
+
 def _matrix(t, what: str, dtypes, shape=None, dev=None) -> int:
     """Checks a 2-D CUDA tensor with unit column stride (and its shape and device); returns its address."""
-    _need(isinstance(t, torch.Tensor) and t.is_cuda and t.dim() == 2 and t.dtype in dtypes
-          and (t.stride(1) == 1 or t.shape[1] <= 1) and (dev is None or t.device == dev)
-          and (shape is None or tuple(t.shape) == tuple(shape)), what)
+    try:
+        ok = (t.dtype in dtypes and t.dim() == 2 and (t.stride(1) == 1 or t.shape[1] <= 1)
+              and (t.is_cuda if dev is None else t.device == dev) and (shape is None or t.shape == shape))
+    except AttributeError:
+        ok = False
+    if not ok:
+        raise MxError(-1, what)
     return t.data_ptr()
 
 
 def _packed(t, what: str, dtype, numel: int, dev) -> int:
-    """Checks a contiguous CUDA tensor of `numel` elements on `dev`; returns its address."""
-    _need(isinstance(t, torch.Tensor) and t.is_cuda and t.dtype == dtype and t.is_contiguous()
-          and t.numel() == numel and t.device == dev, what)
+    """Checks a contiguous tensor of `numel` elements on `dev`; returns its address."""
+    try:
+        ok = t.dtype is dtype and t.numel() == numel and t.is_contiguous() and t.device == dev
+    except AttributeError:
+        ok = False
+    if not ok:
+        raise MxError(-1, what)
     return t.data_ptr()
 
 
@@ -365,6 +379,8 @@ def _call(name: str, dev, *args):
     """One library call on `dev`'s current stream, with `dev` as the current device."""
     fn = getattr(_lib or lib(), name)
     i = dev.index
+    if dev.type != "cuda":
+        raise MxError(-1, f"{name}: CUDA tensors")
     if i == torch.cuda.current_device():
         st = fn(*args, _raw_stream(i))
     else:
