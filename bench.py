@@ -1043,7 +1043,8 @@ def run_breakeven(device, reps=20, passes=BREAKEVEN_PASSES):
 CASES = ("quant-gate-up", "quant-dy-rowcol", "quant-dy-col", "quant-sync-subset", "quant-fwd-1300", "gemm-fwd-10300",
          "gemm-update-fprop", "gemm-update-dgrad", "gemm-moe-gate-up", "gemm-moe-down", "grid-equal-gate-up",
          "swizzle-moe-gate-up", "swizzle-moe-down", "block128-pow2-gate-up", "block128-fp32-gate-up",
-         "sync-fused-subset")
+         "sync-fused-subset", "gemm-fp4-fwd-5200", "gemm-fp4-few-16", "quant-fp4-x-rowcol", "route-moe", "dispatch-moe",
+         "combine-moe", "combine-bwd-moe")
 SUBSET_LAYERS = 2      # quant-sync-subset: the first 2 layers' 8 weights (0.39 G elements, ~1.2 GB on the device)
 
 
@@ -1123,6 +1124,36 @@ def run_case(name: str, reps: int):
         _, _, qwc, swc = mx.quantize(W, False, True)
         C = torch.empty((dY.shape[0], W.shape[1]), dtype=torch.bfloat16, device=dev)
         fn = lambda: mx.gemm(qd, sd, qwc, swc, out=C)
+    elif name.startswith("gemm-fp4"):
+        # The gate_up projection of a 5200-token micro-batch, or the qkv projection of 16 decoding rows.
+        A = synth.fwd_activations(5200 if name == "gemm-fp4-fwd-5200" else 16, device=dev)
+        B = synth.sync_weight(0, 2 if name == "gemm-fp4-fwd-5200" else 0, device=dev)
+        qa, sa, _, _ = mx.quantize_fp4(A)
+        qb, sb, _, _ = mx.quantize_fp4(B)
+        C = torch.empty((A.shape[0], B.shape[0]), dtype=torch.bfloat16, device=dev)
+        fn = lambda: mx.gemm_fp4(qa, sa, qb, sb, out=C)
+    elif name == "quant-fp4-x-rowcol":
+        x, _, _ = synth.update_inputs(device=dev)
+        bufs = mx.quantize_fp4(x, True, True)
+        fn = lambda: mx.quantize_fp4(x, True, True, out=bufs)
+    elif name in ("route-moe", "dispatch-moe", "combine-moe", "combine-bwd-moe"):
+        # The routed layer of an MoE update micro-batch: 20 480 tokens, top-8 of 128 experts, 2048 features.
+        T, E, k, H = synth.MOE_TOKENS, synth.MOE_EXPERTS, synth.MOE_TOPK, synth.MOE_HIDDEN
+        logits = synth.normal_bf16((T, E), seed=1, device=dev)
+        ids, w = mx.route(logits, k)
+        off, slot_row, _ = mx.route_plan(ids, E)
+        x = synth.normal_bf16((T, H), seed=2, device=dev)
+        if name == "route-moe":
+            fn = lambda: mx.route(logits, k, out=(ids, w))
+        elif name == "dispatch-moe":
+            o = mx.dispatch_quantize(x, slot_row, off)
+            fn = lambda: mx.dispatch_quantize(x, slot_row, off, out=o)
+        else:
+            rows = synth.normal_bf16((T * k, H), seed=3, device=dev)
+            y = torch.empty_like(x)
+            o = (torch.empty_like(rows), torch.empty_like(w))
+            fn = ((lambda: mx.combine(rows, slot_row, w, out=y)) if name == "combine-moe"
+                  else (lambda: mx.combine_backward(x, rows, slot_row, w, out=o)))
     else:
         if name == "gemm-fwd-10300":
             A = synth.fwd_activations(10300, device=dev)

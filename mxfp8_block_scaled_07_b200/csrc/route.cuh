@@ -13,8 +13,9 @@
 //   w_j   = scale * s_j / (renormalize ? sum over the chosen of s : 1)
 //
 // The choice is exact: it is what the definition gives in fp64. fp32 scores decide a token when every
-// pair of keys whose order matters lies further apart than the fp32 error bound (kRouteTol below);
-// otherwise (well under a percent of tokens) the warp repeats the choice with fp64 keys.
+// pair of keys whose order matters lies further apart than the fp32 error bound; otherwise (well under a
+// percent of tokens, but one is enough to set a batch's time) the experts in doubt are ordered by fp64
+// keys, or, where more than one left out or a group is in doubt, all of the choice is repeated in fp64.
 #pragma once
 #include <cuda_bf16.h>
 
@@ -254,18 +255,16 @@ __device__ __forceinline__ void route_select(U (&key)[NV], int n, int lane, int&
         if (m == 0) break;
         const int owner = __ffs(__ballot_sync(kFullMask, b[0] == m)) - 1;
         const int e = __shfl_sync(kFullMask, lane * NV + bi[0], owner);
-        if (LEFT && j == n) {
-            left = e;
-            left_key = m;
-            break;
-        }
-        if (lane == j) {
-            id = e;
-            slot_key = m;
-        }
 #pragma unroll
         for (int i = 0; i < NV; ++i)
             if (lane * NV + i == e) key[i] = 0;
+        if (LEFT && j == n) {
+            left = e;
+            left_key = m;
+        } else if (lane == j) {
+            id = e;
+            slot_key = m;
+        }
     }
 }
 
@@ -367,6 +366,40 @@ __device__ __noinline__ int route_exact(const RouteArgs& a, const float (&v)[NV]
     int id = -1, left;
     route_select<NV, false>(key, a.k, lane, id, slot_key, left, left_key);
     return id;
+}
+
+// The order of the k chosen experts (lanes 0 .. k - 1: id, logit x, bias b) and the best one left out (lane k) by
+// fp64 keys: afterwards lane j < k holds the expert of slot j and its logit. All that is needed where no other
+// expert's key comes near the last chosen one's. Lanes without an expert have id -1.
+template <int NV>
+__device__ __noinline__ void route_reorder(const RouteArgs& a, const float (&v)[NV], float M, int lane, int& id, float& x,
+                                           float b) {
+    double z = 1.0;
+    if (!a.sigmoid) {
+        z = 0.0;
+#pragma unroll 1
+        for (int i = 0; i < NV; ++i)
+            if (v[i] > __int_as_float(0xFF800000)) z += exp(static_cast<double>(v[i]) - static_cast<double>(M));
+        z = warp_sum(z);
+    }
+    double key = __longlong_as_double(0xFFF0000000000000ll);
+    if (id >= 0) {
+        const double xd = static_cast<double>(x);
+        key = a.sigmoid ? 1.0 / (1.0 + exp(-xd)) : exp(xd - static_cast<double>(M)) / z;
+        if (a.bias) key += static_cast<double>(b);
+    }
+    int before = 0;
+    for (int i = 0; i <= a.k; ++i) {
+        const double o = __shfl_sync(kFullMask, key, i);
+        const int oi = __shfl_sync(kFullMask, id, i);
+        before += oi >= 0 && (o > key || (o == key && oi < id));
+    }
+    if (id < 0) before = 32 + lane;
+    int from = lane;
+    for (int i = 0; i <= a.k; ++i)
+        if (__shfl_sync(kFullMask, before, i) == lane) from = i;
+    id = __shfl_sync(kFullMask, id, from);
+    x = __shfl_sync(kFullMask, x, from);
 }
 
 template <int NV>
@@ -482,35 +515,42 @@ __global__ void __launch_bounds__(kRouteThreads) route_kernel(const __grid_const
                 s = v[i] > kNone ? s + b[i] : kNone;
                 key[i] = key_of(s);
             }
-            bool near = false;
+            bool near_group = false, near = false;
             if (a.G > 1) {
                 route_groups(a, key, lane, last, next);
-                if (next != 0) near = too_near(value_of(last), value_of(next), tol);
+                near_group = next != 0 && too_near(value_of(last), value_of(next), tol);
             }
             route_select<NV, true>(key, a.k, lane, id, slot_key, left, left_key);
-            // Slot j against slot j + 1, the last one against the best expert left out. Two experts with the same
-            // logit and the same bias have the same score in any precision.
-            const int slot = lane;
-            const bool mine = slot < a.k && slot_key != 0;
+            // Lane k takes the best expert left out. Slot j against slot j + 1, the last one against lane k. Two
+            // experts with the same logit and the same bias have the same score in any precision.
+            if (lane == a.k) {
+                id = left;
+                slot_key = left_key;
+            }
             float bj = 0.0f;
-            if (mine) {
+            if (id >= 0) {
                 x = route_logit(a, t, id);
                 if (a.bias) bj = a.bias[id];
             }
-            uint32_t k2 = __shfl_down_sync(kFullMask, slot_key, 1);
-            float x2 = __shfl_down_sync(kFullMask, x, 1), b2 = __shfl_down_sync(kFullMask, bj, 1);
-            if (slot == a.k - 1) {
-                k2 = left_key;
-                if (left >= 0) {
-                    x2 = route_logit(a, t, left);
-                    b2 = a.bias ? a.bias[left] : 0.0f;
+            const uint32_t k2 = __shfl_down_sync(kFullMask, slot_key, 1);
+            const float x2 = __shfl_down_sync(kFullMask, x, 1), b2 = __shfl_down_sync(kFullMask, bj, 1);
+            if (lane < a.k && slot_key != 0 && k2 != 0 && !(x == x2 && bj == b2))
+                near = too_near(value_of(slot_key), value_of(k2), tol);
+            if (__any_sync(kFullMask, near || near_group)) {
+                // Any other expert near the last chosen one (or a choice of groups in doubt): all of it in fp64.
+                uint32_t rest = 0;
+#pragma unroll
+                for (int i = 0; i < NV; ++i) rest = max(rest, key[i]);
+                rest = warp_max(left_key != 0 ? rest : 0u);
+                const uint32_t border = __shfl_sync(kFullMask, slot_key, a.k - 1);
+                if (near_group || (rest != 0 && left_key != 0 && too_near(value_of(border), value_of(rest), tol))) {
+                    id = route_exact<NV>(a, v, M, lane);
+                    x = id >= 0 ? route_logit(a, t, id) : kNone;
+                } else {
+                    route_reorder<NV>(a, v, M, lane, id, x, bj);
                 }
             }
-            if (mine && k2 != 0 && !(x == x2 && bj == b2)) near |= too_near(value_of(slot_key), value_of(k2), tol);
-            if (__any_sync(kFullMask, near)) {
-                id = route_exact<NV>(a, v, M, lane);
-                x = id >= 0 ? route_logit(a, t, id) : kNone;
-            }
+            if (lane >= a.k) x = kNone;
         }
     }
     const bool got = x > kNone;
