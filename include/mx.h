@@ -328,7 +328,7 @@ int64_t mx_grouped_scale_bytes(int64_t rows, int64_t groups, int64_t kblocks);
  * quantization of x[t, :] (BF16 [T, K], device, row stride ld_x), as mx_quantize (MX_FORMAT_E4M3, q [T * topk, K])
  * or mx_quantize_fp4 (MX_FORMAT_E2M1, q [T * topk, K / 2]) gives it, and s_swz its scales in the grouped tensor-core
  * layout of row_offsets: the A operand of mx_grouped_gemm / mx_grouped_gemm_fp4. Rows of slots without an expert
- * (slot_row < 0) get zero codes and scales. All mx_grouped_scale_bytes(T * topk, E, K / 32) bytes of s_swz are
+ * (slot_row < 0, ~slot_row the row) get zero codes and scales; no two slots may name the same row. All mx_grouped_scale_bytes(T * topk, E, K / 32) bytes of s_swz are
  * written, zeros where no row lies. slot_row and row_offsets: as mx_route_plan writes them. A row index or a place
  * in the layout that lies outside these buffers is skipped.
  * Requirements: those of mx_quantize for x and q, s_swz 16-byte aligned, E <= 1024. T == 0 or K == 0 is a no-op.
@@ -351,7 +351,7 @@ mx_status mx_combine(const void* c, mx_out_dtype c_dtype, int64_t rows, int64_t 
  * The gradients of mx_combine from dy [T, N]: d_c[slot_row[t, j], :] = weights[t, j] * dy[t, :] (in c's type; zeros in
  * the padding rows of slots without an expert) and d_weights[t, j] = sum_n dy[t, n] * c[slot_row[t, j], n] (fp32; 0 for
  * such slots), summed in a fixed order. Either output may be NULL (not both); c is read for d_weights only. Rows of d_c
- * that no slot names are not written.
+ * that no slot names are not written; no two slots may name the same row (as in mx_route_plan's partition).
  */
 mx_status mx_combine_bwd(const void* dy, mx_out_dtype y_dtype, int64_t ld_dy, const void* c, mx_out_dtype c_dtype,
                          int64_t rows, int64_t ld_c, const int32_t* slot_row, const float* weights, int64_t T, int64_t topk,

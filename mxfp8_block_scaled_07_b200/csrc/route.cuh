@@ -507,7 +507,16 @@ __global__ void __launch_bounds__(kRouteThreads) route_kernel(const __grid_const
             // 1.4e-6 + 6e-8 NV. Twice that for a pair of keys, and twice again for a sum of two; the rounding of a
             // key, 2^-24 of it, is in too_near().
             float tol = a.sigmoid ? 8e-7f : (2.8e-6f + 1.2e-7f * NV) / z;
-            if (a.G > 1 && a.top2) tol *= 2.0f;
+            if (a.G > 1 && a.top2) {
+                // A sum of two keys also has its keys' roundings, which it may cancel below: 2^-24 of each and of
+                // the sum, at most 4 * 2^-24 (1 + max |b|), twice that for a pair.
+                float bm = 0.0f;
+#pragma unroll
+                for (int i = 0; i < NV; ++i)
+                    if (v[i] > kNone && b[i] > kNone) bm = fmaxf(bm, fabsf(b[i]));
+                bm = __uint_as_float(warp_max(__float_as_uint(bm)));
+                tol = 2.0f * tol + 4.8e-7f * (1.0f + bm);
+            }
             const float inv_z = 1.0f / z;
 #pragma unroll
             for (int i = 0; i < NV; ++i) {

@@ -590,7 +590,8 @@ def combine(rows: torch.Tensor, slot_row: torch.Tensor, weights=None, out_dtype=
 
 def combine_backward(dy: torch.Tensor, rows: torch.Tensor, slot_row: torch.Tensor, weights=None, need_weights: bool = True, out=None):
     """mx_combine_bwd: (d_rows like rows, d_weights fp32 [T, topk]) from dy [T, N]. need_weights=False leaves
-    d_weights out (None), and rows is then only asked for its shape and type. Padding rows get zeros."""
+    d_weights out (None), and rows is then only asked for its shape and type. Padding rows get zeros. No two slots may
+    name the same row."""
     p = _matrix(rows, "combine_backward: rows must be a 2-D fp32 or BF16 CUDA tensor with unit column stride", _FLOATS)
     _need(slot_row.dim() == 2, "combine_backward: slot_row [T, topk]")
     (T, topk), (R, N), dev = slot_row.shape, rows.shape, rows.device

@@ -141,6 +141,19 @@ def test_extreme_logits_with_bias_and_groups(score, group_score):
         check(rows.to(torch.bfloat16), 4, score, b, 2, 1, group_score, backward=False)
 
 
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+def test_group_sums_that_cancel(score):
+    """Groups whose two largest keys nearly cancel: the sums differ by far less than a key's fp32 rounding."""
+    E, T, B = 32, 30, 3000.0
+    x = logits(T, E, 3, torch.float32, spread=0.5)
+    b = torch.full((E,), -9.0e4)
+    g = torch.Generator().manual_seed(1)
+    for i in range(8):
+        b[4 * i], b[4 * i + 2] = B * (i + 1), -B * (i + 1) + 1e-3 * torch.rand((), generator=g)
+    check(x, 6, score, b, 8, 3, "top2", backward=False)
+    check(x, 2, score, b / 1000, 8, 1, "top2", backward=False)
+
+
 def test_bias_that_cannot_be_chosen():
     x = logits(20, 16, 1, torch.float32)
     b = torch.zeros(16)
