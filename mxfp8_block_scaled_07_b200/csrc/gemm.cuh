@@ -459,46 +459,47 @@ __device__ __forceinline__ void epilogue_swiglu_tile(const GemmArgs& a, const Ti
     }
 }
 
-// Loads the group row offsets into shared memory, checks them and builds the prefix sums of
-// row tiles per group (tile_rows = 128: pm128; also 256: pm256 when given). Returns the tile count
-// (0 and an error bit when the offsets are invalid). Executed by the whole CTA.
-__device__ __forceinline__ int setup_groups(const GemmArgs& a, int32_t* off, int32_t* pm128, int32_t* pm256,
-                                            int tiles_n) {
-    for (int g = threadIdx.x; g <= a.G; g += blockDim.x) off[g] = a.row_offsets[g];
+// Loads the group row offsets into shared memory, checks them and builds the prefix sums of row tiles per
+// group: of 128 rows (pm128) and of TILE rows (pmt, when given). Returns the tile count, of TILE rows if pmt is
+// given, times tiles_n (0 and an error bit when the offsets are invalid). Executed by the whole CTA.
+template <int TILE>
+__device__ __forceinline__ int setup_groups(const int32_t* row_offsets, int G, int rows, uint32_t* err, int32_t* off,
+                                            int32_t* pm128, int32_t* pmt, int tiles_n) {
+    for (int g = threadIdx.x; g <= G; g += blockDim.x) off[g] = row_offsets[g];
     __syncthreads();
     __shared__ int total;
     if (threadIdx.x < 32) {
         // One warp scans 32 groups at a time (a serial walk by one thread took 20 ns a group).
         const int lane = threadIdx.x;
-        bool ok = off[0] == 0 && off[a.G] == a.M;
-        int acc128 = 0, acc256 = 0;
-        for (int g0 = 0; g0 < a.G; g0 += 32) {
+        bool ok = off[0] == 0 && off[G] == rows;
+        int acc128 = 0, acct = 0;
+        for (int g0 = 0; g0 < G; g0 += 32) {
             const int g = g0 + lane;
-            const int n = g < a.G ? off[g + 1] - off[g] : 0;
+            const int n = g < G ? off[g + 1] - off[g] : 0;
             if (n < 0) ok = false;
-            const int t128 = n > 0 ? (n + 127) / 128 : 0, t256 = n > 0 ? (n + 255) / 256 : 0;
-            int i128 = t128, i256 = t256;
+            const int t128 = n > 0 ? (n + 127) / 128 : 0, tt = n > 0 ? (n + TILE - 1) / TILE : 0;
+            int i128 = t128, it = tt;
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
-                const int u128 = __shfl_up_sync(0xFFFFFFFFu, i128, o), u256 = __shfl_up_sync(0xFFFFFFFFu, i256, o);
+                const int u128 = __shfl_up_sync(0xFFFFFFFFu, i128, o), ut = __shfl_up_sync(0xFFFFFFFFu, it, o);
                 if (lane >= o) {
                     i128 += u128;
-                    i256 += u256;
+                    it += ut;
                 }
             }
-            if (g < a.G) {
+            if (g < G) {
                 pm128[g] = acc128 + i128 - t128;
-                if (pm256) pm256[g] = acc256 + i256 - t256;
+                if (pmt) pmt[g] = acct + it - tt;
             }
             acc128 += __shfl_sync(0xFFFFFFFFu, i128, 31);
-            acc256 += __shfl_sync(0xFFFFFFFFu, i256, 31);
+            acct += __shfl_sync(0xFFFFFFFFu, it, 31);
         }
         ok = __all_sync(0xFFFFFFFFu, ok);
         if (lane == 0) {
-            pm128[a.G] = acc128;
-            if (pm256) pm256[a.G] = acc256;
-            if (!ok) atomicOr(a.err, kErrBadOffsets);
-            total = ok ? (pm256 ? acc256 : acc128) * tiles_n : 0;
+            pm128[G] = acc128;
+            if (pmt) pmt[G] = acct;
+            if (!ok) atomicOr(err, kErrBadOffsets);
+            total = ok ? (pmt ? acct : acc128) * tiles_n : 0;
         }
     }
     __syncthreads();
@@ -555,7 +556,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
     }
     int tiles;
     if constexpr (GROUPED)
-        tiles = setup_groups(a, off, pm, nullptr, a.tiles_n);
+        tiles = setup_groups<256>(a.row_offsets, a.G, a.M, a.err, off, pm, nullptr, a.tiles_n);
     else
         tiles = a.tiles_m * a.tiles_n;
     tc_fence_before();
@@ -749,7 +750,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
     }
     int tiles;
     if constexpr (GROUPED)
-        tiles = setup_groups(a, off, pm128, pm256, a.tiles_n);
+        tiles = setup_groups<256>(a.row_offsets, a.G, a.M, a.err, off, pm128, pm256, a.tiles_n);
     else
         tiles = a.tiles_m * a.tiles_n;
     tc_fence_before();

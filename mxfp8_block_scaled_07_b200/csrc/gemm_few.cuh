@@ -52,6 +52,13 @@ struct FewArgs {
     uint64_t timeout_ns;
 };
 
+// mbar_wait by a whole warp with one answer for all its lanes: a lane that sees another role's abort while its
+// neighbours see the phase complete must not leave them alone before a warp-wide instruction.
+__device__ __forceinline__ bool mbar_wait_warp(uint64_t* bar, uint32_t parity, volatile int* abort, uint32_t* err,
+                                               uint64_t timeout_ns) {
+    return __all_sync(0xFFFFFFFFu, mbar_wait(bar, parity, abort, err, timeout_ns));
+}
+
 __device__ __forceinline__ float4 ld_shared_cluster_f32x4(uint32_t cluster_addr) {
     float4 v;
     asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
@@ -119,7 +126,7 @@ __global__ void __launch_bounds__(kFewThreads, 2)
         int stage = ahead % S, issued = ahead;
         uint32_t phase = ahead / S;
         for (int kb = kb_begin + ahead; kb < kb_end; ++kb) {
-            if (!mbar_wait(&empty[stage], phase ^ 1u, abort, a.err, a.timeout_ns)) break;
+            if (!mbar_wait_warp(&empty[stage], phase ^ 1u, abort, a.err, a.timeout_ns)) break;
             __syncwarp();
             load(kb, stage);
             ++issued;
@@ -137,7 +144,7 @@ __global__ void __launch_bounds__(kFewThreads, 2)
         int stage = 0;
         uint32_t phase = 0;
         for (int kb = kb_begin; kb < kb_end; ++kb) {
-            if (!mbar_wait(&full[stage], phase, abort, a.err, a.timeout_ns)) break;
+            if (!mbar_wait_warp(&full[stage], phase, abort, a.err, a.timeout_ns)) break;
             __syncwarp();
             tc_fence_after();
             const uint64_t adesc = sdesc_kmajor_sw128(smem_u32(smem + L::kA + stage * 128 * 128));
@@ -170,7 +177,7 @@ __global__ void __launch_bounds__(kFewThreads, 2)
         // The accumulator: lane l of quadrant q is weight row 32 q + l, column m token m.
         const int q = warp & 3;
         const int n = n0 + 32 * q + lane;
-        const bool ok = mbar_wait(done, 0, abort, a.err, a.timeout_ns) && !*abort;
+        const bool ok = mbar_wait_warp(done, 0, abort, a.err, a.timeout_ns);
         tc_fence_after();
         float* part = reinterpret_cast<float*>(smem + L::kA);            // [NPAD][128]
         if (ok) {
@@ -198,7 +205,7 @@ __global__ void __launch_bounds__(kFewThreads, 2)
     __syncthreads();
     if (ranks > 1) {
         cluster_sync();                         // every CTA's partial sums are in its shared memory
-        if (warp >= 2 && !*abort) {
+        if (warp >= 2 && __all_sync(0xFFFFFFFFu, !*abort)) {
             // Four consecutive columns per thread; width / 4 (a power of two) threads per row.
             const int width = 128 / ranks, per_row = width / 4, t = threadIdx.x - 64;
             const uint32_t part = smem_u32(smem + L::kA);
@@ -230,6 +237,234 @@ __global__ void __launch_bounds__(kFewThreads, 2)
         }
         cluster_sync();                         // no CTA leaves while another reads its shared memory
     }
+    if (warp == 1) {
+        tc_fence_after();
+        tmem_dealloc(tmem_base, kCols);
+    }
+}
+
+// ---- grouped: a decoding step of an MoE layer ------------------------------------------------------------
+//
+// The same transposed tiles for experts of a few rows each, where the CTA-pair kernel's 256 x 256 tiles compute mostly
+// padding: 127 experts of 4 rows (1536 x 2048) took it 47 us, of which the tensor core's work on whole tiles alone is
+// 22 us, while the weights' bytes need 32. Persistent: two CTAs per SM walk the tiles (expert, 128 of its rows, 128
+// weight rows) and the loads of the next tiles run ahead through the ring while a tile is finished. A tile of at
+// most 32 rows loads 32 of the activation and takes them as its MMAs' columns, a larger one 128 and as many columns
+// as it needs (a multiple of 32). Tiles start at multiples of 128 rows of their expert, so that their scales are
+// whole blocks of the layout and start at the first column of their TMEM slot, as an MMA's scales have to.
+constexpr int kGfRows = 128;
+constexpr int kGfSmall = 32;
+constexpr int kGfStages = 3;
+// Taken for at most 32 rows per expert on average (all the host knows). 128 experts of 1536 x 2048, weights not in L2,
+// this kernel against the pair kernel: 8 rows in all 8.6 / 10.1 us, 128 rows (80 experts) 28.2 / 31.7, 512 rows 37.0 /
+// 46.9 (the weights' bytes need 31.5), 2048 rows 41.8 / 48.5, 4096 rows 44.0 / 49.3, 8192 rows 49.9 / 51.2.
+constexpr int64_t kGfMaxMeanRows = 32;
+
+struct GfSmem {
+    static constexpr int kA = 0;                                        // weight tiles
+    static constexpr int kB = kA + kGfStages * 128 * 128;               // token tiles
+    static constexpr int kSfa = kB + kGfStages * kGfRows * 128;
+    static constexpr int kSfb = kSfa + kGfStages * kFewSf;
+    static constexpr int kBar = kSfb + kGfStages * kFewSf;
+    static constexpr int kMisc = kBar + (2 * kGfStages + 3) * 8;
+    static constexpr int kGroups = (kMisc + 16 + 15) / 16 * 16;         // off, first 128-row tile
+    static constexpr int kBytes = kGroups + 2 * (kMaxGroups + 1) * 4 + 1024;
+};
+static_assert(2 * (GfSmem::kBytes + 1024) <= 233472, "two CTAs per SM");
+
+struct GfArgs {
+    const int32_t* row_offsets;
+    void* c;
+    int64_t ldc;
+    int M, N, K, G;
+    int nkb, tiles_n;        // stages of 256 elements of K; 128-row tiles of a weight
+    int out_bf16;
+    uint32_t* err;
+    uint64_t timeout_ns;
+};
+
+struct GfTile {
+    int row0, rows;          // first row of A / C, rows of the tile
+    int w_row0, w_tile;      // first weight row and scale tile (over all experts)
+    int n0;                  // first column of C
+    int sf_tile;             // A's scale tile
+};
+
+__device__ __forceinline__ GfTile gf_tile(const GfArgs& a, int t, const int32_t* off, const int32_t* pm128) {
+    GfTile T;
+    const int nt = t % a.tiles_n;
+    T.sf_tile = t / a.tiles_n;
+    const int g = find_group(pm128, a.G, T.sf_tile);
+    T.row0 = off[g] + (T.sf_tile - pm128[g]) * kGfRows;
+    T.rows = min(kGfRows, off[g + 1] - T.row0);
+    T.n0 = nt * 128;
+    T.w_row0 = g * a.N + T.n0;
+    T.w_tile = g * a.tiles_n + nt;
+    return T;
+}
+
+__global__ void __launch_bounds__(kFewThreads, 2)
+    mx_grouped_gemm_fp4_few_kernel(const __grid_constant__ CUtensorMap tmap_w, const __grid_constant__ CUtensorMap tmap_x,
+                                   const __grid_constant__ CUtensorMap tmap_x_small,
+                                   const __grid_constant__ CUtensorMap tmap_sfw,
+                                   const __grid_constant__ CUtensorMap tmap_sfx, const GfArgs a) {
+    using L = GfSmem;
+    constexpr int S = kGfStages;
+    constexpr uint32_t kCols = 256, kSf = 128;  // TMEM: an accumulator of 128 columns, two scale slots of 8
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    uint64_t* full = reinterpret_cast<uint64_t*>(smem + L::kBar);
+    uint64_t* empty = full + S;
+    uint64_t* tmem_full = empty + S;
+    uint64_t* acc_empty = tmem_full + 1;
+    uint64_t* drain = acc_empty + 1;
+    uint32_t* tmem_base_slot = reinterpret_cast<uint32_t*>(smem + L::kMisc);
+    volatile int* abort = reinterpret_cast<volatile int*>(smem + L::kMisc + 4);
+    int32_t* off = reinterpret_cast<int32_t*>(smem + L::kGroups);
+    int32_t* pm128 = off + (kMaxGroups + 1);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < S; ++s) {
+            mbar_init(&full[s], 1);
+            mbar_init(&empty[s], 1);
+        }
+        mbar_init(tmem_full, 1);
+        mbar_init(acc_empty, 4);
+        mbar_init(drain, 1);
+        *abort = 0;
+        fence_barrier_init();
+    }
+    if (warp == 0 && lane == 0) {
+        prefetch_tensormap(&tmap_w);
+        prefetch_tensormap(&tmap_x);
+        prefetch_tensormap(&tmap_x_small);
+        prefetch_tensormap(&tmap_sfw);
+        prefetch_tensormap(&tmap_sfx);
+    }
+    if (warp == 1) {
+        tmem_alloc(tmem_base_slot, kCols);
+        tmem_relinquish();
+    }
+    const int tiles = setup_groups<kGfRows>(a.row_offsets, a.G, a.M, a.err, off, pm128, nullptr, a.tiles_n);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem_base = *tmem_base_slot;
+
+    if (warp == 0) {
+        int stage = 0, issued = 0;
+        uint32_t phase = 0;
+        bool ok = true;
+        for (int t = blockIdx.x; t < tiles && ok; t += gridDim.x) {
+            const GfTile T = gf_tile(a, t, off, pm128);
+            const bool small = T.rows <= kGfSmall;
+            for (int kb = 0; kb < a.nkb; ++kb) {
+                if (!mbar_wait_warp(&empty[stage], phase ^ 1u, abort, a.err, a.timeout_ns)) { ok = false; break; }
+                __syncwarp();
+                mbar_arrive_expect_tx_elect(&full[stage],
+                                            128 * 128 + (small ? kGfSmall : kGfRows) * 128 + 2 * kFewSf);
+                tma_load_2d_elect(smem + L::kA + stage * 128 * 128, &tmap_w, &full[stage], kb * kBK, T.w_row0);
+                if (small)
+                    tma_load_2d_elect(smem + L::kB + stage * kGfRows * 128, &tmap_x_small, &full[stage], kb * kBK, T.row0);
+                else
+                    tma_load_2d_elect(smem + L::kB + stage * kGfRows * 128, &tmap_x, &full[stage], kb * kBK, T.row0);
+                tma_load_3d_elect(smem + L::kSfa + stage * kFewSf, &tmap_sfw, &full[stage], 0, 4 * kb, T.w_tile);
+                tma_load_3d_elect(smem + L::kSfb + stage * kFewSf, &tmap_sfx, &full[stage], 0, 4 * kb, T.sf_tile);
+                if (issued < S) ++issued;
+                if (++stage == S) { stage = 0; phase ^= 1u; }
+            }
+        }
+        // No copy may be in flight when the CTA leaves, whatever the other roles did.
+        int s = stage;
+        uint32_t p = phase;
+        for (int i = 0; i < issued; ++i) {
+            if (--s < 0) { s = S - 1; p ^= 1u; }
+            mbar_wait_drain(&full[s], p, a.timeout_ns);
+        }
+    } else if (warp == 1) {
+        int stage = 0, j = 0;
+        uint32_t phase = 0, empty_phase = 0;
+        bool ok = true;
+        for (int t = blockIdx.x; t < tiles && ok; t += gridDim.x, ++j) {
+            const GfTile T = gf_tile(a, t, off, pm128);
+            if (j > 0) {                        // the previous tile has been read out of the accumulator
+                if (!mbar_wait_warp(acc_empty, empty_phase, abort, a.err, a.timeout_ns)) break;
+                empty_phase ^= 1u;
+            }
+            tc_fence_after();
+            const uint32_t cols = static_cast<uint32_t>((T.rows + 31) / 32 * 32);
+            const uint32_t idesc[2] = {idesc_mxf4(128, cols, 0), idesc_mxf4(128, cols, 2)};
+            for (int kb = 0; kb < a.nkb; ++kb) {
+                if (!mbar_wait_warp(&full[stage], phase, abort, a.err, a.timeout_ns)) { ok = false; break; }
+                __syncwarp();
+                tc_fence_after();
+                const uint64_t adesc = sdesc_kmajor_sw128(smem_u32(smem + L::kA + stage * 128 * 128));
+                const uint64_t bdesc = sdesc_kmajor_sw128(smem_u32(smem + L::kB + stage * kGfRows * 128));
+                const uint64_t sda = sdesc_scale_block(smem_u32(smem + L::kSfa + stage * kFewSf));
+                const uint64_t sdb = sdesc_scale_block(smem_u32(smem + L::kSfb + stage * kFewSf));
+                const int left = a.K - kb * 256;
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    tc_cp_elect(tmem_base + kSf + 8u * h, sda + 32u * h);
+                    tc_cp_elect(tmem_base + kSf + 8u * h + 4u, sdb + 32u * h);
+                }
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const uint32_t id = 2u * (k & 1), sfa_t = tmem_base + kSf + 8u * (k >> 1);
+                    if (64 * k < left)
+                        tc_mma_mxf4_elect(tmem_base, adesc + 2u * k, bdesc + 2u * k, idesc[k & 1], sfa_t | (id << 30),
+                                          (sfa_t + 4u) | (id << 30), (kb | k) != 0 ? 1u : 0u);
+                }
+                tc_commit_elect(&empty[stage]);
+                if (++stage == S) { stage = 0; phase ^= 1u; }
+            }
+            if (!ok) break;
+            tc_commit_elect(tmem_full);
+        }
+        // Every MMA issued by this warp has completed once `drain` fires.
+        __syncwarp();
+        tc_commit_elect(drain);
+        mbar_wait_drain(drain, 0, a.timeout_ns);
+    } else {
+        // Lane l of quadrant q is weight row 32 q + l, accumulator column m row m of the tile.
+        const int q = warp & 3;
+        uint32_t full_phase = 0;
+        for (int t = blockIdx.x; t < tiles; t += gridDim.x) {
+            const GfTile T = gf_tile(a, t, off, pm128);
+            if (!mbar_wait_warp(tmem_full, full_phase, abort, a.err, a.timeout_ns)) break;
+            full_phase ^= 1u;
+            tc_fence_after();
+            const int n = T.n0 + 32 * q + lane;
+            for (int m0 = 0; m0 < T.rows; m0 += 32) {
+                uint32_t r[32];
+                tc_ld_32x32b_x32(tmem_base + (static_cast<uint32_t>(32 * q) << 16) + m0, r);
+                tc_wait_ld_regs(r);
+                if (m0 + 32 >= T.rows) {        // the last of the tile is in registers
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(acc_empty);
+                }
+                const int64_t at = static_cast<int64_t>(T.row0 + m0) * a.ldc + n;
+                if (n < a.N) {
+                    if (a.out_bf16) {
+                        __nv_bfloat16* c = static_cast<__nv_bfloat16*>(a.c) + at;
+#pragma unroll
+                        for (int m = 0; m < 32; ++m)
+                            if (m0 + m < T.rows) c[m * a.ldc] = __float2bfloat16_rn(__uint_as_float(r[m]));
+                    } else {
+                        float* c = static_cast<float*>(a.c) + at;
+#pragma unroll
+                        for (int m = 0; m < 32; ++m)
+                            if (m0 + m < T.rows) c[m * a.ldc] = __uint_as_float(r[m]);
+                    }
+                }
+                __syncwarp();
+            }
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
     if (warp == 1) {
         tc_fence_after();
         tmem_dealloc(tmem_base, kCols);

@@ -198,7 +198,9 @@ const DeviceInfo* device_info() {
             cudaFuncSetAttribute(mx_gemm_fp4_few_kernel<32>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                  FewSmem<32>::kBytes) != cudaSuccess ||
             cudaFuncSetAttribute(mx_gemm_fp4_few_kernel<64>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                 FewSmem<64>::kBytes) != cudaSuccess)
+                                 FewSmem<64>::kBytes) != cudaSuccess ||
+            cudaFuncSetAttribute(mx_grouped_gemm_fp4_few_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 GfSmem::kBytes) != cudaSuccess)
             return nullptr;
         d.dispatch_blocks_per_sm[0] = occupancy(dispatch_kernel<false>, kExThreads);
         d.dispatch_blocks_per_sm[1] = occupancy(dispatch_kernel<true>, kExThreads);
@@ -1111,6 +1113,35 @@ mx_status mx_grouped_gemm_fp4(const uint8_t* qa, const uint8_t* sa_swz, const ui
     if (empty) return MX_OK;
     const DeviceInfo* d = nullptr;
     if (mx_status st = check_device(&d)) return st;
+    if (total_rows <= kGfMaxMeanRows * G) {
+        GfArgs a;
+        a.row_offsets = row_offsets_dev;
+        a.c = c;
+        a.ldc = ld_c;
+        a.M = static_cast<int>(total_rows);
+        a.N = static_cast<int>(N);
+        a.K = static_cast<int>(K);
+        a.G = static_cast<int>(G);
+        a.nkb = static_cast<int>(ceil_div(K, 2 * kBK));
+        a.tiles_n = static_cast<int>(ceil_div(N, 128));
+        a.out_bf16 = out_dtype == MX_OUT_BF16;
+        a.err = d->status;
+        a.timeout_ns = g_timeout_ns.load();
+        const int64_t ct = ceil_div(K, 128);
+        // Upper bound: every group with rows adds at most one partial tile of 128 rows.
+        const int64_t tiles = (ceil_div(total_rows, kGfRows) + std::min(G, total_rows)) * a.tiles_n;
+        if (tiles < kInt32End) {
+            CUtensorMap tw, tx, txs, tsw, tsx;
+            if (!make_tmap(&tw, qb, K / 2, G * N, kBK, 128) || !make_tmap(&tx, qa, K / 2, total_rows, kBK, kGfRows) ||
+                !make_tmap(&txs, qa, K / 2, total_rows, kBK, kGfSmall) ||
+                !make_tmap_sf_tiles(&tsw, sb_swz, ct, G * a.tiles_n, 1) ||
+                !make_tmap_sf_tiles(&tsx, sa_swz, ct, ceil_div(total_rows, 128) + G, 1))
+                return MX_ERR_CUDA;
+            const unsigned grid = static_cast<unsigned>(std::min<int64_t>(tiles, 2 * int64_t(d->sms)));
+            mx_grouped_gemm_fp4_few_kernel<<<grid, kFewThreads, GfSmem::kBytes, stream>>>(tw, tx, txs, tsw, tsx, a);
+            return launched();
+        }
+    }
     return launch_gemm_fp4(qa, sa_swz, qb, sb_swz, row_offsets_dev, G, total_rows, N, K, c, ld_c, out_dtype, d, stream);
 }
 

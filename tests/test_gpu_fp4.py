@@ -206,16 +206,59 @@ def test_grouped_few_rows(counts):
     grouped(counts, 256, 128, torch.float32, 9)
 
 
-def test_grouped_bad_offsets_write_nothing():
-    qa, sa, _ = operand(128, 128, 1)
+# At most 32 rows per expert on average, with experts of 0, 1, 31, 32, 33, 127, 128, 129 and 300 rows among them.
+@pytest.mark.parametrize("out_dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("counts", [[32, 0, 33, 1, 31, 0, 64, 0], [300] + [0] * 9, [0] * 6 + [127, 1], [128, 129] + [0] * 7, [5] * 40,
+                                    [0] * 70 + [40] + [0] * 57 + [3], [32] * 3])
+@pytest.mark.parametrize("N,K", [(128, 256), (130, 96), (384, 1056), (1, 32)])
+def test_grouped_few_rows_per_expert(N, K, counts, out_dtype):
+    grouped(counts, N, K, out_dtype, len(counts) + N)
+
+
+def test_grouped_few_rows_many_tiles_and_strided_output():
+    """More tiles than CTAs (the ring and the accumulator go round), and untouched columns beside the output."""
+    g = np.random.default_rng(3)
+    counts = g.integers(0, 40, 60)
+    buf = torch.full((int(counts.sum()), 1400 + 3), 3.0, device="cuda")
+    grouped(counts, 1400, 512, torch.float32, 5, out=buf[:, :1400])
+    assert torch.all(buf[:, 1400:] == 3.0)
+
+
+@pytest.mark.parametrize("rows", [128, 20])       # the pair kernel's grouped form and the one for few rows per expert
+def test_grouped_bad_offsets_write_nothing(rows):
+    h = rows // 2
+    qa, sa, _ = operand(rows, 128, 1)
     qb, sb, _ = operand(512, 128, 2)
-    out = torch.full((128, 256), 3.0, device="cuda")
+    out = torch.full((rows, 256), 3.0, device="cuda")
     mx.device_error()
-    for bad in ([0, 100, 64], [0, 64, 127], [1, 64, 128]):
-        mx.grouped_gemm_fp4(cuda(qa), cuda(oracle.swizzle(sa, [64, 64])), cuda(qb.reshape(2, 256, 64)), cuda(oracle.swizzle(sb)),
+    for bad in ([0, rows - 3, h], [0, h, rows - 1], [1, h, rows]):
+        mx.grouped_gemm_fp4(cuda(qa), cuda(oracle.swizzle(sa, [h, h])), cuda(qb.reshape(2, 256, 64)), cuda(oracle.swizzle(sb)),
                             torch.tensor(bad, dtype=torch.int32, device="cuda"), out=out)
         assert mx.device_error() == 2
     assert torch.all(out == 3.0)
+
+
+def test_expired_waits_end_the_grouped_product_for_few_rows_cleanly():
+    G, N, K, rows = 8, 8192, 32768, 200
+    g = torch.Generator(device="cuda").manual_seed(1)
+    qa, qb = (torch.randint(0, 256, s, generator=g, dtype=torch.uint8, device="cuda") for s in ((rows, K // 2), (G, N, K // 2)))
+    sa = torch.full((mx.grouped_scale_bytes_bound(rows, G, K // 32),), 127, dtype=torch.uint8, device="cuda")
+    sb = torch.full((G * mx.swizzled_scale_bytes(N, K // 32),), 127, dtype=torch.uint8, device="cuda")
+    off = torch.arange(0, rows + 1, rows // G, dtype=torch.int32, device="cuda")
+    torch.cuda.synchronize()
+    assert mx.device_error() == 0
+    mx.set_wait_timeout_ns(1)
+    try:
+        for _ in range(8):
+            mx.grouped_gemm_fp4(qa, sa, qb, sb, off)
+            torch.cuda.synchronize()
+            bits = mx.device_error()
+            if bits:
+                break
+    finally:
+        mx.set_wait_timeout_ns(0)
+    assert bits == 1
+    grouped([5] * 40, 130, 96, torch.float32, 3)
 
 
 def test_quantized_linear_all_three_products():
