@@ -1212,8 +1212,12 @@ int cached_occupancy(std::atomic<int>* cache, K kernel) {
     return n;
 }
 
-int plan_blocks(int64_t n) {
-    return n <= kPlanOneBlock ? 1 : static_cast<int>(std::min<int64_t>(kPlanMaxBlocks, ceil_div(n, kPlanThreads)));
+// Blocks that sort n slots, and whether they are one cluster (no counting kernel, no workspace).
+int plan_blocks(int64_t n, bool* cluster) {
+    int blocks = 1;
+    while (blocks < kPlanCluster && int64_t(blocks) * kPlanOneBlock < n) blocks *= 2;
+    *cluster = int64_t(blocks) * kPlanOneBlock >= n;
+    return *cluster ? blocks : static_cast<int>(std::min<int64_t>(kPlanMaxBlocks, ceil_div(n, kPlanThreads)));
 }
 
 template <class CT, class YT>
@@ -1339,16 +1343,18 @@ mx_status mx_route_bwd(const float* d_weights, const void* logits, mx_out_dtype 
 
 int64_t mx_route_plan_workspace_bytes(int64_t slots, int64_t E) {
     if (slots < 0 || slots >= kInt32End || E < 1 || E > kRouteMaxExperts) return -1;
-    const int blocks = plan_blocks(slots);
-    return blocks == 1 ? 0 : int64_t(blocks) * (E + 1) * 4;
+    bool cluster = false;
+    const int blocks = plan_blocks(slots, &cluster);
+    return cluster ? 0 : int64_t(blocks) * (E + 1) * 4;
 }
 
 mx_status mx_route_plan(const int32_t* ids, int64_t slots, int64_t E, int32_t* row_offsets, int32_t* slot_row,
                         int32_t* counts, void* workspace, mx_stream stream) {
     if (slots < 0 || E < 1) return MX_ERR_ARG;
     if (slots >= kInt32End || E > kRouteMaxExperts) return MX_ERR_SHAPE;
-    const int blocks = plan_blocks(slots);
-    if (!row_offsets || !counts || (slots > 0 && (!ids || !slot_row)) || (blocks > 1 && !workspace)) return MX_ERR_ARG;
+    bool cluster = false;
+    const int blocks = plan_blocks(slots, &cluster);
+    if (!row_offsets || !counts || (slots > 0 && (!ids || !slot_row)) || (!cluster && !workspace)) return MX_ERR_ARG;
     if (!word_aligned(ids) || !word_aligned(row_offsets) || !word_aligned(slot_row) || !word_aligned(counts) ||
         !word_aligned(workspace))
         return MX_ERR_ALIGN;
@@ -1359,7 +1365,7 @@ mx_status mx_route_plan(const int32_t* ids, int64_t slots, int64_t E, int32_t* r
     a.offsets = row_offsets;
     a.slot_row = slot_row;
     a.counts = counts;
-    a.block_counts = blocks > 1 ? static_cast<int32_t*>(workspace) : nullptr;
+    a.block_counts = cluster ? nullptr : static_cast<int32_t*>(workspace);
     a.n = static_cast<int32_t>(slots);
     a.E = static_cast<int32_t>(E);
     a.chunk = static_cast<int32_t>(ceil_div(std::max<int64_t>(slots, 1), blocks));
@@ -1367,17 +1373,26 @@ mx_status mx_route_plan(const int32_t* ids, int64_t slots, int64_t E, int32_t* r
         plan_kernel<<<1, kPlanThreads, plan_smem_bytes(static_cast<int>(E)), stream>>>(a);
         return launched();
     }
-    counts_kernel<<<blocks, kPlanThreads, static_cast<size_t>(E + 1) * 4, stream>>>(a);
-    if (mx_status st = launched()) return st;
-    // The second kernel may start while the first still runs; it waits for it before it reads the counts.
+    if (!cluster) {
+        counts_kernel<<<blocks, kPlanThreads, static_cast<size_t>(E + 1) * 4, stream>>>(a);
+        if (mx_status st = launched()) return st;
+    }
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(blocks, 1, 1);
     cfg.blockDim = dim3(kPlanThreads, 1, 1);
     cfg.dynamicSmemBytes = plan_smem_bytes(static_cast<int>(E));
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    if (cluster) {
+        attr[0].id = cudaLaunchAttributeClusterDimension;
+        attr[0].val.clusterDim.x = blocks;
+        attr[0].val.clusterDim.y = 1;
+        attr[0].val.clusterDim.z = 1;
+    } else {
+        // The kernel may start while the counting kernel still runs; it waits for it before it reads the counts.
+        attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attr[0].val.programmaticStreamSerializationAllowed = 1;
+    }
     cfg.attrs = attr;
     cfg.numAttrs = 1;
     if (cudaLaunchKernelEx(&cfg, plan_kernel, a) != cudaSuccess) {

@@ -22,6 +22,7 @@
 #include <cstdint>
 
 #include "fastdiv.cuh"
+#include "ptx.cuh"
 
 namespace mx {
 
@@ -766,9 +767,11 @@ __global__ void __launch_bounds__(kRouteThreads) route_bwd_kernel(const __grid_c
 // A stable counting sort of the n = T * k slots by expert: rows of expert e are its slots in slot
 // order. Slots without an expert come after the last expert's rows and count as padding rows of the
 // last group, so row_offsets always ends at n, as the grouped GEMMs require.
-//   counts_kernel: every block counts the experts of its chunk of slots (n above one block's share);
+//   counts_kernel: every block counts the experts of its chunk of slots (n above one cluster's share);
 //   plan_kernel:   every block adds up the counts of the blocks before it and of all blocks (the
-//                  totals, whose scan are the offsets) and ranks the slots of its chunk.
+//                  totals, whose scan are the offsets) and ranks the slots of its chunk. Up to 4096 slots
+//                  take one block, up to 32 768 a cluster of 2, 4 or 8, which read one another's counts
+//                  through distributed shared memory.
 // Ranks come from per-warp counts in shared memory: a warp owns consecutive slots of the chunk and lanes
 // with the same expert find one another by ballots, so the order never depends on timing.
 
@@ -776,6 +779,7 @@ constexpr int kPlanThreads = 1024;
 constexpr int kPlanWarps = kPlanThreads / 32;
 constexpr int kPlanOneBlock = 4096;       // slots that one block sorts by itself
 constexpr int kPlanAhead = 4;             // loads of ids in flight per lane
+constexpr int kPlanCluster = 8;           // blocks of the largest cluster that sorts without a counting kernel
 constexpr int kPlanMaxBlocks = 128;
 
 struct PlanArgs {
@@ -882,6 +886,31 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const __grid_constan
             total[e] = sum;
         }
         __syncthreads();
+        if (gridDim.x > 1) {
+            // One cluster: this block's counts are its `total` until every block has read them.
+            cluster_sync();
+            int all[2] = {0, 0}, before[2] = {0, 0};         // B <= 1025: at most two buckets per thread
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const int e = tid + i * kPlanThreads;
+                if (e < B)
+                    for (int r = 0; r < static_cast<int>(gridDim.x); ++r) {
+                        const int c = static_cast<int>(ld_shared_cluster_u32(mapa_shared(smem_u32(&total[e]), r)));
+                        all[i] += c;
+                        if (r < static_cast<int>(blockIdx.x)) before[i] += c;
+                    }
+            }
+            cluster_sync();
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const int e = tid + i * kPlanThreads;
+                if (e < B) {
+                    total[e] = all[i];
+                    base[e] = before[i];
+                }
+            }
+            __syncthreads();
+        }
     }
     // Exclusive scan of the totals: first row of every bucket. B <= 1025: buckets past the first 1024
     // (only the last, "no expert") follow after the scan.

@@ -216,7 +216,7 @@ def test_empty_batch():
 # ---- the row partition -------------------------------------------------------------------------------
 
 @pytest.mark.parametrize("T,k,E", [(1, 1, 1), (1, 8, 128), (13, 8, 128), (512, 8, 7), (513, 8, 64), (5000, 1, 1000), (5000, 3, 1024),
-                                   (20480, 8, 128), (300000, 2, 60)])
+                                   (1024, 8, 33), (2049, 4, 1024), (4096, 8, 16), (4097, 8, 128), (32769, 1, 5), (20480, 8, 128), (300000, 2, 60)])
 @pytest.mark.parametrize("dropped", [False, True])
 def test_plan(T, k, E, dropped):
     g = np.random.default_rng(T + E)
@@ -229,10 +229,11 @@ def test_plan(T, k, E, dropped):
     assert np.array_equal(to_np(off), o) and np.array_equal(to_np(counts), c) and np.array_equal(to_np(slot_row), s)
 
 
-def test_plan_in_a_graph_and_two_at_once():
-    """More slots than one block sorts (two kernels, the second launched early): captured and replayed on other ids,
-    and two calls on two streams at the same time, each with its own workspace."""
-    T, k, E = 3000, 8, 100
+@pytest.mark.parametrize("T", [3000, 9000])
+def test_plan_in_a_graph_and_two_at_once(T):
+    """A cluster's sort, and two kernels, the second launched early: captured and replayed on other ids, and two calls
+    on two streams at the same time, each with its own workspace."""
+    k, E = 8, 100
     g = np.random.default_rng(8)
     draw = lambda: torch.from_numpy(g.integers(-1, E, (T, k)).astype(np.int32))  # noqa: E731
     ids = draw().cuda()
