@@ -1,4 +1,5 @@
-"""Builds libmx.so (the CUDA kernels + C ABI) in-tree for sm_100a with nvcc.
+"""Builds libmx.so (the CUDA kernels + C ABI) in-tree for sm_100a with nvcc, and _mxcall.so, the binding's compiled
+call path (csrc/binding.cpp), with g++ against the installed torch.
 
     python -m mxfp8_block_scaled_07_b200.build [--verbose]
 
@@ -31,6 +32,10 @@ NVCC_FLAGS = [
 ]
 
 
+CALL_LIB = os.path.join(HERE, "_mxcall.so")
+CALL_SOURCE = os.path.join(CSRC, "binding.cpp")
+
+
 def nvcc() -> str:
     for cand in (os.environ.get("NVCC"), "/usr/local/cuda/bin/nvcc", "nvcc"):
         if cand and (os.path.sep not in cand or os.path.exists(cand)):
@@ -38,25 +43,48 @@ def nvcc() -> str:
     raise RuntimeError("nvcc not found")
 
 
-def needs_build() -> bool:
-    if not os.path.exists(LIB):
+def needs_build(lib: str = LIB, deps=None) -> bool:
+    if not os.path.exists(lib):
         return True
-    t = os.path.getmtime(LIB)
-    return any(os.path.getmtime(p) > t for p in DEPS)
+    t = os.path.getmtime(lib)
+    return any(os.path.getmtime(p) > t for p in (DEPS if deps is None else deps))
+
+
+def _run(cmd, verbose: bool):
+    res = subprocess.run(cmd, capture_output=True, text=True)
+    if res.returncode != 0:
+        raise RuntimeError(f"{cmd[0]} failed ({res.returncode}):\n{' '.join(cmd)}\n{res.stdout}\n{res.stderr}")
+    if verbose:
+        sys.stdout.write(res.stdout + res.stderr)
 
 
 def build(force: bool = False, verbose: bool = False) -> str:
-    if not force and not needs_build():
-        return LIB
-    tmp = LIB + f".tmp{os.getpid()}"
-    cmd = [nvcc(), *NVCC_FLAGS, *(["-Xptxas", "-v"] if verbose else []), "-o", tmp, *SOURCES]
-    res = subprocess.run(cmd, capture_output=True, text=True)
-    if res.returncode != 0:
-        raise RuntimeError(f"nvcc failed ({res.returncode}):\n{' '.join(cmd)}\n{res.stdout}\n{res.stderr}")
-    if verbose:
-        sys.stdout.write(res.stdout + res.stderr)
-    os.replace(tmp, LIB)
+    if force or needs_build():
+        tmp = LIB + f".tmp{os.getpid()}"
+        _run([nvcc(), *NVCC_FLAGS, *(["-Xptxas", "-v"] if verbose else []), "-o", tmp, *SOURCES], verbose)
+        os.replace(tmp, LIB)
+    build_call(force, verbose)
     return LIB
+
+
+def build_call(force: bool = False, verbose: bool = False) -> str:
+    """_mxcall.so, linked against the libmx.so beside it."""
+    if not force and not needs_build(CALL_LIB, [CALL_SOURCE, os.path.join(ROOT, "include", "mx.h")]):
+        return CALL_LIB
+    import sysconfig
+
+    import torch
+
+    site = os.path.dirname(torch.__file__)
+    cuda = os.path.dirname(os.path.dirname(nvcc())) if os.path.sep in nvcc() else "/usr/local/cuda"
+    includes = [os.path.join(site, "include"), os.path.join(site, "include", "torch", "csrc", "api", "include"),
+                os.path.join(cuda, "include"), sysconfig.get_paths()["include"]]
+    tmp = CALL_LIB + f".tmp{os.getpid()}"
+    _run(["g++", "-O2", "-std=c++17", "-fPIC", "-shared", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+          *(x for p in includes for x in ("-isystem", p)), "-o", tmp, CALL_SOURCE, "-L" + HERE, "-l:libmx.so",
+          "-L" + os.path.join(site, "lib"), "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_python", "-Wl,-rpath,$ORIGIN"], verbose)
+    os.replace(tmp, CALL_LIB)
+    return CALL_LIB
 
 
 if __name__ == "__main__":

@@ -101,13 +101,6 @@ def test_plan_dispatch_combine(L):
     assert L.mx_grouped_scale_bytes(0, 4, 4) == 0 and L.mx_grouped_scale_bytes(1, 8, 1) == 512
     assert L.mx_grouped_scale_bytes(3, 8, 5) == 3 * 128 * 8 and L.mx_grouped_scale_bytes(256, 1, 4) == 1024
 
-    from mxfp8_block_scaled_07_b200 import mx
-
-    for rows, groups, kb in ((0, 4, 4), (1, 8, 1), (3, 8, 5), (256, 1, 4), (163840, 128, 64), (-1, 4, 4), (4, 0, 4), (4, 4, -1)):
-        assert mx.grouped_scale_bytes_bound(rows, groups, kb) == L.mx_grouped_scale_bytes(rows, groups, kb)
-        if rows >= 0 and kb >= 0:
-            assert mx._layout_bytes(rows, kb) == L.mx_swizzled_scale_bytes(rows, kb)
-
     def d(x=F, T=4, K=64, ld=64, sr=F, k=2, off=F, E=4, fmt=0, q=F, s=F):
         return L.mx_dispatch_quantize(x, T, K, ld, sr, k, off, E, fmt, q, s, None)
 
