@@ -1186,20 +1186,22 @@ void launch_route(const RouteArgs& a, bool packed, mx_stream stream) {
     const bool many = packed && NV <= 4 && a.T >= kRouteManyTokens;
     const int lanes = !many ? 32 : (a.k <= 8 ? 8 : 16);
     const unsigned grid = static_cast<unsigned>(ceil_div(a.T, kRouteThreads / lanes));
+    // Groups that cut lanes: a row of keys per warp (at most 32 KB a block).
+    const size_t smem = a.G > 1 && a.lanes_per_group == 0 ? size_t(kRouteThreads / 32) * a.E * 8 : 0;
     if constexpr (NV <= 4) {
         if (lanes == 8) {
-            route_kernel<NV, 8, true><<<grid, kRouteThreads, 0, stream>>>(a);
+            route_kernel<NV, 8, true><<<grid, kRouteThreads, smem, stream>>>(a);
             return;
         }
         if (lanes == 16) {
-            route_kernel<NV, 16, true><<<grid, kRouteThreads, 0, stream>>>(a);
+            route_kernel<NV, 16, true><<<grid, kRouteThreads, smem, stream>>>(a);
             return;
         }
     }
     if (packed)
-        route_kernel<NV, 32, true><<<grid, kRouteThreads, 0, stream>>>(a);
+        route_kernel<NV, 32, true><<<grid, kRouteThreads, smem, stream>>>(a);
     else
-        route_kernel<NV, 32, false><<<grid, kRouteThreads, 0, stream>>>(a);
+        route_kernel<NV, 32, false><<<grid, kRouteThreads, smem, stream>>>(a);
 }
 
 // Resident blocks per SM of a kernel, asked once per device and kept in `cache`.
@@ -1332,12 +1334,16 @@ mx_status mx_route_bwd(const float* d_weights, const void* logits, mx_out_dtype 
     a.dx = d_logits;
     a.ld_dx = ld_d;
     a.vec_dx = route_vec(d_logits, ld_d, E, 4, dtype);
-    const int lanes = topk <= 8 ? 8 : 16;             // one per slot; the other 32 / lanes - 1 tokens share the warp
+    // Lanes per token: a whole warp where whole rows are read, otherwise one per slot.
+    const bool dense = score == MX_SCORE_SOFTMAX && !renormalize;
+    const int lanes = dense ? 32 : (topk <= 8 ? 8 : 16);
     const unsigned grid = static_cast<unsigned>(ceil_div(T, kRouteThreads / lanes));
     if (lanes == 8)
         route_bwd_kernel<8><<<grid, kRouteThreads, 0, stream>>>(a);
-    else
+    else if (lanes == 16)
         route_bwd_kernel<16><<<grid, kRouteThreads, 0, stream>>>(a);
+    else
+        route_bwd_kernel<32><<<grid, kRouteThreads, 0, stream>>>(a);
     return launched();
 }
 

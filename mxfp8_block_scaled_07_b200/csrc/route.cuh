@@ -165,8 +165,11 @@ __device__ __forceinline__ U group_rank(U m, U c, bool top2) {
 
 // Ranks the groups and clears the keys of all but the topg best. `last` and `next`: the ranks of the worst group
 // kept and the best one left (0 if none). Where groups are whole lanes (a power of two of them), a group's two
-// largest keys are merged over its lanes by shuffles and every group counts the groups before it with G
-// independent shuffles; otherwise groups are walked one by one.
+// largest keys are merged over its lanes by shuffles; otherwise the keys go through a row of shared memory (8 bytes an
+// expert and warp) and lane g reads group g's. Every group then counts the groups before it with G independent
+// shuffles. (Walking the groups with a warp maximum each took 4 us more for 5201 tokens of 10 groups of 10.)
+extern __shared__ uint64_t route_smem[];
+
 template <int NV, class U>
 __device__ __forceinline__ void route_groups(const RouteArgs& a, U (&key)[NV], int lane, U& last, U& next) {
     const int G = a.G, L = a.lanes_per_group, per = static_cast<int>(a.per.d);
@@ -190,27 +193,24 @@ __device__ __forceinline__ void route_groups(const RouteArgs& a, U (&key)[NV], i
         rank = group_rank(m, c, top2);
         mine = lane / L;
     } else {
-        for (int g = 0; g < G; ++g) {
-            const int lo = g * per - lane * NV, hi = lo + per;      // the group's range in this lane's indices
-            U b = 0;
-            int bi = -1;
+        U* row = reinterpret_cast<U*>(route_smem) + (threadIdx.x >> 5) * a.E;
 #pragma unroll
-            for (int i = 0; i < NV; ++i)
-                if (i >= lo && i < hi && key[i] > b) {
-                    b = key[i];
-                    bi = i;
-                }
-            const U m = warp_max(b);
-            U c = 0;
-            if (top2 && m != 0) {
-                const int owner = __ffs(__ballot_sync(kFullMask, b == m)) - 1;
-#pragma unroll
-                for (int i = 0; i < NV; ++i)
-                    if (i >= lo && i < hi && !(lane == owner && i == bi) && key[i] > c) c = key[i];
-                c = warp_max(c);
+        for (int i = 0; i < NV; ++i)
+            if (lane * NV + i < a.E) row[lane * NV + i] = key[i];
+        __syncwarp();
+        if (lane < G) {
+            U m = 0, c = 0;
+            const U* mine_keys = row + lane * per;
+#pragma unroll 4
+            for (int j = 0; j < per; ++j) {
+                const U k = mine_keys[j];
+                const U lo = k < m ? k : m;
+                m = k < m ? m : k;
+                c = lo < c ? c : lo;
             }
-            if (lane == g) rank = group_rank(m, c, top2);
+            rank = group_rank(m, c, top2);
         }
+        __syncwarp();
     }
     int before = 0;
     for (int g = 0; g < G; ++g) {
@@ -339,25 +339,37 @@ __device__ __forceinline__ uint32_t route_select_packed(uint32_t (&key)[TOK][NV]
     return got >= 0x10000u ? got : 0u;       // below: nothing was left that can be chosen
 }
 
+// fp64 arithmetic for tokens that fp32 cannot decide. One copy of each, not inlined: a few tokens of a batch come
+// here, and what they cost is the time to fetch the instructions.
+__device__ __noinline__ double route_exp(double x) { return exp(x); }
+__device__ __noinline__ double route_quotient(double a, double b) { return a / b; }
+// The row's softmax denominator (1 for a sigmoid) and the score of logit x.
+template <int NV>
+__device__ __forceinline__ double route_sum(const RouteArgs& a, const float (&v)[NV], float M) {
+    if (a.sigmoid) return 1.0;
+    double z = 0.0;
+#pragma unroll 1
+    for (int i = 0; i < NV; ++i)
+        if (v[i] > __int_as_float(0xFF800000)) z += route_exp(static_cast<double>(v[i]) - static_cast<double>(M));
+    return warp_sum(z);
+}
+__device__ __noinline__ double route_score(bool sigmoid, float x, float M, double z) {
+    const double e = route_exp(sigmoid ? -static_cast<double>(x) : static_cast<double>(x) - static_cast<double>(M));
+    return route_quotient(sigmoid ? 1.0 : e, sigmoid ? 1.0 + e : z);
+}
+
 // The choice in fp64, for a token that fp32 cannot decide: slot j's expert in lane j.
 template <int NV>
 __device__ __noinline__ int route_exact(const RouteArgs& a, const float (&v)[NV], float M, int lane) {
     const double kNone = __longlong_as_double(0xFFF0000000000000ll);
-    double z = 0.0;
-    if (!a.sigmoid) {
-#pragma unroll 1
-        for (int i = 0; i < NV; ++i)
-            if (v[i] > __int_as_float(0xFF800000)) z += exp(static_cast<double>(v[i]) - static_cast<double>(M));
-        z = warp_sum(z);
-    }
+    const double z = route_sum(a, v, M);
     uint64_t key[NV];
 #pragma unroll 1
     for (int i = 0; i < NV; ++i) {
         const int e = lane * NV + i;
         double s = kNone;
         if (e < a.E && v[i] > __int_as_float(0xFF800000)) {
-            const double x = static_cast<double>(v[i]);
-            s = a.sigmoid ? 1.0 / (1.0 + exp(-x)) : exp(x - static_cast<double>(M)) / z;
+            s = route_score(a.sigmoid != 0, v[i], M, z);
             if (a.bias) s += static_cast<double>(a.bias[e]);
         }
         key[i] = key_of(s);
@@ -375,18 +387,10 @@ __device__ __noinline__ int route_exact(const RouteArgs& a, const float (&v)[NV]
 template <int NV>
 __device__ __noinline__ void route_reorder(const RouteArgs& a, const float (&v)[NV], float M, int lane, int& id, float& x,
                                            float b) {
-    double z = 1.0;
-    if (!a.sigmoid) {
-        z = 0.0;
-#pragma unroll 1
-        for (int i = 0; i < NV; ++i)
-            if (v[i] > __int_as_float(0xFF800000)) z += exp(static_cast<double>(v[i]) - static_cast<double>(M));
-        z = warp_sum(z);
-    }
+    const double z = route_sum(a, v, M);
     double key = __longlong_as_double(0xFFF0000000000000ll);
     if (id >= 0) {
-        const double xd = static_cast<double>(x);
-        key = a.sigmoid ? 1.0 / (1.0 + exp(-xd)) : exp(xd - static_cast<double>(M)) / z;
+        key = route_score(a.sigmoid != 0, x, M, z);
         if (a.bias) key += static_cast<double>(b);
     }
     int before = 0;
@@ -594,8 +598,10 @@ __global__ void __launch_bounds__(kRouteThreads) route_kernel(const __grid_const
 //                 softmax: dx_e = p_e * (d_e - sum_j d_j p_j) with d_j = scale * dw_j at the chosen.
 // Only the last form reads whole rows; the others read the k chosen logits and write the row.
 //
-// A warp takes 32 / LPT tokens (LPT = 8 or 16 lanes, one per slot, for each): the slots' arithmetic runs for all of
-// them at once. Then row by row: the chosen experts' parts are put into a row of zeros in shared memory, the row is
+// A warp takes 32 / LPT tokens: LPT = 8 or 16 lanes, one per slot, for each, and the slots' arithmetic runs for all of
+// them at once; LPT = 32, one token, in the last form, whose time is that of its row's exponentials (four tokens'
+// rows in a warp took 8.5 us for 5201 x 100 and 6.3 us for 16 x 128, one 5.3 and 2.9; 20 480 x 128: 12.0 and 12.8).
+// Then row by row: the chosen experts' parts are put into a row of zeros in shared memory, the row is
 // read back four experts per lane, finished and stored, and the parts are cleared again. An expert named twice gets
 // the sum of its parts in slot order.
 template <int LPT>
@@ -646,41 +652,23 @@ __global__ void __launch_bounds__(kRouteThreads) route_bwd_kernel(const __grid_c
         for (int o = LPT / 2; o > 0; o >>= 1) s += __shfl_xor_sync(kFullMask, s, o);
         return s;
     };
-    const bool dense = !a.sigmoid && !a.renorm;
-    float c = 0.0f, row = 0.0f, M = kNone, z = 0.0f;      // the chosen expert's part; the token's sum of d p, max, sum
-    if (dense) {
-        // All tokens' rows side by side (a token past the end stands for the last one): the maxima and the sums.
-        float m[kTokens], s[kTokens];
+    constexpr bool kDense = LPT == 32;
+    float c = 0.0f, row = 0.0f, M = kNone, z = 0.0f;      // the chosen expert's part; the row's sum of d p, max, sum
+    if constexpr (kDense) {
+        for (int ch = 0; ch < chunks; ++ch) {             // a running maximum and the sum relative to it
+            float v[4];
+            load4(t0, ch, v);
+            const float mm = fmaxf(fmaxf(fmaxf(v[0], v[1]), fmaxf(v[2], v[3])), M);
+            if (mm > M) z = M > kNone ? z * expf(M - mm) : 0.0f;
+            M = mm;
 #pragma unroll
-        for (int qq = 0; qq < kTokens; ++qq) {
-            m[qq] = kNone;
-            s[qq] = 0.0f;
+            for (int i = 0; i < 4; ++i) z += v[i] > kNone ? expf(v[i] - mm) : 0.0f;
         }
-        for (int ch = 0; ch < chunks; ++ch) {
-            float v[kTokens][4];
+        float mm = M;
 #pragma unroll
-            for (int qq = 0; qq < kTokens; ++qq) load4(t0 + qq < a.T ? t0 + qq : a.T - 1, ch, v[qq]);
-#pragma unroll
-            for (int qq = 0; qq < kTokens; ++qq) {
-                // A running maximum and the sum relative to it.
-                const float mm = fmaxf(fmaxf(fmaxf(v[qq][0], v[qq][1]), fmaxf(v[qq][2], v[qq][3])), m[qq]);
-                if (mm > m[qq]) s[qq] = m[qq] > kNone ? s[qq] * expf(m[qq] - mm) : 0.0f;
-                m[qq] = mm;
-#pragma unroll
-                for (int i = 0; i < 4; ++i) s[qq] += v[qq][i] > kNone ? expf(v[qq][i] - mm) : 0.0f;
-            }
-        }
-#pragma unroll
-        for (int qq = 0; qq < kTokens; ++qq) {
-            float mm = m[qq];
-#pragma unroll
-            for (int o = 16; o > 0; o >>= 1) mm = fmaxf(mm, __shfl_xor_sync(kFullMask, mm, o));
-            const float sum = warp_sum(m[qq] > kNone ? s[qq] * expf(m[qq] - mm) : 0.0f);
-            if (q == qq) {
-                M = mm;
-                z = sum;
-            }
-        }
+        for (int o = 16; o > 0; o >>= 1) mm = fmaxf(mm, __shfl_xor_sync(kFullMask, mm, o));
+        z = warp_sum(M > kNone ? z * expf(M - mm) : 0.0f);
+        M = mm;
         const float p = got ? expf(x - M) / z : 0.0f;
         c = a.scale * g * p;
         row = sum_slots(c);
@@ -717,17 +705,15 @@ __global__ void __launch_bounds__(kRouteThreads) route_bwd_kernel(const __grid_c
         if (t >= a.T) break;
         if (put && q == qq) buf[id] = c;
         __syncwarp();
-        const float mq = __shfl_sync(kFullMask, M, qq * LPT), zq = __shfl_sync(kFullMask, z, qq * LPT);
-        const float rq = __shfl_sync(kFullMask, row, qq * LPT);
         for (int ch = 0; ch < chunks; ++ch) {
             const float4 o4 = reinterpret_cast<const float4*>(buf)[ch * 32 + lane];
             float o[4] = {o4.x, o4.y, o4.z, o4.w};
-            if (dense) {
+            if constexpr (kDense) {
                 float v[4];
                 load4(t, ch, v);
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
-                    if (v[i] > kNone) o[i] -= expf(v[i] - mq) / zq * rq;
+                    if (v[i] > kNone) o[i] -= expf(v[i] - M) / z * row;
             }
             const int e0 = ch * 128 + lane * 4;
             const int64_t at = t * a.ld_dx + e0;
