@@ -142,7 +142,7 @@ PyObject* route(Args a) {
     const float scale = static_cast<float>(number(a[8]));
     const at::Tensor* bias = optional_tensor(a[3], "route: bias");
     const void* pb = bias ? packed(*bias, at::kFloat, x.n, dev, "route: bias must be fp32 [E]") : nullptr;
-    need(topk >= 1, "route: topk");
+    need(topk >= 1 && topk <= x.n, "route: 1 <= topk <= experts");      // before outputs of that width are allocated
     const Place place(logits);
     at::Tensor ids, weights;
     PyObject *oi = nullptr, *ow = nullptr;

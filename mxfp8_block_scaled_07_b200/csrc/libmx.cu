@@ -260,6 +260,19 @@ constexpr size_t kTmapCacheMax = 4096;
 
 // kind: 0 = E4M3 operand (uint8, 128-byte swizzle), 1 = scale layout (uint8, no swizzle),
 // 2 = BF16 quantizer input (128-byte swizzle).
+bool encode_2d_now(CUtensorMap* map, uint32_t kind, const void* base, uint64_t d0, uint64_t d1, uint64_t stride,
+                   uint32_t b0, uint32_t b1) {
+    if (!encode_fn()) return false;
+    const cuuint64_t dims[2] = {d0, d1};
+    const cuuint64_t strides[1] = {stride};
+    const cuuint32_t box[2] = {b0, b1};
+    const cuuint32_t estr[2] = {1, 1};
+    const CUtensorMapDataType dt = kind == 2 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_UINT8;
+    const CUtensorMapSwizzle sw = kind == 1 ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_128B;
+    return g_encode(map, dt, 2, const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, sw,
+                    CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 bool encode_2d(CUtensorMap* map, uint32_t kind, const void* base, uint64_t d0, uint64_t d1, uint64_t stride,
                uint32_t b0, uint32_t b1) {
     static thread_local std::unordered_map<TmapKey, CUtensorMap, TmapKeyHash> cache;
@@ -269,16 +282,7 @@ bool encode_2d(CUtensorMap* map, uint32_t kind, const void* base, uint64_t d0, u
         *map = it->second;
         return true;
     }
-    if (!encode_fn()) return false;
-    const cuuint64_t dims[2] = {d0, d1};
-    const cuuint64_t strides[1] = {stride};
-    const cuuint32_t box[2] = {b0, b1};
-    const cuuint32_t estr[2] = {1, 1};
-    const CUtensorMapDataType dt = kind == 2 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_UINT8;
-    const CUtensorMapSwizzle sw = kind == 1 ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_128B;
-    if (g_encode(map, dt, 2, const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, sw,
-                 CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
-        return false;
+    if (!encode_2d_now(map, kind, base, d0, d1, stride, b0, b1)) return false;
     if (cache.size() >= kTmapCacheMax) cache.clear();
     cache.emplace(key, *map);
     return true;
@@ -324,29 +328,22 @@ bool make_tmap_sf(CUtensorMap* map, const void* base, int64_t blocks) {
     return encode_2d(map, 1, base, 256, static_cast<uint64_t>(2 * blocks), 256, 256, 2);
 }
 
+// Packed MXFP4 codes [rows, cols_bytes], as make_tmap. The MXFP4 products encode their maps in every call.
+bool make_tmap_fp4(CUtensorMap* map, const void* base, uint64_t cols_bytes, uint64_t rows, uint32_t box_rows) {
+    return encode_2d_now(map, 0, base, cols_bytes, rows, cols_bytes, kBK, box_rows);
+}
+
 // The same layout with its row tiles as a third dimension: `tiles` row tiles of ctiles blocks; a box is two
 // consecutive blocks of box_tiles row tiles (MXFP4: one copy per operand and stage).
 bool make_tmap_sf_tiles(CUtensorMap* map, const void* base, int64_t ctiles, int64_t tiles, uint32_t box_tiles) {
-    static thread_local std::unordered_map<TmapKey, CUtensorMap, TmapKeyHash> cache;
-    const TmapKey key{reinterpret_cast<uintptr_t>(base), static_cast<uint64_t>(ctiles), static_cast<uint64_t>(tiles), 0,
-                      box_tiles, 0, 3};
-    auto it = cache.find(key);
-    if (it != cache.end()) {
-        *map = it->second;
-        return true;
-    }
     if (!encode_fn()) return false;
     const cuuint64_t dims[3] = {256, static_cast<cuuint64_t>(2 * ctiles), static_cast<cuuint64_t>(tiles)};
     const cuuint64_t strides[2] = {256, static_cast<cuuint64_t>(512 * ctiles)};
     const cuuint32_t box[3] = {256, 4, box_tiles};
     const cuuint32_t estr[3] = {1, 1, 1};
-    if (g_encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void*>(base), dims, strides, box, estr,
-                 CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                 CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
-        return false;
-    if (cache.size() >= kTmapCacheMax) cache.clear();
-    cache.emplace(key, *map);
-    return true;
+    return g_encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void*>(base), dims, strides, box, estr,
+                    CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                    CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 // Launches the CTA-pair GEMM with a cluster dimension of 2.
@@ -970,7 +967,7 @@ mx_status launch_gemm_fp4(const uint8_t* qa, const uint8_t* sa, const uint8_t* q
     const int64_t sfa_tiles = offsets ? ceil_div(M, 128) + G : a.sfa_tiles;
     const int64_t tiles = (offsets ? ceil_div(M, 2 * kBM) + G : a.tiles_m) * a.tiles_n;
     CUtensorMap ta, tb, tsa, tsb;
-    if (!make_tmap(&ta, qa, K / 2, M, kBK, kBM) || !make_tmap(&tb, qb, K / 2, G * N, kBK, kBN / 2) ||
+    if (!make_tmap_fp4(&ta, qa, K / 2, M, kBM) || !make_tmap_fp4(&tb, qb, K / 2, G * N, kBN / 2) ||
         !make_tmap_sf_tiles(&tsa, sa, ceil_div(K, 128), sfa_tiles, 1) ||
         !make_tmap_sf_tiles(&tsb, sb, ceil_div(K, 128), G * a.n_rowtiles, 2))
         return MX_ERR_CUDA;
@@ -986,7 +983,7 @@ mx_status launch_few(const uint8_t* qa, const uint8_t* sa, const uint8_t* qb, co
                      const DeviceInfo* d, mx_stream stream) {
     const int64_t tiles = ceil_div(a.N, 128), ct = ceil_div(a.K, 128);
     CUtensorMap tw, tx, tsw, tsx;
-    if (!make_tmap(&tw, qb, a.K / 2, a.N, kBK, 128) || !make_tmap(&tx, qa, a.K / 2, a.M, kBK, NPAD) ||
+    if (!make_tmap_fp4(&tw, qb, a.K / 2, a.N, 128) || !make_tmap_fp4(&tx, qa, a.K / 2, a.M, NPAD) ||
         !make_tmap_sf_tiles(&tsw, sb, ct, tiles, 1) || !make_tmap_sf_tiles(&tsx, sa, ct, 1, 1))
         return MX_ERR_CUDA;
     int ranks = 1;
@@ -1132,8 +1129,8 @@ mx_status mx_grouped_gemm_fp4(const uint8_t* qa, const uint8_t* sa_swz, const ui
         const int64_t tiles = (ceil_div(total_rows, kGfRows) + std::min(G, total_rows)) * a.tiles_n;
         if (tiles < kInt32End) {
             CUtensorMap tw, tx, txs, tsw, tsx;
-            if (!make_tmap(&tw, qb, K / 2, G * N, kBK, 128) || !make_tmap(&tx, qa, K / 2, total_rows, kBK, kGfRows) ||
-                !make_tmap(&txs, qa, K / 2, total_rows, kBK, kGfSmall) ||
+            if (!make_tmap_fp4(&tw, qb, K / 2, G * N, 128) || !make_tmap_fp4(&tx, qa, K / 2, total_rows, kGfRows) ||
+                !make_tmap_fp4(&txs, qa, K / 2, total_rows, kGfSmall) ||
                 !make_tmap_sf_tiles(&tsw, sb_swz, ct, G * a.tiles_n, 1) ||
                 !make_tmap_sf_tiles(&tsx, sa_swz, ct, ceil_div(total_rows, 128) + G, 1))
                 return MX_ERR_CUDA;
