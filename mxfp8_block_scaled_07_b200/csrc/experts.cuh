@@ -86,6 +86,7 @@ __device__ __forceinline__ int last_not_above(const int32_t* a, int E, int x) {
 // tile, and the tiles behind the last group.
 template <bool FP4>
 __global__ void __launch_bounds__(kExThreads) dispatch_kernel(const __grid_constant__ DispatchArgs a) {
+    grid_wait();
     __shared__ int32_t off[kRouteMaxExperts + 1];
     __shared__ int32_t first[kRouteMaxExperts + 1];
     __shared__ int32_t warp_sums[kExThreads / 32];
@@ -119,11 +120,11 @@ __global__ void __launch_bounds__(kExThreads) dispatch_kernel(const __grid_const
         if (in) {
             const uint16_t* p = a.x + t * a.ldx + static_cast<int64_t>(kb) * 32;
             if (a.vec32) {
-                ld_stream_v8(p, b.v[0], b.v[1]);
-                ld_stream_v8(p + 16, b.v[2], b.v[3]);
+                ld_once_v8(p, b.v[0], b.v[1]);
+                ld_once_v8(p + 16, b.v[2], b.v[3]);
             } else {
 #pragma unroll
-                for (int j = 0; j < 4; ++j) b.v[j] = ld_cached_v4(p + 8 * j);
+                for (int j = 0; j < 4; ++j) b.v[j] = reinterpret_cast<const uint4*>(p)[j];
             }
         }
         const uint32_t amax = block_absmax(b);
@@ -228,7 +229,7 @@ __device__ __forceinline__ int64_t piece_col(int64_t c0, int lane, int i, bool v
 
 // A lane's part of a piece of c, as it lies in memory: 8 BF16 or 4 fp32 in 16 bytes. Entries past N are 0.
 __device__ __forceinline__ uint4 load_raw(const uint16_t* row, int64_t c0, int64_t N, int lane, bool vec) {
-    if (vec && c0 + lane * 8 + 8 <= N) return ld_stream_v4(row + c0 + lane * 8);
+    if (vec && c0 + lane * 8 + 8 <= N) return ld_once_v4(row + c0 + lane * 8);
     uint32_t w[4] = {0, 0, 0, 0};
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
@@ -238,7 +239,7 @@ __device__ __forceinline__ uint4 load_raw(const uint16_t* row, int64_t c0, int64
     return make_uint4(w[0], w[1], w[2], w[3]);
 }
 __device__ __forceinline__ uint4 load_raw(const float* row, int64_t c0, int64_t N, int lane, bool vec) {
-    if (vec && c0 + lane * 4 + 4 <= N) return ld_stream_v4(row + c0 + lane * 4);
+    if (vec && c0 + lane * 4 + 4 <= N) return ld_once_v4(row + c0 + lane * 4);
     uint32_t w[4] = {0, 0, 0, 0};
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -330,6 +331,7 @@ __device__ __forceinline__ void load_slot(const CombineArgs& a, int64_t t, int j
 // one: 271 us). Three blocks per SM: 122 us; two (no register limit) 137, four 129.
 template <class CT, class YT>
 __global__ void __launch_bounds__(kExThreads, 3) combine_kernel(const __grid_constant__ CombineArgs a) {
+    grid_wait();
     constexpr int P = 16 / static_cast<int>(sizeof(CT));
     const int lane = threadIdx.x & 31;
     const uint32_t step = gridDim.x * (kExThreads / 32);
@@ -385,6 +387,7 @@ __global__ void __launch_bounds__(kExThreads, 3) combine_kernel(const __grid_con
 // three and four blocks per SM, with plain or streaming stores, and with the dot products before or after them.
 template <class CT, class YT>
 __global__ void __launch_bounds__(kExThreads, 3) combine_bwd_kernel(const __grid_constant__ CombineArgs a) {
+    grid_wait();
     constexpr int P = 16 / static_cast<int>(sizeof(CT));
     __shared__ float part[2][kExThreads / 32][kCombineSlots];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;

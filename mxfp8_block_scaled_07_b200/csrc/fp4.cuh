@@ -133,6 +133,7 @@ struct Fp4Args {
 // 32.5 us for both (154 MB, 4.7 TB/s; two CTAs per SM: 22, 29 and 35 us), where issue slots are 60% busy.
 template <bool ROW, bool COL>
 __global__ void __launch_bounds__(kQThreads, 3) quantize_fp4_kernel(const __grid_constant__ Fp4Args a) {
+    grid_wait();
     __shared__ __align__(128) uint8_t tile[COL ? kQTile * 256 : 16];
     __shared__ __align__(16) uint8_t atom_row[512];
     __shared__ __align__(16) uint8_t atom_col[512];
@@ -147,7 +148,7 @@ __global__ void __launch_bounds__(kQThreads, 3) quantize_fp4_kernel(const __grid
     auto fetch = [&](int m, int k, int h) {
         const int64_t row = static_cast<int64_t>(m) * kQTile + h * 64 + (tid >> 2);
         const int64_t col = static_cast<int64_t>(k) * kQTile + kb * 32;
-        load_block(T, row, col, row < T.M && col < T.K, cur[h]);
+        load_block<true>(T, row, col, row < T.M && col < T.K, cur[h]);
     };
     if (t_begin < t_end) {
         fetch(mt, kt, 0);
@@ -242,6 +243,7 @@ constexpr int kDeqWords = 4;          // words per thread
 // of the bytes are written, and writes alone reach 3.95 TB/s on this part (a fill of 1 GB): that, not the copy
 // bandwidth, is what bounds this kernel.
 __global__ void __launch_bounds__(256) dequantize_fp4_kernel(const __grid_constant__ Fp4DeqArgs a) {
+    grid_wait();
     const uint32_t i0 = blockIdx.x * (256u * kDeqWords) + threadIdx.x;
     const uint8_t* qs = a.q + a.row0 * a.kblocks * 16;
     uint32_t q[kDeqWords], s[kDeqWords];
@@ -252,7 +254,7 @@ __global__ void __launch_bounds__(256) dequantize_fp4_kernel(const __grid_consta
         if (i < a.words) {
             const uint32_t rl = a.words_per_row.div(i), w = i - rl * a.words_per_row.d;     // row, word in it
             const int64_t r = a.row0 + rl, c = w >> 2;
-            q[j] = __ldg(reinterpret_cast<const uint32_t*>(qs) + i);
+            q[j] = reinterpret_cast<const uint32_t*>(qs)[i];
             s[j] = a.s[a.swz ? ((r >> 7) * a.ctiles + (c >> 2)) * 512 + (r & 31) * 16 + ((r & 127) >> 5) * 4 + (c & 3)
                              : r * a.kblocks + c];
             at[j] = r * a.ld + static_cast<int64_t>(w) * 8;

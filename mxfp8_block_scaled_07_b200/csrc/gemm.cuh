@@ -698,6 +698,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
     using L8 = typename std::conditional<GROUPED, SmemPairGrouped, SmemPairDense>::type;
     using L4 = typename std::conditional<GROUPED, SmemPairGroupedFp4, SmemPairDenseFp4>::type;
     using L = typename std::conditional<FP4, L4, L8>::type;
+    if constexpr (FP4) grid_wait();
     constexpr uint32_t kPairStageBytes = kPairStageBytesOf<FP4>;
     constexpr int kSfaStage = (FP4 ? 2 : 1) * kSfaBytes, kSfbStage = (FP4 ? 2 : 1) * kSfbBytes;
     constexpr int S = L::kStages;

@@ -77,6 +77,7 @@ __global__ void __launch_bounds__(kFewThreads, 2)
     constexpr int S = kFewStages;
     constexpr uint32_t kCols = 128;             // TMEM: NPAD accumulator columns, then two scale slots of 8
     constexpr uint32_t kSf = 64;
+    grid_wait();
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     uint64_t* full = reinterpret_cast<uint64_t*>(smem + L::kBar);
@@ -311,6 +312,7 @@ __global__ void __launch_bounds__(kFewThreads, 2)
     using L = GfSmem;
     constexpr int S = kGfStages;
     constexpr uint32_t kCols = 256, kSf = 128;  // TMEM: an accumulator of 128 columns, two scale slots of 8
+    grid_wait();
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     uint64_t* full = reinterpret_cast<uint64_t*>(smem + L::kBar);

@@ -346,15 +346,43 @@ bool make_tmap_sf_tiles(CUtensorMap* map, const void* base, int64_t ctiles, int6
                     CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// Launches a kernel that begins with grid_wait(): it may start as the kernel in front of it in the stream ends.
+// `cluster` CTAs per cluster (1: none).
+template <class... P, class... A>
+mx_status launch_behind(void (*kernel)(P...), int64_t grid, int threads, size_t smem, int cluster, mx_stream stream,
+                        const A&... args) {
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = cluster;
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(grid), 1, 1);
+    cfg.blockDim = dim3(threads, 1, 1);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cfg.attrs = attr;
+    cfg.numAttrs = cluster > 1 ? 2 : 1;
+    if (cudaLaunchKernelEx(&cfg, kernel, args...) != cudaSuccess) {
+        cudaGetLastError();
+        return MX_ERR_CUDA;
+    }
+    return launched();
+}
+
 // Launches the CTA-pair GEMM with a cluster dimension of 2.
 template <bool GROUPED, int EPI = 0, bool FP4 = false>
 mx_status launch_pair(int pairs, const CUtensorMap& ta, const CUtensorMap& tb, const CUtensorMap& tsa,
                       const CUtensorMap& tsb, const GemmArgs& a, mx_stream stream) {
+    if constexpr (FP4)
+        return launch_behind(mx_gemm_pair_kernel<GROUPED, EPI, FP4>, 2 * pairs, kGemmThreads,
+                             GROUPED ? kGemmPairSmemGroupedFp4 : kGemmPairSmemDenseFp4, 2, stream, ta, tb, tsa, tsb, a);
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(2 * pairs, 1, 1);
     cfg.blockDim = dim3(kGemmThreads, 1, 1);
-    cfg.dynamicSmemBytes = FP4 ? (GROUPED ? kGemmPairSmemGroupedFp4 : kGemmPairSmemDenseFp4)
-                               : (GROUPED ? kGemmPairSmemGrouped : kGemmPairSmemDense);
+    cfg.dynamicSmemBytes = GROUPED ? kGemmPairSmemGrouped : kGemmPairSmemDense;
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -988,23 +1016,8 @@ mx_status launch_few(const uint8_t* qa, const uint8_t* sa, const uint8_t* qb, co
         return MX_ERR_CUDA;
     int ranks = 1;
     while (ranks < 8 && tiles * ranks * 2 <= 2 * int64_t(d->sms) && a.nkb >= 4 * ranks) ranks *= 2;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>(tiles * ranks), 1, 1);
-    cfg.blockDim = dim3(kFewThreads, 1, 1);
-    cfg.dynamicSmemBytes = FewSmem<NPAD>::kBytes;
-    cfg.stream = stream;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = ranks;
-    attr[0].val.clusterDim.y = 1;
-    attr[0].val.clusterDim.z = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    if (cudaLaunchKernelEx(&cfg, mx_gemm_fp4_few_kernel<NPAD>, tw, tx, tsw, tsx, a) != cudaSuccess) {
-        cudaGetLastError();
-        return MX_ERR_CUDA;
-    }
-    return launched();
+    return launch_behind(mx_gemm_fp4_few_kernel<NPAD>, tiles * ranks, kFewThreads, FewSmem<NPAD>::kBytes, ranks, stream, tw,
+                         tx, tsw, tsx, a);
 }
 
 }  // namespace
@@ -1035,13 +1048,9 @@ mx_status mx_quantize_fp4(const void* x, int64_t M, int64_t K, int64_t ld_x, int
     a.total_tiles = one.total_tiles;
     const int which = (row ? 1 : 0) | (col ? 2 : 0);
     const int64_t grid = std::min<int64_t>(a.total_tiles, int64_t(d->sms) * d->fp4_blocks_per_sm[which]);
-    if (row && col)
-        quantize_fp4_kernel<true, true><<<grid, kQThreads, 0, stream>>>(a);
-    else if (row)
-        quantize_fp4_kernel<true, false><<<grid, kQThreads, 0, stream>>>(a);
-    else
-        quantize_fp4_kernel<false, true><<<grid, kQThreads, 0, stream>>>(a);
-    return launched();
+    if (row && col) return launch_behind(quantize_fp4_kernel<true, true>, grid, kQThreads, 0, 1, stream, a);
+    if (row) return launch_behind(quantize_fp4_kernel<true, false>, grid, kQThreads, 0, 1, stream, a);
+    return launch_behind(quantize_fp4_kernel<false, true>, grid, kQThreads, 0, 1, stream, a);
 }
 
 mx_status mx_dequantize_fp4(const uint8_t* q, const uint8_t* s, int64_t M, int64_t K, int swizzled, void* out,
@@ -1067,8 +1076,8 @@ mx_status mx_dequantize_fp4(const uint8_t* q, const uint8_t* s, int64_t M, int64
     const int64_t slab = (kInt32End - 1 - 256 * kDeqWords) / (K / 8);
     for (a.row0 = 0; a.row0 < M; a.row0 += slab) {
         a.words = static_cast<uint32_t>(std::min(M - a.row0, slab) * (K / 8));
-        dequantize_fp4_kernel<<<static_cast<unsigned>(ceil_div(a.words, 256 * kDeqWords)), 256, 0, stream>>>(a);
-        if (mx_status st = launched()) return st;
+        if (mx_status st = launch_behind(dequantize_fp4_kernel, ceil_div(a.words, 256 * kDeqWords), 256, 0, 1, stream, a))
+            return st;
     }
     return MX_OK;
 }
@@ -1134,9 +1143,8 @@ mx_status mx_grouped_gemm_fp4(const uint8_t* qa, const uint8_t* sa_swz, const ui
                 !make_tmap_sf_tiles(&tsw, sb_swz, ct, G * a.tiles_n, 1) ||
                 !make_tmap_sf_tiles(&tsx, sa_swz, ct, ceil_div(total_rows, 128) + G, 1))
                 return MX_ERR_CUDA;
-            const unsigned grid = static_cast<unsigned>(std::min<int64_t>(tiles, 2 * int64_t(d->sms)));
-            mx_grouped_gemm_fp4_few_kernel<<<grid, kFewThreads, GfSmem::kBytes, stream>>>(tw, tx, txs, tsw, tsx, a);
-            return launched();
+            return launch_behind(mx_grouped_gemm_fp4_few_kernel, std::min<int64_t>(tiles, 2 * int64_t(d->sms)), kFewThreads,
+                                 GfSmem::kBytes, 1, stream, tw, tx, txs, tsw, tsx, a);
         }
     }
     return launch_gemm_fp4(qa, sa_swz, qb, sb_swz, row_offsets_dev, G, total_rows, N, K, c, ld_c, out_dtype, d, stream);
@@ -1179,26 +1187,18 @@ mx_status route_shape(int64_t T, int64_t E, int64_t topk, int64_t ld, mx_out_dty
 constexpr int64_t kRouteManyTokens = 4096;
 
 template <int NV>
-void launch_route(const RouteArgs& a, bool packed, mx_stream stream) {
+mx_status launch_route(const RouteArgs& a, bool packed, mx_stream stream) {
     const bool many = packed && NV <= 4 && a.T >= kRouteManyTokens;
     const int lanes = !many ? 32 : (a.k <= 8 ? 8 : 16);
-    const unsigned grid = static_cast<unsigned>(ceil_div(a.T, kRouteThreads / lanes));
+    const int64_t grid = ceil_div(a.T, kRouteThreads / lanes);
     // Groups that cut lanes: a row of keys per warp (at most 32 KB a block).
     const size_t smem = a.G > 1 && a.lanes_per_group == 0 ? size_t(kRouteThreads / 32) * a.E * 8 : 0;
     if constexpr (NV <= 4) {
-        if (lanes == 8) {
-            route_kernel<NV, 8, true><<<grid, kRouteThreads, smem, stream>>>(a);
-            return;
-        }
-        if (lanes == 16) {
-            route_kernel<NV, 16, true><<<grid, kRouteThreads, smem, stream>>>(a);
-            return;
-        }
+        if (lanes == 8) return launch_behind(route_kernel<NV, 8, true>, grid, kRouteThreads, smem, 1, stream, a);
+        if (lanes == 16) return launch_behind(route_kernel<NV, 16, true>, grid, kRouteThreads, smem, 1, stream, a);
     }
-    if (packed)
-        route_kernel<NV, 32, true><<<grid, kRouteThreads, smem, stream>>>(a);
-    else
-        route_kernel<NV, 32, false><<<grid, kRouteThreads, smem, stream>>>(a);
+    if (packed) return launch_behind(route_kernel<NV, 32, true>, grid, kRouteThreads, smem, 1, stream, a);
+    return launch_behind(route_kernel<NV, 32, false>, grid, kRouteThreads, smem, 1, stream, a);
 }
 
 // Resident blocks per SM of a kernel, asked once per device and kept in `cache`.
@@ -1231,14 +1231,12 @@ mx_status launch_combine(CombineArgs& a, bool backward, const DeviceInfo* d, mx_
     if (backward) {
         static std::atomic<int> blocks[kMaxDevices];
         const int64_t grid = std::min<int64_t>(a.T, int64_t(d->sms) * cached_occupancy(blocks, combine_bwd_kernel<CT, YT>));
-        combine_bwd_kernel<CT, YT><<<static_cast<unsigned>(grid), kExThreads, 0, stream>>>(a);
-    } else {
-        static std::atomic<int> blocks[kMaxDevices];
-        const int64_t grid = std::min<int64_t>(ceil_div(a.units, kExThreads / 32),
-                                               int64_t(d->sms) * cached_occupancy(blocks, combine_kernel<CT, YT>));
-        combine_kernel<CT, YT><<<static_cast<unsigned>(grid), kExThreads, 0, stream>>>(a);
+        return launch_behind(combine_bwd_kernel<CT, YT>, grid, kExThreads, 0, 1, stream, a);
     }
-    return launched();
+    static std::atomic<int> blocks[kMaxDevices];
+    const int64_t grid = std::min<int64_t>(ceil_div(a.units, kExThreads / 32),
+                                           int64_t(d->sms) * cached_occupancy(blocks, combine_kernel<CT, YT>));
+    return launch_behind(combine_kernel<CT, YT>, grid, kExThreads, 0, 1, stream, a);
 }
 
 mx_status launch_combine_types(CombineArgs& a, mx_out_dtype ct, mx_out_dtype yt, bool backward, const DeviceInfo* d,
@@ -1294,14 +1292,13 @@ mx_status mx_route(const void* logits, mx_out_dtype dtype, int64_t T, int64_t E,
     a.scale = scale;
     const bool packed = a.bf16 && !bias && !(a.G > 1 && a.top2);
     switch (nv) {
-        case 1: launch_route<1>(a, packed, stream); break;
-        case 2: launch_route<2>(a, packed, stream); break;
-        case 4: launch_route<4>(a, packed, stream); break;
-        case 8: launch_route<8>(a, packed, stream); break;
-        case 16: launch_route<16>(a, packed, stream); break;
-        default: launch_route<32>(a, packed, stream); break;
+        case 1: return launch_route<1>(a, packed, stream);
+        case 2: return launch_route<2>(a, packed, stream);
+        case 4: return launch_route<4>(a, packed, stream);
+        case 8: return launch_route<8>(a, packed, stream);
+        case 16: return launch_route<16>(a, packed, stream);
+        default: return launch_route<32>(a, packed, stream);
     }
-    return launched();
 }
 
 mx_status mx_route_bwd(const float* d_weights, const void* logits, mx_out_dtype dtype, int64_t T, int64_t E, int64_t ld,
@@ -1334,14 +1331,10 @@ mx_status mx_route_bwd(const float* d_weights, const void* logits, mx_out_dtype 
     // Lanes per token: a whole warp where whole rows are read, otherwise one per slot.
     const bool dense = score == MX_SCORE_SOFTMAX && !renormalize;
     const int lanes = dense ? 32 : (topk <= 8 ? 8 : 16);
-    const unsigned grid = static_cast<unsigned>(ceil_div(T, kRouteThreads / lanes));
-    if (lanes == 8)
-        route_bwd_kernel<8><<<grid, kRouteThreads, 0, stream>>>(a);
-    else if (lanes == 16)
-        route_bwd_kernel<16><<<grid, kRouteThreads, 0, stream>>>(a);
-    else
-        route_bwd_kernel<32><<<grid, kRouteThreads, 0, stream>>>(a);
-    return launched();
+    const int64_t grid = ceil_div(T, kRouteThreads / lanes);
+    if (lanes == 8) return launch_behind(route_bwd_kernel<8>, grid, kRouteThreads, 0, 1, stream, a);
+    if (lanes == 16) return launch_behind(route_bwd_kernel<16>, grid, kRouteThreads, 0, 1, stream, a);
+    return launch_behind(route_bwd_kernel<32>, grid, kRouteThreads, 0, 1, stream, a);
 }
 
 int64_t mx_route_plan_workspace_bytes(int64_t slots, int64_t E) {
@@ -1372,37 +1365,10 @@ mx_status mx_route_plan(const int32_t* ids, int64_t slots, int64_t E, int32_t* r
     a.n = static_cast<int32_t>(slots);
     a.E = static_cast<int32_t>(E);
     a.chunk = static_cast<int32_t>(ceil_div(std::max<int64_t>(slots, 1), blocks));
-    if (blocks == 1) {
-        plan_kernel<<<1, kPlanThreads, plan_smem_bytes(static_cast<int>(E)), stream>>>(a);
-        return launched();
-    }
-    if (!cluster) {
-        counts_kernel<<<blocks, kPlanThreads, static_cast<size_t>(E + 1) * 4, stream>>>(a);
-        if (mx_status st = launched()) return st;
-    }
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(blocks, 1, 1);
-    cfg.blockDim = dim3(kPlanThreads, 1, 1);
-    cfg.dynamicSmemBytes = plan_smem_bytes(static_cast<int>(E));
-    cfg.stream = stream;
-    cudaLaunchAttribute attr[1];
-    if (cluster) {
-        attr[0].id = cudaLaunchAttributeClusterDimension;
-        attr[0].val.clusterDim.x = blocks;
-        attr[0].val.clusterDim.y = 1;
-        attr[0].val.clusterDim.z = 1;
-    } else {
-        // The kernel may start while the counting kernel still runs; it waits for it before it reads the counts.
-        attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-        attr[0].val.programmaticStreamSerializationAllowed = 1;
-    }
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    if (cudaLaunchKernelEx(&cfg, plan_kernel, a) != cudaSuccess) {
-        cudaGetLastError();
-        return MX_ERR_CUDA;
-    }
-    return launched();
+    const int smem = plan_smem_bytes(static_cast<int>(E));
+    if (!cluster)
+        if (mx_status st = launch_behind(counts_kernel, blocks, kPlanThreads, static_cast<size_t>(E + 1) * 4, 1, stream, a)) return st;
+    return launch_behind(plan_kernel, blocks, kPlanThreads, smem, cluster ? blocks : 1, stream, a);
 }
 
 int64_t mx_grouped_scale_bytes(int64_t rows, int64_t groups, int64_t kblocks) {
@@ -1449,11 +1415,8 @@ mx_status mx_dispatch_quantize(const void* x, int64_t T, int64_t K, int64_t ld_x
     a.vec32 = reinterpret_cast<uintptr_t>(x) % 32 == 0 && ld_x % 16 == 0 && reinterpret_cast<uintptr_t>(q) % 32 == 0;
     const bool fp4 = format == MX_FORMAT_E2M1;
     const int64_t grid = std::min<int64_t>(ceil_div(a.units, kExThreads / 32), int64_t(d->sms) * d->dispatch_blocks_per_sm[fp4]);
-    if (fp4)
-        dispatch_kernel<true><<<static_cast<unsigned>(grid), kExThreads, 0, stream>>>(a);
-    else
-        dispatch_kernel<false><<<static_cast<unsigned>(grid), kExThreads, 0, stream>>>(a);
-    return launched();
+    if (fp4) return launch_behind(dispatch_kernel<true>, grid, kExThreads, 0, 1, stream, a);
+    return launch_behind(dispatch_kernel<false>, grid, kExThreads, 0, 1, stream, a);
 }
 
 mx_status mx_combine(const void* c, mx_out_dtype c_dtype, int64_t rows, int64_t ld_c, const int32_t* slot_row,

@@ -251,13 +251,22 @@ __device__ __forceinline__ TileRef decode_qtile(const QuantArgs<NT>& a, int64_t 
 // the 128 x 128 tile: the block's amax, scale and 32 codes need no cross-lane exchange, and its 64
 // input bytes and 32 output bytes move with 256-bit accesses when the tensor is 32-byte aligned.
 
+template <bool COHERENT = false>
 __device__ __forceinline__ void load_block(const QTensor& T, int64_t row, int64_t col, bool ok, Block32& b) {
     if (!ok) {
         b.v[0] = b.v[1] = b.v[2] = b.v[3] = make_uint4(0, 0, 0, 0);
         return;
     }
     const uint16_t* p = T.x + row * T.ldx + col;
-    if (T.vec32) {
+    if constexpr (COHERENT) {
+        if (T.vec32) {
+            ld_once_v8(p, b.v[0], b.v[1]);
+            ld_once_v8(p + 16, b.v[2], b.v[3]);
+        } else {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) b.v[j] = reinterpret_cast<const uint4*>(p)[j];
+        }
+    } else if (T.vec32) {
         ld_stream_v8(p, b.v[0], b.v[1]);
         ld_stream_v8(p + 16, b.v[2], b.v[3]);
     } else {

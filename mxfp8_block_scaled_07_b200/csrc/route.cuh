@@ -77,7 +77,7 @@ __device__ __forceinline__ void route_load(const ELT* base, int E, int lane, boo
     if (vec && e0 < E) {          // E is a multiple of NV here: a lane is all in or all out
 #pragma unroll
         for (int c = 0; c < NV / kPer; ++c)
-            *reinterpret_cast<V*>(&raw[c * kPer]) = __ldg(reinterpret_cast<const V*>(base + e0) + c);
+            *reinterpret_cast<V*>(&raw[c * kPer]) = reinterpret_cast<const V*>(base + e0)[c];
     }
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
@@ -427,6 +427,7 @@ __device__ __forceinline__ void route_load_row(const RouteArgs& a, int64_t t, in
 // 28.8 us with four, 23.1 us with one).
 template <int NV, int LPT, bool PACKED>
 __global__ void __launch_bounds__(kRouteThreads) route_kernel(const __grid_constant__ RouteArgs a) {
+    grid_wait();
     constexpr int kTokens = 32 / LPT;
     static_assert(PACKED || kTokens == 1, "the general form takes one token per warp");
     const int lane = threadIdx.x & 31;
@@ -606,6 +607,7 @@ __global__ void __launch_bounds__(kRouteThreads) route_kernel(const __grid_const
 // the sum of its parts in slot order.
 template <int LPT>
 __global__ void __launch_bounds__(kRouteThreads) route_bwd_kernel(const __grid_constant__ RouteArgs a) {
+    grid_wait();
     constexpr int kTokens = 32 / LPT;
     __shared__ __align__(16) float rows[kRouteThreads / 32][kRouteMaxExperts];
     const int lane = threadIdx.x & 31;
@@ -631,13 +633,13 @@ __global__ void __launch_bounds__(kRouteThreads) route_bwd_kernel(const __grid_c
         const int e0 = c * 128 + lane * 4;
         if (a.vec && e0 < a.E) {
             if (a.bf16) {
-                const uint2 r = __ldg(reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(a.x) + t * a.ld + e0));
+                const uint2 r = *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(a.x) + t * a.ld + e0);
                 v[0] = __uint_as_float(r.x << 16);
                 v[1] = __uint_as_float(r.x & 0xFFFF0000u);
                 v[2] = __uint_as_float(r.y << 16);
                 v[3] = __uint_as_float(r.y & 0xFFFF0000u);
             } else {
-                const float4 r = __ldg(reinterpret_cast<const float4*>(static_cast<const float*>(a.x) + t * a.ld + e0));
+                const float4 r = *reinterpret_cast<const float4*>(static_cast<const float*>(a.x) + t * a.ld + e0);
                 v[0] = r.x; v[1] = r.y; v[2] = r.z; v[3] = r.w;
             }
 #pragma unroll
@@ -785,7 +787,7 @@ __device__ __forceinline__ int plan_bucket(const PlanArgs& a, int i) {
 __global__ void __launch_bounds__(kPlanThreads) counts_kernel(const __grid_constant__ PlanArgs a) {
     extern __shared__ int32_t plan_smem[];
     const int B = a.E + 1;
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    grid_wait();
     for (int e = threadIdx.x; e < B; e += kPlanThreads) plan_smem[e] = 0;
     __syncthreads();
     const int64_t lo = static_cast<int64_t>(blockIdx.x) * a.chunk;
@@ -802,6 +804,7 @@ __global__ void __launch_bounds__(kPlanThreads) counts_kernel(const __grid_const
 __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const __grid_constant__ PlanArgs a) {
     extern __shared__ int32_t plan_smem[];
     const int B = a.E + 1;
+    grid_wait();
     int32_t* wcount = plan_smem;
     int32_t* base = wcount + kPlanWarps * B;      // slots of the bucket in earlier blocks, then its first row here
     int32_t* total = base + B;
@@ -846,8 +849,6 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const __grid_constan
         }
     }
     if (a.block_counts) {
-        // Launched before the counting kernel has ended (programmatic launch); what stands above needs the ids only.
-        asm volatile("griddepcontrol.wait;" ::: "memory");
         // Earlier blocks' and all blocks' counts of every bucket; a bucket's blocks are split over threads.
         const int blocks = gridDim.x, parts = kPlanThreads / B > 1 ? kPlanThreads / B : 1;
         for (int e = tid; e < B * parts; e += kPlanThreads) {

@@ -265,3 +265,89 @@ def test_layer_replays_in_a_cuda_graph_and_on_another_stream():
         side.synchronize()
         for u, v in zip(got, other):
             assert torch.equal(u, v)
+
+
+class Layer:
+    """An MXFP4 expert layer whose every step writes into buffers of its own that each pass uses again."""
+
+    def __init__(self, T, k, E, H, N, seed):
+        g = torch.Generator().manual_seed(seed)
+        self.k, self.E = k, E
+        self.inputs = [(torch.randn((T, H), generator=g).to(torch.bfloat16).cuda(),
+                        torch.randn((T, E), generator=g).cuda(), torch.randn((E * N, H), generator=g).to(torch.bfloat16).cuda())
+                       for _ in range(3)]
+        self.x, self.logits, self.w = (torch.empty_like(v) for v in self.inputs[0])
+        self.qw = mx.quantize_fp4(self.w)
+        self.wq = self.qw[0].view(E, N, H // 2)
+        self.choice = mx.route(self.logits.zero_(), k)
+        self.part = mx.route_plan(self.choice[0], E)
+        self.q = mx.dispatch_quantize(self.x.zero_(), self.part[1], self.part[0], "mxfp4")
+        self.rows = torch.empty((T * k, N), device="cuda")
+        self.y = torch.empty((T, N), dtype=torch.bfloat16, device="cuda")
+        self.grads = (torch.empty_like(self.rows), torch.empty_like(self.choice[1]))
+        self.d_logits = torch.empty_like(self.logits)
+        self.dense = torch.empty((min(T, 48), E * N), device="cuda")
+        self.back = torch.empty_like(self.x[:len(self.dense)])
+
+    def steps(self, i):
+        """The calls of pass i, in order."""
+        for a, b in zip((self.x, self.logits, self.w), self.inputs[i % len(self.inputs)]):
+            yield lambda a=a, b=b: a.copy_(b)
+        yield lambda: mx.quantize_fp4(self.w, out=self.qw)
+        yield lambda: mx.route(self.logits, self.k, out=self.choice)
+        yield lambda: mx.route_plan(self.choice[0], self.E, out=self.part)
+        yield lambda: mx.dispatch_quantize(self.x, self.part[1], self.part[0], "mxfp4", out=self.q)
+        yield lambda: mx.grouped_gemm_fp4(self.q[0], self.q[1], self.wq, self.qw[1], self.part[0], out=self.rows)
+        yield lambda: mx.combine(self.rows, self.part[1], self.choice[1], out=self.y)
+        yield lambda: mx.combine_backward(self.y, self.rows, self.part[1], self.choice[1], out=self.grads)
+        yield lambda: mx.route_backward(self.grads[1], self.logits, self.choice[0], out=self.d_logits)
+        qx = mx.quantize_fp4(self.x[:len(self.dense)])
+        yield lambda: mx.gemm_fp4(qx[0], qx[1], self.qw[0], self.qw[1], out=self.dense)
+        yield lambda: mx.dequantize_fp4(qx[0], qx[1], out=self.back)
+
+    def answers(self):
+        return [t.clone() for t in (*self.choice, *self.part, *self.q, self.rows, self.y, *self.grads, self.d_logits, self.dense, self.back)]
+
+
+# T * k: a plan of one block, of a cluster, with a counting kernel; grouped products of few and of many rows per expert.
+@pytest.mark.parametrize("T,k,E,H,N", [(24, 2, 64, 256, 128), (700, 8, 16, 512, 256), (9000, 4, 16, 128, 256)])
+def test_calls_back_to_back_wait_for_one_another(T, k, E, H, N):
+    """Kernels become resident before the ones in front of them have ended: passes without a pause, over the same buffers and
+    with changing inputs, give what passes give that wait after every call; so does a captured pass, also where a
+    second stream joins in its middle."""
+    layer = Layer(T, k, E, H, N, T)
+    want = []
+    for i in range(3):
+        for step in layer.steps(i):
+            step()
+            torch.cuda.synchronize()
+        want.append(layer.answers())
+    got = []
+    for i in range(24):
+        for step in layer.steps(i):
+            step()
+        got.append(layer.answers())
+    for i, answers in enumerate(got):
+        for a, b in zip(answers, want[i % 3]):
+            assert torch.equal(a, b)
+
+    side = torch.cuda.Stream()
+    graph = torch.cuda.CUDAGraph()
+    source = [torch.empty_like(v) for v in layer.inputs[0]]
+    layer.inputs.append(tuple(source))
+    with torch.cuda.graph(graph):
+        for n, step in enumerate(layer.steps(3)):
+            if n % 3 == 2:                       # every third call on another stream
+                side.wait_stream(torch.cuda.current_stream())
+                with torch.cuda.stream(side):
+                    step()
+                torch.cuda.current_stream().wait_stream(side)
+            else:
+                step()
+    layer.inputs.pop()
+    for i in range(6):
+        for a, b in zip(source, layer.inputs[i % 3]):
+            a.copy_(b)
+        graph.replay()
+        for a, b in zip(layer.answers(), want[i % 3]):
+            assert torch.equal(a, b)
