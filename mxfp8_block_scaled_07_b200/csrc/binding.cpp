@@ -8,6 +8,8 @@
 #include <Python.h>
 
 #include <ATen/ATen.h>
+#include <ATen/EmptyTensor.h>
+#include <c10/cuda/CUDACachingAllocator.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/Exceptions.h>
@@ -86,8 +88,11 @@ void* packed(const at::Tensor& t, at::ScalarType type, int64_t numel, at::Device
     return t.data_ptr();
 }
 
-at::Tensor fresh(at::IntArrayRef sizes, at::ScalarType type, at::Device dev) {
-    return at::empty(sizes, at::TensorOptions().dtype(type).device(dev));
+// An uninitialized tensor on the current device (Place has made the tensors' device current), from the caching allocator as
+// at::empty gives it, without the dispatcher.
+at::Tensor fresh(at::IntArrayRef sizes, at::ScalarType type) {
+    return at::detail::empty_generic(sizes, c10::cuda::CUDACachingAllocator::get(), c10::DispatchKeySet(c10::DispatchKey::CUDA), type,
+                                     std::nullopt);
 }
 
 template <class T>
@@ -147,8 +152,8 @@ PyObject* route(Args a) {
     at::Tensor ids, weights;
     PyObject *oi = nullptr, *ow = nullptr;
     if (a[9] == Py_None) {
-        ids = fresh({x.m, topk}, at::kInt, dev);
-        weights = fresh({x.m, topk}, at::kFloat, dev);
+        ids = fresh({x.m, topk}, at::kInt);
+        weights = fresh({x.m, topk}, at::kFloat);
     } else {
         oi = out_item(a[9], 0, 2, "route: out (ids, weights)");
         ow = out_item(a[9], 1, 2, "route: out (ids, weights)");
@@ -176,7 +181,7 @@ PyObject* route_backward(Args a) {
     const void* pd = packed(dw, at::kFloat, x.m * topk, dev, "route_backward: d_weights must be fp32 [T, topk]");
     const void* pi = packed(ids, at::kInt, x.m * topk, dev, "route_backward: ids must be int32 [T, topk]");
     const Place place(logits);
-    const at::Tensor out = a[6] == Py_None ? fresh({x.m, x.n}, logits.scalar_type(), dev) : tensor(a[6], "route_backward: out");
+    const at::Tensor out = a[6] == Py_None ? fresh({x.m, x.n}, logits.scalar_type()) : tensor(a[6], "route_backward: out");
     const Matrix o = matrix(out, code_of(logits) == MX_OUT_BF16 ? kBf16 : kF32, x.m, x.n, dev, "route_backward: out must be like logits");
     check(mx_route_bwd(static_cast<const float*>(pd), x.p, code_of(logits), x.m, x.n, x.ld, static_cast<const int32_t*>(pi),
                        static_cast<int>(score), topk, renorm, scale, o.p, o.ld, place.stream),
@@ -196,16 +201,16 @@ PyObject* route_plan(Args a) {
     at::Tensor off, slot_row, counts, ws;
     PyObject* o[3] = {nullptr, nullptr, nullptr};
     if (a[2] == Py_None) {
-        off = fresh({experts + 1}, at::kInt, dev);
-        slot_row = fresh(ids.sizes(), at::kInt, dev);
-        counts = fresh({experts}, at::kInt, dev);
+        off = fresh({experts + 1}, at::kInt);
+        slot_row = fresh(ids.sizes(), at::kInt);
+        counts = fresh({experts}, at::kInt);
     } else {
         for (int i = 0; i < 3; ++i) o[i] = out_item(a[2], i, 3, "route_plan: out (row_offsets, slot_row, counts)");
         off = tensor(o[0], "route_plan: row_offsets");
         slot_row = tensor(o[1], "route_plan: slot_row");
         counts = tensor(o[2], "route_plan: counts");
     }
-    if (bytes) ws = fresh({bytes}, at::kByte, dev);
+    if (bytes) ws = fresh({bytes}, at::kByte);
     void* po = packed(off, at::kInt, experts + 1, dev, "route_plan: row_offsets must be int32 [experts + 1]");
     void* ps = packed(slot_row, at::kInt, n, dev, "route_plan: slot_row must be int32 like ids");
     void* pc = packed(counts, at::kInt, experts, dev, "route_plan: counts must be int32 [experts]");
@@ -231,8 +236,8 @@ PyObject* dispatch_quantize(Args a) {
     at::Tensor q, s;
     PyObject *oq = nullptr, *os = nullptr;
     if (a[4] == Py_None) {
-        q = fresh({rows, width}, at::kByte, dev);
-        s = fresh({size}, at::kByte, dev);
+        q = fresh({rows, width}, at::kByte);
+        s = fresh({size}, at::kByte);
     } else {
         oq = out_item(a[4], 0, 2, "dispatch_quantize: out (q, s)");
         os = out_item(a[4], 1, 2, "dispatch_quantize: out (q, s)");
@@ -258,7 +263,7 @@ PyObject* combine(Args a) {
     const at::Tensor* w = optional_tensor(a[2], "combine: weights");
     const void* pw = w ? packed(*w, at::kFloat, T * topk, dev, "combine: weights must be fp32 [T, topk]") : nullptr;
     const Place place(rows);
-    const at::Tensor out = a[4] == Py_None ? fresh({T, c.n}, code < 0 ? rows.scalar_type() : type_of(code), dev) : tensor(a[4], "combine: out");
+    const at::Tensor out = a[4] == Py_None ? fresh({T, c.n}, code < 0 ? rows.scalar_type() : type_of(code)) : tensor(a[4], "combine: out");
     const Matrix y = matrix(out, kF32 | kBf16, T, c.n, dev, "combine: out must be [T, N], fp32 or BF16");
     check(mx_combine(c.p, code_of(rows), c.m, c.ld, static_cast<const int32_t*>(ps), static_cast<const float*>(pw), T, topk, c.n, y.p,
                      code_of(out), y.ld, place.stream),
@@ -284,10 +289,10 @@ PyObject* combine_backward(Args a) {
     PyObject *orow = nullptr, *ow = nullptr;
     bool weights_out = need_weights;
     if (a[5] == Py_None) {
-        d_rows = fresh({c.m, c.n}, rows.scalar_type(), dev);
+        d_rows = fresh({c.m, c.n}, rows.scalar_type());
         // Every row of a plan's partition is written; rows that no slot names stay as they are, so they start as 0.
         if (c.m != T * topk) d_rows.zero_();
-        if (need_weights) d_w = fresh({T, topk}, at::kFloat, dev);
+        if (need_weights) d_w = fresh({T, topk}, at::kFloat);
     } else {
         orow = out_item(a[5], 0, 2, "combine_backward: out (d_rows, d_weights)");
         ow = out_item(a[5], 1, 2, "combine_backward: out (d_rows, d_weights)");
@@ -324,7 +329,7 @@ PyObject* quantize_fp4(Args a) {
             t[i] = tensor(out_item(a[2], i, 4, "quantize_fp4: out (q_row, s_row, q_col, s_col)"), "quantize_fp4: out");
             p[i] = packed(t[i], at::kByte, bytes[i], dev, "quantize_fp4: out (q_row, s_row, q_col, s_col)");
         } else {
-            t[i] = (i & 1) && swz ? fresh({bytes[i]}, at::kByte, dev) : fresh({shape[i][0], shape[i][1]}, at::kByte, dev);
+            t[i] = (i & 1) && swz ? fresh({bytes[i]}, at::kByte) : fresh({shape[i][0], shape[i][1]}, at::kByte);
             p[i] = t[i].data_ptr();
         }
     }
@@ -347,7 +352,7 @@ PyObject* dequantize_fp4(Args a) {
     const void* pq = packed(q, at::kByte, M * K / 2, dev, "dequantize_fp4: q must be contiguous uint8");
     const void* ps = packed(s, at::kByte, swz ? layout_bytes(M, K / 32) : M * (K / 32), dev, "dequantize_fp4: s");
     const Place place(q);
-    const at::Tensor out = a[3] == Py_None ? fresh({M, K}, at::kBFloat16, dev) : tensor(a[3], "dequantize_fp4: out");
+    const at::Tensor out = a[3] == Py_None ? fresh({M, K}, at::kBFloat16) : tensor(a[3], "dequantize_fp4: out");
     const Matrix o = matrix(out, kBf16, M, K, dev, "dequantize_fp4: out must be BF16 [M, K]");
     check(mx_dequantize_fp4(static_cast<const uint8_t*>(pq), static_cast<const uint8_t*>(ps), M, K, swz, o.p, o.ld, place.stream),
           "mx_dequantize_fp4");
@@ -366,7 +371,7 @@ PyObject* gemm_fp4(Args a) {
     const void* psa = packed(sa, at::kByte, layout_bytes(M, K / 32), dev, "gemm_fp4: sa_swz");
     const void* psb = packed(sb, at::kByte, layout_bytes(N, K / 32), dev, "gemm_fp4: sb_swz");
     const Place place(qa);
-    const at::Tensor out = a[5] == Py_None ? fresh({M, N}, type_of(integer(a[4])), dev) : tensor(a[5], "gemm_fp4: out");
+    const at::Tensor out = a[5] == Py_None ? fresh({M, N}, type_of(integer(a[4]))) : tensor(a[5], "gemm_fp4: out");
     const Matrix c = matrix(out, kF32 | kBf16, M, N, dev, "gemm_fp4: out must be [M, N], fp32 or BF16");
     check(mx_gemm_fp4(static_cast<const uint8_t*>(pa), static_cast<const uint8_t*>(psa), static_cast<const uint8_t*>(pb),
                       static_cast<const uint8_t*>(psb), M, N, K, c.p, c.ld, code_of(out), place.stream),
@@ -390,7 +395,7 @@ PyObject* grouped_gemm_fp4(Args a) {
     const void* psb = packed(sb, at::kByte, G * layout_bytes(N, K / 32), dev, "grouped_gemm_fp4: sb_swz");
     const void* po = packed(off, at::kInt, G + 1, dev, "grouped_gemm_fp4: row_offsets must be int32 [G + 1]");
     const Place place(qa);
-    const at::Tensor out = a[6] == Py_None ? fresh({rows, N}, type_of(integer(a[5])), dev) : tensor(a[6], "grouped_gemm_fp4: out");
+    const at::Tensor out = a[6] == Py_None ? fresh({rows, N}, type_of(integer(a[5]))) : tensor(a[6], "grouped_gemm_fp4: out");
     const Matrix c = matrix(out, kF32 | kBf16, rows, N, dev, "grouped_gemm_fp4: out must be [rows, N], fp32 or BF16");
     check(mx_grouped_gemm_fp4(static_cast<const uint8_t*>(pa), static_cast<const uint8_t*>(psa), static_cast<const uint8_t*>(pb),
                               static_cast<const uint8_t*>(psb), static_cast<const int32_t*>(po), G, rows, N, K, c.p, c.ld,
