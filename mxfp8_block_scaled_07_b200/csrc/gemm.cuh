@@ -216,7 +216,8 @@ __device__ __forceinline__ Tile decode_tile_pair(int t, int rank, const GemmArgs
 // load/store path, not TMA: TMA stores share the SM's TMA unit with the operand loads and were
 // measured to slow those down. Barrier addresses are shared::cluster addresses.
 // ACC1: first column of accumulator 1; columns [ACC1, 256) are shared.
-// DIRECT: where a.direct is set, each lane writes its row's pieces with 32-byte stores from registers.
+// DIRECT (MXFP4): where a.direct is set, each lane writes its row's pieces with 32-byte stores from registers, and BF16 rows
+// without 16-byte alignment leave word by word.
 template <bool GROUPED, uint32_t ACC1 = kAcc1Col, bool DIRECT = false>
 __device__ __forceinline__ void epilogue_tile(const GemmArgs& a, const Tile& T, uint32_t tmem_base, bool acc1,
                                               uint8_t* stage, uint32_t ovl_free_addr, uint32_t acc_empty_addr,
@@ -261,6 +262,41 @@ __device__ __forceinline__ void epilogue_tile(const GemmArgs& a, const Tile& T, 
             st_shared_v4(row + ((static_cast<uint32_t>(i) ^ swz) << 4), p[4 * i], p[4 * i + 1], p[4 * i + 2],
                          p[4 * i + 3]);
         __syncwarp();
+        if (DIRECT && a.out_bf16 && !a.vec_store) {
+            // BF16 rows that are not 16-byte aligned: a row per instruction, a word per lane; a row that begins between two
+            // words leaves as its first element, 31 words of neighbouring elements and its last one. (Eight elements one
+            // by one per lane, as fp32 below, take twice the instructions: 1706 x 9299 x 64 in MXFP4 72 us, this 30 us. Two rows
+            // at a time: the code stands here eight times, and with eight rows it cost the other paths 10%.)
+            const int n = min(64, a.N - col0);
+            uint8_t* dst = static_cast<uint8_t*>(a.c) + (row0 * a.ldc + col0) * 2;
+            const int64_t ld = a.ldc * 2;
+#pragma unroll 1
+            for (int r0 = 0; r0 < warp_rows; r0 += 2) {
+                uint32_t w[2];
+#pragma unroll
+                for (int i = 0; i < 2; ++i)              // the box has all 32 rows
+                    w[i] = ld_shared_u32(box + (r0 + i) * 128 + (((static_cast<uint32_t>(lane) >> 2) ^ ((r0 + i) & 7)) << 4) + (lane & 3) * 4);
+#pragma unroll
+                for (int i = 0; i < 2; ++i, dst += ld) {
+                    if (r0 + i >= warp_rows) break;
+                    if ((reinterpret_cast<uintptr_t>(dst) & 2u) == 0) {
+                        if (2 * lane + 1 < n)
+                            *reinterpret_cast<uint32_t*>(dst + 4 * lane) = w[i];
+                        else if (2 * lane < n)
+                            *reinterpret_cast<uint16_t*>(dst + 4 * lane) = static_cast<uint16_t>(w[i]);
+                    } else {
+                        const uint32_t up = __shfl_down_sync(0xFFFFFFFFu, w[i], 1);
+                        if (lane == 0) *reinterpret_cast<uint16_t*>(dst) = static_cast<uint16_t>(w[i]);
+                        if (2 * lane + 2 < n)            // never the last lane: n <= 64
+                            *reinterpret_cast<uint32_t*>(dst + 4 * lane + 2) = __byte_perm(w[i], up, 0x5432);
+                        else if (2 * lane + 1 < n)
+                            *reinterpret_cast<uint16_t*>(dst + 4 * lane + 2) = static_cast<uint16_t>(w[i] >> 16);
+                    }
+                }
+            }
+            __syncwarp();
+            return;
+        }
         const int c = lane & 7;                          // this lane's 16-byte chunk of each row
         const int gc = col0 + c * epc;
         const int ncols = min(epc, a.N - gc);

@@ -328,3 +328,29 @@ def test_expired_waits_end_the_product_cleanly(M, N, K):
     assert bits == 1
     test_gemm(257, 130, 416, torch.float32)
     test_gemm(16, 1000, 2048, torch.float32)
+
+
+@pytest.mark.parametrize("fmt", ["mxfp4", "mxfp8"])
+@pytest.mark.parametrize("out_dtype", [torch.float32, torch.bfloat16])
+def test_output_rows_at_every_alignment(fmt, out_dtype):
+    """Offsets and row strides that leave rows on every element boundary give the same values as aligned ones, and nothing
+    beside them is written."""
+    M, N, K = 140, 331, 160
+    a, b = (synth.normal_bf16((r, K), seed=r).cuda() for r in (M, N))
+    if fmt == "mxfp4":
+        args, f = (*mx.quantize_fp4(a)[:2], *mx.quantize_fp4(b)[:2]), mx.gemm_fp4
+    else:
+        args, f = (*mx.quantize(a)[:2], *mx.quantize(b)[:2]), mx.gemm
+    want = torch.empty((M, 352), dtype=out_dtype, device="cuda")[:, :N]
+    f(*args, out=want)
+    for n in (N, 320, 257, 65, 64, 1):
+        if fmt == "mxfp4":
+            part = (*args[:2], *mx.quantize_fp4(b[:n].contiguous())[:2])
+        else:
+            part = (*args[:2], *mx.quantize(b[:n].contiguous())[:2])
+        for offset, ld in ((0, 331), (1, 331), (1, 332), (2, 333), (3, 334), (5, 336), (7, 335), (8, 352)):
+            buf = torch.full((offset + M * ld + 8,), -7.0, dtype=out_dtype, device="cuda")
+            f(*part, out=buf.as_strided((M, n), (ld, 1), offset))
+            expect = torch.full_like(buf, -7.0)
+            expect.as_strided((M, n), (ld, 1), offset).copy_(want[:, :n])
+            assert torch.equal(buf, expect), (n, offset, ld)
