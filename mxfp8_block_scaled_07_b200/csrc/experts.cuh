@@ -378,26 +378,27 @@ __global__ void __launch_bounds__(kExThreads, 3) combine_kernel(const __grid_con
     }
 }
 
-// One block per token at a time: warp w takes the row pieces w, w + 8, ...; per piece dy and the token's rows
-// are loaded together, then the rows' gradients are written. Each warp reduces its 8 dot products with 9
+// W warps per token, 8 / W tokens per block at a time (W: as many as a row has pieces, at most 8): warp w of a token
+// takes the row pieces w, w + W, ...; per piece dy and the token's rows are loaded together, then the rows' gradients are written. Each warp reduces its 8 dot products with 9
 // shuffles (halving the values with the lanes) and joins them through shared memory in warp order, so dw does
-// not depend on timing. The next token's slots are loaded before this token's arithmetic. 20 480 tokens x 8 rows
+// not depend on timing. (A whole block for rows of one piece: 12 462 tokens x 1 x 120 took 66 us.) The next token's slots are loaded before this token's arithmetic. 20 480 tokens x 8 rows
 // x 2048 BF16: 263 us, 5.4 TB/s, nearly half of it writes (four slots per pass, two barriers each: 609 us). A form
 // without tests for partial pieces, for rows of whole ones, has two thirds of the instructions and took 327 us at two,
 // three and four blocks per SM, with plain or streaming stores, and with the dot products before or after them.
-template <class CT, class YT>
+template <class CT, class YT, int W>
 __global__ void __launch_bounds__(kExThreads, 3) combine_bwd_kernel(const __grid_constant__ CombineArgs a) {
     grid_wait();
-    constexpr int P = 16 / static_cast<int>(sizeof(CT));
+    constexpr int P = 16 / static_cast<int>(sizeof(CT)), kTokens = kExThreads / 32 / W;
     __shared__ float part[2][kExThreads / 32][kCombineSlots];
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int lane = threadIdx.x & 31, warp = (threadIdx.x >> 5) % W, mate = (threadIdx.x >> 5) / W;   // token of the block
     const CT* c = static_cast<const CT*>(a.c);
-    int64_t t = blockIdx.x;
-    if (t >= a.T) return;
+    const int64_t step = static_cast<int64_t>(gridDim.x) * kTokens;
+    int64_t t = static_cast<int64_t>(blockIdx.x) * kTokens + mate;
+    if (t >= a.T) return;                       // all of the token's warps
     int row, flip = 0;
     float w;
     load_slot(a, t, 0, lane, row, w);
-    for (; t < a.T; t += gridDim.x) {
+    for (; t < a.T; t += step) {
         const YT* dy = static_cast<const YT*>(a.dy) + t * a.lddy;
         for (int j0 = 0; j0 < a.k; j0 += kCombineSlots, flip ^= 1) {
             const int mine = row >= 0 ? row : ~row;                      // a padding row's gradient is 0
@@ -406,12 +407,12 @@ __global__ void __launch_bounds__(kExThreads, 3) combine_bwd_kernel(const __grid
             const float wj = w;
             if (j0 + kCombineSlots < a.k)
                 load_slot(a, t, j0 + kCombineSlots, lane, row, w);
-            else if (t + gridDim.x < a.T)
-                load_slot(a, t + gridDim.x, 0, lane, row, w);
+            else if (t + step < a.T)
+                load_slot(a, t + step, 0, lane, row, w);
             float dot[kCombineSlots];
 #pragma unroll
             for (int j = 0; j < kCombineSlots; ++j) dot[j] = 0.0f;
-            for (int64_t c0 = static_cast<int64_t>(warp) * (32 * P); c0 < a.N; c0 += kExThreads * P) {
+            for (int64_t c0 = static_cast<int64_t>(warp) * (32 * P); c0 < a.N; c0 += W * 32 * P) {
                 uint4 v[kCombineSlots];
                 if (a.dw) {
 #pragma unroll
@@ -462,13 +463,21 @@ __global__ void __launch_bounds__(kExThreads, 3) combine_bwd_kernel(const __grid
                 dot[0] += __shfl_xor_sync(kFullMask, dot[0], 2);
                 dot[0] += __shfl_xor_sync(kFullMask, dot[0], 1);
                 // Value index: bits 4, 3, 2 of the lane.
-                if ((lane & 3) == 0) part[flip][warp][lane >> 2] = dot[0];
-                __syncthreads();
-                if (threadIdx.x < kCombineSlots && j0 + static_cast<int>(threadIdx.x) < a.k) {
-                    float s = 0.0f;
+                if constexpr (W == 1) {
+                    if ((lane & 3) == 0 && j0 + (lane >> 2) < a.k) a.dw[t * a.k + j0 + (lane >> 2)] = dot[0];
+                } else {
+                    if ((lane & 3) == 0) part[flip][mate * W + warp][lane >> 2] = dot[0];
+                    // The token's warps alone: tokens of a block do not wait for one another.
+                    if constexpr (W == kExThreads / 32)
+                        __syncthreads();
+                    else
+                        asm volatile("bar.sync %0, %1;" ::"r"(1 + mate), "n"(32 * W) : "memory");
+                    if (warp == 0 && lane < kCombineSlots && j0 + lane < a.k) {
+                        float s = 0.0f;
 #pragma unroll
-                    for (int v = 0; v < kExThreads / 32; ++v) s += part[flip][v][threadIdx.x];
-                    a.dw[t * a.k + j0 + threadIdx.x] = s;
+                        for (int v = 0; v < W; ++v) s += part[flip][mate * W + v][lane];
+                        a.dw[t * a.k + j0 + lane] = s;
+                    }
                 }
             }
         }

@@ -1219,6 +1219,15 @@ int plan_blocks(int64_t n, bool* cluster) {
     return *cluster ? blocks : static_cast<int>(std::min<int64_t>(kPlanMaxBlocks, ceil_div(n, kPlanThreads)));
 }
 
+// The gradient of combine with W warps per token.
+template <class CT, class YT, int W>
+mx_status launch_combine_bwd(const CombineArgs& a, const DeviceInfo* d, mx_stream stream) {
+    static std::atomic<int> blocks[kMaxDevices];
+    const int64_t grid = std::min<int64_t>(ceil_div(a.T, kExThreads / 32 / W),
+                                           int64_t(d->sms) * cached_occupancy(blocks, combine_bwd_kernel<CT, YT, W>));
+    return launch_behind(combine_bwd_kernel<CT, YT, W>, grid, kExThreads, 0, 1, stream, a);
+}
+
 template <class CT, class YT>
 mx_status launch_combine(CombineArgs& a, bool backward, const DeviceInfo* d, mx_stream stream) {
     const int64_t piece = 512 / static_cast<int64_t>(sizeof(CT));
@@ -1229,9 +1238,10 @@ mx_status launch_combine(CombineArgs& a, bool backward, const DeviceInfo* d, mx_
     a.chunks = FastDiv::of(chunks);
     a.units = static_cast<uint32_t>(a.T * chunks);
     if (backward) {
-        static std::atomic<int> blocks[kMaxDevices];
-        const int64_t grid = std::min<int64_t>(a.T, int64_t(d->sms) * cached_occupancy(blocks, combine_bwd_kernel<CT, YT>));
-        return launch_behind(combine_bwd_kernel<CT, YT>, grid, kExThreads, 0, 1, stream, a);
+        if (chunks <= 1) return launch_combine_bwd<CT, YT, 1>(a, d, stream);
+        if (chunks <= 2) return launch_combine_bwd<CT, YT, 2>(a, d, stream);
+        if (chunks <= 4) return launch_combine_bwd<CT, YT, 4>(a, d, stream);
+        return launch_combine_bwd<CT, YT, 8>(a, d, stream);
     }
     static std::atomic<int> blocks[kMaxDevices];
     const int64_t grid = std::min<int64_t>(ceil_div(a.units, kExThreads / 32),

@@ -351,3 +351,10 @@ def test_calls_back_to_back_wait_for_one_another(T, k, E, H, N):
         graph.replay()
         for a, b in zip(layer.answers(), want[i % 3]):
             assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("ct,yt", [(torch.float32, torch.bfloat16), (torch.bfloat16, torch.float32)])
+@pytest.mark.parametrize("T,k,E,N", [(700, 1, 3, 96), (333, 9, 40, 200), (501, 2, 7, 500), (258, 8, 16, 1000), (129, 3, 5, 1024)])
+def test_combine_and_gradients_of_narrow_rows(T, k, E, N, ct, yt):
+    """Several tokens per block: rows of one, two, four and more pieces, tokens that do not fill the last block."""
+    test_combine_and_gradients(T, k, E, N, ct, yt)
