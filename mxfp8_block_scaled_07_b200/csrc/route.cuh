@@ -166,7 +166,8 @@ __device__ __forceinline__ U group_rank(U m, U c, bool top2) {
 // Ranks the groups and clears the keys of all but the topg best. `last` and `next`: the ranks of the worst group
 // kept and the best one left (0 if none). Where groups are whole lanes (a power of two of them), a group's two
 // largest keys are merged over its lanes by shuffles; otherwise the keys go through a row of shared memory (8 bytes an
-// expert and warp) and lane g reads group g's. Every group then counts the groups before it with G independent
+// expert and warp, for fp32 keys too: while one warp ranks fp64 keys its neighbours may still be at fp32 ones, and nothing
+// orders warps) and lane g reads group g's. Every group then counts the groups before it with G independent
 // shuffles. (Walking the groups with a warp maximum each took 4 us more for 5201 tokens of 10 groups of 10.)
 extern __shared__ uint64_t route_smem[];
 
@@ -193,7 +194,7 @@ __device__ __forceinline__ void route_groups(const RouteArgs& a, U (&key)[NV], i
         rank = group_rank(m, c, top2);
         mine = lane / L;
     } else {
-        U* row = reinterpret_cast<U*>(route_smem) + (threadIdx.x >> 5) * a.E;
+        U* row = reinterpret_cast<U*>(route_smem + (threadIdx.x >> 5) * a.E);
 #pragma unroll
         for (int i = 0; i < NV; ++i)
             if (lane * NV + i < a.E) row[lane * NV + i] = key[i];
