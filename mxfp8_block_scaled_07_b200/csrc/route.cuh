@@ -538,7 +538,7 @@ __global__ void __launch_bounds__(kRouteThreads) route_kernel(const __grid_const
             }
             route_select<NV, true>(key, a.k, lane, id, slot_key, left, left_key);
             // Lane k takes the best expert left out. Slot j against slot j + 1, the last one against lane k. Two
-            // experts with the same logit and the same bias have the same score in any precision.
+            // experts with the same logit and the same bias, twins, have the same score in any precision.
             if (lane == a.k) {
                 id = left;
                 slot_key = left_key;
@@ -550,19 +550,31 @@ __global__ void __launch_bounds__(kRouteThreads) route_kernel(const __grid_const
             }
             const uint32_t k2 = __shfl_down_sync(kFullMask, slot_key, 1);
             const float x2 = __shfl_down_sync(kFullMask, x, 1), b2 = __shfl_down_sync(kFullMask, bj, 1);
-            if (lane < a.k && slot_key != 0 && k2 != 0 && !(x == x2 && bj == b2))
-                near = too_near(value_of(slot_key), value_of(k2), tol);
-            if (__any_sync(kFullMask, near || near_group)) {
-                // Any other expert near the last chosen one (or a choice of groups in doubt): all of it in fp64.
+            bool twins = false;              // the last chosen and the best left out are: others may stand right behind them
+            if (lane < a.k && slot_key != 0 && k2 != 0) {
+                if (x == x2 && bj == b2)
+                    twins = lane == a.k - 1;
+                else
+                    near = too_near(value_of(slot_key), value_of(k2), tol);
+            }
+            if (__any_sync(kFullMask, near || twins || near_group)) {
+                // Any other expert near the last chosen one (or a choice of groups in doubt): all of it in fp64. Where
+                // nothing but twins at the border brought the token here, more twins of theirs (all logits equal, before
+                // a router's first update) do not count: every one of them is behind the chosen by its index.
+                const bool order = __any_sync(kFullMask, near);
+                const float xb = __shfl_sync(kFullMask, x, a.k - 1), bb = __shfl_sync(kFullMask, bj, a.k - 1);
                 uint32_t rest = 0;
 #pragma unroll
-                for (int i = 0; i < NV; ++i) rest = max(rest, key[i]);
+                for (int i = 0; i < NV; ++i) {
+                    const bool twin = !order && key[i] != 0 && v[i] == xb && (!a.bias || a.bias[lane * NV + i] == bb);
+                    rest = max(rest, twin ? 0u : key[i]);
+                }
                 rest = warp_max(left_key != 0 ? rest : 0u);
                 const uint32_t border = __shfl_sync(kFullMask, slot_key, a.k - 1);
                 if (near_group || (rest != 0 && left_key != 0 && too_near(value_of(border), value_of(rest), tol))) {
                     id = route_exact<NV>(a, v, M, lane);
                     x = id >= 0 ? route_logit(a, t, id) : kNone;
-                } else {
+                } else if (order) {
                     route_reorder<NV>(a, v, M, lane, id, x, bj);
                 }
             }

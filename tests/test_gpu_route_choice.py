@@ -41,3 +41,59 @@ def test_near_and_clear_tokens_in_one_block(E, groups, topk_groups, group_score)
             ids, w = mx.route(x, k, bias=bias.cuda(), **args)
             assert np.array_equal(to_np(ids), want[at])
             assert np.allclose(to_np(w), w64[at], rtol=3e-6, atol=0)
+
+
+def choice(x, k, **args):
+    ids, _ = mx.route(x.cuda(), k, **{n: v.cuda() if torch.is_tensor(v) else v for n, v in args.items()})
+    want, _ = plain.route(x.double().numpy(), k, **{n: v.double().numpy() if torch.is_tensor(v) else v for n, v in args.items()})
+    assert np.array_equal(to_np(ids), want), (args, k, np.argwhere(to_np(ids) != want)[0])
+    return to_np(ids)
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_twins_at_the_border_hide_no_better_expert(dtype):
+    """The last chosen expert and the best one left out have the same logit and bias; an expert behind them, whose fp32 key
+    is no larger, has the larger fp64 key."""
+    zero, same = torch.zeros(8), torch.full((8,), 3000.0)
+    x = torch.tensor([[20.0, 20, 25, 0, 0, 0, 0, 0], [20, 20, 20.125, -5, -5, -5, -5, -5], [0, 20, 20, 20, 20, 20, 20, 25],
+                      [30, 20, 20, 20, 21, 20, 24, 0]]).to(dtype)
+    assert choice(x, 1, score="sigmoid", bias=zero)[:, 0].tolist() == [2, 2, 7, 0]
+    for k in (2, 3, 4, 7):
+        choice(x, k, score="sigmoid", bias=zero)
+        choice(x, k, score="sigmoid", bias=same)
+        choice(x, k, score="sigmoid", groups=2, topk_groups=1, group_score="top2")
+        choice(x, k, score="sigmoid", groups=4, topk_groups=3, group_score="top2")
+    y = torch.tensor([[0.0, -200, -200, -190, -300, -400, -410, -420], [0, -30, -30, -20, -40, -40, -30, -19.5],
+                      [-30, -30, -30, -29, 0, -30, -28, -30]]).to(dtype)
+    assert choice(y[:1], 2, bias=zero).tolist() == [[0, 3]]
+    for k in range(1, 8):
+        for bias in (zero, same, torch.full((8,), 0.25)):
+            choice(y, k, bias=bias)
+        choice(y, k, groups=2, topk_groups=1, group_score="top2")
+
+
+@pytest.mark.parametrize("E,groups,topk_groups", [(8, 1, 1), (32, 1, 1), (60, 1, 1), (64, 8, 5), (100, 10, 6), (256, 1, 1), (1024, 4, 3)])
+@pytest.mark.parametrize("score,low,high", [("sigmoid", 17, 36), ("softmax", -60, -17)])
+def test_few_distinct_logits_whose_scores_fp32_merges(E, groups, topk_groups, score, low, high):
+    """BF16 logits drawn from a few values where fp32 scores saturate or vanish, under constant biases: equal experts and
+    hidden ones at every place of the order."""
+    g = torch.Generator().manual_seed(E)
+    for few in (2, 3, 6):
+        T = 120 if E < 256 else 30
+        values = (low + (high - low) * torch.rand((T, few), generator=g)).to(torch.bfloat16)
+        x = torch.gather(values, 1, torch.randint(0, few, (T, E), generator=g))
+        if score == "softmax":
+            x[torch.arange(T), torch.randint(0, E, (T,), generator=g)] = 0.0
+        for k in (1, 2, 5, 8):
+            for b in (0.0, 0.25, 1000.0):
+                choice(x, k, score=score, bias=torch.full((E,), b), groups=groups, topk_groups=topk_groups, group_score="max")
+            choice(x, k, score=score, groups=groups, topk_groups=topk_groups, group_score="top2")
+
+
+def test_equal_logits_everywhere():
+    """All experts alike, as before the first update: the first k."""
+    for E, k in ((128, 8), (100, 6)):
+        x = torch.zeros((50, E))
+        for score in ("softmax", "sigmoid"):
+            for bias in (None, torch.zeros(E), torch.full((E,), 0.1)):
+                assert (choice(x, k, score=score, bias=bias) == np.arange(k)).all()
