@@ -611,8 +611,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
             const bool sfb1 = T.n0 + 128 < a.N;
             const uint32_t bytes = kBM * kBK + kBBytes + kSfaBytes + (sfb1 ? 1024u : 512u);
             for (int kb = 0; kb < a.nkb; ++kb) {
-                if (!mbar_wait(&empty[stage], phase ^ 1u, abort, a.err, a.timeout_ns)) { ok = false; break; }
-                __syncwarp();
+                if (!mbar_wait_warp(&empty[stage], phase ^ 1u, abort, a.err, a.timeout_ns)) { ok = false; break; }
                 mbar_arrive_expect_tx_elect(&full[stage], bytes);
                 tma_load_2d_elect(smem + L::kA + stage * kBM * kBK, &tmap_a, &full[stage], kb * kBK, T.a_row0);
                 tma_load_2d_elect(smem + L::kB + stage * kBBytes, &tmap_b, &full[stage], kb * kBK, T.b_row0);
@@ -646,21 +645,20 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
         int j = 0;
         for (int t = blockIdx.x; t < tiles && ok; t += gridDim.x, ++j) {
             if (j > 1) {                    // the accumulator's previous tile has been read out
-                if (!mbar_wait(&acc_empty[j & 1], (empty_phase >> (j & 1)) & 1u, abort, a.err, a.timeout_ns)) {
+                if (!mbar_wait_warp(&acc_empty[j & 1], (empty_phase >> (j & 1)) & 1u, abort, a.err, a.timeout_ns)) {
                     ok = false;
                     break;
                 }
                 empty_phase ^= 1u << (j & 1);
             }
             if (j > 0) {                    // the previous tile's shared columns have been read
-                if (!mbar_wait(ovl_free, ovl_phase, abort, a.err, a.timeout_ns)) { ok = false; break; }
+                if (!mbar_wait_warp(ovl_free, ovl_phase, abort, a.err, a.timeout_ns)) { ok = false; break; }
                 ovl_phase ^= 1u;
             }
             tc_fence_after();
             const uint32_t acc = tmem_base + ((j & 1) ? kAcc1Col : 0u);
             for (int kb = 0; kb < a.nkb; ++kb) {
-                if (!mbar_wait(&full[stage], phase, abort, a.err, a.timeout_ns)) { ok = false; break; }
-                __syncwarp();
+                if (!mbar_wait_warp(&full[stage], phase, abort, a.err, a.timeout_ns)) { ok = false; break; }
                 tc_fence_after();
                 tc_cp_elect(sfa_t, sdesc_scale_block(smem_u32(smem + L::kSfa + stage * kSfaBytes)));
                 tc_cp_elect(sfb_t, sdesc_scale_block(smem_u32(smem + L::kSfb + stage * kSfbBytes)));
@@ -694,7 +692,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
         uint32_t full_phase = 0;
         for (int t = blockIdx.x + g * gridDim.x; t < tiles; t += 2 * gridDim.x) {
             const Tile T = decode_tile1<GROUPED>(t, a, off, pm);
-            if (!mbar_wait(&tmem_full[g], full_phase, abort, a.err, a.timeout_ns)) break;
+            if (!mbar_wait_warp(&tmem_full[g], full_phase, abort, a.err, a.timeout_ns)) break;
             full_phase ^= 1u;
             tc_fence_after();
             epilogue_tile<GROUPED>(a, T, tmem_base, g != 0, stage, ovl_addr, empty_addr, q, lane);
@@ -805,8 +803,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
         for (int t = pair; t < tiles && ok; t += npairs) {
             const Tile T = decode_tile_pair<GROUPED>(t, rank, a, off, pm128, pm256);
             for (int kb = 0; kb < a.nkb; ++kb) {
-                if (!mbar_wait(&empty[stage], phase ^ 1u, abort, a.err, a.timeout_ns)) { ok = false; break; }
-                __syncwarp();
+                if (!mbar_wait_warp(&empty[stage], phase ^ 1u, abort, a.err, a.timeout_ns)) { ok = false; break; }
                 const uint32_t fb = mapa_shared(smem_u32(&full[stage]), 0);
                 if (leader) mbar_arrive_expect_tx_elect(&full[stage], 2 * kPairStageBytes);
                 tma_load_2d_pair_elect(smem + L::kA + stage * kBM * kBK, &tmap_a, fb, kb * kBK, T.a_row0);
@@ -842,22 +839,21 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
             int j = 0;
             for (int t = pair; t < tiles && ok; t += npairs, ++j) {
                 if (j > 1) {                // the accumulator's previous tile has been read out
-                    if (!mbar_wait(&acc_empty[j & 1], (empty_phase >> (j & 1)) & 1u, abort, a.err,
-                                   a.timeout_ns)) {
+                    if (!mbar_wait_warp(&acc_empty[j & 1], (empty_phase >> (j & 1)) & 1u, abort, a.err,
+                                        a.timeout_ns)) {
                         ok = false;
                         break;
                     }
                     empty_phase ^= 1u << (j & 1);
                 }
                 if (j > 0) {                // the previous tile's shared columns have been read
-                    if (!mbar_wait(ovl_free, ovl_phase, abort, a.err, a.timeout_ns)) { ok = false; break; }
+                    if (!mbar_wait_warp(ovl_free, ovl_phase, abort, a.err, a.timeout_ns)) { ok = false; break; }
                     ovl_phase ^= 1u;
                 }
                 tc_fence_after();
                 const uint32_t acc = tmem_base + ((j & 1) ? kAcc1 : 0u);
                 for (int kb = 0; kb < a.nkb; ++kb) {
-                    if (!mbar_wait(&full[stage], phase, abort, a.err, a.timeout_ns)) { ok = false; break; }
-                    __syncwarp();
+                    if (!mbar_wait_warp(&full[stage], phase, abort, a.err, a.timeout_ns)) { ok = false; break; }
                     tc_fence_after();
                     const uint32_t sfa_s = smem_u32(smem + L::kSfa + stage * kSfaStage);
                     const uint32_t sfb_s = smem_u32(smem + L::kSfb + stage * kSfbStage);
@@ -917,7 +913,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
         uint32_t full_phase = 0;
         for (int t = pair + g * npairs; t < tiles; t += 2 * npairs) {
             const Tile T = decode_tile_pair<GROUPED>(t, rank, a, off, pm128, pm256);
-            if (!mbar_wait(&tmem_full[g], full_phase, abort, a.err, a.timeout_ns)) break;
+            if (!mbar_wait_warp(&tmem_full[g], full_phase, abort, a.err, a.timeout_ns)) break;
             full_phase ^= 1u;
             tc_fence_after();
             if constexpr (EPI == 0)

@@ -52,13 +52,6 @@ struct FewArgs {
     uint64_t timeout_ns;
 };
 
-// mbar_wait by a whole warp with one answer for all its lanes: a lane that sees another role's abort while its
-// neighbours see the phase complete must not leave them alone before a warp-wide instruction.
-__device__ __forceinline__ bool mbar_wait_warp(uint64_t* bar, uint32_t parity, volatile int* abort, uint32_t* err,
-                                               uint64_t timeout_ns) {
-    return __all_sync(0xFFFFFFFFu, mbar_wait(bar, parity, abort, err, timeout_ns));
-}
-
 __device__ __forceinline__ float4 ld_shared_cluster_f32x4(uint32_t cluster_addr) {
     float4 v;
     asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
@@ -128,7 +121,6 @@ __global__ void __launch_bounds__(kFewThreads, 2)
         uint32_t phase = ahead / S;
         for (int kb = kb_begin + ahead; kb < kb_end; ++kb) {
             if (!mbar_wait_warp(&empty[stage], phase ^ 1u, abort, a.err, a.timeout_ns)) break;
-            __syncwarp();
             load(kb, stage);
             ++issued;
             if (++stage == S) { stage = 0; phase ^= 1u; }
@@ -146,7 +138,6 @@ __global__ void __launch_bounds__(kFewThreads, 2)
         uint32_t phase = 0;
         for (int kb = kb_begin; kb < kb_end; ++kb) {
             if (!mbar_wait_warp(&full[stage], phase, abort, a.err, a.timeout_ns)) break;
-            __syncwarp();
             tc_fence_after();
             const uint64_t adesc = sdesc_kmajor_sw128(smem_u32(smem + L::kA + stage * 128 * 128));
             const uint64_t bdesc = sdesc_kmajor_sw128(smem_u32(smem + L::kB + stage * NPAD * 128));
@@ -363,7 +354,6 @@ __global__ void __launch_bounds__(kFewThreads, 2)
             const bool small = T.rows <= kGfSmall;
             for (int kb = 0; kb < a.nkb; ++kb) {
                 if (!mbar_wait_warp(&empty[stage], phase ^ 1u, abort, a.err, a.timeout_ns)) { ok = false; break; }
-                __syncwarp();
                 mbar_arrive_expect_tx_elect(&full[stage],
                                             128 * 128 + (small ? kGfSmall : kGfRows) * 128 + 2 * kFewSf);
                 tma_load_2d_elect(smem + L::kA + stage * 128 * 128, &tmap_w, &full[stage], kb * kBK, T.w_row0);
@@ -399,7 +389,6 @@ __global__ void __launch_bounds__(kFewThreads, 2)
             const uint32_t idesc[2] = {idesc_mxf4(128, cols, 0), idesc_mxf4(128, cols, 2)};
             for (int kb = 0; kb < a.nkb; ++kb) {
                 if (!mbar_wait_warp(&full[stage], phase, abort, a.err, a.timeout_ns)) { ok = false; break; }
-                __syncwarp();
                 tc_fence_after();
                 const uint64_t adesc = sdesc_kmajor_sw128(smem_u32(smem + L::kA + stage * 128 * 128));
                 const uint64_t bdesc = sdesc_kmajor_sw128(smem_u32(smem + L::kB + stage * kGfRows * 128));

@@ -63,6 +63,28 @@ __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity, volati
     }
 }
 
+// mbar_wait by a whole warp with one answer for all its lanes. Every role that goes on to a warp-wide instruction
+// (elect.sync, tcgen05.ld, a shuffle) waits like this: a lane that sees another role's abort while its neighbours see
+// the phase complete must not leave them alone, and the fills and phases that a warp counts stay the same in all lanes.
+__device__ __forceinline__ bool mbar_wait_warp(uint64_t* bar, uint32_t parity, volatile int* abort, uint32_t* err,
+                                               uint64_t timeout_ns) {
+    const uint32_t a = smem_u32(bar);
+    if (__all_sync(0xFFFFFFFFu, mbar_try_wait(a, parity))) return true;
+    const uint64_t t0 = globaltimer_ns();
+    while (!__all_sync(0xFFFFFFFFu, mbar_try_wait(a, parity))) {
+        const bool late = globaltimer_ns() - t0 > timeout_ns;
+        if (__any_sync(0xFFFFFFFFu, late || *abort)) {
+            if (late) {
+                *abort = 1;
+                atomicOr(err, kErrWaitTimeout);
+            }
+            __syncwarp();
+            return false;
+        }
+    }
+    return true;
+}
+
 // Lower bound of the deadline of a drain wait, independent of the (possibly very short) deadline of
 // the ordinary waits: copies and MMAs in flight complete in microseconds, and a CTA must not exit
 // (or free TMEM) before they have.
