@@ -169,7 +169,8 @@ __global__ void __launch_bounds__(kFewThreads, 2)
         // The accumulator: lane l of quadrant q is weight row 32 q + l, column m token m.
         const int q = warp & 3;
         const int n = n0 + 32 * q + lane;
-        const bool ok = mbar_wait_warp(done, 0, abort, a.err, a.timeout_ns);
+        // `done` fires too when the issuer has given up: what it had accumulated until then is no result.
+        const bool ok = mbar_wait_warp(done, 0, abort, a.err, a.timeout_ns) && __all_sync(0xFFFFFFFFu, !*abort);
         tc_fence_after();
         float* part = reinterpret_cast<float*>(smem + L::kA);            // [NPAD][128]
         if (ok) {
@@ -197,7 +198,9 @@ __global__ void __launch_bounds__(kFewThreads, 2)
     __syncthreads();
     if (ranks > 1) {
         cluster_sync();                         // every CTA's partial sums are in its shared memory
-        if (warp >= 2 && __all_sync(0xFFFFFFFFu, !*abort)) {
+        // No CTA writes sums of which another one, whose wait has run out, did not deliver its part.
+        const uint32_t gave_up = ld_shared_cluster_u32(mapa_shared(smem_u32(smem + L::kMisc + 4), lane & (ranks - 1)));
+        if (warp >= 2 && __all_sync(0xFFFFFFFFu, gave_up == 0)) {
             // Four consecutive columns per thread; width / 4 (a power of two) threads per row.
             const int width = 128 / ranks, per_row = width / 4, t = threadIdx.x - 64;
             const uint32_t part = smem_u32(smem + L::kA);
