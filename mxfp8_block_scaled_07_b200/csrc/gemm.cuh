@@ -511,8 +511,10 @@ __device__ __forceinline__ int setup_groups(const int32_t* row_offsets, int G, i
         int acc128 = 0, acct = 0;
         for (int g0 = 0; g0 < G; g0 += 32) {
             const int g = g0 + lane;
-            const int n = g < G ? off[g + 1] - off[g] : 0;
-            if (n < 0) ok = false;
+            // Compared, not subtracted: differences of offsets may wrap, and sums of wrapped ones come back to `rows`.
+            const bool in = g < G && off[g] <= off[g + 1];
+            if (g < G && !in) ok = false;
+            const int n = in ? off[g + 1] - off[g] : 0;
             const int t128 = n > 0 ? (n + 127) / 128 : 0, tt = n > 0 ? (n + TILE - 1) / TILE : 0;
             int i128 = t128, it = tt;
 #pragma unroll
