@@ -9,8 +9,10 @@ travels with the source tree; nothing is installed elsewhere.
 from __future__ import annotations
 
 import os
+import re
 import subprocess
 import sys
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
@@ -67,12 +69,29 @@ def build(force: bool = False, verbose: bool = False) -> str:
     return LIB
 
 
+def call_tag() -> str:
+    """What _mxcall.so depends on beside its source: the torch whose C++ library it is linked against, and the Python."""
+    import torch
+
+    return f"torch {torch.__version__} {torch.version.git_version} {sysconfig.get_config_var('SOABI')}"
+
+
+def built_for(lib: str = CALL_LIB):
+    """The call_tag() that a built _mxcall.so carries (read from the file: one of another torch must not be loaded);
+    None if it carries none."""
+    with open(lib, "rb") as f:
+        found = re.search(rb"mx-call-tag:([^;\0]*);", f.read())
+    return found.group(1).decode() if found else None
+
+
+def call_needs_build() -> bool:
+    return needs_build(CALL_LIB, [CALL_SOURCE, os.path.join(ROOT, "include", "mx.h")]) or built_for() != call_tag()
+
+
 def build_call(force: bool = False, verbose: bool = False) -> str:
     """_mxcall.so, linked against the libmx.so beside it."""
-    if not force and not needs_build(CALL_LIB, [CALL_SOURCE, os.path.join(ROOT, "include", "mx.h")]):
+    if not force and not call_needs_build():
         return CALL_LIB
-    import sysconfig
-
     import torch
 
     site = os.path.dirname(torch.__file__)
@@ -81,6 +100,7 @@ def build_call(force: bool = False, verbose: bool = False) -> str:
                 os.path.join(cuda, "include"), sysconfig.get_paths()["include"]]
     tmp = CALL_LIB + f".tmp{os.getpid()}"
     _run(["g++", "-O2", "-std=c++17", "-fPIC", "-shared", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+          f'-DMX_CALL_TAG="{call_tag()}"',
           *(x for p in includes for x in ("-isystem", p)), "-o", tmp, CALL_SOURCE, "-L" + HERE, "-l:libmx.so",
           "-L" + os.path.join(site, "lib"), "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_python", "-Wl,-rpath,$ORIGIN"], verbose)
     os.replace(tmp, CALL_LIB)

@@ -19,6 +19,9 @@
 
 #include "../../include/mx.h"
 
+// The torch and the Python this was built for, for build.py and mx.py to read from the file before it is loaded.
+extern "C" __attribute__((used, visibility("default"))) const char mx_call_tag[] = "mx-call-tag:" MX_CALL_TAG ";";
+
 namespace {
 
 PyObject* g_error = nullptr;       // the binding's MxError(status, what)

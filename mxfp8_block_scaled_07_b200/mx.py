@@ -334,17 +334,25 @@ def quantize_block128(x: torch.Tensor, pow2_scales: bool, out=None):
 # in Python they took 11 to 15 us a call, more than most of these kernels. Refusals raise MxError like every other call.
 
 _mxcall = None
+_BUILD = "run python -m mxfp8_block_scaled_07_b200.build"
 
 
 def _native():
-    """The compiled call path (raises if it has not been built)."""
+    """The compiled call path (raises if it has not been built, or for another torch or Python than the ones running)."""
     global _mxcall
     if _mxcall is None:
         lib()
+        from . import build
+
+        if not os.path.exists(build.CALL_LIB):
+            raise ImportError(f"_mxcall.so not built; {_BUILD}")
+        made, here = build.built_for(), build.call_tag()
+        if made != here:
+            raise ImportError(f"_mxcall.so was built for {made}, this is {here}; {_BUILD}")
         try:
             from . import _mxcall as module
         except ImportError as e:
-            raise ImportError("_mxcall.so not built; run python -m mxfp8_block_scaled_07_b200.build") from e
+            raise ImportError(f"_mxcall.so does not load ({e}); {_BUILD}") from e
         module.set_error(MxError)
         _mxcall = module
     return _mxcall
