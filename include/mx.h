@@ -237,9 +237,9 @@ mx_status mx_dequantize_fp4(const uint8_t* q, const uint8_t* s, int64_t M, int64
 /*
  * Dense and grouped block-scaled MXFP4 products: mx_gemm and mx_grouped_gemm on packed 4-bit codes
  * (qa [M, K / 2], qb [N, K / 2] or [G, N, K / 2] bytes; K counts elements). Same scale layouts,
- * requirements, errors, device-side checks and accuracy. mx_gemm_fp4 takes at most 64 rows (a decoding step)
- * through a kernel of its own that splits K over a cluster and sums in a fixed order, mx_grouped_gemm_fp4 at most
- * 32 rows per group on average through one for few rows per expert; everything else runs the CTA-pair kernel
+ * requirements, errors, device-side checks and accuracy. mx_gemm_fp4 takes few rows (a decoding step: at most 32, or 64
+ * if K >= 4096) through a kernel of its own that splits K over a cluster and sums in a fixed order, mx_grouped_gemm_fp4 at
+ * most 32 rows per group on average through one for few rows per expert; everything else runs the CTA-pair kernel
  * (mx_set_gemm_variant has no part in any of them).
  */
 mx_status mx_gemm_fp4(const uint8_t* qa, const uint8_t* sa_swz, const uint8_t* qb, const uint8_t* sb_swz, int64_t M,

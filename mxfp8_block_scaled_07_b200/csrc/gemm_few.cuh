@@ -1,4 +1,5 @@
-// MXFP4 product for few rows of A (at most 64: the tokens of a decoding step), bound by one pass over the weight.
+// MXFP4 product for few rows of A (at most 32, up to 64 for a long K: the tokens of a decoding step), bound by one pass
+// over the weight.
 //
 // C[m, n] = sum_k A[m, k] B[n, k] is computed as its transpose: 128 rows of the weight B are the tensor core's 128
 // rows and the tokens its columns (NPAD = 16, 32 or 64 of them), so no lane of the MMA works on padding and a CTA's
@@ -14,9 +15,9 @@
 // most 26 KB, two CTAs per SM, so up to 130 KB of weight are in flight per SM. Waits are bounded as in the other
 // kernels; no load uses cluster multicast.
 //
-// Measured with weights that are not in L2 (a graph over 20 of them): 16 x 6144 x 4096 8.1 us (13.4 MB; the pair kernel
-// 10.4 us with the weight in L2), 64 rows 11.5 us (pair 11.9 us), 16 x 24576 x 4096 14.5 us, 16 x 151936 x 4096 61 us,
-// 5.4 TB/s. The smallest call takes 4.4 us: launch, tensor maps, one load, one MMA, the cluster's sum.
+// Measured with weights that are not in L2 (a graph over up to 20 of them), this kernel / the pair kernel in us: 16 x 6144 x
+// 4096 8.2 / 11.8 (13.4 MB), 16 x 24576 x 4096 13.6 / 20.2, 16 x 151936 x 4096 59 / 77 (5.6 TB/s), 32 x 2048 x 1024
+// 6.6 / 7.0. The smallest call takes 3.3 us: launch, tensor maps, one load, one MMA.
 #pragma once
 #include <cstdint>
 
@@ -24,7 +25,17 @@
 
 namespace mx {
 
+// Up to 32 rows this kernel is the faster one but for weights of many short rows (N >= 40960, K <= 1024: up to 1.8 times the
+// pair kernel's time at 151936 x 256). 33 to 64 rows take its widest form, whose fixed part is larger; this kernel /
+// the pair kernel in us at 64 rows:
+//   K        256          1024         2048         4096         8192
+//   N 512    7.8 / 5.9    8.8 / 7.2    8.4 / 8.6    8.8 / 10.6   9.4 / 15.1
+//   N 8192   7.9 / 6.1    9.6 / 7.6    10.4 / 9.6   12.3 / 12.5  14.6 / 17.3
+//   N 24576  8.8 / 7.4    11.5 / 11.1  13.3 / 13.9  18.1 / 19.8  26.2 / 30.9
+//   N 40960  15.4 / 8.4   19.0 / 12.9  23.2 / 17.8  31.9 / 26.4  48.3 / 44.1
+constexpr int kFewRows = 32;
 constexpr int kFewMaxRows = 64;
+constexpr int kFewLongK = 4096;                 // from here on also for 33 to 64 rows
 constexpr int kFewThreads = 192;
 constexpr int kFewStages = 4;
 constexpr int kFewSf = 1024;                    // two 512-byte scale blocks per operand and stage

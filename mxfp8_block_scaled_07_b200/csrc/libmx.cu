@@ -1004,7 +1004,7 @@ mx_status launch_gemm_fp4(const uint8_t* qa, const uint8_t* sa, const uint8_t* q
                    : launch_pair<false, 0, true>(pairs, ta, tb, tsa, tsb, a, stream);
 }
 
-// The product for at most kFewMaxRows rows: tiles of 128 weight rows, K split over a cluster of CTAs as long as that
+// The product for few rows: tiles of 128 weight rows, K split over a cluster of CTAs as long as that
 // gives every CTA its own place (two per SM) and at least two stages.
 template <int NPAD>
 mx_status launch_few(const uint8_t* qa, const uint8_t* sa, const uint8_t* qb, const uint8_t* sb, const FewArgs& a,
@@ -1089,7 +1089,7 @@ mx_status mx_gemm_fp4(const uint8_t* qa, const uint8_t* sa_swz, const uint8_t* q
     if (empty) return MX_OK;
     const DeviceInfo* d = nullptr;
     if (mx_status st = check_device(&d)) return st;
-    if (M <= kFewMaxRows) {
+    if (M <= kFewRows || (M <= kFewMaxRows && K >= kFewLongK)) {
         FewArgs a;
         a.c = c;
         a.ldc = ld_c;
