@@ -1182,14 +1182,22 @@ mx_status route_shape(int64_t T, int64_t E, int64_t topk, int64_t ld, mx_out_dty
     return MX_OK;
 }
 
-// route_kernel for nv experts per lane. Packed keys: BF16 logits that decide by themselves; several tokens per warp
-// where that measured faster (at most 128 experts and a batch that fills the device without it).
-constexpr int64_t kRouteManyTokens = 4096;
+// route_kernel for nv experts per lane. Packed keys: BF16 logits that decide by themselves; several tokens per warp (4 for
+// k <= 8, else 2) where that measured faster: at most 128 experts and a batch that gives kRouteManyWarps warps of
+// that kind. Several tokens / one token a warp, us:
+//   tokens             2048         4096         6000         8192         20480
+//   32 experts, k 8    2.66 / 2.15  2.87 / 2.56  3.07 / 3.17  3.28 / 3.69  4.61 / 7.17
+//   64 experts, k 2    2.97 / 2.05  3.07 / 2.46  3.18 / 2.97  3.28 / 3.59  4.40 / 6.66
+//   128 experts, k 8   3.59 / 2.46  3.90 / 3.18  4.30 / 4.00  4.81 / 4.77  7.42 / 9.52
+//   32 experts, k 16   2.36 / 2.26  2.87 / 2.97  3.17 / 3.69  3.58 / 4.40  6.76 / 8.70
+//   128 experts, k 16  2.97 / 2.76  3.69 / 3.69  4.41 / 4.71  5.02 / 5.63  10.24 / 11.78
+constexpr int64_t kRouteManyWarps = 2048;
 
 template <int NV>
 mx_status launch_route(const RouteArgs& a, bool packed, mx_stream stream) {
-    const bool many = packed && NV <= 4 && a.T >= kRouteManyTokens;
-    const int lanes = !many ? 32 : (a.k <= 8 ? 8 : 16);
+    const int slots = a.k <= 8 ? 8 : 16;                  // lanes per token of a warp that takes several
+    const bool many = packed && NV <= 4 && a.T >= kRouteManyWarps * (32 / slots);
+    const int lanes = many ? slots : 32;
     const int64_t grid = ceil_div(a.T, kRouteThreads / lanes);
     // Groups that cut lanes: a row of keys per warp (at most 32 KB a block).
     const size_t smem = a.G > 1 && a.lanes_per_group == 0 ? size_t(kRouteThreads / 32) * a.E * 8 : 0;

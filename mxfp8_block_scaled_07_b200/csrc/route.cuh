@@ -423,9 +423,9 @@ __device__ __forceinline__ void route_load_row(const RouteArgs& a, int64_t t, in
 // Bound by the choice's instructions and their latency, not by the one read of the logits (20 480 x 128 BF16 are
 // 5 MB, less than a microsecond): some 25 instructions per chosen expert, 8 with packed keys, whose chains of maxima
 // run side by side for the warp's tokens. Several tokens per warp are for large batches with packed keys and at most
-// 128 experts: 20 480 x 128, top 8: 8.8 us with four tokens a warp, 11.1 us with one; 16 tokens: 3.5 and 2.6 us;
+// 128 experts: 20 480 x 128, top 8: 7.4 us with four tokens a warp, 9.5 us with one; 256 tokens: 3.4 and 2.1 us;
 // 20 480 x 256: 15.4 and 15.1 us. Without packed keys a warp's tokens only queue up (sigmoid with bias, 20 480 x 128:
-// 28.8 us with four, 23.1 us with one).
+// 28.8 us with four where one took 23.1 us).
 template <int NV, int LPT, bool PACKED>
 __global__ void __launch_bounds__(kRouteThreads) route_kernel(const __grid_constant__ RouteArgs a) {
     grid_wait();

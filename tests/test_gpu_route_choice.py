@@ -97,3 +97,26 @@ def test_equal_logits_everywhere():
         for score in ("softmax", "sigmoid"):
             for bias in (None, torch.zeros(E), torch.full((E,), 0.1)):
                 assert (choice(x, k, score=score, bias=bias) == np.arange(k)).all()
+
+
+def test_several_tokens_per_warp_where_they_begin():
+    """BF16 logits that decide by themselves, at most 128 experts: 4 tokens per warp from 8192 on (k <= 8), 2 from 4096 on
+    (k > 8), batches on both sides of each and with every tail. The same choice and weights as of the tokens by themselves."""
+    g = torch.Generator().manual_seed(3)
+    for E, k, sizes in ((128, 8, (8190, 8191, 8192, 8193, 8195)), (40, 3, (8191, 8194)), (17, 1, (8193,)), (64, 9, (4095, 4096, 4097)),
+                        (128, 16, (4097,))):
+        x = (4 * torch.randn((max(sizes), E), generator=g)).round() / 2
+        x[torch.rand(x.shape, generator=g) < 0.2] = float("-inf")
+        x[3] = float("-inf")
+        x = x.to(torch.bfloat16).cuda()
+        want = torch.sort(x.double(), dim=1, descending=True, stable=True)
+        expect = torch.where(want.values[:, :k] > -np.inf, want.indices[:, :k], -1)
+        groups = 8 if E % 8 == 0 else 1
+        for renormalize in (True, False):
+            parts = [mx.route(p, k, renormalize=renormalize) for p in x.split(1000)]
+            of_groups = torch.cat([mx.route(p, k, groups=groups, topk_groups=max(1, groups // 2))[0] for p in x.split(1000)])
+            ids1, w1 = (torch.cat(v) for v in zip(*parts))
+            for T in sizes:
+                ids, w = mx.route(x[:T], k, renormalize=renormalize)
+                assert torch.equal(ids.long(), expect[:T]) and torch.equal(ids, ids1[:T]) and torch.equal(w, w1[:T])
+                assert torch.equal(mx.route(x[:T], k, groups=groups, topk_groups=max(1, groups // 2))[0], of_groups[:T])
