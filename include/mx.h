@@ -30,7 +30,8 @@
  * Errors: arguments are checked on the host before any launch and reported as mx_status; nothing
  * is launched when a check fails. MX_ERR_CUDA reports a failed launch or driver call. Device-side
  * faults that a kernel detects (a bounded wait that expired, invalid grouped-GEMM row offsets)
- * set bits in a device status word readable with mx_device_error.
+ * set bits in a device status word readable with mx_device_error. After an expired wait the call's
+ * outputs are incomplete; an element of a product is then its value or what was there before.
  */
 #ifndef MX_H
 #define MX_H
@@ -276,7 +277,8 @@ typedef enum { MX_FORMAT_E4M3 = 0, MX_FORMAT_E2M1 = 1 } mx_format;
  *   (MX_GROUP_MAX) or by the sum of their two largest (MX_GROUP_TOP2; one, if only one can be chosen); experts
  *   outside the topk_groups best groups cannot be chosen. groups == 1: no such limit.
  *   Choice: the topk largest keys, largest first; equal keys (of experts and of groups): the lower index first.
- *   It is the choice that the definition gives in fp64, whatever the input type.
+ *   It is the choice that the definition gives in fp64, whatever the input type; keys and group sums that are equal
+ *   but for the roundings of fp64 itself (a softmax's sum depends on its order) may come in either order.
  *   Weights: scale * s, divided by the sum of the chosen experts' s if renormalize != 0.
  *   ids [T, topk] int32, weights [T, topk] fp32 (device, packed). Slots for which no expert is left have id -1
  *   and weight 0.

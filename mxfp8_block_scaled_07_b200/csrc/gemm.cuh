@@ -721,7 +721,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
 // of issue per stage were the first cost (see tc_mxf4_stage_pair_elect: 134 400 -> 110 900), the epilogue's staging in
 // shared memory, which the MMAs and TMA writes already keep busy, the next (-> 105 600 with 32-byte stores from
 // registers); what is left are the hand-over between tiles (some 770 cycles each), the C stores and the scale copies.
-// 5200 x 24576 x 4096: 189 us, 5.5 PFLOP/s; back to back under the power cap 213 us, 4.9 PFLOP/s.
+// 5200 x 24576 x 4096: back to back under the power cap (1.40 GHz) 216 us, 4.85 PFLOP/s; in bursts of four 190 us, 5.5.
 template <bool FP4>
 constexpr uint32_t kPairStageBytesOf = kBM * kBK + (kBN / 2) * kBK + (FP4 ? 2 : 1) * (kSfaBytes + kSfbBytes);   // per CTA
 

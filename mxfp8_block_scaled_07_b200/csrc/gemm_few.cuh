@@ -264,6 +264,8 @@ constexpr int kGfStages = 3;
 // Taken for at most 32 rows per expert on average (all the host knows). 128 experts of 1536 x 2048, weights not in L2,
 // this kernel against the pair kernel: 8 rows in all 8.6 / 10.1 us, 128 rows (80 experts) 28.2 / 31.7, 512 rows 37.0 /
 // 46.9 (the weights' bytes need 31.5), 2048 rows 41.8 / 48.5, 4096 rows 44.0 / 49.3, 8192 rows 49.9 / 51.2.
+// Other shapes at 32 and 64 rows per expert: 128 of 2048 x 768 25.9 / 30.2 and 34.6 / 33.0, 256 of 512 x 1024 20.8 / 23.2
+// and 26.2 / 25.1, 8 of 4096 x 4096 17.7 / 21.2 and 19.1 / 21.8 (at 128 rows 27.6 / 22.9).
 constexpr int64_t kGfMaxMeanRows = 32;
 
 struct GfSmem {

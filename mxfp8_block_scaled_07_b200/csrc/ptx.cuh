@@ -361,7 +361,7 @@ __device__ __forceinline__ void tc_mma_mxf4_elect(uint32_t d_tmem, uint64_t ades
 // A whole MXFP4 stage (256 elements of K) under one election: per half of the stage the scale copies (A's and B's two
 // row tiles' blocks; the second half's slot is 12 columns on) and two MMAs of 64 elements, then the commit on `bar` in
 // both CTAs. Issued one by one, each with its own election, the issuing warp and not the tensor core set the pace:
-// 5200 x 24576 x 4096 took 201 us (with a test before each MMA 230), like this, with the epilogue's direct stores, 189;
+// 5200 x 24576 x 4096 took 201 us (with a test before each MMA 230), like this, with the epilogue's direct stores, 190;
 // all copies before all MMAs 192; the next stage's copies between this stage's MMAs 221.
 // sda / sdb0 / sdb1: descriptors of the scale blocks of A and of B's row tiles in shared memory; the second block
 // of each lies 512 bytes (32 descriptor units) behind the first.

@@ -447,7 +447,8 @@ def combine(rows: torch.Tensor, slot_row: torch.Tensor, weights=None, out_dtype=
 def combine_backward(dy: torch.Tensor, rows: torch.Tensor, slot_row: torch.Tensor, weights=None, need_weights: bool = True, out=None):
     """mx_combine_bwd: (d_rows like rows, d_weights fp32 [T, topk]) from dy [T, N]. need_weights=False leaves
     d_weights out (None), and rows is then only asked for its shape and type. Padding rows get zeros. No two slots may
-    name the same row."""
+    name the same row. Rows that no slot names get zeros, except where rows has exactly T * topk of them, as in a
+    plan's partition: then every slot has to name one."""
     return (_mxcall or _native()).combine_backward(dy, rows, slot_row, weights, need_weights, _buffers(out))
 
 
