@@ -1,6 +1,6 @@
 /*
- * libmx -- MXFP8 and MXFP4 quantize, scale layout, block-scaled GEMM, expert routing and grid
- * equality on NVIDIA B200 (sm_100a). C ABI: plain pointers and sizes; no allocation, no host synchronisation (except
+ * libmx -- MXFP8 and MXFP4 quantize, scale layout, block-scaled GEMM, expert routing, an 8-bit paged cache
+ * with attention over it, rotary positions and grid equality on NVIDIA B200 (sm_100a). C ABI: plain pointers and sizes; no allocation, no host synchronisation (except
  * mx_device_error), every call asynchronous on `stream`.
  *
  * The operations follow "End-to-End MXFP8 Reinforcement Learning on Blackwell: What Matching
@@ -58,8 +58,8 @@ typedef enum {
 /* mx_quantize flags. */
 enum { MX_ROWWISE = 1, MX_COLWISE = 2, MX_SWIZZLE = 4 };
 
-/* GEMM output element type. */
-typedef enum { MX_OUT_F32 = 0, MX_OUT_BF16 = 1 } mx_out_dtype;
+/* Element types. GEMM outputs, router and combine tensors are MX_OUT_F32 or MX_OUT_BF16; mx_rope takes all three. */
+typedef enum { MX_OUT_F32 = 0, MX_OUT_BF16 = 1, MX_OUT_F16 = 2 } mx_out_dtype;
 
 /* Bytes of the tensor-core scale layout for a [rows, kblocks] scale matrix:
  * ceil(rows/128)*128 * ceil(kblocks/4)*4. Returns -1 for negative sizes. */
@@ -360,6 +360,110 @@ mx_status mx_combine_bwd(const void* dy, mx_out_dtype y_dtype, int64_t ld_dy, co
                          int64_t rows, int64_t ld_c, const int32_t* slot_row, const float* weights, int64_t T, int64_t topk,
                          int64_t N, void* d_c, int64_t ld_dc, float* d_weights, mx_stream stream);
 
+/* ---- positions, the cache and attention --------------------------------------------------------------
+ * What stands between the qkv and the output projection of a sampler's layer: rotary positions (with their
+ * gradient, for the learner), a paged cache of keys and values on the library's E4M3 / E8M0 grid, and attention
+ * over that cache for prompts and for single tokens.
+ */
+
+/*
+ * Rotation table: for positions first .. first + count - 1, fp32 [count, 2 pairs] (device, packed): amplitude *
+ * cos(p f_i) for every pair i, then amplitude * sin(p f_i). freq (host, `pairs` doubles, read during the call) are the
+ * angles per position; angles are formed in fp64 and the result is rounded once. 1 <= pairs <= 128.
+ */
+mx_status mx_rope_table(const double* freq, int64_t pairs, double amplitude, int64_t first, int64_t count, float* table,
+                        mx_stream stream);
+
+/*
+ * Rotary positions of x [T, H, D] (device; dtype fp32, BF16 or FP16; element strides ldx_t from token to token and ldx_h from
+ * head to head, features packed): pair i of every head of token t is turned by the angle of row pos[t] of `table`
+ * (fp32 [positions, rot], as mx_rope_table writes it):
+ *   y_a = x_a cos - x_b sin,  y_b = x_b cos + x_a sin,
+ * with (a, b) = (i, i + rot / 2), or (2 i, 2 i + 1) if interleaved != 0. Features rot .. D - 1 are copied. Each sum is formed to
+ * 1.5 units in the last place of fp32 and rounded once. pos: int32 [T] (pos64 == 0) or int64 (device), or NULL: 0 .. T - 1.
+ * A token with a negative position (padding) gets zeros; so does one at or behind `positions`, which also sets bit 4 of the
+ * device status word. y (the same shape and type, strides ldy_t, ldy_h) may be x itself with the same strides: features from rot on
+ * then stay as they are.
+ * Requirements: 1 <= D <= 1024, 2 <= rot <= min(D, 256), rot even, heads that do not overlap (|ldx_h| >= D where H > 1);
+ * pointers aligned to their elements. Rows whose pieces are all 16-byte aligned move in 16-byte pieces (and rot a
+ * multiple of 16 bytes of elements, of 32 in the half layout); others element by element. T == 0 or H == 0 is a no-op.
+ */
+mx_status mx_rope(const void* x, mx_out_dtype dtype, int64_t T, int64_t H, int64_t D, int64_t ldx_t, int64_t ldx_h,
+                  const float* table, int64_t positions, int64_t rot, const void* pos, int pos64, int interleaved, void* y,
+                  int64_t ldy_t, int64_t ldy_h, mx_stream stream);
+
+/* The gradient of mx_rope with respect to x, from dy: the transposed rotation (angles negated). Arguments as mx_rope. */
+mx_status mx_rope_bwd(const void* dy, mx_out_dtype dtype, int64_t T, int64_t H, int64_t D, int64_t ldy_t, int64_t ldy_h,
+                      const float* table, int64_t positions, int64_t rot, const void* pos, int pos64, int interleaved,
+                      void* dx, int64_t ldx_t, int64_t ldx_h, mx_stream stream);
+
+/*
+ * A paged cache and a batch of sequences in it (host struct, read during the call; all pointers device).
+ *   k, v: E4M3 codes [pages][heads][page_size][head_dim]; a page's block is packed, pages lie k_stride / v_stride bytes apart.
+ *   k_scale, v_scale: one E8M0 byte per page and head, [pages][heads]; a page's bytes are packed, pages ks_stride / vs_stride
+ *     apart. A value is code * 2^(byte - 127); byte 255 makes all of its page's values of that head NaN.
+ *   page_table [sequences, width] int32, row stride ld_table elements: the page of tokens i * page_size .. of a sequence.
+ *     Entries behind a sequence's last page are not read.
+ *   lengths [sequences] int32: tokens of every sequence, the rows of this call among them (negative: 0).
+ *   row_offsets [sequences + 1] int32, nondecreasing from 0: rows [row_offsets[b], row_offsets[b + 1]) of the batch are the
+ *     last tokens of sequence b. NULL: one row per sequence (rows == sequences). Rows behind the last sequence's are
+ *     neither read nor written.
+ * Row j of a sequence's n has position lengths[b] - n + j; a row of a sequence without tokens (or with fewer than n) has a
+ * negative one: it is padding, nothing is appended for it, and what is computed for it is zero.
+ * Requirements: head_dim 64 or 128, page_size 16, 32, 64 or 128, 1 <= heads <= 1024, codes 16-byte aligned with strides that
+ * are multiples of 16 and at least a page's block, int32 arrays 4-byte aligned, rows < 2^31, sequences < 2^24.
+ * A page id outside [0, pages) or a page behind the table's width sets bit 4 of the device status word; nothing is written for
+ * it, and attention gives NaN to the rows that see it.
+ */
+typedef struct {
+    uint8_t *k, *v, *k_scale, *v_scale;
+    int64_t k_stride, v_stride, ks_stride, vs_stride;
+    int64_t pages, heads, page_size, head_dim;
+    const int32_t* page_table;
+    int64_t ld_table, width;
+    const int32_t* lengths;
+    const int32_t* row_offsets;
+    int64_t sequences, rows;
+} mx_cache_batch;
+
+/*
+ * Appends the rows' keys and values (BF16 [rows, heads, head_dim], strides in elements) to the cache: keys rotated as mx_rope
+ * does it at their positions (table NULL: not rotated), values as they are. The block of a scale is a page's tokens of one head: e =
+ * floor(log2 amax) - 8 over the tokens appended to it in this call, and not below the page's e if it holds older tokens; where
+ * e grew, all of the page's other codes of that head are rounded anew (to nearest even). The page's first token begins it anew,
+ * whatever it held, and leaves the codes behind the new ones alone. Codes are RNE(x 2^-e) saturated to +-448, x being the
+ * rotation in exact arithmetic. NaN or infinity among the new tokens: scale byte 255 and zero codes for the older and the new
+ * ones, until the page is begun anew.
+ * q (BF16 [rows, q_heads, head_dim], or NULL): rotated to q_out at the same positions, in fp32 rounded once; q_out may be q.
+ * No page may be appended to by two sequences in one call. A position behind the rotation table counts as zeros (and sets bit 4).
+ * Requirements: rot a multiple of 16, <= head_dim; BF16 tensors 16-byte aligned with strides that are multiples of 8; table 16-byte
+ * aligned; q_heads <= 4096.
+ */
+mx_status mx_cache_append(const mx_cache_batch* cache, const void* k, int64_t ldk_t, int64_t ldk_h, const void* v,
+                          int64_t ldv_t, int64_t ldv_h, const float* table, int64_t positions, int64_t rot, int interleaved,
+                          const void* q, int64_t q_heads, int64_t ldq_t, int64_t ldq_h, void* q_out, int64_t ldo_t,
+                          int64_t ldo_h, mx_stream stream);
+
+/* Bytes of mx_cache_attention's workspace for such a batch; -1 for sizes it does not take. */
+int64_t mx_cache_attention_workspace_bytes(int64_t head_dim, int64_t rows, int64_t q_heads);
+
+/*
+ * Attention of the rows' queries q (BF16 [rows, q_heads, head_dim], strides in elements) over the cache: query head i reads key
+ * head i / (q_heads / heads). A row at position p sees the keys p - window + 1 .. p of its sequence (window <= 0: 0 .. p):
+ *   out = sum_j softmax_j(scale q . k_j) v_j   (BF16 [rows, q_heads, head_dim], strides ldo_t, ldo_h)
+ *   lse = log sum_j exp(scale q . k_j)         (fp32 [rows, q_heads], packed; NULL: not wanted)
+ * Scores, softmax statistics and sums are fp32; the weights of the values are rounded to 11 bits (f16). A row that sees no key
+ * has out 0 and lse -inf. Values whose page's scale lies more than 2^60 below the largest that the row's part of the work
+ * has met count as 0. Codes 0x7F and 0xFF, which mx_cache_append does not write, count as NaN, and may do so for neighbouring
+ * rows that do not see them. Sums are made in a fixed order.
+ * workspace: mx_cache_attention_workspace_bytes(head_dim, rows, q_heads) device bytes, 16-byte aligned, used during this call only.
+ * Requirements: q_heads a multiple of heads, q_heads <= 4096, 0 < scale < inf, BF16 tensors 16-byte aligned with strides that are multiples
+ * of 8, rows * q_heads < 2^31.
+ */
+mx_status mx_cache_attention(const mx_cache_batch* cache, const void* q, int64_t q_heads, int64_t ldq_t, int64_t ldq_h,
+                             float scale, int64_t window, void* out, int64_t ldo_t, int64_t ldo_h, float* lse,
+                             void* workspace, mx_stream stream);
+
 /*
  * Selects the kernel behind later mx_gemm / mx_grouped_gemm calls (process-wide): 0 (default) the
  * CTA-pair kernel (256 x 256 tiles computed by two SMs with tcgen05.mma.cta_group::2), 1 the
@@ -438,7 +542,8 @@ const char* mx_status_string(mx_status status);
 
 /*
  * Reads and clears the device status word of the current device (synchronizes the device).
- * *bits receives the error bits (1: a bounded wait expired; 2: invalid grouped-GEMM row offsets).
+ * *bits receives the error bits (1: a bounded wait expired; 2: invalid grouped-GEMM row offsets; 4: a page id outside the cache, or a
+ * position behind the rotation table).
  * Returns MX_OK when no bit was set, MX_ERR_DEVICE when some bit was set, MX_ERR_CUDA on failure.
  */
 mx_status mx_device_error(uint32_t* bits);

@@ -1,4 +1,4 @@
-// The call path of the binding's MXFP4 and expert-routing functions: checks of the tensors, allocation of the outputs
+// The call path of the binding's MXFP4, expert-routing, rotation and cache functions: checks of the tensors, allocation of the outputs
 // and the library call (include/mx.h), in one native function per entry point.
 //
 // What a small call costs is host time: through Python attribute checks, torch.empty and ctypes a call took 11 to 15 us
@@ -15,6 +15,7 @@
 #include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
 
+#include <cmath>
 #include <string>
 
 #include "../../include/mx.h"
@@ -407,6 +408,158 @@ PyObject* grouped_gemm_fp4(Args a) {
     return a[6] == Py_None ? wrap(out) : same(a[6]);
 }
 
+// A [rows, heads, D] CUDA tensor with packed features. Strides of a single row or head are never used: a packed tensor's stand for them.
+struct Heads {
+    void* p;
+    int64_t T, H, D, ld_t, ld_h;
+};
+Heads heads(const at::Tensor& t, const char* what) {
+    need(t.is_cuda() && t.dim() == 3 && (t.stride(2) == 1 || t.size(2) <= 1), what);
+    return {t.data_ptr(), t.size(0), t.size(1), t.size(2), t.size(0) > 1 ? t.stride(0) : t.size(1) * t.size(2),
+            t.size(1) > 1 ? t.stride(1) : t.size(2)};
+}
+Heads heads_bf16(const at::Tensor& t, at::Device dev, const char* what) {
+    need(t.scalar_type() == at::kBFloat16 && t.device() == dev, what);
+    return heads(t, what);
+}
+
+// (x, table, positions, interleaved, out)
+template <bool BACKWARD>
+PyObject* rope_call(Args a) {
+    const at::Tensor &x = tensor(a[0], "rope: x"), &table = tensor(a[1], "rope: table");
+    const Heads h = heads(x, "rope: x must be a [T, H, D] CUDA tensor with unit stride along D");
+    const at::ScalarType type = x.scalar_type();
+    need(type == at::kFloat || type == at::kBFloat16 || type == at::kHalf, "rope: x must be fp32, BF16 or FP16");
+    const mx_out_dtype code = type == at::kFloat ? MX_OUT_F32 : type == at::kBFloat16 ? MX_OUT_BF16 : MX_OUT_F16;
+    const at::Device dev = x.device();
+    need(table.dim() == 2, "rope: table must be fp32 [positions, rot]");
+    const void* pt = packed(table, at::kFloat, table.numel(), dev, "rope: table must be a contiguous fp32 tensor [positions, rot]");
+    const at::Tensor* pos = optional_tensor(a[2], "rope: positions");
+    bool pos64 = false;
+    const void* pp = nullptr;
+    if (pos) {
+        pos64 = pos->scalar_type() == at::kLong;
+        pp = packed(*pos, pos64 ? at::kLong : at::kInt, h.T, dev, "rope: positions must be int32 or int64 [T]");
+    }
+    const bool interleaved = truth(a[3]);
+    const Place place(x);
+    const at::Tensor out = a[4] == Py_None ? fresh({h.T, h.H, h.D}, type) : tensor(a[4], "rope: out");
+    const Heads o = heads(out, "rope: out must be like x");
+    need(o.T == h.T && o.H == h.H && o.D == h.D && out.scalar_type() == type && out.device() == dev, "rope: out must be like x");
+    need(o.p != h.p || (o.ld_t == h.ld_t && o.ld_h == h.ld_h), "rope: out on x's memory must be x itself");
+    check((BACKWARD ? mx_rope_bwd : mx_rope)(h.p, code, h.T, h.H, h.D, h.ld_t, h.ld_h, static_cast<const float*>(pt), table.size(0),
+                                             table.size(1), pp, pos64, interleaved, o.p, o.ld_t, o.ld_h, place.stream),
+          BACKWARD ? "mx_rope_bwd" : "mx_rope");
+    return a[4] == Py_None ? wrap(out) : same(a[4]);
+}
+PyObject* rope(Args a) { return rope_call<false>(a); }
+PyObject* rope_backward(Args a) { return rope_call<true>(a); }
+
+// The cache (k, v, k_scale, v_scale), page_table, lengths and row_offsets of a call, for `rows` rows on `dev`.
+mx_cache_batch cache_batch(PyObject* cache, PyObject* table, PyObject* lengths, PyObject* offsets, int64_t rows, at::Device dev) {
+    need(PyTuple_Check(cache) && PyTuple_GET_SIZE(cache) == 4, "cache: a tuple (k, v, k_scale, v_scale)");
+    const at::Tensor* t[4];
+    for (int i = 0; i < 4; ++i) t[i] = &tensor(PyTuple_GET_ITEM(cache, i), "cache: a tuple of tensors (k, v, k_scale, v_scale)");
+    mx_cache_batch c{};
+    const char* codes = "cache: k and v must be uint8 CUDA tensors [pages, heads, page_size, head_dim], packed within a page";
+    need(t[0]->dim() == 4, codes);
+    c.pages = t[0]->size(0), c.heads = t[0]->size(1), c.page_size = t[0]->size(2), c.head_dim = t[0]->size(3);
+    for (int i = 0; i < 2; ++i) {
+        const at::Tensor& x = *t[i];
+        need(x.dim() == 4 && x.scalar_type() == at::kByte && x.device() == dev && x.sizes() == t[0]->sizes() && x.stride(3) == 1 &&
+                 x.stride(2) == c.head_dim && (c.heads <= 1 || x.stride(1) == c.page_size * c.head_dim),
+             codes);
+        const at::Tensor& s = *t[2 + i];
+        need(s.dim() == 2 && s.scalar_type() == at::kByte && s.device() == dev && s.size(0) == c.pages && s.size(1) == c.heads &&
+                 (c.heads <= 1 || s.stride(1) == 1),
+             "cache: k_scale and v_scale must be uint8 CUDA tensors [pages, heads] with unit stride along the heads");
+    }
+    c.k = ptr<uint8_t>(t[0]->data_ptr()), c.v = ptr<uint8_t>(t[1]->data_ptr());
+    c.k_scale = ptr<uint8_t>(t[2]->data_ptr()), c.v_scale = ptr<uint8_t>(t[3]->data_ptr());
+    c.k_stride = t[0]->stride(0), c.v_stride = t[1]->stride(0), c.ks_stride = t[2]->stride(0), c.vs_stride = t[3]->stride(0);
+    const at::Tensor &pt = tensor(table, "page_table"), &ln = tensor(lengths, "lengths");
+    need(pt.scalar_type() == at::kInt && pt.dim() == 2 && pt.device() == dev && (pt.size(1) <= 1 || pt.stride(1) == 1),
+         "page_table must be int32 [sequences, pages] with unit stride along the pages");
+    c.sequences = pt.size(0), c.width = pt.size(1);
+    c.page_table = static_cast<const int32_t*>(pt.data_ptr());
+    c.ld_table = pt.size(0) > 1 ? pt.stride(0) : pt.size(1);
+    c.lengths = static_cast<const int32_t*>(packed(ln, at::kInt, c.sequences, dev, "lengths must be int32 [sequences]"));
+    const at::Tensor* off = optional_tensor(offsets, "row_offsets");
+    if (off) c.row_offsets = static_cast<const int32_t*>(packed(*off, at::kInt, c.sequences + 1, dev, "row_offsets must be int32 [sequences + 1]"));
+    need(off || rows == c.sequences, "without row_offsets there is one row per sequence");
+    c.rows = rows;
+    return c;
+}
+
+// (k, v, cache, page_table, lengths, row_offsets, q, table, interleaved, out)
+PyObject* cache_append(Args a) {
+    const at::Tensor &k = tensor(a[0], "cache_append: k"), &v = tensor(a[1], "cache_append: v");
+    need(k.is_cuda(), "cache_append: CUDA tensors");
+    const at::Device dev = k.device();
+    const char* kv = "cache_append: k and v must be BF16 CUDA tensors [rows, heads, head_dim] with unit stride along head_dim";
+    const Heads hk = heads_bf16(k, dev, kv), hv = heads_bf16(v, dev, kv);
+    const mx_cache_batch c = cache_batch(a[2], a[3], a[4], a[5], hk.T, dev);
+    need(hk.H == c.heads && hk.D == c.head_dim && hv.T == hk.T && hv.H == c.heads && hv.D == c.head_dim, kv);
+    const at::Tensor* table = optional_tensor(a[7], "cache_append: table");
+    const void* pt = nullptr;
+    int64_t positions = 0, rot = 0;
+    if (table) {
+        need(table->dim() == 2, "cache_append: table must be fp32 [positions, rot]");
+        pt = packed(*table, at::kFloat, table->numel(), dev, "cache_append: table must be a contiguous fp32 tensor [positions, rot]");
+        positions = table->size(0), rot = table->size(1);
+    }
+    const at::Tensor* q = optional_tensor(a[6], "cache_append: q");
+    const Place place(k);
+    at::Tensor out;
+    Heads hq{}, ho{};
+    if (q) {
+        const char* what = "cache_append: q and out must be BF16 CUDA tensors [rows, q_heads, head_dim]";
+        hq = heads_bf16(*q, dev, what);
+        need(hq.T == hk.T && hq.D == c.head_dim, what);
+        out = a[9] == Py_None ? fresh({hq.T, hq.H, hq.D}, at::kBFloat16) : tensor(a[9], "cache_append: out");
+        ho = heads_bf16(out, dev, what);
+        need(ho.T == hq.T && ho.H == hq.H && ho.D == hq.D, what);
+        need(ho.p != hq.p || (ho.ld_t == hq.ld_t && ho.ld_h == hq.ld_h), "cache_append: out on q's memory must be q itself");
+    }
+    check(mx_cache_append(&c, hk.p, hk.ld_t, hk.ld_h, hv.p, hv.ld_t, hv.ld_h, static_cast<const float*>(pt), positions, rot, truth(a[8]),
+                          hq.p, hq.H, hq.ld_t, hq.ld_h, ho.p, ho.ld_t, ho.ld_h, place.stream),
+          "mx_cache_append");
+    return !q ? same(Py_None) : a[9] == Py_None ? wrap(out) : same(a[9]);
+}
+
+// (q, cache, page_table, lengths, row_offsets, scale or None, window, want lse, out)
+PyObject* cache_attention(Args a) {
+    const at::Tensor& q = tensor(a[0], "cache_attention: q");
+    need(q.is_cuda(), "cache_attention: CUDA tensors");
+    const at::Device dev = q.device();
+    const char* what = "cache_attention: q and out must be BF16 CUDA tensors [rows, q_heads, head_dim] with unit stride along head_dim";
+    const Heads h = heads_bf16(q, dev, what);
+    const mx_cache_batch c = cache_batch(a[1], a[2], a[3], a[4], h.T, dev);
+    need(h.D == c.head_dim, what);
+    const float scale = a[5] == Py_None ? static_cast<float>(1.0 / std::sqrt(static_cast<double>(h.D))) : static_cast<float>(number(a[5]));
+    const int64_t window = integer(a[6]);
+    const bool want = truth(a[7]);
+    const int64_t bytes = mx_cache_attention_workspace_bytes(h.D, h.T, h.H);
+    if (bytes < 0) throw Refused{MX_ERR_SHAPE, "cache_attention: head_dim 64 or 128, at least one head"};
+    const Place place(q);
+    const at::Tensor ws = fresh({bytes}, at::kByte);
+    at::Tensor out, lse;
+    PyObject *po = nullptr, *pl = nullptr;
+    if (a[8] != Py_None) {
+        po = want ? out_item(a[8], 0, 2, "cache_attention: out (out, lse)") : a[8];
+        if (want) pl = out_item(a[8], 1, 2, "cache_attention: out (out, lse)");
+    }
+    out = po ? tensor(po, "cache_attention: out") : fresh({h.T, h.H, h.D}, at::kBFloat16);
+    const Heads o = heads_bf16(out, dev, what);
+    need(o.T == h.T && o.H == h.H && o.D == h.D, what);
+    if (want) lse = pl ? tensor(pl, "cache_attention: lse") : fresh({h.T, h.H}, at::kFloat);
+    float* l = want ? ptr<float>(packed(lse, at::kFloat, h.T * h.H, dev, "cache_attention: lse must be fp32 [rows, q_heads]")) : nullptr;
+    check(mx_cache_attention(&c, h.p, h.H, h.ld_t, h.ld_h, scale, window, o.p, o.ld_t, o.ld_h, l, ws.data_ptr(), place.stream),
+          "mx_cache_attention");
+    PyObject* r = po ? same(po) : wrap(out);
+    return want ? tuple({r, pl ? same(pl) : wrap(lse)}) : r;
+}
+
 // Argument count, refusals as MxError(status, what), and torch's and Python's own errors as they are.
 template <PyObject* (*F)(Args), Py_ssize_t N>
 PyObject* call(PyObject*, PyObject* const* args, Py_ssize_t nargs) {
@@ -444,6 +597,10 @@ PyMethodDef methods[] = {MX_METHOD(route, 10),
                          MX_METHOD(dequantize_fp4, 4),
                          MX_METHOD(gemm_fp4, 6),
                          MX_METHOD(grouped_gemm_fp4, 7),
+                         MX_METHOD(rope, 5),
+                         MX_METHOD(rope_backward, 5),
+                         MX_METHOD(cache_append, 10),
+                         MX_METHOD(cache_attention, 9),
                          {"set_error", set_error, METH_O, nullptr},
                          {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_mxcall", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};

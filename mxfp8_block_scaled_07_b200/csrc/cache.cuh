@@ -1,0 +1,347 @@
+// A paged cache of keys and values in E4M3 with one E8M0 scale per page and head, and tokens appended to it.
+//
+// Codes [pages, heads, page, D] (a page's tokens of one head are consecutive: page x D bytes), scale bytes [pages,
+// heads]. The grid is the library's (OCP MX v1.0) with the block made of a page's tokens of one head: e = floor(log2 amax) - 8,
+// code = RNE(x 2^-e) saturated to +-448. A page that tokens are appended to over several calls keeps e from falling:
+// when the new tokens need a larger one the page's other codes are rounded anew to it, which a power of two makes exact but for
+// codes that become subnormal. A page with NaN or infinity has scale byte 0xFF and zero codes until it is begun anew.
+//
+// Keys are rotated on the way. A code hangs on the last bits of the rotation, so the sum of the two products is formed
+// exactly (as an unevaluated sum of fp32 numbers) and rounded to odd, which rounds to E4M3 as the exact value does.
+#pragma once
+#include <cuda_bf16.h>
+
+#include <cstdint>
+
+#include "ptx.cuh"
+#include "quantize.cuh"
+#include "rope.cuh"
+
+namespace mx {
+
+// s + t == a + b exactly (Knuth's two-sum).
+__device__ __forceinline__ float two_sum(float a, float b, float& t) {
+    const float s = __fadd_rn(a, b), bb = __fsub_rn(s, a);
+    t = __fadd_rn(__fsub_rn(a, __fsub_rn(s, bb)), __fsub_rn(b, bb));
+    return s;
+}
+
+// a c - b s rounded to odd in fp32 (towards zero, and the last bit set unless exact): rounding that to at most 22
+// bits gives what rounding the exact value would.
+__device__ __forceinline__ float diff_to_odd(float a, float c, float b, float s) {
+    const float p = __fmul_rn(a, c), q = __fmul_rn(b, s);
+    const float ep = __fmaf_rn(a, c, -p), eq = __fmaf_rn(b, s, -q);
+    float t, lo;
+    const float hi0 = two_sum(p, -q, t);
+    const float hi = two_sum(hi0, __fadd_rn(t, __fsub_rn(ep, eq)), lo);
+    uint32_t bits = __float_as_uint(hi);
+    if ((bits & 0x7F800000u) == 0x7F800000u || lo == 0.0f) return hi;
+    if ((bits << 1) == 0) return lo;
+    if ((__float_as_uint(lo) ^ bits) >> 31) bits -= 1;
+    return __uint_as_float(bits | 1u);
+}
+
+__device__ __forceinline__ float bf16_lo(uint32_t w) { return __uint_as_float(w << 16); }
+__device__ __forceinline__ float bf16_hi(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
+
+// 2^(s - 127) of a scale byte below 255.
+__device__ __forceinline__ float scale_value(uint32_t s) { return __uint_as_float(s ? s << 23 : 1u << 22); }
+// Scale byte from the largest magnitude (fp32 bits without the sign) of a block: max(E - 8, 0), 0xFF for NaN or Inf.
+__device__ __forceinline__ uint32_t scale_byte_of(uint32_t amax_bits) {
+    const int E = static_cast<int>(amax_bits >> 23);
+    return E == 255 ? 255u : static_cast<uint32_t>(max(E - 8, 0));
+}
+__device__ __forceinline__ float inv_scale_of(uint32_t s) { return __uint_as_float((254u - s) << 23); }
+
+// Two values to two E4M3 codes (the first in the low byte).
+__device__ __forceinline__ uint32_t e4m3x2(float lo, float hi) {
+    uint16_t r;
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+// Two E4M3 codes (16 bits) to f16x2, exactly.
+__device__ __forceinline__ uint32_t f16x2_of_e4m3(uint32_t two) {
+    uint32_t r;
+    asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, l;\n\t}" : "=r"(r) : "r"(two));
+    return r;
+}
+__device__ __forceinline__ uint32_t f16x2_of_e4m3_hi(uint32_t two) {
+    uint32_t r;
+    asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, h;\n\t}" : "=r"(r) : "r"(two));
+    return r;
+}
+
+// Four codes rounded anew after a factor (a power of two below 1).
+__device__ __forceinline__ uint32_t rescaled(uint32_t codes, float f) {
+    const uint32_t a = f16x2_of_e4m3(codes), b = f16x2_of_e4m3_hi(codes);
+    const float2 x = __half22float2(*reinterpret_cast<const __half2*>(&a)), y = __half22float2(*reinterpret_cast<const __half2*>(&b));
+    return e4m3x2(x.x * f, x.y * f) | (e4m3x2(y.x * f, y.y * f) << 16);
+}
+
+struct CacheView {
+    uint8_t *k, *v;               // codes; a page's [heads, page, D] block is packed
+    uint8_t *ks, *vs;             // scale bytes; a page's [heads] are packed
+    int64_t k_page, v_page, ks_page, vs_page;      // bytes from one page to the next
+    const int32_t* table;         // page ids [B, width], row stride ld_table
+    int64_t ld_table;
+    const int32_t* lengths;       // [B]
+    const int32_t* row_offsets;   // [B + 1], or null: one row per sequence
+    int64_t pages;
+    int32_t width, B, T, Hkv, page_shift;
+};
+
+// Rows [first, first + n) of the batch are sequence b's, whatever the offsets hold: inside [0, T).
+__device__ __forceinline__ void rows_of(const CacheView& c, int b, int& first, int& n) {
+    if (!c.row_offsets) {
+        first = b, n = 1;
+        return;
+    }
+    first = min(max(c.row_offsets[b], 0), c.T);
+    n = min(max(c.row_offsets[b + 1] - first, 0), c.T - first);
+}
+
+// Page id of a sequence's page, or -1 outside the table or the pool.
+__device__ __forceinline__ int64_t page_id(const CacheView& c, int b, int64_t index) {
+    if (index >= c.width) return -1;
+    const int32_t id = c.table[b * c.ld_table + index];
+    return id < 0 || id >= c.pages ? -1 : id;
+}
+
+struct AppendArgs {
+    CacheView c;
+    const __nv_bfloat16 *k, *v, *q;
+    __nv_bfloat16* q_out;
+    const float* table;           // rotations [positions, rot], or null: none
+    int64_t ldk_t, ldk_h, ldv_t, ldv_h, ldq_t, ldq_h, ldo_t, ldo_h;
+    int64_t positions;
+    uint32_t* err;
+    int Hq, D, rot, interleaved;
+    int kv_blocks;                // blocks that append; the ones behind them rotate queries
+    FastDiv heads2;               // 2 * Hkv
+};
+
+// Elements [d, d + 8) of a row, rotated and rounded to odd. x: the row's head.
+__device__ __forceinline__ void rotated8(const __nv_bfloat16* x, int d, const float* angles, int rot, bool interleaved, float (&y)[8]) {
+    const uint4 w = *reinterpret_cast<const uint4*>(x + d);
+    const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) y[2 * i] = bf16_lo(u[i]), y[2 * i + 1] = bf16_hi(u[i]);
+    if (d >= rot) return;
+    const int h = rot / 2;
+    if (interleaved) {
+        float c[4], s[4];
+        load_angles<4>(angles + d / 2, c);
+        load_angles<4>(angles + h + d / 2, s);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const float a = y[2 * i], b = y[2 * i + 1];
+            y[2 * i] = diff_to_odd(a, c[i], b, s[i]);
+            y[2 * i + 1] = diff_to_odd(b, c[i], -a, s[i]);
+        }
+        return;
+    }
+    const bool low = d < h;
+    const int i0 = low ? d : d - h;
+    const uint4 o = *reinterpret_cast<const uint4*>(x + (low ? d + h : d - h));
+    const uint32_t v[4] = {o.x, o.y, o.z, o.w};
+    float c[8], s[8];
+    load_angles<8>(angles + i0, c);
+    load_angles<8>(angles + h + i0, s);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const float other = i & 1 ? bf16_hi(v[i / 2]) : bf16_lo(v[i / 2]);
+        y[i] = diff_to_odd(y[i], c[i], low ? other : -other, s[i]);
+    }
+}
+
+// The angles of a position: null where there is no rotation, `bad` where the position lies outside the table.
+__device__ __forceinline__ const float* angles_of(const AppendArgs& a, int64_t pos, bool& bad) {
+    bad = a.table && (pos < 0 || pos >= a.positions);
+    if (bad && pos >= 0) atomicOr(a.err, kErrBadIndex);
+    return a.table && !bad ? a.table + pos * a.rot : nullptr;
+}
+
+// Sequence of a row: how many sequences begin at or before it, by a whole warp (offsets do not decrease).
+__device__ __forceinline__ int sequence_of_row(const CacheView& c, int row) {
+    if (!c.row_offsets) return row;
+    int n = 0;
+    for (int b0 = 0; b0 < c.B; b0 += 32) {
+        const int b = b0 + (threadIdx.x & 31);
+        n += __popc(__ballot_sync(0xFFFFFFFFu, b < c.B && c.row_offsets[min(b, c.B)] <= row));
+    }
+    return n - 1;
+}
+
+// One warp: one row of queries, all its heads. Rows that no sequence holds are left alone.
+__device__ __forceinline__ void rotate_queries(const AppendArgs& a, int row) {
+    const CacheView& c = a.c;
+    const int b = sequence_of_row(c, row);
+    if (b < 0) return;
+    int first, n;
+    rows_of(c, b, first, n);
+    if (row < first || row >= first + n) return;
+    const int64_t pos = static_cast<int64_t>(c.lengths[b]) - n + (row - first);
+    bool bad;
+    const float* angles = angles_of(a, pos, bad);
+    bad |= pos < 0;
+    const int lanes = a.D / 8;
+    for (int i = threadIdx.x & 31; i < a.Hq * lanes; i += 32) {
+        const int h = i / lanes, d = (i - h * lanes) * 8;
+        float y[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+        if (!bad) rotated8(a.q + row * a.ldq_t + h * a.ldq_h, d, angles, angles ? a.rot : 0, a.interleaved, y);
+        uint32_t o[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const __nv_bfloat162 p = __floats2bfloat162_rn(y[2 * j], y[2 * j + 1]);
+            o[j] = *reinterpret_cast<const uint32_t*>(&p);
+        }
+        *reinterpret_cast<uint4*>(a.q_out + row * a.ldo_t + h * a.ldo_h + d) = make_uint4(o[0], o[1], o[2], o[3]);
+    }
+}
+
+__device__ __forceinline__ uint32_t amax_bits8(const float (&y)[8]) {
+    uint32_t m = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) m = max(m, __float_as_uint(y[i]) & 0x7FFFFFFFu);
+    return m;
+}
+__device__ __forceinline__ uint2 encode8(const float (&y)[8], float inv) {
+    return make_uint2(e4m3x2(y[0] * inv, y[1] * inv) | (e4m3x2(y[2] * inv, y[3] * inv) << 16),
+                      e4m3x2(y[4] * inv, y[5] * inv) | (e4m3x2(y[6] * inv, y[7] * inv) << 16));
+}
+
+constexpr int kAppendOneThreads = 128;
+
+// One new token per sequence: a warp per (sequence, head, keys or values), D / 8 lanes of eight elements.
+template <int D>
+__global__ void __launch_bounds__(kAppendOneThreads) append_one_kernel(const __grid_constant__ AppendArgs a) {
+    grid_wait();
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const CacheView& c = a.c;
+    if (static_cast<int>(blockIdx.x) >= a.kv_blocks) {
+        const int row = (blockIdx.x - a.kv_blocks) * (kAppendOneThreads / 32) + warp;
+        if (row < c.T) rotate_queries(a, row);
+        return;
+    }
+    const uint32_t item = blockIdx.x * (kAppendOneThreads / 32) + warp;
+    const int b = a.heads2.div(item), r = item - b * a.heads2.d, h = r >> 1;
+    if (b >= c.B) return;
+    const bool keys = !(r & 1);
+    const int64_t pos = static_cast<int64_t>(c.lengths[b]) - 1;
+    if (pos < 0) return;
+    const int slot = static_cast<int>(pos & ((1 << c.page_shift) - 1));
+    const int64_t id = page_id(c, b, pos >> c.page_shift);
+    if (id < 0) {
+        if (lane == 0) atomicOr(a.err, kErrBadIndex);
+        return;
+    }
+    uint8_t* codes = (keys ? c.k + id * c.k_page : c.v + id * c.v_page) + (static_cast<int64_t>(h) << c.page_shift) * D;
+    uint8_t* scale = (keys ? c.ks + id * c.ks_page : c.vs + id * c.vs_page) + h;
+    const uint32_t was = slot ? *scale : 0u;
+    float y[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+    if (lane < D / 8) {
+        if (keys) {
+            bool bad;
+            const float* angles = angles_of(a, pos, bad);
+            if (!bad) rotated8(a.k + b * a.ldk_t + h * a.ldk_h, lane * 8, angles, angles ? a.rot : 0, a.interleaved, y);
+        } else {
+            rotated8(a.v + b * a.ldv_t + h * a.ldv_h, lane * 8, nullptr, 0, false, y);
+        }
+    }
+    const uint32_t s = max(was, scale_byte_of(__reduce_max_sync(0xFFFFFFFFu, amax_bits8(y))));
+    if (s > was && slot) {                       // the page's other codes, 16 at a time
+        const float f = s == 255 ? 0.0f : scale_value(was) * inv_scale_of(s);
+        for (int i = lane; i < (D / 16) << c.page_shift; i += 32) {
+            if (i / (D / 16) == slot) continue;
+            uint4 w = *reinterpret_cast<const uint4*>(codes + i * 16);
+            w = s == 255 ? make_uint4(0, 0, 0, 0) : make_uint4(rescaled(w.x, f), rescaled(w.y, f), rescaled(w.z, f), rescaled(w.w, f));
+            *reinterpret_cast<uint4*>(codes + i * 16) = w;
+        }
+    }
+    if (lane < D / 8)
+        *reinterpret_cast<uint2*>(codes + slot * D + lane * 8) = s == 255 ? make_uint2(0, 0) : encode8(y, inv_scale_of(s));
+    if (lane == 0) *scale = static_cast<uint8_t>(s);
+}
+
+// Any number of new tokens per sequence: a block per (page of a sequence, head, keys or values), CH pieces of eight
+// elements per thread (page x D = 8 CH threads). Blocks are numbered without a prefix sum: sequence b's pages start at
+// floor(row_offsets[b] / page) + 2 b, which leaves room for all that its tokens can touch (n tokens touch at most n / page +
+// 2 pages); blocks for which nothing is left return.
+template <int D, int CH, int THREADS>
+__global__ void __launch_bounds__(THREADS) append_kernel(const __grid_constant__ AppendArgs a) {
+    grid_wait();
+    __shared__ uint32_t warp_max[THREADS / 32];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const CacheView& c = a.c;
+    if (static_cast<int>(blockIdx.x) >= a.kv_blocks) {
+        const int row = (blockIdx.x - a.kv_blocks) * (THREADS / 32) + warp;
+        if (row < c.T) rotate_queries(a, row);
+        return;
+    }
+    const int item = a.heads2.div(blockIdx.x), r = blockIdx.x - item * a.heads2.d, h = r >> 1;
+    const bool keys = !(r & 1);
+    const int ps = c.page_shift, page = 1 << ps;
+    int count = 0;
+    for (int b0 = 0; b0 < c.B; b0 += 32) {
+        const int b = b0 + lane;
+        count += __popc(__ballot_sync(0xFFFFFFFFu, b < c.B && (min(max(c.row_offsets[min(b, c.B)], 0), c.T) >> ps) + 2 * b <= item));
+    }
+    const int b = count - 1;
+    if (b < 0) return;
+    int first, n;
+    rows_of(c, b, first, n);
+    const int64_t len = c.lengths[b], start = len - n;
+    const int nth = item - ((first >> ps) + 2 * b);
+    const int64_t index = (max(start, int64_t(0)) >> ps) + nth;
+    const int64_t base = index << ps;            // position of the page's first token
+    if (n <= 0 || nth < 0 || base >= len) return;
+    const int lo = static_cast<int>(max(start - base, int64_t(0))), hi = static_cast<int>(min(len - base, int64_t(page)));
+    const int64_t id = page_id(c, b, index);
+    if (id < 0) {
+        if (threadIdx.x == 0) atomicOr(a.err, kErrBadIndex);
+        return;
+    }
+    uint8_t* codes = (keys ? c.k + id * c.k_page : c.v + id * c.v_page) + (static_cast<int64_t>(h) << ps) * D;
+    uint8_t* scale = (keys ? c.ks + id * c.ks_page : c.vs + id * c.vs_page) + h;
+    const uint32_t was = lo ? *scale : 0u;
+    float y[CH][8];
+    uint32_t m = 0;
+#pragma unroll
+    for (int i = 0; i < CH; ++i) {
+        const int at = i * THREADS + threadIdx.x, tok = at / (D / 8), d = (at % (D / 8)) * 8;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) y[i][j] = 0.0f;
+        if (tok >= lo && tok < hi) {
+            const int64_t row = first + (base + tok - start);
+            if (keys) {
+                bool bad;
+                const float* angles = angles_of(a, base + tok, bad);
+                if (!bad) rotated8(a.k + row * a.ldk_t + h * a.ldk_h, d, angles, angles ? a.rot : 0, a.interleaved, y[i]);
+            } else {
+                rotated8(a.v + row * a.ldv_t + h * a.ldv_h, d, nullptr, 0, false, y[i]);
+            }
+        }
+        m = max(m, amax_bits8(y[i]));
+    }
+    m = __reduce_max_sync(0xFFFFFFFFu, m);
+    if (lane == 0) warp_max[warp] = m;
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < THREADS / 32; ++w) m = max(m, warp_max[w]);
+    const uint32_t s = max(was, scale_byte_of(m));
+    const float inv = s == 255 ? 0.0f : inv_scale_of(s), f = s == 255 ? 0.0f : scale_value(was) * inv;
+#pragma unroll
+    for (int i = 0; i < CH; ++i) {
+        const int at = i * THREADS + threadIdx.x, tok = at / (D / 8);
+        uint2* p = reinterpret_cast<uint2*>(codes + at * 8);
+        if (tok >= lo && tok < hi) {
+            *p = s == 255 ? make_uint2(0, 0) : encode8(y[i], inv);
+        } else if (lo > 0 && s > was) {
+            const uint2 w = *p;
+            *p = s == 255 ? make_uint2(0, 0) : make_uint2(rescaled(w.x, f), rescaled(w.y, f));
+        }
+    }
+    if (threadIdx.x == 0) *scale = static_cast<uint8_t>(s);
+}
+
+}  // namespace mx

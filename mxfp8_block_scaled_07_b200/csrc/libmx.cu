@@ -1,6 +1,6 @@
 // libmx: the C-ABI entry points declared in include/mx.h. Host-side argument checks, tensor-map
 // construction and kernel launches; the kernels themselves are in quantize.cuh, fp4.cuh, gemm.cuh,
-// route.cuh, experts.cuh, swizzle.cuh, blockwise.cuh and grid_equal.cuh. Nothing here allocates device memory or synchronizes (except mx_device_error).
+// route.cuh, experts.cuh, rope.cuh, cache.cuh, attend.cuh, swizzle.cuh, blockwise.cuh and grid_equal.cuh. Nothing here allocates device memory or synchronizes (except mx_device_error).
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -12,7 +12,9 @@
 #include <unordered_map>
 
 #include "../../include/mx.h"
+#include "attend.cuh"
 #include "blockwise.cuh"
+#include "cache.cuh"
 #include "experts.cuh"
 #include "fp4.cuh"
 #include "gemm.cuh"
@@ -21,6 +23,7 @@
 #include "ptx.cuh"
 #include "quantize.cuh"
 #include "quantize_tma.cuh"
+#include "rope.cuh"
 #include "route.cuh"
 #include "swizzle.cuh"
 
@@ -1497,6 +1500,301 @@ mx_status mx_combine_bwd(const void* dy, mx_out_dtype y_dtype, int64_t ld_dy, co
     a.vec = rows_vec(dy, ld_dy, y_dtype) && (!d_weights || rows_vec(c, ld_c, c_dtype)) &&
             (!d_c || rows_vec(d_c, ld_dc, c_dtype));
     return launch_combine_types(a, c_dtype, y_dtype, true, d, stream);
+}
+
+}  // extern "C"
+
+// ---- rotary positions, cache, attention ---------------------------------------------------------------------
+
+namespace mx {
+namespace {
+
+// Heads that one thread walks: 8, 4, 2 or 1, the most that leave kRopeManyThreads threads.
+constexpr int64_t kRopeManyThreads = 148 * 1024;
+
+template <class T, int V, bool IL>
+mx_status launch_rope(RopeArgs& a, const DeviceInfo* d, mx_stream stream) {
+    a.pair_lanes = a.rot / (IL ? V : 2 * V);
+    const int64_t lanes = a.pair_lanes + (a.copy ? ceil_div(a.D - a.rot, V) : 0);
+    int64_t heads = 8;
+    while (heads > 1 && a.T * lanes * ceil_div(a.H, heads) < kRopeManyThreads) heads /= 2;
+    const int64_t chunks = ceil_div(a.H, heads);
+    if (a.T * lanes * chunks >= kInt32End - kRopeThreads) return MX_ERR_SHAPE;
+    a.lanes = FastDiv::of(lanes);
+    a.chunks = FastDiv::of(chunks);
+    const int64_t grid = ceil_div(a.T * lanes * chunks, kRopeThreads);
+    if (heads >= 4) return launch_behind(rope_kernel<T, V, IL, 4>, grid, kRopeThreads, 0, 1, stream, a);
+    return launch_behind(rope_kernel<T, V, IL, 1>, grid, kRopeThreads, 0, 1, stream, a);
+}
+
+template <class T>
+mx_status launch_rope_type(RopeArgs& a, bool interleaved, const DeviceInfo* d, mx_stream stream) {
+    constexpr int V = 16 / sizeof(T);
+    // 16-byte pieces: everything that is accessed as one begins on a multiple of V elements.
+    const int64_t pieces = int64_t(a.D) | a.ldx_t | a.ldx_h | a.ldy_t | a.ldy_h | (interleaved ? a.rot : a.rot / 2);
+    const bool wide = pieces % V == 0 && aligned16(a.x) && aligned16(a.y) && aligned16(a.table) &&
+                      a.rot % 8 == 0;            // the sines' half row of the table
+    if (wide) return interleaved ? launch_rope<T, V, true>(a, d, stream) : launch_rope<T, V, false>(a, d, stream);
+    return interleaved ? launch_rope<T, 2, true>(a, d, stream) : launch_rope<T, 1, false>(a, d, stream);
+}
+
+mx_status rope(const void* x, mx_out_dtype dtype, int64_t T, int64_t H, int64_t D, int64_t ldx_t, int64_t ldx_h,
+               const float* table, int64_t positions, int64_t rot, const void* pos, int pos64, int interleaved, void* y,
+               int64_t ldy_t, int64_t ldy_h, bool negate, mx_stream stream) {
+    if (T < 0 || H < 0 || D < 1 || rot < 2 || positions < 0 || !(dtype == MX_OUT_F16 || elt_ok(dtype))) return MX_ERR_ARG;
+    if (D > 1024 || rot > D || rot > 2 * kRopeMaxPairs || rot % 2 != 0 || T >= kInt32End || H >= kInt32End) return MX_ERR_SHAPE;
+    if (H > 1 && (std::abs(ldx_h) < D || std::abs(ldy_h) < D)) return MX_ERR_SHAPE;
+    if (T == 0 || H == 0) return MX_OK;
+    if (!x || !y || (!table && positions > 0)) return MX_ERR_ARG;
+    const int64_t esz = dtype == MX_OUT_F32 ? 4 : 2;
+    if (reinterpret_cast<uintptr_t>(x) % esz || reinterpret_cast<uintptr_t>(y) % esz || !word_aligned(table) ||
+        reinterpret_cast<uintptr_t>(pos) % (pos64 ? 8 : 4))
+        return MX_ERR_ALIGN;
+    const DeviceInfo* d = nullptr;
+    if (mx_status st = check_device(&d)) return st;
+    RopeArgs a{};
+    a.x = x;
+    a.y = y;
+    a.table = table;
+    a.pos = pos;
+    a.ldx_t = T > 1 ? ldx_t : 0;
+    a.ldx_h = H > 1 ? ldx_h : 0;
+    a.ldy_t = T > 1 ? ldy_t : 0;
+    a.ldy_h = H > 1 ? ldy_h : 0;
+    a.positions = positions;
+    a.T = T;
+    a.err = d->status;
+    a.H = static_cast<int>(H);
+    a.D = static_cast<int>(D);
+    a.rot = static_cast<int>(rot);
+    a.pos64 = pos64 != 0;
+    a.negate = negate;
+    a.copy = x != y;
+    if (dtype == MX_OUT_BF16) return launch_rope_type<__nv_bfloat16>(a, interleaved, d, stream);
+    if (dtype == MX_OUT_F16) return launch_rope_type<__half>(a, interleaved, d, stream);
+    return launch_rope_type<float>(a, interleaved, d, stream);
+}
+
+// A BF16 tensor [rows, heads, D] whose pieces of eight are 16-byte aligned. Strides of a single row or head are not used.
+bool pieces_ok(const void* p, int64_t ld_t, int64_t ld_h) { return aligned16(p) && ld_t % 8 == 0 && ld_h % 8 == 0; }
+
+constexpr int64_t kCacheMaxSequences = int64_t(1) << 24;
+constexpr int64_t kCacheMaxHeads = 1024, kCacheMaxQueryHeads = 4096;
+
+// The batch's sizes and pointers, checked; *empty: nothing to do.
+mx_status cache_checks(const mx_cache_batch* c, bool* empty) {
+    if (!c) return MX_ERR_ARG;
+    if (c->pages < 0 || c->heads < 1 || c->page_size < 1 || c->head_dim < 1 || c->width < 0 || c->sequences < 0 || c->rows < 0)
+        return MX_ERR_ARG;
+    if ((c->head_dim != 64 && c->head_dim != 128) || c->heads > kCacheMaxHeads ||
+        (c->page_size != 16 && c->page_size != 32 && c->page_size != 64 && c->page_size != 128) || c->pages >= kInt32End ||
+        c->width >= kInt32End || c->sequences >= kCacheMaxSequences || c->rows >= kInt32End)
+        return MX_ERR_SHAPE;
+    if (!c->row_offsets && c->rows != c->sequences) return MX_ERR_SHAPE;
+    *empty = c->rows == 0 || c->sequences == 0;
+    if (*empty) return MX_OK;
+    if (!c->lengths || (c->width > 0 && !c->page_table) || (c->pages > 0 && (!c->k || !c->v || !c->k_scale || !c->v_scale)))
+        return MX_ERR_ARG;
+    const int64_t block = c->heads * c->page_size * c->head_dim;
+    if (c->pages > 1 && (c->k_stride < block || c->v_stride < block || c->ks_stride < c->heads || c->vs_stride < c->heads))
+        return MX_ERR_SHAPE;
+    if (c->sequences > 1 && c->ld_table < c->width) return MX_ERR_SHAPE;
+    if (!aligned16(c->k) || !aligned16(c->v) || (c->pages > 1 && (c->k_stride % 16 || c->v_stride % 16)) ||
+        !word_aligned(c->page_table) || !word_aligned(c->lengths) || !word_aligned(c->row_offsets))
+        return MX_ERR_ALIGN;
+    return MX_OK;
+}
+
+CacheView view_of(const mx_cache_batch* c) {
+    CacheView v;
+    v.k = c->k, v.v = c->v, v.ks = c->k_scale, v.vs = c->v_scale;
+    v.k_page = c->k_stride, v.v_page = c->v_stride, v.ks_page = c->ks_stride, v.vs_page = c->vs_stride;
+    v.table = c->page_table;
+    v.ld_table = c->ld_table;
+    v.lengths = c->lengths;
+    v.row_offsets = c->row_offsets;
+    v.pages = c->pages;
+    v.width = static_cast<int32_t>(c->width);
+    v.B = static_cast<int32_t>(c->sequences);
+    v.T = static_cast<int32_t>(c->rows);
+    v.Hkv = static_cast<int32_t>(c->heads);
+    v.page_shift = 0;
+    while ((1 << v.page_shift) < c->page_size) ++v.page_shift;
+    return v;
+}
+
+template <int D, int CH, int THREADS>
+mx_status launch_append(AppendArgs& a, mx_stream stream) {
+    const int64_t items = (a.c.T >> a.c.page_shift) + 2 * int64_t(a.c.B), blocks = items * 2 * a.c.Hkv;
+    const int64_t queries = a.q ? ceil_div(a.c.T, THREADS / 32) : 0;
+    if (blocks + queries >= kInt32End) return MX_ERR_SHAPE;
+    a.kv_blocks = static_cast<int>(blocks);
+    return launch_behind(append_kernel<D, CH, THREADS>, blocks + queries, THREADS, 0, 1, stream, a);
+}
+
+template <int D>
+mx_status launch_append_dim(AppendArgs& a, mx_stream stream) {
+    if (!a.c.row_offsets) {
+        const int64_t items = int64_t(a.c.B) * 2 * a.c.Hkv, per = kAppendOneThreads / 32;
+        const int64_t blocks = ceil_div(items, per), queries = a.q ? ceil_div(a.c.T, per) : 0;
+        if (items + queries * per >= kInt32End - per) return MX_ERR_SHAPE;
+        a.kv_blocks = static_cast<int>(blocks);
+        return launch_behind(append_one_kernel<D>, blocks + queries, kAppendOneThreads, 0, 1, stream, a);
+    }
+    switch ((D << a.c.page_shift) / 1024) {
+        case 1: return launch_append<D, 1, 128>(a, stream);
+        case 2: return launch_append<D, 2, 128>(a, stream);
+        case 4: return launch_append<D, 4, 128>(a, stream);
+        case 8: return launch_append<D, 8, 128>(a, stream);
+    }
+    return launch_append<128, 8, 256>(a, stream);
+}
+
+// Blocks of attend_few_kernel, two an SM; also what sizes the workspace.
+constexpr int64_t kAtMaxBlocks = 320;
+constexpr int kAtMinSteps = 4;
+
+template <class K>
+bool opt_in_smem(std::atomic<bool>* done, K kernel, int bytes) {
+    int dev = 0;
+    cudaGetDevice(&dev);
+    if (done[dev].load(std::memory_order_relaxed)) return true;
+    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess) {
+        cudaGetLastError();
+        return false;
+    }
+    done[dev].store(true, std::memory_order_relaxed);
+    return true;
+}
+
+template <int D, int NT>
+mx_status launch_attend_few(AttendArgs& a, int64_t most_rows, const DeviceInfo* d, mx_stream stream) {
+    static std::atomic<bool> opted[kMaxDevices];
+    constexpr int smem = AtSmem<D, NT>::kBytes;
+    if (!opt_in_smem(opted, attend_few_kernel<D, NT>, smem)) return MX_ERR_CUDA;
+    const int64_t tiles = ceil_div(most_rows, 8 * NT);
+    // No more blocks than steps there can be.
+    const int64_t keys = int64_t(a.c.width) << a.c.page_shift;
+    const double bound = double(a.c.B) * a.c.Hkv * double(tiles) * double(keys / kAtStep + 2);
+    a.blocks = static_cast<int>(std::min<double>(std::min<int64_t>(2 * d->sms, kAtMaxBlocks), bound));
+    if (mx_status st = launch_behind(attend_few_kernel<D, NT>, a.blocks, kAtThreads, smem, 1, stream, a)) return st;
+    const int64_t joins = tiles * a.c.Hkv * a.c.B;
+    if (joins >= kInt32End) return MX_ERR_SHAPE;
+    return launch_behind(attend_join_kernel<D, NT>, joins, kAtThreads, 0, 1, stream, a, static_cast<int>(tiles));
+}
+
+template <int D>
+mx_status launch_attend(AttendArgs& a, const DeviceInfo* d, mx_stream stream) {
+    const int64_t rows = a.c.row_offsets ? int64_t(a.c.T) * a.G : a.G;
+    a.most_rows = static_cast<int>(rows);
+    if (rows <= 8) return launch_attend_few<D, 1>(a, rows, d, stream);
+    return launch_attend_few<D, 2>(a, rows, d, stream);
+}
+
+}  // namespace
+}  // namespace mx
+
+extern "C" {
+
+mx_status mx_rope_table(const double* freq, int64_t pairs, double amplitude, int64_t first, int64_t count, float* table,
+                        mx_stream stream) {
+    if (pairs < 1 || count < 0) return MX_ERR_ARG;
+    if (pairs > kRopeMaxPairs || count >= kInt32End) return MX_ERR_SHAPE;
+    if (!freq || (count > 0 && !table)) return MX_ERR_ARG;
+    if (!word_aligned(table)) return MX_ERR_ALIGN;
+    if (count == 0) return MX_OK;
+    const DeviceInfo* d = nullptr;
+    if (mx_status st = check_device(&d)) return st;
+    RopeTableArgs a{};
+    for (int64_t i = 0; i < pairs; ++i) a.freq[i] = freq[i];
+    a.table = table;
+    a.amplitude = amplitude;
+    a.first = first;
+    a.count = count;
+    a.n = FastDiv::of(pairs);
+    return launch_behind(rope_table_kernel, std::min<int64_t>(count, int64_t(d->sms) * 16), kRopeThreads, 0, 1, stream, a);
+}
+
+mx_status mx_rope(const void* x, mx_out_dtype dtype, int64_t T, int64_t H, int64_t D, int64_t ldx_t, int64_t ldx_h,
+                  const float* table, int64_t positions, int64_t rot, const void* pos, int pos64, int interleaved, void* y,
+                  int64_t ldy_t, int64_t ldy_h, mx_stream stream) {
+    return rope(x, dtype, T, H, D, ldx_t, ldx_h, table, positions, rot, pos, pos64, interleaved, y, ldy_t, ldy_h, false, stream);
+}
+
+mx_status mx_rope_bwd(const void* dy, mx_out_dtype dtype, int64_t T, int64_t H, int64_t D, int64_t ldy_t, int64_t ldy_h,
+                      const float* table, int64_t positions, int64_t rot, const void* pos, int pos64, int interleaved,
+                      void* dx, int64_t ldx_t, int64_t ldx_h, mx_stream stream) {
+    return rope(dy, dtype, T, H, D, ldy_t, ldy_h, table, positions, rot, pos, pos64, interleaved, dx, ldx_t, ldx_h, true, stream);
+}
+
+mx_status mx_cache_append(const mx_cache_batch* cache, const void* k, int64_t ldk_t, int64_t ldk_h, const void* v,
+                          int64_t ldv_t, int64_t ldv_h, const float* table, int64_t positions, int64_t rot, int interleaved,
+                          const void* q, int64_t q_heads, int64_t ldq_t, int64_t ldq_h, void* q_out, int64_t ldo_t,
+                          int64_t ldo_h, mx_stream stream) {
+    bool empty = false;
+    if (mx_status st = cache_checks(cache, &empty)) return st;
+    if ((table && (rot < 1 || positions < 0)) || (q && q_heads < 1)) return MX_ERR_ARG;
+    if ((table && (rot % 16 != 0 || rot > cache->head_dim)) || (q && q_heads > kCacheMaxQueryHeads)) return MX_ERR_SHAPE;
+    if (empty) return MX_OK;
+    if (!k || !v || (q && !q_out)) return MX_ERR_ARG;
+    if (!pieces_ok(k, ldk_t, ldk_h) || !pieces_ok(v, ldv_t, ldv_h) || !aligned16(table) ||
+        (q && (!pieces_ok(q, ldq_t, ldq_h) || !pieces_ok(q_out, ldo_t, ldo_h))))
+        return MX_ERR_ALIGN;
+    const DeviceInfo* d = nullptr;
+    if (mx_status st = check_device(&d)) return st;
+    AppendArgs a{};
+    a.c = view_of(cache);
+    a.k = static_cast<const __nv_bfloat16*>(k);
+    a.v = static_cast<const __nv_bfloat16*>(v);
+    a.q = static_cast<const __nv_bfloat16*>(q);
+    a.q_out = static_cast<__nv_bfloat16*>(q_out);
+    a.table = table;
+    a.ldk_t = ldk_t, a.ldk_h = ldk_h, a.ldv_t = ldv_t, a.ldv_h = ldv_h;
+    a.ldq_t = ldq_t, a.ldq_h = ldq_h, a.ldo_t = ldo_t, a.ldo_h = ldo_h;
+    a.positions = positions;
+    a.err = d->status;
+    a.Hq = static_cast<int>(q_heads);
+    a.D = static_cast<int>(cache->head_dim);
+    a.rot = static_cast<int>(rot);
+    a.interleaved = interleaved != 0;
+    a.heads2 = FastDiv::of(2 * cache->heads);
+    return cache->head_dim == 128 ? launch_append_dim<128>(a, stream) : launch_append_dim<64>(a, stream);
+}
+
+int64_t mx_cache_attention_workspace_bytes(int64_t head_dim, int64_t rows, int64_t q_heads) {
+    if ((head_dim != 64 && head_dim != 128) || rows < 0 || q_heads < 1) return -1;
+    return kAtMaxBlocks * 2 * part_floats(16, static_cast<int>(head_dim)) * 4;
+}
+
+mx_status mx_cache_attention(const mx_cache_batch* cache, const void* q, int64_t q_heads, int64_t ldq_t, int64_t ldq_h,
+                             float scale, int64_t window, void* out, int64_t ldo_t, int64_t ldo_h, float* lse,
+                             void* workspace, mx_stream stream) {
+    bool empty = false;
+    if (mx_status st = cache_checks(cache, &empty)) return st;
+    if (q_heads < 1 || !(scale > 0.0f) || !(scale < INFINITY)) return MX_ERR_ARG;
+    if (q_heads % cache->heads != 0 || q_heads > kCacheMaxQueryHeads || cache->rows * q_heads >= kInt32End) return MX_ERR_SHAPE;
+    if (empty) return MX_OK;
+    if (!q || !out || !workspace) return MX_ERR_ARG;
+    if (!pieces_ok(q, ldq_t, ldq_h) || !pieces_ok(out, ldo_t, ldo_h) || !word_aligned(lse) || !aligned16(workspace))
+        return MX_ERR_ALIGN;
+    const DeviceInfo* d = nullptr;
+    if (mx_status st = check_device(&d)) return st;
+    AttendArgs a{};
+    a.c = view_of(cache);
+    a.q = static_cast<const __nv_bfloat16*>(q);
+    a.out = static_cast<__nv_bfloat16*>(out);
+    a.lse = lse;
+    a.parts = static_cast<float*>(workspace);
+    a.ldq_t = ldq_t, a.ldq_h = ldq_h, a.ldo_t = ldo_t, a.ldo_h = ldo_h;
+    a.window = window > 0 ? std::min<int64_t>(window, int64_t(1) << 62) : int64_t(1) << 62;
+    a.scale_log2 = scale * 1.4426950408889634f;
+    a.err = d->status;
+    a.timeout_ns = g_timeout_ns.load();
+    a.Hq = static_cast<int>(q_heads);
+    a.G = static_cast<int>(q_heads / cache->heads);
+    a.group = FastDiv::of(a.G);
+    a.min_steps = kAtMinSteps;
+    return cache->head_dim == 128 ? launch_attend<128>(a, d, stream) : launch_attend<64>(a, d, stream);
 }
 
 }  // extern "C"

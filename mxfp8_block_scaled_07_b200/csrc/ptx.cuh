@@ -43,6 +43,7 @@ __device__ __forceinline__ bool mbar_try_wait(uint32_t bar, uint32_t parity) {
 enum : uint32_t {
     kErrWaitTimeout = 1u,      // an mbarrier wait ran past its deadline
     kErrBadOffsets = 2u,       // grouped GEMM: row offsets not 0 .. total_rows, nondecreasing
+    kErrBadIndex = 4u,         // a page id outside the cache or its table, a position behind the rotation table
 };
 
 // Bounded wait: returns true once the phase with `parity` has completed; false if `abort` was

@@ -1,5 +1,5 @@
-"""Thin Python binding of libmx (include/mx.h) over ctypes; the MXFP4 and expert-routing calls go through a
-compiled module (csrc/binding.cpp), which costs a third of the host time.
+"""Thin Python binding of libmx (include/mx.h) over ctypes; the MXFP4, expert-routing, rotation and cache calls go
+through a compiled module (csrc/binding.cpp), which costs a third of the host time.
 
 Argument marshalling only: every step runs in the CUDA kernels of ``libmx.so``. PyTorch
 supplies device memory (output tensors are allocated with ``torch.empty`` on the input's
@@ -9,7 +9,9 @@ fails, an exception is raised.
 from __future__ import annotations
 
 import ctypes
+import math
 import os
+from typing import NamedTuple
 
 import numpy as np
 import torch
@@ -43,6 +45,15 @@ class GridRef(ctypes.Structure):
 class ComparePair(ctypes.Structure):
     """mx_compare_pair."""
     _fields_ = [("a", ctypes.c_void_p), ("b", ctypes.c_void_p), ("nbytes", ctypes.c_int64)]
+
+
+class CacheBatch(ctypes.Structure):
+    """mx_cache_batch."""
+    _fields_ = ([(n, ctypes.c_void_p) for n in ("k", "v", "k_scale", "v_scale")]
+                + [(n, ctypes.c_int64) for n in ("k_stride", "v_stride", "ks_stride", "vs_stride", "pages", "heads", "page_size", "head_dim")]
+                + [("page_table", ctypes.c_void_p), ("ld_table", ctypes.c_int64), ("width", ctypes.c_int64),
+                   ("lengths", ctypes.c_void_p), ("row_offsets", ctypes.c_void_p), ("sequences", ctypes.c_int64),
+                   ("rows", ctypes.c_int64)])
 
 
 class MxError(RuntimeError):
@@ -97,6 +108,17 @@ def lib() -> ctypes.CDLL:
         fn = getattr(L, name)
         fn.argtypes = args
         fn.restype = I32
+    F64 = ctypes.c_double
+    rope = [P, I32, I64, I64, I64, I64, I64, P, I64, I64, P, I32, I32, P, I64, I64, P]
+    for name, args in (
+            ("mx_rope_table", [P, I64, F64, I64, I64, P, P]), ("mx_rope", rope), ("mx_rope_bwd", rope),
+            ("mx_cache_append", [P, P, I64, I64, P, I64, I64, P, I64, I64, I32, P, I64, I64, I64, P, I64, I64, P]),
+            ("mx_cache_attention", [P, P, I64, I64, I64, F32, I64, P, I64, I64, P, P, P])):
+        fn = getattr(L, name)
+        fn.argtypes = args
+        fn.restype = I32
+    L.mx_cache_attention_workspace_bytes.argtypes = [I64, I64, I64]
+    L.mx_cache_attention_workspace_bytes.restype = I64
     L.mx_route_plan_workspace_bytes.argtypes = [I64, I64]
     L.mx_route_plan_workspace_bytes.restype = I64
     L.mx_grouped_scale_bytes.argtypes = [I64, I64, I64]
@@ -450,6 +472,105 @@ def combine_backward(dy: torch.Tensor, rows: torch.Tensor, slot_row: torch.Tenso
     name the same row. Rows that no slot names get zeros, except where rows has exactly T * topk of them, as in a
     plan's partition: then every slot has to name one."""
     return (_mxcall or _native()).combine_backward(dy, rows, slot_row, weights, need_weights, _buffers(out))
+
+
+# ---- positions, the cache and attention ------------------------------------------------------------------
+
+def rope_frequencies(rot: int, base: float = 10000.0, scaling=None):
+    """(angles per position of the rot / 2 pairs, factor on cosines and sines) for rope_table(), in fp64 on the host.
+
+    scaling: None; ("linear", factor): positions divided by the factor; ("ntk", factor): the base raised so that the slowest
+    pair is slowed by the factor; ("yarn", factor, original_positions[, beta_fast, beta_slow]): pairs that turn fewer than
+    beta_slow (1) times in the original positions slowed by the factor, those that turn more than beta_fast (32) times left as
+    they are, the ones between blended, and cosines and sines times 0.1 ln(factor) + 1."""
+    if rot < 2 or rot % 2 or not base > 0:
+        raise MxError(-1, "rope_frequencies: an even rot of at least 2, base > 0")
+    kind = scaling[0] if scaling else None
+    if kind == "ntk":
+        base *= float(scaling[1]) ** (rot / (rot - 2)) if rot > 2 else 1.0
+    freq = [base ** (-2.0 * i / rot) for i in range(rot // 2)]
+    if kind in (None, "ntk"):
+        return freq, 1.0
+    factor = float(scaling[1])
+    if not factor > 0:
+        raise MxError(-1, "rope_frequencies: a factor above 0")
+    if kind == "linear":
+        return [f / factor for f in freq], 1.0
+    if kind != "yarn":
+        raise MxError(-1, "rope_frequencies: scaling None, ('linear', factor), ('ntk', factor) or ('yarn', factor, positions)")
+    fast, slow = (list(scaling[3:]) + [32.0, 1.0][len(scaling) - 3:])[:2]
+
+    def pair_that_turns(turns):
+        return rot * math.log(scaling[2] / (2 * math.pi * turns)) / (2 * math.log(base))
+
+    lo, hi = max(math.floor(pair_that_turns(fast)), 0), min(math.ceil(pair_that_turns(slow)), rot - 1)
+    ramp = [min(max((i - lo) / max(hi - lo, 0.001), 0.0), 1.0) for i in range(rot // 2)]
+    return [f / factor * r + f * (1 - r) for f, r in zip(freq, ramp)], 0.1 * math.log(factor) + 1 if factor > 1 else 1.0
+
+
+def rope_table(positions: int, rot: int, base: float = 10000.0, scaling=None, first: int = 0, device="cuda", out=None):
+    """mx_rope_table: fp32 [positions, rot], the cosines and then the sines of positions first, first + 1, ... under
+    rope_frequencies(rot, base, scaling). Made once and kept."""
+    freq, amplitude = rope_frequencies(rot, base, scaling)
+    device = torch.device(device) if out is None else out.device
+    if out is None:
+        out = torch.empty((positions, rot), dtype=torch.float32, device=device)
+    if out.dtype != torch.float32 or out.shape != (positions, rot) or not out.is_contiguous() or not out.is_cuda:
+        raise MxError(-1, "rope_table: out must be a contiguous fp32 CUDA tensor [positions, rot]")
+    host = np.asarray(freq, dtype=np.float64)
+    with torch.cuda.device(out.device):
+        st = lib().mx_rope_table(ctypes.c_void_p(host.ctypes.data), rot // 2, amplitude, first, positions, _p(out),
+                                 ctypes.c_void_p(_stream(out.device)))
+    _check(st, "mx_rope_table")
+    return out
+
+
+def rope(x: torch.Tensor, table: torch.Tensor, positions=None, interleaved: bool = False, out=None):
+    """mx_rope: x [T, H, D] (fp32, BF16 or FP16; any token and head strides) with the first rot = table.shape[1] features of
+    every head rotated by table[positions[t]] (positions int32 or int64 [T]; None: 0, 1, ...), in halves or, interleaved,
+    neighbouring features; the rest copied. A negative position is padding: zeros. ``out`` may be x."""
+    return (_mxcall or _native()).rope(x, table, positions, interleaved, out)
+
+
+def rope_backward(dy: torch.Tensor, table: torch.Tensor, positions=None, interleaved: bool = False, out=None):
+    """mx_rope_bwd: the gradient of rope()'s result with respect to x."""
+    return (_mxcall or _native()).rope_backward(dy, table, positions, interleaved, out)
+
+
+class KVCache(NamedTuple):
+    """Keys and values of one layer: E4M3 codes [pages, heads, page_size, head_dim] and one E8M0 byte per page and head
+    [pages, heads], uint8. Pages may lie at any distance (views of one tensor that holds both, say)."""
+    k: torch.Tensor
+    v: torch.Tensor
+    k_scale: torch.Tensor
+    v_scale: torch.Tensor
+
+
+def cache_create(pages: int, heads: int, head_dim: int, page_size: int = 64, device="cuda") -> KVCache:
+    """An empty cache: zero codes and scales."""
+    if page_size not in (16, 32, 64, 128) or head_dim not in (64, 128):
+        raise MxError(-2, "cache_create: pages of 16, 32, 64 or 128 tokens, heads of 64 or 128 features")
+    codes = torch.zeros((2, pages, heads, page_size, head_dim), dtype=torch.uint8, device=device)
+    scales = torch.zeros((2, pages, heads), dtype=torch.uint8, device=device)
+    return KVCache(codes[0], codes[1], scales[0], scales[1])
+
+
+def cache_append(k: torch.Tensor, v: torch.Tensor, cache, page_table: torch.Tensor, lengths: torch.Tensor, row_offsets=None,
+                 q=None, table=None, interleaved: bool = False, out=None):
+    """mx_cache_append: k, v [rows, heads, head_dim] (BF16) into the pages of their sequences, k rotated by table (as rope(); None:
+    not rotated). page_table int32 [B, width], lengths int32 [B] with the new rows counted, row_offsets int32 [B + 1] (None:
+    one row per sequence). Returns q [rows, q_heads, head_dim] rotated at the same positions (into ``out``, which may be q), or
+    None without q."""
+    return (_mxcall or _native()).cache_append(k, v, cache, page_table, lengths, row_offsets, q, table, interleaved, out)
+
+
+def cache_attention(q: torch.Tensor, cache, page_table: torch.Tensor, lengths: torch.Tensor, row_offsets=None, scale=None,
+                    window: int = 0, return_lse: bool = False, out=None):
+    """mx_cache_attention: attention of q [rows, q_heads, head_dim] (BF16) over the cache, each row over the keys up to its own
+    position (the last `window` of them if window > 0); page_table, lengths and row_offsets as in cache_append(). scale None:
+    head_dim ** -0.5. Returns BF16 like q, or (that, lse fp32 [rows, q_heads]) with return_lse."""
+    return (_mxcall or _native()).cache_attention(q, cache, page_table, lengths, row_offsets, scale, window, return_lse,
+                                                  _buffers(out) if return_lse else out)
 
 
 def grid_equal(a: torch.Tensor, b: torch.Tensor, out=None):
