@@ -21,7 +21,8 @@ LIB = os.path.join(HERE, "libmx.so")
 SOURCES = [os.path.join(CSRC, f) for f in ("libmx.cu",)]
 DEPS = SOURCES + [os.path.join(CSRC, f) for f in ("ptx.cuh", "quantize.cuh", "quantize_tma.cuh", "swizzle.cuh",
                                                        "grid_equal.cuh", "gemm.cuh", "gemm_few.cuh", "blockwise.cuh", "fastdiv.cuh", "fp4.cuh",
-                                                       "route.cuh", "experts.cuh", "rope.cuh", "cache.cuh", "attend.cuh")] + [
+                                                       "route.cuh", "experts.cuh", "rope.cuh", "cache.cuh", "attend.cuh",
+                                                       "attend_many.cuh")] + [
     os.path.join(ROOT, "include", "mx.h")
 ]
 

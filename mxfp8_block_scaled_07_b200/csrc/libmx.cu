@@ -1,6 +1,6 @@
 // libmx: the C-ABI entry points declared in include/mx.h. Host-side argument checks, tensor-map
 // construction and kernel launches; the kernels themselves are in quantize.cuh, fp4.cuh, gemm.cuh,
-// route.cuh, experts.cuh, rope.cuh, cache.cuh, attend.cuh, swizzle.cuh, blockwise.cuh and grid_equal.cuh. Nothing here allocates device memory or synchronizes (except mx_device_error).
+// route.cuh, experts.cuh, rope.cuh, cache.cuh, attend.cuh, attend_many.cuh, swizzle.cuh, blockwise.cuh and grid_equal.cuh. Nothing here allocates device memory or synchronizes (except mx_device_error).
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -13,6 +13,7 @@
 
 #include "../../include/mx.h"
 #include "attend.cuh"
+#include "attend_many.cuh"
 #include "blockwise.cuh"
 #include "cache.cuh"
 #include "experts.cuh"
@@ -1684,11 +1685,24 @@ mx_status launch_attend_few(AttendArgs& a, int64_t most_rows, const DeviceInfo* 
 }
 
 template <int D>
+mx_status launch_attend_many(AttendArgs& a, mx_stream stream) {
+    static std::atomic<bool> opted[kMaxDevices];
+    if (!opt_in_smem(opted, attend_many_kernel<D>, AmSmem<D>::kBytes)) return MX_ERR_CUDA;
+    const int64_t items = int64_t(a.c.T) * a.G / kAmRows + a.c.B, blocks = items * a.c.Hkv;
+    if (blocks >= kInt32End) return MX_ERR_SHAPE;
+    return launch_behind(attend_many_kernel<D>, blocks, kAmThreads, AmSmem<D>::kBytes, 1, stream, a, static_cast<int>(items));
+}
+
+// Rows per sequence and key head (new tokens x G) up to which a sequence of a ragged batch is left to the kernel for few.
+constexpr int64_t kAtFewRows = 32;
+
+template <int D>
 mx_status launch_attend(AttendArgs& a, const DeviceInfo* d, mx_stream stream) {
     const int64_t rows = a.c.row_offsets ? int64_t(a.c.T) * a.G : a.G;
-    a.most_rows = static_cast<int>(rows);
-    if (rows <= 8) return launch_attend_few<D, 1>(a, rows, d, stream);
-    return launch_attend_few<D, 2>(a, rows, d, stream);
+    const int64_t few = a.c.row_offsets ? std::min(rows, kAtFewRows) : rows;
+    a.most_rows = static_cast<int>(few);
+    if (mx_status st = few <= 8 ? launch_attend_few<D, 1>(a, few, d, stream) : launch_attend_few<D, 2>(a, few, d, stream)) return st;
+    return rows > few ? launch_attend_many<D>(a, stream) : MX_OK;
 }
 
 }  // namespace
