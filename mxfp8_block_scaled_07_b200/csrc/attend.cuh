@@ -33,7 +33,7 @@ namespace mx {
 constexpr int kAtThreads = 128;
 constexpr int kAtWarps = kAtThreads / 32;
 constexpr int kAtStep = 64;            // keys per step: 16 per warp
-constexpr float kAtBias = 7.0f;        // P = 2^(t - M + 7)
+constexpr int kAtBias = 7;             // P = 2^(t - M + 7)
 constexpr float kAtSlack = 8.0f;       // M lags behind the maximum by at most this
 constexpr float kAtNone = -1e30f;      // M of a row that has seen no key
 constexpr int kAtValueRange = 60;      // binades of value scales below the largest that count
@@ -410,7 +410,7 @@ __global__ void __launch_bounds__(kAtThreads, 2) attend_few_kernel(const __grid_
             dv -= E;
             // Values that do not count, or that are NaN: weights of their own, l as ever.
             const bool apart = vb == 255 || dv < -kAtValueRange;
-            const float shift = kAtBias + static_cast<float>(apart ? 0 : dv), back = exp2_approx(-shift);
+            const float shift = static_cast<float>(kAtBias + (apart ? 0 : dv)), back = exp2_approx(-shift);
             uint32_t pf[NT][2];
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
@@ -490,7 +490,7 @@ __global__ void __launch_bounds__(kAtThreads, 2) attend_few_kernel(const __grid_
                 const float lw = stat[w][1][n];
                 if (lw == 0.0f) continue;        // no key seen: nothing of this warp counts (its E may be unset)
                 const float f = exp2_approx(stat[w][0][n] - top);
-                const float fo = ldexpf(f, static_cast<int>(stat[w][2][n] - kAtBias));
+                const float fo = ldexpf(f, static_cast<int>(stat[w][2][n]) - kAtBias);
                 sum += lw * f;
 #pragma unroll
                 for (int i = 0; i < D / 32; ++i) acc[i] += fo * reinterpret_cast<const float*>(smem + w * S::kWarp)[n * (D + 4) + lane + 32 * i];
