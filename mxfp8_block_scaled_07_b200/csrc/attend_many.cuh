@@ -5,16 +5,14 @@
 //   S_t = Q_t K^T        tcgen05.mma kind::f16, both operands in shared memory, accumulators in TMEM
 //   P_t = 2^(S_t ...)    one thread per row, read from TMEM and written back over S_t as f16
 //   O_t += P_t V         P_t from TMEM, V from shared memory as it lies (features contiguous: an MN-major operand)
-// While the softmax of one tile runs, the products of the other do. The codes are loaded with plain 16-byte loads, one tile ahead in
-// registers, and written to shared memory as f16 (exact, one conversion for two codes): so pages may be of any size from 16 tokens and lie
-// anywhere, and the scales stay out of the products: a page's key scale is a factor of the softmax's argument, its value
-// scale an exponent of P, both constant over 16 columns. E4M3 operands would run at twice the rate but P (and q) would need two of them each
-// to keep BF16's accuracy, which costs the softmax's threads more than the conversion costs the loaders.
+// While the softmax of one tile runs, the products of the other do. One warp copies the codes with bulk copies of 16 keys each,
+// so that pages may be of any size from 16 tokens and lie anywhere; four warps write them to the products' layout as f16 (exact, one
+// conversion for two codes). The scales stay out of the products: a page's key scale is a factor of the softmax's argument, its
+// value scale an exponent of P, both constant over 16 columns. E4M3 operands would run at twice the rate but P (and q) would need two of
+// them each to keep BF16's accuracy, which costs the softmax's threads more than the conversion costs the converters.
 //
-// Roles (512 threads): warps 0-3 and 4-7 softmax of tiles 0 and 1, warps 8-11 load and convert, warp 12 issues the
-// products and owns TMEM (S_0, S_1: 128 columns each, O_0, O_1: D each), warps 13-15 complete its warpgroup. The launch's 128
-// registers a thread are split 192 / 80 / 40 (8 x 192 + 4 x 80 + 4 x 40 <= 16 x 128): the softmax's threads hold a row of
-// scores. Every wait is bounded.
+// Roles (448 threads): warps 0-3 and 4-7 softmax of tiles 0 and 1, warps 8-11 conversion, warp 12 issues the products and owns TMEM
+// (S_0, S_1: 128 columns each, O_0, O_1: D each), warp 13 copies. Every wait is bounded.
 #pragma once
 #include <cstdint>
 #include <type_traits>
@@ -24,12 +22,14 @@
 
 namespace mx {
 
-constexpr int kAmThreads = 512;
+constexpr int kAmThreads = 448;
 constexpr int kAmRows = 256;           // query rows per block
 constexpr int kAmKeys = 128;           // keys per tile
 constexpr int kAmRing = 2;             // stages of K and of V
+constexpr int kAmRaw = 3;              // half tiles of codes on their way to the loaders
 constexpr int kAmScales = 4;           // tiles whose page scales are kept
 constexpr uint32_t kAmCols = 512;
+constexpr bool kAmFma = true;
 constexpr int kAmNoScale = -100000;    // exponent of a value scale that says NaN
 
 template <int D>
@@ -38,11 +38,13 @@ struct AmSmem {
     static constexpr int kQ = 0;                                   // two tiles
     static constexpr int kK = kQ + 2 * kTile;
     static constexpr int kV = kK + kAmRing * kTile;
-    static constexpr int kScales = kV + kAmRing * kTile;           // [kAmScales][8] (key factor, value exponent as an integer)
+    static constexpr int kRaw = kV + kAmRing * kTile;              // codes of half tiles on their way
+    static constexpr int kHalf = 64 * D;
+    static constexpr int kScales = kRaw + kAmRaw * kHalf;          // [kAmScales][8] (key factor, value exponent as an integer)
     static constexpr int kBar = kScales + kAmScales * 8 * 8;
-    static constexpr int kBars = 4 * kAmRing + kAmScales + 2 * 4 + 1;
+    static constexpr int kBars = 2 * kAmRaw + 4 * kAmRing + kAmScales + 2 * 5 + 1;
     static constexpr int kMisc = kBar + kBars * 8;
-    static constexpr int kBytes = kMisc + 16 + 1024;               // + alignment slack
+    static constexpr int kBytes = kMisc + 8 + 4 * kAmScales + 1024;    // + alignment slack
 };
 
 // ---- f16 products --------------------------------------------------------------------------------------------
@@ -97,23 +99,18 @@ __device__ __forceinline__ void tc_scores_elect(uint32_t d_tmem, uint64_t adesc,
             "l"(adesc), "l"(bdesc), "r"(idesc), "r"(smem_u32(bar))
             : "memory");
 }
-// Eight products O (+)= P V of 16 keys each and the commit: P's next 16 keys lie 8 columns on, V's 2 KB on.
-__device__ __forceinline__ void tc_values_elect(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc, uint32_t idesc, uint32_t accumulate, uint64_t* bar) {
+// Four products O (+)= P V of 16 keys each: P's next 16 keys lie 8 columns on, V's 2 KB on.
+__device__ __forceinline__ void tc_values_elect(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc, uint32_t idesc, uint32_t accumulate) {
     asm volatile(
-        "{\n\t.reg .pred e, t, p;\n\t.reg .b32 a1, a2, a3, a4, a5, a6, a7;\n\t.reg .b64 b1, b2, b3, b4, b5, b6, b7;\n\t"
+        "{\n\t.reg .pred e, t, p;\n\t.reg .b32 a1, a2, a3;\n\t.reg .b64 b1, b2, b3;\n\t"
         "elect.sync _|e, 0xffffffff;\n\tsetp.eq.b32 t, 0, 0;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-        "add.u32 a1, %1, 8;\n\tadd.u32 a2, %1, 16;\n\tadd.u32 a3, %1, 24;\n\tadd.u32 a4, %1, 32;\n\tadd.u32 a5, %1, 40;\n\tadd.u32 a6, %1, 48;\n\tadd.u32 a7, %1, 56;\n\t"
-        "add.s64 b1, %2, 128;\n\tadd.s64 b2, %2, 256;\n\tadd.s64 b3, %2, 384;\n\tadd.s64 b4, %2, 512;\n\tadd.s64 b5, %2, 640;\n\tadd.s64 b6, %2, 768;\n\tadd.s64 b7, %2, 896;\n\t"
+        "add.u32 a1, %1, 8;\n\tadd.u32 a2, %1, 16;\n\tadd.u32 a3, %1, 24;\n\t"
+        "add.s64 b1, %2, 128;\n\tadd.s64 b2, %2, 256;\n\tadd.s64 b3, %2, 384;\n\t"
         "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t"
         "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [a1], b1, %3, t;\n\t"
         "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [a2], b2, %3, t;\n\t"
-        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [a3], b3, %3, t;\n\t"
-        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [a4], b4, %3, t;\n\t"
-        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [a5], b5, %3, t;\n\t"
-        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [a6], b6, %3, t;\n\t"
-        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [a7], b7, %3, t;\n\t"
-        "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%5];\n\t}" ::"r"(d_tmem),
-        "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate), "r"(smem_u32(bar))
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [a3], b3, %3, t;\n\t}" ::"r"(d_tmem),
+        "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate)
         : "memory");
 }
 __device__ __forceinline__ void tc_st_32x32b_x16(uint32_t taddr, const uint32_t (&r)[16]) {
@@ -141,6 +138,42 @@ __device__ __forceinline__ float2 add2(float2 a, float2 b) {
         : "=f"(r.x), "=f"(r.y)
         : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
     return r;
+}
+
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float r;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+    return r;
+}
+// 2^x on the FMA pipe, for x <= 15: x = n + f with |f| <= 1/2 (Cody and Waite's reduction, by adding and subtracting 1.5 2^23),
+// 2^f by a polynomial of degree 5 (minimax by Remez's exchange, coefficients rounded to fp32: 2^-22 relative), n added to the exponent.
+// Below 2^-126 the result is 2^-126. NaN gives 2^-126 too.
+__device__ __forceinline__ float2 exp2_fma(float2 x) {
+    x.x = fmaxf(x.x, -126.0f);
+    x.y = fmaxf(x.y, -126.0f);
+    const float2 t = add2(x, make_float2(12582912.0f, 12582912.0f)), n = add2(t, make_float2(-12582912.0f, -12582912.0f));
+    const float2 f = fma2(n, make_float2(-1.0f, -1.0f), x);
+    float2 y = make_float2(0.0013276472454890609f, 0.0013276472454890609f);
+    y = fma2(y, f, make_float2(0.009675540961325169f, 0.009675540961325169f));
+    y = fma2(y, f, make_float2(0.05550713092088699f, 0.05550713092088699f));
+    y = fma2(y, f, make_float2(0.24022120237350464f, 0.24022120237350464f));
+    y = fma2(y, f, make_float2(0.6931469440460205f, 0.6931469440460205f));
+    y = fma2(y, f, make_float2(1.0000001192092896f, 1.0000001192092896f));
+    return make_float2(__int_as_float(__float_as_int(y.x) + (__float_as_int(t.x) << 23)), __int_as_float(__float_as_int(y.y) + (__float_as_int(t.y) << 23)));
+}
+
+// mbar_wait_warp, with all but the first look out of the way of the roles' loops.
+__device__ __noinline__ bool am_wait_on(uint64_t* bar, uint32_t parity, volatile int* abort, uint32_t* err, uint64_t timeout_ns) {
+    return mbar_wait_warp(bar, parity, abort, err, timeout_ns);
+}
+__device__ __forceinline__ bool am_wait(uint64_t* bar, uint32_t parity, volatile int* abort, uint32_t* err, uint64_t timeout_ns) {
+    return __all_sync(0xFFFFFFFFu, mbar_try_wait(smem_u32(bar), parity)) || am_wait_on(bar, parity, abort, err, timeout_ns);
+}
+
+// Bits of 32 columns from `at` on that lie in [begin, end).
+__device__ __forceinline__ uint32_t seen_bits(int begin, int end, int at) {
+    const int lo = min(max(begin - at, 0), 32), hi = min(max(end - at, 0), 32);
+    return hi <= lo ? 0u : (0xFFFFFFFFu >> (32 - (hi - lo))) << lo;
 }
 
 // ---- the block's work ------------------------------------------------------------------------------------------
@@ -184,13 +217,27 @@ __device__ __forceinline__ bool many_work(const AttendArgs& a, int block, int it
     return true;
 }
 
+// Order in which tiles of keys and values are copied and converted: K 0, then K j + 1 and V j for j = 0, 1, ..., without K N.
+__device__ __forceinline__ int tile_of(int item, int N, bool& keys) {
+    keys = item == 0 || (item % 2 == 1 && item < 2 * N - 1);
+    return item == 0 ? 0 : item == 2 * N - 1 ? N - 1 : keys ? (item + 1) / 2 : item / 2 - 1;
+}
+// A bulk copy of one lane's.
+__device__ __forceinline__ void bulk_load(void* smem_dst, const void* gsrc, uint32_t bytes, uint64_t* bar) {
+    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(smem_u32(smem_dst)),
+                 "l"(reinterpret_cast<uint64_t>(gsrc)), "r"(bytes), "r"(smem_u32(bar))
+                 : "memory");
+}
+
 template <int D>
 __global__ void __launch_bounds__(kAmThreads, 1) attend_many_kernel(const __grid_constant__ AttendArgs a, int items) {
     grid_wait();
     using S = AmSmem<D>;
     extern __shared__ uint8_t dyn[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(dyn) + 1023) & ~uintptr_t(1023));
-    uint64_t* k_full = reinterpret_cast<uint64_t*>(smem + S::kBar);
+    uint64_t* raw_full = reinterpret_cast<uint64_t*>(smem + S::kBar);
+    uint64_t* raw_empty = raw_full + kAmRaw;
+    uint64_t* k_full = raw_empty + kAmRaw;
     uint64_t* k_empty = k_full + kAmRing;
     uint64_t* v_full = k_empty + kAmRing;
     uint64_t* v_empty = v_full + kAmRing;
@@ -198,16 +245,21 @@ __global__ void __launch_bounds__(kAmThreads, 1) attend_many_kernel(const __grid
     uint64_t* q_full = scales_full + kAmScales;
     uint64_t* s_full = q_full + 2;
     uint64_t* p_full = s_full + 2;
-    uint64_t* o_done = p_full + 2;
+    uint64_t* o_done = p_full + 4;               // p_full: two halves of either tile
     uint64_t* drain = o_done + 2;
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + S::kMisc);
     volatile int* abort = reinterpret_cast<volatile int*>(smem + S::kMisc + 4);
+    uint32_t* bad_pages = reinterpret_cast<uint32_t*>(smem + S::kMisc + 8);      // of a tile: a bit per group of 16 keys
     float2* scales = reinterpret_cast<float2*>(smem + S::kScales);
     const CacheView& c = a.c;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     AmWork w;
     if (!many_work(a, blockIdx.x, items, w)) return;       // the same in every warp
     if (threadIdx.x == 0) {
+        for (int i = 0; i < kAmRaw; ++i) {
+            mbar_init(&raw_full[i], 1);
+            mbar_init(&raw_empty[i], 4);
+        }
         for (int i = 0; i < kAmRing; ++i) {
             mbar_init(&k_full[i], 4);
             mbar_init(&k_empty[i], 1);
@@ -218,7 +270,8 @@ __global__ void __launch_bounds__(kAmThreads, 1) attend_many_kernel(const __grid
         for (int i = 0; i < 2; ++i) {
             mbar_init(&q_full[i], 4);
             mbar_init(&s_full[i], 1);
-            mbar_init(&p_full[i], 4);
+            mbar_init(&p_full[2 * i], 4);
+            mbar_init(&p_full[2 * i + 1], 4);
             mbar_init(&o_done[i], 1);
         }
         mbar_init(drain, 1);
@@ -236,115 +289,144 @@ __global__ void __launch_bounds__(kAmThreads, 1) attend_many_kernel(const __grid
     const int N = max(w.tiles[0], w.tiles[1]);
 
     if (warp >= 8 && warp < 12) {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
-        // ---- load and convert, in halves of a tile (64 keys): while one is converted the next two are on their way. Lane l < 8
-        // knows where the 16 keys of group l lie, for the tile whose keys are loaded next, and hands it to the others.
-        constexpr int U = 64 * D / 16 / 128;                 // 16-code pieces per thread and half tile
+        // ---- convert: codes of half tiles, as they lie in their pages, to f16 in the products' layout
+        constexpr int U = 64 * D / 16 / 128;                 // 16-byte pieces per thread and half tile
         constexpr int R = 2048 / D;                          // rows that the four warps take at once: 16 or 32
-        const int wc = warp - 8;
-        // Eight lanes: two rows and four pieces, so that their stores meet every bank once under the swizzle.
-        const int row_in = wc * (R / 4) + (D == 128 ? ((lane >> 2) & 1) + 2 * (lane >> 4) : lane >> 2);
+        // Eight lanes: two rows and four pieces, so that their f16 meets every bank once under the swizzle.
+        const int row_in = (warp - 8) * (R / 4) + (D == 128 ? ((lane >> 2) & 1) + 2 * (lane >> 4) : lane >> 2);
         const int piece = D == 128 ? (lane & 3) + 4 * ((lane >> 3) & 1) : lane & 3;
-        const int in_group = (row_in & 15) * D + piece * 16;
-        int id_next = -1;                                    // page of group `lane`, of the tile behind the last one placed
-        struct Places {
-            int64_t k, v;                                    // of group `lane`: bytes from the codes' beginning
-            int valid;                                       // its keys; 0 outside the sequence or on a bad page
-            uint32_t scales;
-        };
-        auto fetch_id = [&](int j) {
-            const int64_t tok = w.lo + int64_t(j) * kAmKeys + 16 * lane;
-            id_next = -1;
-            if (lane < 8 && j < N && tok < w.hi) {
-                id_next = static_cast<int>(page_id(c, w.b, tok >> c.page_shift));
-                if (id_next < 0) atomicOr(a.err, kErrBadIndex);
+        const uint32_t from = smem_u32(smem) + S::kRaw + row_in * D + piece * 16;
+        const uint32_t to = (piece >> 2) * 16384 + row_in * 128;
+        const uint32_t to0 = to + ((((piece & 3) * 2) ^ (row_in & 7)) << 4), to1 = to + ((((piece & 3) * 2 + 1) ^ (row_in & 7)) << 4);
+        bool ok = true;
+        int stage = 0;
+        uint32_t phase = 0;
+#pragma unroll 1
+        for (int item = 0; ok && item < 2 * N; ++item) {
+            bool keys;
+            const int j = tile_of(item, N, keys), st = j % kAmRing;
+            if (j >= kAmRing) ok = am_wait(keys ? &k_empty[st] : &v_empty[st], (j / kAmRing - 1) & 1, abort, a.err, a.timeout_ns);
+            if (!ok) break;
+            const uint32_t tile = smem_u32(smem) + (keys ? S::kK : S::kV) + st * S::kTile;
+            const int64_t left = w.hi - (w.lo + int64_t(j) * kAmKeys);       // keys from the tile's first on
+#pragma unroll 1
+            for (int half = 0; half < 2; ++half) {
+                ok = am_wait(&raw_full[stage], phase, abort, a.err, a.timeout_ns);
+                if (!ok) break;
+                uint4 x[U];
+#pragma unroll
+                for (int i = 0; i < U; ++i) x[i] = ld_shared_v4(from + stage * S::kHalf + i * 2048);
+                // Behind the sequence's end nothing was copied, nor from a bad page (whose scales say NaN): zeros.
+                if (left < kAmKeys || bad_pages[j % kAmScales] != 0) {
+#pragma unroll
+                    for (int i = 0; i < U; ++i) {
+                        const int row = half * 64 + i * R + row_in;
+                        if (row >= left || (bad_pages[j % kAmScales] >> (row >> 4) & 1)) x[i] = make_uint4(0, 0, 0, 0);
+                    }
+                }
+#pragma unroll
+                for (int i = 0; i < U; ++i) {
+                    const uint32_t at = tile + half * 8192 + i * R * 128;
+                    st_shared_v4(at + to0, f16x2_of_e4m3(x[i].x), f16x2_of_e4m3_hi(x[i].x), f16x2_of_e4m3(x[i].y), f16x2_of_e4m3_hi(x[i].y));
+                    st_shared_v4(at + to1, f16x2_of_e4m3(x[i].z), f16x2_of_e4m3_hi(x[i].z), f16x2_of_e4m3(x[i].w), f16x2_of_e4m3_hi(x[i].w));
+                }
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&raw_empty[stage]);
+                if (++stage == kAmRaw) stage = 0, phase ^= 1;
             }
+            if (!ok) break;
+            fence_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(keys ? &k_full[st] : &v_full[st]);
+        }
+    } else if (warp == 13) {
+        // ---- copy: lane l < 8 copies the 16 keys of group l, half a tile (four lanes) at a time, and brings the page scales
+        int id_next = -1;                                    // page of group `lane`, of the tile behind the last one placed
+        uint32_t ks_next = 255, vs_next = 255, ks = 255, vs = 255;       // scale bytes of the tile last placed and of the one in front of it
+        struct Place {
+            int64_t k, v;                                    // of the lane's group: bytes from the codes' beginning
+            int bytes;                                       // to copy: 0 outside the sequence or on a bad page
+            uint32_t bad;
+        };
+        // Neither an id nor the scales are looked at where they are loaded: a tile later they have come.
+        auto fetch_id = [&](int j) {
+            const int64_t tok = w.lo + int64_t(j) * kAmKeys + 16 * lane, index = tok >> c.page_shift;
+            id_next = -1;
+            if (lane < 8 && j < N && tok < w.hi && index < c.width) id_next = c.table[w.b * c.ld_table + index];
         };
         auto place = [&](int j) {                            // from id_next; then fetches the next tile's
-            Places p;
             const int64_t tok = w.lo + int64_t(j) * kAmKeys + 16 * lane;
+            const bool wanted = lane < 8 && tok < w.hi, good = wanted && id_next >= 0 && id_next < c.pages;
+            if (wanted && !good) atomicOr(a.err, kErrBadIndex);
+            const int64_t id = good ? id_next : 0;
             const int64_t in_page = ((static_cast<int64_t>(w.h) << c.page_shift) + (tok & ((1 << c.page_shift) - 1))) * D;
-            p.valid = id_next < 0 ? 0 : static_cast<int>(min(w.hi - tok, int64_t(16)));
-            p.k = id_next * c.k_page + in_page;
-            p.v = id_next * c.v_page + in_page;
-            p.scales = id_next < 0 ? 0xFFFFu : c.ks[id_next * c.ks_page + w.h] | static_cast<uint32_t>(c.vs[id_next * c.vs_page + w.h]) << 8;
+            Place p;
+            p.k = id * c.k_page + in_page;
+            p.v = id * c.v_page + in_page;
+            p.bytes = good ? static_cast<int>(min(w.hi - tok, int64_t(16))) * D : 0;
+            p.bad = __ballot_sync(0xFFFFFFFFu, wanted && !good);
+            ks = ks_next, vs = vs_next;
+            ks_next = vs_next = 255;
+            if (good) {
+                ks_next = c.ks[id * c.ks_page + w.h];
+                vs_next = c.vs[id * c.vs_page + w.h];
+            }
             fetch_id(j + 1);
             return p;
         };
-        auto load = [&](const uint8_t* base, int64_t of_group, int valid, int half, uint4 (&x)[U]) {
-#pragma unroll
-            for (int i = 0; i < U; ++i) {
-                const int group = half * 4 + (i * R + row_in) / 16;
-                const int64_t at = __shfl_sync(0xFFFFFFFFu, of_group, group);
-                const int rows = __shfl_sync(0xFFFFFFFFu, valid, group);
-                x[i] = make_uint4(0, 0, 0, 0);
-                if ((row_in & 15) < rows) x[i] = ld_once_v4(base + at + in_group);
-            }
-        };
-        auto convert = [&](uint32_t tile, int half, const uint4 (&x)[U]) {
-#pragma unroll
-            for (int i = 0; i < U; ++i) {
-                const int row = half * 64 + i * R + row_in;
-                const uint32_t at = tile + (piece >> 2) * 16384 + row * 128, c0 = (piece & 3) * 2, sw = row & 7;
-                st_shared_v4(at + ((c0 ^ sw) << 4), f16x2_of_e4m3(x[i].x), f16x2_of_e4m3_hi(x[i].x), f16x2_of_e4m3(x[i].y), f16x2_of_e4m3_hi(x[i].y));
-                st_shared_v4(at + (((c0 + 1) ^ sw) << 4), f16x2_of_e4m3(x[i].z), f16x2_of_e4m3_hi(x[i].z), f16x2_of_e4m3(x[i].w), f16x2_of_e4m3_hi(x[i].w));
-            }
-        };
-        uint4 x0[U], x1[U];                                  // the two halves that are converted next
-        // Converts them into `tile` and loads the halves of the tile behind it if there is `more`.
-        auto pass_on = [&](uint32_t tile, bool more, const uint8_t* base, int64_t of_group, int valid) {
-            convert(tile, 0, x0);
-            if (more) load(base, of_group, valid, 0, x0);
-            convert(tile, 1, x1);
-            if (more) load(base, of_group, valid, 1, x1);
-            fence_async_smem();
-            __syncwarp();
-        };
-        auto keys = [&](int j, const Places& p) {            // room for tile j's keys, and its scales
-            if (wc == 0 && lane < 8) {
-                const uint32_t kb = p.scales & 0xFFu, vb = p.scales >> 8;
-                scales[(j % kAmScales) * 8 + lane] = make_float2(kb == 255 ? __uint_as_float(0x7FC00000u) : scale_value(kb),
-                                                                 __int_as_float(vb == 255 ? kAmNoScale : static_cast<int>(vb) - 127));
-            }
-            return j < kAmRing || mbar_wait_warp(&k_empty[j % kAmRing], (j / kAmRing - 1) & 1, abort, a.err, a.timeout_ns);
-        };
-        auto keys_done = [&](int j) {
-            if (lane == 0) {
-                mbar_arrive(&k_full[j % kAmRing]);
-                if (wc == 0) mbar_arrive(&scales_full[j % kAmScales]);
-            }
-        };
-        // Order of the tiles: K 0, then K j + 1 and V j for j = 0, 1, ...
         if (N > 0) {
-            const uint32_t kt = smem_u32(smem) + S::kK, vt = smem_u32(smem) + S::kV;
             fetch_id(0);
-            Places cur = place(0), next = cur;
-            load(c.k, cur.k, cur.valid, 0, x0);
-            load(c.k, cur.k, cur.valid, 1, x1);
+            Place cur = place(0), next = cur;                // of the tile whose values come next, and of the one behind it
             if (N > 1) next = place(1);
-            bool ok = keys(0, cur);
-            pass_on(kt, true, N > 1 ? c.k : c.v, N > 1 ? next.k : cur.v, N > 1 ? next.valid : cur.valid);
-            keys_done(0);
-            for (int j = 0; ok && j < N; ++j) {
-                if (j + 1 < N) {
-                    ok = keys(j + 1, next);
+            Place fetched = next;
+            bool ok = true;
+            int stage = 0, issued = 0;
+            uint32_t phase = 1;
+#pragma unroll 1
+            for (int item = 0; ok && item < 2 * N; ++item) {
+                bool keys;
+                const int j = tile_of(item, N, keys);
+                const bool from_cur = !keys || j == 0;
+                const uint8_t* src = keys ? c.k + (from_cur ? cur.k : next.k) : c.v + cur.v;
+                const int bytes = from_cur ? cur.bytes : next.bytes;
+                int total = bytes;                           // of this half's four lanes
+                total += __shfl_xor_sync(0xFFFFFFFFu, total, 1);
+                total += __shfl_xor_sync(0xFFFFFFFFu, total, 2);
+                if (keys) {
+                    // Tile j's scales, before its keys: the softmax reads them with its scores. place() was last called for tile j, or
+                    // at the start for tile 1. The slot's last reader was done before the keys of tile j - 1 were converted.
+                    const uint32_t kb = j == 0 && N > 1 ? ks : ks_next, vb = j == 0 && N > 1 ? vs : vs_next;
+                    ok = am_wait(&raw_empty[stage], phase, abort, a.err, a.timeout_ns);
                     if (!ok) break;
-                    pass_on(kt + (j + 1) % kAmRing * S::kTile, true, c.v, cur.v, cur.valid);
-                    keys_done(j + 1);
+                    if (lane < 8)
+                        scales[(j % kAmScales) * 8 + lane] = make_float2(kb == 255 ? __uint_as_float(0x7FC00000u) : scale_value(kb),
+                                                                         __int_as_float(vb == 255 ? kAmNoScale : static_cast<int>(vb) - 127));
+                    if (lane == 0) bad_pages[j % kAmScales] = from_cur ? cur.bad : next.bad;
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&scales_full[j % kAmScales]);
                 }
-                Places after = next;
-                if (j + 2 < N) after = place(j + 2);
-                if (j >= kAmRing) ok = mbar_wait_warp(&v_empty[j % kAmRing], (j / kAmRing - 1) & 1, abort, a.err, a.timeout_ns);
-                if (!ok) break;
-                pass_on(vt + j % kAmRing * S::kTile, j + 1 < N, j + 2 < N ? c.k : c.v, j + 2 < N ? after.k : next.v, after.valid);
-                if (lane == 0) mbar_arrive(&v_full[j % kAmRing]);
-                cur = next;
-                next = after;
+#pragma unroll 1
+                for (int half = 0; half < 2; ++half) {
+                    ok = am_wait(&raw_empty[stage], phase, abort, a.err, a.timeout_ns);
+                    if (!ok) break;
+                    if (lane == 4 * half) mbar_arrive_expect_tx(&raw_full[stage], total);
+                    __syncwarp();
+                    if (lane < 8 && lane >> 2 == half && bytes > 0)
+                        bulk_load(smem + S::kRaw + stage * S::kHalf + (lane & 3) * 16 * D, src, bytes, &raw_full[stage]);
+                    ++issued;
+                    if (++stage == kAmRaw) stage = 0, phase ^= 1;
+                }
+                // Behind K j comes V j - 1, then K j + 1: places move on once V j - 1 is copied.
+                if (keys && j > 0 && j + 1 < N) fetched = place(j + 1);
+                if (!keys) {
+                    cur = next;
+                    next = fetched;
+                }
             }
+            // No copy of this block's is left in flight when it ends.
+            for (int i = max(issued - kAmRaw, 0); i < issued; ++i) mbar_wait_drain(&raw_full[i % kAmRaw], (i / kAmRaw) & 1, a.timeout_ns);
         }
-    } else if (warp >= 12) {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");
-        if (warp == 12) {
+    } else if (warp == 12) {
         // ---- products
         constexpr uint32_t idesc_s = idesc_f16(128, kAmKeys, false), idesc_o = idesc_f16(128, D, true);
         const uint32_t base = smem_u32(smem);
@@ -354,8 +436,8 @@ __global__ void __launch_bounds__(kAmThreads, 1) attend_many_kernel(const __grid
         };
         bool ok = true;
         if (N > 0) {
-            ok = mbar_wait_warp(&q_full[0], 0, abort, a.err, a.timeout_ns) && mbar_wait_warp(&q_full[1], 0, abort, a.err, a.timeout_ns) &&
-                 mbar_wait_warp(&k_full[0], 0, abort, a.err, a.timeout_ns);
+            ok = am_wait(&q_full[0], 0, abort, a.err, a.timeout_ns) && am_wait(&q_full[1], 0, abort, a.err, a.timeout_ns) &&
+                 am_wait(&k_full[0], 0, abort, a.err, a.timeout_ns);
             if (ok) {
                 tc_fence_after();
                 for (int t = 0; t < 2; ++t)
@@ -363,21 +445,29 @@ __global__ void __launch_bounds__(kAmThreads, 1) attend_many_kernel(const __grid
                 tc_commit_elect(&k_empty[0]);
             }
         }
+#pragma unroll 1
         for (int j = 0; ok && j < N; ++j) {
             const int vs = j % kAmRing, kn = (j + 1) % kAmRing;
-            ok = mbar_wait_warp(&v_full[vs], (j / kAmRing) & 1, abort, a.err, a.timeout_ns);
+            ok = am_wait(&v_full[vs], (j / kAmRing) & 1, abort, a.err, a.timeout_ns);
             if (!ok) break;
             bool have_k = false;
+#pragma unroll 1
             for (int t = 0; t < 2; ++t) {
                 if (j < w.tiles[t]) {
-                    ok = mbar_wait_warp(&p_full[t], j & 1, abort, a.err, a.timeout_ns);
+                    const uint64_t v_tile = v_desc + vs * (S::kTile >> 4);
+#pragma unroll 1
+                    for (int half = 0; ok && half < 2; ++half) {
+                        ok = am_wait(&p_full[2 * t + half], j & 1, abort, a.err, a.timeout_ns);
+                        if (!ok) break;
+                        tc_fence_after();
+                        tc_values_elect(tmem + 256 + t * D, tmem + t * 128 + 32 * half, v_tile + 512 * half, idesc_o, j != 0 || half != 0);
+                    }
                     if (!ok) break;
-                    tc_fence_after();
-                    tc_values_elect(tmem + 256 + t * D, tmem + t * 128, v_desc + vs * (S::kTile >> 4), idesc_o, j != 0, &o_done[t]);
+                    tc_commit_elect(&o_done[t]);
                 }
                 if (j + 1 < w.tiles[t]) {
                     if (!have_k) {
-                        ok = mbar_wait_warp(&k_full[kn], ((j + 1) / kAmRing) & 1, abort, a.err, a.timeout_ns);
+                        ok = am_wait(&k_full[kn], ((j + 1) / kAmRing) & 1, abort, a.err, a.timeout_ns);
                         if (!ok) break;
                         have_k = true;
                         tc_fence_after();
@@ -393,9 +483,7 @@ __global__ void __launch_bounds__(kAmThreads, 1) attend_many_kernel(const __grid
         tc_commit_elect(drain);
         mbar_wait_drain(drain, 0, a.timeout_ns);
         __syncwarp();
-        }
     } else {
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 192;");
         // ---- softmax: thread = row
         const int t = warp >> 2, row = threadIdx.x & 127;
         const int r = w.row0 + t * 128 + row;                // query row of the sequence
@@ -438,8 +526,8 @@ __global__ void __launch_bounds__(kAmThreads, 1) attend_many_kernel(const __grid
         const int n = w.tiles[t];
         bool ok = true;
         for (int j = 0; j < n; ++j) {
-            ok = mbar_wait_warp(&scales_full[j % kAmScales], (j / kAmScales) & 1, abort, a.err, a.timeout_ns) &&
-                 mbar_wait_warp(&s_full[t], j & 1, abort, a.err, a.timeout_ns);
+            ok = am_wait(&scales_full[j % kAmScales], (j / kAmScales) & 1, abort, a.err, a.timeout_ns) &&
+                 am_wait(&s_full[t], j & 1, abort, a.err, a.timeout_ns);
             if (!ok) break;
             tc_fence_after();
             const float2* sc = scales + (j % kAmScales) * 8;
@@ -448,33 +536,37 @@ __global__ void __launch_bounds__(kAmThreads, 1) attend_many_kernel(const __grid
             const int end = static_cast<int>(min(max(last + 1 - key0, int64_t(0)), int64_t(kAmKeys)));
             const int begin = static_cast<int>(min(max(from - key0, int64_t(0)), int64_t(kAmKeys)));
             const bool masked = __any_sync(0xFFFFFFFFu, end < kAmKeys || begin > 0);
-            // MASKED as a type: the unmasked tiles, nearly all, have no trace of the mask in their code.
-            float s[kAmKeys];
+            // Both passes walk the row in halves. Loops, not 128 columns unrolled: the code
+            // of the roles has to stay in the instruction cache (unrolled, warps waited for instructions a fifth of the time).
+            uint32_t s[2][32];
             float top = -INFINITY;
-            int ev = kAmNoScale;
-            auto read = [&](auto MASKED) {
-                uint32_t(&u)[kAmKeys] = reinterpret_cast<uint32_t(&)[kAmKeys]>(s);
+            int ev = kAmNoScale, least = 1000;
+#pragma unroll 1
+            for (int q = 0; q < 4; q += 2) {
+                tc_ld_32x32b_x32(ts + q * 32, s[0]);
+                tc_ld_32x32b_x32(ts + q * 32 + 32, s[1]);
+                tc_wait_ld_regs(s[0], s[1]);
 #pragma unroll
-                for (int q = 0; q < 4; ++q) tc_ld_32x32b_x32(ts + q * 32, reinterpret_cast<uint32_t(&)[32]>(u[32 * q]));
-                tc_wait_ld_regs(u);
+                for (int k = 0; k < 2; ++k) {
+                    if (masked) {
+                        const uint32_t seen = seen_bits(begin, end, (q + k) * 32);
 #pragma unroll
-                for (int g = 0; g < 8; ++g) {
-                    if constexpr (MASKED.value)
+                        for (int i = 0; i < 32; ++i) s[k][i] = seen >> i & 1 ? s[k][i] : 0xFF800000u;
+                    }
 #pragma unroll
-                        for (int i = 16 * g; i < 16 * g + 16; ++i)
-                            if (i >= end || i < begin) s[i] = -INFINITY;
-                    float m = fmaxf(s[16 * g], s[16 * g + 1]);
-#pragma unroll
-                    for (int i = 2; i < 16; i += 2) m = fmaxf(m, fmaxf(s[16 * g + i], s[16 * g + i + 1]));
-                    const float2 f = sc[g];
-                    top = fmaxf(top, m * (f.x * rowf));
-                    ev = max(ev, __float_as_int(f.y));
+                    for (int g = 0; g < 2; ++g) {
+                        const float* x = reinterpret_cast<const float*>(&s[k][16 * g]);
+                        float m = max3(x[0], x[1], x[2]), m1 = max3(x[3], x[4], x[5]);
+                        m = max3(m, x[6], x[7]), m1 = max3(m1, x[8], x[9]);
+                        m = max3(m, x[10], x[11]), m1 = max3(m1, x[12], x[13]);
+                        m = max3(m, x[14], x[15]);
+                        const float2 f = sc[2 * (q + k) + g];
+                        top = fmaxf(top, fmaxf(m, m1) * (f.x * rowf));
+                        ev = max(ev, __float_as_int(f.y));
+                        least = min(least, __float_as_int(f.y));
+                    }
                 }
-            };
-            if (masked)
-                read(std::true_type());
-            else
-                read(std::false_type());
+            }
             const bool grown = ev > E;                       // the same in every row
             if (__any_sync(0xFFFFFFFFu, top > M + kAtSlack) || grown) {
                 const float next = fmaxf(M, top);
@@ -483,7 +575,7 @@ __global__ void __launch_bounds__(kAmThreads, 1) attend_many_kernel(const __grid
                 l *= f;
                 if (grown) E = ev;
                 if (j > 0) {                                 // O, once its last product is done
-                    ok = mbar_wait_warp(&o_done[t], (j - 1) & 1, abort, a.err, a.timeout_ns);
+                    ok = am_wait(&o_done[t], (j - 1) & 1, abort, a.err, a.timeout_ns);
                     if (!ok) break;
                     tc_fence_after();
 #pragma unroll 1
@@ -497,56 +589,73 @@ __global__ void __launch_bounds__(kAmThreads, 1) attend_many_kernel(const __grid
                     }
                 }
             }
-            // P, and the weights left in s for the sum, which is made once the products have theirs.
-            auto weights = [&](auto MASKED) {
+            const bool odd = __any_sync(0xFFFFFFFFu, least - E < -kAtValueRange);
+            // P by pieces of 32 keys, written over columns that have been read. Three of four exponentials go to the special-function
+            // unit, the others to the FMA pipe. The first half of P is handed over as soon as it is there.
+#pragma unroll 1
+            for (int q = 0; q < 4; q += 2) {
+                tc_ld_32x32b_x32(ts + q * 32, s[0]);
+                tc_ld_32x32b_x32(ts + q * 32 + 32, s[1]);
+                tc_wait_ld_regs(s[0], s[1]);
 #pragma unroll
-                for (int q = 0; q < 4; ++q) {
+                for (int k = 0; k < 2; ++k) {
+                    float* x = reinterpret_cast<float*>(s[k]);
+                    float back[2];
                     uint32_t p[16];
 #pragma unroll
-                    for (int g = 2 * q; g < 2 * q + 2; ++g) {
-                        const float2 f = sc[g];
-                        const int dv = __float_as_int(f.y) - E;
-                        const bool apart = dv < -kAtValueRange;          // values that do not count, or that are NaN
-                        const float kf = f.x * rowf, d = static_cast<float>(kAtBias + (apart ? 0 : dv)) - M;
-                        uint32_t seen = 0xFFFFu;
+                    for (int g = 0; g < 2; ++g) {
+                        const float2 f = sc[2 * (q + k) + g];
+                        const int dv = __float_as_int(f.y) - E, shift = kAtBias + (dv < -kAtValueRange ? 0 : dv);
+                        const float kf = f.x * rowf, d = static_cast<float>(shift) - M;
+                        back[g] = __int_as_float((127 - shift) << 23);
 #pragma unroll
                         for (int i = 16 * g; i < 16 * g + 16; i += 2) {
-                            const bool none0 = MASKED.value && s[i] == -INFINITY, none1 = MASKED.value && s[i + 1] == -INFINITY;
-                            float2 x = fma2(make_float2(s[i], s[i + 1]), make_float2(kf, kf), make_float2(d, d));
-                            s[i] = none0 ? 0.0f : exp2_approx(x.x);
-                            s[i + 1] = none1 ? 0.0f : exp2_approx(x.y);
-                            if (MASKED.value && apart) seen &= ~((none0 ? 1u : 0u) << (i % 16) | (none1 ? 2u : 0u) << (i % 16));
-                            p[(i / 2) % 16] = f16x2(s[i], s[i + 1]);
-                        }
-                        if (apart) {
-                            const bool nan = __float_as_int(f.y) == kAmNoScale;
-#pragma unroll
-                            for (int i = 0; i < 16; i += 2)
-                                p[(8 * g + i / 2) % 16] = nan ? (seen >> i & 1 ? 0x7FFFu : 0u) | (seen >> i & 2 ? 0x7FFF0000u : 0u) : 0u;
+                            float2 e = fma2(make_float2(x[i], x[i + 1]), make_float2(kf, kf), make_float2(d, d));
+                            if (kAmFma && i % 8 == 6) {
+                                e = exp2_fma(e);
+                            } else {
+                                e.x = exp2_approx(e.x);
+                                e.y = exp2_approx(e.y);
+                            }
+                            x[i] = e.x;
+                            x[i + 1] = e.y;
                         }
                     }
-                    tc_st_32x32b_x16(ts + q * 16, p);
+                    if (masked) {
+                        const uint32_t seen = seen_bits(begin, end, (q + k) * 32);
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) x[i] = seen >> i & 1 ? x[i] : 0.0f;
+                    }
+#pragma unroll
+                    for (int g = 0; g < 2; ++g) {
+                        float2 sum = make_float2(x[16 * g], x[16 * g + 1]), sum1 = make_float2(x[16 * g + 2], x[16 * g + 3]);
+#pragma unroll
+                        for (int i = 16 * g; i < 16 * g + 16; i += 2) {
+                            if (i >= 16 * g + 4) (i % 4 ? sum1 : sum) = add2(i % 4 ? sum1 : sum, make_float2(x[i], x[i + 1]));
+                            p[i / 2] = f16x2(x[i], x[i + 1]);
+                        }
+                        sum = add2(sum, sum1);
+                        l += (sum.x + sum.y) * back[g];
+                    }
+                    if (odd) {                               // values that do not count, or that are NaN
+                        const uint32_t seen = seen_bits(begin, end, (q + k) * 32);
+#pragma unroll
+                        for (int i = 0; i < 32; i += 2) {
+                            const int e = __float_as_int(sc[2 * (q + k) + i / 16].y);
+                            const uint32_t nan = (seen >> i & 1 ? 0x7FFFu : 0u) | (seen >> i & 2 ? 0x7FFF0000u : 0u);
+                            if (e - E < -kAtValueRange) p[i / 2] = e == kAmNoScale ? nan : 0u;
+                        }
+                    }
+                    tc_st_32x32b_x16(ts + (q + k) * 16, p);
                 }
-            };
-            if (masked)
-                weights(std::true_type());
-            else
-                weights(std::false_type());
-            tc_wait_st();
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&p_full[t]);
-#pragma unroll
-            for (int g = 0; g < 8; ++g) {
-                const int dv = __float_as_int(sc[g].y) - E, shift = kAtBias + (dv < -kAtValueRange ? 0 : dv);
-                float2 sum = make_float2(s[16 * g], s[16 * g + 1]);
-#pragma unroll
-                for (int i = 16 * g + 2; i < 16 * g + 16; i += 2) sum = add2(sum, make_float2(s[i], s[i + 1]));
-                l += (sum.x + sum.y) * __int_as_float((127 - shift) << 23);
+                tc_wait_st();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&p_full[2 * t + q / 2]);
             }
         }
         // ---- output
-        if (ok && n > 0) ok = mbar_wait_warp(&o_done[t], (n - 1) & 1, abort, a.err, a.timeout_ns);
+        if (ok && n > 0) ok = am_wait(&o_done[t], (n - 1) & 1, abort, a.err, a.timeout_ns);
         if (ok) {
             tc_fence_after();
             const float inv = l == 0.0f ? 0.0f : ldexpf(1.0f / l, E - kAtBias);
