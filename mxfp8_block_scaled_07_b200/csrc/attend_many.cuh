@@ -29,7 +29,8 @@ constexpr int kAmRing = 2;             // stages of K and of V
 constexpr int kAmRaw = 3;              // half tiles of codes on their way to the loaders
 constexpr int kAmScales = 4;           // tiles whose page scales are kept
 constexpr uint32_t kAmCols = 512;
-constexpr bool kAmFma = true;
+constexpr float kAmMost = 32768.0f;     // sum of 16 weights that sends M up: no weight passes f16's range
+constexpr int kAmScaleRow = 10;         // of a tile: 8 groups' (key factor, value exponent), then the largest and the least exponent
 constexpr int kAmNoScale = -100000;    // exponent of a value scale that says NaN
 
 template <int D>
@@ -40,9 +41,9 @@ struct AmSmem {
     static constexpr int kV = kK + kAmRing * kTile;
     static constexpr int kRaw = kV + kAmRing * kTile;              // codes of half tiles on their way
     static constexpr int kHalf = 64 * D;
-    static constexpr int kScales = kRaw + kAmRaw * kHalf;          // [kAmScales][8] (key factor, value exponent as an integer)
-    static constexpr int kBar = kScales + kAmScales * 8 * 8;
-    static constexpr int kBars = 2 * kAmRaw + 4 * kAmRing + kAmScales + 2 * 5 + 1;
+    static constexpr int kScales = kRaw + kAmRaw * kHalf;          // [kAmScales][kAmScaleRow]
+    static constexpr int kBar = kScales + kAmScales * kAmScaleRow * 8;
+    static constexpr int kBars = 2 * kAmRaw + 4 * kAmRing + kAmScales + 12 + 1;
     static constexpr int kMisc = kBar + kBars * 8;
     static constexpr int kBytes = kMisc + 8 + 4 * kAmScales + 1024;    // + alignment slack
 };
@@ -140,28 +141,6 @@ __device__ __forceinline__ float2 add2(float2 a, float2 b) {
     return r;
 }
 
-__device__ __forceinline__ float max3(float a, float b, float c) {
-    float r;
-    asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
-    return r;
-}
-// 2^x on the FMA pipe, for x <= 15: x = n + f with |f| <= 1/2 (Cody and Waite's reduction, by adding and subtracting 1.5 2^23),
-// 2^f by a polynomial of degree 5 (minimax by Remez's exchange, coefficients rounded to fp32: 2^-22 relative), n added to the exponent.
-// Below 2^-126 the result is 2^-126. NaN gives 2^-126 too.
-__device__ __forceinline__ float2 exp2_fma(float2 x) {
-    x.x = fmaxf(x.x, -126.0f);
-    x.y = fmaxf(x.y, -126.0f);
-    const float2 t = add2(x, make_float2(12582912.0f, 12582912.0f)), n = add2(t, make_float2(-12582912.0f, -12582912.0f));
-    const float2 f = fma2(n, make_float2(-1.0f, -1.0f), x);
-    float2 y = make_float2(0.0013276472454890609f, 0.0013276472454890609f);
-    y = fma2(y, f, make_float2(0.009675540961325169f, 0.009675540961325169f));
-    y = fma2(y, f, make_float2(0.05550713092088699f, 0.05550713092088699f));
-    y = fma2(y, f, make_float2(0.24022120237350464f, 0.24022120237350464f));
-    y = fma2(y, f, make_float2(0.6931469440460205f, 0.6931469440460205f));
-    y = fma2(y, f, make_float2(1.0000001192092896f, 1.0000001192092896f));
-    return make_float2(__int_as_float(__float_as_int(y.x) + (__float_as_int(t.x) << 23)), __int_as_float(__float_as_int(y.y) + (__float_as_int(t.y) << 23)));
-}
-
 // mbar_wait_warp, with all but the first look out of the way of the roles' loops.
 __device__ __noinline__ bool am_wait_on(uint64_t* bar, uint32_t parity, volatile int* abort, uint32_t* err, uint64_t timeout_ns) {
     return mbar_wait_warp(bar, parity, abort, err, timeout_ns);
@@ -245,8 +224,8 @@ __global__ void __launch_bounds__(kAmThreads, 1) attend_many_kernel(const __grid
     uint64_t* q_full = scales_full + kAmScales;
     uint64_t* s_full = q_full + 2;
     uint64_t* p_full = s_full + 2;
-    uint64_t* o_done = p_full + 4;               // p_full: two halves of either tile
-    uint64_t* drain = o_done + 2;
+    uint64_t* o_done = p_full + 4;               // p_full, o_done: of two halves of either tile
+    uint64_t* drain = o_done + 4;
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + S::kMisc);
     volatile int* abort = reinterpret_cast<volatile int*>(smem + S::kMisc + 4);
     uint32_t* bad_pages = reinterpret_cast<uint32_t*>(smem + S::kMisc + 8);      // of a tile: a bit per group of 16 keys
@@ -272,7 +251,8 @@ __global__ void __launch_bounds__(kAmThreads, 1) attend_many_kernel(const __grid
             mbar_init(&s_full[i], 1);
             mbar_init(&p_full[2 * i], 4);
             mbar_init(&p_full[2 * i + 1], 4);
-            mbar_init(&o_done[i], 1);
+            mbar_init(&o_done[2 * i], 1);
+            mbar_init(&o_done[2 * i + 1], 1);
         }
         mbar_init(drain, 1);
         *abort = 0;
@@ -398,9 +378,14 @@ __global__ void __launch_bounds__(kAmThreads, 1) attend_many_kernel(const __grid
                     const uint32_t kb = j == 0 && N > 1 ? ks : ks_next, vb = j == 0 && N > 1 ? vs : vs_next;
                     ok = am_wait(&raw_empty[stage], phase, abort, a.err, a.timeout_ns);
                     if (!ok) break;
-                    if (lane < 8)
-                        scales[(j % kAmScales) * 8 + lane] = make_float2(kb == 255 ? __uint_as_float(0x7FC00000u) : scale_value(kb),
-                                                                         __int_as_float(vb == 255 ? kAmNoScale : static_cast<int>(vb) - 127));
+                    // Groups behind the sequence's end take no part in the exponents' range.
+                    const int e = vb == 255 ? kAmNoScale : static_cast<int>(vb) - 127;
+                    const int most = __reduce_max_sync(0xFFFFFFFFu, lane < 8 ? e : kAmNoScale);
+                    const bool part = lane < 8 && w.lo + int64_t(j) * kAmKeys + 16 * lane < w.hi;
+                    const int least = __reduce_min_sync(0xFFFFFFFFu, part ? e : 1000);
+                    float2* row = scales + (j % kAmScales) * kAmScaleRow;
+                    if (lane < 8) row[lane] = make_float2(kb == 255 ? __uint_as_float(0x7FC00000u) : scale_value(kb), __int_as_float(e));
+                    if (lane == 8) row[8] = make_float2(__int_as_float(most), __int_as_float(least));
                     if (lane == 0) bad_pages[j % kAmScales] = from_cur ? cur.bad : next.bad;
                     __syncwarp();
                     if (lane == 0) mbar_arrive(&scales_full[j % kAmScales]);
@@ -461,9 +446,9 @@ __global__ void __launch_bounds__(kAmThreads, 1) attend_many_kernel(const __grid
                         if (!ok) break;
                         tc_fence_after();
                         tc_values_elect(tmem + 256 + t * D, tmem + t * 128 + 32 * half, v_tile + 512 * half, idesc_o, j != 0 || half != 0);
+                        tc_commit_elect(&o_done[2 * t + half]);
                     }
                     if (!ok) break;
-                    tc_commit_elect(&o_done[t]);
                 }
                 if (j + 1 < w.tiles[t]) {
                     if (!have_k) {
@@ -518,7 +503,9 @@ __global__ void __launch_bounds__(kAmThreads, 1) attend_many_kernel(const __grid
             __syncwarp();
             if (lane == 0) mbar_arrive(&q_full[t]);
         }
-        const int64_t last = have ? w.hi - w.n + tok : -1, from = last - a.window + 1;
+        // Keys [start, stop) are seen, counted from the block's first.
+        const int64_t last = have ? w.hi - w.n + tok : -1;
+        const int stop = static_cast<int>(max(last + 1 - w.lo, int64_t(0))), start = static_cast<int>(max(last - a.window + 1 - w.lo, int64_t(0)));
         const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
         const uint32_t ts = tmem + lanes + t * 128, to = tmem + lanes + 256 + t * D;
         float M = kAtNone, l = 0.0f;
@@ -530,132 +517,119 @@ __global__ void __launch_bounds__(kAmThreads, 1) attend_many_kernel(const __grid
                  am_wait(&s_full[t], j & 1, abort, a.err, a.timeout_ns);
             if (!ok) break;
             tc_fence_after();
-            const float2* sc = scales + (j % kAmScales) * 8;
-            const int64_t key0 = w.lo + int64_t(j) * kAmKeys;
-            // Columns [begin, end) of this row are seen.
-            const int end = static_cast<int>(min(max(last + 1 - key0, int64_t(0)), int64_t(kAmKeys)));
-            const int begin = static_cast<int>(min(max(from - key0, int64_t(0)), int64_t(kAmKeys)));
+            const float2* sc = scales + (j % kAmScales) * kAmScaleRow;
+            const int ev = __float_as_int(sc[8].x);              // largest value exponent of the tile
+            const int end = stop - j * kAmKeys, begin = start - j * kAmKeys;     // columns [begin, end) of this row are seen
             const bool masked = __any_sync(0xFFFFFFFFu, end < kAmKeys || begin > 0);
-            // Both passes walk the row in halves. Loops, not 128 columns unrolled: the code
-            // of the roles has to stay in the instruction cache (unrolled, warps waited for instructions a fifth of the time).
-            uint32_t s[2][32];
-            float top = -INFINITY;
-            int ev = kAmNoScale, least = 1000;
+            // Half a row at a time. There is no pass for the maximum: M only has to be near enough above for f16, and the
+            // sum of a half's weights, which is made anyway, tells whether one of them is beyond 2^15. If so, or where a larger value
+            // scale has come, M (and E) move, O is rescaled, and the half is done once more. Loops, so that the roles' code stays
+            // in the instruction cache: unrolled, warps waited for instructions a fifth of the time.
 #pragma unroll 1
-            for (int q = 0; q < 4; q += 2) {
-                tc_ld_32x32b_x32(ts + q * 32, s[0]);
-                tc_ld_32x32b_x32(ts + q * 32 + 32, s[1]);
-                tc_wait_ld_regs(s[0], s[1]);
-#pragma unroll
-                for (int k = 0; k < 2; ++k) {
-                    if (masked) {
-                        const uint32_t seen = seen_bits(begin, end, (q + k) * 32);
-#pragma unroll
-                        for (int i = 0; i < 32; ++i) s[k][i] = seen >> i & 1 ? s[k][i] : 0xFF800000u;
-                    }
-#pragma unroll
-                    for (int g = 0; g < 2; ++g) {
-                        const float* x = reinterpret_cast<const float*>(&s[k][16 * g]);
-                        float m = max3(x[0], x[1], x[2]), m1 = max3(x[3], x[4], x[5]);
-                        m = max3(m, x[6], x[7]), m1 = max3(m1, x[8], x[9]);
-                        m = max3(m, x[10], x[11]), m1 = max3(m1, x[12], x[13]);
-                        m = max3(m, x[14], x[15]);
-                        const float2 f = sc[2 * (q + k) + g];
-                        top = fmaxf(top, fmaxf(m, m1) * (f.x * rowf));
-                        ev = max(ev, __float_as_int(f.y));
-                        least = min(least, __float_as_int(f.y));
-                    }
-                }
-            }
-            const bool grown = ev > E;                       // the same in every row
-            if (__any_sync(0xFFFFFFFFu, top > M + kAtSlack) || grown) {
-                const float next = fmaxf(M, top);
-                const float f = exp2_approx(M - next), fo = grown ? ldexpf(f, max(E - ev, -300)) : f;
-                M = next;
-                l *= f;
-                if (grown) E = ev;
-                if (j > 0) {                                 // O, once its last product is done
-                    ok = am_wait(&o_done[t], (j - 1) & 1, abort, a.err, a.timeout_ns);
-                    if (!ok) break;
-                    tc_fence_after();
+            for (int half = 0; half < 2; ++half) {
+                uint32_t s[2][32], p[2][16];
+                bool move = half == 0 && ev > E, moved = false;  // the same in every row
+                float sum;
+                while (true) {
+                    if (move) {
+                        float top = -INFINITY;
 #pragma unroll 1
-                    for (int q = 0; q < D; q += 16) {
-                        uint32_t x[16];
-                        tc_ld_32x32b_x16(to + q, x);
-                        tc_wait_ld_regs(x);
+                        for (int q = 0; q < 4; ++q) {
+                            uint32_t x[16];
+                            tc_ld_32x32b_x16(ts + half * 64 + q * 16, x);
+                            tc_wait_ld_regs(x);
+                            const uint32_t seen = seen_bits(begin, end, half * 64 + q * 16);
+                            float m = -INFINITY;
 #pragma unroll
-                        for (int i = 0; i < 16; ++i) x[i] = __float_as_uint(__uint_as_float(x[i]) * fo);
-                        tc_st_32x32b_x16(to + q, x);
-                    }
-                }
-            }
-            const bool odd = __any_sync(0xFFFFFFFFu, least - E < -kAtValueRange);
-            // P by pieces of 32 keys, written over columns that have been read. Three of four exponentials go to the special-function
-            // unit, the others to the FMA pipe. The first half of P is handed over as soon as it is there.
+                            for (int i = 0; i < 16; ++i) m = fmaxf(m, seen >> i & 1 ? __uint_as_float(x[i]) : -INFINITY);
+                            top = fmaxf(top, m * (sc[4 * half + q].x * rowf));
+                        }
+                        const float next = fmaxf(M, top), f = exp2_approx(M - next);
+                        const float fo = ev > E ? ldexpf(f, max(E - ev, -300)) : f;
+                        M = next;
+                        l *= f;
+                        E = max(E, ev);
+                        if (j + half > 0) {                      // O, once its last product is done
+                            ok = am_wait(&o_done[2 * t + (half ^ 1)], (half ? j : j - 1) & 1, abort, a.err, a.timeout_ns);
+                            if (!ok) break;
+                            tc_fence_after();
 #pragma unroll 1
-            for (int q = 0; q < 4; q += 2) {
-                tc_ld_32x32b_x32(ts + q * 32, s[0]);
-                tc_ld_32x32b_x32(ts + q * 32 + 32, s[1]);
-                tc_wait_ld_regs(s[0], s[1]);
+                            for (int q = 0; q < D; q += 16) {
+                                uint32_t x[16];
+                                tc_ld_32x32b_x16(to + q, x);
+                                tc_wait_ld_regs(x);
 #pragma unroll
-                for (int k = 0; k < 2; ++k) {
-                    float* x = reinterpret_cast<float*>(s[k]);
-                    float back[2];
-                    uint32_t p[16];
-#pragma unroll
-                    for (int g = 0; g < 2; ++g) {
-                        const float2 f = sc[2 * (q + k) + g];
-                        const int dv = __float_as_int(f.y) - E, shift = kAtBias + (dv < -kAtValueRange ? 0 : dv);
-                        const float kf = f.x * rowf, d = static_cast<float>(shift) - M;
-                        back[g] = __int_as_float((127 - shift) << 23);
-#pragma unroll
-                        for (int i = 16 * g; i < 16 * g + 16; i += 2) {
-                            float2 e = fma2(make_float2(x[i], x[i + 1]), make_float2(kf, kf), make_float2(d, d));
-                            if (kAmFma && i % 8 == 6) {
-                                e = exp2_fma(e);
-                            } else {
-                                e.x = exp2_approx(e.x);
-                                e.y = exp2_approx(e.y);
+                                for (int i = 0; i < 16; ++i) x[i] = __float_as_uint(__uint_as_float(x[i]) * fo);
+                                tc_st_32x32b_x16(to + q, x);
                             }
-                            x[i] = e.x;
-                            x[i + 1] = e.y;
+                        }
+                        moved = true;
+                    }
+                    tc_ld_32x32b_x32(ts + half * 64, s[0]);
+                    tc_ld_32x32b_x32(ts + half * 64 + 32, s[1]);
+                    tc_wait_ld_regs(s[0], s[1]);
+                    float most = 0.0f;
+                    sum = 0.0f;
+#pragma unroll
+                    for (int k = 0; k < 2; ++k) {
+                        float* x = reinterpret_cast<float*>(s[k]);
+                        float back[2];
+#pragma unroll
+                        for (int g = 0; g < 2; ++g) {
+                            const float2 f = sc[4 * half + 2 * k + g];
+                            const int dv = __float_as_int(f.y) - E, shift = kAtBias + (dv < -kAtValueRange ? 0 : dv);
+                            const float kf = f.x * rowf, d = static_cast<float>(shift) - M;
+                            back[g] = __int_as_float((127 - shift) << 23);
+#pragma unroll
+                            for (int i = 16 * g; i < 16 * g + 16; i += 2) {
+                                float2 e = fma2(make_float2(x[i], x[i + 1]), make_float2(kf, kf), make_float2(d, d));
+                                x[i] = exp2_approx(e.x);
+                                x[i + 1] = exp2_approx(e.y);
+                            }
+                        }
+                        if (masked) {
+                            const uint32_t seen = seen_bits(begin, end, half * 64 + k * 32);
+#pragma unroll
+                            for (int i = 0; i < 32; ++i) x[i] = seen >> i & 1 ? x[i] : 0.0f;
+                        }
+#pragma unroll
+                        for (int g = 0; g < 2; ++g) {
+                            float2 r0 = make_float2(x[16 * g], x[16 * g + 1]), r1 = make_float2(x[16 * g + 2], x[16 * g + 3]);
+#pragma unroll
+                            for (int i = 16 * g; i < 16 * g + 16; i += 2) {
+                                if (i >= 16 * g + 4) (i % 4 ? r1 : r0) = add2(i % 4 ? r1 : r0, make_float2(x[i], x[i + 1]));
+                                p[k][i / 2] = f16x2(x[i], x[i + 1]);
+                            }
+                            r0 = add2(r0, r1);
+                            most = fmaxf(most, r0.x + r0.y);
+                            sum += (r0.x + r0.y) * back[g];
                         }
                     }
-                    if (masked) {
-                        const uint32_t seen = seen_bits(begin, end, (q + k) * 32);
-#pragma unroll
-                        for (int i = 0; i < 32; ++i) x[i] = seen >> i & 1 ? x[i] : 0.0f;
-                    }
-#pragma unroll
-                    for (int g = 0; g < 2; ++g) {
-                        float2 sum = make_float2(x[16 * g], x[16 * g + 1]), sum1 = make_float2(x[16 * g + 2], x[16 * g + 3]);
-#pragma unroll
-                        for (int i = 16 * g; i < 16 * g + 16; i += 2) {
-                            if (i >= 16 * g + 4) (i % 4 ? sum1 : sum) = add2(i % 4 ? sum1 : sum, make_float2(x[i], x[i + 1]));
-                            p[i / 2] = f16x2(x[i], x[i + 1]);
-                        }
-                        sum = add2(sum, sum1);
-                        l += (sum.x + sum.y) * back[g];
-                    }
-                    if (odd) {                               // values that do not count, or that are NaN
-                        const uint32_t seen = seen_bits(begin, end, (q + k) * 32);
-#pragma unroll
-                        for (int i = 0; i < 32; i += 2) {
-                            const int e = __float_as_int(sc[2 * (q + k) + i / 16].y);
-                            const uint32_t nan = (seen >> i & 1 ? 0x7FFFu : 0u) | (seen >> i & 2 ? 0x7FFF0000u : 0u);
-                            if (e - E < -kAtValueRange) p[i / 2] = e == kAmNoScale ? nan : 0u;
-                        }
-                    }
-                    tc_st_32x32b_x16(ts + (q + k) * 16, p);
+                    if (moved || !__any_sync(0xFFFFFFFFu, most > kAmMost)) break;
+                    move = true;
                 }
+                if (!ok) break;
+                l += sum;
+                const int least = __float_as_int(sc[8].y);
+                if (least == kAmNoScale || least - E < -kAtValueRange) {         // values that do not count, or that are NaN
+#pragma unroll
+                    for (int i = 0; i < 64; i += 2) {
+                        const int e = __float_as_int(sc[4 * half + i / 16].y);
+                        const bool lo = half * 64 + i < end && half * 64 + i >= begin, hi = half * 64 + i + 1 < end && half * 64 + i + 1 >= begin;
+                        if (e == kAmNoScale || e - E < -kAtValueRange) p[i / 32][i % 32 / 2] = e == kAmNoScale ? (lo ? 0x7FFFu : 0u) | (hi ? 0x7FFF0000u : 0u) : 0u;
+                    }
+                }
+                tc_st_32x32b_x16(ts + half * 32, p[0]);          // over columns that have been read
+                tc_st_32x32b_x16(ts + half * 32 + 16, p[1]);
                 tc_wait_st();
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&p_full[2 * t + q / 2]);
+                if (lane == 0) mbar_arrive(&p_full[2 * t + half]);
             }
+            if (!ok) break;
         }
         // ---- output
-        if (ok && n > 0) ok = am_wait(&o_done[t], (n - 1) & 1, abort, a.err, a.timeout_ns);
+        if (ok && n > 0) ok = am_wait(&o_done[2 * t + 1], (n - 1) & 1, abort, a.err, a.timeout_ns);
         if (ok) {
             tc_fence_after();
             const float inv = l == 0.0f ? 0.0f : ldexpf(1.0f / l, E - kAtBias);
