@@ -11,8 +11,10 @@
 // value scale an exponent of P, both constant over 16 columns. E4M3 operands would run at twice the rate but P (and q) would need two of
 // them each to keep BF16's accuracy, which costs the softmax's threads more than the conversion costs the converters.
 //
-// Roles (448 threads): warps 0-3 and 4-7 softmax of tiles 0 and 1, warps 8-11 conversion, warp 12 issues the products and owns TMEM
-// (S_0, S_1: 128 columns each, O_0, O_1: D each), warp 13 copies. Every wait is bounded.
+// Roles (512 threads): warps 0-3 and 4-7 softmax of tiles 0 and 1, warps 8-11 conversion, warp 12 issues the products and owns TMEM
+// (S_0, S_1: 128 columns each, O_0, O_1: D each), warp 13 copies, warps
+// 14 and 15 complete their warpgroup. The launch's 128 registers a thread are split 168 / 88 / 88 (8 x 168 + 4 x 88 + 4 x 88 = 16 x
+// 128), without which the softmax spills. Every wait is bounded.
 #pragma once
 #include <cstdint>
 #include <type_traits>
@@ -22,11 +24,11 @@
 
 namespace mx {
 
-constexpr int kAmThreads = 448;
+constexpr int kAmThreads = 512;
 constexpr int kAmRows = 256;           // query rows per block
 constexpr int kAmKeys = 128;           // keys per tile
 constexpr int kAmRing = 2;             // stages of K and of V
-constexpr int kAmRaw = 3;              // half tiles of codes on their way to the loaders
+constexpr int kAmRaw = 4;              // half tiles of codes on their way to the loaders
 constexpr int kAmScales = 4;           // tiles whose page scales are kept
 constexpr uint32_t kAmCols = 512;
 constexpr float kAmMost = 32768.0f;     // sum of 16 weights that sends M up: no weight passes f16's range
@@ -124,29 +126,27 @@ __device__ __forceinline__ void tc_st_32x32b_x16(uint32_t taddr, const uint32_t 
 __device__ __forceinline__ void tc_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 __device__ __forceinline__ void fence_async_smem() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 
-// Two fp32 lanes at once: a b + c, and a + b.
-__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
-    float2 r;
-    asm("{\n\t.reg .b64 x, y, z, w;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\tmov.b64 z, {%6, %7};\n\t"
-        "fma.rn.f32x2 w, x, y, z;\n\tmov.b64 {%0, %1}, w;\n\t}"
-        : "=f"(r.x), "=f"(r.y)
-        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+// Pairs of fp32 in a 64-bit register: a b + c, and a + b. (Packed by themselves and not within the arithmetic's asm, which moved
+// every operand anew each time.)
+__device__ __forceinline__ uint64_t pair(float lo, float hi) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
     return r;
 }
-__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+__device__ __forceinline__ float2 unpair(uint64_t x) {
     float2 r;
-    asm("{\n\t.reg .b64 x, y, w;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\tadd.rn.f32x2 w, x, y;\n\tmov.b64 {%0, %1}, w;\n\t}"
-        : "=f"(r.x), "=f"(r.y)
-        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(x));
     return r;
 }
-
-// mbar_wait_warp, with all but the first look out of the way of the roles' loops.
-__device__ __noinline__ bool am_wait_on(uint64_t* bar, uint32_t parity, volatile int* abort, uint32_t* err, uint64_t timeout_ns) {
-    return mbar_wait_warp(bar, parity, abort, err, timeout_ns);
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
 }
-__device__ __forceinline__ bool am_wait(uint64_t* bar, uint32_t parity, volatile int* abort, uint32_t* err, uint64_t timeout_ns) {
-    return __all_sync(0xFFFFFFFFu, mbar_try_wait(smem_u32(bar), parity)) || am_wait_on(bar, parity, abort, err, timeout_ns);
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
 }
 
 // Bits of 32 columns from `at` on that lie in [begin, end).
@@ -269,6 +269,7 @@ __global__ void __launch_bounds__(kAmThreads, 1) attend_many_kernel(const __grid
     const int N = max(w.tiles[0], w.tiles[1]);
 
     if (warp >= 8 && warp < 12) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
         // ---- convert: codes of half tiles, as they lie in their pages, to f16 in the products' layout
         constexpr int U = 64 * D / 16 / 128;                 // 16-byte pieces per thread and half tile
         constexpr int R = 2048 / D;                          // rows that the four warps take at once: 16 or 32
@@ -285,13 +286,13 @@ __global__ void __launch_bounds__(kAmThreads, 1) attend_many_kernel(const __grid
         for (int item = 0; ok && item < 2 * N; ++item) {
             bool keys;
             const int j = tile_of(item, N, keys), st = j % kAmRing;
-            if (j >= kAmRing) ok = am_wait(keys ? &k_empty[st] : &v_empty[st], (j / kAmRing - 1) & 1, abort, a.err, a.timeout_ns);
+            if (j >= kAmRing) ok = mbar_wait_warp(keys ? &k_empty[st] : &v_empty[st], (j / kAmRing - 1) & 1, abort, a.err, a.timeout_ns);
             if (!ok) break;
             const uint32_t tile = smem_u32(smem) + (keys ? S::kK : S::kV) + st * S::kTile;
             const int64_t left = w.hi - (w.lo + int64_t(j) * kAmKeys);       // keys from the tile's first on
 #pragma unroll 1
             for (int half = 0; half < 2; ++half) {
-                ok = am_wait(&raw_full[stage], phase, abort, a.err, a.timeout_ns);
+                ok = mbar_wait_warp(&raw_full[stage], phase, abort, a.err, a.timeout_ns);
                 if (!ok) break;
                 uint4 x[U];
 #pragma unroll
@@ -319,7 +320,66 @@ __global__ void __launch_bounds__(kAmThreads, 1) attend_many_kernel(const __grid
             __syncwarp();
             if (lane == 0) mbar_arrive(keys ? &k_full[st] : &v_full[st]);
         }
-    } else if (warp == 13) {
+    } else if (warp >= 12) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
+        if (warp == 12) {
+        // ---- products
+        constexpr uint32_t idesc_s = idesc_f16(128, kAmKeys, false), idesc_o = idesc_f16(128, D, true);
+        const uint32_t base = smem_u32(smem);
+        const uint64_t q_desc = sdesc_kmajor_sw128(base + S::kQ), k_desc = sdesc_kmajor_sw128(base + S::kK), v_desc = sdesc_mnmajor_sw128(base + S::kV);
+        auto scores = [&](int t, int st) {
+            tc_scores_elect<D>(tmem + t * 128, q_desc + t * (S::kTile >> 4), k_desc + st * (S::kTile >> 4), idesc_s, &s_full[t]);
+        };
+        bool ok = true;
+        if (N > 0) {
+            ok = mbar_wait_warp(&q_full[0], 0, abort, a.err, a.timeout_ns) && mbar_wait_warp(&q_full[1], 0, abort, a.err, a.timeout_ns) &&
+                 mbar_wait_warp(&k_full[0], 0, abort, a.err, a.timeout_ns);
+            if (ok) {
+                tc_fence_after();
+                for (int t = 0; t < 2; ++t)
+                    if (w.tiles[t] > 0) scores(t, 0);
+                tc_commit_elect(&k_empty[0]);
+            }
+        }
+#pragma unroll 1
+        for (int j = 0; ok && j < N; ++j) {
+            const int vs = j % kAmRing, kn = (j + 1) % kAmRing;
+            ok = mbar_wait_warp(&v_full[vs], (j / kAmRing) & 1, abort, a.err, a.timeout_ns);
+            if (!ok) break;
+            bool have_k = false;
+#pragma unroll 1
+            for (int t = 0; t < 2; ++t) {
+                if (j < w.tiles[t]) {
+                    const uint64_t v_tile = v_desc + vs * (S::kTile >> 4);
+#pragma unroll 1
+                    for (int half = 0; ok && half < 2; ++half) {
+                        ok = mbar_wait_warp(&p_full[2 * t + half], j & 1, abort, a.err, a.timeout_ns);
+                        if (!ok) break;
+                        tc_fence_after();
+                        tc_values_elect(tmem + 256 + t * D, tmem + t * 128 + 32 * half, v_tile + 512 * half, idesc_o, j != 0 || half != 0);
+                        tc_commit_elect(&o_done[2 * t + half]);
+                    }
+                    if (!ok) break;
+                }
+                if (j + 1 < w.tiles[t]) {
+                    if (!have_k) {
+                        ok = mbar_wait_warp(&k_full[kn], ((j + 1) / kAmRing) & 1, abort, a.err, a.timeout_ns);
+                        if (!ok) break;
+                        have_k = true;
+                        tc_fence_after();
+                    }
+                    scores(t, kn);
+                }
+            }
+            if (!ok) break;
+            tc_commit_elect(&v_empty[vs]);
+            if (have_k) tc_commit_elect(&k_empty[kn]);
+        }
+        // Every product issued by this warp has completed once `drain` fires.
+        tc_commit_elect(drain);
+        mbar_wait_drain(drain, 0, a.timeout_ns);
+        __syncwarp();
+        } else if (warp == 13) {
         // ---- copy: lane l < 8 copies the 16 keys of group l, half a tile (four lanes) at a time, and brings the page scales
         int id_next = -1;                                    // page of group `lane`, of the tile behind the last one placed
         uint32_t ks_next = 255, vs_next = 255, ks = 255, vs = 255;       // scale bytes of the tile last placed and of the one in front of it
@@ -376,7 +436,7 @@ __global__ void __launch_bounds__(kAmThreads, 1) attend_many_kernel(const __grid
                     // Tile j's scales, before its keys: the softmax reads them with its scores. place() was last called for tile j, or
                     // at the start for tile 1. The slot's last reader was done before the keys of tile j - 1 were converted.
                     const uint32_t kb = j == 0 && N > 1 ? ks : ks_next, vb = j == 0 && N > 1 ? vs : vs_next;
-                    ok = am_wait(&raw_empty[stage], phase, abort, a.err, a.timeout_ns);
+                    ok = mbar_wait_warp(&raw_empty[stage], phase, abort, a.err, a.timeout_ns);
                     if (!ok) break;
                     // Groups behind the sequence's end take no part in the exponents' range.
                     const int e = vb == 255 ? kAmNoScale : static_cast<int>(vb) - 127;
@@ -392,7 +452,7 @@ __global__ void __launch_bounds__(kAmThreads, 1) attend_many_kernel(const __grid
                 }
 #pragma unroll 1
                 for (int half = 0; half < 2; ++half) {
-                    ok = am_wait(&raw_empty[stage], phase, abort, a.err, a.timeout_ns);
+                    ok = mbar_wait_warp(&raw_empty[stage], phase, abort, a.err, a.timeout_ns);
                     if (!ok) break;
                     if (lane == 4 * half) mbar_arrive_expect_tx(&raw_full[stage], total);
                     __syncwarp();
@@ -411,64 +471,9 @@ __global__ void __launch_bounds__(kAmThreads, 1) attend_many_kernel(const __grid
             // No copy of this block's is left in flight when it ends.
             for (int i = max(issued - kAmRaw, 0); i < issued; ++i) mbar_wait_drain(&raw_full[i % kAmRaw], (i / kAmRaw) & 1, a.timeout_ns);
         }
-    } else if (warp == 12) {
-        // ---- products
-        constexpr uint32_t idesc_s = idesc_f16(128, kAmKeys, false), idesc_o = idesc_f16(128, D, true);
-        const uint32_t base = smem_u32(smem);
-        const uint64_t q_desc = sdesc_kmajor_sw128(base + S::kQ), k_desc = sdesc_kmajor_sw128(base + S::kK), v_desc = sdesc_mnmajor_sw128(base + S::kV);
-        auto scores = [&](int t, int st) {
-            tc_scores_elect<D>(tmem + t * 128, q_desc + t * (S::kTile >> 4), k_desc + st * (S::kTile >> 4), idesc_s, &s_full[t]);
-        };
-        bool ok = true;
-        if (N > 0) {
-            ok = am_wait(&q_full[0], 0, abort, a.err, a.timeout_ns) && am_wait(&q_full[1], 0, abort, a.err, a.timeout_ns) &&
-                 am_wait(&k_full[0], 0, abort, a.err, a.timeout_ns);
-            if (ok) {
-                tc_fence_after();
-                for (int t = 0; t < 2; ++t)
-                    if (w.tiles[t] > 0) scores(t, 0);
-                tc_commit_elect(&k_empty[0]);
-            }
         }
-#pragma unroll 1
-        for (int j = 0; ok && j < N; ++j) {
-            const int vs = j % kAmRing, kn = (j + 1) % kAmRing;
-            ok = am_wait(&v_full[vs], (j / kAmRing) & 1, abort, a.err, a.timeout_ns);
-            if (!ok) break;
-            bool have_k = false;
-#pragma unroll 1
-            for (int t = 0; t < 2; ++t) {
-                if (j < w.tiles[t]) {
-                    const uint64_t v_tile = v_desc + vs * (S::kTile >> 4);
-#pragma unroll 1
-                    for (int half = 0; ok && half < 2; ++half) {
-                        ok = am_wait(&p_full[2 * t + half], j & 1, abort, a.err, a.timeout_ns);
-                        if (!ok) break;
-                        tc_fence_after();
-                        tc_values_elect(tmem + 256 + t * D, tmem + t * 128 + 32 * half, v_tile + 512 * half, idesc_o, j != 0 || half != 0);
-                        tc_commit_elect(&o_done[2 * t + half]);
-                    }
-                    if (!ok) break;
-                }
-                if (j + 1 < w.tiles[t]) {
-                    if (!have_k) {
-                        ok = am_wait(&k_full[kn], ((j + 1) / kAmRing) & 1, abort, a.err, a.timeout_ns);
-                        if (!ok) break;
-                        have_k = true;
-                        tc_fence_after();
-                    }
-                    scores(t, kn);
-                }
-            }
-            if (!ok) break;
-            tc_commit_elect(&v_empty[vs]);
-            if (have_k) tc_commit_elect(&k_empty[kn]);
-        }
-        // Every product issued by this warp has completed once `drain` fires.
-        tc_commit_elect(drain);
-        mbar_wait_drain(drain, 0, a.timeout_ns);
-        __syncwarp();
     } else {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 168;");
         // ---- softmax: thread = row
         const int t = warp >> 2, row = threadIdx.x & 127;
         const int r = w.row0 + t * 128 + row;                // query row of the sequence
@@ -513,8 +518,8 @@ __global__ void __launch_bounds__(kAmThreads, 1) attend_many_kernel(const __grid
         const int n = w.tiles[t];
         bool ok = true;
         for (int j = 0; j < n; ++j) {
-            ok = am_wait(&scales_full[j % kAmScales], (j / kAmScales) & 1, abort, a.err, a.timeout_ns) &&
-                 am_wait(&s_full[t], j & 1, abort, a.err, a.timeout_ns);
+            ok = mbar_wait_warp(&scales_full[j % kAmScales], (j / kAmScales) & 1, abort, a.err, a.timeout_ns) &&
+                 mbar_wait_warp(&s_full[t], j & 1, abort, a.err, a.timeout_ns);
             if (!ok) break;
             tc_fence_after();
             const float2* sc = scales + (j % kAmScales) * kAmScaleRow;
@@ -522,96 +527,95 @@ __global__ void __launch_bounds__(kAmThreads, 1) attend_many_kernel(const __grid
             const int end = stop - j * kAmKeys, begin = start - j * kAmKeys;     // columns [begin, end) of this row are seen
             const bool masked = __any_sync(0xFFFFFFFFu, end < kAmKeys || begin > 0);
             // Half a row at a time. There is no pass for the maximum: M only has to be near enough above for f16, and the
-            // sum of a half's weights, which is made anyway, tells whether one of them is beyond 2^15. If so, or where a larger value
-            // scale has come, M (and E) move, O is rescaled, and the half is done once more. Loops, so that the roles' code stays
-            // in the instruction cache: unrolled, warps waited for instructions a fifth of the time.
+            // sums of the weights, which are made anyway, tell whether one of them is beyond 2^15. If so, or where a larger value
+            // scale has come, M (and E) move, O is rescaled, and the half's weights are made once more. Loops, so that the roles'
+            // code stays in the instruction cache: unrolled, warps waited for instructions a fifth of the time.
 #pragma unroll 1
             for (int half = 0; half < 2; ++half) {
-                uint32_t s[2][32], p[2][16];
-                bool move = half == 0 && ev > E, moved = false;  // the same in every row
-                float sum;
-                while (true) {
-                    if (move) {
-                        float top = -INFINITY;
-#pragma unroll 1
-                        for (int q = 0; q < 4; ++q) {
-                            uint32_t x[16];
-                            tc_ld_32x32b_x16(ts + half * 64 + q * 16, x);
-                            tc_wait_ld_regs(x);
-                            const uint32_t seen = seen_bits(begin, end, half * 64 + q * 16);
-                            float m = -INFINITY;
-#pragma unroll
-                            for (int i = 0; i < 16; ++i) m = fmaxf(m, seen >> i & 1 ? __uint_as_float(x[i]) : -INFINITY);
-                            top = fmaxf(top, m * (sc[4 * half + q].x * rowf));
-                        }
-                        const float next = fmaxf(M, top), f = exp2_approx(M - next);
-                        const float fo = ev > E ? ldexpf(f, max(E - ev, -300)) : f;
-                        M = next;
-                        l *= f;
-                        E = max(E, ev);
-                        if (j + half > 0) {                      // O, once its last product is done
-                            ok = am_wait(&o_done[2 * t + (half ^ 1)], (half ? j : j - 1) & 1, abort, a.err, a.timeout_ns);
-                            if (!ok) break;
-                            tc_fence_after();
-#pragma unroll 1
-                            for (int q = 0; q < D; q += 16) {
-                                uint32_t x[16];
-                                tc_ld_32x32b_x16(to + q, x);
-                                tc_wait_ld_regs(x);
-#pragma unroll
-                                for (int i = 0; i < 16; ++i) x[i] = __float_as_uint(__uint_as_float(x[i]) * fo);
-                                tc_st_32x32b_x16(to + q, x);
-                            }
-                        }
-                        moved = true;
-                    }
+                uint32_t s[2][32];
+                float* x = reinterpret_cast<float*>(s[0]);
+                float most, sum;
+                auto weights = [&]() {
                     tc_ld_32x32b_x32(ts + half * 64, s[0]);
                     tc_ld_32x32b_x32(ts + half * 64 + 32, s[1]);
                     tc_wait_ld_regs(s[0], s[1]);
-                    float most = 0.0f;
-                    sum = 0.0f;
+                    float back[4];
 #pragma unroll
-                    for (int k = 0; k < 2; ++k) {
-                        float* x = reinterpret_cast<float*>(s[k]);
-                        float back[2];
+                    for (int g = 0; g < 4; ++g) {
+                        const float2 f = sc[4 * half + g];
+                        const int dv = __float_as_int(f.y) - E, shift = kAtBias + (dv < -kAtValueRange ? 0 : dv);
+                        const float kf = f.x * rowf, d = static_cast<float>(shift) - M;
+                        const uint64_t kf2 = pair(kf, kf), d2 = pair(d, d);
+                        back[g] = __int_as_float((127 - shift) << 23);
 #pragma unroll
-                        for (int g = 0; g < 2; ++g) {
-                            const float2 f = sc[4 * half + 2 * k + g];
-                            const int dv = __float_as_int(f.y) - E, shift = kAtBias + (dv < -kAtValueRange ? 0 : dv);
-                            const float kf = f.x * rowf, d = static_cast<float>(shift) - M;
-                            back[g] = __int_as_float((127 - shift) << 23);
-#pragma unroll
-                            for (int i = 16 * g; i < 16 * g + 16; i += 2) {
-                                float2 e = fma2(make_float2(x[i], x[i + 1]), make_float2(kf, kf), make_float2(d, d));
-                                x[i] = exp2_approx(e.x);
-                                x[i + 1] = exp2_approx(e.y);
-                            }
-                        }
-                        if (masked) {
-                            const uint32_t seen = seen_bits(begin, end, half * 64 + k * 32);
-#pragma unroll
-                            for (int i = 0; i < 32; ++i) x[i] = seen >> i & 1 ? x[i] : 0.0f;
-                        }
-#pragma unroll
-                        for (int g = 0; g < 2; ++g) {
-                            float2 r0 = make_float2(x[16 * g], x[16 * g + 1]), r1 = make_float2(x[16 * g + 2], x[16 * g + 3]);
-#pragma unroll
-                            for (int i = 16 * g; i < 16 * g + 16; i += 2) {
-                                if (i >= 16 * g + 4) (i % 4 ? r1 : r0) = add2(i % 4 ? r1 : r0, make_float2(x[i], x[i + 1]));
-                                p[k][i / 2] = f16x2(x[i], x[i + 1]);
-                            }
-                            r0 = add2(r0, r1);
-                            most = fmaxf(most, r0.x + r0.y);
-                            sum += (r0.x + r0.y) * back[g];
+                        for (int i = 16 * g; i < 16 * g + 16; i += 2) {
+                            const float2 e = unpair(fma2(pair(x[i], x[i + 1]), kf2, d2));
+                            x[i] = exp2_approx(e.x);
+                            x[i + 1] = exp2_approx(e.y);
                         }
                     }
-                    if (moved || !__any_sync(0xFFFFFFFFu, most > kAmMost)) break;
-                    move = true;
+                    if (masked) {
+                        __syncwarp();                            // a branch and not 64 selections in every tile
+#pragma unroll
+                        for (int k = 0; k < 2; ++k) {
+                            const uint32_t seen = seen_bits(begin, end, half * 64 + k * 32);
+#pragma unroll
+                            for (int i = 0; i < 32; ++i) x[32 * k + i] = seen >> i & 1 ? x[32 * k + i] : 0.0f;
+                        }
+                    }
+                    most = sum = 0.0f;
+#pragma unroll
+                    for (int g = 0; g < 4; ++g) {
+                        uint64_t s0 = pair(x[16 * g], x[16 * g + 1]), s1 = pair(x[16 * g + 2], x[16 * g + 3]);
+#pragma unroll
+                        for (int i = 16 * g + 4; i < 16 * g + 16; i += 2) (i % 4 ? s1 : s0) = add2(i % 4 ? s1 : s0, pair(x[i], x[i + 1]));
+                        const float2 r = unpair(add2(s0, s1));
+                        most = fmaxf(most, r.x + r.y);
+                        sum += (r.x + r.y) * back[g];
+                    }
+                };
+                weights();
+                if (__any_sync(0xFFFFFFFFu, most > kAmMost) || (half == 0 && ev > E)) {
+                    float top = -INFINITY;
+#pragma unroll 1
+                    for (int q = 0; q < 4; ++q) {
+                        uint32_t y[16];
+                        tc_ld_32x32b_x16(ts + half * 64 + q * 16, y);
+                        tc_wait_ld_regs(y);
+                        const uint32_t seen = seen_bits(begin, end, half * 64 + q * 16);
+                        float m = -INFINITY;
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) m = fmaxf(m, seen >> i & 1 ? __uint_as_float(y[i]) : -INFINITY);
+                        top = fmaxf(top, m * (sc[4 * half + q].x * rowf));
+                    }
+                    const float next = fmaxf(M, top), f = exp2_approx(M - next);
+                    const float fo = ev > E ? ldexpf(f, max(E - ev, -300)) : f;
+                    M = next;
+                    l *= f;
+                    E = max(E, ev);
+                    if (j + half > 0) {                          // O, once its last product is done
+                        ok = mbar_wait_warp(&o_done[2 * t + (half ^ 1)], (half ? j : j - 1) & 1, abort, a.err, a.timeout_ns);
+                        if (!ok) break;
+                        tc_fence_after();
+#pragma unroll 1
+                        for (int q = 0; q < D; q += 16) {
+                            uint32_t y[16];
+                            tc_ld_32x32b_x16(to + q, y);
+                            tc_wait_ld_regs(y);
+#pragma unroll
+                            for (int i = 0; i < 16; ++i) y[i] = __float_as_uint(__uint_as_float(y[i]) * fo);
+                            tc_st_32x32b_x16(to + q, y);
+                        }
+                    }
+                    weights();
                 }
-                if (!ok) break;
+                uint32_t p[2][16];
+#pragma unroll
+                for (int i = 0; i < 64; i += 2) p[i / 32][i % 32 / 2] = f16x2(x[i], x[i + 1]);
                 l += sum;
                 const int least = __float_as_int(sc[8].y);
                 if (least == kAmNoScale || least - E < -kAtValueRange) {         // values that do not count, or that are NaN
+                    __syncwarp();
 #pragma unroll
                     for (int i = 0; i < 64; i += 2) {
                         const int e = __float_as_int(sc[4 * half + i / 16].y);
@@ -629,7 +633,7 @@ __global__ void __launch_bounds__(kAmThreads, 1) attend_many_kernel(const __grid
             if (!ok) break;
         }
         // ---- output
-        if (ok && n > 0) ok = am_wait(&o_done[2 * t + 1], (n - 1) & 1, abort, a.err, a.timeout_ns);
+        if (ok && n > 0) ok = mbar_wait_warp(&o_done[2 * t + 1], (n - 1) & 1, abort, a.err, a.timeout_ns);
         if (ok) {
             tc_fence_after();
             const float inv = l == 0.0f ? 0.0f : ldexpf(1.0f / l, E - kAtBias);
