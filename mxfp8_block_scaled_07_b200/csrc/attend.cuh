@@ -23,6 +23,7 @@
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
+#include <climits>
 #include <cstdint>
 
 #include "cache.cuh"
@@ -74,6 +75,9 @@ __device__ __forceinline__ uint32_t transposed8x8(uint32_t x) {
     uint32_t r;
     asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
     return r;
+}
+__device__ __forceinline__ void copy16(uint32_t saddr, const void* g) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(saddr), "l"(g) : "memory");
 }
 // 16 bytes to shared memory; zeros where `have` is 0.
 __device__ __forceinline__ void copy16(uint32_t saddr, const void* g, bool have) {
@@ -180,7 +184,8 @@ __host__ __device__ constexpr int64_t part_floats(int rows, int D) { return int6
 template <int D, int NT>
 struct AtSmem {
     static constexpr int kStage = 2 * 16 * D;                     // keys, then values
-    static constexpr int kStages = D == 128 ? 6 : 12;
+    static constexpr int kBlocks = NT == 1 ? 3 : 2;               // an SM's
+    static constexpr int kStages = (NT == 1 ? 4 : 6) * 128 / D;
     static constexpr int kWarp = kStages * kStage;                // a warp's ring; at the end of a tile, its O
     static constexpr int kBytes = kAtWarps * kWarp;
     static_assert(8 * NT * (D + 4) * 4 <= kWarp, "a warp's O takes the place of its ring");
@@ -194,7 +199,7 @@ __device__ __forceinline__ int ring_piece(int row, int piece) {
 }
 
 template <int D, int NT>
-__global__ void __launch_bounds__(kAtThreads, 2) attend_few_kernel(const __grid_constant__ AttendArgs a) {
+__global__ void __launch_bounds__(kAtThreads, NT == 1 ? 3 : 2) attend_few_kernel(const __grid_constant__ AttendArgs a) {
     grid_wait();
     constexpr int ROWS = 8 * NT;
     using S = AtSmem<D, NT>;
@@ -232,7 +237,8 @@ __global__ void __launch_bounds__(kAtThreads, 2) attend_few_kernel(const __grid_
         // lane (., c4) holds of a key: pieces c4 and c4 + 4 (D = 128), or c4 (D = 64).
         uint32_t qf[NT][KS][2];
         float rowf[NT][2];                      // argument of 2^x per unit of S, of columns 2 c4 and 2 c4 + 1
-        int64_t last[NT][2], from[NT][2];       // keys that these columns see: [from, last]
+        int stop[NT][2], start[NT][2];          // keys that these columns see, [start, stop), counted from sq.lo
+        int all_from = 0, all_to = INT_MAX;     // keys that every column of the tile that has a row sees
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
             const int r = row0 + 8 * nt + g;
@@ -270,12 +276,18 @@ __global__ void __launch_bounds__(kAtThreads, 2) attend_few_kernel(const __grid_
             for (int j = 0; j < 2; ++j) {
                 rowf[nt][j] = __shfl_sync(0xFFFFFFFFu, f, (2 * c4 + j) * 4);
                 const int col = row0 + 8 * nt + 2 * c4 + j;
-                const int64_t l = col < sq.rows ? sq.hi - sq.n + a.group.div(col) : -1;
-                last[nt][j] = l;
-                from[nt][j] = l - a.window + 1;
+                const int64_t last = col < sq.rows ? sq.hi - sq.n + a.group.div(col) : -1;
+                stop[nt][j] = static_cast<int>(max(last + 1 - sq.lo, int64_t(0)));
+                start[nt][j] = static_cast<int>(max(last - a.window + 1 - sq.lo, int64_t(0)));
+                if (col < sq.rows) {
+                    all_from = max(all_from, start[nt][j]);
+                    all_to = min(all_to, stop[nt][j]);
+                }
             }
         }
 
+        all_from = __reduce_max_sync(0xFFFFFFFFu, all_from);
+        all_to = __reduce_min_sync(0xFFFFFFFFu, all_to);
         float o[NT][KS][4], M[NT][2], l[NT][2];
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
@@ -289,6 +301,7 @@ __global__ void __launch_bounds__(kAtThreads, 2) attend_few_kernel(const __grid_
         // Pages of 32 steps, a lane each, one batch ahead: (page id, scale bytes).
         const int steps = static_cast<int>(s1 - s0);
         const int64_t tok0 = sq.lo + s0 * kAtStep + 16 * warp;
+        const int key0 = static_cast<int>(s0 * kAtStep) + 16 * warp;
         int64_t next_id = -1, cur_id = -1;
         uint32_t next_sc = 0xFFFF, cur_sc = 0xFFFF;
         auto fetch_ids = [&](int base) {
@@ -302,6 +315,13 @@ __global__ void __launch_bounds__(kAtThreads, 2) attend_few_kernel(const __grid_
         auto fetch_scales = [&]() {
             next_sc = next_id < 0 ? 0xFFFFu : c.ks[next_id * c.ks_page + h] | static_cast<uint32_t>(c.vs[next_id * c.vs_page + h]) << 8;
         };
+        // Where the lane's pieces of a step go, piece i at to[i % 2] + 512 i: the order of a row's pieces repeats every 8 rows.
+        uint32_t to[2];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const int row = (i * 32 + lane) / (D / 16), piece = lane % (D / 16);
+            to[i] = row * D + ring_piece<D>(row, piece) * 16 - i * 512;
+        }
         int put = 0;                            // steps whose copies are issued
         auto issue = [&]() {
             if (put < steps) {
@@ -321,18 +341,25 @@ __global__ void __launch_bounds__(kAtThreads, 2) attend_few_kernel(const __grid_
                 const int stage = put % kS;
                 if (lane == 0) stage_scales[warp][stage] = static_cast<uint16_t>(sc);
                 const int64_t tok = tok0 + int64_t(put) * kAtStep;
-                const int64_t inner = ((static_cast<int64_t>(h) << c.page_shift) + (tok & ((1 << c.page_shift) - 1))) * D;
-                const int valid = id < 0 ? 0 : static_cast<int>(min(sq.hi - tok, int64_t(16)));
-                const uint8_t* kp = c.k + max(id, int64_t(0)) * c.k_page + inner;
-                const uint8_t* vp = c.v + max(id, int64_t(0)) * c.v_page + inner;
+                const int64_t inner = ((static_cast<int64_t>(h) << c.page_shift) + (tok & ((1 << c.page_shift) - 1))) * D + lane * 16;
+                const uint8_t* kp = c.k + (id * c.k_page + inner);
+                const uint8_t* vp = c.v + (id * c.v_page + inner);
                 const uint32_t dst = ring + stage * S::kStage;
+                if (id >= 0 && tok + 16 <= sq.hi) {
 #pragma unroll
-                for (int i = 0; i < D / 32; ++i) {
-                    const int at16 = i * 32 + lane, row = at16 / (D / 16), piece = at16 % (D / 16);
-                    const uint32_t to = dst + row * D + ring_piece<D>(row, piece) * 16;
-                    const int off = row < valid ? at16 * 16 : 0;
-                    copy16(to, valid > 0 ? kp + off : c.k, row < valid);
-                    copy16(to + 16 * D, valid > 0 ? vp + off : c.v, row < valid);
+                    for (int i = 0; i < D / 32; ++i) {
+                        copy16(dst + to[i % 2] + i * 512, kp + i * 512);
+                        copy16(dst + to[i % 2] + i * 512 + 16 * D, vp + i * 512);
+                    }
+                } else {
+                    __syncwarp();
+                    const int valid = id < 0 ? 0 : static_cast<int>(max(min(sq.hi - tok, int64_t(16)), int64_t(0)));
+#pragma unroll
+                    for (int i = 0; i < D / 32; ++i) {
+                        const bool have = (i * 32 + lane) / (D / 16) < valid;
+                        copy16(dst + to[i % 2] + i * 512, have ? kp + i * 512 : c.k, have);
+                        copy16(dst + to[i % 2] + i * 512 + 16 * D, have ? vp + i * 512 : c.v, have);
+                    }
                 }
                 ++put;
             }
@@ -349,7 +376,7 @@ __global__ void __launch_bounds__(kAtThreads, 2) attend_few_kernel(const __grid_
             const uint8_t* kr = ring_p + stage * S::kStage;
             const uint8_t* vr = kr + 16 * D;
             const uint32_t sc = stage_scales[warp][stage];
-            const int64_t tok = tok0 + int64_t(st) * kAtStep;
+            const int key = key0 + st * kAtStep;       // the first of the 16, from sq.lo
 
             float s[NT][4];
 #pragma unroll
@@ -371,15 +398,24 @@ __global__ void __launch_bounds__(kAtThreads, 2) attend_few_kernel(const __grid_
             const uint32_t kb = sc & 0xFFu, vb = sc >> 8;
             const float kscale = kb == 255 ? __uint_as_float(0x7FC00000u) : scale_value(kb);
             bool more = false;
+            const bool edge = key < all_from || key + 16 > all_to;
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
+            for (int nt = 0; nt < NT; ++nt) {
+                const float f0 = rowf[nt][0] * kscale, f1 = rowf[nt][1] * kscale;
+                s[nt][0] *= f0, s[nt][1] *= f1, s[nt][2] *= f0, s[nt][3] *= f1;
+            }
+            if (edge) {
+                __syncwarp();                          // a branch and not selections in every step
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const int64_t j = tok + g + 8 * (i >> 1);
-                    const bool seen = j <= last[nt][i & 1] && j >= from[nt][i & 1];
-                    s[nt][i] = seen ? s[nt][i] * (rowf[nt][i & 1] * kscale) : -INFINITY;
-                    more |= s[nt][i] > M[nt][i & 1] + kAtSlack;
-                }
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const int at = key + g + 8 * (i >> 1);
+                        if (at >= stop[nt][i & 1] || at < start[nt][i & 1]) s[nt][i] = -INFINITY;
+                    }
+            }
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) more |= fmaxf(s[nt][0], s[nt][2]) > M[nt][0] + kAtSlack || fmaxf(s[nt][1], s[nt][3]) > M[nt][1] + kAtSlack;
             if (__any_sync(0xFFFFFFFFu, more)) {
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt)
@@ -416,7 +452,7 @@ __global__ void __launch_bounds__(kAtThreads, 2) attend_few_kernel(const __grid_
             for (int nt = 0; nt < NT; ++nt) {
                 float p[4];
 #pragma unroll
-                for (int i = 0; i < 4; ++i) p[i] = s[nt][i] == -INFINITY ? 0.0f : exp2_approx(s[nt][i] - M[nt][i & 1] + shift);
+                for (int i = 0; i < 4; ++i) p[i] = exp2_approx(s[nt][i] + (shift - M[nt][i & 1]));      // 0 of -inf: M is finite
                 l[nt][0] += (p[0] + p[2]) * back;
                 l[nt][1] += (p[1] + p[3]) * back;
                 if (apart)
@@ -517,48 +553,61 @@ __global__ void __launch_bounds__(kAtThreads, 2) attend_few_kernel(const __grid_
     }
 }
 
+constexpr int kAtJoinThreads = 256;
+
 // Joins the parts of tiles whose steps went to several blocks: a block per (sequence, key head, tile of rows), a warp per
-// row. Parts are added in the order of their keys.
+// row. Parts are added in the order of their keys, 16 of them on their way at a time.
 template <int D, int NT>
-__global__ void __launch_bounds__(kAtThreads) attend_join_kernel(const __grid_constant__ AttendArgs a, int tiles) {
+__global__ void __launch_bounds__(kAtJoinThreads) attend_join_kernel(const __grid_constant__ AttendArgs a, int tiles) {
     grid_wait();
     constexpr int ROWS = 8 * NT;
-    __shared__ Steps<ROWS, kAtThreads> todo;
+    __shared__ Steps<ROWS, kAtJoinThreads> todo;
     const CacheView& c = a.c;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int tile = blockIdx.x % tiles, h = blockIdx.x / tiles % c.Hkv, b = blockIdx.x / tiles / c.Hkv;
     const Sequence sq = sequence<ROWS>(a, b);
     if (tile >= sq.tiles) return;
-    count_steps<ROWS, kAtThreads>(a, todo);
+    count_steps<ROWS, kAtJoinThreads>(a, todo);
     const int64_t share = share_of(a, todo.total);
-    const int64_t s0 = steps_before<ROWS, kAtThreads>(a, todo, b) + (int64_t(h) * sq.tiles + tile) * sq.steps;
+    const int64_t s0 = steps_before<ROWS, kAtJoinThreads>(a, todo, b) + (int64_t(h) * sq.tiles + tile) * sq.steps;
     const int64_t i0 = s0 / share, i1 = (s0 + sq.steps - 1) / share;
     if (i0 == i1) return;
-    const float* first = a.parts + (2 * i0 + 1) * part_floats(ROWS, D);
-    const float* others = a.parts + 2 * (i0 + 1) * part_floats(ROWS, D);
-    const int more = static_cast<int>(i1 - i0);
-    auto part = [&](int i) { return i == 0 ? first : others + 2 * int64_t(i - 1) * part_floats(ROWS, D); };
-    for (int n = warp; n < ROWS && tile * ROWS + n < sq.rows; n += kAtWarps) {
+    const int parts = static_cast<int>(i1 - i0) + 1;
+    // Part 0 is the second of its block's two, the others the first of theirs.
+    auto part = [&](int i) { return a.parts + (2 * (i0 + i) + (i == 0 ? 1 : 0)) * part_floats(ROWS, D); };
+    for (int n = warp; n < ROWS && tile * ROWS + n < sq.rows; n += kAtJoinThreads / 32) {
         float top = kAtNone;
-        for (int i = lane; i <= more; i += 32) top = fmaxf(top, part(i)[ROWS * D + n]);
+        for (int i = lane; i < parts; i += 32) top = fmaxf(top, part(i)[ROWS * D + n]);
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
         float acc[D / 32], sum = 0.0f;
 #pragma unroll
-        for (int i = 0; i < D / 32; ++i) acc[i] = 0.0f;
-#pragma unroll 4
-        for (int i = 0; i <= more; ++i) {
-            const float* p = part(i);
-            const float f = exp2_approx(p[ROWS * D + n] - top);
-            sum += f * p[ROWS * D + ROWS + n];
-#pragma unroll
-            for (int j = 0; j < D / 32; ++j) acc[j] += f * p[n * D + lane + 32 * j];
+        for (int j = 0; j < D / 32; ++j) acc[j] = 0.0f;
+        for (int i = 0; i < parts; i += 32) {
+            // Lane l: the factor and l of part i + l.
+            const bool have = i + lane < parts;
+            const float f = have ? exp2_approx(part(i + lane)[ROWS * D + n] - top) : 0.0f;
+            const float ls = have ? part(i + lane)[ROWS * D + ROWS + n] : 0.0f;
+            const int here = min(parts - i, 32);
+#pragma unroll 16
+            for (int k = 0; k < here; ++k) {
+                const float fk = __shfl_sync(0xFFFFFFFFu, f, k);
+                const float* p = part(i + k) + n * D + lane * (D / 32);
+                sum += fk * __shfl_sync(0xFFFFFFFFu, ls, k);
+                if constexpr (D == 128) {
+                    const float4 v = *reinterpret_cast<const float4*>(p);
+                    acc[0] += fk * v.x, acc[1] += fk * v.y, acc[2] += fk * v.z, acc[3] += fk * v.w;
+                } else {
+                    const float2 v = *reinterpret_cast<const float2*>(p);
+                    acc[0] += fk * v.x, acc[1] += fk * v.y;
+                }
+            }
         }
         const int r = tile * ROWS + n, tok = a.group.div(r), head = h * a.G + (r - tok * a.G);
         const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
-        __nv_bfloat16* dst = a.out + (sq.first + tok) * a.ldo_t + head * a.ldo_h;
+        __nv_bfloat16* dst = a.out + (sq.first + tok) * a.ldo_t + head * a.ldo_h + lane * (D / 32);
 #pragma unroll
-        for (int i = 0; i < D / 32; ++i) dst[lane + 32 * i] = __float2bfloat16_rn(acc[i] * inv);
+        for (int j = 0; j < D / 32; ++j) dst[j] = __float2bfloat16_rn(acc[j] * inv);
         if (a.lse && lane == 0)
             a.lse[static_cast<int64_t>(sq.first + tok) * a.Hq + head] = sum == 0.0f ? -INFINITY : (top + log2f(sum)) * 0.693147180559945f;
     }

@@ -172,10 +172,12 @@ __device__ __forceinline__ int sequence_of_row(const CacheView& c, int row) {
     return n - 1;
 }
 
-// One warp: one row of queries, all its heads. Rows that no sequence holds are left alone.
+// One block: one row of queries. A thread keeps the angles of its piece (eight pairs, or eight features that are copied) over
+// the heads that it walks, two on their way at a time. Rows that no sequence holds are left alone.
+template <int THREADS>
 __device__ __forceinline__ void rotate_queries(const AppendArgs& a, int row) {
     const CacheView& c = a.c;
-    const int b = sequence_of_row(c, row);
+    const int b = sequence_of_row(c, row);                // the same in every warp
     if (b < 0) return;
     int first, n;
     rows_of(c, b, first, n);
@@ -184,18 +186,56 @@ __device__ __forceinline__ void rotate_queries(const AppendArgs& a, int row) {
     bool bad;
     const float* angles = angles_of(a, pos, bad);
     bad |= pos < 0;
-    const int lanes = a.D / 8;
-    for (int i = threadIdx.x & 31; i < a.Hq * lanes; i += 32) {
-        const int h = i / lanes, d = (i - h * lanes) * 8;
-        float y[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-        if (!bad) rotated8(a.q + row * a.ldq_t + h * a.ldq_h, d, angles, angles ? a.rot : 0, a.interleaved, y);
-        uint32_t o[4];
+    const int rot = angles ? a.rot : 0, half = a.rot / 2;
+    const int pairs = a.interleaved ? rot / 8 : rot / 16;  // pieces that are rotated; the others are copied
+    const int lanes = pairs + (a.D - rot) / 8;
+    const int slots = THREADS / lanes, slot = threadIdx.x / lanes, piece = threadIdx.x - slot * lanes;
+    if (slot >= slots) return;
+    const __nv_bfloat16* x = a.q + row * a.ldq_t;
+    __nv_bfloat16* y = a.q_out + row * a.ldo_t;
+    const bool turn = piece < pairs, two = turn && !a.interleaved;
+    const int d0 = turn ? piece * 8 : rot + (piece - pairs) * 8;
+    float cs[8], sn[8];
+    if (turn && two) {
+        load_angles<8>(angles + d0, cs);
+        load_angles<8>(angles + half + d0, sn);
+    } else if (turn) {
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const __nv_bfloat162 p = __floats2bfloat162_rn(y[2 * j], y[2 * j + 1]);
-            o[j] = *reinterpret_cast<const uint32_t*>(&p);
+        for (int i = 0; i < 4; ++i) cs[i] = angles[d0 / 2 + i], sn[i] = angles[half + d0 / 2 + i];
+    }
+    for (int h0 = slot; h0 < a.Hq; h0 += 2 * slots) {
+        Piece<__nv_bfloat16, 8> u[2], w[2];
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            const int h = h0 + j * slots;
+            u[j].w = w[j].w = make_uint4(0, 0, 0, 0);
+            if (h < a.Hq && !bad) {
+                u[j].load(x + h * a.ldq_h + d0);
+                if (two) w[j].load(x + h * a.ldq_h + half + d0);
+            }
         }
-        *reinterpret_cast<uint4*>(a.q_out + row * a.ldo_t + h * a.ldo_h + d) = make_uint4(o[0], o[1], o[2], o[3]);
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            const int h = h0 + j * slots;
+            if (h >= a.Hq) break;
+            if (two) {
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const float p = to_f32(u[j].e[i]), q = to_f32(w[j].e[i]);
+                    u[j].e[i] = from_f32<__nv_bfloat16>(diff_of_products(p, cs[i], q, sn[i]));
+                    w[j].e[i] = from_f32<__nv_bfloat16>(diff_of_products(q, cs[i], -p, sn[i]));
+                }
+                w[j].store(y + h * a.ldo_h + half + d0);
+            } else if (turn) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const float p = to_f32(u[j].e[2 * i]), q = to_f32(u[j].e[2 * i + 1]);
+                    u[j].e[2 * i] = from_f32<__nv_bfloat16>(diff_of_products(p, cs[i], q, sn[i]));
+                    u[j].e[2 * i + 1] = from_f32<__nv_bfloat16>(diff_of_products(q, cs[i], -p, sn[i]));
+                }
+            }
+            u[j].store(y + h * a.ldo_h + d0);
+        }
     }
 }
 
@@ -219,8 +259,7 @@ __global__ void __launch_bounds__(kAppendOneThreads) append_one_kernel(const __g
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const CacheView& c = a.c;
     if (static_cast<int>(blockIdx.x) >= a.kv_blocks) {
-        const int row = (blockIdx.x - a.kv_blocks) * (kAppendOneThreads / 32) + warp;
-        if (row < c.T) rotate_queries(a, row);
+        rotate_queries<kAppendOneThreads>(a, blockIdx.x - a.kv_blocks);
         return;
     }
     const uint32_t item = blockIdx.x * (kAppendOneThreads / 32) + warp;
@@ -274,8 +313,7 @@ __global__ void __launch_bounds__(THREADS) append_kernel(const __grid_constant__
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const CacheView& c = a.c;
     if (static_cast<int>(blockIdx.x) >= a.kv_blocks) {
-        const int row = (blockIdx.x - a.kv_blocks) * (THREADS / 32) + warp;
-        if (row < c.T) rotate_queries(a, row);
+        rotate_queries<THREADS>(a, blockIdx.x - a.kv_blocks);
         return;
     }
     const int item = a.heads2.div(blockIdx.x), r = blockIdx.x - item * a.heads2.d, h = r >> 1;

@@ -1627,7 +1627,7 @@ CacheView view_of(const mx_cache_batch* c) {
 template <int D, int CH, int THREADS>
 mx_status launch_append(AppendArgs& a, mx_stream stream) {
     const int64_t items = (a.c.T >> a.c.page_shift) + 2 * int64_t(a.c.B), blocks = items * 2 * a.c.Hkv;
-    const int64_t queries = a.q ? ceil_div(a.c.T, THREADS / 32) : 0;
+    const int64_t queries = a.q ? a.c.T : 0;
     if (blocks + queries >= kInt32End) return MX_ERR_SHAPE;
     a.kv_blocks = static_cast<int>(blocks);
     return launch_behind(append_kernel<D, CH, THREADS>, blocks + queries, THREADS, 0, 1, stream, a);
@@ -1637,8 +1637,8 @@ template <int D>
 mx_status launch_append_dim(AppendArgs& a, mx_stream stream) {
     if (!a.c.row_offsets) {
         const int64_t items = int64_t(a.c.B) * 2 * a.c.Hkv, per = kAppendOneThreads / 32;
-        const int64_t blocks = ceil_div(items, per), queries = a.q ? ceil_div(a.c.T, per) : 0;
-        if (items + queries * per >= kInt32End - per) return MX_ERR_SHAPE;
+        const int64_t blocks = ceil_div(items, per), queries = a.q ? a.c.T : 0;
+        if (items + queries >= kInt32End - per) return MX_ERR_SHAPE;
         a.kv_blocks = static_cast<int>(blocks);
         return launch_behind(append_one_kernel<D>, blocks + queries, kAppendOneThreads, 0, 1, stream, a);
     }
@@ -1651,8 +1651,8 @@ mx_status launch_append_dim(AppendArgs& a, mx_stream stream) {
     return launch_append<128, 8, 256>(a, stream);
 }
 
-// Blocks of attend_few_kernel, two an SM; also what sizes the workspace.
-constexpr int64_t kAtMaxBlocks = 320;
+// Blocks of attend_few_kernel at most; also what sizes the workspace.
+constexpr int64_t kAtMaxBlocks = 480;
 constexpr int kAtMinSteps = 4;
 
 template <class K>
@@ -1677,11 +1677,11 @@ mx_status launch_attend_few(AttendArgs& a, int64_t most_rows, const DeviceInfo* 
     // No more blocks than steps there can be.
     const int64_t keys = int64_t(a.c.width) << a.c.page_shift;
     const double bound = double(a.c.B) * a.c.Hkv * double(tiles) * double(keys / kAtStep + 2);
-    a.blocks = static_cast<int>(std::min<double>(std::min<int64_t>(2 * d->sms, kAtMaxBlocks), bound));
+    a.blocks = static_cast<int>(std::min<double>(std::min<int64_t>(AtSmem<D, NT>::kBlocks * d->sms, kAtMaxBlocks), bound));
     if (mx_status st = launch_behind(attend_few_kernel<D, NT>, a.blocks, kAtThreads, smem, 1, stream, a)) return st;
     const int64_t joins = tiles * a.c.Hkv * a.c.B;
     if (joins >= kInt32End) return MX_ERR_SHAPE;
-    return launch_behind(attend_join_kernel<D, NT>, joins, kAtThreads, 0, 1, stream, a, static_cast<int>(tiles));
+    return launch_behind(attend_join_kernel<D, NT>, joins, kAtJoinThreads, 0, 1, stream, a, static_cast<int>(tiles));
 }
 
 template <int D>
