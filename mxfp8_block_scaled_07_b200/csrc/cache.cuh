@@ -116,7 +116,7 @@ struct AppendArgs {
     int64_t positions;
     uint32_t* err;
     int Hq, D, rot, interleaved;
-    int kv_blocks;                // blocks that append; the ones behind them rotate queries
+    int kv_blocks;                // append_one_kernel: blocks that append; the ones behind them rotate queries
     FastDiv heads2;               // 2 * Hkv
 };
 
@@ -161,35 +161,45 @@ __device__ __forceinline__ const float* angles_of(const AppendArgs& a, int64_t p
     return a.table && !bad ? a.table + pos * a.rot : nullptr;
 }
 
-// Sequence of a row: how many sequences begin at or before it, by a whole warp (offsets do not decrease).
-__device__ __forceinline__ int sequence_of_row(const CacheView& c, int row) {
-    if (!c.row_offsets) return row;
-    int n = 0;
+// A sequence with its rows [first, first + n) and its length.
+struct Found {
+    int b, first, n;
+    int64_t len;
+};
+// The last sequence whose key(first row, number) is at most `x` (keys rise with the sequence), by a whole warp; b < 0: none. A lane
+// per sequence, with all that is asked of it loaded at once: the search costs one round trip for every 32 sequences.
+template <class Key>
+__device__ __forceinline__ Found find_sequence(const CacheView& c, int x, Key key) {
+    Found f{-1, 0, 0, 0};
     for (int b0 = 0; b0 < c.B; b0 += 32) {
-        const int b = b0 + (threadIdx.x & 31);
-        n += __popc(__ballot_sync(0xFFFFFFFFu, b < c.B && c.row_offsets[min(b, c.B)] <= row));
+        const int b = min(b0 + static_cast<int>(threadIdx.x & 31), c.B - 1);
+        int first, n;
+        rows_of(c, b, first, n);
+        const int len = c.lengths[b];
+        const int at = __popc(__ballot_sync(0xFFFFFFFFu, b0 + static_cast<int>(threadIdx.x & 31) < c.B && key(first, b) <= x)) - 1;
+        if (at < 0) break;
+        f = {b0 + at, __shfl_sync(0xFFFFFFFFu, first, at), __shfl_sync(0xFFFFFFFFu, n, at), __shfl_sync(0xFFFFFFFFu, len, at)};
+        if (at < 31) break;
     }
-    return n - 1;
+    return f;
 }
 
-// One block: one row of queries. A thread keeps the angles of its piece (eight pairs, or eight features that are copied) over
-// the heads that it walks, two on their way at a time. Rows that no sequence holds are left alone.
-template <int THREADS>
-__device__ __forceinline__ void rotate_queries(const AppendArgs& a, int row) {
+// One row of queries by THREADS threads (`tid` of them; whole warps). A thread keeps the angles of its piece (eight pairs, or
+// eight features that are copied) over the heads that it walks, HC of them on their way at a time. Rows that no sequence
+// holds are left alone.
+template <int THREADS, int HC>
+__device__ __forceinline__ void rotate_queries(const AppendArgs& a, int row, int tid) {
     const CacheView& c = a.c;
-    const int b = sequence_of_row(c, row);                // the same in every warp
-    if (b < 0) return;
-    int first, n;
-    rows_of(c, b, first, n);
-    if (row < first || row >= first + n) return;
-    const int64_t pos = static_cast<int64_t>(c.lengths[b]) - n + (row - first);
+    const Found q = c.row_offsets ? find_sequence(c, row, [](int first, int) { return first; }) : Found{row, row, 1, c.lengths[row]};
+    if (q.b < 0 || row < q.first || row >= q.first + q.n) return;
+    const int64_t pos = q.len - q.n + (row - q.first);
     bool bad;
     const float* angles = angles_of(a, pos, bad);
     bad |= pos < 0;
     const int rot = angles ? a.rot : 0, half = a.rot / 2;
     const int pairs = a.interleaved ? rot / 8 : rot / 16;  // pieces that are rotated; the others are copied
     const int lanes = pairs + (a.D - rot) / 8;
-    const int slots = THREADS / lanes, slot = threadIdx.x / lanes, piece = threadIdx.x - slot * lanes;
+    const int slots = THREADS / lanes, slot = tid / lanes, piece = tid - slot * lanes;
     if (slot >= slots) return;
     const __nv_bfloat16* x = a.q + row * a.ldq_t;
     __nv_bfloat16* y = a.q_out + row * a.ldo_t;
@@ -203,10 +213,10 @@ __device__ __forceinline__ void rotate_queries(const AppendArgs& a, int row) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) cs[i] = angles[d0 / 2 + i], sn[i] = angles[half + d0 / 2 + i];
     }
-    for (int h0 = slot; h0 < a.Hq; h0 += 2 * slots) {
-        Piece<__nv_bfloat16, 8> u[2], w[2];
+    for (int h0 = slot; h0 < a.Hq; h0 += HC * slots) {
+        Piece<__nv_bfloat16, 8> u[HC], w[HC];
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
+        for (int j = 0; j < HC; ++j) {
             const int h = h0 + j * slots;
             u[j].w = w[j].w = make_uint4(0, 0, 0, 0);
             if (h < a.Hq && !bad) {
@@ -215,7 +225,7 @@ __device__ __forceinline__ void rotate_queries(const AppendArgs& a, int row) {
             }
         }
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
+        for (int j = 0; j < HC; ++j) {
             const int h = h0 + j * slots;
             if (h >= a.Hq) break;
             if (two) {
@@ -259,7 +269,7 @@ __global__ void __launch_bounds__(kAppendOneThreads) append_one_kernel(const __g
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const CacheView& c = a.c;
     if (static_cast<int>(blockIdx.x) >= a.kv_blocks) {
-        rotate_queries<kAppendOneThreads>(a, blockIdx.x - a.kv_blocks);
+        rotate_queries<kAppendOneThreads, 2>(a, blockIdx.x - a.kv_blocks, threadIdx.x);
         return;
     }
     const uint32_t item = blockIdx.x * (kAppendOneThreads / 32) + warp;
@@ -302,46 +312,40 @@ __global__ void __launch_bounds__(kAppendOneThreads) append_one_kernel(const __g
     if (lane == 0) *scale = static_cast<uint8_t>(s);
 }
 
+// The queries of prompts: a warp per row. A kernel of its own, since it needs half the registers of the one below and lives
+// on many rows on their way (together, with a block per row, 10 200 tokens of 32 + 8 heads took 107 us).
+constexpr int kAppendQueryThreads = 256;
+__global__ void __launch_bounds__(kAppendQueryThreads) append_queries_kernel(const __grid_constant__ AppendArgs a) {
+    grid_wait();
+    const int row = blockIdx.x * (kAppendQueryThreads / 32) + (threadIdx.x >> 5);
+    if (row < a.c.T) rotate_queries<32, 4>(a, row, threadIdx.x & 31);
+}
+
 // Any number of new tokens per sequence: a block per (page of a sequence, head, keys or values), CH pieces of eight
-// elements per thread (page x D = 8 CH threads). Blocks are numbered without a prefix sum: sequence b's pages start at
+// elements per thread (page x D = 8 CH threads). What bounds it is the chain of loads from the offsets to the keys: two pieces a thread
+// leave most warps on their way (eight a thread took 60 us for 10 200 tokens of 8 heads, and a cheaper rotation with the
+// exact one only where a code is in doubt 84, since it needs more registers). Blocks are numbered without a prefix sum: sequence b's pages start at
 // floor(row_offsets[b] / page) + 2 b, which leaves room for all that its tokens can touch (n tokens touch at most n / page +
 // 2 pages); blocks for which nothing is left return.
 template <int D, int CH, int THREADS>
-__global__ void __launch_bounds__(THREADS) append_kernel(const __grid_constant__ AppendArgs a) {
+__global__ void __launch_bounds__(THREADS, THREADS == 1024 ? 1 : 1536 / THREADS) append_kernel(const __grid_constant__ AppendArgs a) {
     grid_wait();
     __shared__ uint32_t warp_max[THREADS / 32];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const CacheView& c = a.c;
-    if (static_cast<int>(blockIdx.x) >= a.kv_blocks) {
-        rotate_queries<THREADS>(a, blockIdx.x - a.kv_blocks);
-        return;
-    }
     const int item = a.heads2.div(blockIdx.x), r = blockIdx.x - item * a.heads2.d, h = r >> 1;
     const bool keys = !(r & 1);
     const int ps = c.page_shift, page = 1 << ps;
-    int count = 0;
-    for (int b0 = 0; b0 < c.B; b0 += 32) {
-        const int b = b0 + lane;
-        count += __popc(__ballot_sync(0xFFFFFFFFu, b < c.B && (min(max(c.row_offsets[min(b, c.B)], 0), c.T) >> ps) + 2 * b <= item));
-    }
-    const int b = count - 1;
-    if (b < 0) return;
-    int first, n;
-    rows_of(c, b, first, n);
-    const int64_t len = c.lengths[b], start = len - n;
-    const int nth = item - ((first >> ps) + 2 * b);
+    const Found q = find_sequence(c, item, [&](int first, int b) { return (first >> ps) + 2 * b; });
+    if (q.b < 0) return;
+    const int first = q.first, n = q.n;
+    const int64_t len = q.len, start = len - n;
+    const int nth = item - ((first >> ps) + 2 * q.b);
     const int64_t index = (max(start, int64_t(0)) >> ps) + nth;
     const int64_t base = index << ps;            // position of the page's first token
     if (n <= 0 || nth < 0 || base >= len) return;
     const int lo = static_cast<int>(max(start - base, int64_t(0))), hi = static_cast<int>(min(len - base, int64_t(page)));
-    const int64_t id = page_id(c, b, index);
-    if (id < 0) {
-        if (threadIdx.x == 0) atomicOr(a.err, kErrBadIndex);
-        return;
-    }
-    uint8_t* codes = (keys ? c.k + id * c.k_page : c.v + id * c.v_page) + (static_cast<int64_t>(h) << ps) * D;
-    uint8_t* scale = (keys ? c.ks + id * c.ks_page : c.vs + id * c.vs_page) + h;
-    const uint32_t was = lo ? *scale : 0u;
+    const int64_t id = page_id(c, q.b, index);   // on its way with the tokens
     float y[CH][8];
     uint32_t m = 0;
 #pragma unroll
@@ -361,6 +365,13 @@ __global__ void __launch_bounds__(THREADS) append_kernel(const __grid_constant__
         }
         m = max(m, amax_bits8(y[i]));
     }
+    if (id < 0) {                                    // the same in the whole block
+        if (threadIdx.x == 0) atomicOr(a.err, kErrBadIndex);
+        return;
+    }
+    uint8_t* codes = (keys ? c.k + id * c.k_page : c.v + id * c.v_page) + (static_cast<int64_t>(h) << ps) * D;
+    uint8_t* scale = (keys ? c.ks + id * c.ks_page : c.vs + id * c.vs_page) + h;
+    const uint32_t was = lo ? *scale : 0u;           // before the barrier, behind which it is written
     m = __reduce_max_sync(0xFFFFFFFFu, m);
     if (lane == 0) warp_max[warp] = m;
     __syncthreads();

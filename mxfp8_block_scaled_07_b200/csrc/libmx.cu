@@ -1627,10 +1627,10 @@ CacheView view_of(const mx_cache_batch* c) {
 template <int D, int CH, int THREADS>
 mx_status launch_append(AppendArgs& a, mx_stream stream) {
     const int64_t items = (a.c.T >> a.c.page_shift) + 2 * int64_t(a.c.B), blocks = items * 2 * a.c.Hkv;
-    const int64_t queries = a.q ? a.c.T : 0;
-    if (blocks + queries >= kInt32End) return MX_ERR_SHAPE;
-    a.kv_blocks = static_cast<int>(blocks);
-    return launch_behind(append_kernel<D, CH, THREADS>, blocks + queries, THREADS, 0, 1, stream, a);
+    if (blocks >= kInt32End) return MX_ERR_SHAPE;
+    if (a.q)
+        if (mx_status st = launch_behind(append_queries_kernel, ceil_div(a.c.T, kAppendQueryThreads / 32), kAppendQueryThreads, 0, 1, stream, a)) return st;
+    return launch_behind(append_kernel<D, CH, THREADS>, blocks, THREADS, 0, 1, stream, a);
 }
 
 template <int D>
@@ -1643,17 +1643,17 @@ mx_status launch_append_dim(AppendArgs& a, mx_stream stream) {
         return launch_behind(append_one_kernel<D>, blocks + queries, kAppendOneThreads, 0, 1, stream, a);
     }
     switch ((D << a.c.page_shift) / 1024) {
-        case 1: return launch_append<D, 1, 128>(a, stream);
+        case 1: return launch_append<D, 2, 64>(a, stream);
         case 2: return launch_append<D, 2, 128>(a, stream);
-        case 4: return launch_append<D, 4, 128>(a, stream);
-        case 8: return launch_append<D, 8, 128>(a, stream);
+        case 4: return launch_append<D, 2, 256>(a, stream);
+        case 8: return launch_append<D, 2, 512>(a, stream);
     }
-    return launch_append<128, 8, 256>(a, stream);
+    return launch_append<128, 2, 1024>(a, stream);
 }
 
 // Blocks of attend_few_kernel at most; also what sizes the workspace.
 constexpr int64_t kAtMaxBlocks = 480;
-constexpr int kAtMinSteps = 4;
+constexpr int kAtMinSteps = 2;
 
 template <class K>
 bool opt_in_smem(std::atomic<bool>* done, K kernel, int bytes) {

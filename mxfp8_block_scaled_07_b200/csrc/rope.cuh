@@ -150,16 +150,26 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const __grid_constan
     if (p >= a.positions) atomicOr(a.err, kErrBadIndex);
     if (piece >= a.pair_lanes) {                   // features that are not rotated
         const int d = a.rot + (piece - a.pair_lanes) * V;
-        for (int h = chunk; h < a.H; h += step) {
-            if (d + V <= a.D) {
-                Piece<T, V> v;
-                v.load(x + h * a.ldx_h + d);
-                if (!known)
+        const bool whole = d + V <= a.D;
+        for (int h0 = chunk; h0 < a.H; h0 += HC * step) {
+            Piece<T, V> v[HC];
 #pragma unroll
-                    for (int i = 0; i < V; ++i) v.e[i] = from_f32<T>(0.0f);
-                v.store(y + h * a.ldy_h + d);
-            } else {
-                for (int e = d; e < a.D; ++e) y[h * a.ldy_h + e] = known ? x[h * a.ldx_h + e] : from_f32<T>(0.0f);
+            for (int j = 0; j < HC; ++j) {
+                const int h = h0 + j * step;
+                if (h < a.H && whole) v[j].load(x + h * a.ldx_h + d);
+            }
+#pragma unroll
+            for (int j = 0; j < HC; ++j) {
+                const int h = h0 + j * step;
+                if (h >= a.H) break;
+                if (whole) {
+                    if (!known)
+#pragma unroll
+                        for (int i = 0; i < V; ++i) v[j].e[i] = from_f32<T>(0.0f);
+                    v[j].store(y + h * a.ldy_h + d);
+                } else {
+                    for (int e = d; e < a.D; ++e) y[h * a.ldy_h + e] = known ? x[h * a.ldx_h + e] : from_f32<T>(0.0f);
+                }
             }
         }
         return;
