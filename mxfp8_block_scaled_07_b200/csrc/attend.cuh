@@ -55,6 +55,9 @@ struct AttendArgs {
     int blocks;                   // blocks that share the steps
     int most_rows;                // sequences with more rows (new tokens x G) are left to the kernel for many
     int min_steps;                // steps that a block takes at least
+    uint8_t* plan;                // of the kernel for many rows, written by this one's last block; null: no such sequences
+    float* many_parts;
+    int many_blocks, plan_items;  // its blocks; items that the plan has room for
 };
 
 __device__ __forceinline__ float exp2_approx(float x) {
@@ -181,6 +184,93 @@ __device__ __forceinline__ int64_t share_of(const AttendArgs& a, int64_t total) 
 // Floats of one part: O [ROWS][D], then M and l [ROWS] each.
 __host__ __device__ constexpr int64_t part_floats(int rows, int D) { return int64_t(rows) * (D + 2); }
 
+// ---- the plan of the kernel for many rows (attend_many.cuh) ------------------------------------------------------
+// Sequences with more rows than most_rows are cut into items of 256 rows. An item of every key head is a unit of work of as many
+// key tiles (128) as its rows see. The cost of all units, item by item and head by head, is shared evenly among the blocks: a
+// unit costs its tiles, and kAmUnitCost in front of them for what is done once per unit. The plan lists the items and the cost
+// in front of each.
+
+constexpr int kAmRows = 256;           // query rows of an item
+constexpr int kAmKeys = 128;           // keys per tile
+constexpr int kAmUnitCost = 3;         // in tiles: 15 000 cycles of queries, output and a first tile's start, 4600 a tile
+
+struct alignas(16) AmItem {
+    int64_t at;                        // cost of all units in front of the item
+    int32_t b, row0, rows;             // sequence; its query rows [row0, row0 + rows)
+    int32_t first, n, hi;              // the sequence's rows in the batch, its keys
+    int32_t lo;                        // first key of the item's tiles (a multiple of 16)
+    int32_t tiles[2];                  // key tiles of the first 128 rows and of the others
+    int32_t unused;
+};
+struct AmHeader {
+    int64_t total;                     // cost of all units
+    int32_t items, unused;
+};
+__device__ __forceinline__ AmHeader* plan_header(const AttendArgs& a) { return reinterpret_cast<AmHeader*>(a.plan); }
+__device__ __forceinline__ AmItem* plan_item(const AttendArgs& a, int i) { return reinterpret_cast<AmItem*>(a.plan + sizeof(AmHeader)) + i; }
+// Tiles of a unit; one at least, since rows without keys are written too.
+__device__ __forceinline__ int unit_tiles(const AmItem& w) { return max(max(w.tiles[0], w.tiles[1]), 1); }
+__device__ __forceinline__ int64_t unit_cost(const AmItem& w) { return unit_tiles(w) + kAmUnitCost; }
+
+__device__ __forceinline__ void set_rows(const AttendArgs& a, AmItem& w, int64_t row0) {
+    w.row0 = static_cast<int>(row0);
+    w.rows = static_cast<int>(min(int64_t(w.n) * a.G - row0, int64_t(kAmRows)));
+    const int64_t start = int64_t(w.hi) - w.n;                   // position of the sequence's first row
+    w.lo = static_cast<int>(min(max(start + a.group.div(w.row0) - a.window + 1, int64_t(0)), int64_t(w.hi)) & ~int64_t(15));
+#pragma unroll
+    for (int t = 0; t < 2; ++t) {
+        const int end = min(w.rows, (t + 1) * 128);              // rows of the halves 0 .. t
+        const int64_t last = end > t * 128 ? start + a.group.div(w.row0 + end - 1) : -1;
+        w.tiles[t] = last < w.lo ? 0 : static_cast<int>((last - w.lo) / kAmKeys) + 1;
+    }
+}
+
+// By one block: thread t lists the items of a stretch of consecutive sequences.
+template <int THREADS>
+__device__ __forceinline__ void write_plan(const AttendArgs& a) {
+    __shared__ int64_t warps[2][THREADS / 32];
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int per = (a.c.B + THREADS - 1) / THREADS;
+    int64_t items = 0, cost = 0;
+    auto walk = [&](bool write, int64_t at, int64_t before) {
+        AmItem w;
+        for (int b = tid * per; b < min((tid + 1) * per, a.c.B); ++b) {
+            rows_of(a.c, b, w.first, w.n);
+            const int64_t rows = int64_t(w.n) * a.G;
+            if (rows <= a.most_rows) continue;
+            w.b = b;
+            w.hi = max(a.c.lengths[b], 0);
+            for (int64_t row0 = 0; row0 < rows; row0 += kAmRows) {
+                set_rows(a, w, row0);
+                w.at = before;
+                if (write && at < a.plan_items) *plan_item(a, static_cast<int>(at)) = w;
+                ++at;
+                before += unit_cost(w) * a.c.Hkv;
+            }
+        }
+        items = at;
+        cost = before;
+    };
+    walk(false, 0, 0);
+    int64_t si = items, st = cost;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int64_t ui = __shfl_up_sync(0xFFFFFFFFu, si, o), ut = __shfl_up_sync(0xFFFFFFFFu, st, o);
+        if (lane >= o) si += ui, st += ut;
+    }
+    if (lane == 31) warps[0][warp] = si, warps[1][warp] = st;
+    __syncthreads();
+    si -= items, st -= cost;
+    for (int w = 0; w < warp; ++w) si += warps[0][w], st += warps[1][w];
+    walk(true, si, st);
+    if (tid == THREADS - 1) {
+        // More items than the batch's rows can make: offsets that name rows twice. Nothing is computed then.
+        const bool good = items <= a.plan_items;
+        *plan_header(a) = {good ? cost : 0, good ? static_cast<int32_t>(items) : 0, 0};
+        if (!good) atomicOr(a.err, kErrBadOffsets);
+    }
+}
+
 template <int D, int NT>
 struct AtSmem {
     static constexpr int kStage = 2 * 16 * D;                     // keys, then values
@@ -211,6 +301,10 @@ __global__ void __launch_bounds__(kAtThreads, NT == 1 ? 3 : 2) attend_few_kernel
     __shared__ uint16_t stage_scales[kAtWarps][kS];
     const CacheView& c = a.c;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, c4 = lane & 3;
+    if (static_cast<int>(blockIdx.x) == a.blocks) {          // there is such a block where a.plan is set
+        write_plan<kAtThreads>(a);
+        return;
+    }
     count_steps<ROWS, kAtThreads>(a, todo);
     const int64_t share = share_of(a, todo.total);
     int64_t at = blockIdx.x * share;
@@ -558,8 +652,7 @@ constexpr int kAtJoinThreads = 256;
 // Joins the parts of tiles whose steps went to several blocks: a block per (sequence, key head, tile of rows), a warp per
 // row. Parts are added in the order of their keys, 16 of them on their way at a time.
 template <int D, int NT>
-__global__ void __launch_bounds__(kAtJoinThreads) attend_join_kernel(const __grid_constant__ AttendArgs a, int tiles) {
-    grid_wait();
+__device__ __forceinline__ void join_few(const AttendArgs& a, int tiles) {
     constexpr int ROWS = 8 * NT;
     __shared__ Steps<ROWS, kAtJoinThreads> todo;
     const CacheView& c = a.c;

@@ -1,7 +1,7 @@
 // Attention over the paged E4M3 cache for many rows per sequence: prompts, and pieces of them.
 //
-// The mathematics is attend.cuh's; here the products decide: 4 D flops per row and key, on tcgen05. A block takes 256 query
-// rows of one sequence and key head (256 / G tokens) as two tiles of 128 and walks their keys in tiles of 128:
+// The mathematics is attend.cuh's; here the products decide: 4 D flops per row and key, on tcgen05. The unit of work is 256 query
+// rows of one sequence and key head (256 / G tokens), two tiles of 128, whose keys are walked in tiles of 128:
 //   S_t = Q_t K^T        tcgen05.mma kind::f16, both operands in shared memory, accumulators in TMEM
 //   P_t = 2^(S_t ...)    one thread per row, read from TMEM and written back over S_t as f16
 //   O_t += P_t V         P_t from TMEM, V from shared memory as it lies (features contiguous: an MN-major operand)
@@ -25,12 +25,11 @@
 namespace mx {
 
 constexpr int kAmThreads = 512;
-constexpr int kAmRows = 256;           // query rows per block
-constexpr int kAmKeys = 128;           // keys per tile
 constexpr int kAmRing = 2;             // stages of K and of V
 constexpr int kAmRaw = 4;              // half tiles of codes on their way to the loaders
 constexpr int kAmScales = 4;           // tiles whose page scales are kept
 constexpr uint32_t kAmCols = 512;
+constexpr int kAmMinCost = 8;          // that a block takes at least
 constexpr float kAmMost = 32768.0f;     // sum of 16 weights that sends M up: no weight passes f16's range
 constexpr int kAmScaleRow = 10;         // of a tile: 8 groups' (key factor, value exponent), then the largest and the least exponent
 constexpr int kAmNoScale = -100000;    // exponent of a value scale that says NaN
@@ -45,7 +44,7 @@ struct AmSmem {
     static constexpr int kHalf = 64 * D;
     static constexpr int kScales = kRaw + kAmRaw * kHalf;          // [kAmScales][kAmScaleRow]
     static constexpr int kBar = kScales + kAmScales * kAmScaleRow * 8;
-    static constexpr int kBars = 2 * kAmRaw + 4 * kAmRing + kAmScales + 12 + 1;
+    static constexpr int kBars = 2 * kAmRaw + 4 * kAmRing + kAmScales + 14 + 1;
     static constexpr int kMisc = kBar + kBars * 8;
     static constexpr int kBytes = kMisc + 8 + 4 * kAmScales + 1024;    // + alignment slack
 };
@@ -157,44 +156,63 @@ __device__ __forceinline__ uint32_t seen_bits(int begin, int end, int at) {
 
 // ---- the block's work ------------------------------------------------------------------------------------------
 
-struct AmWork {
-    int b, h, first, n, row0, rows;      // sequence, key head, its rows in the batch, the block's query rows
-    int64_t hi, lo;                      // keys of the sequence; first key of the block's tiles (a multiple of 16)
-    int tiles[2];                        // key tiles of either tile of rows
-};
-
-// Blocks are numbered without a prefix sum: sequence b's begin at floor(row_offsets[b] G / 256) + b, which leaves room for
-// ceil(n G / 256); blocks for which nothing is left, or whose sequence has few rows, return. The last rows of a batch, which
-// see the most keys, come first. By a whole warp.
-__device__ __forceinline__ bool many_work(const AttendArgs& a, int block, int items, AmWork& w) {
-    const CacheView& c = a.c;
-    const int item = items - 1 - block / c.Hkv;
-    w.h = block % c.Hkv;
-    int count = 0;
-    for (int b0 = 0; b0 < c.B; b0 += 32) {
-        const int b = b0 + (threadIdx.x & 31);
-        const int64_t at = b < c.B ? int64_t(min(max(c.row_offsets[b], 0), c.T)) * a.G / kAmRows + b : INT64_MAX;
-        count += __popc(__ballot_sync(0xFFFFFFFFu, at <= item));
-    }
-    w.b = count - 1;
-    if (w.b < 0) return false;
-    rows_of(c, w.b, w.first, w.n);
-    const int nth = item - static_cast<int>(int64_t(w.first) * a.G / kAmRows + w.b);
-    const int64_t row0 = int64_t(nth) * kAmRows, rows = int64_t(w.n) * a.G;
-    if (nth < 0 || rows <= a.most_rows || row0 >= rows) return false;
-    w.row0 = static_cast<int>(row0);
-    w.rows = static_cast<int>(min(rows - row0, int64_t(kAmRows)));
-    w.hi = max(c.lengths[w.b], 0);
-    const int64_t start = w.hi - w.n;    // position of the sequence's first row
-    w.lo = max(start + a.group.div(w.row0) - a.window + 1, int64_t(0)) & ~int64_t(15);
-#pragma unroll
-    for (int t = 0; t < 2; ++t) {
-        const int end = min(w.rows, (t + 1) * 128);              // rows of tiles 0 .. t
-        const int64_t last = end > t * 128 ? start + a.group.div(w.row0 + end - 1) : -1;
-        w.tiles[t] = last < w.lo ? 0 : static_cast<int>((last - w.lo) / kAmKeys) + 1;
-    }
-    return true;
+// a / b for quotients below 1024 (key heads): a 64-bit division is 70 instructions, and every role divides.
+__device__ __forceinline__ int quotient(int64_t a, int64_t b) {
+    int q = static_cast<int>(__fdividef(static_cast<float>(a), static_cast<float>(b)));
+    while (q * b > a) --q;
+    while ((q + 1) * b <= a) ++q;
+    return q;
 }
+
+// A block walks its share [x, end) of all units' cost: a piece of a unit first, whole units, a piece last. Each role walks by
+// itself. A share that ends within the cost in front of a unit's tiles leaves them all to the next block.
+struct AmWork : AmItem {
+    int h, N;                            // key head; tiles of this piece
+    int64_t from;                        // first key of the piece
+    int part[2];                         // tiles of either half of the rows within the piece
+    bool begins, whole;                  // the piece is the unit's beginning, all of it
+};
+struct AmWalk {
+    int64_t x, end;
+    int item;
+};
+__device__ __forceinline__ bool next_piece(const AttendArgs& a, AmWalk& at, AmWork& w) {
+    while (at.x < at.end) {
+        static_cast<AmItem&>(w) = *plan_item(a, at.item);
+        const int64_t cost = unit_cost(w);
+        if (at.x >= w.at + cost * a.c.Hkv) {
+            ++at.item;                   // there is one: x lies below the total
+            continue;
+        }
+        w.h = quotient(at.x - w.at, cost);
+        const int64_t s0 = w.at + w.h * cost, p1 = min(cost, at.end - s0);
+        const int j0 = static_cast<int>(max(at.x - s0 - kAmUnitCost, int64_t(0))), j1 = static_cast<int>(max(p1 - kAmUnitCost, int64_t(0)));
+        at.x = s0 + p1;
+        if (j1 <= j0) continue;
+        w.N = j1 - j0;
+        w.from = w.lo + int64_t(j0) * kAmKeys;
+#pragma unroll
+        for (int t = 0; t < 2; ++t) w.part[t] = min(max(w.tiles[t] - j0, 0), w.N);
+        w.begins = j0 == 0;
+        w.whole = w.N == unit_tiles(w);
+        return true;
+    }
+    return false;
+}
+__device__ __forceinline__ int64_t many_share(const AttendArgs& a, int64_t total) {
+    return max((total + a.many_blocks - 1) / a.many_blocks, int64_t(kAmMinCost));
+}
+// The item that holds place x of the cost, by a whole block.
+__device__ __forceinline__ int find_item(const AttendArgs& a, int items, int64_t x) {
+    int n = 0;
+    for (int i = 0; i < items; i += blockDim.x) {
+        const int k = i + static_cast<int>(threadIdx.x);
+        n += __syncthreads_count(k < items && plan_item(a, k)->at <= x);
+    }
+    return n - 1;
+}
+// Floats of a part: O [D / 4][256 rows][4], then M and l of the rows.
+__host__ __device__ constexpr int64_t many_part_floats(int D) { return int64_t(kAmRows) * (D + 2); }
 
 // Order in which tiles of keys and values are copied and converted: K 0, then K j + 1 and V j for j = 0, 1, ..., without K N.
 __device__ __forceinline__ int tile_of(int item, int N, bool& keys) {
@@ -209,7 +227,7 @@ __device__ __forceinline__ void bulk_load(void* smem_dst, const void* gsrc, uint
 }
 
 template <int D>
-__global__ void __launch_bounds__(kAmThreads, 1) attend_many_kernel(const __grid_constant__ AttendArgs a, int items) {
+__global__ void __launch_bounds__(kAmThreads, 1) attend_many_kernel(const __grid_constant__ AttendArgs a) {
     grid_wait();
     using S = AmSmem<D>;
     extern __shared__ uint8_t dyn[];
@@ -225,15 +243,23 @@ __global__ void __launch_bounds__(kAmThreads, 1) attend_many_kernel(const __grid
     uint64_t* s_full = q_full + 2;
     uint64_t* p_full = s_full + 2;
     uint64_t* o_done = p_full + 4;               // p_full, o_done: of two halves of either tile
-    uint64_t* drain = o_done + 4;
+    uint64_t* q_seen = o_done + 4;               // the products' issuer has seen q_full
+    uint64_t* drain = q_seen + 2;
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + S::kMisc);
     volatile int* abort = reinterpret_cast<volatile int*>(smem + S::kMisc + 4);
     uint32_t* bad_pages = reinterpret_cast<uint32_t*>(smem + S::kMisc + 8);      // of a tile: a bit per group of 16 keys
     float2* scales = reinterpret_cast<float2*>(smem + S::kScales);
     const CacheView& c = a.c;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    AmWork w;
-    if (!many_work(a, blockIdx.x, items, w)) return;       // the same in every warp
+    AmWalk mine;
+    {
+        const AmHeader plan = *plan_header(a);
+        const int64_t share = many_share(a, plan.total);
+        mine.x = blockIdx.x * share;
+        mine.end = min(mine.x + share, plan.total);
+        if (mine.x >= mine.end) return;
+        mine.item = find_item(a, plan.items, mine.x);
+    }
     if (threadIdx.x == 0) {
         for (int i = 0; i < kAmRaw; ++i) {
             mbar_init(&raw_full[i], 1);
@@ -248,6 +274,7 @@ __global__ void __launch_bounds__(kAmThreads, 1) attend_many_kernel(const __grid
         for (int i = 0; i < kAmScales; ++i) mbar_init(&scales_full[i], 1);
         for (int i = 0; i < 2; ++i) {
             mbar_init(&q_full[i], 4);
+            mbar_init(&q_seen[i], 1);
             mbar_init(&s_full[i], 1);
             mbar_init(&p_full[2 * i], 4);
             mbar_init(&p_full[2 * i + 1], 4);
@@ -266,7 +293,6 @@ __global__ void __launch_bounds__(kAmThreads, 1) attend_many_kernel(const __grid
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
-    const int N = max(w.tiles[0], w.tiles[1]);
 
     if (warp >= 8 && warp < 12) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
@@ -282,14 +308,17 @@ __global__ void __launch_bounds__(kAmThreads, 1) attend_many_kernel(const __grid
         bool ok = true;
         int stage = 0;
         uint32_t phase = 0;
+        int base = 0;                                        // tiles of the pieces in front
+        AmWork w{};
+        while (ok && next_piece(a, mine, w)) {
 #pragma unroll 1
-        for (int item = 0; ok && item < 2 * N; ++item) {
+          for (int item = 0; ok && item < 2 * w.N; ++item) {
             bool keys;
-            const int j = tile_of(item, N, keys), st = j % kAmRing;
+            const int in = tile_of(item, w.N, keys), j = base + in, st = j % kAmRing;
             if (j >= kAmRing) ok = mbar_wait_warp(keys ? &k_empty[st] : &v_empty[st], (j / kAmRing - 1) & 1, abort, a.err, a.timeout_ns);
             if (!ok) break;
             const uint32_t tile = smem_u32(smem) + (keys ? S::kK : S::kV) + st * S::kTile;
-            const int64_t left = w.hi - (w.lo + int64_t(j) * kAmKeys);       // keys from the tile's first on
+            const int64_t left = w.hi - (w.from + int64_t(in) * kAmKeys);       // keys from the tile's first on
 #pragma unroll 1
             for (int half = 0; half < 2; ++half) {
                 ok = mbar_wait_warp(&raw_full[stage], phase, abort, a.err, a.timeout_ns);
@@ -319,61 +348,74 @@ __global__ void __launch_bounds__(kAmThreads, 1) attend_many_kernel(const __grid
             fence_async_smem();
             __syncwarp();
             if (lane == 0) mbar_arrive(keys ? &k_full[st] : &v_full[st]);
+          }
+          base += w.N;
         }
     } else if (warp >= 12) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
         if (warp == 12) {
         // ---- products
         constexpr uint32_t idesc_s = idesc_f16(128, kAmKeys, false), idesc_o = idesc_f16(128, D, true);
-        const uint32_t base = smem_u32(smem);
-        const uint64_t q_desc = sdesc_kmajor_sw128(base + S::kQ), k_desc = sdesc_kmajor_sw128(base + S::kK), v_desc = sdesc_mnmajor_sw128(base + S::kV);
+        const uint32_t sm = smem_u32(smem);
+        const uint64_t q_desc = sdesc_kmajor_sw128(sm + S::kQ), k_desc = sdesc_kmajor_sw128(sm + S::kK), v_desc = sdesc_mnmajor_sw128(sm + S::kV);
         auto scores = [&](int t, int st) {
             tc_scores_elect<D>(tmem + t * 128, q_desc + t * (S::kTile >> 4), k_desc + st * (S::kTile >> 4), idesc_s, &s_full[t]);
         };
         bool ok = true;
-        if (N > 0) {
-            ok = mbar_wait_warp(&q_full[0], 0, abort, a.err, a.timeout_ns) && mbar_wait_warp(&q_full[1], 0, abort, a.err, a.timeout_ns) &&
-                 mbar_wait_warp(&k_full[0], 0, abort, a.err, a.timeout_ns);
-            if (ok) {
-                tc_fence_after();
-                for (int t = 0; t < 2; ++t)
-                    if (w.tiles[t] > 0) scores(t, 0);
-                tc_commit_elect(&k_empty[0]);
-            }
-        }
-#pragma unroll 1
-        for (int j = 0; ok && j < N; ++j) {
-            const int vs = j % kAmRing, kn = (j + 1) % kAmRing;
-            ok = mbar_wait_warp(&v_full[vs], (j / kAmRing) & 1, abort, a.err, a.timeout_ns);
+        int base = 0, turn = 0, seen[2] = {0, 0};            // tiles and pieces in front; tiles of either half of the rows
+        AmWork w{};
+        while (ok && next_piece(a, mine, w)) {
+            ok = mbar_wait_warp(&q_full[0], turn & 1, abort, a.err, a.timeout_ns) && mbar_wait_warp(&q_full[1], turn & 1, abort, a.err, a.timeout_ns) &&
+                 mbar_wait_warp(&k_full[base % kAmRing], (base / kAmRing) & 1, abort, a.err, a.timeout_ns);
             if (!ok) break;
-            bool have_k = false;
-#pragma unroll 1
-            for (int t = 0; t < 2; ++t) {
-                if (j < w.tiles[t]) {
-                    const uint64_t v_tile = v_desc + vs * (S::kTile >> 4);
-#pragma unroll 1
-                    for (int half = 0; ok && half < 2; ++half) {
-                        ok = mbar_wait_warp(&p_full[2 * t + half], j & 1, abort, a.err, a.timeout_ns);
-                        if (!ok) break;
-                        tc_fence_after();
-                        tc_values_elect(tmem + 256 + t * D, tmem + t * 128 + 32 * half, v_tile + 512 * half, idesc_o, j != 0 || half != 0);
-                        tc_commit_elect(&o_done[2 * t + half]);
-                    }
-                    if (!ok) break;
-                }
-                if (j + 1 < w.tiles[t]) {
-                    if (!have_k) {
-                        ok = mbar_wait_warp(&k_full[kn], ((j + 1) / kAmRing) & 1, abort, a.err, a.timeout_ns);
-                        if (!ok) break;
-                        have_k = true;
-                        tc_fence_after();
-                    }
-                    scores(t, kn);
-                }
+            tc_fence_after();
+            if (lane == 0) {
+                mbar_arrive(&q_seen[0]);
+                mbar_arrive(&q_seen[1]);
             }
-            if (!ok) break;
-            tc_commit_elect(&v_empty[vs]);
-            if (have_k) tc_commit_elect(&k_empty[kn]);
+            __syncwarp();
+#pragma unroll 1
+            for (int t = 0; t < 2; ++t)
+                if (w.part[t] > 0) scores(t, base % kAmRing);
+            tc_commit_elect(&k_empty[base % kAmRing]);
+#pragma unroll 1
+            for (int in = 0; ok && in < w.N; ++in) {
+                const int j = base + in, vs = j % kAmRing, kn = (j + 1) % kAmRing;
+                ok = mbar_wait_warp(&v_full[vs], (j / kAmRing) & 1, abort, a.err, a.timeout_ns);
+                if (!ok) break;
+                bool have_k = false;
+#pragma unroll 1
+                for (int t = 0; t < 2; ++t) {
+                    if (in < w.part[t]) {
+                        const uint64_t v_tile = v_desc + vs * (S::kTile >> 4);
+#pragma unroll 1
+                        for (int half = 0; ok && half < 2; ++half) {
+                            ok = mbar_wait_warp(&p_full[2 * t + half], (seen[t] + in) & 1, abort, a.err, a.timeout_ns);
+                            if (!ok) break;
+                            tc_fence_after();
+                            tc_values_elect(tmem + 256 + t * D, tmem + t * 128 + 32 * half, v_tile + 512 * half, idesc_o, in != 0 || half != 0);
+                            tc_commit_elect(&o_done[2 * t + half]);
+                        }
+                        if (!ok) break;
+                    }
+                    if (in + 1 < w.part[t]) {
+                        if (!have_k) {
+                            ok = mbar_wait_warp(&k_full[kn], ((j + 1) / kAmRing) & 1, abort, a.err, a.timeout_ns);
+                            if (!ok) break;
+                            have_k = true;
+                            tc_fence_after();
+                        }
+                        scores(t, kn);
+                    }
+                }
+                if (!ok) break;
+                tc_commit_elect(&v_empty[vs]);
+                if (have_k) tc_commit_elect(&k_empty[kn]);
+            }
+            base += w.N;
+            ++turn;
+            seen[0] += w.part[0];
+            seen[1] += w.part[1];
         }
         // Every product issued by this warp has completed once `drain` fires.
         tc_commit_elect(drain);
@@ -381,6 +423,7 @@ __global__ void __launch_bounds__(kAmThreads, 1) attend_many_kernel(const __grid
         __syncwarp();
         } else if (warp == 13) {
         // ---- copy: lane l < 8 copies the 16 keys of group l, half a tile (four lanes) at a time, and brings the page scales
+        AmWork w{};
         int id_next = -1;                                    // page of group `lane`, of the tile behind the last one placed
         uint32_t ks_next = 255, vs_next = 255, ks = 255, vs = 255;       // scale bytes of the tile last placed and of the one in front of it
         struct Place {
@@ -390,12 +433,12 @@ __global__ void __launch_bounds__(kAmThreads, 1) attend_many_kernel(const __grid
         };
         // Neither an id nor the scales are looked at where they are loaded: a tile later they have come.
         auto fetch_id = [&](int j) {
-            const int64_t tok = w.lo + int64_t(j) * kAmKeys + 16 * lane, index = tok >> c.page_shift;
+            const int64_t tok = w.from + int64_t(j) * kAmKeys + 16 * lane, index = tok >> c.page_shift;
             id_next = -1;
-            if (lane < 8 && j < N && tok < w.hi && index < c.width) id_next = c.table[w.b * c.ld_table + index];
+            if (lane < 8 && j < w.N && tok < w.hi && index < c.width) id_next = c.table[w.b * c.ld_table + index];
         };
         auto place = [&](int j) {                            // from id_next; then fetches the next tile's
-            const int64_t tok = w.lo + int64_t(j) * kAmKeys + 16 * lane;
+            const int64_t tok = w.from + int64_t(j) * kAmKeys + 16 * lane;
             const bool wanted = lane < 8 && tok < w.hi, good = wanted && id_next >= 0 && id_next < c.pages;
             if (wanted && !good) atomicOr(a.err, kErrBadIndex);
             const int64_t id = good ? id_next : 0;
@@ -414,18 +457,19 @@ __global__ void __launch_bounds__(kAmThreads, 1) attend_many_kernel(const __grid
             fetch_id(j + 1);
             return p;
         };
-        if (N > 0) {
+        bool ok = true;
+        int stage = 0, issued = 0, base = 0;
+        uint32_t phase = 1;
+        while (ok && next_piece(a, mine, w)) {
+            const int N = w.N;
             fetch_id(0);
             Place cur = place(0), next = cur;                // of the tile whose values come next, and of the one behind it
             if (N > 1) next = place(1);
             Place fetched = next;
-            bool ok = true;
-            int stage = 0, issued = 0;
-            uint32_t phase = 1;
 #pragma unroll 1
             for (int item = 0; ok && item < 2 * N; ++item) {
                 bool keys;
-                const int j = tile_of(item, N, keys);
+                const int j = tile_of(item, N, keys), slot = (base + j) % kAmScales;
                 const bool from_cur = !keys || j == 0;
                 const uint8_t* src = keys ? c.k + (from_cur ? cur.k : next.k) : c.v + cur.v;
                 const int bytes = from_cur ? cur.bytes : next.bytes;
@@ -441,14 +485,14 @@ __global__ void __launch_bounds__(kAmThreads, 1) attend_many_kernel(const __grid
                     // Groups behind the sequence's end take no part in the exponents' range.
                     const int e = vb == 255 ? kAmNoScale : static_cast<int>(vb) - 127;
                     const int most = __reduce_max_sync(0xFFFFFFFFu, lane < 8 ? e : kAmNoScale);
-                    const bool part = lane < 8 && w.lo + int64_t(j) * kAmKeys + 16 * lane < w.hi;
+                    const bool part = lane < 8 && w.from + int64_t(j) * kAmKeys + 16 * lane < w.hi;
                     const int least = __reduce_min_sync(0xFFFFFFFFu, part ? e : 1000);
-                    float2* row = scales + (j % kAmScales) * kAmScaleRow;
+                    float2* row = scales + slot * kAmScaleRow;
                     if (lane < 8) row[lane] = make_float2(kb == 255 ? __uint_as_float(0x7FC00000u) : scale_value(kb), __int_as_float(e));
                     if (lane == 8) row[8] = make_float2(__int_as_float(most), __int_as_float(least));
-                    if (lane == 0) bad_pages[j % kAmScales] = from_cur ? cur.bad : next.bad;
+                    if (lane == 0) bad_pages[slot] = from_cur ? cur.bad : next.bad;
                     __syncwarp();
-                    if (lane == 0) mbar_arrive(&scales_full[j % kAmScales]);
+                    if (lane == 0) mbar_arrive(&scales_full[slot]);
                 }
 #pragma unroll 1
                 for (int half = 0; half < 2; ++half) {
@@ -468,61 +512,77 @@ __global__ void __launch_bounds__(kAmThreads, 1) attend_many_kernel(const __grid
                     next = fetched;
                 }
             }
-            // No copy of this block's is left in flight when it ends.
-            for (int i = max(issued - kAmRaw, 0); i < issued; ++i) mbar_wait_drain(&raw_full[i % kAmRaw], (i / kAmRaw) & 1, a.timeout_ns);
+            base += N;
         }
+        // No copy of this block's is left in flight when it ends.
+        for (int i = max(issued - kAmRaw, 0); i < issued; ++i) mbar_wait_drain(&raw_full[i % kAmRaw], (i / kAmRaw) & 1, a.timeout_ns);
         }
     } else {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 168;");
         // ---- softmax: thread = row
         const int t = warp >> 2, row = threadIdx.x & 127;
-        const int r = w.row0 + t * 128 + row;                // query row of the sequence
-        const bool have = t * 128 + row < w.rows;
-        const int tok = have ? a.group.div(r) : 0, head = w.h * a.G + (r - tok * a.G);
-        float rowf;
-        {
+        float rowf;                                          // argument of 2^x per unit of S
+        auto bring_queries = [&](const AmWork& w) {
+            const int r = w.row0 + t * 128 + row;            // query row of the sequence
+            const bool have = t * 128 + row < w.rows;
+            const int tok = have ? a.group.div(r) : 0, head = w.h * a.G + (r - tok * a.G);
             const __nv_bfloat16* src = a.q + (w.first + tok) * a.ldq_t + head * a.ldq_h;
             uint4 x[D / 8];
             uint32_t m = 0;
 #pragma unroll
-            for (int i = 0; i < D / 8; ++i) {
-                x[i] = have ? *reinterpret_cast<const uint4*>(src + i * 8) : make_uint4(0, 0, 0, 0);
-                const uint32_t u[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+            for (int i = 0; i < D / 8; ++i) x[i] = have ? *reinterpret_cast<const uint4*>(src + i * 8) : make_uint4(0, 0, 0, 0);
+            // max of both halves of every word, signs cleared
 #pragma unroll
-                for (int k = 0; k < 4; ++k) m = max(m, max(u[k] & 0x7FFFu, (u[k] >> 16) & 0x7FFFu));
-            }
+            for (int i = 0; i < D / 8; ++i)
+                m = max_u16x2(m, max_u16x2(max_u16x2(x[i].x & 0x7FFF7FFFu, x[i].y & 0x7FFF7FFFu), max_u16x2(x[i].z & 0x7FFF7FFFu, x[i].w & 0x7FFF7FFFu)));
+            m = max(m & 0xFFFFu, m >> 16);
             const int E = static_cast<int>(m >> 7);
             const int up = E == 255 || m == 0 ? 0 : min(max(141 - E, -126), 126);      // as in attend_few_kernel
             const float mul = __uint_as_float(static_cast<uint32_t>(127 + up) << 23);
             rowf = a.scale_log2 * __uint_as_float(static_cast<uint32_t>(127 - up) << 23);
             const uint32_t dst = smem_u32(smem) + S::kQ + t * S::kTile + row * 128;
+            const uint64_t mul2 = pair(mul, mul), none = pair(-0.0f, -0.0f);
 #pragma unroll
             for (int i = 0; i < D / 8; ++i) {
                 const uint32_t u[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
                 uint32_t o[4];
 #pragma unroll
-                for (int k = 0; k < 4; ++k) o[k] = f16x2(bf16_lo(u[k]) * mul, bf16_hi(u[k]) * mul);
+                for (int k = 0; k < 4; ++k) {
+                    const float2 v = unpair(fma2(pair(bf16_lo(u[k]), bf16_hi(u[k])), mul2, none));
+                    o[k] = f16x2(v.x, v.y);
+                }
                 st_shared_v4(dst + (i >> 3) * 16384 + (((i & 7) ^ (row & 7)) << 4), o[0], o[1], o[2], o[3]);
             }
             fence_async_smem();
             __syncwarp();
             if (lane == 0) mbar_arrive(&q_full[t]);
-        }
-        // Keys [start, stop) are seen, counted from the block's first.
-        const int64_t last = have ? w.hi - w.n + tok : -1;
-        const int stop = static_cast<int>(max(last + 1 - w.lo, int64_t(0))), start = static_cast<int>(max(last - a.window + 1 - w.lo, int64_t(0)));
+        };
         const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
         const uint32_t ts = tmem + lanes + t * 128, to = tmem + lanes + 256 + t * D;
-        float M = kAtNone, l = 0.0f;
-        int E = kAmNoScale;
-        const int n = w.tiles[t];
         bool ok = true;
-        for (int j = 0; j < n; ++j) {
-            ok = mbar_wait_warp(&scales_full[j % kAmScales], (j / kAmScales) & 1, abort, a.err, a.timeout_ns) &&
-                 mbar_wait_warp(&s_full[t], j & 1, abort, a.err, a.timeout_ns);
+        int base = 0, count = 0, turn = 0;                   // tiles in front; those of this half of the rows; pieces in front
+        AmWork w{}, next{};
+        bool more = next_piece(a, mine, w);
+        if (more) bring_queries(w);
+        while (ok && more) {
+          more = next_piece(a, mine, next);                  // on its way while this one is worked on
+          const int n = w.part[t];
+          // Keys [start, stop) are seen, counted from the piece's first.
+          const int r = w.row0 + t * 128 + row;
+          const bool have = t * 128 + row < w.rows;
+          const int tok = have ? a.group.div(r) : 0, head = w.h * a.G + (r - tok * a.G);
+          const int64_t last = have ? int64_t(w.hi) - w.n + tok : -1;
+          const int stop = static_cast<int>(max(last + 1 - w.from, int64_t(0))), start = static_cast<int>(max(last - a.window + 1 - w.from, int64_t(0)));
+          float M = kAtNone, l = 0.0f;
+          int E = kAmNoScale;
+          for (int j = 0; j < n; ++j) {
+            const int slot = (base + j) % kAmScales;
+            // In this order: with the scores made, the scales' phase is this tile's and no earlier one's.
+            ok = mbar_wait_warp(&s_full[t], (count + j) & 1, abort, a.err, a.timeout_ns) &&
+                 mbar_wait_warp(&scales_full[slot], ((base + j) / kAmScales) & 1, abort, a.err, a.timeout_ns);
             if (!ok) break;
             tc_fence_after();
-            const float2* sc = scales + (j % kAmScales) * kAmScaleRow;
+            const float2* sc = scales + slot * kAmScaleRow;
             const int ev = __float_as_int(sc[8].x);              // largest value exponent of the tile
             const int end = stop - j * kAmKeys, begin = start - j * kAmKeys;     // columns [begin, end) of this row are seen
             const bool masked = __any_sync(0xFFFFFFFFu, end < kAmKeys || begin > 0);
@@ -534,7 +594,7 @@ __global__ void __launch_bounds__(kAmThreads, 1) attend_many_kernel(const __grid
             for (int half = 0; half < 2; ++half) {
                 uint32_t s[2][32];
                 float* x = reinterpret_cast<float*>(s[0]);
-                float most, sum;
+                float most = 0.0f, sum;
                 auto weights = [&]() {
                     tc_ld_32x32b_x32(ts + half * 64, s[0]);
                     tc_ld_32x32b_x32(ts + half * 64 + 32, s[1]);
@@ -574,8 +634,9 @@ __global__ void __launch_bounds__(kAmThreads, 1) attend_many_kernel(const __grid
                         sum += (r.x + r.y) * back[g];
                     }
                 };
-                weights();
-                if (__any_sync(0xFFFFFFFFu, most > kAmMost) || (half == 0 && ev > E)) {
+                const bool larger = half == 0 && ev > E;         // the same in every row; so it is at the beginning, where M is not known
+                if (!larger) weights();
+                if (larger || __any_sync(0xFFFFFFFFu, most > kAmMost)) {
                     float top = -INFINITY;
 #pragma unroll 1
                     for (int q = 0; q < 4; ++q) {
@@ -594,7 +655,7 @@ __global__ void __launch_bounds__(kAmThreads, 1) attend_many_kernel(const __grid
                     l *= f;
                     E = max(E, ev);
                     if (j + half > 0) {                          // O, once its last product is done
-                        ok = mbar_wait_warp(&o_done[2 * t + (half ^ 1)], (half ? j : j - 1) & 1, abort, a.err, a.timeout_ns);
+                        ok = mbar_wait_warp(&o_done[2 * t + (half ^ 1)], (count + (half ? j : j - 1)) & 1, abort, a.err, a.timeout_ns);
                         if (!ok) break;
                         tc_fence_after();
 #pragma unroll 1
@@ -632,39 +693,125 @@ __global__ void __launch_bounds__(kAmThreads, 1) attend_many_kernel(const __grid
             }
             if (!ok) break;
         }
-        // ---- output
-        if (ok && n > 0) ok = mbar_wait_warp(&o_done[2 * t + 1], (n - 1) & 1, abort, a.err, a.timeout_ns);
-        if (ok) {
-            tc_fence_after();
-            const float inv = l == 0.0f ? 0.0f : ldexpf(1.0f / l, E - kAtBias);
-            __nv_bfloat16* dst = a.out + (w.first + tok) * a.ldo_t + head * a.ldo_h;
+          if (!ok) break;
+          // The next piece's queries may come once this one's are no longer read: the last scores told that, and where there were none,
+          // that their barrier's phase has been seen.
+          ok = mbar_wait_warp(&q_seen[t], turn & 1, abort, a.err, a.timeout_ns);
+          if (!ok) break;
+          ++turn;
+          const int first = w.first;
+          const bool whole = w.whole;
+          float* part = a.many_parts + (2 * static_cast<int64_t>(blockIdx.x) + (w.begins ? 1 : 0)) * many_part_floats(D);
+          base += w.N;
+          count += n;
+          w = next;
+          if (more) bring_queries(w);
+          // ---- output
+          if (n > 0) {
+            ok = mbar_wait_warp(&o_done[2 * t + 1], (count - 1) & 1, abort, a.err, a.timeout_ns);
+            if (!ok) break;
+          }
+          tc_fence_after();
+          const float inv = l == 0.0f ? 0.0f : ldexpf(whole ? 1.0f / l : 1.0f, E - kAtBias);
+          __nv_bfloat16* dst = a.out + (first + tok) * a.ldo_t + head * a.ldo_h;
+#pragma unroll 1
+          for (int q = 0; q < D; q += 32) {
+            uint32_t x[32];
+            if (n > 0) {
+                tc_ld_32x32b_x32(to + q, x);
+                tc_wait_ld_regs(x);
+            }
 #pragma unroll
-            for (int q = 0; q < D / 32; ++q) {
-                uint32_t x[32];
-                if (n > 0) {
-                    tc_ld_32x32b_x32(to + q * 32, x);
-                    tc_wait_ld_regs(x);
-                }
-                if (!have) continue;
+            for (int i = 0; i < 32; ++i) x[i] = n > 0 && l != 0.0f ? __float_as_uint(__uint_as_float(x[i]) * inv) : 0u;
+            if (!whole) {
+#pragma unroll
+                for (int i = 0; i < 32; i += 4)
+                    *reinterpret_cast<uint4*>(part + ((q + i) / 4 * kAmRows + t * 128 + row) * 4) = make_uint4(x[i], x[i + 1], x[i + 2], x[i + 3]);
+            } else if (have) {
 #pragma unroll
                 for (int i = 0; i < 32; i += 8) {
                     uint32_t o[4];
 #pragma unroll
                     for (int k = 0; k < 4; ++k) {
-                        const __nv_bfloat162 v = __floats2bfloat162_rn(__uint_as_float(x[i + 2 * k]) * inv, __uint_as_float(x[i + 2 * k + 1]) * inv);
-                        o[k] = n > 0 && l != 0.0f ? *reinterpret_cast<const uint32_t*>(&v) : 0u;
+                        const __nv_bfloat162 v = __floats2bfloat162_rn(__uint_as_float(x[i + 2 * k]), __uint_as_float(x[i + 2 * k + 1]));
+                        o[k] = *reinterpret_cast<const uint32_t*>(&v);
                     }
-                    *reinterpret_cast<uint4*>(dst + q * 32 + i) = make_uint4(o[0], o[1], o[2], o[3]);
+                    *reinterpret_cast<uint4*>(dst + q + i) = make_uint4(o[0], o[1], o[2], o[3]);
                 }
             }
-            if (have && a.lse)
-                a.lse[static_cast<int64_t>(w.first + tok) * a.Hq + head] = l == 0.0f ? -INFINITY : (M + log2f(l)) * 0.693147180559945f;
+          }
+          if (!whole) {
+            part[kAmRows * D + t * 128 + row] = M;
+            part[kAmRows * D + kAmRows + t * 128 + row] = l;
+          } else if (have && a.lse) {
+            a.lse[static_cast<int64_t>(first + tok) * a.Hq + head] = l == 0.0f ? -INFINITY : (M + log2f(l)) * 0.693147180559945f;
+          }
+          tc_fence_before();
         }
-        tc_fence_before();
     }
     __syncthreads();
     tc_fence_after();
     if (warp == 12) tmem_dealloc(tmem, kAmCols);
+}
+
+// Joins the parts of units whose tiles went to several blocks (attend_many_kernel): kAmJoins blocks for every place where one block's share ends
+// and the next one's begins, each with D / kAmJoins features of the unit that is cut there, if the cut is the unit's first. A
+// thread per row; parts in the order of their keys.
+constexpr int kAmJoins = 4;
+
+template <int D>
+__device__ __forceinline__ void join_many(const AttendArgs& a, int block) {
+    const int cut = block / kAmJoins + 1, piece = block % kAmJoins, row = threadIdx.x;
+    const AmHeader plan = *plan_header(a);
+    const int64_t share = many_share(a, plan.total), x = cut * share;
+    if (x >= plan.total) return;
+    const AmItem w = *plan_item(a, find_item(a, plan.items, x));
+    const int64_t cost = unit_cost(w);
+    const int h = quotient(x - w.at, cost);
+    const int64_t s0 = w.at + h * cost;
+    if (x - s0 <= kAmUnitCost || x - share - s0 > kAmUnitCost) return;      // no tile in front of the cut, or not the first one
+    const int parts = static_cast<int>((s0 + cost - 1) / share) - cut + 2;
+    auto part = [&](int i) { return a.many_parts + (2 * int64_t(cut - 1 + i) + (i == 0 ? 1 : 0)) * many_part_floats(D); };
+    float top = kAtNone, sum = 0.0f;
+    for (int i = 0; i < parts; ++i) top = fmaxf(top, part(i)[kAmRows * D + row]);
+    for (int i = 0; i < parts; ++i) sum += exp2_approx(part(i)[kAmRows * D + row] - top) * part(i)[kAmRows * D + kAmRows + row];
+    if (row >= w.rows) return;
+    const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+    const int r = w.row0 + row, tok = a.group.div(r), head = h * a.G + (r - tok * a.G);
+    __nv_bfloat16* dst = a.out + (w.first + tok) * a.ldo_t + head * a.ldo_h;
+#pragma unroll
+    for (int c = 0; c < D / kAmJoins; c += 8) {
+        const int d = piece * (D / kAmJoins) + c;
+        float acc[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+        for (int i = 0; i < parts; ++i) {
+            const float f = exp2_approx(part(i)[kAmRows * D + row] - top);
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                const float4 v = *reinterpret_cast<const float4*>(part(i) + ((d / 4 + k) * kAmRows + row) * 4);
+                acc[4 * k] += f * v.x, acc[4 * k + 1] += f * v.y, acc[4 * k + 2] += f * v.z, acc[4 * k + 3] += f * v.w;
+            }
+        }
+        uint32_t o[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const __nv_bfloat162 v = __floats2bfloat162_rn(acc[2 * k] * inv, acc[2 * k + 1] * inv);
+            o[k] = *reinterpret_cast<const uint32_t*>(&v);
+        }
+        *reinterpret_cast<uint4*>(dst + d) = make_uint4(o[0], o[1], o[2], o[3]);
+    }
+    if (a.lse && piece == 0)
+        a.lse[static_cast<int64_t>(w.first + tok) * a.Hq + head] = sum == 0.0f ? -INFINITY : (top + log2f(sum)) * 0.693147180559945f;
+}
+
+// `few` blocks join the parts of attend_few_kernel, the others those of attend_many_kernel.
+static_assert(kAtJoinThreads == kAmRows, "a thread per row of an item");
+template <int D, int NT>
+__global__ void __launch_bounds__(kAtJoinThreads) attend_join_kernel(const __grid_constant__ AttendArgs a, int tiles, int few) {
+    grid_wait();
+    if (static_cast<int>(blockIdx.x) < few)
+        join_few<D, NT>(a, tiles);
+    else
+        join_many<D>(a, blockIdx.x - few);
 }
 
 }  // namespace mx

@@ -1668,41 +1668,53 @@ bool opt_in_smem(std::atomic<bool>* done, K kernel, int bytes) {
     return true;
 }
 
+// Rows per sequence and key head (new tokens x G) up to which a sequence of a ragged batch is left to the kernel for few.
+constexpr int64_t kAtFewRows = 32;
+constexpr int64_t kAmMaxBlocks = 160;
+
+// Items of 256 rows that sequences of more than kAtFewRows rows can make of `rows` rows.
+int64_t plan_items(int64_t rows) { return rows / kAmRows + rows / (kAtFewRows + 1) + 1; }
+
+struct AttendSpace {
+    int64_t many_parts, plan, bytes;             // offsets in the workspace; the parts of few rows begin it
+};
+// Only row_offsets can bring many rows: without them a sequence has G.
+AttendSpace attend_space(int64_t D, int64_t all_rows) {
+    AttendSpace s;
+    s.many_parts = kAtMaxBlocks * 2 * part_floats(16, static_cast<int>(D)) * 4;
+    s.plan = s.many_parts + kAmMaxBlocks * 2 * many_part_floats(static_cast<int>(D)) * 4;
+    s.bytes = s.plan + int64_t(sizeof(AmHeader)) + plan_items(all_rows) * int64_t(sizeof(AmItem));
+    return s;
+}
+
 template <int D, int NT>
-mx_status launch_attend_few(AttendArgs& a, int64_t most_rows, const DeviceInfo* d, mx_stream stream) {
-    static std::atomic<bool> opted[kMaxDevices];
+mx_status launch_attend(AttendArgs& a, int64_t few, bool many, const DeviceInfo* d, mx_stream stream) {
+    static std::atomic<bool> opted[kMaxDevices], opted_many[kMaxDevices];
     constexpr int smem = AtSmem<D, NT>::kBytes;
     if (!opt_in_smem(opted, attend_few_kernel<D, NT>, smem)) return MX_ERR_CUDA;
-    const int64_t tiles = ceil_div(most_rows, 8 * NT);
+    if (many && !opt_in_smem(opted_many, attend_many_kernel<D>, AmSmem<D>::kBytes)) return MX_ERR_CUDA;
+    const int64_t tiles = ceil_div(few, 8 * NT), joins = tiles * a.c.Hkv * a.c.B;
+    a.most_rows = static_cast<int>(few);
     // No more blocks than steps there can be.
     const int64_t keys = int64_t(a.c.width) << a.c.page_shift;
     const double bound = double(a.c.B) * a.c.Hkv * double(tiles) * double(keys / kAtStep + 2);
     a.blocks = static_cast<int>(std::min<double>(std::min<int64_t>(AtSmem<D, NT>::kBlocks * d->sms, kAtMaxBlocks), bound));
-    if (mx_status st = launch_behind(attend_few_kernel<D, NT>, a.blocks, kAtThreads, smem, 1, stream, a)) return st;
-    const int64_t joins = tiles * a.c.Hkv * a.c.B;
-    if (joins >= kInt32End) return MX_ERR_SHAPE;
-    return launch_behind(attend_join_kernel<D, NT>, joins, kAtJoinThreads, 0, 1, stream, a, static_cast<int>(tiles));
+    a.many_blocks = static_cast<int>(std::min<int64_t>(d->sms, kAmMaxBlocks));
+    const int64_t cuts = many ? int64_t(a.many_blocks - 1) * kAmJoins : 0;
+    if (joins + cuts >= kInt32End) return MX_ERR_SHAPE;
+    if (!many) a.plan = nullptr;
+    if (mx_status st = launch_behind(attend_few_kernel<D, NT>, a.blocks + (many ? 1 : 0), kAtThreads, smem, 1, stream, a)) return st;
+    if (many)
+        if (mx_status st = launch_behind(attend_many_kernel<D>, a.many_blocks, kAmThreads, AmSmem<D>::kBytes, 1, stream, a)) return st;
+    return launch_behind(attend_join_kernel<D, NT>, joins + cuts, kAtJoinThreads, 0, 1, stream, a, static_cast<int>(tiles),
+                         static_cast<int>(joins));
 }
 
 template <int D>
-mx_status launch_attend_many(AttendArgs& a, mx_stream stream) {
-    static std::atomic<bool> opted[kMaxDevices];
-    if (!opt_in_smem(opted, attend_many_kernel<D>, AmSmem<D>::kBytes)) return MX_ERR_CUDA;
-    const int64_t items = int64_t(a.c.T) * a.G / kAmRows + a.c.B, blocks = items * a.c.Hkv;
-    if (blocks >= kInt32End) return MX_ERR_SHAPE;
-    return launch_behind(attend_many_kernel<D>, blocks, kAmThreads, AmSmem<D>::kBytes, 1, stream, a, static_cast<int>(items));
-}
-
-// Rows per sequence and key head (new tokens x G) up to which a sequence of a ragged batch is left to the kernel for few.
-constexpr int64_t kAtFewRows = 32;
-
-template <int D>
-mx_status launch_attend(AttendArgs& a, const DeviceInfo* d, mx_stream stream) {
+mx_status launch_attend_rows(AttendArgs& a, const DeviceInfo* d, mx_stream stream) {
     const int64_t rows = a.c.row_offsets ? int64_t(a.c.T) * a.G : a.G;
     const int64_t few = a.c.row_offsets ? std::min(rows, kAtFewRows) : rows;
-    a.most_rows = static_cast<int>(few);
-    if (mx_status st = few <= 8 ? launch_attend_few<D, 1>(a, few, d, stream) : launch_attend_few<D, 2>(a, few, d, stream)) return st;
-    return rows > few ? launch_attend_many<D>(a, stream) : MX_OK;
+    return few <= 8 ? launch_attend<D, 1>(a, few, rows > few, d, stream) : launch_attend<D, 2>(a, few, rows > few, d, stream);
 }
 
 }  // namespace
@@ -1777,7 +1789,7 @@ mx_status mx_cache_append(const mx_cache_batch* cache, const void* k, int64_t ld
 
 int64_t mx_cache_attention_workspace_bytes(int64_t head_dim, int64_t rows, int64_t q_heads) {
     if ((head_dim != 64 && head_dim != 128) || rows < 0 || q_heads < 1) return -1;
-    return kAtMaxBlocks * 2 * part_floats(16, static_cast<int>(head_dim)) * 4;
+    return rows * q_heads < kInt32End ? attend_space(head_dim, rows * q_heads).bytes : -1;
 }
 
 mx_status mx_cache_attention(const mx_cache_batch* cache, const void* q, int64_t q_heads, int64_t ldq_t, int64_t ldq_h,
@@ -1808,7 +1820,11 @@ mx_status mx_cache_attention(const mx_cache_batch* cache, const void* q, int64_t
     a.G = static_cast<int>(q_heads / cache->heads);
     a.group = FastDiv::of(a.G);
     a.min_steps = kAtMinSteps;
-    return cache->head_dim == 128 ? launch_attend<128>(a, d, stream) : launch_attend<64>(a, d, stream);
+    const AttendSpace space = attend_space(cache->head_dim, cache->rows * q_heads);
+    a.plan = static_cast<uint8_t*>(workspace) + space.plan;
+    a.many_parts = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + space.many_parts);
+    a.plan_items = static_cast<int>(plan_items(cache->rows * a.G));
+    return cache->head_dim == 128 ? launch_attend_rows<128>(a, d, stream) : launch_attend_rows<64>(a, d, stream);
 }
 
 }  // extern "C"
