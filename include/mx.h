@@ -380,7 +380,7 @@ mx_status mx_rope_table(const double* freq, int64_t pairs, double amplitude, int
  * (fp32 [positions, rot], as mx_rope_table writes it):
  *   y_a = x_a cos - x_b sin,  y_b = x_b cos + x_a sin,
  * with (a, b) = (i, i + rot / 2), or (2 i, 2 i + 1) if interleaved != 0. Features rot .. D - 1 are copied. Each sum is formed to
- * 1.5 units in the last place of fp32 and rounded once. pos: int32 [T] (pos64 == 0) or int64 (device), or NULL: 0 .. T - 1.
+ * 1.5 units in the last place of fp32 and rounded once. pos: int32 [T] (pos64 == 0) or int64 (device), or NULL: 0 .. T - 1 (T <= positions).
  * A token with a negative position (padding) gets zeros; so does one at or behind `positions`, which also sets bit 4 of the
  * device status word. y (the same shape and type, strides ldy_t, ldy_h) may be x itself with the same strides: features from rot on
  * then stay as they are.
@@ -456,7 +456,9 @@ int64_t mx_cache_attention_workspace_bytes(int64_t head_dim, int64_t rows, int64
  * has out 0 and lse -inf. Values whose page's scale lies more than 2^60 below the largest that the row's part of the work
  * has met count as 0. Codes 0x7F and 0xFF, which mx_cache_append does not write, count as NaN, and may do so for neighbouring
  * rows that do not see them. Sums are made in a fixed order.
- * workspace: mx_cache_attention_workspace_bytes(head_dim, rows, q_heads) device bytes, 16-byte aligned, used during this call only.
+ * workspace: mx_cache_attention_workspace_bytes(head_dim, rows, q_heads) device bytes, 16-byte aligned, used during this call only (calls that
+ * may run at the same time need their own). row_offsets that name rows twice may leave rows unwritten, with bit 2 of the status word.
+ * After an expired wait a row is its value or what was there before.
  * Requirements: q_heads a multiple of heads, q_heads <= 4096, 0 < scale < inf, BF16 tensors 16-byte aligned with strides that are multiples
  * of 8, rows * q_heads < 2^31.
  */
@@ -542,7 +544,7 @@ const char* mx_status_string(mx_status status);
 
 /*
  * Reads and clears the device status word of the current device (synchronizes the device).
- * *bits receives the error bits (1: a bounded wait expired; 2: invalid grouped-GEMM row offsets; 4: a page id outside the cache, or a
+ * *bits receives the error bits (1: a bounded wait expired; 2: invalid row offsets (grouped GEMMs, attention); 4: a page id outside the cache, or a
  * position behind the rotation table).
  * Returns MX_OK when no bit was set, MX_ERR_DEVICE when some bit was set, MX_ERR_CUDA on failure.
  */

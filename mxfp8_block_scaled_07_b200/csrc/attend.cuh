@@ -202,9 +202,11 @@ struct alignas(16) AmItem {
     int32_t tiles[2];                  // key tiles of the first 128 rows and of the others
     int32_t unused;
 };
-struct AmHeader {
+constexpr int kAmMaxBlocks = 160;      // of the kernel for many rows
+struct alignas(16) AmHeader {
     int64_t total;                     // cost of all units
     int32_t items, unused;
+    int32_t done[kAmMaxBlocks];        // blocks whose parts are complete (no wait of theirs has run out)
 };
 __device__ __forceinline__ AmHeader* plan_header(const AttendArgs& a) { return reinterpret_cast<AmHeader*>(a.plan); }
 __device__ __forceinline__ AmItem* plan_item(const AttendArgs& a, int i) { return reinterpret_cast<AmItem*>(a.plan + sizeof(AmHeader)) + i; }
@@ -231,6 +233,7 @@ __device__ __forceinline__ void write_plan(const AttendArgs& a) {
     __shared__ int64_t warps[2][THREADS / 32];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int per = (a.c.B + THREADS - 1) / THREADS;
+    for (int i = tid; i < kAmMaxBlocks; i += THREADS) plan_header(a)->done[i] = 0;
     int64_t items = 0, cost = 0;
     auto walk = [&](bool write, int64_t at, int64_t before) {
         AmItem w;
@@ -266,7 +269,8 @@ __device__ __forceinline__ void write_plan(const AttendArgs& a) {
     if (tid == THREADS - 1) {
         // More items than the batch's rows can make: offsets that name rows twice. Nothing is computed then.
         const bool good = items <= a.plan_items;
-        *plan_header(a) = {good ? cost : 0, good ? static_cast<int32_t>(items) : 0, 0};
+        plan_header(a)->total = good ? cost : 0;
+        plan_header(a)->items = good ? static_cast<int32_t>(items) : 0;
         if (!good) atomicOr(a.err, kErrBadOffsets);
     }
 }
@@ -451,8 +455,8 @@ __global__ void __launch_bounds__(kAtThreads, NT == 1 ? 3 : 2) attend_few_kernel
 #pragma unroll
                     for (int i = 0; i < D / 32; ++i) {
                         const bool have = (i * 32 + lane) / (D / 16) < valid;
-                        copy16(dst + to[i % 2] + i * 512, have ? kp + i * 512 : c.k, have);
-                        copy16(dst + to[i % 2] + i * 512 + 16 * D, have ? vp + i * 512 : c.v, have);
+                        copy16(dst + to[i % 2] + i * 512, have ? static_cast<const void*>(kp + i * 512) : a.q, have);
+                        copy16(dst + to[i % 2] + i * 512 + 16 * D, have ? static_cast<const void*>(vp + i * 512) : a.q, have);
                     }
                 }
                 ++put;

@@ -253,12 +253,11 @@ __global__ void __launch_bounds__(kAmThreads, 1) attend_many_kernel(const __grid
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     AmWalk mine;
     {
-        const AmHeader plan = *plan_header(a);
-        const int64_t share = many_share(a, plan.total);
+        const int64_t total = plan_header(a)->total, share = many_share(a, total);
         mine.x = blockIdx.x * share;
-        mine.end = min(mine.x + share, plan.total);
+        mine.end = min(mine.x + share, total);
         if (mine.x >= mine.end) return;
-        mine.item = find_item(a, plan.items, mine.x);
+        mine.item = find_item(a, plan_header(a)->items, mine.x);
     }
     if (threadIdx.x == 0) {
         for (int i = 0; i < kAmRaw; ++i) {
@@ -752,6 +751,7 @@ __global__ void __launch_bounds__(kAmThreads, 1) attend_many_kernel(const __grid
     __syncthreads();
     tc_fence_after();
     if (warp == 12) tmem_dealloc(tmem, kAmCols);
+    if (threadIdx.x == 0 && !*abort) plan_header(a)->done[blockIdx.x] = 1;
 }
 
 // Joins the parts of units whose tiles went to several blocks (attend_many_kernel): kAmJoins blocks for every place where one block's share ends
@@ -762,16 +762,17 @@ constexpr int kAmJoins = 4;
 template <int D>
 __device__ __forceinline__ void join_many(const AttendArgs& a, int block) {
     const int cut = block / kAmJoins + 1, piece = block % kAmJoins, row = threadIdx.x;
-    const AmHeader plan = *plan_header(a);
-    const int64_t share = many_share(a, plan.total), x = cut * share;
-    if (x >= plan.total) return;
-    const AmItem w = *plan_item(a, find_item(a, plan.items, x));
+    const int64_t total = plan_header(a)->total, share = many_share(a, total), x = cut * share;
+    if (x >= total) return;
+    const AmItem w = *plan_item(a, find_item(a, plan_header(a)->items, x));
     const int64_t cost = unit_cost(w);
     const int h = quotient(x - w.at, cost);
     const int64_t s0 = w.at + h * cost;
     if (x - s0 <= kAmUnitCost || x - share - s0 > kAmUnitCost) return;      // no tile in front of the cut, or not the first one
     const int parts = static_cast<int>((s0 + cost - 1) / share) - cut + 2;
     auto part = [&](int i) { return a.many_parts + (2 * int64_t(cut - 1 + i) + (i == 0 ? 1 : 0)) * many_part_floats(D); };
+    for (int i = 0; i < parts; ++i)
+        if (!plan_header(a)->done[cut - 1 + i]) return;      // a wait has run out: its rows stay as they were
     float top = kAtNone, sum = 0.0f;
     for (int i = 0; i < parts; ++i) top = fmaxf(top, part(i)[kAmRows * D + row]);
     for (int i = 0; i < parts; ++i) sum += exp2_approx(part(i)[kAmRows * D + row] - top) * part(i)[kAmRows * D + kAmRows + row];

@@ -1547,6 +1547,7 @@ mx_status rope(const void* x, mx_out_dtype dtype, int64_t T, int64_t H, int64_t 
     if (H > 1 && (std::abs(ldx_h) < D || std::abs(ldy_h) < D)) return MX_ERR_SHAPE;
     if (T == 0 || H == 0) return MX_OK;
     if (!x || !y || (!table && positions > 0)) return MX_ERR_ARG;
+    if (!pos && T > positions) return MX_ERR_SHAPE;
     const int64_t esz = dtype == MX_OUT_F32 ? 4 : 2;
     if (reinterpret_cast<uintptr_t>(x) % esz || reinterpret_cast<uintptr_t>(y) % esz || !word_aligned(table) ||
         reinterpret_cast<uintptr_t>(pos) % (pos64 ? 8 : 4))
@@ -1670,7 +1671,6 @@ bool opt_in_smem(std::atomic<bool>* done, K kernel, int bytes) {
 
 // Rows per sequence and key head (new tokens x G) up to which a sequence of a ragged batch is left to the kernel for few.
 constexpr int64_t kAtFewRows = 32;
-constexpr int64_t kAmMaxBlocks = 160;
 
 // Items of 256 rows that sequences of more than kAtFewRows rows can make of `rows` rows.
 int64_t plan_items(int64_t rows) { return rows / kAmRows + rows / (kAtFewRows + 1) + 1; }
@@ -1682,7 +1682,7 @@ struct AttendSpace {
 AttendSpace attend_space(int64_t D, int64_t all_rows) {
     AttendSpace s;
     s.many_parts = kAtMaxBlocks * 2 * part_floats(16, static_cast<int>(D)) * 4;
-    s.plan = s.many_parts + kAmMaxBlocks * 2 * many_part_floats(static_cast<int>(D)) * 4;
+    s.plan = s.many_parts + int64_t(kAmMaxBlocks) * 2 * many_part_floats(static_cast<int>(D)) * 4;
     s.bytes = s.plan + int64_t(sizeof(AmHeader)) + plan_items(all_rows) * int64_t(sizeof(AmItem));
     return s;
 }

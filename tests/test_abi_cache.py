@@ -40,7 +40,7 @@ def test_rope(mx, name):
     assert r(x=None) == ARG and r(y=None) == ARG and r(tab=None) == ARG and r(dt=3) == ARG and r(dt=-1) == ARG
     assert r(T=-1) == ARG and r(H=-1) == ARG and r(D=0) == ARG and r(rot=0) == ARG and r(n=-1) == ARG
     assert r(rot=33) == SHAPE and r(rot=66) == SHAPE and r(D=1025) == SHAPE and r(D=512, lh=512, yh=512, rot=258) == SHAPE
-    assert r(T=BIG) == SHAPE and r(lh=63) == SHAPE and r(yh=-63) == SHAPE
+    assert r(T=17) == SHAPE and r(T=BIG, pos=F) == SHAPE and r(lh=63) == SHAPE and r(yh=-63) == SHAPE
     assert r(x=BYTE) == ALIGN and r(y=BYTE) == ALIGN and r(tab=BYTE) == ALIGN and r(dt=0, x=ctypes.c_void_p(A + 2)) == ALIGN
     assert r(pos=ctypes.c_void_p(A + 4), p64=1) == ALIGN and r(pos=BYTE) == ALIGN
     assert r(T=0, x=None, y=None, tab=None) == 0 and r(H=0, x=None, y=None) == 0
