@@ -302,7 +302,6 @@ __global__ void __launch_bounds__(kAtThreads, NT == 1 ? 3 : 2) attend_few_kernel
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ Steps<ROWS, kAtThreads> todo;
     __shared__ float stat[kAtWarps][3][ROWS];
-    __shared__ uint16_t stage_scales[kAtWarps][kS];
     const CacheView& c = a.c;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, c4 = lane & 3;
     if (static_cast<int>(blockIdx.x) == a.blocks) {          // there is such a block where a.plan is set
@@ -331,6 +330,87 @@ __global__ void __launch_bounds__(kAtThreads, NT == 1 ? 3 : 2) attend_few_kernel
         const int h = static_cast<int>(unit / sq.tiles), tile = static_cast<int>(unit - int64_t(h) * sq.tiles);
         const int row0 = tile * ROWS;
 
+        float o[NT][KS][4], M[NT][2], l[NT][2];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+            for (int k = 0; k < KS; ++k) o[nt][k][0] = o[nt][k][1] = o[nt][k][2] = o[nt][k][3] = 0.0f;
+            M[nt][0] = M[nt][1] = kAtNone;
+            l[nt][0] = l[nt][1] = 0.0f;
+        }
+        int E = -1000;                          // exponent of the largest value scale so far
+
+        // Pages of 32 steps, a lane each, one batch ahead: (page id, scale bytes).
+        const int steps = static_cast<int>(s1 - s0);
+        const int64_t tok0 = sq.lo + s0 * kAtStep + 16 * warp;
+        const int key0 = static_cast<int>(s0 * kAtStep) + 16 * warp;
+        int64_t next_id = -1, cur_id = -1;
+        uint32_t next_sc = 0xFFFF, cur_sc = 0xFFFF, last_sc = 0xFFFF;
+        auto fetch_ids = [&](int base) {
+            const int64_t tok = tok0 + int64_t(base + lane) * kAtStep;
+            next_id = -1;
+            if (base + lane < steps && tok < sq.hi) {
+                next_id = page_id(c, b, tok >> c.page_shift);
+                if (next_id < 0) atomicOr(a.err, kErrBadIndex);
+            }
+        };
+        auto fetch_scales = [&]() {
+            next_sc = 0xFFFFu;
+            if (next_id >= 0) next_sc = c.ks[next_id * c.ks_page + h] | static_cast<uint32_t>(c.vs[next_id * c.vs_page + h]) << 8;
+        };
+        // Where the lane's pieces of a step go, piece i at to[i % 2] + 512 i: the order of a row's pieces repeats every 8 rows.
+        uint32_t to[2];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const int row = (i * 32 + lane) / (D / 16), piece = lane % (D / 16);
+            to[i] = row * D + ring_piece<D>(row, piece) * 16 - i * 512;
+        }
+        int put = 0;                            // steps whose copies are issued
+        auto issue = [&]() {
+            if (put < steps) {
+                const int in = put & 31;
+                if (in == 0) {
+                    if (put == 0) {
+                        fetch_ids(0);
+                        fetch_scales();                // looked at with the first scores
+                    }
+                    cur_id = next_id;
+                    last_sc = cur_sc;
+                    cur_sc = next_sc;
+                    fetch_ids(put + 32);
+                }
+                if (in == 16) fetch_scales();
+                const int64_t id = __shfl_sync(0xFFFFFFFFu, cur_id, in);
+                const int stage = put % kS;
+                const int64_t tok = tok0 + int64_t(put) * kAtStep;
+                const int64_t inner = ((static_cast<int64_t>(h) << c.page_shift) + (tok & ((1 << c.page_shift) - 1))) * D + lane * 16;
+                const uint8_t* kp = c.k + (id * c.k_page + inner);
+                const uint8_t* vp = c.v + (id * c.v_page + inner);
+                const uint32_t dst = ring + stage * S::kStage;
+                if (id >= 0 && tok + 16 <= sq.hi) {
+#pragma unroll
+                    for (int i = 0; i < D / 32; ++i) {
+                        copy16(dst + to[i % 2] + i * 512, kp + i * 512);
+                        copy16(dst + to[i % 2] + i * 512 + 16 * D, vp + i * 512);
+                    }
+                } else {
+                    __syncwarp();
+                    const int valid = id < 0 ? 0 : static_cast<int>(max(min(sq.hi - tok, int64_t(16)), int64_t(0)));
+#pragma unroll
+                    for (int i = 0; i < D / 32; ++i) {
+                        const bool have = (i * 32 + lane) / (D / 16) < valid;
+                        copy16(dst + to[i % 2] + i * 512, have ? static_cast<const void*>(kp + i * 512) : a.q, have);
+                        copy16(dst + to[i % 2] + i * 512 + 16 * D, have ? static_cast<const void*>(vp + i * 512) : a.q, have);
+                    }
+                }
+                ++put;
+            }
+            copies_commit();
+        };
+#pragma unroll
+        for (int i = 0; i < kS - 1; ++i) issue();
+
+        // The first keys are on their way.
         // Queries: column n = 8 nt + g of S^T is row row0 + n. Lane (g, c4) holds the features of the pieces that
         // lane (., c4) holds of a key: pieces c4 and c4 + 4 (D = 128), or c4 (D = 64).
         uint32_t qf[NT][KS][2];
@@ -386,86 +466,6 @@ __global__ void __launch_bounds__(kAtThreads, NT == 1 ? 3 : 2) attend_few_kernel
 
         all_from = __reduce_max_sync(0xFFFFFFFFu, all_from);
         all_to = __reduce_min_sync(0xFFFFFFFFu, all_to);
-        float o[NT][KS][4], M[NT][2], l[NT][2];
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-#pragma unroll
-            for (int k = 0; k < KS; ++k) o[nt][k][0] = o[nt][k][1] = o[nt][k][2] = o[nt][k][3] = 0.0f;
-            M[nt][0] = M[nt][1] = kAtNone;
-            l[nt][0] = l[nt][1] = 0.0f;
-        }
-        int E = -1000;                          // exponent of the largest value scale so far
-
-        // Pages of 32 steps, a lane each, one batch ahead: (page id, scale bytes).
-        const int steps = static_cast<int>(s1 - s0);
-        const int64_t tok0 = sq.lo + s0 * kAtStep + 16 * warp;
-        const int key0 = static_cast<int>(s0 * kAtStep) + 16 * warp;
-        int64_t next_id = -1, cur_id = -1;
-        uint32_t next_sc = 0xFFFF, cur_sc = 0xFFFF;
-        auto fetch_ids = [&](int base) {
-            const int64_t tok = tok0 + int64_t(base + lane) * kAtStep;
-            next_id = -1;
-            if (base + lane < steps && tok < sq.hi) {
-                next_id = page_id(c, b, tok >> c.page_shift);
-                if (next_id < 0) atomicOr(a.err, kErrBadIndex);
-            }
-        };
-        auto fetch_scales = [&]() {
-            next_sc = next_id < 0 ? 0xFFFFu : c.ks[next_id * c.ks_page + h] | static_cast<uint32_t>(c.vs[next_id * c.vs_page + h]) << 8;
-        };
-        // Where the lane's pieces of a step go, piece i at to[i % 2] + 512 i: the order of a row's pieces repeats every 8 rows.
-        uint32_t to[2];
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            const int row = (i * 32 + lane) / (D / 16), piece = lane % (D / 16);
-            to[i] = row * D + ring_piece<D>(row, piece) * 16 - i * 512;
-        }
-        int put = 0;                            // steps whose copies are issued
-        auto issue = [&]() {
-            if (put < steps) {
-                const int in = put & 31;
-                if (in == 0) {
-                    if (put == 0) {
-                        fetch_ids(0);
-                        fetch_scales();
-                    }
-                    cur_id = next_id;
-                    cur_sc = next_sc;
-                    fetch_ids(put + 32);
-                }
-                if (in == 16) fetch_scales();
-                const int64_t id = __shfl_sync(0xFFFFFFFFu, cur_id, in);
-                const uint32_t sc = __shfl_sync(0xFFFFFFFFu, cur_sc, in);
-                const int stage = put % kS;
-                if (lane == 0) stage_scales[warp][stage] = static_cast<uint16_t>(sc);
-                const int64_t tok = tok0 + int64_t(put) * kAtStep;
-                const int64_t inner = ((static_cast<int64_t>(h) << c.page_shift) + (tok & ((1 << c.page_shift) - 1))) * D + lane * 16;
-                const uint8_t* kp = c.k + (id * c.k_page + inner);
-                const uint8_t* vp = c.v + (id * c.v_page + inner);
-                const uint32_t dst = ring + stage * S::kStage;
-                if (id >= 0 && tok + 16 <= sq.hi) {
-#pragma unroll
-                    for (int i = 0; i < D / 32; ++i) {
-                        copy16(dst + to[i % 2] + i * 512, kp + i * 512);
-                        copy16(dst + to[i % 2] + i * 512 + 16 * D, vp + i * 512);
-                    }
-                } else {
-                    __syncwarp();
-                    const int valid = id < 0 ? 0 : static_cast<int>(max(min(sq.hi - tok, int64_t(16)), int64_t(0)));
-#pragma unroll
-                    for (int i = 0; i < D / 32; ++i) {
-                        const bool have = (i * 32 + lane) / (D / 16) < valid;
-                        copy16(dst + to[i % 2] + i * 512, have ? static_cast<const void*>(kp + i * 512) : a.q, have);
-                        copy16(dst + to[i % 2] + i * 512 + 16 * D, have ? static_cast<const void*>(vp + i * 512) : a.q, have);
-                    }
-                }
-                ++put;
-            }
-            copies_commit();
-        };
-#pragma unroll
-        for (int i = 0; i < kS - 1; ++i) issue();
-
         for (int st = 0; st < steps; ++st) {
             copies_wait<kS - 2>();
             __syncwarp();
@@ -473,7 +473,8 @@ __global__ void __launch_bounds__(kAtThreads, NT == 1 ? 3 : 2) attend_few_kernel
             const int stage = st % kS;
             const uint8_t* kr = ring_p + stage * S::kStage;
             const uint8_t* vr = kr + 16 * D;
-            const uint32_t sc = stage_scales[warp][stage];
+            // Its scales: of the batch that copies are issued from, or of the one before it.
+            const uint32_t sc = __shfl_sync(0xFFFFFFFFu, st >> 5 == (put - 1) >> 5 ? cur_sc : last_sc, st & 31);
             const int key = key0 + st * kAtStep;       // the first of the 16, from sq.lo
 
             float s[NT][4];
