@@ -655,7 +655,7 @@ __global__ void __launch_bounds__(kAtThreads, NT == 1 ? 3 : 2) attend_few_kernel
 constexpr int kAtJoinThreads = 256;
 
 // Joins the parts of tiles whose steps went to several blocks: a block per (sequence, key head, tile of rows), a warp per
-// row. Parts are added in the order of their keys, 16 of them on their way at a time.
+// row. Parts are added in the order of their keys.
 template <int D, int NT>
 __device__ __forceinline__ void join_few(const AttendArgs& a, int tiles) {
     constexpr int ROWS = 8 * NT;
@@ -673,32 +673,41 @@ __device__ __forceinline__ void join_few(const AttendArgs& a, int tiles) {
     const int parts = static_cast<int>(i1 - i0) + 1;
     // Part 0 is the second of its block's two, the others the first of theirs.
     auto part = [&](int i) { return a.parts + (2 * (i0 + i) + (i == 0 ? 1 : 0)) * part_floats(ROWS, D); };
+    constexpr int W = D / 32;                        // features of a lane
     for (int n = warp; n < ROWS && tile * ROWS + n < sq.rows; n += kAtJoinThreads / 32) {
-        float top = kAtNone;
-        for (int i = lane; i < parts; i += 32) top = fmaxf(top, part(i)[ROWS * D + n]);
+        float acc[W], sum = 0.0f, top = kAtNone;
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
-        float acc[D / 32], sum = 0.0f;
+        for (int j = 0; j < W; ++j) acc[j] = 0.0f;
+        for (int i = 0; i < parts; i += 16) {
+            // 16 parts at a time: O, and M and l (lane l those of part i + l), all on their way at once.
+            float v[16][W];
+            const bool have = lane < 16 && i + lane < parts;
+            const float* mine = part(i + (have ? lane : 0)) + ROWS * D + n;
+            const float M = have ? mine[0] : kAtNone, ls = have ? mine[ROWS] : 0.0f;
 #pragma unroll
-        for (int j = 0; j < D / 32; ++j) acc[j] = 0.0f;
-        for (int i = 0; i < parts; i += 32) {
-            // Lane l: the factor and l of part i + l.
-            const bool have = i + lane < parts;
-            const float f = have ? exp2_approx(part(i + lane)[ROWS * D + n] - top) : 0.0f;
-            const float ls = have ? part(i + lane)[ROWS * D + ROWS + n] : 0.0f;
-            const int here = min(parts - i, 32);
-#pragma unroll 16
-            for (int k = 0; k < here; ++k) {
+            for (int k = 0; k < 16; ++k) {
+                const float* p = part(min(i + k, parts - 1)) + n * D + lane * W;
+                if constexpr (W == 4)
+                    *reinterpret_cast<float4*>(v[k]) = *reinterpret_cast<const float4*>(p);
+                else
+                    *reinterpret_cast<float2*>(v[k]) = *reinterpret_cast<const float2*>(p);
+            }
+            float next = fmaxf(top, M);
+#pragma unroll
+            for (int o = 8; o > 0; o >>= 1) next = fmaxf(next, __shfl_xor_sync(0xFFFFFFFFu, next, o));
+            next = __shfl_sync(0xFFFFFFFFu, next, 0);
+            const float back = exp2_approx(top - next), f = have ? exp2_approx(M - next) : 0.0f;
+            top = next;
+            sum *= back;
+#pragma unroll
+            for (int j = 0; j < W; ++j) acc[j] *= back;
+#pragma unroll
+            for (int k = 0; k < 16; ++k) {
+                if (i + k >= parts) break;
                 const float fk = __shfl_sync(0xFFFFFFFFu, f, k);
-                const float* p = part(i + k) + n * D + lane * (D / 32);
                 sum += fk * __shfl_sync(0xFFFFFFFFu, ls, k);
-                if constexpr (D == 128) {
-                    const float4 v = *reinterpret_cast<const float4*>(p);
-                    acc[0] += fk * v.x, acc[1] += fk * v.y, acc[2] += fk * v.z, acc[3] += fk * v.w;
-                } else {
-                    const float2 v = *reinterpret_cast<const float2*>(p);
-                    acc[0] += fk * v.x, acc[1] += fk * v.y;
-                }
+#pragma unroll
+                for (int j = 0; j < W; ++j) acc[j] += fk * v[k][j];
             }
         }
         const int r = tile * ROWS + n, tok = a.group.div(r), head = h * a.G + (r - tok * a.G);
