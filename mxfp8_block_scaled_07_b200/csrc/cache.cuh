@@ -34,11 +34,9 @@ __device__ __forceinline__ float diff_to_odd(float a, float c, float b, float s)
     float t, lo;
     const float hi0 = two_sum(p, -q, t);
     const float hi = two_sum(hi0, __fadd_rn(t, __fsub_rn(ep, eq)), lo);
-    uint32_t bits = __float_as_uint(hi);
-    if ((bits & 0x7F800000u) == 0x7F800000u || lo == 0.0f) return hi;
-    if ((bits << 1) == 0) return lo;
-    if ((__float_as_uint(lo) ^ bits) >> 31) bits -= 1;
-    return __uint_as_float(bits | 1u);
+    if (!(fabsf(lo) > 0.0f)) return hi;          // exact (so it is where hi is 0), or hi is no finite number
+    const int bits = __float_as_int(hi);
+    return __int_as_float((bits + ((__float_as_int(lo) ^ bits) >> 31)) | 1);
 }
 
 __device__ __forceinline__ float bf16_lo(uint32_t w) { return __uint_as_float(w << 16); }
