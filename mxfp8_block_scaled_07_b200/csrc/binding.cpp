@@ -446,7 +446,7 @@ PyObject* rope_call(Args a) {
     const at::Tensor out = a[4] == Py_None ? fresh({h.T, h.H, h.D}, type) : tensor(a[4], "rope: out");
     const Heads o = heads(out, "rope: out must be like x");
     need(o.T == h.T && o.H == h.H && o.D == h.D && out.scalar_type() == type && out.device() == dev, "rope: out must be like x");
-    need(o.p != h.p || (o.ld_t == h.ld_t && o.ld_h == h.ld_h), "rope: out on x's memory must be x itself");
+    need(!o.p || o.p != h.p || (o.ld_t == h.ld_t && o.ld_h == h.ld_h), "rope: out on x's memory must be x itself");
     check((BACKWARD ? mx_rope_bwd : mx_rope)(h.p, code, h.T, h.H, h.D, h.ld_t, h.ld_h, static_cast<const float*>(pt), table.size(0),
                                              table.size(1), pp, pos64, interleaved, o.p, o.ld_t, o.ld_h, place.stream),
           BACKWARD ? "mx_rope_bwd" : "mx_rope");
@@ -519,7 +519,7 @@ PyObject* cache_append(Args a) {
         out = a[9] == Py_None ? fresh({hq.T, hq.H, hq.D}, at::kBFloat16) : tensor(a[9], "cache_append: out");
         ho = heads_bf16(out, dev, what);
         need(ho.T == hq.T && ho.H == hq.H && ho.D == hq.D, what);
-        need(ho.p != hq.p || (ho.ld_t == hq.ld_t && ho.ld_h == hq.ld_h), "cache_append: out on q's memory must be q itself");
+        need(!ho.p || ho.p != hq.p || (ho.ld_t == hq.ld_t && ho.ld_h == hq.ld_h), "cache_append: out on q's memory must be q itself");
     }
     check(mx_cache_append(&c, hk.p, hk.ld_t, hk.ld_h, hv.p, hv.ld_t, hv.ld_h, static_cast<const float*>(pt), positions, rot, truth(a[8]),
                           hq.p, hq.H, hq.ld_t, hq.ld_h, ho.p, ho.ld_t, ho.ld_h, place.stream),
