@@ -237,3 +237,10 @@ def test_a_layers_steps():
         verify(out, lse, qr, [codes[0], codes[1], byte[0], byte[1]], table, lengths, offsets, D ** -0.5, 0, D)
         rows = np.ones(B, np.int64)
         lengths = lengths + 1
+
+
+@pytest.mark.parametrize("G,rows", [(1, [32, 33, 47, 48, 49, 50]), (4, [8, 9, 12, 13]), (5, [9, 10]), (12, [4, 5])])
+def test_rows_around_the_kernels_border(G, rows):
+    """Sequences whose rows per key head are just below, at and above the number that one kernel hands to the other."""
+    check([n + before for n, before in zip(rows, [0, 300, 7, 1100, 64, 2])], rows, 2, G, 128, 32, seed=G, tail=1)
+    check([n + 90 for n in rows], rows, 1, G, 64, 16, window=33, seed=G)
