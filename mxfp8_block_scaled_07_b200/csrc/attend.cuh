@@ -10,10 +10,13 @@
 // written back to shared memory.
 //
 // Types: q rows are scaled by a power of two each and become f16 (exact but for elements 2^29 below the row's largest); S, softmax
-// statistics and O are fp32; P becomes f16 under a bias of 2^7 (11 bits from 2^-21 of the largest up). A page's key scale enters
-// with the softmax's argument, its value scale P's exponent, against the largest value scale met so far (E): values whose scale
-// lies more than 2^60 below that one count as 0. The running maximum M and E are moved only when P would leave f16's range
-// (8 binades), so that O is seldom rescaled.
+// statistics and O are fp32. A page's key scale enters with the softmax's argument t, its value scale with P's exponent: P =
+// 2^(t + e - M + 7), e the exponent of the page's values and M a whole number near the largest t + e that the row sees, so that
+// P, as f16, has 11 bits from 2^-20 of the row's largest product of weight and value scale up, however far scales lie apart and
+// whatever pages it does not see hold. The sum l of the weights has a reference of its own, the largest t, kept as the distance
+// `lift` of M from it: l takes P 2^(lift - e - 7) from P in fp32, and where e lies so far below M's that P would leave fp32's
+// range, both take e to be lift - 100 (2^-93 of the row's largest: 0 as f16 in either case). M and lift are moved only when P would
+// leave f16's range (8 binades) or l grows by 2^40, so that O is seldom rescaled.
 //
 // Work is split evenly: every sequence, key head and tile of rows has its keys cut into steps of 64, and block i of n takes the
 // i-th n-th of all steps, wherever it begins and ends. Blocks that share a tile leave (O, M, l) in a workspace, which
@@ -37,10 +40,11 @@ namespace mx {
 constexpr int kAtThreads = 128;
 constexpr int kAtWarps = kAtThreads / 32;
 constexpr int kAtStep = 64;            // keys per step: 16 per warp
-constexpr int kAtBias = 7;             // P = 2^(t - M + 7)
+constexpr float kAtBias = 7.0f;        // P = 2^(t + e - M + 7)
 constexpr float kAtSlack = 8.0f;       // M lags behind the maximum by at most this
+constexpr float kAtSumSlack = 40.0f;   // weights in l reach at most 2^40
 constexpr float kAtNone = -1e30f;      // M of a row that has seen no key
-constexpr int kAtValueRange = 60;      // binades of value scales below the largest that count
+constexpr float kAtLeast = 100.0f;     // exponents of value scales below lift - 100 count as that
 
 struct AttendArgs {
     CacheView c;
@@ -67,6 +71,10 @@ __device__ __forceinline__ float exp2_approx(float x) {
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
+}
+// 2^(x - 127) of a whole number x <= 254; 0 below 1.
+__device__ __forceinline__ float pow2_biased(float x) {
+    return __int_as_float(__float_as_int(fmaxf(x, 0.0f) + 8388608.0f) << 23);      // the sum's last bits are x
 }
 __device__ __forceinline__ uint32_t f16x2(float lo, float hi) {
     const __half2 h = __floats2half2_rn(lo, hi);
@@ -184,8 +192,12 @@ __device__ __forceinline__ int64_t share_of(const AttendArgs& a, int64_t total) 
     return max((total + a.blocks - 1) / a.blocks, int64_t(a.min_steps));
 }
 
-// Floats of one part: O [ROWS][D], then M and l [ROWS] each.
-__host__ __device__ constexpr int64_t part_floats(int rows, int D) { return int64_t(rows) * (D + 2); }
+// What a quotient O / l is in units of, for M - lift = M's distance from the reference of l. (An exponent that P's own cannot have
+// stands for rows of infinities, whose quotients are NaN.)
+__device__ __forceinline__ float out_unit(float lift) { return ldexpf(1.0f, static_cast<int>(fminf(fmaxf(lift - kAtBias, -300.0f), 300.0f))); }
+
+// Floats of one part: O [ROWS][D], then M, l and lift [ROWS] each.
+__host__ __device__ constexpr int64_t part_floats(int rows, int D) { return int64_t(rows) * (D + 3); }
 
 // ---- the plan of the kernel for many rows (attend_many.cuh) ------------------------------------------------------
 // Sequences with more rows than most_rows are cut into items of 256 rows. An item of every key head is a unit of work of as many
@@ -333,15 +345,14 @@ __global__ void __launch_bounds__(kAtThreads, NT == 1 ? 3 : 2) attend_few_kernel
         const int h = static_cast<int>(unit / sq.tiles), tile = static_cast<int>(unit - int64_t(h) * sq.tiles);
         const int row0 = tile * ROWS;
 
-        float o[NT][KS][4], M[NT][2], l[NT][2];
+        float o[NT][KS][4], M[NT][2], l[NT][2], lift[NT][2];
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
             for (int k = 0; k < KS; ++k) o[nt][k][0] = o[nt][k][1] = o[nt][k][2] = o[nt][k][3] = 0.0f;
             M[nt][0] = M[nt][1] = kAtNone;
-            l[nt][0] = l[nt][1] = 0.0f;
+            l[nt][0] = l[nt][1] = lift[nt][0] = lift[nt][1] = 0.0f;
         }
-        int E = -1000;                          // exponent of the largest value scale so far
 
         // Pages of 32 steps, a lane each, one batch ahead: (page id, scale bytes).
         const int steps = static_cast<int>(s1 - s0);
@@ -499,6 +510,7 @@ __global__ void __launch_bounds__(kAtThreads, NT == 1 ? 3 : 2) attend_few_kernel
             // 2^x arguments of (token g, columns 2 c4, 2 c4 + 1), (token g + 8, the same columns).
             const uint32_t kb = sc & 0xFFu, vb = sc >> 8;
             const float kscale = kb == 255 ? __uint_as_float(0x7FC00000u) : scale_value(kb);
+            const float e = vb == 255 ? 0.0f : static_cast<float>(static_cast<int>(vb) - 127);
             bool more = false;
             const bool edge = key < all_from || key + 16 > all_to;
 #pragma unroll
@@ -517,7 +529,10 @@ __global__ void __launch_bounds__(kAtThreads, NT == 1 ? 3 : 2) attend_few_kernel
                     }
             }
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt) more |= fmaxf(s[nt][0], s[nt][2]) > M[nt][0] + kAtSlack || fmaxf(s[nt][1], s[nt][3]) > M[nt][1] + kAtSlack;
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int j = 0; j < 2; ++j)
+                    more |= fmaxf(s[nt][j], s[nt][2 + j]) > M[nt][j] + fminf(kAtSlack - e, kAtSumSlack - lift[nt][j]);
             if (__any_sync(0xFFFFFFFFu, more)) {
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt)
@@ -527,39 +542,29 @@ __global__ void __launch_bounds__(kAtThreads, NT == 1 ? 3 : 2) attend_few_kernel
                         m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, 4));
                         m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, 8));
                         m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, 16));
-                        const float to = fmaxf(M[nt][j], m), f = exp2_approx(M[nt][j] - to);
+                        const float to = fmaxf(M[nt][j], rintf(m + e)), f = exp2_approx(M[nt][j] - to);
+                        const float up = to - fmaxf(M[nt][j] - lift[nt][j], rintf(m));
+                        l[nt][j] *= exp2_approx((M[nt][j] - to) - (lift[nt][j] - up));
                         M[nt][j] = to;
-                        l[nt][j] *= f;
+                        lift[nt][j] = up;
 #pragma unroll
                         for (int k = 0; k < KS; ++k) o[nt][k][j] *= f, o[nt][k][2 + j] *= f;
                     }
             }
-            int dv = vb == 255 ? 0 : static_cast<int>(vb) - 127;
-            if (vb != 255 && dv > E) {           // a larger value scale than any before
-                const float f = exp2_approx(static_cast<float>(max(E - dv, -200)));
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                    for (int k = 0; k < KS; ++k)
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) o[nt][k][i] *= f;
-                E = dv;
-            }
-            dv -= E;
-            // Values that do not count, or that are NaN: weights of their own, l as ever.
-            const bool apart = vb == 255 || dv < -kAtValueRange;
-            const float shift = static_cast<float>(kAtBias + (apart ? 0 : dv)), back = exp2_approx(-shift);
             uint32_t pf[NT][2];
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
                 float p[4];
 #pragma unroll
-                for (int i = 0; i < 4; ++i) p[i] = exp2_approx(s[nt][i] + (shift - M[nt][i & 1]));      // 0 of -inf: M is finite
-                l[nt][0] += (p[0] + p[2]) * back;
-                l[nt][1] += (p[1] + p[3]) * back;
-                if (apart)
+                for (int j = 0; j < 2; ++j) {
+                    const float el = fmaxf(e, lift[nt][j] - kAtLeast), d = el - (M[nt][j] - kAtBias);
+                    p[j] = exp2_approx(s[nt][j] + d);                   // 0 of -inf: M is finite
+                    p[2 + j] = exp2_approx(s[nt][2 + j] + d);
+                    l[nt][j] += (p[j] + p[2 + j]) * pow2_biased(lift[nt][j] + (127.0f - kAtBias) - el);
+                }
+                if (vb == 255)                                          // values that are NaN
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) p[i] = vb == 255 && s[nt][i] != -INFINITY ? __uint_as_float(0x7FC00000u) : 0.0f;
+                    for (int i = 0; i < 4; ++i) p[i] = s[nt][i] != -INFINITY ? __uint_as_float(0x7FC00000u) : 0.0f;
                 pf[nt][0] = transposed8x8(f16x2(p[0], p[1]));
                 pf[nt][1] = transposed8x8(f16x2(p[2], p[3]));
             }
@@ -591,8 +596,8 @@ __global__ void __launch_bounds__(kAtThreads, NT == 1 ? 3 : 2) attend_few_kernel
             }
         }
 
-        // The four warps' parts, joined in shared memory: M, l and E per row, O relative to the largest M. No copy is in
-        // flight: the last groups are empty.
+        // The four warps' parts, joined in shared memory: M, l and lift per row, O relative to the largest M, l to the largest
+        // M - lift. No copy is in flight: the last groups are empty.
         copies_wait<0>();
         __syncwarp();
 #pragma unroll
@@ -607,7 +612,7 @@ __global__ void __launch_bounds__(kAtThreads, NT == 1 ? 3 : 2) attend_few_kernel
                 if (g == 0) {
                     stat[warp][0][n] = M[nt][j];
                     stat[warp][1][n] = x;
-                    stat[warp][2][n] = static_cast<float>(E);
+                    stat[warp][2][n] = lift[nt][j];
                 }
                 float* dst = reinterpret_cast<float*>(smem + warp * S::kWarp) + n * (D + 4) + g * (D / 8);
 #pragma unroll
@@ -617,36 +622,39 @@ __global__ void __launch_bounds__(kAtThreads, NT == 1 ? 3 : 2) attend_few_kernel
         const bool whole = s0 == 0 && s1 == sq.steps;
         float* part = a.parts + (2 * static_cast<int64_t>(blockIdx.x) + (s0 == 0 ? 1 : 0)) * part_floats(ROWS, D);
         for (int n = warp; n < ROWS && row0 + n < sq.rows; n += kAtWarps) {
-            float top = kAtNone, sum = 0.0f;
+            float top = kAtNone, ref = kAtNone, sum = 0.0f;
 #pragma unroll
-            for (int w = 0; w < kAtWarps; ++w) top = fmaxf(top, stat[w][0][n]);
+            for (int w = 0; w < kAtWarps; ++w) {
+                top = fmaxf(top, stat[w][0][n]);
+                ref = fmaxf(ref, stat[w][0][n] - stat[w][2][n]);
+            }
             float acc[D / 32];
 #pragma unroll
             for (int i = 0; i < D / 32; ++i) acc[i] = 0.0f;
 #pragma unroll
             for (int w = 0; w < kAtWarps; ++w) {
                 const float lw = stat[w][1][n];
-                if (lw == 0.0f) continue;        // no key seen: nothing of this warp counts (its E may be unset)
+                if (lw == 0.0f) continue;        // no key seen: nothing of this warp counts
                 const float f = exp2_approx(stat[w][0][n] - top);
-                const float fo = ldexpf(f, static_cast<int>(stat[w][2][n]) - kAtBias);
-                sum += lw * f;
+                sum += lw * exp2_approx(stat[w][0][n] - stat[w][2][n] - ref);
 #pragma unroll
-                for (int i = 0; i < D / 32; ++i) acc[i] += fo * reinterpret_cast<const float*>(smem + w * S::kWarp)[n * (D + 4) + lane + 32 * i];
+                for (int i = 0; i < D / 32; ++i) acc[i] += f * reinterpret_cast<const float*>(smem + w * S::kWarp)[n * (D + 4) + lane + 32 * i];
             }
             if (whole) {
                 const int r = row0 + n, tok = a.group.div(r), head = h * a.G + (r - tok * a.G);
-                const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+                const float inv = sum == 0.0f ? 0.0f : 1.0f / sum, unit = out_unit(top - ref);
                 __nv_bfloat16* dst = a.out + (sq.first + tok) * a.ldo_t + head * a.ldo_h;
 #pragma unroll
-                for (int i = 0; i < D / 32; ++i) dst[lane + 32 * i] = __float2bfloat16_rn(acc[i] * inv);
+                for (int i = 0; i < D / 32; ++i) dst[lane + 32 * i] = __float2bfloat16_rn(acc[i] * inv * unit);
                 if (a.lse && lane == 0)
-                    a.lse[static_cast<int64_t>(sq.first + tok) * a.Hq + head] = sum == 0.0f ? -INFINITY : (top + log2f(sum)) * 0.693147180559945f;
+                    a.lse[static_cast<int64_t>(sq.first + tok) * a.Hq + head] = sum == 0.0f ? -INFINITY : (ref + log2f(sum)) * 0.693147180559945f;
             } else {
 #pragma unroll
                 for (int i = 0; i < D / 32; ++i) part[n * D + lane + 32 * i] = acc[i];
                 if (lane == 0) {
                     part[ROWS * D + n] = top;
                     part[ROWS * D + ROWS + n] = sum;
+                    part[ROWS * D + 2 * ROWS + n] = top - ref;
                 }
             }
         }
@@ -678,15 +686,15 @@ __device__ __forceinline__ void join_few(const AttendArgs& a, int tiles) {
     auto part = [&](int i) { return a.parts + (2 * (i0 + i) + (i == 0 ? 1 : 0)) * part_floats(ROWS, D); };
     constexpr int W = D / 32;                        // features of a lane
     for (int n = warp; n < ROWS && tile * ROWS + n < sq.rows; n += kAtJoinThreads / 32) {
-        float acc[W], sum = 0.0f, top = kAtNone;
+        float acc[W], sum = 0.0f, top = kAtNone, ref = kAtNone;
 #pragma unroll
         for (int j = 0; j < W; ++j) acc[j] = 0.0f;
         for (int i = 0; i < parts; i += 16) {
-            // 16 parts at a time: O, and M and l (lane l those of part i + l), all on their way at once.
+            // 16 parts at a time: O, and M, l and lift (lane l those of part i + l), all on their way at once.
             float v[16][W];
             const bool have = lane < 16 && i + lane < parts;
             const float* mine = part(i + (have ? lane : 0)) + ROWS * D + n;
-            const float M = have ? mine[0] : kAtNone, ls = have ? mine[ROWS] : 0.0f;
+            const float M = have ? mine[0] : kAtNone, ls = have ? mine[ROWS] : 0.0f, L = M - (have ? mine[2 * ROWS] : 0.0f);
 #pragma unroll
             for (int k = 0; k < 16; ++k) {
                 const float* p = part(min(i + k, parts - 1)) + n * D + lane * W;
@@ -695,31 +703,37 @@ __device__ __forceinline__ void join_few(const AttendArgs& a, int tiles) {
                 else
                     *reinterpret_cast<float2*>(v[k]) = *reinterpret_cast<const float2*>(p);
             }
-            float next = fmaxf(top, M);
+            float next = fmaxf(top, M), base = fmaxf(ref, L);
 #pragma unroll
-            for (int o = 8; o > 0; o >>= 1) next = fmaxf(next, __shfl_xor_sync(0xFFFFFFFFu, next, o));
+            for (int o = 8; o > 0; o >>= 1) {
+                next = fmaxf(next, __shfl_xor_sync(0xFFFFFFFFu, next, o));
+                base = fmaxf(base, __shfl_xor_sync(0xFFFFFFFFu, base, o));
+            }
             next = __shfl_sync(0xFFFFFFFFu, next, 0);
+            base = __shfl_sync(0xFFFFFFFFu, base, 0);
             const float back = exp2_approx(top - next), f = have ? exp2_approx(M - next) : 0.0f;
+            const float weight = have ? ls * exp2_approx(L - base) : 0.0f;
+            sum *= exp2_approx(ref - base);
             top = next;
-            sum *= back;
+            ref = base;
 #pragma unroll
             for (int j = 0; j < W; ++j) acc[j] *= back;
 #pragma unroll
             for (int k = 0; k < 16; ++k) {
                 if (i + k >= parts) break;
                 const float fk = __shfl_sync(0xFFFFFFFFu, f, k);
-                sum += fk * __shfl_sync(0xFFFFFFFFu, ls, k);
+                sum += __shfl_sync(0xFFFFFFFFu, weight, k);
 #pragma unroll
                 for (int j = 0; j < W; ++j) acc[j] += fk * v[k][j];
             }
         }
         const int r = tile * ROWS + n, tok = a.group.div(r), head = h * a.G + (r - tok * a.G);
-        const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+        const float inv = sum == 0.0f ? 0.0f : 1.0f / sum, unit = out_unit(top - ref);
         __nv_bfloat16* dst = a.out + (sq.first + tok) * a.ldo_t + head * a.ldo_h + lane * (D / 32);
 #pragma unroll
-        for (int j = 0; j < D / 32; ++j) dst[j] = __float2bfloat16_rn(acc[j] * inv);
+        for (int j = 0; j < D / 32; ++j) dst[j] = __float2bfloat16_rn(acc[j] * inv * unit);
         if (a.lse && lane == 0)
-            a.lse[static_cast<int64_t>(sq.first + tok) * a.Hq + head] = sum == 0.0f ? -INFINITY : (top + log2f(sum)) * 0.693147180559945f;
+            a.lse[static_cast<int64_t>(sq.first + tok) * a.Hq + head] = sum == 0.0f ? -INFINITY : (ref + log2f(sum)) * 0.693147180559945f;
     }
 }
 

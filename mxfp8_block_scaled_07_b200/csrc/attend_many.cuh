@@ -8,7 +8,7 @@
 // While the softmax of one tile runs, the products of the other do. One warp copies the codes with bulk copies of 16 keys each,
 // so that pages may be of any size from 16 tokens and lie anywhere; four warps write them to the products' layout as f16 (exact, one
 // conversion for two codes). The scales stay out of the products: a page's key scale is a factor of the softmax's argument, its
-// value scale an exponent of P, both constant over 16 columns. E4M3 operands would run at twice the rate but P (and q) would need two of
+// value scale's exponent part of P's, both constant over 16 columns. E4M3 operands would run at twice the rate but P (and q) would need two of
 // them each to keep BF16's accuracy, which costs the softmax's threads more than the conversion costs the converters.
 //
 // Roles (512 threads): warps 0-3 and 4-7 softmax of tiles 0 and 1, warps 8-11 conversion, warp 12 issues the products and owns TMEM
@@ -34,8 +34,8 @@ constexpr int kAmScales = 4;           // tiles whose page scales are kept
 constexpr uint32_t kAmCols = 512;
 constexpr int kAmMinCost = 8;          // that a block takes at least
 constexpr float kAmMost = 32768.0f;     // sum of 16 weights that sends M up: no weight passes f16's range
-constexpr int kAmScaleRow = 10;         // of a tile: 8 groups' (key factor, value exponent), then the largest and the least exponent
-constexpr int kAmNoScale = -100000;    // exponent of a value scale that says NaN
+constexpr float kAmMostSum = 1.1e12f;   // 2^kAtSumSlack: what 64 keys add to l, beyond which its reference goes up
+constexpr int kAmScaleRow = 10;         // of a tile: 8 groups' (key factor, value exponent), then a bit per group whose values are NaN
 
 template <int D>
 struct AmSmem {
@@ -214,8 +214,8 @@ __device__ __forceinline__ int find_item(const AttendArgs& a, int items, int64_t
     }
     return n - 1;
 }
-// Floats of a part: O [D / 4][256 rows][4], then M and l of the rows.
-__host__ __device__ constexpr int64_t many_part_floats(int D) { return int64_t(kAmRows) * (D + 2); }
+// Floats of a part: O [D / 4][256 rows][4], then M, l and lift of the rows.
+__host__ __device__ constexpr int64_t many_part_floats(int D) { return int64_t(kAmRows) * (D + 3); }
 
 // Order in which tiles of keys and values are copied and converted: K 0, then K j + 1 and V j for j = 0, 1, ..., without K N.
 __device__ __forceinline__ int tile_of(int item, int N, bool& keys) {
@@ -484,14 +484,12 @@ __global__ void __launch_bounds__(kAmThreads, 1) attend_many_kernel(const __grid
                     const uint32_t kb = j == 0 && N > 1 ? ks : ks_next, vb = j == 0 && N > 1 ? vs : vs_next;
                     ok = mbar_wait_warp(&raw_empty[stage], phase, abort, a.err, a.timeout_ns);
                     if (!ok) break;
-                    // Groups behind the sequence's end take no part in the exponents' range.
-                    const int e = vb == 255 ? kAmNoScale : static_cast<int>(vb) - 127;
-                    const int most = __reduce_max_sync(0xFFFFFFFFu, lane < 8 ? e : kAmNoScale);
-                    const bool part = lane < 8 && w.from + int64_t(j) * kAmKeys + 16 * lane < w.hi;
-                    const int least = __reduce_min_sync(0xFFFFFFFFu, part ? e : 1000);
+                    const float e = vb == 255 ? 0.0f : static_cast<float>(static_cast<int>(vb) - 127);
+                    const bool part = lane < 8 && w.from + int64_t(j) * kAmKeys + 16 * lane < w.hi;      // none behind the sequence's end
+                    const uint32_t nans = __ballot_sync(0xFFFFFFFFu, part && vb == 255);
                     float2* row = scales + slot * kAmScaleRow;
-                    if (lane < 8) row[lane] = make_float2(kb == 255 ? __uint_as_float(0x7FC00000u) : scale_value(kb), __int_as_float(e));
-                    if (lane == 8) row[8] = make_float2(__int_as_float(most), __int_as_float(least));
+                    if (lane < 8) row[lane] = make_float2(kb == 255 ? __uint_as_float(0x7FC00000u) : scale_value(kb), e);
+                    if (lane == 8) row[8].x = __uint_as_float(nans);
                     if (lane == 0) bad_pages[slot] = from_cur ? cur.bad : next.bad;
                     __syncwarp();
                     if (lane == 0) mbar_arrive(&scales_full[slot]);
@@ -575,8 +573,7 @@ __global__ void __launch_bounds__(kAmThreads, 1) attend_many_kernel(const __grid
           const int tok = have ? a.group.div(r) : 0, head = w.h * a.G + (r - tok * a.G);
           const int64_t last = have ? int64_t(w.hi) - w.n + tok : -1;
           const int stop = static_cast<int>(max(last + 1 - w.from, int64_t(0))), start = static_cast<int>(max(last - a.window + 1 - w.from, int64_t(0)));
-          float M = kAtNone, l = 0.0f;
-          int E = kAmNoScale;
+          float M = kAtNone, l = 0.0f, lift = 0.0f;            // as in attend_few_kernel
           for (int j = 0; j < n; ++j) {
             const int slot = (base + j) % kAmScales;
             // In this order: with the scores made, the scales' phase is this tile's and no earlier one's.
@@ -585,12 +582,11 @@ __global__ void __launch_bounds__(kAmThreads, 1) attend_many_kernel(const __grid
             if (!ok) break;
             tc_fence_after();
             const float2* sc = scales + slot * kAmScaleRow;
-            const int ev = __float_as_int(sc[8].x);              // largest value exponent of the tile
             const int end = stop - j * kAmKeys, begin = start - j * kAmKeys;     // columns [begin, end) of this row are seen
             const bool masked = __any_sync(0xFFFFFFFFu, end < kAmKeys || begin > 0);
             // Half a row at a time. There is no pass for the maximum: M only has to be near enough above for f16, and the
-            // sums of the weights, which are made anyway, tell whether one of them is beyond 2^15. If so, or where a larger value
-            // scale has come, M (and E) move, O is rescaled, and the half's weights are made once more. Loops, so that the roles'
+            // sums of the weights, which are made anyway, tell whether one of them is beyond 2^15 (or l's would be beyond 2^40). If so,
+            // M and lift move, O is rescaled, and the half's weights are made once more. Loops, so that the roles'
             // code stays in the instruction cache: unrolled, warps waited for instructions a fifth of the time.
 #pragma unroll 1
             for (int half = 0; half < 2; ++half) {
@@ -601,14 +597,15 @@ __global__ void __launch_bounds__(kAmThreads, 1) attend_many_kernel(const __grid
                     tc_ld_32x32b_x32(ts + half * 64, s[0]);
                     tc_ld_32x32b_x32(ts + half * 64 + 32, s[1]);
                     tc_wait_ld_regs(s[0], s[1]);
+                    const float least = lift - kAtLeast, above = lift + (127.0f - kAtBias), from = M - kAtBias;
                     float back[4];
 #pragma unroll
                     for (int g = 0; g < 4; ++g) {
                         const float2 f = sc[4 * half + g];
-                        const int dv = __float_as_int(f.y) - E, shift = kAtBias + (dv < -kAtValueRange ? 0 : dv);
-                        const float kf = f.x * rowf, d = static_cast<float>(shift) - M;
+                        const float e = fmaxf(f.y, least);
+                        const float kf = f.x * rowf, d = e - from;
                         const uint64_t kf2 = pair(kf, kf), d2 = pair(d, d);
-                        back[g] = __int_as_float((127 - shift) << 23);
+                        back[g] = pow2_biased(above - e);
 #pragma unroll
                         for (int i = 16 * g; i < 16 * g + 16; i += 2) {
                             const float2 e = unpair(fma2(pair(x[i], x[i + 1]), kf2, d2));
@@ -636,10 +633,10 @@ __global__ void __launch_bounds__(kAmThreads, 1) attend_many_kernel(const __grid
                         sum += (r.x + r.y) * back[g];
                     }
                 };
-                const bool larger = half == 0 && ev > E;         // the same in every row; so it is at the beginning, where M is not known
-                if (!larger) weights();
-                if (larger || __any_sync(0xFFFFFFFFu, most > kAmMost)) {
-                    float top = -INFINITY;
+                const bool begins = j + half == 0;               // M is not known
+                if (!begins) weights();
+                if (begins || __any_sync(0xFFFFFFFFu, most > kAmMost || sum > kAmMostSum)) {
+                    float top = -INFINITY, high = -INFINITY;     // of t + e, of t
 #pragma unroll 1
                     for (int q = 0; q < 4; ++q) {
                         uint32_t y[16];
@@ -649,14 +646,17 @@ __global__ void __launch_bounds__(kAmThreads, 1) attend_many_kernel(const __grid
                         float m = -INFINITY;
 #pragma unroll
                         for (int i = 0; i < 16; ++i) m = fmaxf(m, seen >> i & 1 ? __uint_as_float(y[i]) : -INFINITY);
-                        top = fmaxf(top, m * (sc[4 * half + q].x * rowf));
+                        const float2 g = sc[4 * half + q];
+                        m *= g.x * rowf;
+                        top = fmaxf(top, m + g.y);
+                        high = fmaxf(high, m);
                     }
-                    const float next = fmaxf(M, top), f = exp2_approx(M - next);
-                    const float fo = ev > E ? ldexpf(f, max(E - ev, -300)) : f;
+                    const float next = fmaxf(M, rintf(top)), f = exp2_approx(M - next);
+                    const float up = next - fmaxf(M - lift, rintf(high));
+                    l *= exp2_approx((M - next) - (lift - up));
                     M = next;
-                    l *= f;
-                    E = max(E, ev);
-                    if (j + half > 0) {                          // O, once its last product is done
+                    lift = up;
+                    if (!begins) {                               // O, once its last product is done
                         ok = mbar_wait_warp(&o_done[2 * t + (half ^ 1)], (count + (half ? j : j - 1)) & 1, abort, a.err, a.timeout_ns);
                         if (!ok) break;
                         tc_fence_after();
@@ -666,7 +666,7 @@ __global__ void __launch_bounds__(kAmThreads, 1) attend_many_kernel(const __grid
                             tc_ld_32x32b_x16(to + q, y);
                             tc_wait_ld_regs(y);
 #pragma unroll
-                            for (int i = 0; i < 16; ++i) y[i] = __float_as_uint(__uint_as_float(y[i]) * fo);
+                            for (int i = 0; i < 16; ++i) y[i] = __float_as_uint(__uint_as_float(y[i]) * f);
                             tc_st_32x32b_x16(to + q, y);
                         }
                     }
@@ -676,14 +676,13 @@ __global__ void __launch_bounds__(kAmThreads, 1) attend_many_kernel(const __grid
 #pragma unroll
                 for (int i = 0; i < 64; i += 2) p[i / 32][i % 32 / 2] = f16x2(x[i], x[i + 1]);
                 l += sum;
-                const int least = __float_as_int(sc[8].y);
-                if (least == kAmNoScale || least - E < -kAtValueRange) {         // values that do not count, or that are NaN
+                const uint32_t nans = __float_as_uint(sc[8].x) >> 4 * half & 15;
+                if (nans) {
                     __syncwarp();
 #pragma unroll
                     for (int i = 0; i < 64; i += 2) {
-                        const int e = __float_as_int(sc[4 * half + i / 16].y);
                         const bool lo = half * 64 + i < end && half * 64 + i >= begin, hi = half * 64 + i + 1 < end && half * 64 + i + 1 >= begin;
-                        if (e == kAmNoScale || e - E < -kAtValueRange) p[i / 32][i % 32 / 2] = e == kAmNoScale ? (lo ? 0x7FFFu : 0u) | (hi ? 0x7FFF0000u : 0u) : 0u;
+                        if (nans >> i / 16 & 1) p[i / 32][i % 32 / 2] = (lo ? 0x7FFFu : 0u) | (hi ? 0x7FFF0000u : 0u);
                     }
                 }
                 tc_st_32x32b_x16(ts + half * 32, p[0]);          // over columns that have been read
@@ -714,7 +713,7 @@ __global__ void __launch_bounds__(kAmThreads, 1) attend_many_kernel(const __grid
             if (!ok) break;
           }
           tc_fence_after();
-          const float inv = l == 0.0f ? 0.0f : ldexpf(whole ? 1.0f / l : 1.0f, E - kAtBias);
+          const float inv = whole && l != 0.0f ? 1.0f / l : 1.0f, unit = whole ? out_unit(lift) : 1.0f;
           __nv_bfloat16* dst = a.out + (first + tok) * a.ldo_t + head * a.ldo_h;
 #pragma unroll 1
           for (int q = 0; q < D; q += 32) {
@@ -724,7 +723,7 @@ __global__ void __launch_bounds__(kAmThreads, 1) attend_many_kernel(const __grid
                 tc_wait_ld_regs(x);
             }
 #pragma unroll
-            for (int i = 0; i < 32; ++i) x[i] = n > 0 && l != 0.0f ? __float_as_uint(__uint_as_float(x[i]) * inv) : 0u;
+            for (int i = 0; i < 32; ++i) x[i] = n > 0 && l != 0.0f ? __float_as_uint(__uint_as_float(x[i]) * inv * unit) : 0u;
             if (!whole) {
 #pragma unroll
                 for (int i = 0; i < 32; i += 4)
@@ -745,8 +744,9 @@ __global__ void __launch_bounds__(kAmThreads, 1) attend_many_kernel(const __grid
           if (!whole) {
             part[kAmRows * D + t * 128 + row] = M;
             part[kAmRows * D + kAmRows + t * 128 + row] = l;
+            part[kAmRows * D + 2 * kAmRows + t * 128 + row] = lift;
           } else if (have && a.lse) {
-            a.lse[static_cast<int64_t>(first + tok) * a.Hq + head] = l == 0.0f ? -INFINITY : (M + log2f(l)) * 0.693147180559945f;
+            a.lse[static_cast<int64_t>(first + tok) * a.Hq + head] = l == 0.0f ? -INFINITY : (M - lift + log2f(l)) * 0.693147180559945f;
           }
           tc_fence_before();
         }
@@ -776,11 +776,15 @@ __device__ __forceinline__ void join_many(const AttendArgs& a, int block) {
     auto part = [&](int i) { return a.many_parts + (2 * int64_t(cut - 1 + i) + (i == 0 ? 1 : 0)) * many_part_floats(D); };
     for (int i = 0; i < parts; ++i)
         if (!plan_header(a)->done[cut - 1 + i]) return;      // a wait has run out: its rows stay as they were
-    float top = kAtNone, sum = 0.0f;
-    for (int i = 0; i < parts; ++i) top = fmaxf(top, part(i)[kAmRows * D + row]);
-    for (int i = 0; i < parts; ++i) sum += exp2_approx(part(i)[kAmRows * D + row] - top) * part(i)[kAmRows * D + kAmRows + row];
+    auto stat = [&](int i, int k) { return part(i)[kAmRows * D + k * kAmRows + row]; };      // M, l, lift
+    float top = kAtNone, ref = kAtNone, sum = 0.0f;
+    for (int i = 0; i < parts; ++i) {
+        top = fmaxf(top, stat(i, 0));
+        ref = fmaxf(ref, stat(i, 0) - stat(i, 2));
+    }
+    for (int i = 0; i < parts; ++i) sum += exp2_approx(stat(i, 0) - stat(i, 2) - ref) * stat(i, 1);
     if (row >= w.rows) return;
-    const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+    const float inv = sum == 0.0f ? 0.0f : 1.0f / sum, unit = out_unit(top - ref);
     const int r = w.row0 + row, tok = a.group.div(r), head = h * a.G + (r - tok * a.G);
     __nv_bfloat16* dst = a.out + (w.first + tok) * a.ldo_t + head * a.ldo_h;
 #pragma unroll
@@ -788,7 +792,7 @@ __device__ __forceinline__ void join_many(const AttendArgs& a, int block) {
         const int d = piece * (D / kAmJoins) + c;
         float acc[8] = {0, 0, 0, 0, 0, 0, 0, 0};
         for (int i = 0; i < parts; ++i) {
-            const float f = exp2_approx(part(i)[kAmRows * D + row] - top);
+            const float f = exp2_approx(stat(i, 0) - top);
 #pragma unroll
             for (int k = 0; k < 2; ++k) {
                 const float4 v = *reinterpret_cast<const float4*>(part(i) + ((d / 4 + k) * kAmRows + row) * 4);
@@ -798,13 +802,13 @@ __device__ __forceinline__ void join_many(const AttendArgs& a, int block) {
         uint32_t o[4];
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
-            const __nv_bfloat162 v = __floats2bfloat162_rn(acc[2 * k] * inv, acc[2 * k + 1] * inv);
+            const __nv_bfloat162 v = __floats2bfloat162_rn(acc[2 * k] * inv * unit, acc[2 * k + 1] * inv * unit);
             o[k] = *reinterpret_cast<const uint32_t*>(&v);
         }
         *reinterpret_cast<uint4*>(dst + d) = make_uint4(o[0], o[1], o[2], o[3]);
     }
     if (a.lse && piece == 0)
-        a.lse[static_cast<int64_t>(w.first + tok) * a.Hq + head] = sum == 0.0f ? -INFINITY : (top + log2f(sum)) * 0.693147180559945f;
+        a.lse[static_cast<int64_t>(w.first + tok) * a.Hq + head] = sum == 0.0f ? -INFINITY : (ref + log2f(sum)) * 0.693147180559945f;
 }
 
 // `few` blocks join the parts of attend_few_kernel, the others those of attend_many_kernel.
