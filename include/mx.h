@@ -403,7 +403,8 @@ mx_status mx_rope_bwd(const void* dy, mx_out_dtype dtype, int64_t T, int64_t H, 
  *   k_scale, v_scale: one E8M0 byte per page and head, [pages][heads]; a page's bytes are packed, pages ks_stride / vs_stride
  *     apart. A value is code * 2^(byte - 127); byte 255 makes all of its page's values of that head NaN.
  *   page_table [sequences, width] int32, row stride ld_table elements: the page of tokens i * page_size .. of a sequence.
- *     Entries behind a sequence's last page are not read.
+ *     Entries behind a sequence's last page are not read, nor by attention those of pages that lie wholly in front of the first
+ *     row's window.
  *   lengths [sequences] int32: tokens of every sequence, the rows of this call among them (negative: 0).
  *   row_offsets [sequences + 1] int32, nondecreasing from 0: rows [row_offsets[b], row_offsets[b + 1]) of the batch are the
  *     last tokens of sequence b. NULL: one row per sequence (rows == sequences). Rows behind the last sequence's are

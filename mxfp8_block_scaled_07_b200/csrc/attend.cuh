@@ -363,7 +363,8 @@ __global__ void __launch_bounds__(kAtThreads, NT == 1 ? 3 : 2) attend_few_kernel
         auto fetch_ids = [&](int base) {
             const int64_t tok = tok0 + int64_t(base + lane) * kAtStep;
             next_id = -1;
-            if (base + lane < steps && tok < sq.hi) {
+            // 16 keys in front of the first row's window, whose page may be another sequence's by now, are as if behind the end: masked.
+            if (base + lane < steps && tok < sq.hi && tok + 16 > sq.hi - sq.n - a.window + 1) {
                 next_id = page_id(c, b, tok >> c.page_shift);
                 if (next_id < 0) atomicOr(a.err, kErrBadIndex);
             }
