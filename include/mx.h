@@ -433,8 +433,9 @@ typedef struct {
  * floor(log2 amax) - 8 over the tokens appended to it in this call, and not below the page's e if it holds older tokens; where
  * e grew, all of the page's other codes of that head are rounded anew (to nearest even). The page's first token begins it anew,
  * whatever it held, and leaves the codes behind the new ones alone. Codes are RNE(x 2^-e) saturated to +-448, x being the
- * rotation in exact arithmetic. NaN or infinity among the new tokens: scale byte 255 and zero codes for the older and the new
- * ones, until the page is begun anew.
+ * rotation in exact arithmetic (but a product beyond fp32's range may count as an infinity, and a zero code has either sign where
+ * |x| < 2^-149). NaN or infinity among the new tokens: scale byte 255 and zero codes for the older and the new ones, until the
+ * page is begun anew.
  * q (BF16 [rows, q_heads, head_dim], or NULL): rotated to q_out at the same positions, in fp32 rounded once; q_out may be q.
  * No page may be appended to by two sequences in one call. A position behind the rotation table counts as zeros (and sets bit 4).
  * Requirements: rot a multiple of 16, <= head_dim; BF16 tensors 16-byte aligned with strides that are multiples of 8; table 16-byte

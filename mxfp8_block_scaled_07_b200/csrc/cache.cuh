@@ -6,8 +6,9 @@
 // when the new tokens need a larger one the page's other codes are rounded anew to it, which a power of two makes exact but for
 // codes that become subnormal. A page with NaN or infinity has scale byte 0xFF and zero codes until it is begun anew.
 //
-// Keys are rotated on the way. A code hangs on the last bits of the rotation, so the sum of the two products is formed
-// exactly (as an unevaluated sum of fp32 numbers) and rounded to odd, which rounds to E4M3 as the exact value does.
+// Keys are rotated on the way, and their codes are those of the exact rotation. A sum of two products within 1.5 ulp has the exact one's
+// code unless it lies next to a tie between codes or a power of two; those sums (one in 2^16) are formed in fp64
+// and rounded to odd, which rounds to E4M3 as the exact value does.
 //
 // One token of 64 sequences, 8 key and 32 query heads of 128: 2.6 us, a chain of four loads. Prompts of 10 200 tokens: queries 31 us
 // (5.3 TB/s), keys and values 39 us, 70% of the issue slots in the exact rotation.
@@ -22,24 +23,25 @@
 
 namespace mx {
 
-// s + t == a + b exactly (Knuth's two-sum).
-__device__ __forceinline__ float two_sum(float a, float b, float& t) {
-    const float s = __fadd_rn(a, b), bb = __fsub_rn(s, a);
-    t = __fadd_rn(__fsub_rn(a, __fsub_rn(s, bb)), __fsub_rn(b, bb));
-    return s;
+// a c - b s rounded to odd in fp32 (towards zero, and the last bit set unless exact), a and b of 8 bits: rounding that to at most 22
+// bits gives what rounding the exact value would. In fp64, where a c is exact and one rounding is left, made in each direction. (Beyond
+// fp32's range: an infinity.)
+__device__ __forceinline__ float diff_to_odd(float a, float c, float b, float s) {
+    const float near = __fmaf_rn(a, c, -__fmul_rn(b, s));
+    // No number; a pair that is not turned (the first position), which is exact.
+    if (!(fabsf(near) < INFINITY) || (c == 1.0f && s == 0.0f)) return near;
+    const double p = static_cast<double>(a) * c, x = -static_cast<double>(b), y = s;
+    const float f = __double2float_rz(__fma_rz(x, y, p));
+    return __fma_rd(x, y, p) == f && __fma_ru(x, y, p) == f ? f : __int_as_float(__float_as_int(f) | 1);
 }
 
-// a c - b s rounded to odd in fp32 (towards zero, and the last bit set unless exact): rounding that to at most 22
-// bits gives what rounding the exact value would.
-__device__ __forceinline__ float diff_to_odd(float a, float c, float b, float s) {
-    const float p = __fmul_rn(a, c), q = __fmul_rn(b, s);
-    const float ep = __fmaf_rn(a, c, -p), eq = __fmaf_rn(b, s, -q);
-    float t, lo;
-    const float hi0 = two_sum(p, -q, t);
-    const float hi = two_sum(hi0, __fadd_rn(t, __fsub_rn(ep, eq)), lo);
-    if (!(fabsf(lo) > 0.0f)) return hi;          // exact (so it is where hi is 0), or hi is no finite number
-    const int bits = __float_as_int(hi);
-    return __int_as_float((bits + ((__float_as_int(lo) ^ bits) >> 31)) | 1);
+// a c - b s within 1.5 ulp (rope.cuh), and whether a rounding to E4M3 under any power of two, or the power of two below, may hang on
+// what is missing: ties between codes have 5 bits, so the last 19 bits of a number within 1.5 ulp of one are within 4 units of zero
+// (3 below a power of two). Below 2^-100, where products lose bits, always; but 0 is exact, or less than 2^-147 and its code 0.
+__device__ __forceinline__ float diff_in_doubt(float a, float c, float b, float s, bool& doubt) {
+    const float w = __fmul_rn(b, s), y = __fsub_rn(__fmaf_rn(a, c, -w), __fmaf_rn(b, s, -w));      // keeps the sign of zeros
+    doubt = (((__float_as_uint(y) + 4) & 0x7FFFF) <= 8 || fabsf(y) < 0x1p-100f) && y != 0.0f;
+    return y;
 }
 
 __device__ __forceinline__ float bf16_lo(uint32_t w) { return __uint_as_float(w << 16); }
@@ -121,14 +123,16 @@ struct AppendArgs {
     FastDiv heads2;               // 2 * Hkv
 };
 
-// Elements [d, d + 8) of a row, rotated and rounded to odd. x: the row's head.
-__device__ __forceinline__ void rotated8(const __nv_bfloat16* x, int d, const float* angles, int rot, bool interleaved, float (&y)[8]) {
+// Elements [d, d + 8) of a row, rotated, and a bit for each that is in doubt. x: the row's head.
+__device__ __forceinline__ uint32_t rotated8(const __nv_bfloat16* x, int d, const float* angles, int rot, bool interleaved, float (&y)[8]) {
     const uint4 w = *reinterpret_cast<const uint4*>(x + d);
     const uint32_t u[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
     for (int i = 0; i < 4; ++i) y[2 * i] = bf16_lo(u[i]), y[2 * i + 1] = bf16_hi(u[i]);
-    if (d >= rot) return;
+    if (d >= rot) return 0;
     const int h = rot / 2;
+    uint32_t doubts = 0;
+    bool doubt;
     if (interleaved) {
         float c[4], s[4];
         load_angles<4>(angles + d / 2, c);
@@ -136,10 +140,12 @@ __device__ __forceinline__ void rotated8(const __nv_bfloat16* x, int d, const fl
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             const float a = y[2 * i], b = y[2 * i + 1];
-            y[2 * i] = diff_to_odd(a, c[i], b, s[i]);
-            y[2 * i + 1] = diff_to_odd(b, c[i], -a, s[i]);
+            y[2 * i] = diff_in_doubt(a, c[i], b, s[i], doubt);
+            doubts |= doubt ? 1u << 2 * i : 0u;
+            y[2 * i + 1] = diff_in_doubt(b, c[i], -a, s[i], doubt);
+            doubts |= doubt ? 2u << 2 * i : 0u;
         }
-        return;
+        return doubts;
     }
     const bool low = d < h;
     const int i0 = low ? d : d - h;
@@ -151,8 +157,18 @@ __device__ __forceinline__ void rotated8(const __nv_bfloat16* x, int d, const fl
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
         const float other = i & 1 ? bf16_hi(v[i / 2]) : bf16_lo(v[i / 2]);
-        y[i] = diff_to_odd(y[i], c[i], low ? other : -other, s[i]);
+        y[i] = diff_in_doubt(y[i], c[i], low ? other : -other, s[i], doubt);
+        doubts |= doubt ? 1u << i : 0u;
     }
+    return doubts;
+}
+// Element d of a row again, without doubt.
+__device__ __forceinline__ float rotated_to_odd(const __nv_bfloat16* x, int d, const float* angles, int rot, bool interleaved) {
+    const int h = rot / 2;
+    const bool first = interleaved ? !(d & 1) : d < h;
+    const int other = interleaved ? d ^ 1 : first ? d + h : d - h, pair = interleaved ? d / 2 : first ? d : d - h;
+    const float b = to_f32(x[other]);
+    return diff_to_odd(to_f32(x[d]), angles[pair], first ? b : -b, angles[h + pair]);
 }
 
 // The angles of a position: null where there is no rotation, `bad` where the position lies outside the table.
@@ -293,7 +309,15 @@ __global__ void __launch_bounds__(kAppendOneThreads) append_one_kernel(const __g
         if (keys) {
             bool bad;
             const float* angles = angles_of(a, pos, bad);
-            if (!bad) rotated8(a.k + b * a.ldk_t + h * a.ldk_h, lane * 8, angles, angles ? a.rot : 0, a.interleaved, y);
+            const __nv_bfloat16* x = a.k + b * a.ldk_t + h * a.ldk_h;
+            uint32_t doubts = bad ? 0 : rotated8(x, lane * 8, angles, angles ? a.rot : 0, a.interleaved, y);
+#pragma unroll 1
+            for (; doubts; doubts &= doubts - 1) {
+                const int i = __ffs(doubts) - 1;
+                const float exact = rotated_to_odd(x, lane * 8 + i, angles, a.rot, a.interleaved);
+#pragma unroll
+                for (int k = 0; k < 8; ++k) y[k] = k == i ? exact : y[k];
+            }
         } else {
             rotated8(a.v + b * a.ldv_t + h * a.ldv_h, lane * 8, nullptr, 0, false, y);
         }
@@ -324,8 +348,8 @@ __global__ void __launch_bounds__(kAppendQueryThreads) append_queries_kernel(con
 
 // Any number of new tokens per sequence: a block per (page of a sequence, head, keys or values), CH pieces of eight
 // elements per thread (page x D = 8 CH threads). What bounds it is the chain of loads from the offsets to the keys: two pieces a thread
-// leave most warps on their way (eight a thread took 60 us for 10 200 tokens of 8 heads, and a cheaper rotation with the
-// exact one only where a code is in doubt 84, since it needs more registers). Blocks are numbered without a prefix sum: sequence b's pages start at
+// leave most warps on their way (eight a thread took 60 us for 10 200 tokens of 8 heads; forming every sum exactly in fp32 instead of those in
+// doubt 39). Blocks are numbered without a prefix sum: sequence b's pages start at
 // floor(row_offsets[b] / page) + 2 b, which leaves room for all that its tokens can touch (n tokens touch at most n / page +
 // 2 pages); blocks for which nothing is left return.
 template <int D, int CH, int THREADS>
@@ -348,7 +372,7 @@ __global__ void __launch_bounds__(THREADS, THREADS == 1024 ? 1 : 1536 / THREADS)
     const int lo = static_cast<int>(max(start - base, int64_t(0))), hi = static_cast<int>(min(len - base, int64_t(page)));
     const int64_t id = page_id(c, q.b, index);   // on its way with the tokens
     float y[CH][8];
-    uint32_t m = 0;
+    uint32_t m = 0, doubts = 0;
 #pragma unroll
     for (int i = 0; i < CH; ++i) {
         const int at = i * THREADS + threadIdx.x, tok = at / (D / 8), d = (at % (D / 8)) * 8;
@@ -359,13 +383,23 @@ __global__ void __launch_bounds__(THREADS, THREADS == 1024 ? 1 : 1536 / THREADS)
             if (keys) {
                 bool bad;
                 const float* angles = angles_of(a, base + tok, bad);
-                if (!bad) rotated8(a.k + row * a.ldk_t + h * a.ldk_h, d, angles, angles ? a.rot : 0, a.interleaved, y[i]);
+                if (!bad) doubts |= rotated8(a.k + row * a.ldk_t + h * a.ldk_h, d, angles, angles ? a.rot : 0, a.interleaved, y[i]) << 8 * i;
             } else {
                 rotated8(a.v + row * a.ldv_t + h * a.ldv_h, d, nullptr, 0, false, y[i]);
             }
         }
-        m = max(m, amax_bits8(y[i]));
     }
+    // Elements in doubt (one in 2^16; one in 8 of what is not turned) from memory, one by one: with their inputs kept for that, the
+    // kernel spilled.
+#pragma unroll 1
+    for (; doubts; doubts &= doubts - 1) {
+        const int k = __ffs(doubts) - 1, at = k / 8 * THREADS + threadIdx.x, tok = at / (D / 8), d = (at % (D / 8)) * 8 + k % 8;
+        const float exact = rotated_to_odd(a.k + (first + (base + tok - start)) * a.ldk_t + h * a.ldk_h, d, a.table + (base + tok) * a.rot, a.rot, a.interleaved);
+#pragma unroll
+        for (int i = 0; i < 8 * CH; ++i) y[i / 8][i % 8] = i == k ? exact : y[i / 8][i % 8];
+    }
+#pragma unroll
+    for (int i = 0; i < CH; ++i) m = max(m, amax_bits8(y[i]));
     if (id < 0) {                                    // the same in the whole block
         if (threadIdx.x == 0) atomicOr(a.err, kErrBadIndex);
         return;
