@@ -507,6 +507,7 @@ PyObject* cache_append(Args a) {
         need(table->dim() == 2, "cache_append: table must be fp32 [positions, rot]");
         pt = packed(*table, at::kFloat, table->numel(), dev, "cache_append: table must be a contiguous fp32 tensor [positions, rot]");
         positions = table->size(0), rot = table->size(1);
+        if (!pt && positions == 0) pt = hk.p;        // a table without positions, not none: NULL would say so. Nothing of it is read
     }
     const at::Tensor* q = optional_tensor(a[6], "cache_append: q");
     const Place place(k);
