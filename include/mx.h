@@ -383,7 +383,7 @@ mx_status mx_rope_table(const double* freq, int64_t pairs, double amplitude, int
  * 1.5 units in the last place of fp32 and rounded once. pos: int32 [T] (pos64 == 0) or int64 (device), or NULL: 0 .. T - 1 (T <= positions).
  * A token with a negative position (padding) gets zeros; so does one at or behind `positions`, which also sets bit 4 of the
  * device status word. y (the same shape and type, strides ldy_t, ldy_h) may be x itself with the same strides: features from rot on
- * then stay as they are.
+ * then stay as they are. Otherwise no two of their rows may overlap.
  * Requirements: 1 <= D <= 1024, 2 <= rot <= min(D, 256), rot even, heads that do not overlap (|ldx_h| >= D where H > 1);
  * pointers aligned to their elements. Rows whose pieces are all 16-byte aligned move in 16-byte pieces (and rot a
  * multiple of 16 bytes of elements, of 32 in the half layout); others element by element. T == 0 or H == 0 is a no-op.
@@ -436,7 +436,8 @@ typedef struct {
  * rotation in exact arithmetic (but a product beyond fp32's range may count as an infinity, and a zero code has either sign where
  * |x| < 2^-149). NaN or infinity among the new tokens: scale byte 255 and zero codes for the older and the new ones, until the
  * page is begun anew.
- * q (BF16 [rows, q_heads, head_dim], or NULL): rotated to q_out at the same positions, in fp32 rounded once; q_out may be q.
+ * q (BF16 [rows, q_heads, head_dim], or NULL): rotated to q_out at the same positions, in fp32 rounded once; q_out may be q
+ * with the same strides, and no rows of it may overlap others of its own, q's, k's or v's.
  * No page may be appended to by two sequences in one call. A position behind the rotation table counts as zeros (and sets bit 4).
  * Requirements: rot a multiple of 16, <= head_dim; BF16 tensors 16-byte aligned with strides that are multiples of 8; table 16-byte
  * aligned; q_heads <= 4096.
@@ -457,7 +458,7 @@ int64_t mx_cache_attention_workspace_bytes(int64_t head_dim, int64_t rows, int64
  * Scores, softmax statistics and sums are fp32; what multiplies a value's code, weight times scale, is rounded to f16 relative to
  * the largest that the row sees: 11 bits from 2^-20 of that one up, an error of less than 2^-31 of it below. Scales may lie as far
  * apart as they like, and pages that a row does not see change nothing. A row that sees no key has out 0 and lse -inf. Codes 0x7F and 0xFF, which mx_cache_append does not write, count as NaN, and may do so for neighbouring
- * rows that do not see them. Sums are made in a fixed order.
+ * rows that do not see them. Sums are made in a fixed order. out may be q with the same strides; otherwise no two of their rows may overlap.
  * workspace: mx_cache_attention_workspace_bytes(head_dim, rows, q_heads) device bytes, 16-byte aligned, used during this call only (calls that
  * may run at the same time need their own). row_offsets that name rows twice may leave rows unwritten, with bit 2 of the status word.
  * After an expired wait a row is its value or what was there before.

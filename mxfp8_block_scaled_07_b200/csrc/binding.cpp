@@ -15,7 +15,9 @@
 #include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
 
+#include <algorithm>
 #include <cmath>
+#include <cstdlib>
 #include <string>
 
 #include "../../include/mx.h"
@@ -423,6 +425,56 @@ Heads heads_bf16(const at::Tensor& t, at::Device dev, const char* what) {
     return heads(t, what);
 }
 
+int64_t span(const Heads& x) { return (x.T - 1) * x.ld_t + (x.H - 1) * x.ld_h + x.D; }
+
+// Whether rows of D elements at i sa and d + j sb, i < na and j < nb, overlap anywhere.
+bool rows_meet(int64_t d, int64_t sa, int64_t na, int64_t sb, int64_t nb, int64_t D) {
+    // The k of [lo, hi] that brings d + k s nearest 0.
+    auto near = [D](int64_t d, int64_t s, int64_t lo, int64_t hi) {
+        if (s == 0) return std::abs(d) < D;
+        const int64_t k = -d / s;                            // towards 0: this one or the next on either side
+        for (int64_t c = k - 1; c <= k + 1; ++c)
+            if (std::abs(d + std::min(std::max(c, lo), hi) * s) < D) return true;
+        return false;
+    };
+    if (sa == sb) return near(d, sa, 1 - na, nb - 1);
+    for (int64_t j = 0; j < nb; ++j)
+        if (near(d + j * sb, -sa, 0, na - 1)) return true;
+    return false;
+}
+// Whether two tensors of one element size share elements: their first and last bytes tell almost always, else, of views of one fused
+// projection, their places within a token.
+bool overlap(const Heads& x, const Heads& y, int64_t size) {
+    if (x.T == 0 || x.H == 0 || x.D == 0 || y.T == 0 || y.H == 0 || y.D == 0) return false;
+    const char *px = static_cast<const char*>(x.p), *py = static_cast<const char*>(y.p);
+    const int64_t sx = span(x), sy = span(y);
+    if (px + sx * size <= py || py + sy * size <= px) return false;
+    const int64_t d = (py - px) / size, D = std::max(x.D, y.D);
+    const int64_t st = x.T > 1 ? x.ld_t : y.ld_t, wx = sx - (x.T - 1) * x.ld_t, wy = sy - (y.T - 1) * y.ld_t;
+    if ((y.T == 1 || y.ld_t == st) && st > 0 && wx <= st && wy <= st) {
+        const int64_t at = (d % st + st) % st;
+        if (at >= wx && at + wy <= st) return false;
+    }
+    for (int64_t g = 0; g < x.H; ++g)
+        for (int64_t h = 0; h < y.H; ++h)
+            if (rows_meet(d + h * y.ld_h - g * x.ld_h, x.ld_t, x.T, y.ld_t, y.T, D)) return true;
+    return false;
+}
+// Whether rows of a tensor share elements with one another (expanded ones, say).
+bool overlaps_itself(const Heads& x) {
+    if (x.T == 0 || x.H == 0 || x.D == 0) return false;
+    if ((x.H == 1 || x.ld_h >= x.D) && (x.T == 1 || x.ld_t >= (x.H - 1) * x.ld_h + x.D)) return false;
+    if (x.T > 1 && x.ld_t < x.D) return true;
+    for (int64_t h = 1; h < x.H; ++h)
+        if (rows_meet(h * x.ld_h, x.ld_t, x.T, x.ld_t, x.T, x.D)) return true;
+    return false;
+}
+// An output that may be the input itself, and shares no elements with it or its own otherwise.
+bool fit_for(const Heads& out, const Heads& in, int64_t size) {
+    const bool same = out.p == in.p && out.ld_t == in.ld_t && out.ld_h == in.ld_h && out.H == in.H && out.T == in.T && out.D == in.D;
+    return !overlaps_itself(out) && (same || !overlap(out, in, size));
+}
+
 // (x, table, positions, interleaved, out)
 template <bool BACKWARD>
 PyObject* rope_call(Args a) {
@@ -446,7 +498,7 @@ PyObject* rope_call(Args a) {
     const at::Tensor out = a[4] == Py_None ? fresh({h.T, h.H, h.D}, type) : tensor(a[4], "rope: out");
     const Heads o = heads(out, "rope: out must be like x");
     need(o.T == h.T && o.H == h.H && o.D == h.D && out.scalar_type() == type && out.device() == dev, "rope: out must be like x");
-    need(!o.p || o.p != h.p || (o.ld_t == h.ld_t && o.ld_h == h.ld_h), "rope: out on x's memory must be x itself");
+    if (a[4] != Py_None) need(fit_for(o, h, x.element_size()), "rope: out must be x itself or lie apart from it, and its rows from one another");
     check((BACKWARD ? mx_rope_bwd : mx_rope)(h.p, code, h.T, h.H, h.D, h.ld_t, h.ld_h, static_cast<const float*>(pt), table.size(0),
                                              table.size(1), pp, pos64, interleaved, o.p, o.ld_t, o.ld_h, place.stream),
           BACKWARD ? "mx_rope_bwd" : "mx_rope");
@@ -520,7 +572,9 @@ PyObject* cache_append(Args a) {
         out = a[9] == Py_None ? fresh({hq.T, hq.H, hq.D}, at::kBFloat16) : tensor(a[9], "cache_append: out");
         ho = heads_bf16(out, dev, what);
         need(ho.T == hq.T && ho.H == hq.H && ho.D == hq.D, what);
-        need(!ho.p || ho.p != hq.p || (ho.ld_t == hq.ld_t && ho.ld_h == hq.ld_h), "cache_append: out on q's memory must be q itself");
+        if (a[9] != Py_None)
+            need(fit_for(ho, hq, 2) && !overlap(ho, hk, 2) && !overlap(ho, hv, 2),
+                 "cache_append: out must be q itself or lie apart from it, and from k and v, and its rows from one another");
     }
     check(mx_cache_append(&c, hk.p, hk.ld_t, hk.ld_h, hv.p, hv.ld_t, hv.ld_h, static_cast<const float*>(pt), positions, rot, truth(a[8]),
                           hq.p, hq.H, hq.ld_t, hq.ld_h, ho.p, ho.ld_t, ho.ld_h, place.stream),
@@ -553,6 +607,7 @@ PyObject* cache_attention(Args a) {
     out = po ? tensor(po, "cache_attention: out") : fresh({h.T, h.H, h.D}, at::kBFloat16);
     const Heads o = heads_bf16(out, dev, what);
     need(o.T == h.T && o.H == h.H && o.D == h.D, what);
+    if (po) need(fit_for(o, h, 2), "cache_attention: out must be q itself or lie apart from it, and its rows from one another");
     if (want) lse = pl ? tensor(pl, "cache_attention: lse") : fresh({h.T, h.H}, at::kFloat);
     float* l = want ? ptr<float>(packed(lse, at::kFloat, h.T * h.H, dev, "cache_attention: lse must be fp32 [rows, q_heads]")) : nullptr;
     check(mx_cache_attention(&c, h.p, h.H, h.ld_t, h.ld_h, scale, window, o.p, o.ld_t, o.ld_h, l, ws.data_ptr(), place.stream),

@@ -7,6 +7,7 @@ import plain_cache as plain
 from helpers import to_np
 from mxfp8_block_scaled_07_b200 import mx
 from test_gpu_cache_append import i32, normal
+from test_gpu_cache_attention import cache_of
 
 pytestmark = pytest.mark.gpu
 
@@ -27,3 +28,67 @@ def test_a_rotation_table_without_positions(single):
         want = plain.append((np.zeros((n, H, page, D), np.uint8), np.zeros((n, H), np.uint8)), x, pages, lengths, offsets)
         assert np.array_equal(to_np(code), want[0]) and np.array_equal(to_np(byte), want[1])
     assert not mx.rope(q.cuda(), table, i32(lengths)).any() and mx.device_error() == 4
+
+
+def views(buf):
+    """(x, out, may be) over a buffer [20, 12, 64]: [5, 4, 64] each."""
+    flat = buf.view(-1)
+    packed = flat[:5 * 4 * 64].view(5, 4, 64)
+    return [(buf[:5, :4], buf[:5, :4], True), (buf[:5, :4], buf[:5, 4:8], True), (buf[:5, 8:], buf[:5, :4], True), (buf[:5, :4], buf[5:10, :4], True),
+            (buf[0:10:2, :4], buf[1:11:2, :4], True), (buf[0:10:2, :4], buf[0:10:2, 4:8], True),
+            (buf[:5, 0:8:2], buf[:5, 1:9:2], True), (packed, flat[5 * 4 * 64:2 * 5 * 4 * 64].view(4, 5, 64).transpose(0, 1), True), (packed, buf[2:7, 4:8], True),
+            (buf[:5, :4], buf[1:6, :4], False), (buf[:5, :4], buf[:5, 1:5], False), (buf[:5, :4], buf[:5, 3:7], False), (packed, flat[8:8 + 1280].view(5, 4, 64), False),
+            (packed, flat[64:64 + 1280].view(5, 4, 64), False), (packed, flat[:1280].view(4, 5, 64).transpose(0, 1), False), (packed, buf[1:6, 4:8], False),
+            (buf[:5, :4], buf[10:11, :4].expand(5, 4, 64), False), (buf[:5, :4], flat[8000:].as_strided((5, 4, 64), (192, 64, 1), 8000), False),
+            (buf[:5, :4], flat.as_strided((5, 4, 64), (64, 192, 1), 8000), False)]
+
+
+@pytest.mark.parametrize("i", range(len(views(torch.zeros(20, 12, 64)))))
+def test_outputs_on_their_inputs_memory(i):
+    """Outputs that are their input or lie beside it in one buffer are right; those that overlap it, or themselves, are refused and nothing is written."""
+    base = normal((20, 12, 64), 1).cuda()
+    cache, D, page = mx.cache_create(5, 4, 64, 16), 64, 16
+    table = mx.rope_table(64, D)
+    pages, lengths = i32(np.arange(5)[:, None]), i32([1, 16, 3, 9, 0])
+    mx.cache_append(base[:5, :4], base[:5, 4:8], cache, pages, lengths)
+
+    def append(x, out):
+        k = base[:5, :4]
+        return mx.cache_append(k, k, mx.KVCache(*(t.clone() for t in cache)), pages, lengths, q=x, table=table, out=out)
+
+    calls = [lambda x, out: mx.rope(x, table, out=out), lambda x, out: mx.rope_backward(x, table, interleaved=True, out=out), append,
+             lambda x, out: mx.cache_attention(x, cache, pages, lengths, out=out),
+             lambda x, out: mx.cache_attention(x, cache, pages, lengths, i32([0, 1, 2, 5, 5, 5]), out=out)]
+    for call in calls:
+        buf = base.clone()
+        x, out, may = views(buf)[i]
+        if not may:
+            with pytest.raises(mx.MxError):
+                call(x, out)
+            assert torch.equal(buf, base)
+            continue
+        want = call(x, None)
+        assert torch.equal(buf, base) and call(x, out) is out and torch.equal(out, want)
+
+
+def test_queries_written_over_keys_or_values_are_refused():
+    buf = normal((5, 12, 64), 1).cuda()
+    cache = mx.cache_create(5, 4, 64, 16)
+    where = (cache, i32(np.arange(5)[:, None]), i32([1] * 5))
+    for q, k, v, out in ((buf[:, :4], buf[:, 4:8], buf[:, 8:], buf[:, 4:8]), (buf[:, :4], buf[:, 4:8], buf[:, 8:], buf[:, 7:11]),
+                         (buf[:, :4], buf[:, 4:8], buf[:, 8:], buf[:, 8:])):
+        with pytest.raises(mx.MxError):
+            mx.cache_append(k, v, *where, q=q, out=out)
+    assert not cache.k.any() and not cache.v_scale.any()
+
+
+@pytest.mark.parametrize("rows", [1, 30, 400])
+def test_attention_over_its_queries(rows):
+    """out may be q, with units of every kind: few rows and many, whole and cut."""
+    lengths = np.array([rows, rows + 70, 9000])
+    cache, dev, table = cache_of(lengths, 2, 128, 64, 3)
+    q = normal((3 * rows, 10, 128), 1).cuda()
+    where = (dev, i32(table), i32(lengths), i32(np.arange(4) * rows))
+    want = mx.cache_attention(q[:, 1:9], *where)
+    x = q[:, 1:9]
+    assert mx.cache_attention(x, *where, out=x) is x and torch.equal(x, want)
