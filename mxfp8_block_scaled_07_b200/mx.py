@@ -485,23 +485,32 @@ def rope_frequencies(rot: int, base: float = 10000.0, scaling=None):
     they are, the ones between blended, and cosines and sines times 0.1 ln(factor) + 1."""
     if rot < 2 or rot % 2 or not base > 0:
         raise MxError(-1, "rope_frequencies: an even rot of at least 2, base > 0")
-    kind = scaling[0] if scaling else None
-    if kind == "ntk":
-        base *= float(scaling[1]) ** (rot / (rot - 2)) if rot > 2 else 1.0
-    freq = [base ** (-2.0 * i / rot) for i in range(rot // 2)]
+    what = "rope_frequencies: scaling None, ('linear', factor), ('ntk', factor) or ('yarn', factor, positions[, beta_fast, beta_slow])"
+    try:
+        kind, *numbers = scaling or (None,)
+        least, most = {None: (0, 0), "linear": (1, 1), "ntk": (1, 1), "yarn": (2, 4)}[kind]
+        numbers = [float(x) for x in numbers[:most]]
+    except (TypeError, ValueError, KeyError):
+        raise MxError(-1, what) from None
+    if len(numbers) < least:
+        raise MxError(-1, what)
+    if not all(0 < x < math.inf for x in numbers) or (kind == "yarn" and base == 1):
+        raise MxError(-1, "rope_frequencies: a factor above 0, positions and turns too; for yarn a base other than 1")
+    try:
+        if kind == "ntk":
+            base *= numbers[0] ** (rot / (rot - 2)) if rot > 2 else 1.0
+        freq = [base ** (-2.0 * i / rot) for i in range(rot // 2)]
+    except OverflowError:
+        raise MxError(-1, "rope_frequencies: a base and a factor within fp64's range") from None
     if kind in (None, "ntk"):
         return freq, 1.0
-    factor = float(scaling[1])
-    if not factor > 0:
-        raise MxError(-1, "rope_frequencies: a factor above 0")
+    factor = numbers[0]
     if kind == "linear":
         return [f / factor for f in freq], 1.0
-    if kind != "yarn":
-        raise MxError(-1, "rope_frequencies: scaling None, ('linear', factor), ('ntk', factor) or ('yarn', factor, positions)")
-    fast, slow = (list(scaling[3:]) + [32.0, 1.0][len(scaling) - 3:])[:2]
+    fast, slow = (numbers[2:] + [32.0, 1.0][len(numbers) - 2:])[:2]
 
     def pair_that_turns(turns):
-        return rot * math.log(scaling[2] / (2 * math.pi * turns)) / (2 * math.log(base))
+        return rot * math.log(numbers[1] / (2 * math.pi * turns)) / (2 * math.log(base))
 
     lo, hi = max(math.floor(pair_that_turns(fast)), 0), min(math.ceil(pair_that_turns(slow)), rot - 1)
     ramp = [min(max((i - lo) / max(hi - lo, 0.001), 0.0), 1.0) for i in range(rot // 2)]
