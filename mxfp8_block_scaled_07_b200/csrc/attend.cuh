@@ -513,7 +513,7 @@ __global__ void __launch_bounds__(kAtThreads, NT == 1 ? 3 : 2) attend_few_kernel
             const float kscale = kb == 255 ? __uint_as_float(0x7FC00000u) : scale_value(kb);
             const float e = vb == 255 ? 0.0f : static_cast<float>(static_cast<int>(vb) - 127);
             bool more = false;
-            const bool edge = key < all_from || key + 16 > all_to;
+            const bool edge = key < all_from || key > all_to - 16;       // key + 16 may pass 2^31 - 1
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
                 const float f0 = rowf[nt][0] * kscale, f1 = rowf[nt][1] * kscale;
