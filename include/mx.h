@@ -455,7 +455,8 @@ int64_t mx_cache_attention_workspace_bytes(int64_t head_dim, int64_t rows, int64
  * head i / (q_heads / heads). A row at position p sees the keys p - window + 1 .. p of its sequence (window <= 0: 0 .. p):
  *   out = sum_j softmax_j(scale q . k_j) v_j   (BF16 [rows, q_heads, head_dim], strides ldo_t, ldo_h)
  *   lse = log sum_j exp(scale q . k_j)         (fp32 [rows, q_heads], packed; NULL: not wanted)
- * Scores, softmax statistics and sums are fp32; what multiplies a value's code, weight times scale, is rounded to f16 relative to
+ * Scores, softmax statistics and sums are fp32 (a row whose scores times log2 e lie beyond +-2^24, where fp32 does not tell
+ * neighbouring ones apart, has no defined result); what multiplies a value's code, weight times scale, is rounded to f16 relative to
  * the largest that the row sees: 11 bits from 2^-20 of that one up, an error of less than 2^-31 of it below. Scales may lie as far
  * apart as they like, and pages that a row does not see change nothing. A row that sees no key has out 0 and lse -inf. Codes 0x7F and 0xFF, which mx_cache_append does not write, count as NaN, and may do so for neighbouring
  * rows that do not see them. Sums are made in a fixed order. out may be q with the same strides; otherwise no two of their rows may overlap.
