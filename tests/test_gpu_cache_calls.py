@@ -92,3 +92,14 @@ def test_attention_over_its_queries(rows):
     want = mx.cache_attention(q[:, 1:9], *where)
     x = q[:, 1:9]
     assert mx.cache_attention(x, *where, out=x) is x and torch.equal(x, want)
+
+
+def test_rows_named_twice_set_their_bit():
+    """30 sequences that all name the same 100 rows make 60 items of 256 query rows, where 400 query rows make 10 at most: bit 2, and nothing computed."""
+    cache, dev, table = cache_of([200] * 60, 1, 64, 16, 7)
+    q = normal((100, 4, 64), 1).cuda()
+    out = torch.full((100, 4, 64), 5.0, dtype=torch.bfloat16, device="cuda")
+    mx.device_error()
+    mx.cache_attention(q, dev, i32(table), i32([200] * 60), i32([0, 100] * 30 + [0]), out=out)
+    assert mx.device_error() == 2
+    assert (out == 5).all()
