@@ -594,10 +594,8 @@ PyObject* cache_attention(Args a) {
     const float scale = a[5] == Py_None ? static_cast<float>(1.0 / std::sqrt(static_cast<double>(h.D))) : static_cast<float>(number(a[5]));
     const int64_t window = integer(a[6]);
     const bool want = truth(a[7]);
-    const int64_t bytes = mx_cache_attention_workspace_bytes(h.D, h.T, h.H);
-    if (bytes < 0) throw Refused{MX_ERR_SHAPE, "cache_attention: head_dim 64 or 128, at least one head"};
     const Place place(q);
-    const at::Tensor ws = fresh({bytes}, at::kByte);
+    const at::Tensor ws = fresh({std::max<int64_t>(mx_cache_attention_batch_bytes(&c, h.H), 0)}, at::kByte);       // -1: the call says why
     at::Tensor out, lse;
     PyObject *po = nullptr, *pl = nullptr;
     if (a[8] != Py_None) {

@@ -6,6 +6,7 @@
 #include <cuda_runtime.h>
 
 #include <atomic>
+#include <cmath>
 #include <cstdint>
 #include <cstring>
 #include <mutex>
@@ -1607,6 +1608,12 @@ mx_status cache_checks(const mx_cache_batch* c, bool* empty) {
     return MX_OK;
 }
 
+mx_status attention_checks(const mx_cache_batch* c, int64_t q_heads, bool* empty, bool good = true) {
+    if (mx_status st = cache_checks(c, empty)) return st;
+    if (q_heads < 1 || !good) return MX_ERR_ARG;
+    return q_heads % c->heads != 0 || q_heads > kCacheMaxQueryHeads || c->rows * q_heads >= kInt32End ? MX_ERR_SHAPE : MX_OK;
+}
+
 CacheView view_of(const mx_cache_batch* c) {
     CacheView v;
     v.k = c->k, v.v = c->v, v.ks = c->k_scale, v.vs = c->v_scale;
@@ -1652,7 +1659,7 @@ mx_status launch_append_dim(AppendArgs& a, mx_stream stream) {
     return launch_append<128, 2, 1024>(a, stream);
 }
 
-// Blocks of attend_few_kernel at most; also what sizes the workspace.
+// Blocks of attend_few_kernel at most.
 constexpr int64_t kAtMaxBlocks = 480;
 constexpr int kAtMinSteps = 2;
 
@@ -1681,43 +1688,63 @@ int64_t plan_items(int64_t rows) { return rows / kAmRows + rows / (kAtFewRows + 
 struct AttendSpace {
     int64_t many_parts, plan, bytes;             // offsets in the workspace; the parts of few rows begin it
 };
-// Only row_offsets can bring many rows: without them a sequence has G.
-AttendSpace attend_space(int64_t D, int64_t all_rows) {
+AttendSpace attend_space(int64_t D, int64_t blocks, int64_t part_rows, int64_t many_blocks, int64_t items) {
     AttendSpace s;
-    s.many_parts = kAtMaxBlocks * 2 * part_floats(16, static_cast<int>(D)) * 4;
-    s.plan = s.many_parts + int64_t(kAmMaxBlocks) * 2 * many_part_floats(static_cast<int>(D)) * 4;
-    s.bytes = s.plan + int64_t(sizeof(AmHeader)) + plan_items(all_rows) * int64_t(sizeof(AmItem));
+    s.many_parts = blocks * 2 * part_floats(static_cast<int>(part_rows), static_cast<int>(D)) * 4;
+    s.plan = s.many_parts + many_blocks * 2 * many_part_floats(static_cast<int>(D)) * 4;
+    s.bytes = s.plan + (items ? int64_t(sizeof(AmHeader)) + items * int64_t(sizeof(AmItem)) : 0);
+    return s;
+}
+
+// How a batch's work is laid out: which kernels run, with how many blocks at most (both kernels' least shares bound them too: more
+// would stay idle), and the workspace. Only row_offsets can bring many rows: without them a sequence has G.
+struct AttendShape {
+    int64_t few, tile_rows, tiles, blocks, many_blocks, items;
+    bool many;
+    AttendSpace space;
+};
+AttendShape attend_shape(const mx_cache_batch* c, int64_t q_heads) {
+    AttendShape s;
+    const int64_t G = q_heads / c->heads, rows = c->row_offsets ? c->rows * G : G;
+    s.few = c->row_offsets ? std::min(rows, kAtFewRows) : rows;
+    s.many = rows > s.few;
+    s.tile_rows = s.few <= 8 ? 8 : 16;
+    s.tiles = ceil_div(s.few, s.tile_rows);
+    // Steps and key tiles that there can be (longer sequences than the table is wide have bad pages).
+    const int64_t keys = c->width * c->page_size;
+    const double steps = double(c->sequences) * c->heads * double(s.tiles) * double(keys / kAtStep + 2);
+    s.blocks = static_cast<int64_t>(std::min<double>(kAtMaxBlocks, std::ceil(steps / kAtMinSteps)));
+    s.items = s.many ? plan_items(rows) : 0;
+    const double cost = double(s.items) * c->heads * double(keys / kAmKeys + 2 + kAmUnitCost);
+    s.many_blocks = static_cast<int64_t>(std::min<double>(kAmMaxBlocks, std::ceil(cost / kAmMinCost)));
+    s.space = attend_space(c->head_dim, s.blocks, s.tile_rows, s.many_blocks, s.items);
     return s;
 }
 
 template <int D, int NT>
-mx_status launch_attend(AttendArgs& a, int64_t few, bool many, const DeviceInfo* d, mx_stream stream) {
+mx_status launch_attend(AttendArgs& a, const AttendShape& shape, const DeviceInfo* d, mx_stream stream) {
     static std::atomic<bool> opted[kMaxDevices], opted_many[kMaxDevices];
     constexpr int smem = AtSmem<D, NT>::kBytes;
     if (!opt_in_smem(opted, attend_few_kernel<D, NT>, smem)) return MX_ERR_CUDA;
+    const bool many = shape.many;
     if (many && !opt_in_smem(opted_many, attend_many_kernel<D>, AmSmem<D>::kBytes)) return MX_ERR_CUDA;
-    const int64_t tiles = ceil_div(few, 8 * NT), joins = tiles * a.c.Hkv * a.c.B;
-    a.most_rows = static_cast<int>(few);
-    // No more blocks than steps there can be.
-    const int64_t keys = int64_t(a.c.width) << a.c.page_shift;
-    const double bound = double(a.c.B) * a.c.Hkv * double(tiles) * double(keys / kAtStep + 2);
-    a.blocks = static_cast<int>(std::min<double>(std::min<int64_t>(AtSmem<D, NT>::kBlocks * d->sms, kAtMaxBlocks), bound));
-    a.many_blocks = static_cast<int>(std::min<int64_t>(d->sms, kAmMaxBlocks));
+    const int64_t joins = shape.tiles * a.c.Hkv * a.c.B;
+    a.most_rows = static_cast<int>(shape.few);
+    a.blocks = static_cast<int>(std::min<int64_t>(AtSmem<D, NT>::kBlocks * d->sms, shape.blocks));
+    a.many_blocks = static_cast<int>(std::min<int64_t>(d->sms, shape.many_blocks));
     const int64_t cuts = many ? int64_t(a.many_blocks - 1) * kAmJoins : 0;
     if (joins + cuts >= kInt32End) return MX_ERR_SHAPE;
     if (!many) a.plan = nullptr;
     if (mx_status st = launch_behind(attend_few_kernel<D, NT>, a.blocks + (many ? 1 : 0), kAtThreads, smem, 1, stream, a)) return st;
     if (many)
         if (mx_status st = launch_behind(attend_many_kernel<D>, a.many_blocks, kAmThreads, AmSmem<D>::kBytes, 1, stream, a)) return st;
-    return launch_behind(attend_join_kernel<D, NT>, joins + cuts, kAtJoinThreads, 0, 1, stream, a, static_cast<int>(tiles),
-                         static_cast<int>(joins));
+    return launch_behind(attend_join_kernel<D, NT>, joins + cuts, kAtJoinThreads, 0, 1, stream, a,
+                         static_cast<int>(shape.tiles), static_cast<int>(joins));
 }
 
 template <int D>
-mx_status launch_attend_rows(AttendArgs& a, const DeviceInfo* d, mx_stream stream) {
-    const int64_t rows = a.c.row_offsets ? int64_t(a.c.T) * a.G : a.G;
-    const int64_t few = a.c.row_offsets ? std::min(rows, kAtFewRows) : rows;
-    return few <= 8 ? launch_attend<D, 1>(a, few, rows > few, d, stream) : launch_attend<D, 2>(a, few, rows > few, d, stream);
+mx_status launch_attend_rows(AttendArgs& a, const AttendShape& shape, const DeviceInfo* d, mx_stream stream) {
+    return shape.tile_rows == 8 ? launch_attend<D, 1>(a, shape, d, stream) : launch_attend<D, 2>(a, shape, d, stream);
 }
 
 }  // namespace
@@ -1792,16 +1819,20 @@ mx_status mx_cache_append(const mx_cache_batch* cache, const void* k, int64_t ld
 
 int64_t mx_cache_attention_workspace_bytes(int64_t head_dim, int64_t rows, int64_t q_heads) {
     if ((head_dim != 64 && head_dim != 128) || rows < 0 || q_heads < 1) return -1;
-    return rows * q_heads < kInt32End ? attend_space(head_dim, rows * q_heads).bytes : -1;
+    return rows * q_heads < kInt32End ? attend_space(head_dim, kAtMaxBlocks, 16, kAmMaxBlocks, plan_items(rows * q_heads)).bytes : -1;
+}
+
+int64_t mx_cache_attention_batch_bytes(const mx_cache_batch* cache, int64_t q_heads) {
+    bool empty = false;
+    if (attention_checks(cache, q_heads, &empty) != MX_OK) return -1;
+    return empty ? 0 : attend_shape(cache, q_heads).space.bytes;
 }
 
 mx_status mx_cache_attention(const mx_cache_batch* cache, const void* q, int64_t q_heads, int64_t ldq_t, int64_t ldq_h,
                              float scale, int64_t window, void* out, int64_t ldo_t, int64_t ldo_h, float* lse,
                              void* workspace, mx_stream stream) {
     bool empty = false;
-    if (mx_status st = cache_checks(cache, &empty)) return st;
-    if (q_heads < 1 || !(scale > 0.0f) || !(scale < INFINITY)) return MX_ERR_ARG;
-    if (q_heads % cache->heads != 0 || q_heads > kCacheMaxQueryHeads || cache->rows * q_heads >= kInt32End) return MX_ERR_SHAPE;
+    if (mx_status st = attention_checks(cache, q_heads, &empty, scale > 0.0f && scale < INFINITY)) return st;
     if (empty) return MX_OK;
     if (!q || !out || !workspace) return MX_ERR_ARG;
     if (!pieces_ok(q, ldq_t, ldq_h) || !pieces_ok(out, ldo_t, ldo_h) || !word_aligned(lse) || !aligned16(workspace))
@@ -1823,11 +1854,11 @@ mx_status mx_cache_attention(const mx_cache_batch* cache, const void* q, int64_t
     a.G = static_cast<int>(q_heads / cache->heads);
     a.group = FastDiv::of(a.G);
     a.min_steps = kAtMinSteps;
-    const AttendSpace space = attend_space(cache->head_dim, cache->rows * q_heads);
-    a.plan = static_cast<uint8_t*>(workspace) + space.plan;
-    a.many_parts = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + space.many_parts);
-    a.plan_items = static_cast<int>(plan_items(cache->rows * a.G));
-    return cache->head_dim == 128 ? launch_attend_rows<128>(a, d, stream) : launch_attend_rows<64>(a, d, stream);
+    const AttendShape shape = attend_shape(cache, q_heads);
+    a.plan = static_cast<uint8_t*>(workspace) + shape.space.plan;
+    a.many_parts = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + shape.space.many_parts);
+    a.plan_items = static_cast<int>(shape.items);
+    return cache->head_dim == 128 ? launch_attend_rows<128>(a, shape, d, stream) : launch_attend_rows<64>(a, shape, d, stream);
 }
 
 }  // extern "C"

@@ -119,6 +119,8 @@ def lib() -> ctypes.CDLL:
         fn.restype = I32
     L.mx_cache_attention_workspace_bytes.argtypes = [I64, I64, I64]
     L.mx_cache_attention_workspace_bytes.restype = I64
+    L.mx_cache_attention_batch_bytes.argtypes = [P, I64]
+    L.mx_cache_attention_batch_bytes.restype = I64
     L.mx_route_plan_workspace_bytes.argtypes = [I64, I64]
     L.mx_route_plan_workspace_bytes.restype = I64
     L.mx_grouped_scale_bytes.argtypes = [I64, I64, I64]

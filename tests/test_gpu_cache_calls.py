@@ -1,4 +1,6 @@
 """Calls of the rotation, cache and attention functions that are unusual but allowed, or that only look so and are refused."""
+import ctypes
+
 import numpy as np
 import pytest
 import torch
@@ -7,7 +9,7 @@ import plain_cache as plain
 from helpers import to_np
 from mxfp8_block_scaled_07_b200 import mx
 from test_gpu_cache_append import i32, normal
-from test_gpu_cache_attention import cache_of
+from test_gpu_cache_attention import cache_of, verify
 
 pytestmark = pytest.mark.gpu
 
@@ -103,3 +105,30 @@ def test_rows_named_twice_set_their_bit():
     mx.cache_attention(q, dev, i32(table), i32([200] * 60), i32([0, 100] * 30 + [0]), out=out)
     assert mx.device_error() == 2
     assert (out == 5).all()
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("lengths,rows", [([1000], None), ([5, 900, 0, 17], None), ([40] * 200, None), ([700, 300], [13, 1]), ([700, 300], [300, 40]), ([64], [64]),
+                                          ([9000], [257]), ([100] * 9, [100] * 9), ([20000, 300], [600, 300])])
+@pytest.mark.parametrize("Hq", [2, 12])
+def test_the_workspace_is_as_large_as_it_says(D, lengths, rows, Hq):
+    """A workspace of exactly the bytes for the batch, between bytes that stay as they are; the same result as with the larger one of any batch."""
+    Hkv, page = 2, 32
+    lengths, offsets = np.array(lengths), np.concatenate([[0], np.cumsum(rows or [1] * len(lengths))])
+    cache, dev, table = cache_of(lengths, Hkv, D, page, 3)
+    q = normal((int(offsets[-1]), Hq, D), 1).cuda()
+    t, ln, off = i32(table), i32(lengths), i32(offsets)
+    c = mx.CacheBatch(dev.k.data_ptr(), dev.v.data_ptr(), dev.k_scale.data_ptr(), dev.v_scale.data_ptr(), dev.k.stride(0), dev.v.stride(0),
+                      dev.k_scale.stride(0), dev.v_scale.stride(0), dev.k.shape[0], Hkv, page, D, t.data_ptr(), t.stride(0), t.shape[1], ln.data_ptr(),
+                      off.data_ptr() if rows else None, len(lengths), q.shape[0])
+    L, got = mx.lib(), []
+    for size in (L.mx_cache_attention_batch_bytes(ctypes.byref(c), Hq), L.mx_cache_attention_workspace_bytes(D, q.shape[0], Hq)):
+        space = torch.full((size + 8192,), 0xA5, dtype=torch.uint8, device="cuda")
+        out = torch.empty_like(q)
+        assert L.mx_cache_attention(ctypes.byref(c), q.data_ptr(), Hq, Hq * D, D, D ** -0.5, 0, out.data_ptr(), Hq * D, D, None, space.data_ptr() + 4096,
+                                    torch.cuda.current_stream().cuda_stream) == 0
+        assert (space[:4096] == 0xA5).all() and (space[4096 + size:] == 0xA5).all()
+        got.append(out)
+    assert mx.device_error() == 0 and torch.equal(got[0], got[1])
+    assert torch.equal(got[0], mx.cache_attention(q, dev, t, ln, off if rows else None))
+    verify(got[0], None, q, cache, table, lengths, offsets, D ** -0.5, 0, D)
