@@ -23,8 +23,8 @@
 // a second kernel joins; sums are made in the order of the keys. Each of a block's four warps streams its own 16 tokens of
 // a step through a private ring of cp.async stages: no block-wide wait until a tile ends.
 //
-// 64 tokens over 2000 to 8000 keys of 8 heads of 128 (628 MB): 115 us, 108 of them here (5.8 TB/s); 4 over 30 000 to 120 000 of 4 heads
-// (381 MB): 81 us; one over 1000: 10.7 us, nearly all of it chains of loads.
+// 64 tokens over 2000 to 8000 keys of 8 heads of 128 (628 MB): 113 us, 106 of them here (5.9 TB/s); 4 over 30 000 to 120 000 of 4 heads
+// (381 MB): 83 us, 73 of them here; one over 1000: 10.5 us, nearly all of it chains of loads.
 #pragma once
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -207,7 +207,7 @@ __host__ __device__ constexpr int64_t part_floats(int rows, int D) { return int6
 
 constexpr int kAmRows = 256;           // query rows of an item
 constexpr int kAmKeys = 128;           // keys per tile
-constexpr int kAmUnitCost = 3;         // in tiles: 15 000 cycles of queries, output and a first tile's start, 4600 a tile
+constexpr int kAmUnitCost = 3;         // in tiles: 15 000 cycles of queries, output and a first tile's start, 4600 a tile (heads of 128; taken for 64 too)
 
 struct alignas(16) AmItem {
     int64_t at;                        // cost of all units in front of the item

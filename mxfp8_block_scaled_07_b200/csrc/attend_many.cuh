@@ -16,8 +16,9 @@
 // 14 and 15 complete their warpgroup. The launch's 128 registers a thread are split 168 / 88 / 88 (8 x 168 + 4 x 88 + 4 x 88 = 16 x
 // 128), without which the softmax spills. Every wait is bounded.
 //
-// 2048 rows x 32 heads of 128 against 16 000 keys (504 GFLOP): 557 us, 905 TFLOP/s, 0.56 of the dense rate in bursts; the products of a
-// tile need 2048 cycles of the 4600 it takes, the softmax's threads the rest.
+// 2048 rows x 32 heads of 128 against 16 000 keys (504 GFLOP): 562 us, 897 TFLOP/s, 0.55 of the dense rate in bursts. Of the 4600 cycles
+// that a tile takes the products of both halves need 2048 and each half's softmax 3100; the rest a half waits for its next scores, which are
+// made only once its second weights have been multiplied (P lies over the scores' columns) and behind the other half's products.
 #pragma once
 #include <cstdint>
 #include <type_traits>

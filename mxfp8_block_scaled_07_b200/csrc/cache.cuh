@@ -11,7 +11,7 @@
 // and rounded to odd, which rounds to E4M3 as the exact value does.
 //
 // One token of 64 sequences, 8 key and 32 query heads of 128: 2.6 us, a chain of four loads. Prompts of 10 200 tokens: queries 31 us
-// (5.3 TB/s), keys and values 39 us, 70% of the issue slots in the exact rotation.
+// (5.3 TB/s), keys and values 35 us, 73% of the issue slots busy with the rotation, its check and the codes.
 #pragma once
 #include <cuda_bf16.h>
 

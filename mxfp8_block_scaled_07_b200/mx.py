@@ -550,7 +550,8 @@ def rope_backward(dy: torch.Tensor, table: torch.Tensor, positions=None, interle
 
 class KVCache(NamedTuple):
     """Keys and values of one layer: E4M3 codes [pages, heads, page_size, head_dim] and one E8M0 byte per page and head
-    [pages, heads], uint8. Pages may lie at any distance (views of one tensor that holds both, say)."""
+    [pages, heads], uint8. Pages may lie at any distance (views of one tensor that holds both, say). What is rounded here a learner
+    without such a cache does not see: between the two, a BF16 cache agrees better."""
     k: torch.Tensor
     v: torch.Tensor
     k_scale: torch.Tensor
