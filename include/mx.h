@@ -388,7 +388,8 @@ mx_status mx_rope_table(const double* freq, int64_t pairs, double amplitude, int
  * then stay as they are. Otherwise no two of their rows may overlap.
  * Requirements: 1 <= D <= 1024, 2 <= rot <= min(D, 256), rot even, heads that do not overlap (|ldx_h| >= D where H > 1);
  * pointers aligned to their elements. Rows whose pieces are all 16-byte aligned move in 16-byte pieces (and rot a
- * multiple of 16 bytes of elements, of 32 in the half layout); others element by element. T == 0 or H == 0 is a no-op.
+ * multiple of 16 bytes of elements, of 32 in the half layout); others element by element. T * ceil(H / 8) times a head's pieces, or
+ * elements, below 2^31. T == 0 or H == 0 is a no-op.
  */
 mx_status mx_rope(const void* x, mx_out_dtype dtype, int64_t T, int64_t H, int64_t D, int64_t ldx_t, int64_t ldx_h,
                   const float* table, int64_t positions, int64_t rot, const void* pos, int pos64, int interleaved, void* y,

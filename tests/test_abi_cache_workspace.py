@@ -3,12 +3,13 @@ import ctypes
 
 import pytest
 
-from mxfp8_block_scaled_07_b200 import mx
+from mxfp8_block_scaled_07_b200 import build as mxbuild, mx
 from test_abi_cache import A, BAD_BATCHES, BIG, batch
 
 
 @pytest.fixture(scope="module")
 def sizes():
+    mxbuild.build()
     lib = mx.lib()
     return lambda q_heads=8, **kw: lib.mx_cache_attention_batch_bytes(ctypes.byref(batch(mx, **{**dict(sequences=4, rows=4, row_offsets=None), **kw})), q_heads)
 
