@@ -385,7 +385,7 @@ mx_status mx_rope_table(const double* freq, int64_t pairs, double amplitude, int
  * 1.5 units in the last place of fp32 and rounded once. pos: int32 [T] (pos64 == 0) or int64 (device), or NULL: 0 .. T - 1 (T <= positions).
  * A token with a negative position (padding) gets zeros; so does one at or behind `positions`, which also sets bit 4 of the
  * device status word. y (the same shape and type, strides ldy_t, ldy_h) may be x itself with the same strides: features from rot on
- * then stay as they are. Otherwise no two of their rows may overlap.
+ * then stay as they are, but for tokens that get zeros. Otherwise no two of their rows may overlap.
  * Requirements: 1 <= D <= 1024, 2 <= rot <= min(D, 256), rot even, heads that do not overlap (|ldx_h| >= D where H > 1);
  * pointers aligned to their elements. Rows whose pieces are all 16-byte aligned move in 16-byte pieces (and rot a
  * multiple of 16 bytes of elements, of 32 in the half layout); others element by element. T * ceil(H / 8) times a head's pieces, or

@@ -7,8 +7,8 @@
 // of products, within 1.5 ulp however much cancels), so that one rounding to the output type is all that is lost.
 //
 // Bound by HBM: an element is read and written once; a thread keeps its pairs' cosines and sines in registers over
-// several heads of a token, so that the table adds a few percent. 12 288 tokens of 40 heads of 128 in BF16 take 46 us each way
-// (5.6 TB/s), 5201 of 12 heads of 128 in fp32, half rotated, 15 us (4.3 TB/s); 13 tokens of 32 heads 1.8 us.
+// several heads of a token, so that the table adds a few percent. 12 288 tokens of 40 heads of 128 in BF16 take 44 us each way
+// (5.8 TB/s), 5201 of 12 heads of 128 in fp32, half rotated, 14.5 us (4.5 TB/s); 13 tokens of 32 heads 1.8 us.
 #pragma once
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -129,6 +129,30 @@ struct RopeArgs {
     int pos64, negate, copy;    // copy: features from rot on are written too (y is not x)
 };
 
+// Zeros in a thread's pieces of its heads; in place, where no thread has the features from rot on, those that turn the others share them.
+template <class T, int V, bool IL>
+__device__ __noinline__ void zero_heads(const RopeArgs& a, T* y, int chunk, int step, int piece) {
+    Piece<T, V> none;
+#pragma unroll
+    for (int i = 0; i < V; ++i) none.e[i] = from_f32<T>(0.0f);
+    auto zeros = [&](T* p, int d, int end) {
+        if (d + V <= end) none.store(p + d);
+        else
+            for (int e = d; e < end; ++e) p[e] = from_f32<T>(0.0f);
+    };
+    for (int h = chunk; h < a.H; h += step) {
+        T* p = y + h * a.ldy_h;
+        if (piece >= a.pair_lanes) {
+            zeros(p, a.rot + (piece - a.pair_lanes) * V, a.D);
+            continue;
+        }
+        zeros(p, piece * V, a.rot);
+        if (!IL) zeros(p, a.rot / 2 + piece * V, a.rot);
+        if (!a.copy)
+            for (int d = a.rot + piece * V; d < a.D; d += a.pair_lanes * V) zeros(p, d, a.D);
+    }
+}
+
 // One thread: one piece of every head of a chunk (heads chunk, chunk + chunks, ...: the threads of a token walk
 // neighbouring heads together), V elements of both halves in the half layout, V consecutive ones in the interleaved.
 // HC heads are loaded before the first is written. A negative position is a padding token: zeros. A position behind
@@ -149,6 +173,10 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const __grid_constan
     if (a.pos) p = a.pos64 ? static_cast<const int64_t*>(a.pos)[t] : static_cast<const int32_t*>(a.pos)[t];
     const bool known = p >= 0 && p < a.positions;
     if (p >= a.positions) atomicOr(a.err, kErrBadIndex);
+    if (!known) {                                  // every thread zeros of its own
+        zero_heads<T, V, IL>(a, y, chunk, step, piece);
+        return;
+    }
     if (piece >= a.pair_lanes) {                   // features that are not rotated
         const int d = a.rot + (piece - a.pair_lanes) * V;
         const bool whole = d + V <= a.D;
@@ -164,22 +192,17 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const __grid_constan
                 const int h = h0 + j * step;
                 if (h >= a.H) break;
                 if (whole) {
-                    if (!known)
-#pragma unroll
-                        for (int i = 0; i < V; ++i) v[j].e[i] = from_f32<T>(0.0f);
                     v[j].store(y + h * a.ldy_h + d);
                 } else {
-                    for (int e = d; e < a.D; ++e) y[h * a.ldy_h + e] = known ? x[h * a.ldx_h + e] : from_f32<T>(0.0f);
+                    for (int e = d; e < a.D; ++e) y[h * a.ldy_h + e] = x[h * a.ldx_h + e];
                 }
             }
         }
         return;
     }
     float c[W], s[W];
-    if (known) {
-        load_angles<W>(a.table + p * a.rot + piece * W, c);
-        load_angles<W>(a.table + p * a.rot + a.rot / 2 + piece * W, s);
-    }
+    load_angles<W>(a.table + p * a.rot + piece * W, c);
+    load_angles<W>(a.table + p * a.rot + a.rot / 2 + piece * W, s);
 #pragma unroll
     for (int i = 0; i < W; ++i) s[i] = a.negate ? -s[i] : s[i];
     const int d0 = piece * V, d1 = a.rot / 2 + piece * V;
@@ -202,8 +225,8 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const __grid_constan
                 T& ta = IL ? u[j].e[2 * i] : u[j].e[i];
                 T& tb = IL ? u[j].e[(2 * i + 1) % V] : w[IL ? 0 : j].e[i];
                 const float xa = to_f32(ta), xb = to_f32(tb);
-                ta = from_f32<T>(known ? diff_of_products(xa, c[i], xb, s[i]) : 0.0f);
-                tb = from_f32<T>(known ? diff_of_products(xb, c[i], -xa, s[i]) : 0.0f);
+                ta = from_f32<T>(diff_of_products(xa, c[i], xb, s[i]));
+                tb = from_f32<T>(diff_of_products(xb, c[i], -xa, s[i]));
             }
             u[j].store(y + h * a.ldy_h + d0);
             if constexpr (!IL) w[j].store(y + h * a.ldy_h + d1);

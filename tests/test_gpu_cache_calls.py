@@ -132,3 +132,21 @@ def test_the_workspace_is_as_large_as_it_says(D, lengths, rows, Hq):
     assert mx.device_error() == 0 and torch.equal(got[0], got[1])
     assert torch.equal(got[0], mx.cache_attention(q, dev, t, ln, off if rows else None))
     verify(got[0], None, q, cache, table, lengths, offsets, D ** -0.5, 0, D)
+
+
+@pytest.mark.parametrize("back", [False, True])
+@pytest.mark.parametrize("interleaved", [False, True])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16, torch.float32])
+@pytest.mark.parametrize("H,D,rot,gap", [(1, 64, 32, 0), (9, 128, 64, 0), (3, 80, 16, 8), (5, 30, 14, 0), (2, 129, 128, 1), (40, 96, 96, 0), (1, 1024, 2, 0)])
+def test_padding_tokens_in_place(H, D, rot, gap, dtype, interleaved, back):
+    """A token of a negative position or one behind the table is zeros whole, rotated in place as elsewhere; gaps between heads stay."""
+    T = 6
+    f = mx.rope_backward if back else mx.rope
+    table = torch.from_numpy(plain.table(10, plain.frequencies(rot))).cuda()
+    pos = torch.tensor([3, -1, 9, 10, 0, -7], device="cuda")
+    buf = normal((T, H, D + gap), 1).to(dtype).cuda()
+    x = buf[:, :, :D]
+    want, rest = f(x, table, pos, interleaved), buf[:, :, D:].clone()
+    assert not want[1].any() and not want[3].any() and not want[5].any() and want[2, :, rot:].equal(x[2, :, rot:])
+    assert f(x, table, pos, interleaved, out=x) is x
+    assert torch.equal(x, want) and torch.equal(buf[:, :, D:], rest) and mx.device_error() == 4
