@@ -452,9 +452,8 @@ mx_status mx_cache_append(const mx_cache_batch* cache, const void* k, int64_t ld
 
 /*
  * Bytes of mx_cache_attention's workspace: for this batch (its sizes and whether it has row_offsets; what its arrays hold is
- * not read), or for any batch of such sizes. Without row_offsets, 8.1 MB at most; with them, up to 43 MB and two
- * bytes per row and query head more. -1 for sizes that
- * mx_cache_attention does not take.
+ * not read), or for any batch of such sizes. Without row_offsets, 8.1 MB at most; with them, up to 43 MB and two bytes per row
+ * and query head more. -1 for what mx_cache_attention does not take.
  */
 int64_t mx_cache_attention_batch_bytes(const mx_cache_batch* cache, int64_t q_heads);
 int64_t mx_cache_attention_workspace_bytes(int64_t head_dim, int64_t rows, int64_t q_heads);
@@ -467,8 +466,9 @@ int64_t mx_cache_attention_workspace_bytes(int64_t head_dim, int64_t rows, int64
  * Scores, softmax statistics and sums are fp32 (a row whose scores times log2 e lie beyond +-2^24, where fp32 does not tell
  * neighbouring ones apart, has no defined result); what multiplies a value's code, weight times scale, is rounded to f16 relative to
  * the largest that the row sees: 11 bits from 2^-20 of that one up, an error of less than 2^-31 of it below. Scales may lie as far
- * apart as they like, and pages that a row does not see change nothing. A row that sees no key has out 0 and lse -inf. Codes 0x7F and 0xFF, which mx_cache_append does not write, count as NaN, and may do so for neighbouring
- * rows that do not see them. Sums are made in a fixed order. out may be q with the same strides; otherwise no two of their rows may overlap.
+ * apart as they like, and pages that a row does not see change nothing. A row that sees no key has out 0 and lse -inf. Codes 0x7F
+ * and 0xFF, which mx_cache_append does not write, count as NaN, and may do so for neighbouring rows that do not see them. Sums are
+ * made in a fixed order. out may be q with the same strides; otherwise no two of their rows may overlap.
  * workspace: as many device bytes as either function above says, 16-byte aligned, used during this call only (calls that
  * may run at the same time need their own). row_offsets that name rows twice may leave rows unwritten, with bit 2 of the status word.
  * After an expired wait a row is its value or what was there before.

@@ -1677,9 +1677,9 @@ bool opt_in_smem(std::atomic<bool>* done, K kernel, int bytes) {
 }
 
 // Rows per sequence and key head (new tokens x G) up to which a sequence of a ragged batch is left to the kernel for few: one number
-// for every D, G and context, measured where most of the work is and not tuned elsewhere. D = 128, 8 key heads, G = 4, the kernel for few against the one for many: 32 sequences behind 2000 keys take 52 and 112 us
-// with 16 rows each, 109 and 111 with 48, 142 and 109 with 64; behind 500 keys 56 and 53 with 48; 4 sequences behind 16 000
-// keys 92 and 103 with 48, 113 and 101 with 64; behind 300 keys 24 and 38 with 48; one behind 16 000 keys 42 and 58.
+// for every D, G and context, measured at D = 128, 8 key heads, G = 4 only. The kernel for few against the one for many: 32 sequences
+// behind 2000 keys take 52 and 112 us with 16 rows each, 109 and 111 with 48, 142 and 109 with 64; behind 500 keys 56 and 53 with 48; 4
+// sequences behind 16 000 keys 92 and 103 with 48, 113 and 101 with 64; behind 300 keys 24 and 38 with 48; one behind 16 000 keys 42 and 58.
 constexpr int64_t kAtFewRows = 48;
 
 // Items of 256 rows that sequences of more than kAtFewRows rows can make of `rows` rows.
